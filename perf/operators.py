@@ -272,8 +272,10 @@ def _power(byte):
 def _plain_e4m3(x):
     """e4m3 bytes of rows [..., 64] and the byte of their power-of-two scale."""
     x = x.float()
-    part, power = torch.frexp(x.abs().amax(-1))
-    e = (power - torch.where(part > 0.875, 8, 9)).clamp(min=LEAST)      # 448 = 0.875 * 2^9
+    most = x.abs().amax(-1)
+    part, power = torch.frexp(most)
+    e = power - torch.where(part > 0.875, 8, 9)      # 448 = 0.875 * 2^9
+    e = torch.where(most > 0, e, LEAST).clamp(min=LEAST)
     q = (x * _power(127 - e)[..., None]).to(torch.float8_e4m3fn)
     return q.view(torch.uint8), (e + 127).to(torch.uint8)
 
