@@ -221,6 +221,74 @@ oasr_status oasr_project_qkv_pos(const void* x, const void* w_qkv, const void* b
                                  void* rel, int M, int R, int d_model, int H, oasr_dtype dt,
                                  cudaStream_t stream);
 
+/*
+ * The 8-bit cache: K and V pools whose rows (one head of one frame, 64 values) are e4m3 with one
+ * power-of-two scale each, half the bytes of bf16 pools (64 + 1 instead of 128 per row).
+ *
+ *   k_pool, v_pool : [num_blocks, H, block_size, 64] e4m3 bytes
+ *   kv_scale       : [num_blocks, H, 2, block_size] bytes (index 0 of the third axis: K, 1: V)
+ *
+ * A row r stands for q * 2^e, with e = max(-100, the least e for which max|r| <= 448 * 2^e), the
+ * stored scale byte e + 127 and q = r * 2^-e rounded to e4m3 (nearest, ties to even).  A row with a
+ * NaN or an infinity has the scale byte 255 and stands for NaN in every element.  q * 2^e is exact in
+ * bf16 and fp32, so a row read back and written again keeps its bytes.  Block ids, block_table and
+ * cache_seqlens mean what they mean for the other pools (oasr_window_commit serves both).  Every
+ * pointer, kv_scale included, must be 16-byte aligned.
+ *
+ * oasr_paged_append_e4m3: as oasr_paged_append, the rows of k_new, v_new ([B, T, H, 64], `dt`)
+ * quantised as they are written.  D = 64; 2 * H * T < 2^30.  Rows whose position lies past the table,
+ * or whose block id is outside [0, num_blocks), are skipped (status bit OASR_ERR_BOUNDS).
+ */
+oasr_status oasr_paged_append_e4m3(const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                                   void* kv_scale, int num_blocks, int block_size,
+                                   const int32_t* block_table, int max_blocks_per_seq,
+                                   const int32_t* cache_seqlens, int B, int T, int H, int D,
+                                   oasr_dtype dt, cudaStream_t stream);
+
+/*
+ * Read cached rows back: k[b][i][h][:] and v[b][i][h][:] ([B, L, H, 64], `dt`) become the values of
+ * stream b's position start[b] + i (start may be null: 0), for i < L.  Positions at or past
+ * cache_seqlens[b] give zeros; negative positions, positions past the table's pages and invalid block
+ * ids give zeros and raise OASR_ERR_BOUNDS.  D = 64; H * L < 2^30.
+ */
+oasr_status oasr_paged_read_e4m3(const void* k_pool, const void* v_pool, const void* kv_scale,
+                                 int num_blocks, int block_size, const int32_t* block_table,
+                                 int max_blocks_per_seq, const int32_t* cache_seqlens,
+                                 const int32_t* start, void* k, void* v, int B, int L, int H, int D,
+                                 oasr_dtype dt, cudaStream_t stream);
+
+/*
+ * oasr_chunk_relattn_paged over the 8-bit cache: the attention of that call on the values the pools
+ * stand for.  D = 64; 1 <= T <= 64; block_size a power of two in [8, 256]; max_blocks_per_seq <= 512;
+ * num_blocks * H * block_size < 2^31.  A stream with C_b + T > max_blocks_per_seq * block_size has the
+ * keys past the table dropped; distances the rel table lacks (R < C_b + 2T - 1) count as zero rows; an
+ * invalid block id reads as zero rows; each raises OASR_ERR_BOUNDS.
+ * bf16: the chunk, biases, rel and out are bf16; the position term is rounded to bf16, P (times its
+ * key's V scale) likewise, everything else is fp32.  f32: fp32 throughout.
+ */
+oasr_status oasr_chunk_relattn_paged_e4m3(const void* q, const void* k_pool, const void* v_pool,
+                                          const void* kv_scale, int num_blocks, int block_size,
+                                          const int32_t* block_table, int max_blocks_per_seq,
+                                          const int32_t* cache_seqlens, const void* pos_bias_u,
+                                          const void* pos_bias_v, const void* rel, int R, void* out,
+                                          int B, int T, int H, int D, float scale, oasr_dtype dt,
+                                          cudaStream_t stream);
+
+/*
+ * One fused streaming step over the 8-bit cache: oasr_paged_append_e4m3 followed by
+ * oasr_chunk_relattn_paged_e4m3 (in one launch for bf16, in two for f32).  The chunk's own keys are
+ * attended to as quantised, so the result is that of the two calls up to summation order, and the
+ * pools afterwards are bit-identical.  The requirements of both apply.  Block ids of different streams
+ * must not alias a block that this step writes.
+ */
+oasr_status oasr_chunk_step_paged_e4m3(const void* q, const void* k_new, const void* v_new,
+                                       void* k_pool, void* v_pool, void* kv_scale, int num_blocks,
+                                       int block_size, const int32_t* block_table,
+                                       int max_blocks_per_seq, const int32_t* cache_seqlens,
+                                       const void* pos_bias_u, const void* pos_bias_v,
+                                       const void* rel, int R, void* out, int B, int T, int H,
+                                       int D, float scale, oasr_dtype dt, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* oasr_status_string(oasr_status status);
 

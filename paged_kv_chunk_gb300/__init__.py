@@ -22,11 +22,14 @@ CUDA device; the layer's pools, the shared block table and cache lengths persist
 The offline pass over packed utterances is ``oasr_packed_relattn_varlen`` (or
 ``oasr_packed_relattn_chunked`` under the Nemotron chunked-limited window).
 """
-from .capi import (OasrError, oasr_chunk_relattn_paged, oasr_chunk_step_paged,  # noqa: F401
-                   oasr_device_status, oasr_packed_relattn_chunked, oasr_packed_relattn_varlen,
-                   oasr_paged_append, oasr_project_qkv_pos, oasr_selftest_wait, oasr_version,
-                   oasr_window_commit)
+from .capi import (OasrError, oasr_chunk_relattn_paged, oasr_chunk_relattn_paged_e4m3,  # noqa: F401
+                   oasr_chunk_step_paged, oasr_chunk_step_paged_e4m3, oasr_device_status,
+                   oasr_packed_relattn_chunked, oasr_packed_relattn_varlen, oasr_paged_append,
+                   oasr_paged_append_e4m3, oasr_paged_read_e4m3, oasr_project_qkv_pos,
+                   oasr_selftest_wait, oasr_version, oasr_window_commit)
 
 __all__ = ["OasrError", "oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
            "oasr_packed_relattn_varlen", "oasr_packed_relattn_chunked", "oasr_window_commit",
-           "oasr_project_qkv_pos", "oasr_device_status", "oasr_selftest_wait", "oasr_version"]
+           "oasr_project_qkv_pos", "oasr_paged_append_e4m3", "oasr_paged_read_e4m3",
+           "oasr_chunk_relattn_paged_e4m3", "oasr_chunk_step_paged_e4m3", "oasr_device_status",
+           "oasr_selftest_wait", "oasr_version"]

@@ -56,7 +56,15 @@ def load() -> ctypes.CDLL:
                                                   I, S]
         L.oasr_window_commit.argtypes = [P, P, I, I, I, I, I, S]
         L.oasr_project_qkv_pos.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, S]
-        for fn in ("oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
+        L.oasr_paged_append_e4m3.argtypes = [P, P, P, P, P, I, I, P, I, P, I, I, I, I, I, S]
+        L.oasr_paged_read_e4m3.argtypes = [P, P, P, I, I, P, I, P, P, P, P, I, I, I, I, I, S]
+        L.oasr_chunk_relattn_paged_e4m3.argtypes = [P, P, P, P, I, I, P, I, P, P, P, P, I, P, I, I,
+                                                    I, I, F, I, S]
+        L.oasr_chunk_step_paged_e4m3.argtypes = [P, P, P, P, P, P, I, I, P, I, P, P, P, P, I, P, I,
+                                                 I, I, I, F, I, S]
+        for fn in ("oasr_paged_append_e4m3", "oasr_paged_read_e4m3",
+                   "oasr_chunk_relattn_paged_e4m3", "oasr_chunk_step_paged_e4m3",
+                   "oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
                    "oasr_packed_relattn_varlen", "oasr_packed_relattn_chunked",
                    "oasr_window_commit", "oasr_project_qkv_pos"):
             getattr(L, fn).restype = I
@@ -279,6 +287,111 @@ def oasr_project_qkv_pos(x, w_qkv, b_qkv, pos_emb, w_pos, H, q=None, k=None, v=N
     return q, k, v, rel
 
 
+def _pools_e4m3(k_pool, v_pool, kv_scale, H, D):
+    """Device pointers and sizes of an 8-bit cache (pools [nb,H,bs,D], scales [nb,H,2,bs])."""
+    if k_pool.dim() != 4 or k_pool.shape[1] != H or k_pool.shape[3] != D:
+        raise ValueError("k_pool must be [num_blocks, H, block_size, D]")
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("v_pool must have k_pool's shape")
+    nb, bs = k_pool.shape[0], k_pool.shape[2]
+    if tuple(kv_scale.shape) != (nb, H, 2, bs):
+        raise ValueError("kv_scale must be [num_blocks, H, 2, block_size]")
+    return (_dev(k_pool, "k_pool", torch.float8_e4m3fn), _dev(v_pool, "v_pool", torch.float8_e4m3fn),
+            _dev(kv_scale, "kv_scale", torch.uint8), nb, bs)
+
+
+def _table(block_table, cache_seqlens, B):
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(cache_seqlens.shape) != (B,):
+        raise ValueError("block_table must be [B, mbps] and cache_seqlens [B]")
+    return (_dev(block_table, "block_table", torch.int32), block_table.shape[1],
+            _dev(cache_seqlens, "cache_seqlens", torch.int32))
+
+
+def oasr_paged_append_e4m3(k_new, v_new, k_pool, v_pool, kv_scale, block_table, cache_seqlens,
+                           stream=None):
+    """Quantise the chunk (k_new, v_new [B,T,H,64]) into the 8-bit pools (float8_e4m3fn
+    [nb,H,bs,64]) and their scales (uint8 [nb,H,2,bs]), in place."""
+    L = load()
+    dt = _dtype_code(k_new)
+    B, T, H, D = k_new.shape
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must share their shape [B, T, H, D]")
+    _check("oasr_paged_append_e4m3", L.oasr_paged_append_e4m3(
+        _dev(k_new, "k_new", k_new.dtype), _dev(v_new, "v_new", k_new.dtype),
+        *_pools_e4m3(k_pool, v_pool, kv_scale, H, D), *_table(block_table, cache_seqlens, B), B, T, H,
+        D, dt, _stream(stream)))
+
+
+def oasr_paged_read_e4m3(k_pool, v_pool, kv_scale, block_table, cache_seqlens, length, start=None,
+                         k=None, v=None, dtype=torch.bfloat16, stream=None):
+    """Values of each stream's positions start[b] .. start[b] + length - 1 (start None: from 0) as
+    dense [B,length,H,64] tensors (k, v) of ``dtype`` (or of the k and v given); zeros past the
+    cached length."""
+    L = load()
+    B, H, D, n = block_table.shape[0], k_pool.shape[1], k_pool.shape[3], int(length)
+    if n < 1:
+        raise ValueError("length must be at least 1")
+    k = torch.empty((B, n, H, D), dtype=dtype, device=k_pool.device) if k is None else k
+    v = torch.empty((B, n, H, D), dtype=k.dtype, device=k_pool.device) if v is None else v
+    if tuple(k.shape) != (B, n, H, D) or tuple(v.shape) != (B, n, H, D):
+        raise ValueError("k and v must be [B, length, H, D]")
+    if start is not None and tuple(start.shape) != (B,):
+        raise ValueError("start must be [B]")
+    _check("oasr_paged_read_e4m3", L.oasr_paged_read_e4m3(
+        *_pools_e4m3(k_pool, v_pool, kv_scale, H, D), *_table(block_table, cache_seqlens, B),
+        None if start is None else _dev(start, "start", torch.int32), _dev(k, "k", k.dtype),
+        _dev(v, "v", k.dtype), B, n, H, D, _dtype_code(k), _stream(stream)))
+    return k, v
+
+
+def _chunk_e4m3(q, pos_bias_u, pos_bias_v, rel, out):
+    B, T, H, D = q.shape
+    if tuple(pos_bias_u.shape) != (H, D) or tuple(pos_bias_v.shape) != (H, D):
+        raise ValueError("pos biases must be [H, D]")
+    if rel.dim() != 3 or tuple(rel.shape[1:]) != (H, D):
+        raise ValueError("rel must be [R, H, D]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must be [B, T, H, D] of q's dtype")
+    return B, T, H, D, out
+
+
+def oasr_chunk_relattn_paged_e4m3(q, k_pool, v_pool, kv_scale, block_table, cache_seqlens,
+                                  pos_bias_u, pos_bias_v, rel, out=None, scale=None, stream=None):
+    """Streaming chunk attention over the 8-bit paged cache; returns out [B,T,H,64]."""
+    L = load()
+    dt = _dtype_code(q)
+    B, T, H, D, out = _chunk_e4m3(q, pos_bias_u, pos_bias_v, rel, out)
+    scale = D ** -0.5 if scale is None else float(scale)
+    _check("oasr_chunk_relattn_paged_e4m3", L.oasr_chunk_relattn_paged_e4m3(
+        _dev(q, "q", q.dtype), *_pools_e4m3(k_pool, v_pool, kv_scale, H, D),
+        *_table(block_table, cache_seqlens, B), _dev(pos_bias_u, "pos_bias_u", q.dtype),
+        _dev(pos_bias_v, "pos_bias_v", q.dtype), _dev(rel, "rel", q.dtype), rel.shape[0],
+        _dev(out, "out", q.dtype), B, T, H, D, scale, dt, _stream(stream)))
+    return out
+
+
+def oasr_chunk_step_paged_e4m3(q, k_new, v_new, k_pool, v_pool, kv_scale, block_table,
+                               cache_seqlens, pos_bias_u, pos_bias_v, rel, out=None, scale=None,
+                               stream=None):
+    """Fused append + streaming chunk attention over the 8-bit paged cache; returns out
+    [B,T,H,64]."""
+    L = load()
+    dt = _dtype_code(q)
+    B, T, H, D, out = _chunk_e4m3(q, pos_bias_u, pos_bias_v, rel, out)
+    if k_new.shape != q.shape or v_new.shape != q.shape:
+        raise ValueError("k_new, v_new must be [B, T, H, D]")
+    scale = D ** -0.5 if scale is None else float(scale)
+    _check("oasr_chunk_step_paged_e4m3", L.oasr_chunk_step_paged_e4m3(
+        _dev(q, "q", q.dtype), _dev(k_new, "k_new", q.dtype), _dev(v_new, "v_new", q.dtype),
+        *_pools_e4m3(k_pool, v_pool, kv_scale, H, D), *_table(block_table, cache_seqlens, B),
+        _dev(pos_bias_u, "pos_bias_u", q.dtype), _dev(pos_bias_v, "pos_bias_v", q.dtype),
+        _dev(rel, "rel", q.dtype), rel.shape[0], _dev(out, "out", q.dtype), B, T, H, D, scale, dt,
+        _stream(stream)))
+    return out
+
+
 def oasr_device_status(clear: bool = True) -> int:
     """Raw device status bits (1 = an index was out of range, 2 = a wait timed out)."""
     L = load()
@@ -317,5 +430,7 @@ def _traced(fn):
 if NVTX:
     for _name in ("oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
                   "oasr_packed_relattn_varlen", "oasr_packed_relattn_chunked", "oasr_window_commit",
-                  "oasr_project_qkv_pos", "oasr_selftest_wait"):
+                  "oasr_project_qkv_pos", "oasr_selftest_wait", "oasr_paged_append_e4m3",
+                  "oasr_paged_read_e4m3", "oasr_chunk_relattn_paged_e4m3",
+                  "oasr_chunk_step_paged_e4m3"):
         globals()[_name] = _traced(globals()[_name])

@@ -1,0 +1,887 @@
+// Streaming chunk attention over the 8-bit paged cache (oasr_chunk_relattn_paged_e4m3) and the
+// fused append + attention step (oasr_chunk_step_paged_e4m3).  Score, masking and table index
+// are those of the 16-bit calls (chunk_attn.cu); the keys and values are what the pool's e4m3
+// rows and their power-of-two scales stand for (e4m3.cuh).
+//
+//   s_ij = scale * (2^ek_j (q_i + u) . k8_j + (q_i + v) . rel[R - T - C + j - i])
+//   out_i = sum_j softmax(s_i)_j 2^ev_j v8_j
+//
+// The scales stay out of the products: 2^ek multiplies the accumulated score of its key (one fused
+// multiply-add with the position term) and 2^ev the probability of its key before that is rounded
+// to bf16.  Both are exact, so the result is that of the 16-bit computation on the read-back rows.
+// k8 and v8 go into the bf16 matrix instructions as themselves: e4m3's exponent and fraction,
+// shifted into a bf16's, are the value times 2^-120, subnormals included, and one packed multiply
+// by 2^120 gives it back (e4m3_to_bf16).
+//
+// One CTA per (stream, head, block of up to 32 queries, share of the keys): four consumer warps and
+// a producer warp.  The producer brings stages of 64 keys by TMA (a box of K and one of V per page,
+// 64-byte rows, 64-byte swizzle, and one bulk copy of the page's scales) into a ring; consumer warp
+// w takes keys 16w .. 16w+15 of each stage for all the CTA's queries.  The position term is computed
+// per segment of the keys into a pre-skewed bf16 table (PosTable, attn_core.cuh), so its shared
+// memory does not grow with the history.  The chunk itself never comes through the pool: the
+// consumer warps quantise it from k_new / v_new into a region of its own, from which it is attended
+// to, and store the same bytes into the pool.
+//
+// When the (stream, head) pairs are too few to fill the GPU the keys of each are divided over a
+// cluster of up to eight CTAs, whose partial sums meet through distributed shared memory.
+#include "attn_core.cuh"
+#include "e4m3.cuh"
+#include "host_common.h"
+
+namespace oasr {
+
+namespace {
+
+constexpr int kE4MaxPages = 512;              // block-table entries a CTA caches
+constexpr int kE4Stage = 2 * kStageKeys * kE4Row;   // K and V rows of a stage
+constexpr int kE4MaxT = 64;
+
+struct E4Args {
+    const __nv_bfloat16* k_new;   // fused only
+    const __nv_bfloat16* v_new;   // fused only
+    uint8_t* k_pool;
+    uint8_t* v_pool;
+    uint8_t* kv_scale;
+    const int32_t* block_table;
+    const int32_t* cache_seqlens;
+    const uint16_t* pos_bias_u;
+    const uint16_t* pos_bias_v;
+    const uint16_t* rel;
+    uint16_t* out;
+    unsigned* status;
+    int num_blocks, block_size, bs_shift, mbps, T, H, R;
+    int q_tiles, splits;
+    int seg;          // stages per segment of the position table
+    int gt_w;         // row stride of the table (bf16 elements)
+    float scale_log2; // scale * log2(e)
+};
+
+// Shared memory (byte offsets from a 1024-aligned base).  The ring's rows are reused by the
+// combine once the key loop is over.
+template <int MT, int NS>
+struct E4Smem {
+    static constexpr int Tp = 16 * MT;
+    static constexpr int off_q = NS * kE4Stage;
+    static constexpr int off_ck = off_q + Tp * kRowBytes;             // the chunk's K and V rows
+    static constexpr int off_sc = off_ck + 2 * kE4MaxT * kE4Row;      // scales [NS][2 * 64]
+    static constexpr int off_csc = off_sc + NS * 2 * kStageKeys;      // the chunk's [2][64]
+    static constexpr int off_u = off_csc + 2 * kE4MaxT;
+    static constexpr int off_vb = off_u + kHeadDim * 4;
+    static constexpr int off_bt = off_vb + kHeadDim * 4;
+    static constexpr int off_bar = off_bt + kE4MaxPages * 4;          // full[NS], empty[NS], q
+    static constexpr int off_gt = (off_bar + (2 * NS + 1) * 8 + 15) & ~15;
+    static constexpr int bytes = off_gt + 1024;                       // + Tp * gt_w * 2
+    // combine: the warps' partials, then the CTA's own for its cluster
+    static constexpr int comb_o = 0;
+    static constexpr int comb_m = comb_o + kConsumerWarps * Tp * kOW * 4;
+    static constexpr int comb_l = comb_m + kConsumerWarps * Tp * 4;
+    static constexpr int part_o = comb_l + kConsumerWarps * Tp * 4;
+    static constexpr int part_m = part_o + Tp * kHeadDim * 4;
+    static constexpr int part_l = part_m + Tp * 4;
+    static_assert(part_l + Tp * 4 <= NS * kE4Stage, "combine area");
+    static_assert(off_q % 1024 == 0 && off_ck % 1024 == 0 && off_sc % 16 == 0, "TMA alignment");
+};
+
+// Byte offset of 16-byte chunk c (0..3) of row r in a tile of 64-byte rows written by TMA with
+// 64-byte swizzling (tile base 512-byte aligned).
+__device__ __forceinline__ uint32_t swz64(int r, int c)
+{
+    return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Bytes 0, 2 (lo) and 1, 3 (hi) of w, e4m3, as pairs of bf16 times 2^-120 ...
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) { return ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u); }
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) { return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u); }
+// ... and the packed multiply that makes them the values themselves (exact).
+__device__ __forceinline__ uint32_t times_2p120(uint32_t x)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
+    return r;
+}
+
+// A slice of 16 keys in registers: its raw K and V words and its scales.
+struct E4Slice {
+    uint4 k[2];         // keys g4 and 8 + g4, dims 16 t4 ..
+    uint32_t v[8];      // [chunk of 16 dims][keys 2 t4, 2 t4 + 1 | 8 + those]: bytes k0d0 k0d1 k1d0 k1d1
+    uint32_t ks, vs;    // scale bytes of keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+};
+
+// k_s, v_s: shared addresses of the slice's first rows; sc: its first K scale, v_off bytes
+// before its first V scale.  box: keys of one page's scales (the K scales of a page come before
+// its V scales); a slice of 16 keys lies in one page, or in two pages of eight.
+__device__ __forceinline__ void load_slice(E4Slice& x, uint32_t k_s, uint32_t v_s, const uint8_t* sc,
+                                           int next8, int v_off, int lane)
+{
+    const int g4 = lane >> 2, t4 = lane & 3, mi = lane >> 3;
+    const int row = ((mi & 1) << 3) + (lane & 7);
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.k[n].x), "=r"(x.k[n].y), "=r"(x.k[n].z), "=r"(x.k[n].w)
+                     : "r"(k_s + swz64(8 * n + g4, t4)));
+#pragma unroll
+    for (int dp = 0; dp < 2; ++dp)
+        ldsm_x4_t(v_s + swz64(row, 2 * dp + (mi >> 1)), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
+    const uint8_t* p = sc + 2 * t4;
+    x.ks = *reinterpret_cast<const uint16_t*>(p) | (*reinterpret_cast<const uint16_t*>(p + next8) << 16);
+    p += v_off;
+    x.vs = *reinterpret_cast<const uint16_t*>(p) | (*reinterpret_cast<const uint16_t*>(p + next8) << 16);
+}
+
+// A fragments of bf16(q + u) for 16 query rows, the head dimension in the order of the e4m3
+// words: quad position t4 holds dims 16 t4 .., k-step ks the word 4 ks, its bytes 0, 2 then 1, 3.
+__device__ __forceinline__ void make_qu_e4m3(uint32_t (&qu)[4][4], const uint8_t* q_tile, const float* u,
+                                             int mt, int lane)
+{
+    const int g4 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int row = 16 * mt + g4 + 8 * half;
+        const uint4 c0 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4));
+        const uint4 c1 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4 + 1));
+        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const float* b = u + 16 * t4 + 4 * ks;
+            const float d0 = bf16_lo(w[2 * ks]) + b[0], d1 = bf16_hi(w[2 * ks]) + b[1];
+            const float d2 = bf16_lo(w[2 * ks + 1]) + b[2], d3 = bf16_hi(w[2 * ks + 1]) + b[3];
+            qu[ks][half] = pack_bf16(d0, d2);
+            qu[ks][half + 2] = pack_bf16(d1, d3);
+        }
+    }
+}
+
+// One warp, 16 MT query rows against one slice.  gq: the position table at the slice's first key
+// (key jl of query row i reads gq[i * W + jl]); keys [0, kvalid) of the slice exist.
+// acc.o[mt][2c + e] holds dims 16 c + 4 t4 + e and + 2 + e of rows g4 and g4 + 8.
+template <int MT>
+__device__ __forceinline__ void slice_e4m3(WarpAcc (&acc)[MT], const uint32_t (&qu)[MT][4][4], E4Slice& x,
+                                           const uint16_t* gq, int W, bool even, int kvalid, float scale_log2,
+                                           int lane)
+{
+    const int g4 = lane >> 2, t4 = lane & 3;
+    float s[MT][2][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const uint32_t w[4] = {x.k[n].x, x.k[n].y, x.k[n].z, x.k[n].w};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t b0 = times_2p120(e4m3_lo(w[ks])), b1 = times_2p120(e4m3_hi(w[ks]));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) mma_bf16_16816(s[mt][n], qu[mt][ks], b0, b1);
+        }
+    }
+    float ks[4], vs[4];   // keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+    const bool tail = kvalid < 16;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        ks[e] = e4m3_scale((x.ks >> (8 * e)) & 255u);
+        vs[e] = e4m3_scale((x.vs >> (8 * e)) & 255u);
+    }
+    if (tail) {   // rows past the last key may hold anything: their scales and V bytes are dropped
+        const int k0 = 2 * t4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (k0 + (e & 1) + 8 * (e >> 1) >= kvalid) vs[e] = 0.f;
+        const uint32_t m0 = (k0 < kvalid ? 0xffffu : 0u) | (k0 + 1 < kvalid ? 0xffff0000u : 0u);
+        const uint32_t m1 = (k0 + 8 < kvalid ? 0xffffu : 0u) | (k0 + 9 < kvalid ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.v[i] &= (i & 1) ? m1 : m0;
+    }
+    uint32_t pa[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        WarpAcc& a = acc[mt];
+        float mx0 = a.m[0], mx1 = a.m[1];
+        const uint16_t* r0 = gq + (16 * mt + g4) * W + 2 * t4;
+        const uint16_t* r1 = r0 + 8 * W;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float gb[4];
+            if (even) {
+                const uint32_t y0 = *reinterpret_cast<const uint32_t*>(r0 + 8 * n);
+                const uint32_t y1 = *reinterpret_cast<const uint32_t*>(r1 + 8 * n);
+                gb[0] = bf16_lo(y0);
+                gb[1] = bf16_hi(y0);
+                gb[2] = bf16_lo(y1);
+                gb[3] = bf16_hi(y1);
+            } else {
+                gb[0] = bf16_lo(r0[8 * n]);
+                gb[1] = bf16_lo(r0[8 * n + 1]);
+                gb[2] = bf16_lo(r1[8 * n]);
+                gb[3] = bf16_lo(r1[8 * n + 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool ok = 8 * n + 2 * t4 + (e & 1) < kvalid;
+                s[mt][n][e] = ok ? fmaf(s[mt][n][e], ks[2 * n + (e & 1)], gb[e]) * scale_log2 : -INFINITY;
+            }
+            mx0 = fmaxf(mx0, fmaxf(s[mt][n][0], s[mt][n][1]));
+            mx1 = fmaxf(mx1, fmaxf(s[mt][n][2], s[mt][n][3]));
+        }
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+        const float base0 = (mx0 == -INFINITY) ? 0.f : mx0;
+        const float base1 = (mx1 == -INFINITY) ? 0.f : mx1;
+        if (mx0 != a.m[0] || mx1 != a.m[1]) {
+            const float alpha0 = ex2_approx(a.m[0] - base0);
+            const float alpha1 = ex2_approx(a.m[1] - base1);
+            a.l[0] *= alpha0;
+            a.l[1] *= alpha1;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+                a.o[d][0] *= alpha0;
+                a.o[d][1] *= alpha0;
+                a.o[d][2] *= alpha1;
+                a.o[d][3] *= alpha1;
+            }
+            a.m[0] = mx0;
+            a.m[1] = mx1;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            s[mt][n][0] = ex2_approx(s[mt][n][0] - base0);
+            s[mt][n][1] = ex2_approx(s[mt][n][1] - base0);
+            s[mt][n][2] = ex2_approx(s[mt][n][2] - base1);
+            s[mt][n][3] = ex2_approx(s[mt][n][3] - base1);
+            a.l[0] += s[mt][n][0] + s[mt][n][1];
+            a.l[1] += s[mt][n][2] + s[mt][n][3];
+            pa[mt][2 * n] = pack_bf16(s[mt][n][0] * vs[2 * n], s[mt][n][1] * vs[2 * n + 1]);
+            pa[mt][2 * n + 1] = pack_bf16(s[mt][n][2] * vs[2 * n], s[mt][n][3] * vs[2 * n + 1]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t w0 = x.v[2 * c], w1 = x.v[2 * c + 1];
+        const uint32_t e0 = times_2p120(e4m3_lo(w0)), e1 = times_2p120(e4m3_lo(w1));
+        const uint32_t d0 = times_2p120(e4m3_hi(w0)), d1 = times_2p120(e4m3_hi(w1));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            mma_bf16_16816(acc[mt].o[2 * c], pa[mt], e0, e1);
+            mma_bf16_16816(acc[mt].o[2 * c + 1], pa[mt], d0, d1);
+        }
+    }
+}
+
+__device__ __noinline__ bool e4_wait_slow(uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity); }
+__device__ __forceinline__ bool e4_wait(uint32_t bar, uint32_t parity)
+{
+    return mbar_try_wait(bar, parity) || e4_wait_slow(bar, parity);
+}
+
+// 2-D tiled bulk load with an L2 hint, and an untiled bulk copy; both count bytes on `bar`.
+__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                                 uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
+{
+    float v;
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+template <int MT, int NS, int CTAS, bool FUSED>
+__global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v, const E4Args a)
+{
+    using SP = E4Smem<MT, NS>;
+    constexpr int Tp = SP::Tp;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_addr(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = a.splits, T = a.T, H = a.H;
+    int idx = blockIdx.x;
+    const int split = idx % S;
+    idx /= S;
+    const int qt = idx % a.q_tiles;
+    idx /= a.q_tiles;
+    const int b = idx / H, h = idx - b * H;
+    const int i0 = qt * Tp;                       // the CTA's first query
+    const int Tq = min(Tp, T - i0);               // its queries
+    unsigned err = 0;
+    const bool producer = warp == kConsumerWarps;
+    if (producer && lane == 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    grid_dep_wait();
+    const uint32_t bar_full = sb + SP::off_bar;
+    const uint32_t bar_empty = bar_full + NS * 8;
+    const uint32_t bar_q = bar_empty + NS * 8;
+    float* s_u = reinterpret_cast<float*>(sm + SP::off_u);
+    float* s_vb = reinterpret_cast<float*>(sm + SP::off_vb);
+    int* s_bt = reinterpret_cast<int*>(sm + SP::off_bt);
+    __shared__ int s_failed;
+
+    int C = __ldg(a.cache_seqlens + b);
+    if (producer) {
+        const int32_t* bt_row = a.block_table + static_cast<long long>(b) * a.mbps;
+        constexpr int kRowRegs = 4;
+        int row[kRowRegs];
+#pragma unroll
+        for (int k = 0; k < kRowRegs; ++k)
+            if (lane + 32 * k < a.mbps) row[k] = __ldg(bt_row + lane + 32 * k);
+        if (lane == 0) {
+            for (int i = 0; i < NS; ++i) {
+                mbar_init(bar_full + 8 * i, 1);
+                mbar_init(bar_empty + 8 * i, 32 * kConsumerWarps);
+            }
+            mbar_init(bar_q, 1);
+            fence_mbar_init();
+            s_failed = 0;
+            mbar_arrive_expect_tx(bar_q, Tp * kRowBytes);
+            tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, h, b * T + i0);
+        }
+#pragma unroll
+        for (int k = 0; k < kRowRegs; ++k)
+            if (lane + 32 * k < a.mbps) s_bt[lane + 32 * k] = row[k];
+        for (int i = lane + 32 * kRowRegs; i < a.mbps; i += 32) s_bt[i] = __ldg(bt_row + i);
+        __syncwarp();
+        named_bar_arrive(2, kThreads);
+    } else {
+        if (tid < kHeadDim)
+            s_u[tid] = bf16_lo(__ldg(a.pos_bias_u + h * kHeadDim + tid));
+        else
+            s_vb[tid - kHeadDim] = bf16_lo(__ldg(a.pos_bias_v + h * kHeadDim + tid - kHeadDim));
+        named_bar_sync(2, kThreads);
+    }
+    if (C < 0) { C = 0; err |= kErrBounds; }
+    const int sh = a.bs_shift, bs = a.block_size;
+    const int cap = a.mbps << sh;                 // keys the table's pages hold (at most 2^17)
+    if (C > cap) { C = cap; err |= kErrBounds; }
+    int K = C + T;
+    if (K > cap) { K = cap; err |= kErrBounds; }
+    if (C + 2 * T - 1 > a.R) err |= kErrBounds;   // distances the rel table does not hold
+    const int off = a.R - T - C;                  // rel row of query i and key j: off + j - i
+    const int kc = FUSED ? C : K;       // keys that come from the pool
+    const int n_all = (kc + kStageKeys - 1) / kStageKeys;
+    const int st0 = static_cast<int>(static_cast<long long>(n_all) * split / S);
+    const int st1 = static_cast<int>(static_cast<long long>(n_all) * (split + 1) / S);
+    const bool chunk_here = FUSED && split == S - 1;   // the chunk follows the last pool keys
+    const int nc = chunk_here ? K - kc : 0;            // its keys (fewer when it runs past the table)
+    const int box = min(bs, kStageKeys), box_sh = min(sh, 6);
+
+    if (producer) {
+        const uint64_t pol = policy_evict_first();
+        int n_issued = 0;
+        for (int s = st0; s < st1; ++s) {
+            const int it = s - st0, slot = it % NS;
+            if (!__all_sync(0xffffffffu, it < NS || e4_wait(bar_empty + 8 * slot, ((it / NS) - 1) & 1))) {
+                err |= kErrTimeout;
+                break;
+            }
+            const uint32_t bar = bar_full + 8 * slot;
+            const int j0 = s * kStageKeys;
+            const int nbox = min(kStageKeys >> box_sh, (kc - j0 + box - 1) >> box_sh);
+            // lane q: K box of page piece q and its scales, lane 16 + q: its V box
+            const int q = lane & 15;
+            const int j = j0 + q * box;
+            const int blk = q < nbox ? s_bt[j >> sh] : -1;
+            const bool valid = blk >= 0 && blk < a.num_blocks;
+            const uint32_t sc_dst = sb + SP::off_sc + slot * 2 * kStageKeys + q * 2 * box;
+            if (q < nbox && !valid) {   // no such block: its rows read as zeros, with scales of zero
+                err |= kErrBounds;
+                if (lane < 16) {
+                    for (int i = 0; i < box / 2; ++i)
+                        *reinterpret_cast<uint32_t*>(sm + (sc_dst - sb) + 4 * i) = 0u;
+                    fence_proxy_async_smem();
+                }
+            }
+            const int nvalid = __popc(__ballot_sync(0xffffffffu, valid) & 0xffffu);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nbox * box * 2 * kE4Row + nvalid * 2 * box));
+            __syncwarp();
+            if (q < nbox) {
+                const int in_page = j & (bs - 1);
+                const long long page = static_cast<long long>(valid ? blk : 0) * H + h;
+                // an invalid block's box lies outside the pool and reads zeros
+                const int row = valid ? static_cast<int>(page * bs) + in_page : -2 * box;
+                const uint32_t dst = sb + slot * kE4Stage + q * box * kE4Row;
+                if (lane < 16) {
+                    tma_load_2d_hint(dst, &tm_k, bar, 0, row, pol);
+                    if (valid) {
+                        const uint8_t* src = a.kv_scale + 2 * page * bs + in_page;
+                        if (bs <= kStageKeys) {
+                            bulk_load(sc_dst, src, 2 * box, bar);   // K and V scales of the page are adjacent
+                        } else {
+                            bulk_load(sc_dst, src, box, bar);
+                            bulk_load(sc_dst + box, src + bs, box, bar);
+                        }
+                    }
+                } else {
+                    tma_load_2d_hint(dst + kStageKeys * kE4Row, &tm_v, bar, 0, row, pol);
+                }
+            }
+            n_issued = it + 1;
+        }
+        // every copy this CTA requested lands before it ends
+        for (int x = n_issued > NS ? n_issued - NS : 0; x < n_issued; ++x)
+            if (!mbar_wait_idle(bar_full + 8 * (x % NS), (x / NS) & 1)) err |= kErrTimeout;
+        if (!mbar_wait_idle(bar_q, 0)) err |= kErrTimeout;
+        if (err) atomicOr(a.status, err);
+        if (S > 1) {
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    bool failed = false;
+    WarpAcc acc[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc_init(acc[mt]);
+    uint16_t* gs = reinterpret_cast<uint16_t*>(sm + SP::off_gt);
+    const int W = a.gt_w;
+    if (FUSED && chunk_here) {
+        // the chunk's rows: quantised into the chunk region (rows past T zero) and, by the first
+        // query tile, into the pool.  Eight lanes per row.
+        const int nrow = (T + 15) & ~15;
+        for (int r = tid >> 3; r < 2 * nrow; r += 4 * kConsumerWarps) {
+            const int kv = r >= nrow, t = r - kv * nrow, l8 = lane & 7;
+            const unsigned mask = 0xffu << (lane & 24);
+            uint2 q = make_uint2(0u, 0u);
+            uint32_t byte = 0;
+            if (t < nc) {
+                float x[8];
+                load8((kv ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + t) * H + h) * kE4Row + 8 * l8, x);
+                byte = e4m3_quantise8(x, mask, q);
+                const int p = C + t;
+                const int blk = s_bt[p >> sh];
+                if (blk < 0 || blk >= a.num_blocks) {   // dropped by the append: reads as zeros
+                    err |= kErrBounds;
+                    q = make_uint2(0u, 0u);
+                    byte = 0;
+                } else if (qt == 0) {
+                    const int slot = p & (bs - 1);
+                    const long long page = static_cast<long long>(blk) * H + h;
+                    *reinterpret_cast<uint2*>((kv ? a.v_pool : a.k_pool) + (page * bs + slot) * kE4Row + 8 * l8) = q;
+                    if (l8 == 0) a.kv_scale[(2 * page + kv) * bs + slot] = static_cast<uint8_t>(byte);
+                }
+            }
+            *reinterpret_cast<uint2*>(sm + SP::off_ck + kv * kE4MaxT * kE4Row + swz64(t, l8 >> 1) + 8 * (l8 & 1)) = q;
+            if (l8 == 0) sm[SP::off_csc + kv * kE4MaxT + t] = static_cast<uint8_t>(byte);
+        }
+    }
+    PosTable<MT == 1 ? 5 : 4, MT> pt;
+    pt.rel_h = a.rel + h * kHeadDim;
+    pt.stride = static_cast<long long>(H) * kHeadDim;
+    pt.R = a.R;
+    pt.warp = warp;
+    pt.nw = kConsumerWarps;
+    pt.lane = lane;
+    if (!e4_wait(bar_q, 0)) failed = true;
+    const int jl = 16 * warp;   // this warp's keys of a stage
+    const int next8 = box == 8 ? 16 : 8;   // scales of keys 8 .. 15 of a slice, from those of keys 0 .. 7
+    const int sc_off = ((jl >> box_sh) << (box_sh + 1)) + (jl & (box - 1));
+    for (int seg0 = st0;; seg0 += a.seg) {
+        // the position term of this segment's keys [64 seg0, jend) and, with the last, the chunk's
+        const int seg1 = min(seg0 + a.seg, st1);
+        const bool last = seg1 >= st1;
+        const int jbase = seg0 * kStageKeys;
+        const int nkeys = (last && chunk_here) ? K - jbase : min(seg1 * kStageKeys, kc) - jbase;
+        if (nkeys > 0) {
+            if (seg0 > st0) named_bar_sync(1, 32 * kConsumerWarps);   // the previous table has been read
+            if (!failed) {
+                pt.rho0 = off + jbase - i0 - (Tp - 1);
+                pt.ncols = nkeys + Tp - 1;
+                pt.load(warp);
+                pt.build(gs, W, sm + SP::off_q, s_vb);
+            }
+            named_bar_sync(1, 32 * kConsumerWarps);   // the table (and the chunk region) are complete
+        }
+        uint32_t qu[MT][4][4];   // made per segment: they would not fit beside the table's operands
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) make_qu_e4m3(qu[mt], sm + SP::off_q, s_u, mt, lane);
+        for (int s = seg0; s < seg1; ++s) {
+            const int it = s - st0, slot = it % NS;
+            if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
+            const int kv = min(kc - s * kStageKeys, kStageKeys) - jl;
+            E4Slice x;
+            if (kv > 0)
+                load_slice(x, sb + slot * kE4Stage + jl * kE4Row, sb + slot * kE4Stage + (kStageKeys + jl) * kE4Row,
+                           sm + SP::off_sc + slot * 2 * kStageKeys + sc_off, next8, box, lane);
+            mbar_arrive_release(bar_empty + 8 * slot);
+            if (kv > 0) {
+                const int x0 = (s - seg0) * kStageKeys + jl + Tp;
+                slice_e4m3<MT>(acc, qu, x, gs + x0, W, true, kv, a.scale_log2, lane);
+            }
+        }
+        if (last) {
+            if (nc > jl && !failed) {
+                E4Slice x;
+                load_slice(x, sb + SP::off_ck + jl * kE4Row, sb + SP::off_ck + (kE4MaxT + jl) * kE4Row,
+                           sm + SP::off_csc + jl, 8, kE4MaxT, lane);
+                const int x0 = C + jl - jbase + Tp;
+                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 1) == 0, nc - jl, a.scale_log2, lane);
+            }
+            break;
+        }
+    }
+    if (failed) s_failed = 1;
+    grid_dep_trigger();
+    named_bar_sync(1, 32 * kConsumerWarps);
+    if (s_failed) err |= kErrTimeout;
+    if (err) atomicOr(a.status, err);
+    if (s_failed && S == 1) return;
+    // the warps' partials, in the ring's memory (every stage has been read)
+    float* comb_o = reinterpret_cast<float*>(sm + SP::comb_o);
+    float* comb_m = reinterpret_cast<float*>(sm + SP::comb_m);
+    float* comb_l = reinterpret_cast<float*>(sm + SP::comb_l);
+    if (!s_failed) {
+        const int g4 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            acc_reduce_l(acc[mt]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = warp * Tp + 16 * mt + g4 + 8 * half;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    *reinterpret_cast<float4*>(comb_o + r * kOW + 16 * c + 4 * t4) =
+                        make_float4(acc[mt].o[2 * c][2 * half], acc[mt].o[2 * c + 1][2 * half],
+                                    acc[mt].o[2 * c][2 * half + 1], acc[mt].o[2 * c + 1][2 * half + 1]);
+                if (t4 == 0) {
+                    comb_m[r] = acc[mt].m[half];
+                    comb_l[r] = acc[mt].l[half];
+                }
+            }
+        }
+    }
+    named_bar_sync(1, 32 * kConsumerWarps);
+    if (S == 1) {
+        for (int i = tid; i < Tq * 8; i += 32 * kConsumerWarps) {
+            const int row = i >> 3, d0 = (i & 7) * 8;
+            const uint4 v = combine_row8(comb_o, comb_m, comb_l, kConsumerWarps, Tp, row, d0);
+            *reinterpret_cast<uint4*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim + d0) = v;
+        }
+        return;
+    }
+    // the CTA's share, unnormalised: a warp without keys has a maximum of -inf and weight 0
+    float* part_o = reinterpret_cast<float*>(sm + SP::part_o);
+    float* part_m = reinterpret_cast<float*>(sm + SP::part_m);
+    float* part_l = reinterpret_cast<float*>(sm + SP::part_l);
+    for (int i = tid; i < Tq * kHeadDim; i += 32 * kConsumerWarps) {
+        const int row = i / kHeadDim, d = i % kHeadDim;
+        float m = -INFINITY, o = 0.f, l = 0.f;
+        if (!s_failed) {
+#pragma unroll
+            for (int k = 0; k < kConsumerWarps; ++k) m = fmaxf(m, comb_m[k * Tp + row]);
+#pragma unroll
+            for (int k = 0; k < kConsumerWarps; ++k) {
+                const float mk = comb_m[k * Tp + row];
+                const float w = (mk == -INFINITY) ? 0.f : ex2_approx(mk - m);
+                l += w * comb_l[k * Tp + row];
+                o += w * comb_o[(k * Tp + row) * kOW + d];
+            }
+        }
+        part_o[i] = o;
+        if (d == 0) {
+            part_m[row] = m;
+            part_l[row] = l;
+        }
+    }
+    cluster_sync();
+    // rows split, split + S, ... of the cluster's queries are finished here
+    for (int row = split + S * warp; row < Tq; row += S * kConsumerWarps) {
+        float m = -INFINITY;
+        for (int k = 0; k < S; ++k) m = fmaxf(m, ld_cluster(sb + SP::part_m + 4 * row, k));
+        float l = 0.f, o0 = 0.f, o1 = 0.f;
+        for (int k = 0; k < S; ++k) {
+            const float mk = ld_cluster(sb + SP::part_m + 4 * row, k);
+            const float w = (mk == -INFINITY) ? 0.f : ex2_approx(mk - m);
+            l += w * ld_cluster(sb + SP::part_l + 4 * row, k);
+            o0 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane), k);
+            o1 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane + 1), k);
+        }
+        const float inv = 1.f / l;
+        reinterpret_cast<uint32_t*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim)[lane] =
+            pack_bf16(o0 * inv, o1 * inv);
+    }
+    cluster_sync();   // no CTA ends while another may still read its share
+}
+
+// ----------------------------------------------------------------------------- fp32
+
+// One warp per query row, lanes over keys, fp32 throughout (the 16-bit pools' fp32 kernel with
+// rows decoded on the way in).  The chunk is already in the pool.
+__global__ void __launch_bounds__(128) chunk_e4m3_f32_kernel(
+    const float* __restrict__ q, const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
+    const uint8_t* __restrict__ kv_scale, int num_blocks, int block_size,
+    const int32_t* __restrict__ block_table, int mbps, const int32_t* __restrict__ cache_seqlens,
+    const float* __restrict__ u, const float* __restrict__ vb, const float* __restrict__ rel, int R,
+    float* __restrict__ out, int T, int H, float scale, unsigned* status)
+{
+    __shared__ float s_qu[kE4MaxT][kHeadDim];
+    __shared__ float s_qv[kE4MaxT][kHeadDim];
+    const int b = blockIdx.x / H, h = blockIdx.x % H;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    unsigned err = 0;
+    int C = cache_seqlens[b];
+    if (C < 0) { C = 0; err |= kErrBounds; }
+    const int cap = mbps * block_size;
+    if (C > cap) { C = cap; err |= kErrBounds; }
+    int K = C + T;
+    if (K > cap) { K = cap; err |= kErrBounds; }
+    if (C + 2 * T - 1 > R) err |= kErrBounds;
+    const int off = R - T - C;
+    for (int idx = tid; idx < T * kHeadDim; idx += blockDim.x) {
+        const int t = idx / kHeadDim, d = idx % kHeadDim;
+        const float qq = q[((static_cast<long long>(b) * T + t) * H + h) * kHeadDim + d];
+        s_qu[t][d] = qq + u[h * kHeadDim + d];
+        s_qv[t][d] = qq + vb[h * kHeadDim + d];
+    }
+    __syncthreads();
+    for (int i = warp; i < T; i += 4) {
+        float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+        for (int j0 = 0; j0 < K; j0 += 32) {
+            const int j = j0 + lane;
+            float sc = -INFINITY, vs = 0.f;
+            long long row_off = -1;
+            if (j < K) {
+                const int lb = j / block_size;
+                const int blk = block_table[static_cast<long long>(b) * mbps + lb];
+                float acc = 0.f;
+                if (blk >= 0 && blk < num_blocks) {
+                    const long long page = static_cast<long long>(blk) * H + h;
+                    const int slot = j - lb * block_size;
+                    row_off = (page * block_size + slot) * kE4Row;
+                    vs = e4m3_scale(kv_scale[(2 * page + 1) * block_size + slot]);
+                    const uint4* kr = reinterpret_cast<const uint4*>(k_pool + row_off);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint4 w4 = kr[c];
+                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 lo = e4m3_unpack2(w[e]), hi = e4m3_unpack2(w[e] >> 16);
+                            const float* qq = &s_qu[i][16 * c + 4 * e];
+                            acc = fmaf(qq[0], lo.x, acc);
+                            acc = fmaf(qq[1], lo.y, acc);
+                            acc = fmaf(qq[2], hi.x, acc);
+                            acc = fmaf(qq[3], hi.y, acc);
+                        }
+                    }
+                    acc *= e4m3_scale(kv_scale[2 * page * block_size + slot]);
+                } else {
+                    err |= kErrBounds;
+                }
+                const int rho = off + j - i;
+                if (rho >= 0 && rho < R) {
+                    const float4* rr = reinterpret_cast<const float4*>(rel + (static_cast<long long>(rho) * H + h) * kHeadDim);
+#pragma unroll 4
+                    for (int d4 = 0; d4 < kHeadDim / 4; ++d4) {
+                        const float4 r4 = rr[d4];
+                        acc = fmaf(s_qv[i][4 * d4], r4.x, acc);
+                        acc = fmaf(s_qv[i][4 * d4 + 1], r4.y, acc);
+                        acc = fmaf(s_qv[i][4 * d4 + 2], r4.z, acc);
+                        acc = fmaf(s_qv[i][4 * d4 + 3], r4.w, acc);
+                    }
+                }
+                sc = acc * scale;
+            }
+            float mx = sc;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float m_new = fmaxf(m, mx);
+            const float alpha = (m == -INFINITY) ? 0.f : expf(m - m_new);
+            const float p = (j < K) ? expf(sc - m_new) : 0.f;
+            float psum = p;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) psum += __shfl_xor_sync(0xffffffffu, psum, o);
+            l = l * alpha + psum;
+            o0 *= alpha;
+            o1 *= alpha;
+            const float pv = p * vs;
+            const int nj = min(32, K - j0);
+            for (int jj = 0; jj < nj; ++jj) {
+                const float pj = __shfl_sync(0xffffffffu, pv, jj);
+                const long long ro = __shfl_sync(0xffffffffu, row_off, jj);
+                if (ro >= 0) {
+                    const float2 v2 = e4m3_unpack2(*reinterpret_cast<const uint16_t*>(v_pool + ro + 2 * lane));
+                    o0 = fmaf(pj, v2.x, o0);
+                    o1 = fmaf(pj, v2.y, o1);
+                }
+            }
+            m = m_new;
+        }
+        float2* dst = reinterpret_cast<float2*>(out + ((static_cast<long long>(b) * T + i) * H + h) * kHeadDim);
+        dst[lane] = make_float2(o0 / l, o1 / l);
+    }
+    if (err) atomicOr(status, err);
+}
+
+// --------------------------------------------------------------------------- host
+
+int g_smem_done_e4[8][64];
+
+// Row stride (bf16 elements) of the position table: every access stays below nkeys + 2 Tp, and a
+// stride of 16 mod 64 elements keeps the 4-byte reads of a slice conflict-free.
+inline int e4_table_stride(int nkeys, int Tp) { return ((nkeys + 2 * Tp + 63) & ~63) + 16; }
+
+template <int MT, int NS, int CTAS, bool FUSED>
+oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int slot, cudaStream_t stream)
+{
+    using SP = E4Smem<MT, NS>;
+    CUtensorMap tm_q, tm_k, tm_v;
+    const int box = a.block_size < kStageKeys ? a.block_size : kStageKeys;
+    const long long rows = static_cast<long long>(a.num_blocks) * a.H * a.block_size;
+    if (!encode_rows_bf16(&tm_q, q, static_cast<long long>(B) * a.T, a.H, SP::Tp) ||
+        !encode_rows_e4m3(&tm_k, a.k_pool, rows, box) || !encode_rows_e4m3(&tm_v, a.v_pool, rows, box))
+        return OASR_ERR_INVALID_ARG;
+    auto kern = chunk_e4m3_kernel<MT, NS, CTAS, FUSED>;
+    // segments of at most eight stages and a part of one, sized for the keys a call can have
+    const int stages = (k_max + kStageKeys - 1) / kStageKeys;
+    a.seg = stages < 9 ? stages : 9;
+    a.gt_w = e4_table_stride(a.seg * kStageKeys + (FUSED ? ((a.T + 15) & ~15) : 0), SP::Tp);
+    const int smem = SP::bytes + SP::Tp * a.gt_w * 2;
+    if (!ensure_smem(kern, smem, g_smem_done_e4[slot])) return OASR_ERR_CUDA;
+    a.q_tiles = (a.T + SP::Tp - 1) / SP::Tp;
+    const long long pairs = static_cast<long long>(B) * a.H * a.q_tiles;
+    const int sms = sm_count();
+    a.splits = 1;
+    while (a.splits < 8 && pairs * a.splits * 2 <= sms && stages >= 2 * a.splits) a.splits *= 2;
+    if (pairs * a.splits > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pairs * a.splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, static_cast<const E4Args>(a)) != cudaSuccess)
+        return OASR_ERR_CUDA;
+    return launch_status();
+}
+
+template <bool FUSED>
+oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                        void* kv_scale, int num_blocks, int block_size, const int32_t* bt, int mbps,
+                        const int32_t* cs, const void* u, const void* vb, const void* rel, int R, void* out, int B,
+                        int T, int H, int D, float scale, oasr_dtype dt, cudaStream_t stream)
+{
+    if (!q || !k_pool || !v_pool || !kv_scale || !bt || !cs || !u || !vb || !rel || !out)
+        return OASR_ERR_INVALID_ARG;
+    if (FUSED && (!k_new || !v_new)) return OASR_ERR_INVALID_ARG;
+    if (num_blocks <= 0 || block_size <= 0 || mbps <= 0 || R <= 0 || B <= 0 || T <= 0 || H <= 0 || D <= 0)
+        return OASR_ERR_INVALID_ARG;
+    if (dt != OASR_F32 && dt != OASR_BF16) return OASR_ERR_UNSUPPORTED;
+    if (D != kHeadDim || T > kE4MaxT) return OASR_ERR_UNSUPPORTED;
+    if (block_size < 8 || block_size > 256 || (block_size & (block_size - 1))) return OASR_ERR_UNSUPPORTED;
+    if (mbps > kE4MaxPages) return OASR_ERR_UNSUPPORTED;
+    // pool rows and query rows are 32-bit copy coordinates
+    if (static_cast<long long>(num_blocks) * H > 0x7fffffffLL / block_size ||
+        static_cast<long long>(B) * T > 0x7fffffffLL - 64 || static_cast<long long>(B) * H > 0x7fffffffLL)
+        return OASR_ERR_UNSUPPORTED;
+    const void* ptrs[] = {q, k_pool, v_pool, kv_scale, u, vb, rel, out, FUSED ? k_new : q, FUSED ? v_new : q};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return OASR_ERR_INVALID_ARG;
+    unsigned* status = status_word();
+    if (!status || !sm_count()) return OASR_ERR_CUDA;
+    if (dt == OASR_F32) {
+        if (FUSED) {
+            const oasr_status st = oasr_paged_append_e4m3(k_new, v_new, k_pool, v_pool, kv_scale, num_blocks,
+                                                          block_size, bt, mbps, cs, B, T, H, D, dt, stream);
+            if (st != OASR_OK) return st;
+        }
+        chunk_e4m3_f32_kernel<<<static_cast<unsigned>(B) * H, 128, 0, stream>>>(
+            static_cast<const float*>(q), static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool),
+            static_cast<const uint8_t*>(kv_scale), num_blocks, block_size, bt, mbps, cs,
+            static_cast<const float*>(u), static_cast<const float*>(vb), static_cast<const float*>(rel), R,
+            static_cast<float*>(out), T, H, scale, status);
+        return launch_status();
+    }
+    E4Args a = {};
+    a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    a.k_pool = static_cast<uint8_t*>(k_pool);
+    a.v_pool = static_cast<uint8_t*>(v_pool);
+    a.kv_scale = static_cast<uint8_t*>(kv_scale);
+    a.block_table = bt;
+    a.cache_seqlens = cs;
+    a.pos_bias_u = static_cast<const uint16_t*>(u);
+    a.pos_bias_v = static_cast<const uint16_t*>(vb);
+    a.rel = static_cast<const uint16_t*>(rel);
+    a.out = static_cast<uint16_t*>(out);
+    a.status = status;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.bs_shift = __builtin_ctz(static_cast<unsigned>(block_size));
+    a.mbps = mbps;
+    a.T = T;
+    a.H = H;
+    a.R = R;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    // keys a well-formed stream of the call can have
+    const long long pages = static_cast<long long>(mbps) * block_size, dist = static_cast<long long>(R) - T + 1;
+    const long long k_max = pages < dist ? pages : dist;
+    const int km = static_cast<int>(k_max < T ? T : k_max);
+    if (T <= 16) return launch_e4<1, 4, 3, FUSED>(q, a, km, B, FUSED ? 1 : 0, stream);
+    return launch_e4<2, 6, 2, FUSED>(q, a, km, B, FUSED ? 3 : 2, stream);
+}
+
+}  // namespace
+}  // namespace oasr
+
+extern "C" oasr_status oasr_chunk_relattn_paged_e4m3(
+    const void* q, const void* k_pool, const void* v_pool, const void* kv_scale, int num_blocks, int block_size,
+    const int32_t* block_table, int max_blocks_per_seq, const int32_t* cache_seqlens, const void* pos_bias_u,
+    const void* pos_bias_v, const void* rel, int R, void* out, int B, int T, int H, int D, float scale,
+    oasr_dtype dt, cudaStream_t stream)
+{
+    return oasr::dispatch_e4<false>(q, nullptr, nullptr, const_cast<void*>(k_pool), const_cast<void*>(v_pool),
+                                    const_cast<void*>(kv_scale), num_blocks, block_size, block_table,
+                                    max_blocks_per_seq, cache_seqlens, pos_bias_u, pos_bias_v, rel, R, out, B, T, H,
+                                    D, scale, dt, stream);
+}
+
+extern "C" oasr_status oasr_chunk_step_paged_e4m3(
+    const void* q, const void* k_new, const void* v_new, void* k_pool, void* v_pool, void* kv_scale, int num_blocks,
+    int block_size, const int32_t* block_table, int max_blocks_per_seq, const int32_t* cache_seqlens,
+    const void* pos_bias_u, const void* pos_bias_v, const void* rel, int R, void* out, int B, int T, int H, int D,
+    float scale, oasr_dtype dt, cudaStream_t stream)
+{
+    return oasr::dispatch_e4<true>(q, k_new, v_new, k_pool, v_pool, kv_scale, num_blocks, block_size, block_table,
+                                   max_blocks_per_seq, cache_seqlens, pos_bias_u, pos_bias_v, rel, R, out, B, T, H, D,
+                                   scale, dt, stream);
+}
