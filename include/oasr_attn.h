@@ -289,6 +289,43 @@ oasr_status oasr_chunk_step_paged_e4m3(const void* q, const void* k_new, const v
                                        const void* rel, int R, void* out, int B, int T, int H,
                                        int D, float scale, oasr_dtype dt, cudaStream_t stream);
 
+/*
+ * Quantise the rows of x ([M, K], `dt`) to 8-bit integers with one scale each: with
+ * m = max(max|x_row|, 2^-100) in fp32, x8 = rint(x * (127 / m)) ([M, K] int8, ties to even; both
+ * operations rounded to fp32) and scale = m / 127 ([M] fp32), so x is about x8 * scale.  A row with a
+ * NaN or an infinity gets zeros and a NaN scale, so that every result it enters is NaN.  Tokens are
+ * rows of activations, output channels rows of a weight [N, K].  K must be a multiple of 16.
+ */
+oasr_status oasr_quantize_rows(const void* x, void* x8, float* scale, int M, int K, oasr_dtype dt,
+                               cudaStream_t stream);
+
+/*
+ * Product of 8-bit integers with a scale per token and per output channel:
+ *
+ *   out[i][n] = (sum_k x8[i][k] * w8[n][k]) * x_scale[i] * w_scale[n] + bias[n]
+ *
+ * x8 [M, K] and w8 [N, K] int8, x_scale [M] and w_scale [N] fp32, bias [N] (null: none) and out [M, N]
+ * of `dt`.  The sum is exact for K <= 1024 and for M <= 8 and is accumulated in fp32 otherwise; the
+ * scales and the bias are applied in that order in fp32, and the result is rounded once.  K a multiple
+ * of 16, at most 65536; every pointer 16-byte aligned.
+ */
+oasr_status oasr_linear_w8a8(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
+                             const void* bias, void* out, int M, int N, int K, oasr_dtype dt,
+                             cudaStream_t stream);
+
+/*
+ * oasr_project_qkv_pos with 8-bit integer products (one launch): q | k | v from x8 [M, d_model] and
+ * w_qkv8 [3 d_model, d_model] with bias b_qkv [3 d_model], each written as [M, H, 64], and rel
+ * [R, H, 64] from pos8 [R, d_model] and w_pos8 [d_model, d_model], without bias.  Scales, rounding and
+ * the sums are those of oasr_linear_w8a8.  d_model = 64 H, at most 16384; outputs and bias of `dt`.
+ */
+oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_scale, const void* w_qkv8,
+                                      const float* w_qkv_scale, const void* b_qkv, const void* pos8,
+                                      const float* pos_scale, const void* w_pos8,
+                                      const float* w_pos_scale, void* q, void* k, void* v, void* rel,
+                                      int M, int R, int d_model, int H, oasr_dtype dt,
+                                      cudaStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* oasr_status_string(oasr_status status);
 

@@ -24,12 +24,14 @@ The offline pass over packed utterances is ``oasr_packed_relattn_varlen`` (or
 """
 from .capi import (OasrError, oasr_chunk_relattn_paged, oasr_chunk_relattn_paged_e4m3,  # noqa: F401
                    oasr_chunk_step_paged, oasr_chunk_step_paged_e4m3, oasr_device_status,
-                   oasr_packed_relattn_chunked, oasr_packed_relattn_varlen, oasr_paged_append,
-                   oasr_paged_append_e4m3, oasr_paged_read_e4m3, oasr_project_qkv_pos,
+                   oasr_linear_w8a8, oasr_packed_relattn_chunked, oasr_packed_relattn_varlen,
+                   oasr_paged_append, oasr_paged_append_e4m3, oasr_paged_read_e4m3,
+                   oasr_project_qkv_pos, oasr_project_qkv_pos_w8a8, oasr_quantize_rows,
                    oasr_selftest_wait, oasr_version, oasr_window_commit)
 
 __all__ = ["OasrError", "oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
            "oasr_packed_relattn_varlen", "oasr_packed_relattn_chunked", "oasr_window_commit",
            "oasr_project_qkv_pos", "oasr_paged_append_e4m3", "oasr_paged_read_e4m3",
-           "oasr_chunk_relattn_paged_e4m3", "oasr_chunk_step_paged_e4m3", "oasr_device_status",
+           "oasr_chunk_relattn_paged_e4m3", "oasr_chunk_step_paged_e4m3", "oasr_quantize_rows",
+           "oasr_linear_w8a8", "oasr_project_qkv_pos_w8a8", "oasr_device_status",
            "oasr_selftest_wait", "oasr_version"]

@@ -62,7 +62,11 @@ def load() -> ctypes.CDLL:
                                                     I, I, F, I, S]
         L.oasr_chunk_step_paged_e4m3.argtypes = [P, P, P, P, P, P, I, I, P, I, P, P, P, P, I, P, I,
                                                  I, I, I, F, I, S]
-        for fn in ("oasr_paged_append_e4m3", "oasr_paged_read_e4m3",
+        L.oasr_quantize_rows.argtypes = [P, P, P, I, I, I, S]
+        L.oasr_linear_w8a8.argtypes = [P, P, P, P, P, P, I, I, I, I, S]
+        L.oasr_project_qkv_pos_w8a8.argtypes = [P] * 13 + [I, I, I, I, I, S]
+        for fn in ("oasr_quantize_rows", "oasr_linear_w8a8", "oasr_project_qkv_pos_w8a8",
+                   "oasr_paged_append_e4m3", "oasr_paged_read_e4m3",
                    "oasr_chunk_relattn_paged_e4m3", "oasr_chunk_step_paged_e4m3",
                    "oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
                    "oasr_packed_relattn_varlen", "oasr_packed_relattn_chunked",
@@ -392,6 +396,71 @@ def oasr_chunk_step_paged_e4m3(q, k_new, v_new, k_pool, v_pool, kv_scale, block_
     return out
 
 
+def oasr_quantize_rows(x, x8=None, scale=None, stream=None):
+    """Rows of x [M,K] as 8-bit integers with a scale each; returns (x8 int8 [M,K], scale
+    float32 [M])."""
+    L = load()
+    M, K = x.shape
+    x8 = torch.empty((M, K), dtype=torch.int8, device=x.device) if x8 is None else x8
+    scale = torch.empty((M,), dtype=torch.float32, device=x.device) if scale is None else scale
+    if tuple(x8.shape) != (M, K) or tuple(scale.shape) != (M,):
+        raise ValueError("x8 must be [M, K] and scale [M]")
+    _check("oasr_quantize_rows", L.oasr_quantize_rows(
+        _dev(x, "x", x.dtype), _dev(x8, "x8", torch.int8), _dev(scale, "scale", torch.float32), M, K,
+        _dtype_code(x), _stream(stream)))
+    return x8, scale
+
+
+def oasr_linear_w8a8(x8, x_scale, w8, w_scale, bias=None, out=None, out_dtype=torch.bfloat16,
+                     stream=None):
+    """(x8 . w8^T) * x_scale[:, None] * w_scale + bias from int8 x8 [M,K], w8 [N,K]; returns out
+    [M,N] of ``out_dtype`` (or of the out given)."""
+    L = load()
+    M, K = x8.shape
+    N = w8.shape[0]
+    if w8.dim() != 2 or w8.shape[1] != K or tuple(x_scale.shape) != (M,) or tuple(w_scale.shape) != (N,):
+        raise ValueError("shapes: x8 [M,K], x_scale [M], w8 [N,K], w_scale [N]")
+    out = torch.empty((M, N), dtype=out_dtype, device=x8.device) if out is None else out
+    if tuple(out.shape) != (M, N) or (bias is not None and tuple(bias.shape) != (N,)):
+        raise ValueError("out must be [M, N] and bias [N]")
+    _check("oasr_linear_w8a8", L.oasr_linear_w8a8(
+        _dev(x8, "x8", torch.int8), _dev(x_scale, "x_scale", torch.float32),
+        _dev(w8, "w8", torch.int8), _dev(w_scale, "w_scale", torch.float32),
+        None if bias is None else _dev(bias, "bias", out.dtype), _dev(out, "out", out.dtype), M, N,
+        K, _dtype_code(out), _stream(stream)))
+    return out
+
+
+def oasr_project_qkv_pos_w8a8(x8, x_scale, w_qkv8, w_qkv_scale, b_qkv, pos8, pos_scale, w_pos8,
+                              w_pos_scale, H, q=None, k=None, v=None, rel=None, stream=None):
+    """q, k, v [M,H,64] and rel [R,H,64] by 8-bit integer products, one launch; the outputs have
+    b_qkv's dtype.  Returns (q, k, v, rel)."""
+    L = load()
+    M, d = x8.shape
+    R = pos8.shape[0]
+    if tuple(w_qkv8.shape) != (3 * d, d) or tuple(w_qkv_scale.shape) != (3 * d,) or \
+            tuple(b_qkv.shape) != (3 * d,) or tuple(pos8.shape) != (R, d) or \
+            tuple(w_pos8.shape) != (d, d) or tuple(w_pos_scale.shape) != (d,) or \
+            tuple(x_scale.shape) != (M,) or tuple(pos_scale.shape) != (R,) or d % H:
+        raise ValueError("shapes: x8 [M,d], x_scale [M], w_qkv8 [3d,d], w_qkv_scale and b_qkv [3d], "
+                         "pos8 [R,d], pos_scale [R], w_pos8 [d,d], w_pos_scale [d]")
+    D, dt, dv = d // H, b_qkv.dtype, x8.device
+    q = torch.empty((M, H, D), dtype=dt, device=dv) if q is None else q
+    k = torch.empty((M, H, D), dtype=dt, device=dv) if k is None else k
+    v = torch.empty((M, H, D), dtype=dt, device=dv) if v is None else v
+    rel = torch.empty((R, H, D), dtype=dt, device=dv) if rel is None else rel
+    if any(tuple(t.shape) != (M, H, D) for t in (q, k, v)) or tuple(rel.shape) != (R, H, D):
+        raise ValueError("q, k, v must be [M, H, d/H] and rel [R, H, d/H]")
+    _check("oasr_project_qkv_pos_w8a8", L.oasr_project_qkv_pos_w8a8(
+        _dev(x8, "x8", torch.int8), _dev(x_scale, "x_scale", torch.float32),
+        _dev(w_qkv8, "w_qkv8", torch.int8), _dev(w_qkv_scale, "w_qkv_scale", torch.float32),
+        _dev(b_qkv, "b_qkv", dt), _dev(pos8, "pos8", torch.int8),
+        _dev(pos_scale, "pos_scale", torch.float32), _dev(w_pos8, "w_pos8", torch.int8),
+        _dev(w_pos_scale, "w_pos_scale", torch.float32), _dev(q, "q", dt), _dev(k, "k", dt),
+        _dev(v, "v", dt), _dev(rel, "rel", dt), M, R, d, H, _dtype_code(b_qkv), _stream(stream)))
+    return q, k, v, rel
+
+
 def oasr_device_status(clear: bool = True) -> int:
     """Raw device status bits (1 = an index was out of range, 2 = a wait timed out)."""
     L = load()
@@ -432,5 +501,6 @@ if NVTX:
                   "oasr_packed_relattn_varlen", "oasr_packed_relattn_chunked", "oasr_window_commit",
                   "oasr_project_qkv_pos", "oasr_selftest_wait", "oasr_paged_append_e4m3",
                   "oasr_paged_read_e4m3", "oasr_chunk_relattn_paged_e4m3",
-                  "oasr_chunk_step_paged_e4m3"):
+                  "oasr_chunk_step_paged_e4m3", "oasr_quantize_rows", "oasr_linear_w8a8",
+                  "oasr_project_qkv_pos_w8a8"):
         globals()[_name] = _traced(globals()[_name])
