@@ -291,8 +291,8 @@ oasr_status oasr_chunk_step_paged_e4m3(const void* q, const void* k_new, const v
 
 /*
  * Quantise the rows of x ([M, K], `dt`) to 8-bit integers with one scale each: with
- * m = max(max|x_row|, 2^-100) in fp32, x8 = rint(x * (127 / m)) ([M, K] int8, ties to even; both
- * operations rounded to fp32) and scale = m / 127 ([M] fp32), so x is about x8 * scale.  A row with a
+ * m = max(max|x_row|, 2^-100) in fp32, x8 = rint(x * (127 * (1 / m))) ([M, K] int8, ties to even; each
+ * of the three operations rounded to fp32) and scale = m / 127 ([M] fp32), so x is about x8 * scale.  A row with a
  * NaN or an infinity gets zeros and a NaN scale, so that every result it enters is NaN.  Tokens are
  * rows of activations, output channels rows of a weight [N, K].  K must be a multiple of 16.
  */

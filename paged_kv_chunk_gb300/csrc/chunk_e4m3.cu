@@ -7,11 +7,12 @@
 //   out_i = sum_j softmax(s_i)_j 2^ev_j v8_j
 //
 // The scales stay out of the products: 2^ek multiplies the accumulated score of its key (one fused
-// multiply-add with the position term) and 2^ev the probability of its key before that is rounded
-// to bf16.  Both are exact, so the result is that of the 16-bit computation on the read-back rows.
-// k8 and v8 go into the bf16 matrix instructions as themselves: e4m3's exponent and fraction,
-// shifted into a bf16's, are the value times 2^-120, subnormals included, and one packed multiply
-// by 2^120 gives it back (e4m3_to_bf16).
+// multiply-add with the position term) and 2^ev adds ev to the exponent of its key's weight; both are
+// exact.  k8 and v8 go into fp16 matrix instructions: e4m3's exponent and fraction, shifted into an
+// fp16's, are the value times 2^-8, subnormals included, for three or four integer instructions per
+// two values.  fp16 holds q + u (each query row scaled by a power of two) and the weights with three
+// bits more than bf16 would: rms error against 64 bits 0.0021 of the output's on random data, 0.0031
+// with bf16 (0.0017 is the rounding of the output itself).
 //
 // One CTA per (stream, head, block of up to 32 queries, share of the keys): four consumer warps and
 // a producer warp.  The producer brings stages of 64 keys by TMA (a box of K and one of V per page,
@@ -35,6 +36,7 @@ namespace {
 constexpr int kE4MaxPages = 512;              // block-table entries a CTA caches
 constexpr int kE4Stage = 2 * kStageKeys * kE4Row;   // K and V rows of a stage
 constexpr int kE4MaxT = 64;
+constexpr int kMaxRowExp = 120;
 
 struct E4Args {
     const __nv_bfloat16* k_new;   // fused only
@@ -67,7 +69,8 @@ struct E4Smem {
     static constexpr int off_csc = off_sc + NS * 2 * kStageKeys;      // the chunk's [2][64]
     static constexpr int off_u = off_csc + 2 * kE4MaxT;
     static constexpr int off_vb = off_u + kHeadDim * 4;
-    static constexpr int off_bt = off_vb + kHeadDim * 4;
+    static constexpr int off_re = off_vb + kHeadDim * 4;              // the query rows' exponents
+    static constexpr int off_bt = off_re + Tp * 4;
     static constexpr int off_bar = off_bt + kE4MaxPages * 4;          // full[NS], empty[NS], q
     static constexpr int off_gt = (off_bar + (2 * NS + 1) * 8 + 15) & ~15;
     static constexpr int bytes = off_gt + 1024;                       // + Tp * gt_w * 2
@@ -89,15 +92,25 @@ __device__ __forceinline__ uint32_t swz64(int r, int c)
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// Bytes 0, 2 (lo) and 1, 3 (hi) of w, e4m3, as pairs of bf16 times 2^-120 ...
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) { return ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u); }
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) { return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u); }
-// ... and the packed multiply that makes them the values themselves (exact).
-__device__ __forceinline__ uint32_t times_2p120(uint32_t x)
+// Bytes 0, 2 (lo) and 1, 3 (hi) of w, e4m3, as pairs of fp16 times 2^-8: e4m3's exponent and
+// fraction in the low bits of an fp16's, subnormals included (all exact, all finite).
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) { return ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u); }
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) { return ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u); }
+
+// D += A (16x16 fp16, row) * B (16x8 fp16, col), fp32 accumulators.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
-    return r;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
 }
 
 // A slice of 16 keys in registers: its raw K and V words and its scales.
@@ -129,36 +142,147 @@ __device__ __forceinline__ void load_slice(E4Slice& x, uint32_t k_s, uint32_t v_
     x.vs = *reinterpret_cast<const uint16_t*>(p) | (*reinterpret_cast<const uint16_t*>(p + next8) << 16);
 }
 
-// A fragments of bf16(q + u) for 16 query rows, the head dimension in the order of the e4m3
+// Words of a query row's dims 16 t4 .. 16 t4 + 15 (128-byte-swizzled Q tile).
+__device__ __forceinline__ void q_words(uint32_t (&w)[8], const uint8_t* q_tile, int row, int t4)
+{
+    const uint4 c0 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4));
+    const uint4 c1 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4 + 1));
+    w[0] = c0.x; w[1] = c0.y; w[2] = c0.z; w[3] = c0.w;
+    w[4] = c1.x; w[5] = c1.y; w[6] = c1.z; w[7] = c1.w;
+}
+
+// Power of two, as an exponent, that brings the largest |q + u| of a row into [1, 2).
+__device__ __forceinline__ int row_exponent(const uint8_t* q_tile, const float* u, int row, int t4)
+{
+    uint32_t w[8];
+    q_words(w, q_tile, row, t4);
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i]) + u[16 * t4 + 2 * i]), fabsf(bf16_hi(w[i]) + u[16 * t4 + 2 * i + 1])));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int x = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+    return max(-kMaxRowExp, min(kMaxRowExp, x));
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// A fragments of fp16((q + u) 2^-x) for 16 query rows, the head dimension in the order of the e4m3
 // words: quad position t4 holds dims 16 t4 .., k-step ks the word 4 ks, its bytes 0, 2 then 1, 3.
 __device__ __forceinline__ void make_qu_e4m3(uint32_t (&qu)[4][4], const uint8_t* q_tile, const float* u,
-                                             int mt, int lane)
+                                             const int* row_exp, int mt, int lane)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int row = 16 * mt + g4 + 8 * half;
-        const uint4 c0 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4));
-        const uint4 c1 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4 + 1));
-        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float f = pow2(-row_exp[row]);
+        uint32_t w[8];
+        q_words(w, q_tile, row, t4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             const float* b = u + 16 * t4 + 4 * ks;
-            const float d0 = bf16_lo(w[2 * ks]) + b[0], d1 = bf16_hi(w[2 * ks]) + b[1];
-            const float d2 = bf16_lo(w[2 * ks + 1]) + b[2], d3 = bf16_hi(w[2 * ks + 1]) + b[3];
-            qu[ks][half] = pack_bf16(d0, d2);
-            qu[ks][half + 2] = pack_bf16(d1, d3);
+            const float d0 = (bf16_lo(w[2 * ks]) + b[0]) * f, d1 = (bf16_hi(w[2 * ks]) + b[1]) * f;
+            const float d2 = (bf16_lo(w[2 * ks + 1]) + b[2]) * f, d3 = (bf16_hi(w[2 * ks + 1]) + b[3]) * f;
+            qu[ks][half] = pack_f16(d0, d2);
+            qu[ks][half + 2] = pack_f16(d1, d3);
         }
     }
 }
 
+// The position table of one segment (PosTable in attn_core.cuh), each row times its 2^-x: the CTA's
+// Tp query rows against rel rows rho0 .. rho0 + ncols - 1, G[i][c] at gs[i * W + c + i + 1], so that query i
+// and the segment's key j read gs[i * W + j + Tp].  BATCH column tiles of a warp are in flight together.
+template <int BATCH, int MT>
+struct E4Table {
+    const uint16_t* rel_h;
+    long long stride;
+    int R, rho0, ncols, warp, lane;
+    uint4 bl[BATCH], bh[BATCH];
+
+    __device__ __forceinline__ int ntiles() const { return (ncols + 7) >> 3; }
+
+    __device__ __forceinline__ void load(int nb0)
+    {
+        const int g4 = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int rho = rho0 + 8 * (nb0 + u * kConsumerWarps) + g4;
+            bl[u] = bh[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (nb0 + u * kConsumerWarps < ntiles() && rho >= 0 && rho < R) {
+                const uint4* src = reinterpret_cast<const uint4*>(rel_h + rho * stride + 16 * t4);
+                bl[u] = __ldg(src);
+                bh[u] = __ldg(src + 1);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void build(uint16_t* gs, int W, const uint8_t* q_tile, const float* v, const int* row_exp)
+    {
+        const int g4 = lane >> 2, t4 = lane & 3;
+        uint32_t qa[MT][4][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = 16 * mt + g4 + 8 * half;
+                const float f = pow2(-row_exp[row]);
+                uint32_t w[8];
+                q_words(w, q_tile, row, t4);
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+                    qa[mt][m >> 1][half + 2 * (m & 1)] = pack_bf16((bf16_lo(w[m]) + v[16 * t4 + 2 * m]) * f,
+                                                                   (bf16_hi(w[m]) + v[16 * t4 + 2 * m + 1]) * f);
+            }
+        for (int nb0 = warp; nb0 < ntiles(); nb0 += BATCH * kConsumerWarps) {
+            if (nb0 != warp) load(nb0);
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const int col = 8 * (nb0 + u * kConsumerWarps) + 2 * t4;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_bf16_16816(c, qa[mt][0], bl[u].x, bl[u].y);
+                    mma_bf16_16816(c, qa[mt][1], bl[u].z, bl[u].w);
+                    mma_bf16_16816(c, qa[mt][2], bh[u].x, bh[u].y);
+                    mma_bf16_16816(c, qa[mt][3], bh[u].z, bh[u].w);
+                    const int i = 16 * mt + g4;
+                    uint16_t* d = gs + i * W + col + i + 1;
+                    if (col < ncols) {
+                        d[0] = bf16_bits(c[0]);
+                        d[8 * W + 8] = bf16_bits(c[2]);
+                    }
+                    if (col + 1 < ncols) {
+                        d[1] = bf16_bits(c[1]);
+                        d[8 * W + 9] = bf16_bits(c[3]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+// Running state of 16 query rows of one warp.  With t_ij = s_ij + ev_j (log2 units: the size of key j's
+// contribution to the output), m is the running maximum of t, o the sum of 2^(t - m) v8 2^-8 and l the
+// sum of 2^(s - m + E), where E is within 20 of the largest V scale exponent so far.
+struct E4Acc {
+    float o[8][4];   // o[2c + e]: dims 16 c + 4 t4 + e, + 2 + e of row g4, then of row g4 + 8
+    float m[2], l[2];
+};
+
 // One warp, 16 MT query rows against one slice.  gq: the position table at the slice's first key
-// (key jl of query row i reads gq[i * W + jl]); keys [0, kvalid) of the slice exist.
-// acc.o[mt][2c + e] holds dims 16 c + 4 t4 + e and + 2 + e of rows g4 and g4 + 8.
+// (key jl of query row i reads gq[i * W + jl]); keys [0, kvalid) of the slice exist; sc: scale * log2(e) * 2^x of
+// rows g4 and g4 + 8 of each m-tile.
+//
+// P is 2^(t - m), at most one, and goes into the product as fp16: its rounding is 2^-11 of each
+// weight and never more than 2^-25 of the row's largest contribution, whatever the scales.  The
+// row sum takes p back out of it, l += P 2^(E - ev); a slice with a scale below 2^(E - 40) (a row of
+// zeros has 2^-100), where that could underflow, sums 2^(s - m + E) of its own.
 template <int MT>
-__device__ __forceinline__ void slice_e4m3(WarpAcc (&acc)[MT], const uint32_t (&qu)[MT][4][4], E4Slice& x,
-                                           const uint16_t* gq, int W, bool even, int kvalid, float scale_log2,
-                                           int lane)
+__device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu)[MT][4][4], const E4Slice& x,
+                                           const uint16_t* gq, int W, bool even, int kvalid,
+                                           const float (&sc)[MT][2], int& E, int lane)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
     float s[MT][2][4];
@@ -171,32 +295,42 @@ __device__ __forceinline__ void slice_e4m3(WarpAcc (&acc)[MT], const uint32_t (&
         const uint32_t w[4] = {x.k[n].x, x.k[n].y, x.k[n].z, x.k[n].w};
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t b0 = times_2p120(e4m3_lo(w[ks])), b1 = times_2p120(e4m3_hi(w[ks]));
+            const uint32_t b0 = e4m3_lo(w[ks]), b1 = e4m3_hi(w[ks]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma_bf16_16816(s[mt][n], qu[mt][ks], b0, b1);
+            for (int mt = 0; mt < MT; ++mt) mma_f16_16816(s[mt][n], qu[mt][ks], b0, b1);
         }
     }
-    float ks[4], vs[4];   // keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
-    const bool tail = kvalid < 16;
+    // keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4: 2^(ek + 8), ev and 2^(E - ev)
+    float ks[4], ev[4], back[4];
+    int v[4];
+    bool odd = false;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        ks[e] = e4m3_scale((x.ks >> (8 * e)) & 255u);
-        vs[e] = e4m3_scale((x.vs >> (8 * e)) & 255u);
+        const int jl = 2 * t4 + (e & 1) + 8 * (e >> 1);
+        ks[e] = e4m3_scale((x.ks >> (8 * e)) & 255u) * 256.f;
+        v[e] = static_cast<int>((x.vs >> (8 * e)) & 255u) - 127;
+        if (jl >= kvalid) v[e] = E;          // rows past the last key may hold anything
+        odd |= static_cast<unsigned>(v[e] - E + 40) > 60u;
     }
-    if (tail) {   // rows past the last key may hold anything: their scales and V bytes are dropped
-        const int k0 = 2 * t4;
+    bool far = false;
+    float dE = 0.f;
+    if (__any_sync(0xffffffffu, odd)) {
+        const int top = __reduce_max_sync(0xffffffffu, max(max(v[0], v[1]), max(v[2], v[3])));
+        if (top > E + 20) {
+            dE = static_cast<float>(top - E);
+            E = top;
+        }
+        far = __any_sync(0xffffffffu, min(min(v[0], v[1]), min(v[2], v[3])) < E - 40);
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (k0 + (e & 1) + 8 * (e >> 1) >= kvalid) vs[e] = 0.f;
-        const uint32_t m0 = (k0 < kvalid ? 0xffffu : 0u) | (k0 + 1 < kvalid ? 0xffff0000u : 0u);
-        const uint32_t m1 = (k0 + 8 < kvalid ? 0xffffu : 0u) | (k0 + 9 < kvalid ? 0xffff0000u : 0u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x.v[i] &= (i & 1) ? m1 : m0;
+    for (int e = 0; e < 4; ++e) {
+        ev[e] = v[e] == 128 ? NAN : static_cast<float>(v[e]);
+        back[e] = far ? 0.f : pow2(E - v[e]);
     }
     uint32_t pa[MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-        WarpAcc& a = acc[mt];
+        E4Acc& a = acc[mt];
         float mx0 = a.m[0], mx1 = a.m[1];
         const uint16_t* r0 = gq + (16 * mt + g4) * W + 2 * t4;
         const uint16_t* r1 = r0 + 8 * W;
@@ -218,11 +352,12 @@ __device__ __forceinline__ void slice_e4m3(WarpAcc (&acc)[MT], const uint32_t (&
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+                const int k = 2 * n + (e & 1);
                 const bool ok = 8 * n + 2 * t4 + (e & 1) < kvalid;
-                s[mt][n][e] = ok ? fmaf(s[mt][n][e], ks[2 * n + (e & 1)], gb[e]) * scale_log2 : -INFINITY;
+                s[mt][n][e] = ok ? fmaf(fmaf(s[mt][n][e], ks[k], gb[e]), sc[mt][e >> 1], ev[k]) : -INFINITY;
             }
-            mx0 = fmaxf(mx0, fmaxf(s[mt][n][0], s[mt][n][1]));
-            mx1 = fmaxf(mx1, fmaxf(s[mt][n][2], s[mt][n][3]));
+            mx0 = fmax3(mx0, s[mt][n][0], s[mt][n][1]);
+            mx1 = fmax3(mx1, s[mt][n][2], s[mt][n][3]);
         }
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
@@ -230,11 +365,11 @@ __device__ __forceinline__ void slice_e4m3(WarpAcc (&acc)[MT], const uint32_t (&
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
         const float base0 = (mx0 == -INFINITY) ? 0.f : mx0;
         const float base1 = (mx1 == -INFINITY) ? 0.f : mx1;
-        if (mx0 != a.m[0] || mx1 != a.m[1]) {
+        if (mx0 != a.m[0] || mx1 != a.m[1] || dE != 0.f) {
             const float alpha0 = ex2_approx(a.m[0] - base0);
             const float alpha1 = ex2_approx(a.m[1] - base1);
-            a.l[0] *= alpha0;
-            a.l[1] *= alpha1;
+            a.l[0] *= ex2_approx(fminf(a.m[0] - base0 + dE, 126.f));
+            a.l[1] *= ex2_approx(fminf(a.m[1] - base1 + dE, 126.f));
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
                 a.o[d][0] *= alpha0;
@@ -245,27 +380,37 @@ __device__ __forceinline__ void slice_e4m3(WarpAcc (&acc)[MT], const uint32_t (&
             a.m[0] = mx0;
             a.m[1] = mx1;
         }
+        if (far) {
+            const float off = static_cast<float>(E);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = 2 * n + e;
+                    a.l[0] += ex2_approx(s[mt][n][e] - ev[k] - base0 + off);
+                    a.l[1] += ex2_approx(s[mt][n][2 + e] - ev[k] - base1 + off);
+                }
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             s[mt][n][0] = ex2_approx(s[mt][n][0] - base0);
             s[mt][n][1] = ex2_approx(s[mt][n][1] - base0);
             s[mt][n][2] = ex2_approx(s[mt][n][2] - base1);
             s[mt][n][3] = ex2_approx(s[mt][n][3] - base1);
-            a.l[0] += s[mt][n][0] + s[mt][n][1];
-            a.l[1] += s[mt][n][2] + s[mt][n][3];
-            pa[mt][2 * n] = pack_bf16(s[mt][n][0] * vs[2 * n], s[mt][n][1] * vs[2 * n + 1]);
-            pa[mt][2 * n + 1] = pack_bf16(s[mt][n][2] * vs[2 * n], s[mt][n][3] * vs[2 * n + 1]);
+            a.l[0] = fmaf(s[mt][n][0], back[2 * n], fmaf(s[mt][n][1], back[2 * n + 1], a.l[0]));
+            a.l[1] = fmaf(s[mt][n][2], back[2 * n], fmaf(s[mt][n][3], back[2 * n + 1], a.l[1]));
+            pa[mt][2 * n] = pack_f16(s[mt][n][0], s[mt][n][1]);
+            pa[mt][2 * n + 1] = pack_f16(s[mt][n][2], s[mt][n][3]);
         }
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const uint32_t w0 = x.v[2 * c], w1 = x.v[2 * c + 1];
-        const uint32_t e0 = times_2p120(e4m3_lo(w0)), e1 = times_2p120(e4m3_lo(w1));
-        const uint32_t d0 = times_2p120(e4m3_hi(w0)), d1 = times_2p120(e4m3_hi(w1));
+        const uint32_t e0 = e4m3_lo(w0), e1 = e4m3_lo(w1), d0 = e4m3_hi(w0), d1 = e4m3_hi(w1);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            mma_bf16_16816(acc[mt].o[2 * c], pa[mt], e0, e1);
-            mma_bf16_16816(acc[mt].o[2 * c + 1], pa[mt], d0, d1);
+            mma_f16_16816(acc[mt].o[2 * c], pa[mt], e0, e1);
+            mma_f16_16816(acc[mt].o[2 * c + 1], pa[mt], d0, d1);
         }
     }
 }
@@ -303,6 +448,14 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
+
+// Weight of a share whose maximum (log2) is `x` against the largest, `top`; a share without keys has
+// -inf and weight 0.
+//
+// Shares of a row are joined from o, m and lambda = log2(sum of 2^s) = m - E + log2(l): the V scales
+// move m away from the scores (a share of zero rows has an m of s - 100), so the row sum has a
+// maximum of its own.  out = 2^8 sum(o 2^(m - m*)) 2^(m* - lambda*) / sum(2^(lambda - lambda*)).
+__device__ __forceinline__ float part_weight(float x, float top) { return x == -INFINITY ? 0.f : ex2_approx(x - top); }
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -461,9 +614,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
 
     // ---------------------------------------------------------------- consumers
     bool failed = false;
-    WarpAcc acc[MT];
+    E4Acc acc[MT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc_init(acc[mt]);
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) acc[mt].o[d][0] = acc[mt].o[d][1] = acc[mt].o[d][2] = acc[mt].o[d][3] = 0.f;
+        acc[mt].m[0] = acc[mt].m[1] = -INFINITY;
+        acc[mt].l[0] = acc[mt].l[1] = 0.f;
+    }
+    int E = -127;   // the smallest a scale byte says; the first keys raise it
     uint16_t* gs = reinterpret_cast<uint16_t*>(sm + SP::off_gt);
     const int W = a.gt_w;
     if (FUSED && chunk_here) {
@@ -496,14 +655,19 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             if (l8 == 0) sm[SP::off_csc + kv * kE4MaxT + t] = static_cast<uint8_t>(byte);
         }
     }
-    PosTable<MT == 1 ? 5 : 4, MT> pt;
+    E4Table<MT == 1 ? 5 : 4, MT> pt;
     pt.rel_h = a.rel + h * kHeadDim;
     pt.stride = static_cast<long long>(H) * kHeadDim;
     pt.R = a.R;
     pt.warp = warp;
-    pt.nw = kConsumerWarps;
     pt.lane = lane;
     if (!e4_wait(bar_q, 0)) failed = true;
+    int* s_re = reinterpret_cast<int*>(sm + SP::off_re);
+    if (warp < 2 * MT) {   // eight query rows a warp
+        const int x = row_exponent(sm + SP::off_q, s_u, 8 * warp + (lane >> 2), lane & 3);
+        if ((lane & 3) == 0) s_re[8 * warp + (lane >> 2)] = x;
+    }
+    named_bar_sync(1, 32 * kConsumerWarps);   // the rows' exponents are known
     const int jl = 16 * warp;   // this warp's keys of a stage
     const int next8 = box == 8 ? 16 : 8;   // scales of keys 8 .. 15 of a slice, from those of keys 0 .. 7
     const int sc_off = ((jl >> box_sh) << (box_sh + 1)) + (jl & (box - 1));
@@ -519,13 +683,19 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 pt.rho0 = off + jbase - i0 - (Tp - 1);
                 pt.ncols = nkeys + Tp - 1;
                 pt.load(warp);
-                pt.build(gs, W, sm + SP::off_q, s_vb);
+                pt.build(gs, W, sm + SP::off_q, s_vb, s_re);
             }
             named_bar_sync(1, 32 * kConsumerWarps);   // the table (and the chunk region) are complete
         }
         uint32_t qu[MT][4][4];   // made per segment: they would not fit beside the table's operands
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) make_qu_e4m3(qu[mt], sm + SP::off_q, s_u, mt, lane);
+        for (int mt = 0; mt < MT; ++mt) make_qu_e4m3(qu[mt], sm + SP::off_q, s_u, s_re, mt, lane);
+        float sc[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            sc[mt][0] = a.scale_log2 * pow2(s_re[16 * mt + (lane >> 2)]);
+            sc[mt][1] = a.scale_log2 * pow2(s_re[16 * mt + (lane >> 2) + 8]);
+        }
         for (int s = seg0; s < seg1; ++s) {
             const int it = s - st0, slot = it % NS;
             if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
@@ -537,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             mbar_arrive_release(bar_empty + 8 * slot);
             if (kv > 0) {
                 const int x0 = (s - seg0) * kStageKeys + jl + Tp;
-                slice_e4m3<MT>(acc, qu, x, gs + x0, W, true, kv, a.scale_log2, lane);
+                slice_e4m3<MT>(acc, qu, x, gs + x0, W, true, kv, sc, E, lane);
             }
         }
         if (last) {
@@ -546,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 load_slice(x, sb + SP::off_ck + jl * kE4Row, sb + SP::off_ck + (kE4MaxT + jl) * kE4Row,
                            sm + SP::off_csc + jl, 8, kE4MaxT, lane);
                 const int x0 = C + jl - jbase + Tp;
-                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 1) == 0, nc - jl, a.scale_log2, lane);
+                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 1) == 0, nc - jl, sc, E, lane);
             }
             break;
         }
@@ -565,9 +735,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         const int g4 = lane >> 2, t4 = lane & 3;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            acc_reduce_l(acc[mt]);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                float l = acc[mt].l[half];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
                 const int r = warp * Tp + 16 * mt + g4 + 8 * half;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -576,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                                     acc[mt].o[2 * c][2 * half + 1], acc[mt].o[2 * c + 1][2 * half + 1]);
                 if (t4 == 0) {
                     comb_m[r] = acc[mt].m[half];
-                    comb_l[r] = acc[mt].l[half];
+                    comb_l[r] = acc[mt].m[half] - static_cast<float>(E) + log2f(l);
                 }
             }
         }
@@ -585,51 +757,72 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     if (S == 1) {
         for (int i = tid; i < Tq * 8; i += 32 * kConsumerWarps) {
             const int row = i >> 3, d0 = (i & 7) * 8;
-            const uint4 v = combine_row8(comb_o, comb_m, comb_l, kConsumerWarps, Tp, row, d0);
-            *reinterpret_cast<uint4*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim + d0) = v;
+            float m = comb_m[row], l = comb_l[row];
+#pragma unroll
+            for (int k = 1; k < kConsumerWarps; ++k) {
+                m = fmaxf(m, comb_m[k * Tp + row]);
+                l = fmaxf(l, comb_l[k * Tp + row]);
+            }
+            float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kConsumerWarps; ++k) {
+                const float w = part_weight(comb_m[k * Tp + row], m);
+                sum += part_weight(comb_l[k * Tp + row], l);
+                const float4* src = reinterpret_cast<const float4*>(comb_o + (k * Tp + row) * kOW + d0);
+                const float4 x = src[0], y = src[1];
+                o[0] += w * x.x; o[1] += w * x.y; o[2] += w * x.z; o[3] += w * x.w;
+                o[4] += w * y.x; o[5] += w * y.y; o[6] += w * y.z; o[7] += w * y.w;
+            }
+            const float f = exp2f(m - l + 8.f) / sum;
+            *reinterpret_cast<uint4*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim + d0) =
+                make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
+                           pack_bf16(o[6] * f, o[7] * f));
         }
         return;
     }
-    // the CTA's share, unnormalised: a warp without keys has a maximum of -inf and weight 0
+    // the CTA's share
     float* part_o = reinterpret_cast<float*>(sm + SP::part_o);
     float* part_m = reinterpret_cast<float*>(sm + SP::part_m);
     float* part_l = reinterpret_cast<float*>(sm + SP::part_l);
     for (int i = tid; i < Tq * kHeadDim; i += 32 * kConsumerWarps) {
         const int row = i / kHeadDim, d = i % kHeadDim;
-        float m = -INFINITY, o = 0.f, l = 0.f;
+        float m = -INFINITY, l = -INFINITY, o = 0.f, sum = 0.f;
         if (!s_failed) {
 #pragma unroll
-            for (int k = 0; k < kConsumerWarps; ++k) m = fmaxf(m, comb_m[k * Tp + row]);
+            for (int k = 0; k < kConsumerWarps; ++k) {
+                m = fmaxf(m, comb_m[k * Tp + row]);
+                l = fmaxf(l, comb_l[k * Tp + row]);
+            }
 #pragma unroll
             for (int k = 0; k < kConsumerWarps; ++k) {
-                const float mk = comb_m[k * Tp + row];
-                const float w = (mk == -INFINITY) ? 0.f : ex2_approx(mk - m);
-                l += w * comb_l[k * Tp + row];
-                o += w * comb_o[(k * Tp + row) * kOW + d];
+                o += part_weight(comb_m[k * Tp + row], m) * comb_o[(k * Tp + row) * kOW + d];
+                sum += part_weight(comb_l[k * Tp + row], l);
             }
         }
         part_o[i] = o;
         if (d == 0) {
             part_m[row] = m;
-            part_l[row] = l;
+            part_l[row] = l + log2f(sum);
         }
     }
     cluster_sync();
     // rows split, split + S, ... of the cluster's queries are finished here
     for (int row = split + S * warp; row < Tq; row += S * kConsumerWarps) {
-        float m = -INFINITY;
-        for (int k = 0; k < S; ++k) m = fmaxf(m, ld_cluster(sb + SP::part_m + 4 * row, k));
-        float l = 0.f, o0 = 0.f, o1 = 0.f;
+        float m = -INFINITY, l = -INFINITY;
         for (int k = 0; k < S; ++k) {
-            const float mk = ld_cluster(sb + SP::part_m + 4 * row, k);
-            const float w = (mk == -INFINITY) ? 0.f : ex2_approx(mk - m);
-            l += w * ld_cluster(sb + SP::part_l + 4 * row, k);
+            m = fmaxf(m, ld_cluster(sb + SP::part_m + 4 * row, k));
+            l = fmaxf(l, ld_cluster(sb + SP::part_l + 4 * row, k));
+        }
+        float o0 = 0.f, o1 = 0.f, sum = 0.f;
+        for (int k = 0; k < S; ++k) {
+            const float w = part_weight(ld_cluster(sb + SP::part_m + 4 * row, k), m);
+            sum += part_weight(ld_cluster(sb + SP::part_l + 4 * row, k), l);
             o0 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane), k);
             o1 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane + 1), k);
         }
-        const float inv = 1.f / l;
+        const float f = exp2f(m - l + 8.f) / sum;
         reinterpret_cast<uint32_t*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim)[lane] =
-            pack_bf16(o0 * inv, o1 * inv);
+            pack_bf16(o0 * f, o1 * f);
     }
     cluster_sync();   // no CTA ends while another may still read its share
 }

@@ -1,6 +1,6 @@
 // 8-bit integer products with a scale per token and per output channel:
 //
-//   oasr_quantize_rows         m = max(max|x_row|, 2^-100), x8 = rint(x (127 / m)), scale = m / 127
+//   oasr_quantize_rows         m = max(max|x_row|, 2^-100), x8 = rint(x (127 (1 / m))), scale = m / 127
 //   oasr_linear_w8a8           out[i][n] = (sum_k x8[i][k] w8[n][k]) x_scale[i] w_scale[n] + bias[n]
 //   oasr_project_qkv_pos_w8a8  the same for a step's q, k, v and its position table, in one launch
 //
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const Elem* __restri
     }
     const bool bad = m == INFINITY;
     m = fmaxf(m, kLeastMax);
-    const float f = bad ? 0.f : __fdiv_rn(127.f, m);
+    const float f = bad ? 0.f : __fmul_rn(__frcp_rn(m), 127.f);
     if (on) {
         if (l == 0) scale[row] = bad ? NAN : __fdiv_rn(m, 127.f);
         int8_t* dst = x8 + static_cast<long long>(row) * K;

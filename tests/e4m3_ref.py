@@ -98,7 +98,10 @@ def attention(q, u, vb, rel, history, C, scale, dtype, K=None):
               Second-order terms and the change of units by log2(e) are covered by a factor 1.05.
       weights p_ij = exp(s_ij) / sum: a change of every score by at most ds changes p by at most a
               factor exp(2 ds); exp2 and the row sum add less than 2^-20 * (1 + K * 2^-4).
-              bf16 rounds each weight once more: r.
+              bf16 rounds each weight once more: r.  Where rows of V differ by octaves the weights are
+              held in fp16 relative to the largest contribution p_j 2^e_j: one below 2^-14 of it is off by
+              up to 2^-25 of it, 2^-25 * 448 2^e_j <= 2^-24 of max|v_j| (a row's largest value is above
+              224 2^e), for at most K keys.
       result  rounded once: r |out|.
     """
     T, H, _ = q.shape
@@ -119,4 +122,5 @@ def attention(q, u, vb, rel, history, C, scale, dtype, K=None):
     ds = ds.amax(-1)                                           # [H, T]
     weight = torch.expm1(2 * ds) + 2.0 ** -20 * (1 + K / 16) + (r if dtype == torch.bfloat16 else 0)
     mag = torch.einsum("hij,jhd->ihd", p, v.abs())
-    return out, weight.t()[..., None] * mag * 1.05 + r * out.abs() + 1e-30
+    top = (p * v.abs().amax(-1).t()[:, None]).amax(-1) * K * 2.0 ** -24 if dtype == torch.bfloat16 else torch.zeros_like(ds)
+    return out, (weight.t()[..., None] * mag + top.t()[..., None]) * 1.05 + r * out.abs() + 1e-30

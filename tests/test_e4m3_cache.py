@@ -308,6 +308,43 @@ def test_rows_of_far_magnitudes(T, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 20])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_mixed_magnitudes(T, dtype):
+    """Zero rows and rows many octaves apart in one stream, in every order: none may disturb the sums
+    of the others."""
+    C = 70
+    for seed, mags in enumerate(((0.0, 1.0), (1.0, 0.0), (2.0 ** 60, 0.0, 1.0), (0.0, 2.0 ** -70, 2.0 ** 90),
+                                 (2.0 ** -110, 2.0 ** 30), (2.0 ** 12, 2.0 ** -12, 1.0))):
+        c, x, lens = make(1, 2, T, [C], 16, dtype, 30 + seed, fill=False)
+        g = torch.Generator().manual_seed(seed)
+        # runs of 16 keys (a slice of one warp) first, then key by key
+        size = torch.tensor([mags[(j // 16 if j < 48 else j) % len(mags)] for j in range(C + T)])[None, :, None, None]
+        k, v = torch.randn(1, C + T, 2, 64, generator=g), torch.randn(1, C + T, 2, 64, generator=g) * size
+        c.append(k[:, :C].to(DT[dtype]), v[:, :C].to(DT[dtype]), [0])
+        x["k_new"], x["v_new"] = k[:, C:].to(DT[dtype]).contiguous(), v[:, C:].to(DT[dtype]).contiguous()
+        out, pools = step(c, x, lens)
+        c.append(x["k_new"], x["v_new"], lens)
+        assert c.same(*pools[:3])
+        check(c, x, lens, out, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 20])
+def test_rows_of_far_queries(T):
+    """Query rows of magnitudes far from one, each scaled into fp16 by its own power of two."""
+    c, x, lens = make(1, 2, T, [70], 16, "bf16", 40)
+    mags = torch.tensor([2.0 ** e for e in (-60, 0, 8, -20, 3)])[torch.arange(T) % 5][None, :, None, None]
+    x["q"] = (x["q"].float() * mags).bfloat16()
+    x["u"], x["vb"] = x["u"] * 2.0 ** -12, x["vb"] * 2.0 ** -12
+    for scale in (0.125, 2.0 ** -9):
+        out, _ = step(c, x, lens, scale=scale)
+        cc, _, _ = make(1, 2, T, [70], 16, "bf16", 40)
+        cc.append(x["k_new"], x["v_new"], lens)
+        check(cc, x, lens, out, "bf16", scale)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,C", [(4, 40), (16, 700), (40, 40)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("fused", [True, False])

@@ -11,9 +11,10 @@ TINY = 2.0 ** -100
 
 
 def rows(x):
-    """x8 and scale by the definition: the two fp32 operations written out, the scale in 64 bits."""
+    """x8 and scale by the definition: the three fp32 operations written out (each a 64-bit one of
+    operands of 24 bits, rounded), the scale in 64 bits."""
     m = x.float().abs().amax(1).clamp(min=TINY)
-    f = (127.0 / m.double()).float()                        # one rounding
+    f = ((1.0 / m.double()).float().double() * 127.0).float()
     q = torch.round((x.float().double() * f.double()[:, None]).float())
     return q.to(torch.int8), m.double() / 127.0
 
