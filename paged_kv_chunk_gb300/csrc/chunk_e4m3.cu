@@ -28,15 +28,22 @@
 #include "attn_core.cuh"
 #include "e4m3.cuh"
 #include "host_common.h"
+#include "tcgen05.cuh"
 
 namespace oasr {
 
 namespace {
 
+#ifndef E4NS
+#define E4NS 4
+#define E4CTAS 3
+#define E4SEG 9
+#endif
 constexpr int kE4MaxPages = 512;              // block-table entries a CTA caches
 constexpr int kE4Stage = 2 * kStageKeys * kE4Row;   // K and V rows of a stage
 constexpr int kE4MaxT = 64;
 constexpr int kMaxRowExp = 120;
+constexpr float kNoMax = -3.0e38f;   // the running maximum before any key
 
 struct E4Args {
     const __nv_bfloat16* k_new;   // fused only
@@ -63,13 +70,13 @@ struct E4Args {
 template <int MT, int NS>
 struct E4Smem {
     static constexpr int Tp = 16 * MT;
-    static constexpr int off_q = NS * kE4Stage;
-    static constexpr int off_ck = off_q + Tp * kRowBytes;             // the chunk's K and V rows
-    static constexpr int off_sc = off_ck + 2 * kE4MaxT * kE4Row;      // scales [NS][2 * 64]
-    static constexpr int off_csc = off_sc + NS * 2 * kStageKeys;      // the chunk's [2][64]
-    static constexpr int off_u = off_csc + 2 * kE4MaxT;
-    static constexpr int off_vb = off_u + kHeadDim * 4;
-    static constexpr int off_re = off_vb + kHeadDim * 4;              // the query rows' exponents
+    static constexpr int Tc = MT == 1 ? 16 : kE4MaxT;                 // rows of the chunk region
+    static constexpr int off_q = NS * kE4Stage;                       // q, then bf16((q + v) 2^-x)
+    static constexpr int off_qu = off_q + Tp * kRowBytes;             // fp16((q + u) 2^-x)
+    static constexpr int off_ck = off_qu + Tp * kRowBytes;            // the chunk's K and V rows
+    static constexpr int off_sc = off_ck + 2 * Tc * kE4Row;           // scales [NS][2 * 64]
+    static constexpr int off_csc = off_sc + NS * 2 * kStageKeys;      // the chunk's [2][Tc]
+    static constexpr int off_re = off_csc + 2 * Tc;                   // 2^x of the query rows
     static constexpr int off_bt = off_re + Tp * 4;
     static constexpr int off_bar = off_bt + kE4MaxPages * 4;          // full[NS], empty[NS], q
     static constexpr int off_gt = (off_bar + (2 * NS + 1) * 8 + 15) & ~15;
@@ -92,10 +99,14 @@ __device__ __forceinline__ uint32_t swz64(int r, int c)
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// Bytes 0, 2 (lo) and 1, 3 (hi) of w, e4m3, as pairs of fp16 times 2^-8: e4m3's exponent and
-// fraction in the low bits of an fp16's, subnormals included (all exact, all finite).
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) { return ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u); }
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) { return ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u); }
+// Bytes 0, 1 (lo) and 2, 3 (hi) of w, e4m3, as pairs of fp16 (exact).
+__device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
 
 // D += A (16x16 fp16, row) * B (16x8 fp16, col), fp32 accumulators.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -107,172 +118,170 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same without an addend.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Two 16 x 16 byte matrices, transposed: lane (g4, t4) gets bytes 4 t4 .. 4 t4 + 3 of columns g4
+// (r0, r2) and 8 + g4 (r1, r3), a byte index being a row.
+__device__ __forceinline__ void ldsm8_x2_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3)
+{
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr));
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// A slice of 16 keys in registers: its raw K and V words and its scales.
+// A slice of 16 keys in registers: raw K and V words and scale bytes.  A lane's four keys are
+// neighbours, 4 t4 .. 4 t4 + 3: as columns of the scores they are columns 2 t4, 2 t4 + 1 of two 8-key tiles
+// (tile n holds keys 4 i + 2 n and 4 i + 2 n + 1), as rows of V the bytes of a transposed word.
 struct E4Slice {
-    uint4 k[2];         // keys g4 and 8 + g4, dims 16 t4 ..
-    uint32_t v[8];      // [chunk of 16 dims][keys 2 t4, 2 t4 + 1 | 8 + those]: bytes k0d0 k0d1 k1d0 k1d1
-    uint32_t ks, vs;    // scale bytes of keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+    uint4 k[2];         // key 4 (g4 / 2) + 2 n + g4 % 2, dims 16 t4 ..
+    uint32_t v[8];      // dim 8 i + g4 of keys 4 t4 ..
+    uint32_t ks, vs;    // scale bytes of keys 4 t4 ..
 };
 
-// k_s, v_s: shared addresses of the slice's first rows; sc: its first K scale, v_off bytes
-// before its first V scale.  box: keys of one page's scales (the K scales of a page come before
-// its V scales); a slice of 16 keys lies in one page, or in two pages of eight.
-__device__ __forceinline__ void load_slice(E4Slice& x, uint32_t k_s, uint32_t v_s, const uint8_t* sc,
-                                           int next8, int v_off, int lane)
+// k_s, v_s: shared addresses of the slice's first rows; sc: its first K scale, v_off bytes before its first
+// V scale; far_off: bytes from the scales of keys 0 .. 7 to those of keys 8 .. 15 (pages of eight keys
+// hold 16 scales each).
+__device__ __forceinline__ void load_slice(E4Slice& x, uint32_t k_s, uint32_t v_s, const uint8_t* sc, int far_off,
+                                           int v_off, int lane)
 {
-    const int g4 = lane >> 2, t4 = lane & 3, mi = lane >> 3;
-    const int row = ((mi & 1) << 3) + (lane & 7);
+    const int g4 = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int n = 0; n < 2; ++n)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x.k[n].x), "=r"(x.k[n].y), "=r"(x.k[n].z), "=r"(x.k[n].w)
-                     : "r"(k_s + swz64(8 * n + g4, t4)));
+                     : "r"(k_s + swz64(4 * (g4 >> 1) + 2 * n + (g4 & 1), t4)));
 #pragma unroll
     for (int dp = 0; dp < 2; ++dp)
-        ldsm_x4_t(v_s + swz64(row, 2 * dp + (mi >> 1)), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
-    const uint8_t* p = sc + 2 * t4;
-    x.ks = *reinterpret_cast<const uint16_t*>(p) | (*reinterpret_cast<const uint16_t*>(p + next8) << 16);
-    p += v_off;
-    x.vs = *reinterpret_cast<const uint16_t*>(p) | (*reinterpret_cast<const uint16_t*>(p + next8) << 16);
-}
-
-// Words of a query row's dims 16 t4 .. 16 t4 + 15 (128-byte-swizzled Q tile).
-__device__ __forceinline__ void q_words(uint32_t (&w)[8], const uint8_t* q_tile, int row, int t4)
-{
-    const uint4 c0 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4));
-    const uint4 c1 = *reinterpret_cast<const uint4*>(q_tile + swz128(row, 2 * t4 + 1));
-    w[0] = c0.x; w[1] = c0.y; w[2] = c0.z; w[3] = c0.w;
-    w[4] = c1.x; w[5] = c1.y; w[6] = c1.z; w[7] = c1.w;
-}
-
-// Power of two, as an exponent, that brings the largest |q + u| of a row into [1, 2).
-__device__ __forceinline__ int row_exponent(const uint8_t* q_tile, const float* u, int row, int t4)
-{
-    uint32_t w[8];
-    q_words(w, q_tile, row, t4);
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i]) + u[16 * t4 + 2 * i]), fabsf(bf16_hi(w[i]) + u[16 * t4 + 2 * i + 1])));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int x = static_cast<int>(__float_as_uint(m) >> 23) - 127;
-    return max(-kMaxRowExp, min(kMaxRowExp, x));
+        ldsm8_x2_t(v_s + swz64(lane & 15, 2 * dp + (lane >> 4)), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
+    const uint8_t* p = sc + 4 * (t4 & 1) + (t4 >> 1) * far_off;
+    x.ks = *reinterpret_cast<const uint32_t*>(p);
+    x.vs = *reinterpret_cast<const uint32_t*>(p + v_off);
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// A fragments of fp16((q + u) 2^-x) for 16 query rows, the head dimension in the order of the e4m3
-// words: quad position t4 holds dims 16 t4 .., k-step ks the word 4 ks, its bytes 0, 2 then 1, 3.
-__device__ __forceinline__ void make_qu_e4m3(uint32_t (&qu)[4][4], const uint8_t* q_tile, const float* u,
-                                             const int* row_exp, int mt, int lane)
+// Eight dims (chunk l8) of one query row, by eight neighbouring lanes: bf16(q + v) over q's own place in
+// the swizzled tile and fp16(q + u) into qu, both times the power of two that brings the row's largest
+// |q + u| into [1, 2), and its inverse into row_pow.  u, v: the head's biases.
+__device__ __forceinline__ void prepare_row(uint8_t* q_tile, uint8_t* qu, float* row_pow, const uint16_t* u,
+                                            const uint16_t* v, int row, int l8)
+{
+    const uint4 qw = *reinterpret_cast<const uint4*>(q_tile + swz128(row, l8));
+    const uint4 uw = __ldg(reinterpret_cast<const uint4*>(u) + l8), vw = __ldg(reinterpret_cast<const uint4*>(v) + l8);
+    const uint32_t q[4] = {qw.x, qw.y, qw.z, qw.w}, un[4] = {uw.x, uw.y, uw.z, uw.w}, vn[4] = {vw.x, vw.y, vw.z, vw.w};
+    float a[8];
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[2 * i] = bf16_lo(q[i]) + bf16_lo(un[i]);
+        a[2 * i + 1] = bf16_hi(q[i]) + bf16_hi(un[i]);
+        m = fmax3(m, fabsf(a[2 * i]), fabsf(a[2 * i + 1]));
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int x = max(-kMaxRowExp, min(kMaxRowExp, static_cast<int>(__float_as_uint(m) >> 23) - 127));
+    const float f = pow2(-x);
+    uint32_t pu[4], pv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        pu[i] = pack_f16(a[2 * i] * f, a[2 * i + 1] * f);
+        pv[i] = pack_bf16((bf16_lo(q[i]) + bf16_lo(vn[i])) * f, (bf16_hi(q[i]) + bf16_hi(vn[i])) * f);
+    }
+    *reinterpret_cast<uint4*>(qu + swz128(row, l8)) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
+    *reinterpret_cast<uint4*>(q_tile + swz128(row, l8)) = make_uint4(pv[0], pv[1], pv[2], pv[3]);
+    if (l8 == 0) row_pow[row] = pow2(x);
+}
+
+// A fragments of 16 rows of a prepared tile, the head dimension in the order of the e4m3 words: quad
+// position t4 holds dims 16 t4 .., k-step ks the dims 4 ks .. 4 ks + 3 of them.
+__device__ __forceinline__ void load_a(uint32_t (&f)[4][4], const uint8_t* tile, int mt, int lane)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int row = 16 * mt + g4 + 8 * half;
-        const float f = pow2(-row_exp[row]);
-        uint32_t w[8];
-        q_words(w, q_tile, row, t4);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            const float* b = u + 16 * t4 + 4 * ks;
-            const float d0 = (bf16_lo(w[2 * ks]) + b[0]) * f, d1 = (bf16_hi(w[2 * ks]) + b[1]) * f;
-            const float d2 = (bf16_lo(w[2 * ks + 1]) + b[2]) * f, d3 = (bf16_hi(w[2 * ks + 1]) + b[3]) * f;
-            qu[ks][half] = pack_f16(d0, d2);
-            qu[ks][half + 2] = pack_f16(d1, d3);
+        for (int c = 0; c < 2; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(tile + swz128(row, 2 * t4 + c));
+            f[2 * c][half] = w.x;
+            f[2 * c][half + 2] = w.y;
+            f[2 * c + 1][half] = w.z;
+            f[2 * c + 1][half + 2] = w.w;
         }
     }
 }
 
-// The position table of one segment (PosTable in attn_core.cuh), each row times its 2^-x: the CTA's
-// Tp query rows against rel rows rho0 .. rho0 + ncols - 1, G[i][c] at gs[i * W + c + i + 1], so that query i
-// and the segment's key j read gs[i * W + j + Tp].  BATCH column tiles of a warp are in flight together.
-template <int BATCH, int MT>
-struct E4Table {
-    const uint16_t* rel_h;
-    long long stride;
-    int R, rho0, ncols, warp, lane;
-    uint4 bl[BATCH], bh[BATCH];
-
-    __device__ __forceinline__ int ntiles() const { return (ncols + 7) >> 3; }
-
-    __device__ __forceinline__ void load(int nb0)
-    {
-        const int g4 = lane >> 2, t4 = lane & 3;
+// Two column tiles of the position table (PosTable in attn_core.cuh; each row times its 2^-x): the CTA's
+// Tp query rows (qa: bf16((q + v) 2^-x)) against rel rows 8 tile .. and 8 tile + 32 .. of the segment, the rows in the ring
+// slot `rows` (64 of them, 128-byte swizzled).  G[i][c] goes to gs[i * W + c + i + 1], so that query i and the
+// segment's key j read gs[i * W + j + Tp].  Every lane arrives on release_bar once it has read its rows.
+template <int MT>
+__device__ __forceinline__ void table_tiles(uint16_t* gs, int W, const uint32_t (&qa)[MT][4][4], const uint8_t* rows,
+                                            int col0, int ntiles, int warp, int lane, uint32_t release_bar)
+{
+    const int g4 = lane >> 2, t4 = lane & 3;
+    uint4 bl[2], bh[2];
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int rho = rho0 + 8 * (nb0 + u * kConsumerWarps) + g4;
-            bl[u] = bh[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (nb0 + u * kConsumerWarps < ntiles() && rho >= 0 && rho < R) {
-                const uint4* src = reinterpret_cast<const uint4*>(rel_h + rho * stride + 16 * t4);
-                bl[u] = __ldg(src);
-                bh[u] = __ldg(src + 1);
-            }
+    for (int u = 0; u < 2; ++u) {
+        const int r = 8 * (warp + 4 * u) + g4;
+        bl[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4));
+        bh[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4 + 1));
+    }
+    mbar_arrive_release(release_bar);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if (warp + 4 * u >= ntiles) break;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            float c[4];
+            mma_bf16_first(c, qa[mt][0], bl[u].x, bl[u].y);
+            mma_bf16_16816(c, qa[mt][1], bl[u].z, bl[u].w);
+            mma_bf16_16816(c, qa[mt][2], bh[u].x, bh[u].y);
+            mma_bf16_16816(c, qa[mt][3], bh[u].z, bh[u].w);
+            // columns past the last stay within their row (its stride leaves room for a tile)
+            uint16_t* d = gs + (16 * mt + g4) * (W + 1) + 1 + 2 * t4 + col0 + 8 * (warp + 4 * u);
+            const uint32_t w0 = pack_bf16(c[0], c[1]), w1 = pack_bf16(c[2], c[3]);
+            d[0] = static_cast<uint16_t>(w0);
+            d[1] = static_cast<uint16_t>(w0 >> 16);
+            d[8 * W + 8] = static_cast<uint16_t>(w1);
+            d[8 * W + 9] = static_cast<uint16_t>(w1 >> 16);
         }
     }
-
-    __device__ __forceinline__ void build(uint16_t* gs, int W, const uint8_t* q_tile, const float* v, const int* row_exp)
-    {
-        const int g4 = lane >> 2, t4 = lane & 3;
-        uint32_t qa[MT][4][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int row = 16 * mt + g4 + 8 * half;
-                const float f = pow2(-row_exp[row]);
-                uint32_t w[8];
-                q_words(w, q_tile, row, t4);
-#pragma unroll
-                for (int m = 0; m < 8; ++m)
-                    qa[mt][m >> 1][half + 2 * (m & 1)] = pack_bf16((bf16_lo(w[m]) + v[16 * t4 + 2 * m]) * f,
-                                                                   (bf16_hi(w[m]) + v[16 * t4 + 2 * m + 1]) * f);
-            }
-        for (int nb0 = warp; nb0 < ntiles(); nb0 += BATCH * kConsumerWarps) {
-            if (nb0 != warp) load(nb0);
-#pragma unroll
-            for (int u = 0; u < BATCH; ++u) {
-                const int col = 8 * (nb0 + u * kConsumerWarps) + 2 * t4;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_bf16_16816(c, qa[mt][0], bl[u].x, bl[u].y);
-                    mma_bf16_16816(c, qa[mt][1], bl[u].z, bl[u].w);
-                    mma_bf16_16816(c, qa[mt][2], bh[u].x, bh[u].y);
-                    mma_bf16_16816(c, qa[mt][3], bh[u].z, bh[u].w);
-                    const int i = 16 * mt + g4;
-                    uint16_t* d = gs + i * W + col + i + 1;
-                    if (col < ncols) {
-                        d[0] = bf16_bits(c[0]);
-                        d[8 * W + 8] = bf16_bits(c[2]);
-                    }
-                    if (col + 1 < ncols) {
-                        d[1] = bf16_bits(c[1]);
-                        d[8 * W + 9] = bf16_bits(c[3]);
-                    }
-                }
-            }
-        }
-    }
-};
+}
 
 // Running state of 16 query rows of one warp.  With t_ij = s_ij + ev_j (log2 units: the size of key j's
-// contribution to the output), m is the running maximum of t, o the sum of 2^(t - m) v8 2^-8 and l the
-// sum of 2^(s - m + E), where E is within 20 of the largest V scale exponent so far.
+// contribution to the output), m is the running maximum of t, o the sum of 2^(t - m) v8 and l the
+// sum of 2^(s - m + E), where E is within 7 of the largest V scale exponent so far.
 struct E4Acc {
-    float o[8][4];   // o[2c + e]: dims 16 c + 4 t4 + e, + 2 + e of row g4, then of row g4 + 8
+    float o[8][4];   // o[d]: dims 8 d + 2 t4, 8 d + 2 t4 + 1 of row g4, then of row g4 + 8
     float m[2], l[2];
 };
 
 // One warp, 16 MT query rows against one slice.  gq: the position table at the slice's first key
-// (key jl of query row i reads gq[i * W + jl]); keys [0, kvalid) of the slice exist; sc: scale * log2(e) * 2^x of
+// (key jl of query row i reads gq[i * W + jl], aligned: eight bytes at a time); keys [0, kvalid) of the slice exist; sc: scale * log2(e) * 2^x of
 // rows g4 and g4 + 8 of each m-tile.
 //
 // P is 2^(t - m), at most one, and goes into the product as fp16: its rounding is 2^-11 of each
@@ -280,96 +289,100 @@ struct E4Acc {
 // row sum takes p back out of it, l += P 2^(E - ev); a slice with a scale below 2^(E - 40) (a row of
 // zeros has 2^-100), where that could underflow, sums 2^(s - m + E) of its own.
 template <int MT>
-__device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu)[MT][4][4], const E4Slice& x,
-                                           const uint16_t* gq, int W, bool even, int kvalid,
+__device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu)[MT][4][4], E4Slice& x,
+                                           const uint16_t* gq, int W, bool aligned, int kvalid,
                                            const float (&sc)[MT][2], int& E, int lane)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
     float s[MT][2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
-#pragma unroll
     for (int n = 0; n < 2; ++n) {
         const uint32_t w[4] = {x.k[n].x, x.k[n].y, x.k[n].z, x.k[n].w};
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t b0 = e4m3_lo(w[ks]), b1 = e4m3_hi(w[ks]);
+            uint32_t b0, b1;
+            e4m3_to_f16(w[ks], b0, b1);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma_f16_16816(s[mt][n], qu[mt][ks], b0, b1);
+            for (int mt = 0; mt < MT; ++mt) {
+                if (ks == 0)
+                    mma_f16_first(s[mt][n], qu[mt][ks], b0, b1);
+                else
+                    mma_f16_16816(s[mt][n], qu[mt][ks], b0, b1);
+            }
         }
     }
-    // keys 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4: 2^(ek + 8), ev and 2^(E - ev)
-    float ks[4], ev[4], back[4];
-    int v[4];
-    bool odd = false;
+    const bool tail = kvalid < 16;
+    if (tail) {   // rows past the last key may hold anything: V bytes and scales (their scores are replaced below)
+        const int have = max(0, min(4, kvalid - 4 * t4));
+        const uint32_t mask = have == 4 ? 0xffffffffu : (1u << (8 * have)) - 1u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int jl = 2 * t4 + (e & 1) + 8 * (e >> 1);
-        ks[e] = e4m3_scale((x.ks >> (8 * e)) & 255u) * 256.f;
-        v[e] = static_cast<int>((x.vs >> (8 * e)) & 255u) - 127;
-        if (jl >= kvalid) v[e] = E;          // rows past the last key may hold anything
-        odd |= static_cast<unsigned>(v[e] - E + 40) > 60u;
+        for (int i = 0; i < 8; ++i) x.v[i] &= mask;
+        x.vs = (x.vs & mask) | (static_cast<uint32_t>(E + 127) * 0x01010101u & ~mask);
     }
+    // keys 4 t4 ..: 2^ek, ev and 2^(E - ev), from the scale bytes in place
+    // (0x4b000000 | byte is 2^23 + byte)
     bool far = false;
     float dE = 0.f;
-    if (__any_sync(0xffffffffu, odd)) {
-        const int top = __reduce_max_sync(0xffffffffu, max(max(v[0], v[1]), max(v[2], v[3])));
-        if (top > E + 20) {
-            dE = static_cast<float>(top - E);
-            E = top;
+    {
+        const int mine = static_cast<int>((x.vs >> (8 * (g4 & 3))) & 255u) - 127;   // each key by some lane
+        if (__any_sync(0xffffffffu, static_cast<unsigned>(mine - E + 40) > 47u)) {
+            const int top = __reduce_max_sync(0xffffffffu, mine);
+            if (top > E + 7) {
+                dE = static_cast<float>(top - E);
+                E = top;
+            }
+            far = __any_sync(0xffffffffu, mine < E - 40);
         }
-        far = __any_sync(0xffffffffu, min(min(v[0], v[1]), min(v[2], v[3])) < E - 40);
     }
+    float ks[4], ev[4], back[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        ev[e] = v[e] == 128 ? NAN : static_cast<float>(v[e]);
-        back[e] = far ? 0.f : pow2(E - v[e]);
+        ks[e] = __uint_as_float(__byte_perm(x.ks, 0u, 0x0444 | (e << 12)) >> 1);
+        const uint32_t w = __byte_perm(x.vs, 0x4b000000u, 0x7440 | e);
+        ev[e] = __uint_as_float(w) - 8388735.f;                    // 2^23 + 127
+        back[e] = __uint_as_float(static_cast<uint32_t>(E + 254) * 0x00800000u - w * 0x00800000u);
     }
     uint32_t pa[MT][4];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         E4Acc& a = acc[mt];
         float mx0 = a.m[0], mx1 = a.m[1];
-        const uint16_t* r0 = gq + (16 * mt + g4) * W + 2 * t4;
+        const uint16_t* r0 = gq + (16 * mt + g4) * W + 4 * t4;
         const uint16_t* r1 = r0 + 8 * W;
+        uint32_t y0[2], y1[2];
+        if (aligned) {
+            const uint2 p0 = *reinterpret_cast<const uint2*>(r0), p1 = *reinterpret_cast<const uint2*>(r1);
+            y0[0] = p0.x; y0[1] = p0.y;
+            y1[0] = p1.x; y1[1] = p1.y;
+        } else {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                y0[n] = r0[2 * n] | static_cast<uint32_t>(r0[2 * n + 1]) << 16;
+                y1[n] = r1[2 * n] | static_cast<uint32_t>(r1[2 * n + 1]) << 16;
+            }
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            float gb[4];
-            if (even) {
-                const uint32_t y0 = *reinterpret_cast<const uint32_t*>(r0 + 8 * n);
-                const uint32_t y1 = *reinterpret_cast<const uint32_t*>(r1 + 8 * n);
-                gb[0] = bf16_lo(y0);
-                gb[1] = bf16_hi(y0);
-                gb[2] = bf16_lo(y1);
-                gb[3] = bf16_hi(y1);
-            } else {
-                gb[0] = bf16_lo(r0[8 * n]);
-                gb[1] = bf16_lo(r0[8 * n + 1]);
-                gb[2] = bf16_lo(r1[8 * n]);
-                gb[3] = bf16_lo(r1[8 * n + 1]);
-            }
+            const float gb[4] = {bf16_lo(y0[n]), bf16_hi(y0[n]), bf16_lo(y1[n]), bf16_hi(y1[n])};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int k = 2 * n + (e & 1);
-                const bool ok = 8 * n + 2 * t4 + (e & 1) < kvalid;
-                s[mt][n][e] = ok ? fmaf(fmaf(s[mt][n][e], ks[k], gb[e]), sc[mt][e >> 1], ev[k]) : -INFINITY;
+                s[mt][n][e] = fmaf(fmaf(s[mt][n][e], ks[k], gb[e]), sc[mt][e >> 1], ev[k]);
+                if (tail && 4 * t4 + k >= kvalid) s[mt][n][e] = -INFINITY;
             }
             mx0 = fmax3(mx0, s[mt][n][0], s[mt][n][1]);
             mx1 = fmax3(mx1, s[mt][n][2], s[mt][n][3]);
         }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-        const float base0 = (mx0 == -INFINITY) ? 0.f : mx0;
-        const float base1 = (mx1 == -INFINITY) ? 0.f : mx1;
-        if (mx0 != a.m[0] || mx1 != a.m[1] || dE != 0.f) {
-            const float alpha0 = ex2_approx(a.m[0] - base0);
-            const float alpha1 = ex2_approx(a.m[1] - base1);
-            a.l[0] *= ex2_approx(fminf(a.m[0] - base0 + dE, 126.f));
-            a.l[1] *= ex2_approx(fminf(a.m[1] - base1 + dE, 126.f));
+        // the reference only moves when a weight would pass 2^8 (fp16 holds 2^15)
+        if (__any_sync(0xffffffffu, mx0 > a.m[0] + 8.f || mx1 > a.m[1] + 8.f) || dE != 0.f) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+            const float d0 = a.m[0] - mx0, d1 = a.m[1] - mx1;
+            const float alpha0 = ex2_approx(d0), alpha1 = ex2_approx(d1);
+            a.l[0] *= ex2_approx(fminf(d0 + dE, 126.f));
+            a.l[1] *= ex2_approx(fminf(d1 + dE, 126.f));
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
                 a.o[d][0] *= alpha0;
@@ -380,6 +393,7 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu
             a.m[0] = mx0;
             a.m[1] = mx1;
         }
+        const float base0 = a.m[0], base1 = a.m[1];
         if (far) {
             const float off = static_cast<float>(E);
 #pragma unroll
@@ -389,6 +403,7 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu
                     const int k = 2 * n + e;
                     a.l[0] += ex2_approx(s[mt][n][e] - ev[k] - base0 + off);
                     a.l[1] += ex2_approx(s[mt][n][2 + e] - ev[k] - base1 + off);
+                    back[k] = 0.f;
                 }
         }
 #pragma unroll
@@ -404,21 +419,24 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu
         }
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const uint32_t w0 = x.v[2 * c], w1 = x.v[2 * c + 1];
-        const uint32_t e0 = e4m3_lo(w0), e1 = e4m3_lo(w1), d0 = e4m3_hi(w0), d1 = e4m3_hi(w1);
+    for (int d = 0; d < 8; ++d) {
+        uint32_t b0, b1;
+        e4m3_to_f16(x.v[d], b0, b1);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            mma_f16_16816(acc[mt].o[2 * c], pa[mt], e0, e1);
-            mma_f16_16816(acc[mt].o[2 * c + 1], pa[mt], d0, d1);
-        }
+        for (int mt = 0; mt < MT; ++mt) mma_f16_16816(acc[mt].o[d], pa[mt], b0, b1);
     }
 }
 
-__device__ __noinline__ bool e4_wait_slow(uint32_t bar, uint32_t parity) { return mbar_wait(bar, parity); }
+// Bounded wait, inline: a call would spill the registers that live across it.
 __device__ __forceinline__ bool e4_wait(uint32_t bar, uint32_t parity)
 {
-    return mbar_try_wait(bar, parity) || e4_wait_slow(bar, parity);
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        for (int k = 0; k < 16; ++k)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
 }
 
 // 2-D tiled bulk load with an L2 hint, and an untiled bulk copy; both count bytes on `bar`.
@@ -450,12 +468,12 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
 }
 
 // Weight of a share whose maximum (log2) is `x` against the largest, `top`; a share without keys has
-// -inf and weight 0.
+// kNoMax (or -inf) and weight 0.
 //
 // Shares of a row are joined from o, m and lambda = log2(sum of 2^s) = m - E + log2(l): the V scales
 // move m away from the scores (a share of zero rows has an m of s - 100), so the row sum has a
-// maximum of its own.  out = 2^8 sum(o 2^(m - m*)) 2^(m* - lambda*) / sum(2^(lambda - lambda*)).
-__device__ __forceinline__ float part_weight(float x, float top) { return x == -INFINITY ? 0.f : ex2_approx(x - top); }
+// maximum of its own.  out = sum(o 2^(m - m*)) 2^(m* - lambda*) / sum(2^(lambda - lambda*)).
+__device__ __forceinline__ float part_weight(float x, float top) { return x <= kNoMax ? 0.f : ex2_approx(x - top); }
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -466,7 +484,7 @@ __device__ __forceinline__ void cluster_sync()
 template <int MT, int NS, int CTAS, bool FUSED>
 __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-    const __grid_constant__ CUtensorMap tm_v, const E4Args a)
+    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r, const E4Args a)
 {
     using SP = E4Smem<MT, NS>;
     constexpr int Tp = SP::Tp;
@@ -489,17 +507,28 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_r);
     }
     grid_dep_wait();
     const uint32_t bar_full = sb + SP::off_bar;
     const uint32_t bar_empty = bar_full + NS * 8;
     const uint32_t bar_q = bar_empty + NS * 8;
-    float* s_u = reinterpret_cast<float*>(sm + SP::off_u);
-    float* s_vb = reinterpret_cast<float*>(sm + SP::off_vb);
+    float* s_pow = reinterpret_cast<float*>(sm + SP::off_re);
     int* s_bt = reinterpret_cast<int*>(sm + SP::off_bt);
     __shared__ int s_failed;
 
     int C = __ldg(a.cache_seqlens + b);
+    // consumers, T <= 16: the thread's two chunk rows (eight lanes each), requested first of all
+    uint4 pre[2] = {};
+    if (FUSED && !producer && split == S - 1) {
+        if constexpr (MT == 1) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv)
+                if (tid >> 3 < T)
+                    pre[kv] = __ldg(reinterpret_cast<const uint4*>(
+                        (kv ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + (tid >> 3)) * H + h) * kE4Row) + (lane & 7));
+        }
+    }
     if (producer) {
         const int32_t* bt_row = a.block_table + static_cast<long long>(b) * a.mbps;
         constexpr int kRowRegs = 4;
@@ -525,10 +554,6 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         __syncwarp();
         named_bar_arrive(2, kThreads);
     } else {
-        if (tid < kHeadDim)
-            s_u[tid] = bf16_lo(__ldg(a.pos_bias_u + h * kHeadDim + tid));
-        else
-            s_vb[tid - kHeadDim] = bf16_lo(__ldg(a.pos_bias_v + h * kHeadDim + tid - kHeadDim));
         named_bar_sync(2, kThreads);
     }
     if (C < 0) { C = 0; err |= kErrBounds; }
@@ -546,16 +571,35 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     const bool chunk_here = FUSED && split == S - 1;   // the chunk follows the last pool keys
     const int nc = chunk_here ? K - kc : 0;            // its keys (fewer when it runs past the table)
     const int box = min(bs, kStageKeys), box_sh = min(sh, 6);
+    // keys of the segment of stages [seg0, seg1): the last one of the last split has the chunk's too
+    auto segment_keys = [&](int seg0, int seg1) {
+        return max(0, ((seg1 >= st1 && chunk_here) ? K : min(seg1 * kStageKeys, kc)) - seg0 * kStageKeys);
+    };
+    // its position table has a column for each distance: rel rows rho0 .., in ring slots of 64 rows
+    auto segment_rel = [&](int nkeys) { return nkeys ? (nkeys + Tp - 1 + 63) >> 6 : 0; };
 
     if (producer) {
         const uint64_t pol = policy_evict_first();
         int n_issued = 0;
-        for (int s = st0; s < st1; ++s) {
-            const int it = s - st0, slot = it % NS;
-            if (!__all_sync(0xffffffffu, it < NS || e4_wait(bar_empty + 8 * slot, ((it / NS) - 1) & 1))) {
-                err |= kErrTimeout;
-                break;
+        bool ok = true;
+        for (int seg0 = st0;;) {
+            const int seg1 = min(seg0 + a.seg, st1);
+            const int nrel = segment_rel(segment_keys(seg0, seg1));
+            for (int r = 0; r < nrel && ok; ++r) {
+                const int it = n_issued, slot = it % NS;
+                ok = __all_sync(0xffffffffu, it < NS || e4_wait(bar_empty + 8 * slot, ((it / NS) - 1) & 1));
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t bar = bar_full + 8 * slot;
+                    mbar_arrive_expect_tx(bar, kE4Stage);
+                    tma_load_3d(sb + slot * kE4Stage, &tm_r, bar, 0, h, off + (seg0 + r) * kStageKeys - i0 - (Tp - 1));
+                }
+                ++n_issued;
             }
+            for (int s = seg0; s < seg1 && ok; ++s) {
+            const int it = n_issued, slot = it % NS;
+            ok = __all_sync(0xffffffffu, it < NS || e4_wait(bar_empty + 8 * slot, ((it / NS) - 1) & 1));
+            if (!ok) break;
             const uint32_t bar = bar_full + 8 * slot;
             const int j0 = s * kStageKeys;
             const int nbox = min(kStageKeys >> box_sh, (kc - j0 + box - 1) >> box_sh);
@@ -598,8 +642,12 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                     tma_load_2d_hint(dst + kStageKeys * kE4Row, &tm_v, bar, 0, row, pol);
                 }
             }
-            n_issued = it + 1;
+            ++n_issued;
+            }
+            seg0 = seg1;
+            if (seg0 >= st1 || !ok) break;
         }
+        if (!ok) err |= kErrTimeout;
         // every copy this CTA requested lands before it ends
         for (int x = n_issued > NS ? n_issued - NS : 0; x < n_issued; ++x)
             if (!mbar_wait_idle(bar_full + 8 * (x % NS), (x / NS) & 1)) err |= kErrTimeout;
@@ -614,30 +662,24 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
 
     // ---------------------------------------------------------------- consumers
     bool failed = false;
-    E4Acc acc[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[mt].o[d][0] = acc[mt].o[d][1] = acc[mt].o[d][2] = acc[mt].o[d][3] = 0.f;
-        acc[mt].m[0] = acc[mt].m[1] = -INFINITY;
-        acc[mt].l[0] = acc[mt].l[1] = 0.f;
-    }
-    int E = -127;   // the smallest a scale byte says; the first keys raise it
     uint16_t* gs = reinterpret_cast<uint16_t*>(sm + SP::off_gt);
     const int W = a.gt_w;
     if (FUSED && chunk_here) {
         // the chunk's rows: quantised into the chunk region (rows past T zero) and, by the first
         // query tile, into the pool.  Eight lanes per row.
         const int nrow = (T + 15) & ~15;
+#pragma unroll 1
         for (int r = tid >> 3; r < 2 * nrow; r += 4 * kConsumerWarps) {
             const int kv = r >= nrow, t = r - kv * nrow, l8 = lane & 7;
-            const unsigned mask = 0xffu << (lane & 24);
             uint2 q = make_uint2(0u, 0u);
             uint32_t byte = 0;
             if (t < nc) {
                 float x[8];
-                load8((kv ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + t) * H + h) * kE4Row + 8 * l8, x);
-                byte = e4m3_quantise8(x, mask, q);
+                if constexpr (MT == 1)
+                    unpack8(kv ? pre[1] : pre[0], x);
+                else
+                    load8((kv ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + t) * H + h) * kE4Row + 8 * l8, x);
+                byte = e4m3_quantise8(x, 0xffu << (lane & 24), q);
                 const int p = C + t;
                 const int blk = s_bt[p >> sh];
                 if (blk < 0 || blk >= a.num_blocks) {   // dropped by the append: reads as zeros
@@ -651,53 +693,60 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                     if (l8 == 0) a.kv_scale[(2 * page + kv) * bs + slot] = static_cast<uint8_t>(byte);
                 }
             }
-            *reinterpret_cast<uint2*>(sm + SP::off_ck + kv * kE4MaxT * kE4Row + swz64(t, l8 >> 1) + 8 * (l8 & 1)) = q;
-            if (l8 == 0) sm[SP::off_csc + kv * kE4MaxT + t] = static_cast<uint8_t>(byte);
+            *reinterpret_cast<uint2*>(sm + SP::off_ck + kv * SP::Tc * kE4Row + swz64(t, l8 >> 1) + 8 * (l8 & 1)) = q;
+            if (l8 == 0) sm[SP::off_csc + kv * SP::Tc + t] = static_cast<uint8_t>(byte);
         }
     }
-    E4Table<MT == 1 ? 5 : 4, MT> pt;
-    pt.rel_h = a.rel + h * kHeadDim;
-    pt.stride = static_cast<long long>(H) * kHeadDim;
-    pt.R = a.R;
-    pt.warp = warp;
-    pt.lane = lane;
     if (!e4_wait(bar_q, 0)) failed = true;
-    int* s_re = reinterpret_cast<int*>(sm + SP::off_re);
-    if (warp < 2 * MT) {   // eight query rows a warp
-        const int x = row_exponent(sm + SP::off_q, s_u, 8 * warp + (lane >> 2), lane & 3);
-        if ((lane & 3) == 0) s_re[8 * warp + (lane >> 2)] = x;
-    }
-    named_bar_sync(1, 32 * kConsumerWarps);   // the rows' exponents are known
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+        prepare_row(sm + SP::off_q, sm + SP::off_qu, s_pow, a.pos_bias_u + h * kHeadDim, a.pos_bias_v + h * kHeadDim,
+                    16 * mt + (tid >> 3), lane & 7);
+    named_bar_sync(1, 32 * kConsumerWarps);   // the query tiles and the chunk region are complete
     const int jl = 16 * warp;   // this warp's keys of a stage
     const int next8 = box == 8 ? 16 : 8;   // scales of keys 8 .. 15 of a slice, from those of keys 0 .. 7
     const int sc_off = ((jl >> box_sh) << (box_sh + 1)) + (jl & (box - 1));
+    E4Acc acc[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) acc[mt].o[d][0] = acc[mt].o[d][1] = acc[mt].o[d][2] = acc[mt].o[d][3] = 0.f;
+        acc[mt].m[0] = acc[mt].m[1] = kNoMax;
+        acc[mt].l[0] = acc[mt].l[1] = 0.f;
+    }
+    int E = -127;   // the smallest a scale byte says; the first keys raise it
+    int it = 0;   // ring slots read
+#pragma unroll 1
     for (int seg0 = st0;; seg0 += a.seg) {
-        // the position term of this segment's keys [64 seg0, jend) and, with the last, the chunk's
         const int seg1 = min(seg0 + a.seg, st1);
         const bool last = seg1 >= st1;
         const int jbase = seg0 * kStageKeys;
-        const int nkeys = (last && chunk_here) ? K - jbase : min(seg1 * kStageKeys, kc) - jbase;
-        if (nkeys > 0) {
-            if (seg0 > st0) named_bar_sync(1, 32 * kConsumerWarps);   // the previous table has been read
-            if (!failed) {
-                pt.rho0 = off + jbase - i0 - (Tp - 1);
-                pt.ncols = nkeys + Tp - 1;
-                pt.load(warp);
-                pt.build(gs, W, sm + SP::off_q, s_vb, s_re);
-            }
-            named_bar_sync(1, 32 * kConsumerWarps);   // the table (and the chunk region) are complete
-        }
-        uint32_t qu[MT][4][4];   // made per segment: they would not fit beside the table's operands
+        const int nkeys = segment_keys(seg0, seg1);
+        if (nkeys) {
+            uint32_t qa[MT][4][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) make_qu_e4m3(qu[mt], sm + SP::off_q, s_u, s_re, mt, lane);
+            for (int mt = 0; mt < MT; ++mt) load_a(qa[mt], sm + SP::off_q, mt, lane);
+            const int ntiles = (nkeys + Tp - 1 + 7) >> 3, nrel = segment_rel(nkeys);
+#pragma unroll 1
+            for (int r = 0; r < nrel; ++r, ++it) {
+                const int slot = it % NS;
+                if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
+                table_tiles<MT>(gs, W, qa, sm + slot * kE4Stage, 64 * r, ntiles - 8 * r, warp, lane,
+                                bar_empty + 8 * slot);
+            }
+            named_bar_sync(1, 32 * kConsumerWarps);   // the table is complete
+        }
+        uint32_t qu[MT][4][4];
         float sc[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            sc[mt][0] = a.scale_log2 * pow2(s_re[16 * mt + (lane >> 2)]);
-            sc[mt][1] = a.scale_log2 * pow2(s_re[16 * mt + (lane >> 2) + 8]);
+            load_a(qu[mt], sm + SP::off_qu, mt, lane);
+            sc[mt][0] = a.scale_log2 * s_pow[16 * mt + (lane >> 2)];
+            sc[mt][1] = a.scale_log2 * s_pow[16 * mt + (lane >> 2) + 8];
         }
-        for (int s = seg0; s < seg1; ++s) {
-            const int it = s - st0, slot = it % NS;
+#pragma unroll 1
+        for (int s = seg0; s < seg1; ++s, ++it) {
+            const int slot = it % NS;
             if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
             const int kv = min(kc - s * kStageKeys, kStageKeys) - jl;
             E4Slice x;
@@ -713,13 +762,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         if (last) {
             if (nc > jl && !failed) {
                 E4Slice x;
-                load_slice(x, sb + SP::off_ck + jl * kE4Row, sb + SP::off_ck + (kE4MaxT + jl) * kE4Row,
-                           sm + SP::off_csc + jl, 8, kE4MaxT, lane);
+                load_slice(x, sb + SP::off_ck + jl * kE4Row, sb + SP::off_ck + (SP::Tc + jl) * kE4Row,
+                           sm + SP::off_csc + jl, 8, SP::Tc, lane);
                 const int x0 = C + jl - jbase + Tp;
-                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 1) == 0, nc - jl, sc, E, lane);
+                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 3) == 0, nc - jl, sc, E, lane);
             }
             break;
         }
+        named_bar_sync(1, 32 * kConsumerWarps);   // the table has been read
     }
     if (failed) s_failed = 1;
     grid_dep_trigger();
@@ -742,10 +792,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
                 const int r = warp * Tp + 16 * mt + g4 + 8 * half;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    *reinterpret_cast<float4*>(comb_o + r * kOW + 16 * c + 4 * t4) =
-                        make_float4(acc[mt].o[2 * c][2 * half], acc[mt].o[2 * c + 1][2 * half],
-                                    acc[mt].o[2 * c][2 * half + 1], acc[mt].o[2 * c + 1][2 * half + 1]);
+                for (int d = 0; d < 8; ++d)
+                    *reinterpret_cast<float2*>(comb_o + r * kOW + 8 * d + 2 * t4) =
+                        make_float2(acc[mt].o[d][2 * half], acc[mt].o[d][2 * half + 1]);
                 if (t4 == 0) {
                     comb_m[r] = acc[mt].m[half];
                     comb_l[r] = acc[mt].m[half] - static_cast<float>(E) + log2f(l);
@@ -773,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 o[0] += w * x.x; o[1] += w * x.y; o[2] += w * x.z; o[3] += w * x.w;
                 o[4] += w * y.x; o[5] += w * y.y; o[6] += w * y.z; o[7] += w * y.w;
             }
-            const float f = exp2f(m - l + 8.f) / sum;
+            const float f = exp2f(m - l) / sum;
             *reinterpret_cast<uint4*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim + d0) =
                 make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
                            pack_bf16(o[6] * f, o[7] * f));
@@ -820,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             o0 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane), k);
             o1 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane + 1), k);
         }
-        const float f = exp2f(m - l + 8.f) / sum;
+        const float f = exp2f(m - l) / sum;
         reinterpret_cast<uint32_t*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim)[lane] =
             pack_bf16(o0 * f, o1 * f);
     }
@@ -941,24 +990,24 @@ __global__ void __launch_bounds__(128) chunk_e4m3_f32_kernel(
 
 int g_smem_done_e4[8][64];
 
-// Row stride (bf16 elements) of the position table: every access stays below nkeys + 2 Tp, and a
-// stride of 16 mod 64 elements keeps the 4-byte reads of a slice conflict-free.
+// Row stride (bf16 elements) of the position table: every access stays below nkeys + 2 Tp + 8, and a
+// stride of 16 mod 64 elements (8 mod 32 words) keeps the 8-byte reads of a slice conflict-free.
 inline int e4_table_stride(int nkeys, int Tp) { return ((nkeys + 2 * Tp + 63) & ~63) + 16; }
 
 template <int MT, int NS, int CTAS, bool FUSED>
 oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int slot, cudaStream_t stream)
 {
     using SP = E4Smem<MT, NS>;
-    CUtensorMap tm_q, tm_k, tm_v;
+    CUtensorMap tm_q, tm_k, tm_v, tm_r;
     const int box = a.block_size < kStageKeys ? a.block_size : kStageKeys;
     const long long rows = static_cast<long long>(a.num_blocks) * a.H * a.block_size;
     if (!encode_rows_bf16(&tm_q, q, static_cast<long long>(B) * a.T, a.H, SP::Tp) ||
-        !encode_rows_e4m3(&tm_k, a.k_pool, rows, box) || !encode_rows_e4m3(&tm_v, a.v_pool, rows, box))
+        !encode_rows_bf16(&tm_r, a.rel, a.R, a.H, kStageKeys) || !encode_rows_e4m3(&tm_k, a.k_pool, rows, box) || !encode_rows_e4m3(&tm_v, a.v_pool, rows, box))
         return OASR_ERR_INVALID_ARG;
     auto kern = chunk_e4m3_kernel<MT, NS, CTAS, FUSED>;
     // segments of at most eight stages and a part of one, sized for the keys a call can have
     const int stages = (k_max + kStageKeys - 1) / kStageKeys;
-    a.seg = stages < 9 ? stages : 9;
+    a.seg = stages < E4SEG ? stages : E4SEG;
     a.gt_w = e4_table_stride(a.seg * kStageKeys + (FUSED ? ((a.T + 15) & ~15) : 0), SP::Tp);
     const int smem = SP::bytes + SP::Tp * a.gt_w * 2;
     if (!ensure_smem(kern, smem, g_smem_done_e4[slot])) return OASR_ERR_CUDA;
@@ -982,7 +1031,7 @@ oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int slot, cuda
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, static_cast<const E4Args>(a)) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, tm_r, static_cast<const E4Args>(a)) != cudaSuccess)
         return OASR_ERR_CUDA;
     return launch_status();
 }
@@ -1049,7 +1098,7 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     const long long pages = static_cast<long long>(mbps) * block_size, dist = static_cast<long long>(R) - T + 1;
     const long long k_max = pages < dist ? pages : dist;
     const int km = static_cast<int>(k_max < T ? T : k_max);
-    if (T <= 16) return launch_e4<1, 4, 3, FUSED>(q, a, km, B, FUSED ? 1 : 0, stream);
+    if (T <= 16) return launch_e4<1, E4NS, E4CTAS, FUSED>(q, a, km, B, FUSED ? 1 : 0, stream);
     return launch_e4<2, 6, 2, FUSED>(q, a, km, B, FUSED ? 3 : 2, stream);
 }
 

@@ -81,16 +81,21 @@ __device__ __forceinline__ uint32_t e4m3_quantise8(const float (&x)[8], unsigned
     return byte;
 }
 
-// Eight values of a row from global memory.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8])
+// Eight bf16 values as fp32.
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8])
 {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(v[i] << 16);
         x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
     }
+}
+
+// Eight values of a row from global memory.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8])
+{
+    unpack8(__ldg(reinterpret_cast<const uint4*>(p)), x);
 }
 
 __device__ __forceinline__ void load8(const float* p, float (&x)[8])
