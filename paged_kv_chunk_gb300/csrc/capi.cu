@@ -99,13 +99,13 @@ bool encode_head_pairs_bf16(CUtensorMap* map, const void* base, long long rows, 
 bool encode_rows_e4m3(CUtensorMap* map, const void* base, long long rows, int box_rows)
 {
     EncodeTiledFn fn = encode_fn();
-    if (!fn || rows < 1 || box_rows < 8 || box_rows > 64 || !aligned16(base)) return false;
-    const cuuint64_t dims[2] = {64, static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {64};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    if (!fn || rows < 2 || (rows & 1) || box_rows < 8 || box_rows > 64 || (box_rows & 1) || !aligned16(base)) return false;
+    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows / 2)};
+    const cuuint64_t strides[1] = {128};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows / 2)};
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

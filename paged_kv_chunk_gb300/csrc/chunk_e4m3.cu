@@ -35,9 +35,14 @@ namespace oasr {
 namespace {
 
 #ifndef E4NS
-#define E4NS 4
-#define E4CTAS 3
-#define E4SEG 9
+#define E4NS 3
+#define E4CTAS 5
+#define E4SEG 2
+#define E4NW 2
+#define E4NS2 4
+#define E4CTAS2 3
+#define E4SEG2 2
+#define E4NW2 2
 #endif
 constexpr int kE4MaxPages = 512;              // block-table entries a CTA caches
 constexpr int kE4Stage = 2 * kStageKeys * kE4Row;   // K and V rows of a stage
@@ -67,10 +72,10 @@ struct E4Args {
 
 // Shared memory (byte offsets from a 1024-aligned base).  The ring's rows are reused by the
 // combine once the key loop is over.
-template <int MT, int NS>
+template <int MT, int NW, int NS>
 struct E4Smem {
     static constexpr int Tp = 16 * MT;
-    static constexpr int Tc = MT == 1 ? 16 : kE4MaxT;                 // rows of the chunk region
+    static constexpr int Tc = 16;                                     // rows of the chunk region (one m-tile)
     static constexpr int off_q = NS * kE4Stage;                       // q, then bf16((q + v) 2^-x)
     static constexpr int off_qu = off_q + Tp * kRowBytes;             // fp16((q + u) 2^-x)
     static constexpr int off_ck = off_qu + Tp * kRowBytes;            // the chunk's K and V rows
@@ -83,21 +88,18 @@ struct E4Smem {
     static constexpr int bytes = off_gt + 1024;                       // + Tp * gt_w * 2
     // combine: the warps' partials, then the CTA's own for its cluster
     static constexpr int comb_o = 0;
-    static constexpr int comb_m = comb_o + kConsumerWarps * Tp * kOW * 4;
-    static constexpr int comb_l = comb_m + kConsumerWarps * Tp * 4;
-    static constexpr int part_o = comb_l + kConsumerWarps * Tp * 4;
+    static constexpr int comb_m = comb_o + NW * Tp * kOW * 4;
+    static constexpr int comb_l = comb_m + NW * Tp * 4;
+    static constexpr int part_o = comb_l + NW * Tp * 4;
     static constexpr int part_m = part_o + Tp * kHeadDim * 4;
     static constexpr int part_l = part_m + Tp * 4;
     static_assert(part_l + Tp * 4 <= NS * kE4Stage, "combine area");
     static_assert(off_q % 1024 == 0 && off_ck % 1024 == 0 && off_sc % 16 == 0, "TMA alignment");
 };
 
-// Byte offset of 16-byte chunk c (0..3) of row r in a tile of 64-byte rows written by TMA with
-// 64-byte swizzling (tile base 512-byte aligned).
-__device__ __forceinline__ uint32_t swz64(int r, int c)
-{
-    return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
+// Byte offset of 16-byte chunk c (0..3) of key r in a tile of 64-byte rows, two to a 128-byte line,
+// written by TMA with 128-byte swizzling (tile base 1024-byte aligned).
+__device__ __forceinline__ uint32_t swz_key(int r, int c) { return swz128(r >> 1, 4 * (r & 1) + c); }
 
 // Bytes 0, 1 (lo) and 2, 3 (hi) of w, e4m3, as pairs of fp16 (exact).
 __device__ __forceinline__ void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
@@ -172,10 +174,10 @@ __device__ __forceinline__ void load_slice(E4Slice& x, uint32_t k_s, uint32_t v_
     for (int n = 0; n < 2; ++n)
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x.k[n].x), "=r"(x.k[n].y), "=r"(x.k[n].z), "=r"(x.k[n].w)
-                     : "r"(k_s + swz64(4 * (g4 >> 1) + 2 * n + (g4 & 1), t4)));
+                     : "r"(k_s + swz_key(4 * (g4 >> 1) + 2 * n + (g4 & 1), t4)));
 #pragma unroll
     for (int dp = 0; dp < 2; ++dp)
-        ldsm8_x2_t(v_s + swz64(lane & 15, 2 * dp + (lane >> 4)), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
+        ldsm8_x2_t(v_s + swz_key(lane & 15, 2 * dp + (lane >> 4)), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
     const uint8_t* p = sc + 4 * (t4 & 1) + (t4 >> 1) * far_off;
     x.ks = *reinterpret_cast<const uint32_t*>(p);
     x.vs = *reinterpret_cast<const uint32_t*>(p + v_off);
@@ -234,26 +236,27 @@ __device__ __forceinline__ void load_a(uint32_t (&f)[4][4], const uint8_t* tile,
     }
 }
 
-// Two column tiles of the position table (PosTable in attn_core.cuh; each row times its 2^-x): the CTA's
-// Tp query rows (qa: bf16((q + v) 2^-x)) against rel rows 8 tile .. and 8 tile + 32 .. of the segment, the rows in the ring
-// slot `rows` (64 of them, 128-byte swizzled).  G[i][c] goes to gs[i * W + c + i + 1], so that query i and the
+// A warp's column tiles of the position table (PosTable in attn_core.cuh; each row times its 2^-x): the CTA's
+// Tp query rows (qa: bf16((q + v) 2^-x)) against every NW-th eight of the 64 rel rows in the ring slot `rows`
+// (128-byte swizzled), table columns col0 ...  G[i][c] goes to gs[i * W + c + i + 1], so that query i and the
 // segment's key j read gs[i * W + j + Tp].  Every lane arrives on release_bar once it has read its rows.
-template <int MT>
+template <int MT, int NW>
 __device__ __forceinline__ void table_tiles(uint16_t* gs, int W, const uint32_t (&qa)[MT][4][4], const uint8_t* rows,
                                             int col0, int ntiles, int warp, int lane, uint32_t release_bar)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
-    uint4 bl[2], bh[2];
+    constexpr int N = 8 / NW;
+    uint4 bl[N], bh[N];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int r = 8 * (warp + 4 * u) + g4;
+    for (int u = 0; u < N; ++u) {
+        const int r = 8 * (warp + NW * u) + g4;
         bl[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4));
         bh[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4 + 1));
     }
     mbar_arrive_release(release_bar);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        if (warp + 4 * u >= ntiles) break;
+    for (int u = 0; u < N; ++u) {
+        if (warp + NW * u >= ntiles) break;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             float c[4];
@@ -262,7 +265,7 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, int W, const uint32_t 
             mma_bf16_16816(c, qa[mt][2], bh[u].x, bh[u].y);
             mma_bf16_16816(c, qa[mt][3], bh[u].z, bh[u].w);
             // columns past the last stay within their row (its stride leaves room for a tile)
-            uint16_t* d = gs + (16 * mt + g4) * (W + 1) + 1 + 2 * t4 + col0 + 8 * (warp + 4 * u);
+            uint16_t* d = gs + (16 * mt + g4) * (W + 1) + 1 + 2 * t4 + col0 + 8 * (warp + NW * u);
             const uint32_t w0 = pack_bf16(c[0], c[1]), w1 = pack_bf16(c[2], c[3]);
             d[0] = static_cast<uint16_t>(w0);
             d[1] = static_cast<uint16_t>(w0 >> 16);
@@ -481,13 +484,14 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <int MT, int NS, int CTAS, bool FUSED>
-__global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
+template <int MT, int NW, int NS, int CTAS, bool FUSED>
+__global__ void __launch_bounds__(32 * (NW + 1), CTAS) chunk_e4m3_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r, const E4Args a)
 {
-    using SP = E4Smem<MT, NS>;
-    constexpr int Tp = SP::Tp;
+    static_assert(!FUSED || MT == 1, "the chunk region holds one m-tile's rows");
+    using SP = E4Smem<MT, NW, NS>;
+    constexpr int Tp = SP::Tp, kCons = 32 * NW;   // consumer threads
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_addr(sm);
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     const int i0 = qt * Tp;                       // the CTA's first query
     const int Tq = min(Tp, T - i0);               // its queries
     unsigned err = 0;
-    const bool producer = warp == kConsumerWarps;
+    const bool producer = warp == NW;
     if (producer && lane == 0) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_k);
@@ -518,15 +522,16 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     __shared__ int s_failed;
 
     int C = __ldg(a.cache_seqlens + b);
-    // consumers, T <= 16: the thread's two chunk rows (eight lanes each), requested first of all
-    uint4 pre[2] = {};
+    // consumers: the thread's chunk rows (eight lanes each), requested first of all
+    constexpr int kRounds = 32 / (4 * NW);
+    uint4 pre[kRounds] = {};
     if (FUSED && !producer && split == S - 1) {
-        if constexpr (MT == 1) {
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv)
-                if (tid >> 3 < T)
-                    pre[kv] = __ldg(reinterpret_cast<const uint4*>(
-                        (kv ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + (tid >> 3)) * H + h) * kE4Row) + (lane & 7));
+        for (int i = 0; i < kRounds; ++i) {
+            const int r = (tid >> 3) + 4 * NW * i, t = r & 15;
+            if (t < T)
+                pre[i] = __ldg(reinterpret_cast<const uint4*>(
+                    (r >= 16 ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + t) * H + h) * kE4Row) + (lane & 7));
         }
     }
     if (producer) {
@@ -539,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         if (lane == 0) {
             for (int i = 0; i < NS; ++i) {
                 mbar_init(bar_full + 8 * i, 1);
-                mbar_init(bar_empty + 8 * i, 32 * kConsumerWarps);
+                mbar_init(bar_empty + 8 * i, kCons);
             }
             mbar_init(bar_q, 1);
             fence_mbar_init();
@@ -552,9 +557,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             if (lane + 32 * k < a.mbps) s_bt[lane + 32 * k] = row[k];
         for (int i = lane + 32 * kRowRegs; i < a.mbps; i += 32) s_bt[i] = __ldg(bt_row + i);
         __syncwarp();
-        named_bar_arrive(2, kThreads);
+        named_bar_arrive(2, kCons + 32);
     } else {
-        named_bar_sync(2, kThreads);
+        named_bar_sync(2, kCons + 32);
     }
     if (C < 0) { C = 0; err |= kErrBounds; }
     const int sh = a.bs_shift, bs = a.block_size;
@@ -625,10 +630,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 const int in_page = j & (bs - 1);
                 const long long page = static_cast<long long>(valid ? blk : 0) * H + h;
                 // an invalid block's box lies outside the pool and reads zeros
-                const int row = valid ? static_cast<int>(page * bs) + in_page : -2 * box;
+                const int line = valid ? static_cast<int>((page * bs + in_page) >> 1) : -2 * box;
                 const uint32_t dst = sb + slot * kE4Stage + q * box * kE4Row;
                 if (lane < 16) {
-                    tma_load_2d_hint(dst, &tm_k, bar, 0, row, pol);
+                    tma_load_2d_hint(dst, &tm_k, bar, 0, line, pol);
                     if (valid) {
                         const uint8_t* src = a.kv_scale + 2 * page * bs + in_page;
                         if (bs <= kStageKeys) {
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                         }
                     }
                 } else {
-                    tma_load_2d_hint(dst + kStageKeys * kE4Row, &tm_v, bar, 0, row, pol);
+                    tma_load_2d_hint(dst + kStageKeys * kE4Row, &tm_v, bar, 0, line, pol);
                 }
             }
             ++n_issued;
@@ -667,18 +672,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     if (FUSED && chunk_here) {
         // the chunk's rows: quantised into the chunk region (rows past T zero) and, by the first
         // query tile, into the pool.  Eight lanes per row.
-        const int nrow = (T + 15) & ~15;
-#pragma unroll 1
-        for (int r = tid >> 3; r < 2 * nrow; r += 4 * kConsumerWarps) {
-            const int kv = r >= nrow, t = r - kv * nrow, l8 = lane & 7;
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            const int r = (tid >> 3) + 4 * NW * i, kv = r >= 16, t = r & 15, l8 = lane & 7;
             uint2 q = make_uint2(0u, 0u);
             uint32_t byte = 0;
             if (t < nc) {
                 float x[8];
-                if constexpr (MT == 1)
-                    unpack8(kv ? pre[1] : pre[0], x);
-                else
-                    load8((kv ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + t) * H + h) * kE4Row + 8 * l8, x);
+                unpack8(pre[i], x);
                 byte = e4m3_quantise8(x, 0xffu << (lane & 24), q);
                 const int p = C + t;
                 const int blk = s_bt[p >> sh];
@@ -693,19 +694,19 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                     if (l8 == 0) a.kv_scale[(2 * page + kv) * bs + slot] = static_cast<uint8_t>(byte);
                 }
             }
-            *reinterpret_cast<uint2*>(sm + SP::off_ck + kv * SP::Tc * kE4Row + swz64(t, l8 >> 1) + 8 * (l8 & 1)) = q;
+            *reinterpret_cast<uint2*>(sm + SP::off_ck + kv * SP::Tc * kE4Row + swz_key(t, l8 >> 1) + 8 * (l8 & 1)) = q;
             if (l8 == 0) sm[SP::off_csc + kv * SP::Tc + t] = static_cast<uint8_t>(byte);
         }
     }
     if (!e4_wait(bar_q, 0)) failed = true;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int r = 0; r < Tp; r += 4 * NW)
         prepare_row(sm + SP::off_q, sm + SP::off_qu, s_pow, a.pos_bias_u + h * kHeadDim, a.pos_bias_v + h * kHeadDim,
-                    16 * mt + (tid >> 3), lane & 7);
-    named_bar_sync(1, 32 * kConsumerWarps);   // the query tiles and the chunk region are complete
-    const int jl = 16 * warp;   // this warp's keys of a stage
-    const int next8 = box == 8 ? 16 : 8;   // scales of keys 8 .. 15 of a slice, from those of keys 0 .. 7
-    const int sc_off = ((jl >> box_sh) << (box_sh + 1)) + (jl & (box - 1));
+                    r + (tid >> 3), lane & 7);
+    named_bar_sync(1, kCons);   // the query tiles and the chunk region are complete
+    // this warp's keys of a stage: 16 from each of 16 (warp + NW u)
+    const int far_off = box == 8 ? 16 : 8;   // scales of keys 8 .. 15 of a slice, from those of keys 0 .. 7
+    auto scale_off = [&](int jl) { return ((jl >> box_sh) << (box_sh + 1)) + (jl & (box - 1)); };
     E4Acc acc[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -731,10 +732,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             for (int r = 0; r < nrel; ++r, ++it) {
                 const int slot = it % NS;
                 if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
-                table_tiles<MT>(gs, W, qa, sm + slot * kE4Stage, 64 * r, ntiles - 8 * r, warp, lane,
+                table_tiles<MT, NW>(gs, W, qa, sm + slot * kE4Stage, 64 * r, ntiles - 8 * r, warp, lane,
                                 bar_empty + 8 * slot);
             }
-            named_bar_sync(1, 32 * kConsumerWarps);   // the table is complete
+            named_bar_sync(1, kCons);   // the table is complete
         }
         uint32_t qu[MT][4][4];
         float sc[MT][2];
@@ -748,32 +749,38 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         for (int s = seg0; s < seg1; ++s, ++it) {
             const int slot = it % NS;
             if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
-            const int kv = min(kc - s * kStageKeys, kStageKeys) - jl;
-            E4Slice x;
-            if (kv > 0)
-                load_slice(x, sb + slot * kE4Stage + jl * kE4Row, sb + slot * kE4Stage + (kStageKeys + jl) * kE4Row,
-                           sm + SP::off_sc + slot * 2 * kStageKeys + sc_off, next8, box, lane);
+            constexpr int N = 4 / NW;
+            const int kv = min(kc - s * kStageKeys, kStageKeys);
+            E4Slice x[N];
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                const int jl = 16 * (warp + NW * u);
+                if (kv > jl)
+                    load_slice(x[u], sb + slot * kE4Stage + jl * kE4Row, sb + slot * kE4Stage + (kStageKeys + jl) * kE4Row,
+                               sm + SP::off_sc + slot * 2 * kStageKeys + scale_off(jl), far_off, box, lane);
+            }
             mbar_arrive_release(bar_empty + 8 * slot);
-            if (kv > 0) {
-                const int x0 = (s - seg0) * kStageKeys + jl + Tp;
-                slice_e4m3<MT>(acc, qu, x, gs + x0, W, true, kv, sc, E, lane);
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                const int jl = 16 * (warp + NW * u);
+                if (kv > jl)
+                    slice_e4m3<MT>(acc, qu, x[u], gs + (s - seg0) * kStageKeys + jl + Tp, W, true, kv - jl, sc, E, lane);
             }
         }
         if (last) {
-            if (nc > jl && !failed) {
+            if (nc > 0 && warp == NW - 1 && !failed) {   // the chunk: one slice
                 E4Slice x;
-                load_slice(x, sb + SP::off_ck + jl * kE4Row, sb + SP::off_ck + (SP::Tc + jl) * kE4Row,
-                           sm + SP::off_csc + jl, 8, SP::Tc, lane);
-                const int x0 = C + jl - jbase + Tp;
-                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 3) == 0, nc - jl, sc, E, lane);
+                load_slice(x, sb + SP::off_ck, sb + SP::off_ck + SP::Tc * kE4Row, sm + SP::off_csc, 8, SP::Tc, lane);
+                const int x0 = C - jbase + Tp;
+                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 3) == 0, nc, sc, E, lane);
             }
             break;
         }
-        named_bar_sync(1, 32 * kConsumerWarps);   // the table has been read
+        named_bar_sync(1, kCons);   // the table has been read
     }
     if (failed) s_failed = 1;
     grid_dep_trigger();
-    named_bar_sync(1, 32 * kConsumerWarps);
+    named_bar_sync(1, kCons);
     if (s_failed) err |= kErrTimeout;
     if (err) atomicOr(a.status, err);
     if (s_failed && S == 1) return;
@@ -802,19 +809,19 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             }
         }
     }
-    named_bar_sync(1, 32 * kConsumerWarps);
+    named_bar_sync(1, kCons);
     if (S == 1) {
-        for (int i = tid; i < Tq * 8; i += 32 * kConsumerWarps) {
+        for (int i = tid; i < Tq * 8; i += kCons) {
             const int row = i >> 3, d0 = (i & 7) * 8;
             float m = comb_m[row], l = comb_l[row];
 #pragma unroll
-            for (int k = 1; k < kConsumerWarps; ++k) {
+            for (int k = 1; k < NW; ++k) {
                 m = fmaxf(m, comb_m[k * Tp + row]);
                 l = fmaxf(l, comb_l[k * Tp + row]);
             }
             float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < kConsumerWarps; ++k) {
+            for (int k = 0; k < NW; ++k) {
                 const float w = part_weight(comb_m[k * Tp + row], m);
                 sum += part_weight(comb_l[k * Tp + row], l);
                 const float4* src = reinterpret_cast<const float4*>(comb_o + (k * Tp + row) * kOW + d0);
@@ -833,17 +840,17 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     float* part_o = reinterpret_cast<float*>(sm + SP::part_o);
     float* part_m = reinterpret_cast<float*>(sm + SP::part_m);
     float* part_l = reinterpret_cast<float*>(sm + SP::part_l);
-    for (int i = tid; i < Tq * kHeadDim; i += 32 * kConsumerWarps) {
+    for (int i = tid; i < Tq * kHeadDim; i += kCons) {
         const int row = i / kHeadDim, d = i % kHeadDim;
         float m = -INFINITY, l = -INFINITY, o = 0.f, sum = 0.f;
         if (!s_failed) {
 #pragma unroll
-            for (int k = 0; k < kConsumerWarps; ++k) {
+            for (int k = 0; k < NW; ++k) {
                 m = fmaxf(m, comb_m[k * Tp + row]);
                 l = fmaxf(l, comb_l[k * Tp + row]);
             }
 #pragma unroll
-            for (int k = 0; k < kConsumerWarps; ++k) {
+            for (int k = 0; k < NW; ++k) {
                 o += part_weight(comb_m[k * Tp + row], m) * comb_o[(k * Tp + row) * kOW + d];
                 sum += part_weight(comb_l[k * Tp + row], l);
             }
@@ -856,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     }
     cluster_sync();
     // rows split, split + S, ... of the cluster's queries are finished here
-    for (int row = split + S * warp; row < Tq; row += S * kConsumerWarps) {
+    for (int row = split + S * warp; row < Tq; row += S * NW) {
         float m = -INFINITY, l = -INFINITY;
         for (int k = 0; k < S; ++k) {
             m = fmaxf(m, ld_cluster(sb + SP::part_m + 4 * row, k));
@@ -994,21 +1001,21 @@ int g_smem_done_e4[8][64];
 // stride of 16 mod 64 elements (8 mod 32 words) keeps the 8-byte reads of a slice conflict-free.
 inline int e4_table_stride(int nkeys, int Tp) { return ((nkeys + 2 * Tp + 63) & ~63) + 16; }
 
-template <int MT, int NS, int CTAS, bool FUSED>
-oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int slot, cudaStream_t stream)
+template <int MT, int NW, int NS, int CTAS, bool FUSED>
+oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int seg, int slot, cudaStream_t stream)
 {
-    using SP = E4Smem<MT, NS>;
+    using SP = E4Smem<MT, NW, NS>;
     CUtensorMap tm_q, tm_k, tm_v, tm_r;
     const int box = a.block_size < kStageKeys ? a.block_size : kStageKeys;
     const long long rows = static_cast<long long>(a.num_blocks) * a.H * a.block_size;
     if (!encode_rows_bf16(&tm_q, q, static_cast<long long>(B) * a.T, a.H, SP::Tp) ||
         !encode_rows_bf16(&tm_r, a.rel, a.R, a.H, kStageKeys) || !encode_rows_e4m3(&tm_k, a.k_pool, rows, box) || !encode_rows_e4m3(&tm_v, a.v_pool, rows, box))
         return OASR_ERR_INVALID_ARG;
-    auto kern = chunk_e4m3_kernel<MT, NS, CTAS, FUSED>;
+    auto kern = chunk_e4m3_kernel<MT, NW, NS, CTAS, FUSED>;
     // segments of at most eight stages and a part of one, sized for the keys a call can have
     const int stages = (k_max + kStageKeys - 1) / kStageKeys;
-    a.seg = stages < E4SEG ? stages : E4SEG;
-    a.gt_w = e4_table_stride(a.seg * kStageKeys + (FUSED ? ((a.T + 15) & ~15) : 0), SP::Tp);
+    a.seg = stages < seg ? stages : seg;
+    a.gt_w = e4_table_stride(a.seg * kStageKeys + (FUSED ? 16 : 0), SP::Tp);
     const int smem = SP::bytes + SP::Tp * a.gt_w * 2;
     if (!ensure_smem(kern, smem, g_smem_done_e4[slot])) return OASR_ERR_CUDA;
     a.q_tiles = (a.T + SP::Tp - 1) / SP::Tp;
@@ -1019,7 +1026,7 @@ oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int slot, cuda
     if (pairs * a.splits > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(pairs * a.splits));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * (NW + 1));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1060,12 +1067,13 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
         if (!aligned16(p)) return OASR_ERR_INVALID_ARG;
     unsigned* status = status_word();
     if (!status || !sm_count()) return OASR_ERR_CUDA;
+    // more than one m-tile of queries (and fp32): the append first, then the attention over the pool
+    if (FUSED && (dt == OASR_F32 || T > 16)) {
+        const oasr_status st = oasr_paged_append_e4m3(k_new, v_new, k_pool, v_pool, kv_scale, num_blocks, block_size,
+                                                      bt, mbps, cs, B, T, H, D, dt, stream);
+        if (st != OASR_OK) return st;
+    }
     if (dt == OASR_F32) {
-        if (FUSED) {
-            const oasr_status st = oasr_paged_append_e4m3(k_new, v_new, k_pool, v_pool, kv_scale, num_blocks,
-                                                          block_size, bt, mbps, cs, B, T, H, D, dt, stream);
-            if (st != OASR_OK) return st;
-        }
         chunk_e4m3_f32_kernel<<<static_cast<unsigned>(B) * H, 128, 0, stream>>>(
             static_cast<const float*>(q), static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool),
             static_cast<const uint8_t*>(kv_scale), num_blocks, block_size, bt, mbps, cs,
@@ -1098,8 +1106,8 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     const long long pages = static_cast<long long>(mbps) * block_size, dist = static_cast<long long>(R) - T + 1;
     const long long k_max = pages < dist ? pages : dist;
     const int km = static_cast<int>(k_max < T ? T : k_max);
-    if (T <= 16) return launch_e4<1, E4NS, E4CTAS, FUSED>(q, a, km, B, FUSED ? 1 : 0, stream);
-    return launch_e4<2, 6, 2, FUSED>(q, a, km, B, FUSED ? 3 : 2, stream);
+    if (T <= 16) return launch_e4<1, E4NW, E4NS, E4CTAS, FUSED>(q, a, km, B, E4SEG, FUSED ? 1 : 0, stream);
+    return launch_e4<2, E4NW2, E4NS2, E4CTAS2, false>(q, a, km, B, E4SEG2, 2, stream);
 }
 
 }  // namespace

@@ -27,8 +27,9 @@ bool encode_rows_bf16(CUtensorMap* map, const void* base, long long rows, int H,
 // 8 rows of one head form one 1 KB swizzle atom.  Returns false if the driver rejects it.
 bool encode_head_pairs_bf16(CUtensorMap* map, const void* base, long long rows, int H, int box_rows);
 
-// Encode a 2-D map over 64-byte rows (the 8-bit pools) with a box of box_rows rows, 64-byte
-// swizzled.  Returns false if the driver rejects it.
+// Encode a 2-D map over 64-byte rows (the 8-bit pools; an even number of them) with a box of box_rows
+// rows, as 128-byte lines of two, 128-byte swizzled; its second coordinate counts lines.  Returns
+// false if the driver rejects it.
 bool encode_rows_e4m3(CUtensorMap* map, const void* base, long long rows, int box_rows);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
