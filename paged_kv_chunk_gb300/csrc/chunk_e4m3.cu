@@ -35,24 +35,22 @@ namespace oasr {
 namespace {
 
 #ifndef E4NS
-#define E4NS 3
-#define E4CTAS 5
-#define E4SEG 2
-#define E4NW 2
-#define E4NS2 4
-#define E4CTAS2 3
-#define E4SEG2 2
-#define E4NW2 2
+#define E4NS 5
+#define E4CTAS 3
+#define E4NS2 6
+#define E4CTAS2 2
 #endif
-constexpr int kE4MaxPages = 512;              // block-table entries a CTA caches
-constexpr int kE4Stage = 2 * kStageKeys * kE4Row;   // K and V rows of a stage
+constexpr int kE4MaxPages = 512;                    // block-table entries a CTA caches
+constexpr int kE4Stage = 2 * kStageKeys * kE4Row;   // a ring slot: K and V rows of a stage, or 64 rel rows
 constexpr int kE4MaxT = 64;
+constexpr int kChunkRows = 16;                      // rows of the chunk region (fused: T <= 16)
+constexpr int kE4Consumers = 32 * kConsumerWarps;
+constexpr int kTableW = 256;                        // columns of the position table's window
+constexpr int kTableStride = kTableW + 16;          // 8 mod 32 words: 8-byte reads without conflicts
 constexpr int kMaxRowExp = 120;
-constexpr float kNoMax = -3.0e38f;   // the running maximum before any key
+constexpr float kNoMax = -3.0e38f;                  // the running maximum before any key
 
 struct E4Args {
-    const __nv_bfloat16* k_new;   // fused only
-    const __nv_bfloat16* v_new;   // fused only
     uint8_t* k_pool;
     uint8_t* v_pool;
     uint8_t* kv_scale;
@@ -60,41 +58,42 @@ struct E4Args {
     const int32_t* cache_seqlens;
     const uint16_t* pos_bias_u;
     const uint16_t* pos_bias_v;
-    const uint16_t* rel;
     uint16_t* out;
     unsigned* status;
     int num_blocks, block_size, bs_shift, mbps, T, H, R;
+    int items;        // (stream, head, query tile)
     int q_tiles, splits;
-    int seg;          // stages per segment of the position table
-    int gt_w;         // row stride of the table (bf16 elements)
     float scale_log2; // scale * log2(e)
 };
 
-// Shared memory (byte offsets from a 1024-aligned base).  The ring's rows are reused by the
-// combine once the key loop is over.
-template <int MT, int NW, int NS>
+// Shared memory (byte offsets from a 1024-aligned base).
+template <int MT, int NS, bool FUSED>
 struct E4Smem {
     static constexpr int Tp = 16 * MT;
-    static constexpr int Tc = 16;                                     // rows of the chunk region (one m-tile)
-    static constexpr int off_q = NS * kE4Stage;                       // q, then bf16((q + v) 2^-x)
-    static constexpr int off_qu = off_q + Tp * kRowBytes;             // fp16((q + u) 2^-x)
-    static constexpr int off_ck = off_qu + Tp * kRowBytes;            // the chunk's K and V rows
-    static constexpr int off_sc = off_ck + 2 * Tc * kE4Row;           // scales [NS][2 * 64]
-    static constexpr int off_csc = off_sc + NS * 2 * kStageKeys;      // the chunk's [2][Tc]
-    static constexpr int off_re = off_csc + 2 * Tc;                   // 2^x of the query rows
-    static constexpr int off_bt = off_re + Tp * 4;
-    static constexpr int off_bar = off_bt + kE4MaxPages * 4;          // full[NS], empty[NS], q
-    static constexpr int off_gt = (off_bar + (2 * NS + 1) * 8 + 15) & ~15;
-    static constexpr int bytes = off_gt + 1024;                       // + Tp * gt_w * 2
-    // combine: the warps' partials, then the CTA's own for its cluster
-    static constexpr int comb_o = 0;
-    static constexpr int comb_m = comb_o + NW * Tp * kOW * 4;
-    static constexpr int comb_l = comb_m + NW * Tp * 4;
-    static constexpr int part_o = comb_l + NW * Tp * 4;
+    static constexpr int off_ring = 0;
+    static constexpr int off_q = off_ring + NS * kE4Stage;            // q as it comes
+    static constexpr int off_qv = off_q + Tp * kRowBytes;             // bf16((q + v) 2^-x)
+    static constexpr int off_qu = off_qv + Tp * kRowBytes;            // fp16((q + u) 2^-x)
+    static constexpr int off_cn = off_qu + Tp * kRowBytes;            // the chunk's K and V rows as they come ...
+    static constexpr int off_ck = off_cn + (FUSED ? 2 * kChunkRows * kRowBytes : 0);   // ... and quantised
+    static constexpr int off_gt = off_ck + (FUSED ? 2 * kChunkRows * kE4Row : 0);      // the position table's window;
+    static constexpr int off_co = off_gt;                             // after the keys: two shares' rows, m, lambda
+    static constexpr int off_cm = off_co + 2 * Tp * kOW * 4;
+    static constexpr int off_cl = off_cm + 2 * Tp * 4;
+    static constexpr int gt_bytes = Tp * kTableStride * 2, comb_bytes = off_cl + 2 * Tp * 4 - off_co;
+    static constexpr int off_sc = off_gt + (gt_bytes > comb_bytes ? gt_bytes : comb_bytes);   // scales [NS][2 * 64]
+    static constexpr int off_csc = off_sc + NS * 2 * kStageKeys;      // the chunk's [2][16]
+    static constexpr int off_re = off_csc + 2 * kChunkRows;           // 2^x of the query rows
+    static constexpr int off_item = off_re + Tp * 4;                  // cache length of the item, two of them; failed
+    static constexpr int off_bar = off_item + 16;                     // full[NS], empty[NS], q full, q free
+    static constexpr int off_bt = off_bar + (2 * NS + 2) * 8;         // block-table row, two of them
+    static constexpr int bytes = off_bt;                              // + 2 * mbps * 4
+    // clusters (one item each): the CTA's share, in the ring's memory
+    static constexpr int part_o = 0;
     static constexpr int part_m = part_o + Tp * kHeadDim * 4;
     static constexpr int part_l = part_m + Tp * 4;
-    static_assert(part_l + Tp * 4 <= NS * kE4Stage, "combine area");
-    static_assert(off_q % 1024 == 0 && off_ck % 1024 == 0 && off_sc % 16 == 0, "TMA alignment");
+    static_assert(part_l + Tp * 4 <= NS * kE4Stage, "share area");
+    static_assert(off_ck % 1024 == 0 && off_gt % 16 == 0 && off_sc % 16 == 0 && off_bar % 8 == 0, "alignment");
 };
 
 // Byte offset of 16-byte chunk c (0..3) of key r in a tile of 64-byte rows, two to a 128-byte line,
@@ -166,30 +165,43 @@ struct E4Slice {
 // k_s, v_s: shared addresses of the slice's first rows; sc: its first K scale, v_off bytes before its first
 // V scale; far_off: bytes from the scales of keys 0 .. 7 to those of keys 8 .. 15 (pages of eight keys
 // hold 16 scales each).
-__device__ __forceinline__ void load_slice(E4Slice& x, uint32_t k_s, uint32_t v_s, const uint8_t* sc, int far_off,
-                                           int v_off, int lane)
+// The lane's part of the addresses is computed once (E4Lane); the other rows and chunks it reads differ from
+// it in single bits of the swizzled offset.
+struct E4Lane {
+    uint32_t k, v, sc;
+};
+
+__device__ __forceinline__ E4Lane e4_lane(int lane, int far_off)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
+    E4Lane l;
+    l.k = swz_key(4 * (g4 >> 1) + (g4 & 1), t4);
+    l.v = swz_key(lane & 15, lane >> 4);
+    l.sc = 4 * (t4 & 1) + (t4 >> 1) * far_off;
+    return l;
+}
+
+__device__ __forceinline__ void load_slice(E4Slice& x, const E4Lane& l, uint32_t k_s, uint32_t v_s, uint32_t sc, uint32_t v_off)
+{
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2; ++n)   // two keys on: the next line, its swizzle's lowest bit flipped
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x.k[n].x), "=r"(x.k[n].y), "=r"(x.k[n].z), "=r"(x.k[n].w)
-                     : "r"(k_s + swz_key(4 * (g4 >> 1) + 2 * n + (g4 & 1), t4)));
+                     : "r"((k_s + l.k) ^ (144u * n)));
 #pragma unroll
-    for (int dp = 0; dp < 2; ++dp)
-        ldsm8_x2_t(v_s + swz_key(lane & 15, 2 * dp + (lane >> 4)), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
-    const uint8_t* p = sc + 4 * (t4 & 1) + (t4 >> 1) * far_off;
-    x.ks = *reinterpret_cast<const uint32_t*>(p);
-    x.vs = *reinterpret_cast<const uint32_t*>(p + v_off);
+    for (int dp = 0; dp < 2; ++dp)   // two chunks on
+        ldsm8_x2_t((v_s + l.v) ^ (32u * dp), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.ks) : "r"(sc + l.sc));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.vs) : "r"(sc + l.sc + v_off));
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Eight dims (chunk l8) of one query row, by eight neighbouring lanes: bf16(q + v) over q's own place in
-// the swizzled tile and fp16(q + u) into qu, both times the power of two that brings the row's largest
-// |q + u| into [1, 2), and its inverse into row_pow.  u, v: the head's biases.
-__device__ __forceinline__ void prepare_row(uint8_t* q_tile, uint8_t* qu, float* row_pow, const uint16_t* u,
-                                            const uint16_t* v, int row, int l8)
+// Eight dims (chunk l8) of one query row, by eight neighbouring lanes: bf16(q + v) into the swizzled
+// tile qv and fp16(q + u) into qu, both times the power of two that brings the row's largest |q + u|
+// into [1, 2), and its inverse into row_pow.  u, v: the head's biases.
+__device__ __forceinline__ void prepare_row(const uint8_t* q_tile, uint8_t* qv, uint8_t* qu, float* row_pow,
+                                            const uint16_t* u, const uint16_t* v, int row, int l8)
 {
     const uint4 qw = *reinterpret_cast<const uint4*>(q_tile + swz128(row, l8));
     const uint4 uw = __ldg(reinterpret_cast<const uint4*>(u) + l8), vw = __ldg(reinterpret_cast<const uint4*>(v) + l8);
@@ -213,7 +225,7 @@ __device__ __forceinline__ void prepare_row(uint8_t* q_tile, uint8_t* qu, float*
         pv[i] = pack_bf16((bf16_lo(q[i]) + bf16_lo(vn[i])) * f, (bf16_hi(q[i]) + bf16_hi(vn[i])) * f);
     }
     *reinterpret_cast<uint4*>(qu + swz128(row, l8)) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
-    *reinterpret_cast<uint4*>(q_tile + swz128(row, l8)) = make_uint4(pv[0], pv[1], pv[2], pv[3]);
+    *reinterpret_cast<uint4*>(qv + swz128(row, l8)) = make_uint4(pv[0], pv[1], pv[2], pv[3]);
     if (l8 == 0) row_pow[row] = pow2(x);
 }
 
@@ -221,13 +233,15 @@ __device__ __forceinline__ void prepare_row(uint8_t* q_tile, uint8_t* qu, float*
 // position t4 holds dims 16 t4 .., k-step ks the dims 4 ks .. 4 ks + 3 of them.
 __device__ __forceinline__ void load_a(uint32_t (&f)[4][4], const uint8_t* tile, int mt, int lane)
 {
-    const int g4 = lane >> 2, t4 = lane & 3;
+    const uint32_t at = smem_addr(tile) + swz128(lane >> 2, 2 * (lane & 3));
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const int row = 16 * mt + g4 + 8 * half;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(tile + swz128(row, 2 * t4 + c));
+            uint4 w;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"((at ^ (16u * c)) + (2 * mt + half) * 1024));
             f[2 * c][half] = w.x;
             f[2 * c][half + 2] = w.y;
             f[2 * c + 1][half] = w.z;
@@ -236,41 +250,48 @@ __device__ __forceinline__ void load_a(uint32_t (&f)[4][4], const uint8_t* tile,
     }
 }
 
-// A warp's column tiles of the position table (PosTable in attn_core.cuh; each row times its 2^-x): the CTA's
-// Tp query rows (qa: bf16((q + v) 2^-x)) against every NW-th eight of the 64 rel rows in the ring slot `rows`
-// (128-byte swizzled), table columns col0 ...  G[i][c] goes to gs[i * W + c + i + 1], so that query i and the
-// segment's key j read gs[i * W + j + Tp].  Every lane arrives on release_bar once it has read its rows.
-template <int MT, int NW>
-__device__ __forceinline__ void table_tiles(uint16_t* gs, int W, const uint32_t (&qa)[MT][4][4], const uint8_t* rows,
-                                            int col0, int ntiles, int warp, int lane, uint32_t release_bar)
+// A warp's column tiles of the position term: the CTA's Tp query rows (qv tile) against two eights of the
+// 64 rel rows in the ring slot `rows` (128-byte swizzled), which are columns col0 .. col0 + 63 of the item's
+// table G[i][c], c counting rel rows from the one of the last query's first key.  G[i][c] goes to
+// gs[i * kTableStride + (c + i + 1) % kTableW] rounded to bf16 (a relative 2^-8 of the position term, the
+// size of the rounding of q + v), so that query i and key j read column (j + Tp) % kTableW of row i.
+// Every lane arrives on release_bar once it has read its rows.
+template <int MT>
+__device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, const uint8_t* rows, int col0, int warp,
+                                            int lane, uint32_t release_bar)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
-    constexpr int N = 8 / NW;
-    uint4 bl[N], bh[N];
+    uint4 bl[2], bh[2];
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-        const int r = 8 * (warp + NW * u) + g4;
+    for (int u = 0; u < 2; ++u) {
+        const int r = 8 * (warp + kConsumerWarps * u) + g4;
         bl[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4));
         bh[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4 + 1));
     }
     mbar_arrive_release(release_bar);
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-        if (warp + NW * u >= ntiles) break;
+    for (int mt = 0; mt < MT; ++mt) {
+        uint32_t qa[4][4];
+        load_a(qa, qv, mt, lane);
+        uint16_t* r0 = gs + (16 * mt + g4) * kTableStride;
+        uint16_t* r1 = r0 + 8 * kTableStride;
+        float c[2][4];
+        mma_bf16_first(c[0], qa[0], bl[0].x, bl[0].y);
+        mma_bf16_first(c[1], qa[0], bl[1].x, bl[1].y);
+        mma_bf16_16816(c[0], qa[1], bl[0].z, bl[0].w);
+        mma_bf16_16816(c[1], qa[1], bl[1].z, bl[1].w);
+        mma_bf16_16816(c[0], qa[2], bh[0].x, bh[0].y);
+        mma_bf16_16816(c[1], qa[2], bh[1].x, bh[1].y);
+        mma_bf16_16816(c[0], qa[3], bh[0].z, bh[0].w);
+        mma_bf16_16816(c[1], qa[3], bh[1].z, bh[1].w);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            float c[4];
-            mma_bf16_first(c, qa[mt][0], bl[u].x, bl[u].y);
-            mma_bf16_16816(c, qa[mt][1], bl[u].z, bl[u].w);
-            mma_bf16_16816(c, qa[mt][2], bh[u].x, bh[u].y);
-            mma_bf16_16816(c, qa[mt][3], bh[u].z, bh[u].w);
-            // columns past the last stay within their row (its stride leaves room for a tile)
-            uint16_t* d = gs + (16 * mt + g4) * (W + 1) + 1 + 2 * t4 + col0 + 8 * (warp + NW * u);
-            const uint32_t w0 = pack_bf16(c[0], c[1]), w1 = pack_bf16(c[2], c[3]);
-            d[0] = static_cast<uint16_t>(w0);
-            d[1] = static_cast<uint16_t>(w0 >> 16);
-            d[8 * W + 8] = static_cast<uint16_t>(w1);
-            d[8 * W + 9] = static_cast<uint16_t>(w1 >> 16);
+        for (int u = 0; u < 2; ++u) {
+            const int x = col0 + 8 * (warp + kConsumerWarps * u) + 2 * t4 + 16 * mt + g4 + 1;
+            const uint32_t w0 = pack_bf16(c[u][0], c[u][1]), w1 = pack_bf16(c[u][2], c[u][3]);
+            r0[x & (kTableW - 1)] = static_cast<uint16_t>(w0);
+            r0[(x + 1) & (kTableW - 1)] = static_cast<uint16_t>(w0 >> 16);
+            r1[(x + 8) & (kTableW - 1)] = static_cast<uint16_t>(w1);
+            r1[(x + 9) & (kTableW - 1)] = static_cast<uint16_t>(w1 >> 16);
         }
     }
 }
@@ -283,34 +304,40 @@ struct E4Acc {
     float m[2], l[2];
 };
 
-// One warp, 16 MT query rows against one slice.  gq: the position table at the slice's first key
-// (key jl of query row i reads gq[i * W + jl], aligned: eight bytes at a time); keys [0, kvalid) of the slice exist; sc: scale * log2(e) * 2^x of
-// rows g4 and g4 + 8 of each m-tile.
+// One warp, 16 MT query rows against one slice.  x0: the position table's column of the slice's first key
+// (aligned: a multiple of 16, so that a lane's four keys are eight bytes of one row); keys [0, kvalid) of
+// the slice exist; sc: scale * log2(e) * 2^x of rows g4 and g4 + 8 of each m-tile.
 //
 // P is 2^(t - m), at most one, and goes into the product as fp16: its rounding is 2^-11 of each
 // weight and never more than 2^-25 of the row's largest contribution, whatever the scales.  The
 // row sum takes p back out of it, l += P 2^(E - ev); a slice with a scale below 2^(E - 40) (a row of
 // zeros has 2^-100), where that could underflow, sums 2^(s - m + E) of its own.
 template <int MT>
-__device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu)[MT][4][4], E4Slice& x,
-                                           const uint16_t* gq, int W, bool aligned, int kvalid,
+__device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_tile, E4Slice& x,
+                                           const uint16_t* gs, int x0, bool aligned, int kvalid,
                                            const float (&sc)[MT][2], int& E, int lane)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
     float s[MT][2][4];
+    {
+        // (q + u) from shared memory again for each slice: kept in registers it costs more in spilled addresses
+        uint32_t qu[MT][4][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-        const uint32_t w[4] = {x.k[n].x, x.k[n].y, x.k[n].z, x.k[n].w};
+        for (int mt = 0; mt < MT; ++mt) load_a(qu[mt], qu_tile, mt, lane);
+        const uint32_t w[2][4] = {{x.k[0].x, x.k[0].y, x.k[0].z, x.k[0].w}, {x.k[1].x, x.k[1].y, x.k[1].z, x.k[1].w}};
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t b0, b1;
-            e4m3_to_f16(w[ks], b0, b1);
+        for (int ks = 0; ks < 4; ++ks) {   // the tiles in turn: independent products back to back
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (ks == 0)
-                    mma_f16_first(s[mt][n], qu[mt][ks], b0, b1);
-                else
-                    mma_f16_16816(s[mt][n], qu[mt][ks], b0, b1);
+            for (int n = 0; n < 2; ++n) {
+                uint32_t b0, b1;
+                e4m3_to_f16(w[n][ks], b0, b1);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    if (ks == 0)
+                        mma_f16_first(s[mt][n], qu[mt][ks], b0, b1);
+                    else
+                        mma_f16_16816(s[mt][n], qu[mt][ks], b0, b1);
+                }
             }
         }
     }
@@ -350,18 +377,20 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint32_t (&qu
     for (int mt = 0; mt < MT; ++mt) {
         E4Acc& a = acc[mt];
         float mx0 = a.m[0], mx1 = a.m[1];
-        const uint16_t* r0 = gq + (16 * mt + g4) * W + 4 * t4;
-        const uint16_t* r1 = r0 + 8 * W;
+        const uint16_t* r0 = gs + (16 * mt + g4) * kTableStride;
+        const uint16_t* r1 = r0 + 8 * kTableStride;
         uint32_t y0[2], y1[2];
         if (aligned) {
-            const uint2 p0 = *reinterpret_cast<const uint2*>(r0), p1 = *reinterpret_cast<const uint2*>(r1);
+            const int c = (x0 & (kTableW - 1)) + 4 * t4;
+            const uint2 p0 = *reinterpret_cast<const uint2*>(r0 + c), p1 = *reinterpret_cast<const uint2*>(r1 + c);
             y0[0] = p0.x; y0[1] = p0.y;
             y1[0] = p1.x; y1[1] = p1.y;
         } else {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                y0[n] = r0[2 * n] | static_cast<uint32_t>(r0[2 * n + 1]) << 16;
-                y1[n] = r1[2 * n] | static_cast<uint32_t>(r1[2 * n + 1]) << 16;
+                const int c = (x0 + 4 * t4 + 2 * n) & (kTableW - 1), d = (x0 + 4 * t4 + 2 * n + 1) & (kTableW - 1);
+                y0[n] = r0[c] | static_cast<uint32_t>(r0[d]) << 16;
+                y1[n] = r1[c] | static_cast<uint32_t>(r1[d]) << 16;
             }
         }
 #pragma unroll
@@ -484,179 +513,197 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <int MT, int NW, int NS, int CTAS, bool FUSED>
-__global__ void __launch_bounds__(32 * (NW + 1), CTAS) chunk_e4m3_kernel(
+// What a CTA does with one item: keys, ring slots and the position table, from the stream's cache length.
+struct E4Item {
+    int C, K;          // cached frames; keys (frames and chunk, as far as the table reaches)
+    int kc, nc;        // keys from the pool, from the chunk region
+    int st0, st1;      // stages of this CTA's share
+    int nrel;          // rel slots: the table has a column for each distance of the share's keys
+    int off;           // rel row of query i and key j: off + j - i
+    unsigned err;
+};
+
+template <int MT, bool FUSED>
+__device__ __forceinline__ E4Item e4_item(const E4Args& a, int C, int split)
+{
+    E4Item t;
+    t.err = 0;
+    const int cap = a.mbps << a.bs_shift;                 // keys the block table holds (at most 2^17)
+    if (C < 0) { C = 0; t.err = kErrBounds; }
+    if (C > cap) { C = cap; t.err = kErrBounds; }
+    t.C = C;
+    t.K = C + a.T;
+    if (t.K > cap) { t.K = cap; t.err = kErrBounds; }
+    if (C + 2 * a.T - 1 > a.R) t.err = kErrBounds;        // distances the rel table does not hold
+    t.off = a.R - a.T - C;
+    t.kc = FUSED ? C : t.K;
+    const int n = (t.kc + kStageKeys - 1) / kStageKeys;
+    t.st0 = n * split / a.splits;                         // n <= 2^11
+    t.st1 = n * (split + 1) / a.splits;
+    const bool last = split == a.splits - 1;              // the chunk follows the last pool keys
+    t.nc = FUSED && last ? t.K - t.kc : 0;
+    const int nkeys = (last ? t.K : t.st1 * kStageKeys) - t.st0 * kStageKeys;
+    t.nrel = nkeys > 0 ? (nkeys + 16 * MT - 1 + 63) >> 6 : 0;
+    return t;
+}
+
+// Persistent: CTA x takes items x, x + grid, ...  The producer warp runs ahead of the consumers by the
+// ring's slots, across items, so the next item's rows arrive while this one's are multiplied and joined.
+// Ring order of an item with stages s = 0, 1, ..: rel slots 0 and 1, stage 0, rel slot 2, stage 1, ...
+// (stage s needs the table's columns up to rel slot s + 1).
+template <int MT, int NS, int CTAS, bool FUSED>
+__global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r, const E4Args a)
+    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r,
+    const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn, const E4Args a)
 {
     static_assert(!FUSED || MT == 1, "the chunk region holds one m-tile's rows");
-    using SP = E4Smem<MT, NW, NS>;
-    constexpr int Tp = SP::Tp, kCons = 32 * NW;   // consumer threads
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    using SP = E4Smem<MT, NS, FUSED>;
+    constexpr int Tp = SP::Tp;
+    extern __shared__ __align__(1024) uint8_t sm[];   // the only shared memory: its base is aligned
     const uint32_t sb = smem_addr(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int S = a.splits, T = a.T, H = a.H;
-    int idx = blockIdx.x;
-    const int split = idx % S;
-    idx /= S;
-    const int qt = idx % a.q_tiles;
-    idx /= a.q_tiles;
-    const int b = idx / H, h = idx - b * H;
-    const int i0 = qt * Tp;                       // the CTA's first query
-    const int Tq = min(Tp, T - i0);               // its queries
+    const int S = a.splits, T = a.T, H = a.H, sh = a.bs_shift, bs = a.block_size;
+    const int split = blockIdx.x % S, first = blockIdx.x / S, step = gridDim.x / S;
+    const uint32_t bar_full = sb + SP::off_bar;
+    const uint32_t bar_empty = bar_full + NS * 8;
+    const uint32_t bar_q = bar_empty + NS * 8;    // an item's q, chunk rows, cache length and block-table row are in
+    const uint32_t bar_qfree = bar_q + 8;         // ... and have been read
+    int* s_len = reinterpret_cast<int*>(sm + SP::off_item);
+    int* s_bt = reinterpret_cast<int*>(sm + SP::off_bt);
+    volatile int& s_failed = s_len[2];
     unsigned err = 0;
-    const bool producer = warp == NW;
-    if (producer && lane == 0) {
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, kE4Consumers);
+        }
+        mbar_init(bar_q, 1);
+        mbar_init(bar_qfree, kE4Consumers);
+        fence_mbar_init();
+        s_failed = 0;
+    }
+    if (warp == kConsumerWarps && lane == 0) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
         prefetch_tensormap(&tm_r);
     }
-    grid_dep_wait();
-    const uint32_t bar_full = sb + SP::off_bar;
-    const uint32_t bar_empty = bar_full + NS * 8;
-    const uint32_t bar_q = bar_empty + NS * 8;
-    float* s_pow = reinterpret_cast<float*>(sm + SP::off_re);
-    int* s_bt = reinterpret_cast<int*>(sm + SP::off_bt);
-    __shared__ int s_failed;
+    __syncthreads();
+    grid_dep_wait();   // the previous grid on the stream has finished (programmatic launch)
 
-    int C = __ldg(a.cache_seqlens + b);
-    // consumers: the thread's chunk rows (eight lanes each), requested first of all
-    constexpr int kRounds = 32 / (4 * NW);
-    uint4 pre[kRounds] = {};
-    if (FUSED && !producer && split == S - 1) {
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-            const int r = (tid >> 3) + 4 * NW * i, t = r & 15;
-            if (t < T)
-                pre[i] = __ldg(reinterpret_cast<const uint4*>(
-                    (r >= 16 ? a.v_new : a.k_new) + ((static_cast<long long>(b) * T + t) * H + h) * kE4Row) + (lane & 7));
-        }
-    }
-    if (producer) {
-        const int32_t* bt_row = a.block_table + static_cast<long long>(b) * a.mbps;
-        constexpr int kRowRegs = 4;
-        int row[kRowRegs];
-#pragma unroll
-        for (int k = 0; k < kRowRegs; ++k)
-            if (lane + 32 * k < a.mbps) row[k] = __ldg(bt_row + lane + 32 * k);
-        if (lane == 0) {
-            for (int i = 0; i < NS; ++i) {
-                mbar_init(bar_full + 8 * i, 1);
-                mbar_init(bar_empty + 8 * i, kCons);
-            }
-            mbar_init(bar_q, 1);
-            fence_mbar_init();
-            s_failed = 0;
-            mbar_arrive_expect_tx(bar_q, Tp * kRowBytes);
-            tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, h, b * T + i0);
-        }
-#pragma unroll
-        for (int k = 0; k < kRowRegs; ++k)
-            if (lane + 32 * k < a.mbps) s_bt[lane + 32 * k] = row[k];
-        for (int i = lane + 32 * kRowRegs; i < a.mbps; i += 32) s_bt[i] = __ldg(bt_row + i);
-        __syncwarp();
-        named_bar_arrive(2, kCons + 32);
-    } else {
-        named_bar_sync(2, kCons + 32);
-    }
-    if (C < 0) { C = 0; err |= kErrBounds; }
-    const int sh = a.bs_shift, bs = a.block_size;
-    const int cap = a.mbps << sh;                 // keys the table's pages hold (at most 2^17)
-    if (C > cap) { C = cap; err |= kErrBounds; }
-    int K = C + T;
-    if (K > cap) { K = cap; err |= kErrBounds; }
-    if (C + 2 * T - 1 > a.R) err |= kErrBounds;   // distances the rel table does not hold
-    const int off = a.R - T - C;                  // rel row of query i and key j: off + j - i
-    const int kc = FUSED ? C : K;       // keys that come from the pool
-    const int n_all = (kc + kStageKeys - 1) / kStageKeys;
-    const int st0 = static_cast<int>(static_cast<long long>(n_all) * split / S);
-    const int st1 = static_cast<int>(static_cast<long long>(n_all) * (split + 1) / S);
-    const bool chunk_here = FUSED && split == S - 1;   // the chunk follows the last pool keys
-    const int nc = chunk_here ? K - kc : 0;            // its keys (fewer when it runs past the table)
-    const int box = min(bs, kStageKeys), box_sh = min(sh, 6);
-    // keys of the segment of stages [seg0, seg1): the last one of the last split has the chunk's too
-    auto segment_keys = [&](int seg0, int seg1) {
-        return max(0, ((seg1 >= st1 && chunk_here) ? K : min(seg1 * kStageKeys, kc)) - seg0 * kStageKeys);
-    };
-    // its position table has a column for each distance: rel rows rho0 .., in ring slots of 64 rows
-    auto segment_rel = [&](int nkeys) { return nkeys ? (nkeys + Tp - 1 + 63) >> 6 : 0; };
-
-    if (producer) {
+    if (warp == kConsumerWarps) {
+        // ------------------------------------------------------------ producer
         const uint64_t pol = policy_evict_first();
-        int n_issued = 0;
+        const int box = min(bs, kStageKeys), box_sh = min(sh, 6);
+        int n_issued = 0, n_items = 0;
         bool ok = true;
-        for (int seg0 = st0;;) {
-            const int seg1 = min(seg0 + a.seg, st1);
-            const int nrel = segment_rel(segment_keys(seg0, seg1));
-            for (int r = 0; r < nrel && ok; ++r) {
-                const int it = n_issued, slot = it % NS;
-                ok = __all_sync(0xffffffffu, it < NS || e4_wait(bar_empty + 8 * slot, ((it / NS) - 1) & 1));
+        auto acquire = [&]() {   // the next slot is free
+            ok = ok && __all_sync(0xffffffffu, n_issued < NS ||
+                                                   e4_wait(bar_empty + 8 * (n_issued % NS), ((n_issued / NS) - 1) & 1));
+            return ok;
+        };
+        constexpr int kRowRegs = 4;   // entries of a lane loaded ahead (128 pages); the rest of a longer row later
+        int C = 0, row[kRowRegs];
+        auto request = [&](int item) {
+            const int b = item / (H * a.q_tiles);
+            C = __ldg(a.cache_seqlens + b);
+#pragma unroll
+            for (int k = 0; k < kRowRegs; ++k)
+                if (lane + 32 * k < a.mbps) row[k] = __ldg(a.block_table + static_cast<long long>(b) * a.mbps + lane + 32 * k);
+        };
+        if (first < a.items) request(first);
+        for (int item = first; item < a.items && ok; item += step, ++n_items) {
+            const int qt = item % a.q_tiles, bh = item / a.q_tiles;
+            const int b = bh / H, h = bh - b * H, i0 = qt * Tp;
+            // the item's cache length and block-table row, into the buffers of the item before last
+            if (n_items >= 1) {
+                ok = __all_sync(0xffffffffu, e4_wait(bar_qfree, (n_items - 1) & 1));
                 if (!ok) break;
+            }
+            int* bt = s_bt + (n_items & 1) * a.mbps;
+#pragma unroll
+            for (int k = 0; k < kRowRegs; ++k)
+                if (lane + 32 * k < a.mbps) bt[lane + 32 * k] = row[k];
+            for (int i = lane + 32 * kRowRegs; i < a.mbps; i += 32)
+                bt[i] = __ldg(a.block_table + static_cast<long long>(b) * a.mbps + i);
+            if (lane == 0) s_len[n_items & 1] = C;
+            const E4Item t = e4_item<MT, FUSED>(a, C, split);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar_q, Tp * kRowBytes + (FUSED ? 2 * kChunkRows * kRowBytes : 0));
+                tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, h, b * T + i0);
+                if (FUSED) {
+                    tma_load_3d(sb + SP::off_cn, &tm_kn, bar_q, 0, h, b * T);
+                    tma_load_3d(sb + SP::off_cn + kChunkRows * kRowBytes, &tm_vn, bar_q, 0, h, b * T);
+                }
+            }
+            if (item + step < a.items) request(item + step);
+            auto issue_rel = [&](int r) {
+                if (!acquire()) return;
                 if (lane == 0) {
-                    const uint32_t bar = bar_full + 8 * slot;
+                    const uint32_t bar = bar_full + 8 * (n_issued % NS);
                     mbar_arrive_expect_tx(bar, kE4Stage);
-                    tma_load_3d(sb + slot * kE4Stage, &tm_r, bar, 0, h, off + (seg0 + r) * kStageKeys - i0 - (Tp - 1));
+                    tma_load_3d(sb + (n_issued % NS) * kE4Stage, &tm_r, bar, 0, h,
+                                t.off + (t.st0 + r) * kStageKeys - i0 - (Tp - 1));
+                }
+                ++n_issued;
+            };
+            if (t.nrel > 0) issue_rel(0);
+            for (int s = t.st0; s < t.st1 && ok; ++s) {
+                if (s - t.st0 + 1 < t.nrel) issue_rel(s - t.st0 + 1);
+                if (!acquire()) break;
+                const int slot = n_issued % NS;
+                const uint32_t bar = bar_full + 8 * slot;
+                const int j0 = s * kStageKeys;
+                const int nbox = min(kStageKeys >> box_sh, (t.kc - j0 + box - 1) >> box_sh);
+                // lane q: K box of page piece q and its scales, lane 16 + q: its V box
+                const int q = lane & 15;
+                const int j = j0 + q * box;
+                const int blk = q < nbox ? bt[j >> sh] : -1;
+                const bool valid = blk >= 0 && blk < a.num_blocks;
+                const uint32_t sc_dst = SP::off_sc + slot * 2 * kStageKeys + q * 2 * box;
+                if (q < nbox && !valid) {   // no such block: its rows read as zeros, with scales of zero
+                    err |= kErrBounds;
+                    if (lane < 16) {
+                        for (int i = 0; i < box / 2; ++i) *reinterpret_cast<uint32_t*>(sm + sc_dst + 4 * i) = 0u;
+                        fence_proxy_async_smem();
+                    }
+                }
+                const int nvalid = __popc(__ballot_sync(0xffffffffu, valid) & 0xffffu);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nbox * box * 2 * kE4Row + nvalid * 2 * box));
+                __syncwarp();
+                if (q < nbox) {
+                    const int in_page = j & (bs - 1);
+                    const long long page = static_cast<long long>(valid ? blk : 0) * H + h;
+                    // an invalid block's box lies outside the pool and reads zeros
+                    const int line = valid ? static_cast<int>((page * bs + in_page) >> 1) : -2 * box;
+                    const uint32_t dst = sb + slot * kE4Stage + q * box * kE4Row;
+                    if (lane < 16) {
+                        tma_load_2d_hint(dst, &tm_k, bar, 0, line, pol);
+                        if (valid) {
+                            const uint8_t* src = a.kv_scale + 2 * page * bs + in_page;
+                            if (bs <= kStageKeys) {
+                                bulk_load(sb + sc_dst, src, 2 * box, bar);   // K and V scales of the page are adjacent
+                            } else {
+                                bulk_load(sb + sc_dst, src, box, bar);
+                                bulk_load(sb + sc_dst + box, src + bs, box, bar);
+                            }
+                        }
+                    } else {
+                        tma_load_2d_hint(dst + kStageKeys * kE4Row, &tm_v, bar, 0, line, pol);
+                    }
                 }
                 ++n_issued;
             }
-            for (int s = seg0; s < seg1 && ok; ++s) {
-            const int it = n_issued, slot = it % NS;
-            ok = __all_sync(0xffffffffu, it < NS || e4_wait(bar_empty + 8 * slot, ((it / NS) - 1) & 1));
-            if (!ok) break;
-            const uint32_t bar = bar_full + 8 * slot;
-            const int j0 = s * kStageKeys;
-            const int nbox = min(kStageKeys >> box_sh, (kc - j0 + box - 1) >> box_sh);
-            // lane q: K box of page piece q and its scales, lane 16 + q: its V box
-            const int q = lane & 15;
-            const int j = j0 + q * box;
-            const int blk = q < nbox ? s_bt[j >> sh] : -1;
-            const bool valid = blk >= 0 && blk < a.num_blocks;
-            const uint32_t sc_dst = sb + SP::off_sc + slot * 2 * kStageKeys + q * 2 * box;
-            if (q < nbox && !valid) {   // no such block: its rows read as zeros, with scales of zero
-                err |= kErrBounds;
-                if (lane < 16) {
-                    for (int i = 0; i < box / 2; ++i)
-                        *reinterpret_cast<uint32_t*>(sm + (sc_dst - sb) + 4 * i) = 0u;
-                    fence_proxy_async_smem();
-                }
-            }
-            const int nvalid = __popc(__ballot_sync(0xffffffffu, valid) & 0xffffu);
-            if (lane == 0)
-                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nbox * box * 2 * kE4Row + nvalid * 2 * box));
-            __syncwarp();
-            if (q < nbox) {
-                const int in_page = j & (bs - 1);
-                const long long page = static_cast<long long>(valid ? blk : 0) * H + h;
-                // an invalid block's box lies outside the pool and reads zeros
-                const int line = valid ? static_cast<int>((page * bs + in_page) >> 1) : -2 * box;
-                const uint32_t dst = sb + slot * kE4Stage + q * box * kE4Row;
-                if (lane < 16) {
-                    tma_load_2d_hint(dst, &tm_k, bar, 0, line, pol);
-                    if (valid) {
-                        const uint8_t* src = a.kv_scale + 2 * page * bs + in_page;
-                        if (bs <= kStageKeys) {
-                            bulk_load(sc_dst, src, 2 * box, bar);   // K and V scales of the page are adjacent
-                        } else {
-                            bulk_load(sc_dst, src, box, bar);
-                            bulk_load(sc_dst + box, src + bs, box, bar);
-                        }
-                    }
-                } else {
-                    tma_load_2d_hint(dst + kStageKeys * kE4Row, &tm_v, bar, 0, line, pol);
-                }
-            }
-            ++n_issued;
-            }
-            seg0 = seg1;
-            if (seg0 >= st1 || !ok) break;
         }
         if (!ok) err |= kErrTimeout;
         // every copy this CTA requested lands before it ends
         for (int x = n_issued > NS ? n_issued - NS : 0; x < n_issued; ++x)
             if (!mbar_wait_idle(bar_full + 8 * (x % NS), (x / NS) & 1)) err |= kErrTimeout;
-        if (!mbar_wait_idle(bar_q, 0)) err |= kErrTimeout;
+        if (n_items > 0 && !mbar_wait_idle(bar_q, (n_items - 1) & 1)) err |= kErrTimeout;
         if (err) atomicOr(a.status, err);
         if (S > 1) {
             cluster_sync();
@@ -666,221 +713,229 @@ __global__ void __launch_bounds__(32 * (NW + 1), CTAS) chunk_e4m3_kernel(
     }
 
     // ---------------------------------------------------------------- consumers
-    bool failed = false;
+    const int g4 = lane >> 2, t4 = lane & 3;
+    const int box_sh = min(sh, 6), box = 1 << box_sh;
+    const int jl = 16 * warp;   // this warp's keys of a stage
+    const int far_off = box == 8 ? 16 : 8;   // scales of keys 8 .. 15 of a slice, from those of keys 0 .. 7
+    const int sc_off = SP::off_sc + ((jl >> box_sh) << (box_sh + 1)) + (jl & (box - 1));
+    const E4Lane ll = e4_lane(lane, far_off);
     uint16_t* gs = reinterpret_cast<uint16_t*>(sm + SP::off_gt);
-    const int W = a.gt_w;
-    if (FUSED && chunk_here) {
-        // the chunk's rows: quantised into the chunk region (rows past T zero) and, by the first
-        // query tile, into the pool.  Eight lanes per row.
+    float* s_pow = reinterpret_cast<float*>(sm + SP::off_re);
+    float* comb_o = reinterpret_cast<float*>(sm + SP::off_co);
+    float* comb_m = reinterpret_cast<float*>(sm + SP::off_cm);
+    float* comb_l = reinterpret_cast<float*>(sm + SP::off_cl);
+    bool failed = false;
+    int it = 0, n_items = 0;   // ring slots read, items begun
+#pragma unroll 1
+    for (int item = first; item < a.items; item += step, ++n_items) {
+        const int qt = item % a.q_tiles, bh = item / a.q_tiles;
+        const int b = bh / H, h = bh - b * H, i0 = qt * Tp;
+        if (!failed && !e4_wait(bar_q, n_items & 1)) failed = true;
+        const E4Item t = e4_item<MT, FUSED>(a, failed ? 0 : s_len[n_items & 1], split);
+        err |= t.err;
+        if (FUSED && t.nc > 0 && !failed) {
+            // the chunk's rows, eight lanes each: quantised into the chunk region (rows past T zero) and the pool
+            const int r = tid >> 3, l8 = lane & 7;
+            const int p = t.C + r;
+            const int blk = r < t.nc ? s_bt[(n_items & 1) * a.mbps + (p >> sh)] : -1;
+            const bool valid = blk >= 0 && blk < a.num_blocks;
+            if (r < t.nc && !valid) err |= kErrBounds;   // dropped by the append: reads as zeros
+            const long long page = static_cast<long long>(valid ? blk : 0) * H + h;
+            const int slot = p & (bs - 1);
 #pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-            const int r = (tid >> 3) + 4 * NW * i, kv = r >= 16, t = r & 15, l8 = lane & 7;
-            uint2 q = make_uint2(0u, 0u);
-            uint32_t byte = 0;
-            if (t < nc) {
+            for (int kv = 0; kv < 2; ++kv) {
                 float x[8];
-                unpack8(pre[i], x);
-                byte = e4m3_quantise8(x, 0xffu << (lane & 24), q);
-                const int p = C + t;
-                const int blk = s_bt[p >> sh];
-                if (blk < 0 || blk >= a.num_blocks) {   // dropped by the append: reads as zeros
-                    err |= kErrBounds;
-                    q = make_uint2(0u, 0u);
-                    byte = 0;
-                } else if (qt == 0) {
-                    const int slot = p & (bs - 1);
-                    const long long page = static_cast<long long>(blk) * H + h;
+                unpack8(*reinterpret_cast<const uint4*>(sm + SP::off_cn + kv * kChunkRows * kRowBytes + swz128(r, l8)), x);
+                uint2 q;
+                uint32_t byte = e4m3_quantise8(x, 0xffffffffu, q);
+                if (valid) {
                     *reinterpret_cast<uint2*>((kv ? a.v_pool : a.k_pool) + (page * bs + slot) * kE4Row + 8 * l8) = q;
                     if (l8 == 0) a.kv_scale[(2 * page + kv) * bs + slot] = static_cast<uint8_t>(byte);
+                } else {
+                    q = make_uint2(0u, 0u);
+                    byte = 0;
                 }
+                *reinterpret_cast<uint2*>(sm + SP::off_ck + kv * kChunkRows * kE4Row + swz_key(r, l8 >> 1) + 8 * (l8 & 1)) = q;
+                if (l8 == 0) sm[SP::off_csc + kv * kChunkRows + r] = static_cast<uint8_t>(byte);
             }
-            *reinterpret_cast<uint2*>(sm + SP::off_ck + kv * SP::Tc * kE4Row + swz_key(t, l8 >> 1) + 8 * (l8 & 1)) = q;
-            if (l8 == 0) sm[SP::off_csc + kv * SP::Tc + t] = static_cast<uint8_t>(byte);
         }
-    }
-    if (!e4_wait(bar_q, 0)) failed = true;
 #pragma unroll
-    for (int r = 0; r < Tp; r += 4 * NW)
-        prepare_row(sm + SP::off_q, sm + SP::off_qu, s_pow, a.pos_bias_u + h * kHeadDim, a.pos_bias_v + h * kHeadDim,
-                    r + (tid >> 3), lane & 7);
-    named_bar_sync(1, kCons);   // the query tiles and the chunk region are complete
-    // this warp's keys of a stage: 16 from each of 16 (warp + NW u)
-    const int far_off = box == 8 ? 16 : 8;   // scales of keys 8 .. 15 of a slice, from those of keys 0 .. 7
-    auto scale_off = [&](int jl) { return ((jl >> box_sh) << (box_sh + 1)) + (jl & (box - 1)); };
-    E4Acc acc[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[mt].o[d][0] = acc[mt].o[d][1] = acc[mt].o[d][2] = acc[mt].o[d][3] = 0.f;
-        acc[mt].m[0] = acc[mt].m[1] = kNoMax;
-        acc[mt].l[0] = acc[mt].l[1] = 0.f;
-    }
-    int E = -127;   // the smallest a scale byte says; the first keys raise it
-    int it = 0;   // ring slots read
-#pragma unroll 1
-    for (int seg0 = st0;; seg0 += a.seg) {
-        const int seg1 = min(seg0 + a.seg, st1);
-        const bool last = seg1 >= st1;
-        const int jbase = seg0 * kStageKeys;
-        const int nkeys = segment_keys(seg0, seg1);
-        if (nkeys) {
-            uint32_t qa[MT][4][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) load_a(qa[mt], sm + SP::off_q, mt, lane);
-            const int ntiles = (nkeys + Tp - 1 + 7) >> 3, nrel = segment_rel(nkeys);
-#pragma unroll 1
-            for (int r = 0; r < nrel; ++r, ++it) {
-                const int slot = it % NS;
-                if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
-                table_tiles<MT, NW>(gs, W, qa, sm + slot * kE4Stage, 64 * r, ntiles - 8 * r, warp, lane,
-                                bar_empty + 8 * slot);
-            }
-            named_bar_sync(1, kCons);   // the table is complete
-        }
-        uint32_t qu[MT][4][4];
+        for (int r = 0; r < Tp; r += 4 * kConsumerWarps)
+            prepare_row(sm + SP::off_q, sm + SP::off_qv, sm + SP::off_qu, s_pow, a.pos_bias_u + h * kHeadDim,
+                        a.pos_bias_v + h * kHeadDim, r + (tid >> 3), lane & 7);
+        fence_proxy_async_smem();   // the next item's q and chunk rows overwrite what was read here
+        mbar_arrive_release(bar_qfree);
+        named_bar_sync(1, kE4Consumers);   // the query tiles and the chunk region are complete
+
         float sc[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            load_a(qu[mt], sm + SP::off_qu, mt, lane);
-            sc[mt][0] = a.scale_log2 * s_pow[16 * mt + (lane >> 2)];
-            sc[mt][1] = a.scale_log2 * s_pow[16 * mt + (lane >> 2) + 8];
+            sc[mt][0] = a.scale_log2 * s_pow[16 * mt + g4];
+            sc[mt][1] = a.scale_log2 * s_pow[16 * mt + g4 + 8];
         }
-#pragma unroll 1
-        for (int s = seg0; s < seg1; ++s, ++it) {
-            const int slot = it % NS;
-            if (failed || !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) { failed = true; break; }
-            constexpr int N = 4 / NW;
-            const int kv = min(kc - s * kStageKeys, kStageKeys);
-            E4Slice x[N];
-#pragma unroll
-            for (int u = 0; u < N; ++u) {
-                const int jl = 16 * (warp + NW * u);
-                if (kv > jl)
-                    load_slice(x[u], sb + slot * kE4Stage + jl * kE4Row, sb + slot * kE4Stage + (kStageKeys + jl) * kE4Row,
-                               sm + SP::off_sc + slot * 2 * kStageKeys + scale_off(jl), far_off, box, lane);
-            }
-            mbar_arrive_release(bar_empty + 8 * slot);
-#pragma unroll
-            for (int u = 0; u < N; ++u) {
-                const int jl = 16 * (warp + NW * u);
-                if (kv > jl)
-                    slice_e4m3<MT>(acc, qu, x[u], gs + (s - seg0) * kStageKeys + jl + Tp, W, true, kv - jl, sc, E, lane);
-            }
-        }
-        if (last) {
-            if (nc > 0 && warp == NW - 1 && !failed) {   // the chunk: one slice
-                E4Slice x;
-                load_slice(x, sb + SP::off_ck, sb + SP::off_ck + SP::Tc * kE4Row, sm + SP::off_csc, 8, SP::Tc, lane);
-                const int x0 = C - jbase + Tp;
-                slice_e4m3<MT>(acc, qu, x, gs + x0, W, (x0 & 3) == 0, nc, sc, E, lane);
-            }
-            break;
-        }
-        named_bar_sync(1, kCons);   // the table has been read
-    }
-    if (failed) s_failed = 1;
-    grid_dep_trigger();
-    named_bar_sync(1, kCons);
-    if (s_failed) err |= kErrTimeout;
-    if (err) atomicOr(a.status, err);
-    if (s_failed && S == 1) return;
-    // the warps' partials, in the ring's memory (every stage has been read)
-    float* comb_o = reinterpret_cast<float*>(sm + SP::comb_o);
-    float* comb_m = reinterpret_cast<float*>(sm + SP::comb_m);
-    float* comb_l = reinterpret_cast<float*>(sm + SP::comb_l);
-    if (!s_failed) {
-        const int g4 = lane >> 2, t4 = lane & 3;
+        E4Acc acc[MT];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int d = 0; d < 8; ++d) acc[mt].o[d][0] = acc[mt].o[d][1] = acc[mt].o[d][2] = acc[mt].o[d][3] = 0.f;
+            acc[mt].m[0] = acc[mt].m[1] = kNoMax;
+            acc[mt].l[0] = acc[mt].l[1] = 0.f;
+        }
+        int E = -127;   // the smallest a scale byte says; the first keys raise it
+        const int n = t.st1 - t.st0;
+        // rel slots 0 and 1, then a stage and the next rel slot at a time; after the stages the chunk
+        int r = 0;
+        auto next_rel = [&]() {
+            if (!failed && !e4_wait(bar_full + 8 * (it % NS), (it / NS) & 1)) failed = true;
+            if (!failed)
+                table_tiles<MT>(gs, sm + SP::off_qv, sm + (it % NS) * kE4Stage, kStageKeys * r, warp, lane,
+                                bar_empty + 8 * (it % NS));
+            ++it;
+            ++r;
+        };
+        if (t.nrel > 0) next_rel();
+#pragma unroll 1
+        for (int s = 0; s < n; ++s) {
+            if (r < t.nrel) next_rel();
+            named_bar_sync(1, kE4Consumers);   // the columns of this stage's keys are complete
+            const int slot = it % NS;
+            if (!failed && !e4_wait(bar_full + 8 * slot, (it / NS) & 1)) failed = true;
+            ++it;
+            if (failed) continue;
+            const int kv = min(t.kc - (t.st0 + s) * kStageKeys, kStageKeys) - jl;
+            E4Slice x;
+            if (kv > 0)
+                load_slice(x, ll, sb + slot * kE4Stage + jl * kE4Row, sb + slot * kE4Stage + (kStageKeys + jl) * kE4Row,
+                           sb + sc_off + slot * 2 * kStageKeys, box);
+            mbar_arrive_release(bar_empty + 8 * slot);
+            if (kv > 0) slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, s * kStageKeys + jl + Tp, true, kv, sc, E, lane);
+        }
+        if (FUSED && t.nc > 0) {
+            if (n == 0) named_bar_sync(1, kE4Consumers);
+            if (warp == kConsumerWarps - 1 && !failed) {   // one slice
+                E4Slice x;
+                load_slice(x, e4_lane(lane, 8), sb + SP::off_ck, sb + SP::off_ck + kChunkRows * kE4Row, sb + SP::off_csc, kChunkRows);
+                const int x0 = t.C - t.st0 * kStageKeys + Tp;
+                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, x0, (x0 & 15) == 0, t.nc, sc, E, lane);
+            }
+        }
+
+        // the warps' shares of each row: two warps write, two add theirs and write, all finish
+        auto put = [&](int part) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = part * Tp + 16 * mt + g4 + 8 * half;
+#pragma unroll
+                    for (int d = 0; d < 8; ++d)
+                        *reinterpret_cast<float2*>(comb_o + row * kOW + 8 * d + 2 * t4) =
+                            make_float2(acc[mt].o[d][2 * half], acc[mt].o[d][2 * half + 1]);
+                    if (t4 == 0) {
+                        comb_m[row] = acc[mt].m[half];
+                        comb_l[row] = acc[mt].l[half];
+                    }
+                }
+        };
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 float l = acc[mt].l[half];
                 l += __shfl_xor_sync(0xffffffffu, l, 1);
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
-                const int r = warp * Tp + 16 * mt + g4 + 8 * half;
+                acc[mt].l[half] = acc[mt].m[half] - static_cast<float>(E) + log2f(l);   // lambda from here on
+            }
+        named_bar_sync(1, kE4Consumers);   // every warp is done with the table
+        if (warp >= 2) put(warp - 2);
+        if (failed) s_failed = 1;
+        named_bar_sync(1, kE4Consumers);
+        if (warp < 2) {
 #pragma unroll
-                for (int d = 0; d < 8; ++d)
-                    *reinterpret_cast<float2*>(comb_o + r * kOW + 8 * d + 2 * t4) =
-                        make_float2(acc[mt].o[d][2 * half], acc[mt].o[d][2 * half + 1]);
-                if (t4 == 0) {
-                    comb_m[r] = acc[mt].m[half];
-                    comb_l[r] = acc[mt].m[half] - static_cast<float>(E) + log2f(l);
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = warp * Tp + 16 * mt + g4 + 8 * half;
+                    const float m2 = comb_m[row], l2 = comb_l[row];
+                    const float m = fmaxf(acc[mt].m[half], m2), l = fmaxf(acc[mt].l[half], l2);
+                    const float w1 = part_weight(acc[mt].m[half], m), w2 = part_weight(m2, m);
+                    acc[mt].l[half] = l + log2f(part_weight(acc[mt].l[half], l) + part_weight(l2, l));
+                    acc[mt].m[half] = m;
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) {
+                        const float2 o = *reinterpret_cast<const float2*>(comb_o + row * kOW + 8 * d + 2 * t4);
+                        acc[mt].o[d][2 * half] = acc[mt].o[d][2 * half] * w1 + o.x * w2;
+                        acc[mt].o[d][2 * half + 1] = acc[mt].o[d][2 * half + 1] * w1 + o.y * w2;
+                    }
                 }
+            __syncwarp();
+            put(warp);
+        }
+        if (item + step >= a.items) grid_dep_trigger();   // the next grid may schedule (it waits for this one)
+        named_bar_sync(1, kE4Consumers);
+        if (s_failed) {
+            failed = true;
+            if (S == 1) break;
+        }
+        const int Tq = min(Tp, T - i0);
+        if (S == 1) {
+            for (int i = tid; i < Tq * 8; i += kE4Consumers) {
+                const int row = i >> 3, d0 = (i & 7) * 8;
+                const float m0 = comb_m[row], m1 = comb_m[Tp + row], l0 = comb_l[row], l1 = comb_l[Tp + row];
+                const float m = fmaxf(m0, m1), l = fmaxf(l0, l1);
+                const float f = exp2f(m - l) / (part_weight(l0, l) + part_weight(l1, l));
+                const float w0 = part_weight(m0, m) * f, w1 = part_weight(m1, m) * f;
+                const float4* p0 = reinterpret_cast<const float4*>(comb_o + row * kOW + d0);
+                const float4* p1 = reinterpret_cast<const float4*>(comb_o + (Tp + row) * kOW + d0);
+                uint32_t o[4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float4 x = p0[c], y = p1[c];
+                    o[2 * c] = pack_bf16(x.x * w0 + y.x * w1, x.y * w0 + y.y * w1);
+                    o[2 * c + 1] = pack_bf16(x.z * w0 + y.z * w1, x.w * w0 + y.w * w1);
+                }
+                *reinterpret_cast<uint4*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim + d0) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            continue;
+        }
+        // a cluster's only item: the CTA's share into the ring's memory (every slot has been read)
+        float* part_o = reinterpret_cast<float*>(sm + SP::part_o);
+        float* part_m = reinterpret_cast<float*>(sm + SP::part_m);
+        float* part_l = reinterpret_cast<float*>(sm + SP::part_l);
+        for (int i = tid; i < Tq * kHeadDim; i += kE4Consumers) {
+            const int row = i / kHeadDim, d = i % kHeadDim;
+            const float m0 = comb_m[row], m1 = comb_m[Tp + row], l0 = comb_l[row], l1 = comb_l[Tp + row];
+            const float m = failed ? kNoMax : fmaxf(m0, m1), l = failed ? -INFINITY : fmaxf(l0, l1);
+            part_o[i] = failed ? 0.f : part_weight(m0, m) * comb_o[row * kOW + d] + part_weight(m1, m) * comb_o[(Tp + row) * kOW + d];
+            if (d == 0) {
+                part_m[row] = m;
+                part_l[row] = failed ? l : l + log2f(part_weight(l0, l) + part_weight(l1, l));
             }
         }
-    }
-    named_bar_sync(1, kCons);
-    if (S == 1) {
-        for (int i = tid; i < Tq * 8; i += kCons) {
-            const int row = i >> 3, d0 = (i & 7) * 8;
-            float m = comb_m[row], l = comb_l[row];
-#pragma unroll
-            for (int k = 1; k < NW; ++k) {
-                m = fmaxf(m, comb_m[k * Tp + row]);
-                l = fmaxf(l, comb_l[k * Tp + row]);
+        cluster_sync();
+        // rows split, split + S, ... of the cluster's queries are finished here
+        for (int row = split + S * warp; row < Tq; row += S * kConsumerWarps) {
+            float m = kNoMax, l = -INFINITY;
+            for (int k = 0; k < S; ++k) {
+                m = fmaxf(m, ld_cluster(sb + SP::part_m + 4 * row, k));
+                l = fmaxf(l, ld_cluster(sb + SP::part_l + 4 * row, k));
             }
-            float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < NW; ++k) {
-                const float w = part_weight(comb_m[k * Tp + row], m);
-                sum += part_weight(comb_l[k * Tp + row], l);
-                const float4* src = reinterpret_cast<const float4*>(comb_o + (k * Tp + row) * kOW + d0);
-                const float4 x = src[0], y = src[1];
-                o[0] += w * x.x; o[1] += w * x.y; o[2] += w * x.z; o[3] += w * x.w;
-                o[4] += w * y.x; o[5] += w * y.y; o[6] += w * y.z; o[7] += w * y.w;
+            float o0 = 0.f, o1 = 0.f, sum = 0.f;
+            for (int k = 0; k < S; ++k) {
+                const float w = part_weight(ld_cluster(sb + SP::part_m + 4 * row, k), m);
+                sum += part_weight(ld_cluster(sb + SP::part_l + 4 * row, k), l);
+                o0 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane), k);
+                o1 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane + 1), k);
             }
             const float f = exp2f(m - l) / sum;
-            *reinterpret_cast<uint4*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim + d0) =
-                make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
-                           pack_bf16(o[6] * f, o[7] * f));
+            reinterpret_cast<uint32_t*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim)[lane] =
+                pack_bf16(o0 * f, o1 * f);
         }
-        return;
+        cluster_sync();   // no CTA ends while another may still read its share
     }
-    // the CTA's share
-    float* part_o = reinterpret_cast<float*>(sm + SP::part_o);
-    float* part_m = reinterpret_cast<float*>(sm + SP::part_m);
-    float* part_l = reinterpret_cast<float*>(sm + SP::part_l);
-    for (int i = tid; i < Tq * kHeadDim; i += kCons) {
-        const int row = i / kHeadDim, d = i % kHeadDim;
-        float m = -INFINITY, l = -INFINITY, o = 0.f, sum = 0.f;
-        if (!s_failed) {
-#pragma unroll
-            for (int k = 0; k < NW; ++k) {
-                m = fmaxf(m, comb_m[k * Tp + row]);
-                l = fmaxf(l, comb_l[k * Tp + row]);
-            }
-#pragma unroll
-            for (int k = 0; k < NW; ++k) {
-                o += part_weight(comb_m[k * Tp + row], m) * comb_o[(k * Tp + row) * kOW + d];
-                sum += part_weight(comb_l[k * Tp + row], l);
-            }
-        }
-        part_o[i] = o;
-        if (d == 0) {
-            part_m[row] = m;
-            part_l[row] = l + log2f(sum);
-        }
-    }
-    cluster_sync();
-    // rows split, split + S, ... of the cluster's queries are finished here
-    for (int row = split + S * warp; row < Tq; row += S * NW) {
-        float m = -INFINITY, l = -INFINITY;
-        for (int k = 0; k < S; ++k) {
-            m = fmaxf(m, ld_cluster(sb + SP::part_m + 4 * row, k));
-            l = fmaxf(l, ld_cluster(sb + SP::part_l + 4 * row, k));
-        }
-        float o0 = 0.f, o1 = 0.f, sum = 0.f;
-        for (int k = 0; k < S; ++k) {
-            const float w = part_weight(ld_cluster(sb + SP::part_m + 4 * row, k), m);
-            sum += part_weight(ld_cluster(sb + SP::part_l + 4 * row, k), l);
-            o0 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane), k);
-            o1 += w * ld_cluster(sb + SP::part_o + 4 * (row * kHeadDim + 2 * lane + 1), k);
-        }
-        const float f = exp2f(m - l) / sum;
-        reinterpret_cast<uint32_t*>(a.out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim)[lane] =
-            pack_bf16(o0 * f, o1 * f);
-    }
-    cluster_sync();   // no CTA ends while another may still read its share
+    if (s_failed) err |= kErrTimeout;
+    if (err) atomicOr(a.status, err);
 }
 
 // ----------------------------------------------------------------------------- fp32
@@ -997,36 +1052,36 @@ __global__ void __launch_bounds__(128) chunk_e4m3_f32_kernel(
 
 int g_smem_done_e4[8][64];
 
-// Row stride (bf16 elements) of the position table: every access stays below nkeys + 2 Tp + 8, and a
-// stride of 16 mod 64 elements (8 mod 32 words) keeps the 8-byte reads of a slice conflict-free.
-inline int e4_table_stride(int nkeys, int Tp) { return ((nkeys + 2 * Tp + 63) & ~63) + 16; }
-
-template <int MT, int NW, int NS, int CTAS, bool FUSED>
-oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int seg, int slot, cudaStream_t stream)
+template <int MT, int NS, int CTAS, bool FUSED>
+oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const void* rel, E4Args& a, int k_max, int B,
+                      int slot, cudaStream_t stream)
 {
-    using SP = E4Smem<MT, NW, NS>;
-    CUtensorMap tm_q, tm_k, tm_v, tm_r;
+    using SP = E4Smem<MT, NS, FUSED>;
+    CUtensorMap tm_q, tm_k, tm_v, tm_r, tm_kn, tm_vn;
     const int box = a.block_size < kStageKeys ? a.block_size : kStageKeys;
-    const long long rows = static_cast<long long>(a.num_blocks) * a.H * a.block_size;
-    if (!encode_rows_bf16(&tm_q, q, static_cast<long long>(B) * a.T, a.H, SP::Tp) ||
-        !encode_rows_bf16(&tm_r, a.rel, a.R, a.H, kStageKeys) || !encode_rows_e4m3(&tm_k, a.k_pool, rows, box) || !encode_rows_e4m3(&tm_v, a.v_pool, rows, box))
+    const long long rows = static_cast<long long>(a.num_blocks) * a.H * a.block_size, frames = static_cast<long long>(B) * a.T;
+    if (!encode_rows_bf16(&tm_q, q, frames, a.H, SP::Tp) || !encode_rows_bf16(&tm_r, rel, a.R, a.H, kStageKeys) ||
+        !encode_rows_e4m3(&tm_k, a.k_pool, rows, box) || !encode_rows_e4m3(&tm_v, a.v_pool, rows, box))
         return OASR_ERR_INVALID_ARG;
-    auto kern = chunk_e4m3_kernel<MT, NW, NS, CTAS, FUSED>;
-    // segments of at most eight stages and a part of one, sized for the keys a call can have
-    const int stages = (k_max + kStageKeys - 1) / kStageKeys;
-    a.seg = stages < seg ? stages : seg;
-    a.gt_w = e4_table_stride(a.seg * kStageKeys + (FUSED ? 16 : 0), SP::Tp);
-    const int smem = SP::bytes + SP::Tp * a.gt_w * 2;
+    tm_kn = tm_vn = tm_q;   // unused without the chunk
+    if (FUSED && (!encode_rows_bf16(&tm_kn, k_new, frames, a.H, kChunkRows) ||
+                  !encode_rows_bf16(&tm_vn, v_new, frames, a.H, kChunkRows)))
+        return OASR_ERR_INVALID_ARG;
+    auto kern = chunk_e4m3_kernel<MT, NS, CTAS, FUSED>;
+    const int smem = SP::bytes + 2 * a.mbps * 4;
     if (!ensure_smem(kern, smem, g_smem_done_e4[slot])) return OASR_ERR_CUDA;
+    const int stages = (k_max + kStageKeys - 1) / kStageKeys;   // of a well-formed stream, at most
     a.q_tiles = (a.T + SP::Tp - 1) / SP::Tp;
     const long long pairs = static_cast<long long>(B) * a.H * a.q_tiles;
     const int sms = sm_count();
     a.splits = 1;
     while (a.splits < 8 && pairs * a.splits * 2 <= sms && stages >= 2 * a.splits) a.splits *= 2;
-    if (pairs * a.splits > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
+    if (pairs > 0x7fffffffLL / 2) return OASR_ERR_UNSUPPORTED;
+    a.items = static_cast<int>(pairs);
+    const long long ctas = a.splits > 1 ? pairs * a.splits : pairs < static_cast<long long>(CTAS) * sms ? pairs : static_cast<long long>(CTAS) * sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(pairs * a.splits));
-    cfg.blockDim = dim3(32 * (NW + 1));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1038,7 +1093,7 @@ oasr_status launch_e4(const void* q, E4Args& a, int k_max, int B, int seg, int s
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, tm_r, static_cast<const E4Args>(a)) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, tm_r, tm_kn, tm_vn, static_cast<const E4Args>(a)) != cudaSuccess)
         return OASR_ERR_CUDA;
     return launch_status();
 }
@@ -1082,8 +1137,6 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
         return launch_status();
     }
     E4Args a = {};
-    a.k_new = static_cast<const __nv_bfloat16*>(k_new);
-    a.v_new = static_cast<const __nv_bfloat16*>(v_new);
     a.k_pool = static_cast<uint8_t*>(k_pool);
     a.v_pool = static_cast<uint8_t*>(v_pool);
     a.kv_scale = static_cast<uint8_t*>(kv_scale);
@@ -1091,7 +1144,6 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     a.cache_seqlens = cs;
     a.pos_bias_u = static_cast<const uint16_t*>(u);
     a.pos_bias_v = static_cast<const uint16_t*>(vb);
-    a.rel = static_cast<const uint16_t*>(rel);
     a.out = static_cast<uint16_t*>(out);
     a.status = status;
     a.num_blocks = num_blocks;
@@ -1106,8 +1158,8 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     const long long pages = static_cast<long long>(mbps) * block_size, dist = static_cast<long long>(R) - T + 1;
     const long long k_max = pages < dist ? pages : dist;
     const int km = static_cast<int>(k_max < T ? T : k_max);
-    if (T <= 16) return launch_e4<1, E4NW, E4NS, E4CTAS, FUSED>(q, a, km, B, E4SEG, FUSED ? 1 : 0, stream);
-    return launch_e4<2, E4NW2, E4NS2, E4CTAS2, false>(q, a, km, B, E4SEG2, 2, stream);
+    if (T <= 16) return launch_e4<1, E4NS, E4CTAS, FUSED>(q, k_new, v_new, rel, a, km, B, FUSED ? 1 : 0, stream);
+    return launch_e4<2, E4NS2, E4CTAS2, false>(q, k_new, v_new, rel, a, km, B, 2, stream);
 }
 
 }  // namespace
