@@ -91,6 +91,10 @@ def header_symbols() -> list[str]:
     return sorted(set(re.findall(r"\b(oasr_[a-z0-9_]+)\s*\(", text)))
 
 
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _check(fn: str, status: int):
     if status != OASR_OK:
         msg = load().oasr_status_string(status).decode()
@@ -123,6 +127,8 @@ def _dev(t: torch.Tensor, name: str, dtype=None, ndim=None) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch._C._cuda_getDevice())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -291,39 +297,83 @@ def oasr_project_qkv_pos(x, w_qkv, b_qkv, pos_emb, w_pos, H, q=None, k=None, v=N
     return q, k, v, rel
 
 
-def _pools_e4m3(k_pool, v_pool, kv_scale, H, D):
-    """Device pointers and sizes of an 8-bit cache (pools [nb,H,bs,D], scales [nb,H,2,bs])."""
-    if k_pool.dim() != 4 or k_pool.shape[1] != H or k_pool.shape[3] != D:
+def _good(device, dtype, *tensors) -> bool:
+    """Whether the tensors are what `_dev` asks for: contiguous, of the dtype, on the device.  It runs
+    on every call, so it makes do with the attribute reads that tell."""
+    try:
+        for t in tensors:
+            if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+                return False
+    except AttributeError:
+        return False
+    return True
+
+
+def _refuse(**named):
+    """Raise what `_dev` finds wrong with the first bad (tensor, dtype)."""
+    for name, (t, dtype) in named.items():
+        _dev(t, name, dtype)
+    raise ValueError("tensors on another device than the current one")
+
+
+_DTYPES = {torch.float32: OASR_F32, torch.bfloat16: OASR_BF16}
+
+
+def _code(dtype) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}: bf16 or float32")
+    return code
+
+
+def _lib_device():
+    """The library and the current device (-2 without one: no tensor is on it)."""
+    try:
+        return _lib or load(), torch._C._cuda_getDevice()
+    except RuntimeError:
+        if _lib is None:
+            raise
+        return _lib, -2
+
+
+def _cache_e4m3(dev, k_pool, v_pool, kv_scale, block_table, cache_seqlens, B, H, D):
+    """Checks an 8-bit cache (pools [nb,H,bs,D], scales [nb,H,2,bs]) and its table; returns
+    num_blocks, block_size and max_blocks_per_seq."""
+    shape = k_pool.shape
+    if len(shape) != 4 or shape[1] != H or shape[3] != D:
         raise ValueError("k_pool must be [num_blocks, H, block_size, D]")
-    if v_pool.shape != k_pool.shape:
+    if v_pool.shape != shape:
         raise ValueError("v_pool must have k_pool's shape")
-    nb, bs = k_pool.shape[0], k_pool.shape[2]
-    if tuple(kv_scale.shape) != (nb, H, 2, bs):
+    nb, bs = shape[0], shape[2]
+    if kv_scale.shape != (nb, H, 2, bs):
         raise ValueError("kv_scale must be [num_blocks, H, 2, block_size]")
-    return (_dev(k_pool, "k_pool", torch.float8_e4m3fn), _dev(v_pool, "v_pool", torch.float8_e4m3fn),
-            _dev(kv_scale, "kv_scale", torch.uint8), nb, bs)
-
-
-def _table(block_table, cache_seqlens, B):
-    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(cache_seqlens.shape) != (B,):
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B or cache_seqlens.shape != (B,):
         raise ValueError("block_table must be [B, mbps] and cache_seqlens [B]")
-    return (_dev(block_table, "block_table", torch.int32), block_table.shape[1],
-            _dev(cache_seqlens, "cache_seqlens", torch.int32))
+    if not (_good(dev, torch.float8_e4m3fn, k_pool, v_pool) and _good(dev, torch.uint8, kv_scale)
+            and _good(dev, torch.int32, block_table, cache_seqlens)):
+        _refuse(k_pool=(k_pool, torch.float8_e4m3fn), v_pool=(v_pool, torch.float8_e4m3fn),
+                kv_scale=(kv_scale, torch.uint8), block_table=(block_table, torch.int32),
+                cache_seqlens=(cache_seqlens, torch.int32))
+    return nb, bs, table[1]
 
 
 def oasr_paged_append_e4m3(k_new, v_new, k_pool, v_pool, kv_scale, block_table, cache_seqlens,
                            stream=None):
     """Quantise the chunk (k_new, v_new [B,T,H,64]) into the 8-bit pools (float8_e4m3fn
     [nb,H,bs,64]) and their scales (uint8 [nb,H,2,bs]), in place."""
-    L = load()
-    dt = _dtype_code(k_new)
+    L, dev = _lib_device()
+    dt = k_new.dtype
+    code = _code(dt)
     B, T, H, D = k_new.shape
     if v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must share their shape [B, T, H, D]")
+    nb, bs, mbps = _cache_e4m3(dev, k_pool, v_pool, kv_scale, block_table, cache_seqlens, B, H, D)
+    if not _good(dev, dt, k_new, v_new):
+        _refuse(k_new=(k_new, dt), v_new=(v_new, dt))
     _check("oasr_paged_append_e4m3", L.oasr_paged_append_e4m3(
-        _dev(k_new, "k_new", k_new.dtype), _dev(v_new, "v_new", k_new.dtype),
-        *_pools_e4m3(k_pool, v_pool, kv_scale, H, D), *_table(block_table, cache_seqlens, B), B, T, H,
-        D, dt, _stream(stream)))
+        k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scale.data_ptr(), nb, bs,
+        block_table.data_ptr(), mbps, cache_seqlens.data_ptr(), B, T, H, D, code, _stream(stream)))
 
 
 def oasr_paged_read_e4m3(k_pool, v_pool, kv_scale, block_table, cache_seqlens, length, start=None,
@@ -331,48 +381,65 @@ def oasr_paged_read_e4m3(k_pool, v_pool, kv_scale, block_table, cache_seqlens, l
     """Values of each stream's positions start[b] .. start[b] + length - 1 (start None: from 0) as
     dense [B,length,H,64] tensors (k, v) of ``dtype`` (or of the k and v given); zeros past the
     cached length."""
-    L = load()
-    B, H, D, n = block_table.shape[0], k_pool.shape[1], k_pool.shape[3], int(length)
+    L, dev = _lib_device()
+    B, n = block_table.shape[0], int(length)
+    _, H, _, D = k_pool.shape
     if n < 1:
         raise ValueError("length must be at least 1")
-    k = torch.empty((B, n, H, D), dtype=dtype, device=k_pool.device) if k is None else k
-    v = torch.empty((B, n, H, D), dtype=k.dtype, device=k_pool.device) if v is None else v
-    if tuple(k.shape) != (B, n, H, D) or tuple(v.shape) != (B, n, H, D):
-        raise ValueError("k and v must be [B, length, H, D]")
-    if start is not None and tuple(start.shape) != (B,):
+    if start is not None and start.shape != (B,):
         raise ValueError("start must be [B]")
+    nb, bs, mbps = _cache_e4m3(dev, k_pool, v_pool, kv_scale, block_table, cache_seqlens, B, H, D)
+    shape = (B, n, H, D)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=k_pool.device)
+    if v is None:
+        v = torch.empty_like(k)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("k and v must be [B, length, H, D]")
+    dt = k.dtype
+    code = _code(dt)
+    if not _good(dev, dt, k, v) or (start is not None and not _good(dev, torch.int32, start)):
+        _refuse(k=(k, dt), v=(v, dt), **({} if start is None else {"start": (start, torch.int32)}))
     _check("oasr_paged_read_e4m3", L.oasr_paged_read_e4m3(
-        *_pools_e4m3(k_pool, v_pool, kv_scale, H, D), *_table(block_table, cache_seqlens, B),
-        None if start is None else _dev(start, "start", torch.int32), _dev(k, "k", k.dtype),
-        _dev(v, "v", k.dtype), B, n, H, D, _dtype_code(k), _stream(stream)))
+        k_pool.data_ptr(), v_pool.data_ptr(), kv_scale.data_ptr(), nb, bs, block_table.data_ptr(), mbps,
+        cache_seqlens.data_ptr(), None if start is None else start.data_ptr(), k.data_ptr(), v.data_ptr(), B, n,
+        H, D, code, _stream(stream)))
     return k, v
 
 
-def _chunk_e4m3(q, pos_bias_u, pos_bias_v, rel, out):
-    B, T, H, D = q.shape
-    if tuple(pos_bias_u.shape) != (H, D) or tuple(pos_bias_v.shape) != (H, D):
+def _attention_e4m3(dev, q, pos_bias_u, pos_bias_v, rel, out, k_new=None, v_new=None):
+    """Checks the attention's own tensors; returns the output, the sizes and the dtype's code."""
+    shape = q.shape
+    B, T, H, D = shape
+    dt = q.dtype
+    code = _code(dt)
+    if pos_bias_u.shape != (H, D) or pos_bias_v.shape != (H, D):
         raise ValueError("pos biases must be [H, D]")
-    if rel.dim() != 3 or tuple(rel.shape[1:]) != (H, D):
+    r = rel.shape
+    if len(r) != 3 or r[1] != H or r[2] != D:
         raise ValueError("rel must be [R, H, D]")
     if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = torch.empty(shape, dtype=dt, device=q.device)
+    elif out.shape != shape or out.dtype != dt:
         raise ValueError("out must be [B, T, H, D] of q's dtype")
-    return B, T, H, D, out
+    if k_new is not None and (k_new.shape != shape or v_new.shape != shape):
+        raise ValueError("k_new, v_new must be [B, T, H, D]")
+    if not _good(dev, dt, q, pos_bias_u, pos_bias_v, rel, out, *(() if k_new is None else (k_new, v_new))):
+        _refuse(q=(q, dt), pos_bias_u=(pos_bias_u, dt), pos_bias_v=(pos_bias_v, dt), rel=(rel, dt), out=(out, dt),
+                **({} if k_new is None else {"k_new": (k_new, dt), "v_new": (v_new, dt)}))
+    return out, B, T, H, D, r[0], code
 
 
 def oasr_chunk_relattn_paged_e4m3(q, k_pool, v_pool, kv_scale, block_table, cache_seqlens,
                                   pos_bias_u, pos_bias_v, rel, out=None, scale=None, stream=None):
     """Streaming chunk attention over the 8-bit paged cache; returns out [B,T,H,64]."""
-    L = load()
-    dt = _dtype_code(q)
-    B, T, H, D, out = _chunk_e4m3(q, pos_bias_u, pos_bias_v, rel, out)
-    scale = D ** -0.5 if scale is None else float(scale)
+    L, dev = _lib_device()
+    out, B, T, H, D, R, code = _attention_e4m3(dev, q, pos_bias_u, pos_bias_v, rel, out)
+    nb, bs, mbps = _cache_e4m3(dev, k_pool, v_pool, kv_scale, block_table, cache_seqlens, B, H, D)
     _check("oasr_chunk_relattn_paged_e4m3", L.oasr_chunk_relattn_paged_e4m3(
-        _dev(q, "q", q.dtype), *_pools_e4m3(k_pool, v_pool, kv_scale, H, D),
-        *_table(block_table, cache_seqlens, B), _dev(pos_bias_u, "pos_bias_u", q.dtype),
-        _dev(pos_bias_v, "pos_bias_v", q.dtype), _dev(rel, "rel", q.dtype), rel.shape[0],
-        _dev(out, "out", q.dtype), B, T, H, D, scale, dt, _stream(stream)))
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scale.data_ptr(), nb, bs, block_table.data_ptr(),
+        mbps, cache_seqlens.data_ptr(), pos_bias_u.data_ptr(), pos_bias_v.data_ptr(), rel.data_ptr(), R,
+        out.data_ptr(), B, T, H, D, D ** -0.5 if scale is None else scale, code, _stream(stream)))
     return out
 
 
@@ -381,33 +448,34 @@ def oasr_chunk_step_paged_e4m3(q, k_new, v_new, k_pool, v_pool, kv_scale, block_
                                stream=None):
     """Fused append + streaming chunk attention over the 8-bit paged cache; returns out
     [B,T,H,64]."""
-    L = load()
-    dt = _dtype_code(q)
-    B, T, H, D, out = _chunk_e4m3(q, pos_bias_u, pos_bias_v, rel, out)
-    if k_new.shape != q.shape or v_new.shape != q.shape:
-        raise ValueError("k_new, v_new must be [B, T, H, D]")
-    scale = D ** -0.5 if scale is None else float(scale)
+    L, dev = _lib_device()
+    out, B, T, H, D, R, code = _attention_e4m3(dev, q, pos_bias_u, pos_bias_v, rel, out, k_new, v_new)
+    nb, bs, mbps = _cache_e4m3(dev, k_pool, v_pool, kv_scale, block_table, cache_seqlens, B, H, D)
     _check("oasr_chunk_step_paged_e4m3", L.oasr_chunk_step_paged_e4m3(
-        _dev(q, "q", q.dtype), _dev(k_new, "k_new", q.dtype), _dev(v_new, "v_new", q.dtype),
-        *_pools_e4m3(k_pool, v_pool, kv_scale, H, D), *_table(block_table, cache_seqlens, B),
-        _dev(pos_bias_u, "pos_bias_u", q.dtype), _dev(pos_bias_v, "pos_bias_v", q.dtype),
-        _dev(rel, "rel", q.dtype), rel.shape[0], _dev(out, "out", q.dtype), B, T, H, D, scale, dt,
-        _stream(stream)))
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), kv_scale.data_ptr(),
+        nb, bs, block_table.data_ptr(), mbps, cache_seqlens.data_ptr(), pos_bias_u.data_ptr(),
+        pos_bias_v.data_ptr(), rel.data_ptr(), R, out.data_ptr(), B, T, H, D,
+        D ** -0.5 if scale is None else scale, code, _stream(stream)))
     return out
 
 
 def oasr_quantize_rows(x, x8=None, scale=None, stream=None):
     """Rows of x [M,K] as 8-bit integers with a scale each; returns (x8 int8 [M,K], scale
     float32 [M])."""
-    L = load()
+    L, dev = _lib_device()
+    dt = x.dtype
+    code = _code(dt)
     M, K = x.shape
-    x8 = torch.empty((M, K), dtype=torch.int8, device=x.device) if x8 is None else x8
-    scale = torch.empty((M,), dtype=torch.float32, device=x.device) if scale is None else scale
-    if tuple(x8.shape) != (M, K) or tuple(scale.shape) != (M,):
+    if x8 is None:
+        x8 = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+    if x8.shape != (M, K) or scale.shape != (M,):
         raise ValueError("x8 must be [M, K] and scale [M]")
+    if not (_good(dev, dt, x) and _good(dev, torch.int8, x8) and _good(dev, torch.float32, scale)):
+        _refuse(x=(x, dt), x8=(x8, torch.int8), scale=(scale, torch.float32))
     _check("oasr_quantize_rows", L.oasr_quantize_rows(
-        _dev(x, "x", x.dtype), _dev(x8, "x8", torch.int8), _dev(scale, "scale", torch.float32), M, K,
-        _dtype_code(x), _stream(stream)))
+        x.data_ptr(), x8.data_ptr(), scale.data_ptr(), M, K, code, _stream(stream)))
     return x8, scale
 
 
@@ -415,19 +483,24 @@ def oasr_linear_w8a8(x8, x_scale, w8, w_scale, bias=None, out=None, out_dtype=to
                      stream=None):
     """(x8 . w8^T) * x_scale[:, None] * w_scale + bias from int8 x8 [M,K], w8 [N,K]; returns out
     [M,N] of ``out_dtype`` (or of the out given)."""
-    L = load()
+    L, dev = _lib_device()
     M, K = x8.shape
-    N = w8.shape[0]
-    if w8.dim() != 2 or w8.shape[1] != K or tuple(x_scale.shape) != (M,) or tuple(w_scale.shape) != (N,):
+    N, Kw = w8.shape
+    if Kw != K or x_scale.shape != (M,) or w_scale.shape != (N,):
         raise ValueError("shapes: x8 [M,K], x_scale [M], w8 [N,K], w_scale [N]")
-    out = torch.empty((M, N), dtype=out_dtype, device=x8.device) if out is None else out
-    if tuple(out.shape) != (M, N) or (bias is not None and tuple(bias.shape) != (N,)):
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x8.device)
+    if out.shape != (M, N) or (bias is not None and bias.shape != (N,)):
         raise ValueError("out must be [M, N] and bias [N]")
+    dt = out.dtype
+    code = _code(dt)
+    if not (_good(dev, torch.int8, x8, w8) and _good(dev, torch.float32, x_scale, w_scale) and _good(dev, dt, out)
+            and (bias is None or _good(dev, dt, bias))):
+        _refuse(x8=(x8, torch.int8), x_scale=(x_scale, torch.float32), w8=(w8, torch.int8),
+                w_scale=(w_scale, torch.float32), out=(out, dt), **({} if bias is None else {"bias": (bias, dt)}))
     _check("oasr_linear_w8a8", L.oasr_linear_w8a8(
-        _dev(x8, "x8", torch.int8), _dev(x_scale, "x_scale", torch.float32),
-        _dev(w8, "w8", torch.int8), _dev(w_scale, "w_scale", torch.float32),
-        None if bias is None else _dev(bias, "bias", out.dtype), _dev(out, "out", out.dtype), M, N,
-        K, _dtype_code(out), _stream(stream)))
+        x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(),
+        None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K, code, _stream(stream)))
     return out
 
 
@@ -435,29 +508,35 @@ def oasr_project_qkv_pos_w8a8(x8, x_scale, w_qkv8, w_qkv_scale, b_qkv, pos8, pos
                               w_pos_scale, H, q=None, k=None, v=None, rel=None, stream=None):
     """q, k, v [M,H,64] and rel [R,H,64] by 8-bit integer products, one launch; the outputs have
     b_qkv's dtype.  Returns (q, k, v, rel)."""
-    L = load()
+    L, dev = _lib_device()
     M, d = x8.shape
     R = pos8.shape[0]
-    if tuple(w_qkv8.shape) != (3 * d, d) or tuple(w_qkv_scale.shape) != (3 * d,) or \
-            tuple(b_qkv.shape) != (3 * d,) or tuple(pos8.shape) != (R, d) or \
-            tuple(w_pos8.shape) != (d, d) or tuple(w_pos_scale.shape) != (d,) or \
-            tuple(x_scale.shape) != (M,) or tuple(pos_scale.shape) != (R,) or d % H:
+    if w_qkv8.shape != (3 * d, d) or w_qkv_scale.shape != (3 * d,) or b_qkv.shape != (3 * d,) or \
+            pos8.shape != (R, d) or w_pos8.shape != (d, d) or w_pos_scale.shape != (d,) or \
+            x_scale.shape != (M,) or pos_scale.shape != (R,) or d % H:
         raise ValueError("shapes: x8 [M,d], x_scale [M], w_qkv8 [3d,d], w_qkv_scale and b_qkv [3d], "
                          "pos8 [R,d], pos_scale [R], w_pos8 [d,d], w_pos_scale [d]")
-    D, dt, dv = d // H, b_qkv.dtype, x8.device
-    q = torch.empty((M, H, D), dtype=dt, device=dv) if q is None else q
-    k = torch.empty((M, H, D), dtype=dt, device=dv) if k is None else k
-    v = torch.empty((M, H, D), dtype=dt, device=dv) if v is None else v
-    rel = torch.empty((R, H, D), dtype=dt, device=dv) if rel is None else rel
-    if any(tuple(t.shape) != (M, H, D) for t in (q, k, v)) or tuple(rel.shape) != (R, H, D):
+    D, dt = d // H, b_qkv.dtype
+    code = _code(dt)
+    rows = (M, H, D)
+    if q is None and k is None and v is None:
+        q, k, v = torch.empty((3, M, H, D), dtype=dt, device=x8.device).unbind(0)
+    else:
+        q, k, v = (torch.empty(rows, dtype=dt, device=x8.device) if t is None else t for t in (q, k, v))
+    if rel is None:
+        rel = torch.empty((R, H, D), dtype=dt, device=x8.device)
+    if q.shape != rows or k.shape != rows or v.shape != rows or rel.shape != (R, H, D):
         raise ValueError("q, k, v must be [M, H, d/H] and rel [R, H, d/H]")
+    i8, f32 = torch.int8, torch.float32
+    if not (_good(dev, i8, x8, w_qkv8, pos8, w_pos8) and _good(dev, dt, b_qkv, q, k, v, rel)
+            and _good(dev, f32, x_scale, w_qkv_scale, pos_scale, w_pos_scale)):
+        _refuse(x8=(x8, i8), x_scale=(x_scale, f32), w_qkv8=(w_qkv8, i8), w_qkv_scale=(w_qkv_scale, f32),
+                b_qkv=(b_qkv, dt), pos8=(pos8, i8), pos_scale=(pos_scale, f32), w_pos8=(w_pos8, i8),
+                w_pos_scale=(w_pos_scale, f32), q=(q, dt), k=(k, dt), v=(v, dt), rel=(rel, dt))
     _check("oasr_project_qkv_pos_w8a8", L.oasr_project_qkv_pos_w8a8(
-        _dev(x8, "x8", torch.int8), _dev(x_scale, "x_scale", torch.float32),
-        _dev(w_qkv8, "w_qkv8", torch.int8), _dev(w_qkv_scale, "w_qkv_scale", torch.float32),
-        _dev(b_qkv, "b_qkv", dt), _dev(pos8, "pos8", torch.int8),
-        _dev(pos_scale, "pos_scale", torch.float32), _dev(w_pos8, "w_pos8", torch.int8),
-        _dev(w_pos_scale, "w_pos_scale", torch.float32), _dev(q, "q", dt), _dev(k, "k", dt),
-        _dev(v, "v", dt), _dev(rel, "rel", dt), M, R, d, H, _dtype_code(b_qkv), _stream(stream)))
+        x8.data_ptr(), x_scale.data_ptr(), w_qkv8.data_ptr(), w_qkv_scale.data_ptr(), b_qkv.data_ptr(),
+        pos8.data_ptr(), pos_scale.data_ptr(), w_pos8.data_ptr(), w_pos_scale.data_ptr(), q.data_ptr(), k.data_ptr(),
+        v.data_ptr(), rel.data_ptr(), M, R, d, H, code, _stream(stream)))
     return q, k, v, rel
 
 
