@@ -165,6 +165,8 @@ struct E4Slice {
 // k_s, v_s: shared addresses of the slice's first rows; sc: its first K scale, v_off bytes before its first
 // V scale; far_off: bytes from the scales of keys 0 .. 7 to those of keys 8 .. 15 (pages of eight keys
 // hold 16 scales each).
+// K comes last: once a product has taken K's registers, all of the slice has been read (the loads complete
+// in order), and only then may the slot be released; an arrival right behind the loads can overtake them.
 // The lane's part of the addresses is computed once (E4Lane); the other rows and chunks it reads differ from
 // it in single bits of the swizzled offset.
 struct E4Lane {
@@ -183,16 +185,16 @@ __device__ __forceinline__ E4Lane e4_lane(int lane, int far_off)
 
 __device__ __forceinline__ void load_slice(E4Slice& x, const E4Lane& l, uint32_t k_s, uint32_t v_s, uint32_t sc, uint32_t v_off)
 {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.ks) : "r"(sc + l.sc));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.vs) : "r"(sc + l.sc + v_off));
+#pragma unroll
+    for (int dp = 0; dp < 2; ++dp)   // two chunks on
+        ldsm8_x2_t((v_s + l.v) ^ (32u * dp), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
 #pragma unroll
     for (int n = 0; n < 2; ++n)   // two keys on: the next line, its swizzle's lowest bit flipped
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x.k[n].x), "=r"(x.k[n].y), "=r"(x.k[n].z), "=r"(x.k[n].w)
                      : "r"((k_s + l.k) ^ (144u * n)));
-#pragma unroll
-    for (int dp = 0; dp < 2; ++dp)   // two chunks on
-        ldsm8_x2_t((v_s + l.v) ^ (32u * dp), x.v[4 * dp], x.v[4 * dp + 1], x.v[4 * dp + 2], x.v[4 * dp + 3]);
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.ks) : "r"(sc + l.sc));
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.vs) : "r"(sc + l.sc + v_off));
 }
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
@@ -268,7 +270,6 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, con
         bl[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4));
         bh[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4 + 1));
     }
-    mbar_arrive_release(release_bar);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
         uint32_t qa[4][4];
@@ -284,6 +285,7 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, con
         mma_bf16_16816(c[1], qa[2], bh[1].x, bh[1].y);
         mma_bf16_16816(c[0], qa[3], bh[0].z, bh[0].w);
         mma_bf16_16816(c[1], qa[3], bh[1].z, bh[1].w);
+        if (mt == 0) mbar_arrive_release(release_bar);   // the rel rows are in registers
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int x = col0 + 8 * (warp + kConsumerWarps * u) + 2 * t4 + 16 * mt + g4 + 1;
@@ -306,7 +308,8 @@ struct E4Acc {
 
 // One warp, 16 MT query rows against one slice.  x0: the position table's column of the slice's first key
 // (aligned: a multiple of 16, so that a lane's four keys are eight bytes of one row); keys [0, kvalid) of
-// the slice exist; sc: scale * log2(e) * 2^x of rows g4 and g4 + 8 of each m-tile.
+// the slice exist; sc: scale * log2(e) * 2^x of rows g4 and g4 + 8 of each m-tile.  Every lane arrives on
+// release_bar (unless 0) when the slice has been read.
 //
 // P is 2^(t - m), at most one, and goes into the product as fp16: its rounding is 2^-11 of each
 // weight and never more than 2^-25 of the row's largest contribution, whatever the scales.  The
@@ -315,7 +318,7 @@ struct E4Acc {
 template <int MT>
 __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_tile, E4Slice& x,
                                            const uint16_t* gs, int x0, bool aligned, int kvalid,
-                                           const float (&sc)[MT][2], int& E, int lane)
+                                           const float (&sc)[MT][2], int& E, int lane, uint32_t release_bar)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
     float s[MT][2][4];
@@ -341,6 +344,7 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
             }
         }
     }
+    if (release_bar) mbar_arrive_release(release_bar);
     const bool tail = kvalid < 16;
     if (tail) {   // rows past the last key may hold anything: V bytes and scales (their scores are replaced below)
         const int have = max(0, min(4, kvalid - 4 * t4));
@@ -807,8 +811,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             if (kv > 0)
                 load_slice(x, ll, sb + slot * kE4Stage + jl * kE4Row, sb + slot * kE4Stage + (kStageKeys + jl) * kE4Row,
                            sb + sc_off + slot * 2 * kStageKeys, box);
-            mbar_arrive_release(bar_empty + 8 * slot);
-            if (kv > 0) slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, s * kStageKeys + jl + Tp, true, kv, sc, E, lane);
+            if (kv > 0)
+                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, s * kStageKeys + jl + Tp, true, kv, sc, E, lane, bar_empty + 8 * slot);
+            else
+                mbar_arrive_release(bar_empty + 8 * slot);
         }
         if (FUSED && t.nc > 0) {
             if (n == 0) named_bar_sync(1, kE4Consumers);
@@ -816,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 E4Slice x;
                 load_slice(x, e4_lane(lane, 8), sb + SP::off_ck, sb + SP::off_ck + kChunkRows * kE4Row, sb + SP::off_csc, kChunkRows);
                 const int x0 = t.C - t.st0 * kStageKeys + Tp;
-                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, x0, (x0 & 15) == 0, t.nc, sc, E, lane);
+                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, x0, (x0 & 15) == 0, t.nc, sc, E, lane, 0u);
             }
         }
 

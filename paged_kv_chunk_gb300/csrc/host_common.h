@@ -32,6 +32,10 @@ bool encode_head_pairs_bf16(CUtensorMap* map, const void* base, long long rows, 
 // false if the driver rejects it.
 bool encode_rows_e4m3(CUtensorMap* map, const void* base, long long rows, int box_rows);
 
+// Encode a 2-D map over rows of row_bytes bytes (a multiple of 16) with a box of 64 bytes of box_rows rows,
+// not swizzled.  Returns false if the driver rejects it.
+bool encode_bytes(CUtensorMap* map, const void* base, long long rows, int row_bytes, int box_rows);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline oasr_status launch_status()

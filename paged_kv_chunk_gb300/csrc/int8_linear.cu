@@ -123,25 +123,46 @@ __device__ __forceinline__ uint4 i8_to_f16(uint32_t w0, uint32_t w1)
                       i8_sub(__byte_perm(w1, 0x64646464u, 0x4140)), i8_sub(__byte_perm(w1, 0x64646464u, 0x4342)));
 }
 
-constexpr int kI8Threads = 13 * 32;   // four epilogue warps, the issuer, eight converter warps
-constexpr int kI8Conv = 256;
+// Warps: eight for the epilogue, two groups of eight converters, the issuer, the TMA producer.  The producer
+// brings 8-bit tiles of 64 K into a ring; the converter groups take its slots in turn (one group's proxy
+// fence and waits pass while the other converts) and write the fp16 ring that the products read; two
+// accumulators let a tile's epilogue overlap the next tile's products.
+constexpr int kI8EpiWarps = 8, kI8Group = 256, kI8Groups = 2;
+constexpr int kI8Conv0 = 32 * kI8EpiWarps;                        // first converter thread
+constexpr int kI8Issuer = kI8EpiWarps + kI8Groups * kI8Group / 32;   // its warp; the producer's is the next
+constexpr int kI8Threads = 32 * (kI8Issuer + 2);
+constexpr int kI8OutStride = 20;   // floats of a row of an epilogue warp's staging tile (32 x 16)
 
 template <int BN>
 struct I8Smem {
-    static constexpr int tile_a = 128 * 128, tile = tile_a + BN * 128;   // fp16, 64 of K
-    static constexpr int stages = BN == 128 ? 6 : 8;
-    static constexpr int off_ws = stages * tile;             // [4 warps][2 * BN] floats
-    static constexpr int off_bar = off_ws + 4 * 2 * BN * 4;  // full, empty, acc full[2], acc free[2], drain
-    static constexpr int off_misc = off_bar + (2 * stages + 5) * 8;
+    static constexpr int rows = 128 + BN;                              // x rows, then w rows
+    static constexpr int tile_a = 128 * 128, tile = rows * 128;        // fp16, 64 of K
+    static constexpr int raw = rows * 64;                              // 8-bit, 64 of K
+    static constexpr int stages = BN == 256 ? 3 : 4, raws = BN == 256 ? 2 : 4;
+    static constexpr int off_raw = stages * tile;
+    static constexpr int off_out = off_raw + raws * raw;               // [8 warps][32][kI8OutStride] floats
+    static constexpr int off_ws = off_out + kI8EpiWarps * 32 * kI8OutStride * 4;   // [8 warps][2][BN / 2] floats
+    static constexpr int off_bar = off_ws + kI8EpiWarps * BN * 4;      // full, empty, raw full, raw empty, acc full[2], acc free[2], drain
+    static constexpr int off_misc = off_bar + (2 * stages + 2 * raws + 5) * 8;
     static constexpr int bytes = off_misc + 16 + 1024;
     static constexpr int cols = 2 * BN < 32 ? 32 : 2 * BN;
 };
 
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
 template <int BN, typename Elem>
-__global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(const I8Args a)
+__global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
+    const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_w0,
+    const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_w1, const I8Args a)
 {
     using SP = I8Smem<BN>;
-    constexpr int S = SP::stages;
+    constexpr int S = SP::stages, R = SP::raws;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_addr(sm);
@@ -149,21 +170,32 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(const I8Args a
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SP::off_misc);
     volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SP::off_misc + 4);
     const uint32_t bar_full = sb + SP::off_bar, bar_empty = bar_full + 8 * S;
-    const uint32_t bar_acc_full = bar_empty + 8 * S, bar_acc_free = bar_acc_full + 16;
+    const uint32_t bar_raw = bar_empty + 8 * S, bar_raw_free = bar_raw + 8 * R;
+    const uint32_t bar_acc_full = bar_raw_free + 8 * R, bar_acc_free = bar_acc_full + 16;
     const uint32_t bar_drain = bar_acc_free + 16;
     const int ksteps = (a.K + 63) / 64;
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(bar_full + 8 * i, kI8Conv);
+            mbar_init(bar_full + 8 * i, kI8Group);
             mbar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < R; ++i) {
+            mbar_init(bar_raw + 8 * i, 1);
+            mbar_init(bar_raw_free + 8 * i, kI8Group);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_acc_full + 8 * i, 1);
-            mbar_init(bar_acc_free + 8 * i, 4);
+            mbar_init(bar_acc_free + 8 * i, kI8EpiWarps);
         }
         mbar_init(bar_drain, 1);
         fence_mbar_init();
         *s_abort = 0;
+    }
+    if (warp == kI8Issuer + 1 && lane == 0) {
+        prefetch_tensormap(&tm_x0);
+        prefetch_tensormap(&tm_w0);
+        prefetch_tensormap(&tm_x1);
+        prefetch_tensormap(&tm_w1);
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)),
@@ -184,69 +216,34 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(const I8Args a
         nt = t - mt * n;
     };
     const int my_tiles = static_cast<int>(blockIdx.x) < a.tiles ? (a.tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    const int iters = my_tiles * ksteps;
 
-    if (warp >= 5) {
-        // ------------------------------------------------------------ converters
-        // thread: 16 bytes (chunk c) of rows r0, r0 + 64, ... of the tile's x rows, then its w rows
-        constexpr int NU = (128 + BN + 63) / 64;
-        const int ct = tid - 160, c = ct & 3, r0 = ct >> 2;
-        const int iters = my_tiles * ksteps;
-        int lt = -1, lk = ksteps;           // the next step to load: tile, K step
-        const int8_t* src[NU];
-        auto load = [&](uint4 (&buf)[NU]) {
-            if (++lk >= ksteps) {
-                lk = 0;
-                ++lt;
+    if (warp == kI8Issuer + 1) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int i = 0;
+            bool ok = true;
+            for (int lt = 0; lt < my_tiles && ok; ++lt) {
                 int g, mt, nt;
                 decode(blockIdx.x + lt * gridDim.x, g, mt, nt);
-                const I8Problem& p = a.p[g];
-#pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                    const int r = r0 + 64 * u;
-                    src[u] = nullptr;
-                    if (r < 128) {
-                        if (mt * 128 + r < p.M) src[u] = p.x + static_cast<long long>(mt * 128 + r) * a.K + 16 * c;
-                    } else if (r < 128 + BN) {
-                        const int n = nt * BN + r - 128;
-                        if (n < p.N) src[u] = p.w + static_cast<long long>(n) * a.K + 16 * c;
+                for (int kb = 0; kb < ksteps; ++kb, ++i) {
+                    const int slot = i % R;
+                    if (i >= R && !wait_or_abort(bar_raw_free + 8 * slot, ((i / R) - 1) & 1, s_abort)) {
+                        ok = false;
+                        break;
                     }
+                    // rows past M or N and bytes past K come as zeros
+                    const uint32_t dst = sb + SP::off_raw + slot * SP::raw, bar = bar_raw + 8 * slot;
+                    mbar_arrive_expect_tx(bar, SP::raw);
+                    tma_load_2d(dst, g ? &tm_x1 : &tm_x0, bar, 64 * kb, mt * 128);
+                    tma_load_2d(dst + 128 * 64, g ? &tm_w1 : &tm_w0, bar, 64 * kb, nt * BN);
                 }
             }
-            const bool in = 64 * lk + 16 * c < a.K;
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                buf[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (in && src[u]) buf[u] = __ldg(reinterpret_cast<const uint4*>(src[u] + 64 * lk));
-            }
-        };
-        auto convert = [&](int i, const uint4 (&buf)[NU]) {
-            const int slot = i % S;
-            if (i >= S && !wait_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort)) return false;
-            uint8_t* base = sm + slot * SP::tile;
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const int r = r0 + 64 * u;      // w rows follow the x rows: 128 bytes each
-                if (r < 128 + BN) {
-                    *reinterpret_cast<uint4*>(base + swz128(r, 2 * c)) = i8_to_f16(buf[u].x, buf[u].y);
-                    *reinterpret_cast<uint4*>(base + swz128(r, 2 * c + 1)) = i8_to_f16(buf[u].z, buf[u].w);
-                }
-            }
-            fence_proxy_async_smem();
-            mbar_arrive_release(bar_full + 8 * slot);
-            return true;
-        };
-        uint4 b0[NU], b1[NU];
-        if (iters > 0) load(b0);
-        if (iters > 1) load(b1);
-        for (int i = 0; i < iters; i += 2) {
-            if (!convert(i, b0)) break;
-            if (i + 2 < iters) load(b0);
-            if (i + 1 < iters) {
-                if (!convert(i + 1, b1)) break;
-                if (i + 3 < iters) load(b1);
-            }
+            // no copy may still be landing when the CTA exits
+            for (int u = i - R; u < i; ++u)
+                if (u >= 0 && !mbar_wait(bar_raw + 8 * (u % R), (u / R) & 1)) *s_abort = 1;
         }
-    } else if (warp == 4) {
+    } else if (warp == kI8Issuer) {
         // ------------------------------------------------------------- MMA issuer
         if (lane == 0) {
             // fp16 A and B, fp32 D
@@ -284,62 +281,111 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(const I8Args a
                 if (u >= 0) drained = mbar_wait(bar_empty + 8 * (u % S), (u / S) & 1) && drained;
             if (!drained) *s_abort = 1;
         }
+    } else if (warp >= kI8EpiWarps) {
+        // ------------------------------------------------------------ converters
+        // thread: 16 bytes (chunk c) of rows r0, r0 + 64, ...
+        constexpr int NU = (SP::rows + 63) / 64;
+        const int grp = (tid - kI8Conv0) / kI8Group, ct = (tid - kI8Conv0) % kI8Group, c = ct & 3, r0 = ct >> 2;
+        for (int i = grp; i < iters; i += kI8Groups) {
+            const int rs = i % R, slot = i % S;
+            if (!wait_or_abort(bar_raw + 8 * rs, (i / R) & 1, s_abort)) break;
+            const uint8_t* src = sm + SP::off_raw + rs * SP::raw + 16 * ct;
+            uint4 buf[NU];
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                if (r0 + 64 * u < SP::rows) buf[u] = *reinterpret_cast<const uint4*>(src + 4096 * u);
+            if (i >= S && !wait_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort)) break;
+            uint8_t* lo = sm + slot * SP::tile + swz128(r0, 2 * c);
+            uint8_t* hi = sm + slot * SP::tile + swz128(r0, 2 * c + 1);
+#pragma unroll
+            for (int u = 0; u < NU; ++u)   // 64 rows on, the same swizzle
+                if (r0 + 64 * u < SP::rows) {
+                    *reinterpret_cast<uint4*>(lo + 8192 * u) = i8_to_f16(buf[u].x, buf[u].y);
+                    *reinterpret_cast<uint4*>(hi + 8192 * u) = i8_to_f16(buf[u].z, buf[u].w);
+                }
+            fence_proxy_async_smem();
+            mbar_arrive_release(bar_full + 8 * slot);
+            // the raw slot is released only here, its words converted: an arrival right behind the loads can
+            // overtake them (they wait in another unit's queue), and a copy then lands under them
+            mbar_arrive_release(bar_raw_free + 8 * rs);
+        }
     } else {
         // --------------------------------------------------------------- epilogue
-        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * warp) << 16);
-        float* s_ws = reinterpret_cast<float*>(sm + SP::off_ws) + warp * 2 * BN;   // w scales, then biases
+        // warp: 32 rows (its TMEM lanes, warp % 4) of one half of the tile's columns (warp / 4)
+        constexpr int HN = BN / 2;
+        const int rq = warp & 3, half = warp >> 2;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * rq) << 16) + half * HN;
+        float* s_ws = reinterpret_cast<float*>(sm + SP::off_ws) + warp * BN;   // w scales, then biases
+        float* s_out = reinterpret_cast<float*>(sm + SP::off_out) + warp * 32 * kI8OutStride;
         for (int lt = 0; lt < my_tiles; ++lt) {
             int g, mt, nt;
             decode(blockIdx.x + lt * gridDim.x, g, mt, nt);
             const I8Problem& p = a.p[g];
             const int buf = lt & 1;
             const Elem* bias = static_cast<const Elem*>(p.bias);
+            const int row0 = mt * 128 + 32 * rq, col0 = nt * BN + half * HN;
             __syncwarp();
-            for (int j = lane; j < BN; j += 32) {
-                const int n = nt * BN + j;
+            for (int j = lane; j < HN; j += 32) {
+                const int n = col0 + j;
                 s_ws[j] = n < p.N ? __ldg(p.ws + n) : 0.f;
-                s_ws[BN + j] = bias && n < p.N ? bias_at(bias, n) : 0.f;
+                s_ws[HN + j] = bias && n < p.N ? bias_at(bias, n) : 0.f;
             }
-            const int row = mt * 128 + 32 * warp + lane;
-            const float xs = row < p.M ? __ldg(p.xs + row) : 0.f;
+            const float xs = row0 + lane < p.M ? __ldg(p.xs + row0 + lane) : 0.f;
             __syncwarp();
             if (!__all_sync(0xffffffffu, wait_or_abort(bar_acc_full + 8 * buf, (lt >> 1) & 1, s_abort))) break;
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-                uint32_t r[32];
-                OASR_TMEM_LD32(tl + buf * BN + 32 * c, r);
+#pragma unroll 1
+            for (int c = 0; c < HN / 16; ++c) {
+                const int col = col0 + 16 * c;
+                if (col >= p.N) break;
+                uint32_t r[16];
+                OASR_TMEM_LD16(tl + buf * BN + 16 * c, r);
                 tmem_wait_ld();
-                const int col = nt * BN + 32 * c;
-                if (row < p.M && col < p.N) {
-                    // a block of 32 columns lies within one output (widths are multiples of 64,
-                    // or there is one output)
-                    const int which = g ? 3 : col / a.width;
-                    const int width = g ? p.N : a.width;
-                    void* ob = which == 0 ? a.out[0] : which == 1 ? a.out[1] : which == 2 ? a.out[2] : a.out[3];
-                    Elem* dst = static_cast<Elem*>(ob) + static_cast<long long>(row) * width + (col - (g ? 0 : which * a.width));
-                    float v[32];
+                // thread = row: scaled, into the staging tile
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j]), xs), s_ws[32 * c + j]), s_ws[BN + 32 * c + j]);
-                    if (col + 32 <= p.N && (width & 7) == 0) {
-                        if constexpr (sizeof(Elem) == 2) {
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 w4 = *reinterpret_cast<const float4*>(s_ws + 16 * c + j);
+                    const float4 b4 = *reinterpret_cast<const float4*>(s_ws + HN + 16 * c + j);
+                    float4 v;
+                    v.x = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j]), xs), w4.x), b4.x);
+                    v.y = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j + 1]), xs), w4.y), b4.y);
+                    v.z = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j + 2]), xs), w4.z), b4.z);
+                    v.w = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j + 3]), xs), w4.w), b4.w);
+                    *reinterpret_cast<float4*>(s_out + lane * kI8OutStride + j) = v;
+                }
+                __syncwarp();
+                // rows from there in whole 64- or 32-byte runs.  A block of 16 columns lies within one
+                // output (widths are multiples of 64, or there is one output).
+                const int which = g ? 3 : col / a.width;
+                const int width = g ? p.N : a.width;
+                void* ob = which == 0 ? a.out[0] : which == 1 ? a.out[1] : which == 2 ? a.out[2] : a.out[3];
+                Elem* dst = static_cast<Elem*>(ob) + (col - (g ? 0 : which * a.width));
+                if (col + 16 <= p.N && (width & 7) == 0) {
+                    constexpr int V = 16 / sizeof(Elem), L = 16 / V;   // values of a store, lanes of a row
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8)
-                                *reinterpret_cast<uint4*>(dst + j) =
-                                    make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-                                               pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4)
-                                *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    for (int i = 0; i < 32; i += 32 / L) {
+                        const int rr = i + lane / L, j = (lane % L) * V;
+                        if (row0 + rr < p.M) {
+                            const float* v = s_out + rr * kI8OutStride + j;
+                            Elem* to = dst + static_cast<long long>(row0 + rr) * width + j;
+                            const float4 v0 = *reinterpret_cast<const float4*>(v);
+                            if constexpr (sizeof(Elem) == 2) {
+                                const float4 v1 = *reinterpret_cast<const float4*>(v + 4);
+                                *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(v0.x, v0.y), pack_bf16(v0.z, v0.w),
+                                                                           pack_bf16(v1.x, v1.y), pack_bf16(v1.z, v1.w));
+                            } else {
+                                *reinterpret_cast<float4*>(to) = v0;
+                            }
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < p.N) put(dst + j, v[j]);
+                    }
+                } else {
+                    for (int e = lane; e < 512; e += 32) {
+                        const int rr = e >> 4, j = e & 15;
+                        if (row0 + rr < p.M && col + j < p.N)
+                            put(dst + static_cast<long long>(row0 + rr) * width + j, s_out[rr * kI8OutStride + j]);
                     }
                 }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
@@ -397,7 +443,7 @@ __global__ void __launch_bounds__(256) linear_i8_few_kernel(const I8Problem p, E
 
 // --------------------------------------------------------------------------- host
 
-int g_smem_done_i8[6][64];
+int g_smem_done_i8[8][64];
 
 template <int BN, typename Elem>
 oasr_status launch_i8(I8Args a, int slot, int sms, cudaStream_t stream)
@@ -411,26 +457,41 @@ oasr_status launch_i8(I8Args a, int slot, int sms, cudaStream_t stream)
     a.tiles = static_cast<int>(t0 + t1);
     auto kern = linear_i8_kernel<BN, Elem>;
     if (!ensure_smem(kern, I8Smem<BN>::bytes, g_smem_done_i8[slot])) return OASR_ERR_CUDA;
-    return launch_pdl(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(kI8Threads), I8Smem<BN>::bytes, stream,
-                      static_cast<const I8Args>(a));
+    CUtensorMap tm[4];
+    for (int g = 0; g < 2; ++g) {
+        const I8Problem& p = a.p[a.p[1].M ? g : 0];   // one problem: its maps stand in for the other's
+        if (!encode_bytes(&tm[2 * g], p.x, p.M, a.K, 128) || !encode_bytes(&tm[2 * g + 1], p.w, p.N, a.K, BN))
+            return OASR_ERR_INVALID_ARG;
+    }
+    return launch_pdl(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(kI8Threads), I8Smem<BN>::bytes, stream, tm[0], tm[1],
+                      tm[2], tm[3], static_cast<const I8Args>(a));
 }
 
-// The widest of 128, 64 and 32 columns whose tiles cover the SMs.
+// Tile width: the one of the least estimated time, waves of tiles times a tile's cycles.  A K step of 64
+// costs the larger of converting its 128 + BN rows (I8COST cycles a row) and the matrix instructions.
 template <typename Elem>
 oasr_status dispatch_i8(const I8Args& a, cudaStream_t stream)
 {
     const int sms = sm_count();
     if (!sms || !a.status) return OASR_ERR_CUDA;
-    auto tiles = [&](int bn) {
+    int best = 256;
+    long long least = 0x7fffffffffffffffLL;
+    for (int bn = 256; bn >= 32; bn /= 2) {
         long long n = 0;
         for (const I8Problem& p : a.p)
             if (p.M) n += ((p.M + 127LL) / 128) * ((p.N + bn - 1) / bn);
-        return n;
-    };
-    constexpr int s = sizeof(Elem) == 4 ? 3 : 0;
-    if (tiles(128) >= sms) return launch_i8<128, Elem>(a, s, sms, stream);
-    if (tiles(64) >= sms) return launch_i8<64, Elem>(a, s + 1, sms, stream);
-    return launch_i8<32, Elem>(a, s + 2, sms, stream);
+        const long long step = 2 * (128 + bn), fill = 1500 + 8 * bn;
+        const long long t = ((n + sms - 1) / sms) * step * ((a.K + 63) / 64) + fill;
+        if (t < least) {
+            least = t;
+            best = bn;
+        }
+    }
+    constexpr int s = sizeof(Elem) == 4 ? 4 : 0;
+    if (best == 256) return launch_i8<256, Elem>(a, s, sms, stream);
+    if (best == 128) return launch_i8<128, Elem>(a, s + 1, sms, stream);
+    if (best == 64) return launch_i8<64, Elem>(a, s + 2, sms, stream);
+    return launch_i8<32, Elem>(a, s + 3, sms, stream);
 }
 
 template <typename Elem>
