@@ -13,7 +13,16 @@
 namespace oasr {
 namespace {
 
-constexpr int kRowsPerGroup = 2;   // rows of one 8-lane group, loaded before either is reduced
+constexpr int kRowsPerGroup = 2;   // rows of one 8-lane group, loaded before either is reduced (1, 4, 8: slower)
+
+// Page of position p (below 2^31) and its place there: a shift where block_size is a power of two (shift
+// >= 0), else a 32-bit division (64-bit ones took half of the append's time).
+__device__ __forceinline__ int page_of(int p, int block_size, int shift, int& slot)
+{
+    const int lb = shift >= 0 ? p >> shift : static_cast<int>(static_cast<unsigned>(p) / static_cast<unsigned>(block_size));
+    slot = p - lb * block_size;
+    return lb;
+}
 
 // Eight lanes per row, four rows per warp and step; rows of one stream in the order (K or V,
 // head, frame), so neighbouring groups write neighbouring rows and scale bytes of a page.
@@ -21,7 +30,7 @@ constexpr int kRowsPerGroup = 2;   // rows of one 8-lane group, loaded before ei
 template <typename Elem>
 __global__ void __launch_bounds__(256) append_e4m3_kernel(
     const Elem* __restrict__ k_new, const Elem* __restrict__ v_new, uint8_t* __restrict__ k_pool,
-    uint8_t* __restrict__ v_pool, uint8_t* __restrict__ kv_scale, int num_blocks, int block_size,
+    uint8_t* __restrict__ v_pool, uint8_t* __restrict__ kv_scale, int num_blocks, int block_size, int shift,
     const int32_t* __restrict__ block_table, int mbps, const int32_t* __restrict__ cache_seqlens,
     int T, int H, int blocks_per_stream, unsigned* status)
 {
@@ -42,20 +51,19 @@ __global__ void __launch_bounds__(256) append_e4m3_kernel(
         h[u] = rh - (kv[u] ? H : 0);
         load8((kv[u] ? v_new : k_new) + ((static_cast<long long>(b) * T + t[u]) * H + h[u]) * kE4Row + 8 * l8, x[u]);
     }
-    const long long C = __ldg(cache_seqlens + b);
+    const int C = __ldg(cache_seqlens + b);
 #pragma unroll
     for (int u = 0; u < kRowsPerGroup; ++u) {
         uint2 q;
         const uint32_t byte = e4m3_quantise8(x[u], 0xffffffffu, q);
         if (r0 + 4 * u < rows) {
-            const long long p = C + t[u];
-            const long long lb = p / block_size;
-            int blk = -1;
+            const int p = static_cast<int>(static_cast<unsigned>(C) + t[u]);   // negative when it passes 2^31 too
+            int slot, blk = -1;
+            const int lb = page_of(p, block_size, shift, slot);
             if (p >= 0 && lb < mbps) blk = __ldg(block_table + static_cast<long long>(b) * mbps + lb);
-            if (p < 0 || blk < 0 || blk >= num_blocks) {
+            if (blk < 0 || blk >= num_blocks) {
                 err = kErrBounds;
             } else {
-                const int slot = static_cast<int>(p - lb * block_size);
                 const long long page = static_cast<long long>(blk) * H + h[u];
                 *reinterpret_cast<uint2*>((kv[u] ? v_pool : k_pool) + (page * block_size + slot) * kE4Row + 8 * l8) = q;
                 if (l8 == 0) kv_scale[(2 * page + kv[u]) * block_size + slot] = static_cast<uint8_t>(byte);
@@ -88,7 +96,7 @@ __device__ __forceinline__ void store16(float* p, const float (&x)[16])
 template <typename Elem>
 __global__ void __launch_bounds__(256) read_e4m3_kernel(
     const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
-    const uint8_t* __restrict__ kv_scale, int num_blocks, int block_size,
+    const uint8_t* __restrict__ kv_scale, int num_blocks, int block_size, int shift,
     const int32_t* __restrict__ block_table, int mbps, const int32_t* __restrict__ cache_seqlens,
     const int32_t* __restrict__ start, Elem* __restrict__ k, Elem* __restrict__ v, int L, int H,
     int blocks_per_stream, unsigned* status)
@@ -107,12 +115,12 @@ __global__ void __launch_bounds__(256) read_e4m3_kernel(
         if (p < 0 || len < 0) {
             err = kErrBounds;
         } else if (p < len) {
-            const long long lb = p / block_size;
+            int slot;                       // p < len <= 2^31 - 1
+            const int lb = page_of(static_cast<int>(p), block_size, shift, slot);
             const int blk = lb < mbps ? __ldg(block_table + static_cast<long long>(b) * mbps + lb) : -1;
             if (blk < 0 || blk >= num_blocks) {
                 err = kErrBounds;
             } else {
-                const int slot = static_cast<int>(p - lb * block_size);
                 const long long page = static_cast<long long>(blk) * H + h;
                 const long long row = (page * block_size + slot) * kE4Row + 16 * l4;
                 q[0] = __ldg(reinterpret_cast<const uint4*>(k_pool + row));
@@ -140,6 +148,9 @@ __global__ void __launch_bounds__(256) read_e4m3_kernel(
     grid_dep_trigger();
     if (err && l4 == 0) atomicOr(status, err);
 }
+
+// log2 of a power of two, else -1
+int shift_of(int block_size) { return block_size & (block_size - 1) ? -1 : __builtin_ctz(static_cast<unsigned>(block_size)); }
 
 }  // namespace
 }  // namespace oasr
@@ -169,7 +180,7 @@ extern "C" oasr_status oasr_paged_append_e4m3(const void* k_new, const void* v_n
     auto go = [&](auto* kn, auto* vn, auto kern) {
         return launch_pdl(kern, dim3(static_cast<unsigned>(per_stream * B)), dim3(256), 0, stream, kn, vn,
                           static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool),
-                          static_cast<uint8_t*>(kv_scale), num_blocks, block_size, block_table,
+                          static_cast<uint8_t*>(kv_scale), num_blocks, block_size, shift_of(block_size), block_table,
                           max_blocks_per_seq, cache_seqlens, T, H, static_cast<int>(per_stream), status);
     };
     if (dt == OASR_F32)
@@ -202,7 +213,7 @@ extern "C" oasr_status oasr_paged_read_e4m3(const void* k_pool, const void* v_po
     auto go = [&](auto* kd, auto* vd, auto kern) {
         return launch_pdl(kern, dim3(static_cast<unsigned>(per_stream * B)), dim3(256), 0, stream,
                           static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool),
-                          static_cast<const uint8_t*>(kv_scale), num_blocks, block_size, block_table,
+                          static_cast<const uint8_t*>(kv_scale), num_blocks, block_size, shift_of(block_size), block_table,
                           max_blocks_per_seq, cache_seqlens, start, kd, vd, L, H,
                           static_cast<int>(per_stream), status);
     };

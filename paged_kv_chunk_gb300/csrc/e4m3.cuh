@@ -59,22 +59,17 @@ __device__ __forceinline__ float2 e4m3_unpack2(uint32_t w)
 // byte (in every lane) and this lane's eight bytes.  All eight lanes must be active.
 __device__ __forceinline__ uint32_t e4m3_quantise8(const float (&x)[8], unsigned mask, uint2& q)
 {
-    float amax = 0.f;
-    bool bad = false;
+    // the largest magnitude by its bits, which order as the values do, with NaN above infinity
+    uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(x[i]);
-        bad |= !(a < INFINITY);
-        amax = fmaxf(amax, a);
-    }
-    if (bad) amax = INFINITY;
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-    if (amax == INFINITY) {
+    for (int o = 1; o < 8; o <<= 1) amax = max(amax, __shfl_xor_sync(mask, amax, o));
+    if (amax >= 0x7f800000u) {
         q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
         return kE4NanScale;
     }
-    const uint32_t byte = e4m3_scale_byte(amax);
+    const uint32_t byte = e4m3_scale_byte(__uint_as_float(amax));
     const float s = e4m3_scale_inverse(byte);
     q.x = e4m3_pack2(x[0] * s, x[1] * s) | (e4m3_pack2(x[2] * s, x[3] * s) << 16);
     q.y = e4m3_pack2(x[4] * s, x[5] * s) | (e4m3_pack2(x[6] * s, x[7] * s) << 16);

@@ -9,6 +9,8 @@
 // read the 8-bit rows and write them as fp16 into the swizzled tiles the matrix instructions
 // read.  A sum stays below 2^24 for K <= 1024, where fp32 holds every integer: the accumulated
 // sum is the integer sum.  For longer K it is that of an fp32 accumulation.
+#include <type_traits>
+
 #include "attn_core.cuh"
 #include "e4m3.cuh"
 #include "host_common.h"
@@ -20,10 +22,10 @@ namespace {
 // ------------------------------------------------------------------ rows to 8 bits
 
 constexpr float kLeastMax = 7.8886090522101181e-31f;   // 2^-100
-constexpr int kKeep = 4;   // chunks of eight values a thread keeps between its two passes
 
-// TPR threads per row; each takes every TPR-th chunk of eight values.
-template <typename Elem, int TPR>
+// TPR threads per row, each with NC chunks of eight values in registers (NC 0: a longer row, read a second
+// time for its quantisation).  Bound by HBM: 2 or 4 bytes in, one out per value.
+template <typename Elem, int TPR, int NC>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const Elem* __restrict__ x, int8_t* __restrict__ x8,
                                                             float* __restrict__ scale, int M, int K)
 {
@@ -32,18 +34,28 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const Elem* __restri
     const int l = threadIdx.x % TPR, chunks = K / 8;
     const bool on = row < M;
     const Elem* src = x + static_cast<long long>(on ? row : 0) * K;
-    float keep[kKeep][8];
+    constexpr int N = NC ? NC : 1;
+    float v[N][8];
     float m = 0.f;
-    for (int i = 0, c = l; c < chunks; ++i, c += TPR) {
-        float v[8];
-        load8(src + 8 * c, v);
+    auto largest = [&](const float (&w)[8]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fabsf(v[e]) < INFINITY ? fmaxf(m, fabsf(v[e])) : INFINITY;
+        for (int e = 0; e < 8; ++e) m = fabsf(w[e]) < INFINITY ? fmaxf(m, fabsf(w[e])) : INFINITY;
+    };
+    if constexpr (NC > 0) {
 #pragma unroll
-        for (int k = 0; k < kKeep; ++k)
-            if (k == i)
+        for (int i = 0; i < NC; ++i) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) keep[k][e] = v[e];
+            for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+            if (l + TPR * i < chunks) load8(src + 8 * (l + TPR * i), v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) largest(v[i]);
+    } else {
+#pragma unroll 4
+        for (int c = l; c < chunks; c += TPR) {
+            load8(src + 8 * c, v[0]);
+            largest(v[0]);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -56,28 +68,27 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const Elem* __restri
     }
     const bool bad = m == INFINITY;
     m = fmaxf(m, kLeastMax);
-    const float f = bad ? 0.f : __fmul_rn(__frcp_rn(m), 127.f);
+    const float f = __fmul_rn(__frcp_rn(m), 127.f);
     if (on) {
         if (l == 0) scale[row] = bad ? NAN : __fdiv_rn(m, 127.f);
         int8_t* dst = x8 + static_cast<long long>(row) * K;
-        for (int i = 0, c = l; c < chunks; ++i, c += TPR) {
-            float v[8];
-            bool kept = false;
+        auto put8 = [&](int c, const float (&w)[8]) {
+            uint32_t q[2] = {0u, 0u};
 #pragma unroll
-            for (int k = 0; k < kKeep; ++k)
-                if (k == i) {
-                    kept = true;
+            for (int e = 0; e < 8; ++e)
+                q[e >> 2] |= (static_cast<uint32_t>(__float2int_rn(__fmul_rn(w[e], f))) & 255u) << (8 * (e & 3));
+            *reinterpret_cast<uint2*>(dst + 8 * c) = bad ? make_uint2(0u, 0u) : make_uint2(q[0], q[1]);
+        };
+        if constexpr (NC > 0) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = keep[k][e];
-                }
-            if (!kept) load8(src + 8 * c, v);
-            uint32_t w[2] = {0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int q = bad ? 0 : __float2int_rn(__fmul_rn(v[e], f));
-                w[e >> 2] |= (static_cast<uint32_t>(q) & 255u) << (8 * (e & 3));
+            for (int i = 0; i < NC; ++i)
+                if (l + TPR * i < chunks) put8(l + TPR * i, v[i]);
+        } else {
+#pragma unroll 2
+            for (int c = l; c < chunks; c += TPR) {
+                load8(src + 8 * c, v[0]);
+                put8(c, v[0]);
             }
-            *reinterpret_cast<uint2*>(dst + 8 * c) = make_uint2(w[0], w[1]);
         }
     }
     grid_dep_trigger();
@@ -138,7 +149,7 @@ struct I8Smem {
     static constexpr int rows = 128 + BN;                              // x rows, then w rows
     static constexpr int tile_a = 128 * 128, tile = rows * 128;        // fp16, 64 of K
     static constexpr int raw = rows * 64;                              // 8-bit, 64 of K
-    static constexpr int stages = BN == 256 ? 3 : 4, raws = BN == 256 ? 2 : 4;
+    static constexpr int stages = BN == 256 ? 2 : 4, raws = 4;
     static constexpr int off_raw = stages * tile;
     static constexpr int off_out = off_raw + raws * raw;               // [8 warps][32][kI8OutStride] floats
     static constexpr int off_ws = off_out + kI8EpiWarps * 32 * kI8OutStride * 4;   // [8 warps][2][BN / 2] floats
@@ -516,17 +527,20 @@ extern "C" oasr_status oasr_quantize_rows(const void* x, void* x8, float* scale,
     if (!x || !x8 || !scale || M <= 0 || K <= 0) return OASR_ERR_INVALID_ARG;
     if ((dt != OASR_F32 && dt != OASR_BF16) || K % 16) return OASR_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(x8) || !aligned16(scale)) return OASR_ERR_INVALID_ARG;
-    auto go = [&](auto* src, auto warp_kern, auto block_kern) {
-        // a warp per row keeps up to 1024 values in registers; longer rows take a block each
-        const bool warp = K <= 32 * 8 * kKeep;
-        const unsigned grid = warp ? (static_cast<unsigned>(M) + 7) / 8 : static_cast<unsigned>(M);
-        return launch_pdl(warp ? warp_kern : block_kern, dim3(grid), dim3(256), 0, stream, src,
-                          static_cast<int8_t*>(x8), scale, M, K);
+    // a warp per row while its values fit the warp's registers, a block per longer row
+    auto go = [&](auto* src, auto kern, int rows_per_block) {
+        return launch_pdl(kern, dim3((static_cast<unsigned>(M) + rows_per_block - 1) / rows_per_block), dim3(256), 0, stream,
+                          src, static_cast<int8_t*>(x8), scale, M, K);
     };
-    if (dt == OASR_F32)
-        return go(static_cast<const float*>(x), quantize_rows_kernel<float, 32>, quantize_rows_kernel<float, 256>);
-    return go(static_cast<const __nv_bfloat16*>(x), quantize_rows_kernel<__nv_bfloat16, 32>,
-              quantize_rows_kernel<__nv_bfloat16, 256>);
+    auto by_length = [&](auto* src) {
+        using E = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
+        if (K <= 256) return go(src, quantize_rows_kernel<E, 32, 1>, 8);
+        if (K <= 512) return go(src, quantize_rows_kernel<E, 32, 2>, 8);
+        if (K <= 1024) return go(src, quantize_rows_kernel<E, 32, 4>, 8);
+        if (K <= 8192) return go(src, quantize_rows_kernel<E, 256, 4>, 1);
+        return go(src, quantize_rows_kernel<E, 256, 0>, 1);
+    };
+    return dt == OASR_F32 ? by_length(static_cast<const float*>(x)) : by_length(static_cast<const __nv_bfloat16*>(x));
 }
 
 extern "C" oasr_status oasr_linear_w8a8(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
