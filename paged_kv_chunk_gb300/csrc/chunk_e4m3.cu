@@ -63,7 +63,7 @@ struct E4Args {
     int num_blocks, block_size, bs_shift, mbps, T, H, R;
     int items;        // (stream, head, query tile)
     int q_tiles, splits;
-    float scale_log2; // scale * log2(e)
+    float scale, scale_log2;   // the latter times log2(e)
 };
 
 // Shared memory (byte offsets from a 1024-aligned base).
@@ -946,117 +946,281 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
 
 // ----------------------------------------------------------------------------- fp32
 
-// One warp per query row, lanes over keys, fp32 throughout (the 16-bit pools' fp32 kernel with
-// rows decoded on the way in).  The chunk is already in the pool.
-__global__ void __launch_bounds__(128) chunk_e4m3_f32_kernel(
-    const float* __restrict__ q, const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
-    const uint8_t* __restrict__ kv_scale, int num_blocks, int block_size,
-    const int32_t* __restrict__ block_table, int mbps, const int32_t* __restrict__ cache_seqlens,
-    const float* __restrict__ u, const float* __restrict__ vb, const float* __restrict__ rel, int R,
-    float* __restrict__ out, int T, int H, float scale, unsigned* status)
+// fp32 throughout (no TF32), the chunk already in the pool.  One CTA per (stream, head, 16 queries, share
+// of the keys); tiles of 64 keys, K and V decoded to fp32 on their way into shared memory (exact), the
+// rel rows the tile's distances need (79 of them) copied beside them a tile ahead.  Content and position
+// products are register tiles of 2 rows by 4 keys or 5 distances, summed apart (their sum is rounded
+// once); the position term is skewed through shared memory.  Bound by the fp32 FMA rate: 16 * 64 * (64 +
+// 80 + 64) of them a tile.
+constexpr int kFRows = 16, kFKeys = 64, kFRel = 80;
+constexpr int kFStride = 68;      // floats of a 64-value row: rows apart by four banks
+constexpr int kFThreads = 128;
+
+struct F32Smem {
+    float qu[kFRows][kFStride], qv[kFRows][kFStride];
+    float k[kFKeys][kFStride], v[kFKeys][kFStride];
+    float rel[2][kFRel][kFStride];
+    float g[kFRows][kFRel + 4];
+    float p[kFRows][kFStride];
+    float part_o[kFRows][kHeadDim], part_m[kFRows], part_l[kFRows];
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on)
 {
-    __shared__ float s_qu[kE4MaxT][kHeadDim];
-    __shared__ float s_qv[kE4MaxT][kHeadDim];
-    const int b = blockIdx.x / H, h = blockIdx.x % H;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    unsigned err = 0;
-    int C = cache_seqlens[b];
-    if (C < 0) { C = 0; err |= kErrBounds; }
-    const int cap = mbps * block_size;
-    if (C > cap) { C = cap; err |= kErrBounds; }
-    int K = C + T;
-    if (K > cap) { K = cap; err |= kErrBounds; }
-    if (C + 2 * T - 1 > R) err |= kErrBounds;
-    const int off = R - T - C;
-    for (int idx = tid; idx < T * kHeadDim; idx += blockDim.x) {
-        const int t = idx / kHeadDim, d = idx % kHeadDim;
-        const float qq = q[((static_cast<long long>(b) * T + t) * H + h) * kHeadDim + d];
-        s_qu[t][d] = qq + u[h * kHeadDim + d];
-        s_qv[t][d] = qq + vb[h * kHeadDim + d];
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+
+__global__ void __launch_bounds__(kFThreads) chunk_e4m3_f32_kernel(
+    const float* __restrict__ q, const uint8_t* __restrict__ k_pool, const uint8_t* __restrict__ v_pool,
+    const uint8_t* __restrict__ kv_scale, const float* __restrict__ u, const float* __restrict__ vb,
+    const float* __restrict__ rel, float* __restrict__ out, const E4Args a)
+{
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    F32Smem& sm = *reinterpret_cast<F32Smem*>(smem_raw);
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int S = a.splits, T = a.T, H = a.H, bs = a.block_size;
+    int idx = blockIdx.x;
+    const int split = idx % S;
+    idx /= S;
+    const int i0 = (idx % a.q_tiles) * kFRows;
+    idx /= a.q_tiles;
+    const int b = idx / H, h = idx - b * H;
+    grid_dep_wait();
+    const E4Item t = e4_item<1, false>(a, __ldg(a.cache_seqlens + b), split);
+    unsigned err = t.err;
+    // query rows past T are zero
+    for (int i = tid; i < kFRows * 16; i += kFThreads) {
+        const int r = i >> 4, d = 4 * (i & 15);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + r < T) x = __ldg(reinterpret_cast<const float4*>(q + ((static_cast<long long>(b) * T + i0 + r) * H + h) * kHeadDim + d));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(u + h * kHeadDim + d));
+        const float4 z = __ldg(reinterpret_cast<const float4*>(vb + h * kHeadDim + d));
+        *reinterpret_cast<float4*>(&sm.qu[r][d]) = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        *reinterpret_cast<float4*>(&sm.qv[r][d]) = make_float4(x.x + z.x, x.y + z.y, x.z + z.z, x.w + z.w);
     }
-    __syncthreads();
-    for (int i = warp; i < T; i += 4) {
-        float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-        for (int j0 = 0; j0 < K; j0 += 32) {
-            const int j = j0 + lane;
-            float sc = -INFINITY, vs = 0.f;
-            long long row_off = -1;
-            if (j < K) {
-                const int lb = j / block_size;
-                const int blk = block_table[static_cast<long long>(b) * mbps + lb];
-                float acc = 0.f;
-                if (blk >= 0 && blk < num_blocks) {
-                    const long long page = static_cast<long long>(blk) * H + h;
-                    const int slot = j - lb * block_size;
-                    row_off = (page * block_size + slot) * kE4Row;
-                    vs = e4m3_scale(kv_scale[(2 * page + 1) * block_size + slot]);
-                    const uint4* kr = reinterpret_cast<const uint4*>(k_pool + row_off);
+    // this thread's 32 bytes of a key's K and V rows
+    const int kr = tid >> 1, kd = 32 * (tid & 1);
+    uint4 raw[4];
+    float ks = 0.f, vs = 0.f;
+    auto request = [&](int s) {
+        const int j = s * kFKeys + kr;
+        ks = vs = 0.f;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint4 w4 = kr[c];
-                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 lo = e4m3_unpack2(w[e]), hi = e4m3_unpack2(w[e] >> 16);
-                            const float* qq = &s_qu[i][16 * c + 4 * e];
-                            acc = fmaf(qq[0], lo.x, acc);
-                            acc = fmaf(qq[1], lo.y, acc);
-                            acc = fmaf(qq[2], hi.x, acc);
-                            acc = fmaf(qq[3], hi.y, acc);
-                        }
-                    }
-                    acc *= e4m3_scale(kv_scale[2 * page * block_size + slot]);
-                } else {
-                    err |= kErrBounds;
-                }
-                const int rho = off + j - i;
-                if (rho >= 0 && rho < R) {
-                    const float4* rr = reinterpret_cast<const float4*>(rel + (static_cast<long long>(rho) * H + h) * kHeadDim);
-#pragma unroll 4
-                    for (int d4 = 0; d4 < kHeadDim / 4; ++d4) {
-                        const float4 r4 = rr[d4];
-                        acc = fmaf(s_qv[i][4 * d4], r4.x, acc);
-                        acc = fmaf(s_qv[i][4 * d4 + 1], r4.y, acc);
-                        acc = fmaf(s_qv[i][4 * d4 + 2], r4.z, acc);
-                        acc = fmaf(s_qv[i][4 * d4 + 3], r4.w, acc);
-                    }
-                }
-                sc = acc * scale;
+        for (int i = 0; i < 4; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (j < t.K) {
+            const int lb = j >> a.bs_shift;
+            const int blk = __ldg(a.block_table + static_cast<long long>(b) * a.mbps + lb);
+            if (blk >= 0 && blk < a.num_blocks) {
+                const long long page = static_cast<long long>(blk) * H + h;
+                const int slot = j & (bs - 1);
+                const uint4* kp = reinterpret_cast<const uint4*>(k_pool + (page * bs + slot) * kE4Row + kd);
+                const uint4* vp = reinterpret_cast<const uint4*>(v_pool + (page * bs + slot) * kE4Row + kd);
+                raw[0] = kp[0];
+                raw[1] = kp[1];
+                raw[2] = vp[0];
+                raw[3] = vp[1];
+                ks = e4m3_scale(kv_scale[2 * page * bs + slot]);
+                vs = e4m3_scale(kv_scale[(2 * page + 1) * bs + slot]);
+            } else {
+                err |= kErrBounds;
             }
-            float mx = sc;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float m_new = fmaxf(m, mx);
-            const float alpha = (m == -INFINITY) ? 0.f : expf(m - m_new);
-            const float p = (j < K) ? expf(sc - m_new) : 0.f;
-            float psum = p;
-#pragma unroll
-            for (int o = 16; o; o >>= 1) psum += __shfl_xor_sync(0xffffffffu, psum, o);
-            l = l * alpha + psum;
-            o0 *= alpha;
-            o1 *= alpha;
-            const float pv = p * vs;
-            const int nj = min(32, K - j0);
-            for (int jj = 0; jj < nj; ++jj) {
-                const float pj = __shfl_sync(0xffffffffu, pv, jj);
-                const long long ro = __shfl_sync(0xffffffffu, row_off, jj);
-                if (ro >= 0) {
-                    const float2 v2 = e4m3_unpack2(*reinterpret_cast<const uint16_t*>(v_pool + ro + 2 * lane));
-                    o0 = fmaf(pj, v2.x, o0);
-                    o1 = fmaf(pj, v2.y, o1);
-                }
-            }
-            m = m_new;
         }
-        float2* dst = reinterpret_cast<float2*>(out + ((static_cast<long long>(b) * T + i) * H + h) * kHeadDim);
-        dst[lane] = make_float2(o0 / l, o1 / l);
+    };
+    auto request_rel = [&](int s, int buf) {   // table rows of the distances of keys 64 s .. and the queries
+        for (int i = tid; i < (kFRel - 1) * 16; i += kFThreads) {
+            const int r = i >> 4, d = 4 * (i & 15);
+            const int rho = t.off + s * kFKeys - i0 - (kFRows - 1) + r;
+            const bool on = rho >= 0 && rho < a.R;
+            cp_async16(smem_addr(&sm.rel[buf][r][d]), rel + (static_cast<long long>(on ? rho : 0) * H + h) * kHeadDim + d, on);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][4] = {};
+    if (t.st0 < t.st1) {
+        request(t.st0);
+        request_rel(t.st0, 0);
     }
-    if (err) atomicOr(status, err);
+    for (int s = t.st0; s < t.st1; ++s) {
+        const int buf = (s - t.st0) & 1;
+        __syncthreads();   // the previous tile has been read
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            float* dst = (i < 2 ? sm.k : sm.v)[kr] + kd + 16 * (i & 1);
+            const float sc = i < 2 ? ks : vs;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 lo = e4m3_unpack2(w[e]), hi = e4m3_unpack2(w[e] >> 16);
+                *reinterpret_cast<float4*>(dst + 4 * e) = make_float4(lo.x * sc, lo.y * sc, hi.x * sc, hi.y * sc);
+            }
+        }
+        if (s + 1 < t.st1) {
+            request(s + 1);
+            request_rel(s + 1, buf ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncthreads();
+        float sc[2][4] = {}, gc[2][5] = {};
+#pragma unroll 4
+        for (int d = 0; d < kHeadDim; d += 4) {
+            const float4 q0 = *reinterpret_cast<const float4*>(&sm.qu[ty][d]), q1 = *reinterpret_cast<const float4*>(&sm.qu[ty + 8][d]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float4 kk = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * c][d]);
+                sc[0][c] = fmaf(q0.w, kk.w, fmaf(q0.z, kk.z, fmaf(q0.y, kk.y, fmaf(q0.x, kk.x, sc[0][c]))));
+                sc[1][c] = fmaf(q1.w, kk.w, fmaf(q1.z, kk.z, fmaf(q1.y, kk.y, fmaf(q1.x, kk.x, sc[1][c]))));
+            }
+        }
+#pragma unroll 4
+        for (int d = 0; d < kHeadDim; d += 4) {
+            const float4 q0 = *reinterpret_cast<const float4*>(&sm.qv[ty][d]), q1 = *reinterpret_cast<const float4*>(&sm.qv[ty + 8][d]);
+#pragma unroll
+            for (int c = 0; c < 5; ++c) {
+                const float4 rr = *reinterpret_cast<const float4*>(&sm.rel[buf][tx + 16 * c][d]);
+                gc[0][c] = fmaf(q0.w, rr.w, fmaf(q0.z, rr.z, fmaf(q0.y, rr.y, fmaf(q0.x, rr.x, gc[0][c]))));
+                gc[1][c] = fmaf(q1.w, rr.w, fmaf(q1.z, rr.z, fmaf(q1.y, rr.y, fmaf(q1.x, rr.x, gc[1][c]))));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < 5; ++c) sm.g[ty + 8 * r][tx + 16 * c] = gc[r][c];
+        __syncwarp();      // a row's 16 threads are half a warp
+        const int left = t.K - s * kFKeys;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = ty + 8 * r;
+            float mx = m[r];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = tx + 16 * c;
+                sc[r][c] = j < left ? (sc[r][c] + sm.g[row][j + kFRows - 1 - row]) * a.scale : -INFINITY;
+                mx = fmaxf(mx, sc[r][c]);
+            }
+#pragma unroll
+            for (int x = 8; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float base = mx == -INFINITY ? 0.f : mx;
+            const float alpha = expf(m[r] - base);
+            m[r] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float e = expf(sc[r][c] - base);
+                sum += e;
+                sm.p[row][tx + 16 * c] = e;
+            }
+            l[r] = fmaf(l[r], alpha, sum);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][e] *= alpha;
+        }
+        __syncwarp();
+        float acc[2][4] = {};   // the tile's own sum, added to the running one once
+#pragma unroll 4
+        for (int j = 0; j < kFKeys; j += 4) {
+            const float4 p0 = *reinterpret_cast<const float4*>(&sm.p[ty][j]), p1 = *reinterpret_cast<const float4*>(&sm.p[ty + 8][j]);
+            const float w0[4] = {p0.x, p0.y, p0.z, p0.w}, w1[4] = {p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 vv = *reinterpret_cast<const float4*>(&sm.v[j + e][4 * tx]);
+                acc[0][0] = fmaf(w0[e], vv.x, acc[0][0]);
+                acc[0][1] = fmaf(w0[e], vv.y, acc[0][1]);
+                acc[0][2] = fmaf(w0[e], vv.z, acc[0][2]);
+                acc[0][3] = fmaf(w0[e], vv.w, acc[0][3]);
+                acc[1][0] = fmaf(w1[e], vv.x, acc[1][0]);
+                acc[1][1] = fmaf(w1[e], vv.y, acc[1][1]);
+                acc[1][2] = fmaf(w1[e], vv.z, acc[1][2]);
+                acc[1][3] = fmaf(w1[e], vv.w, acc[1][3]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][e] += acc[r][e];
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int x = 8; x; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
+    grid_dep_trigger();
+    if (err) atomicOr(a.status, err);
+    if (S == 1) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = i0 + ty + 8 * r;
+            if (row < T)
+                *reinterpret_cast<float4*>(out + ((static_cast<long long>(b) * T + row) * H + h) * kHeadDim + 4 * tx) =
+                    make_float4(o[r][0] / l[r], o[r][1] / l[r], o[r][2] / l[r], o[r][3] / l[r]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        *reinterpret_cast<float4*>(&sm.part_o[ty + 8 * r][4 * tx]) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+        if (tx == 0) {
+            sm.part_m[ty + 8 * r] = m[r];
+            sm.part_l[ty + 8 * r] = l[r];
+        }
+    }
+    cluster_sync();
+    // rows split, split + S, ... of the cluster's queries are finished here, a warp each
+    const uint32_t po = smem_addr(&sm.part_o[0][0]), pm = smem_addr(&sm.part_m[0]), pl = smem_addr(&sm.part_l[0]);
+    const int lane = tid & 31;
+    for (int row = split + S * (tid >> 5); row < min(kFRows, T - i0); row += S * (kFThreads / 32)) {
+        float mx = -INFINITY;
+        for (int k = 0; k < S; ++k) mx = fmaxf(mx, ld_cluster(pm + 4 * row, k));
+        float o0 = 0.f, o1 = 0.f, sum = 0.f;
+        for (int k = 0; k < S; ++k) {
+            const float mk = ld_cluster(pm + 4 * row, k);
+            const float w = mk == -INFINITY ? 0.f : expf(mk - mx);   // a share without keys
+            sum = fmaf(w, ld_cluster(pl + 4 * row, k), sum);
+            o0 = fmaf(w, ld_cluster(po + 4 * (row * kHeadDim + 2 * lane), k), o0);
+            o1 = fmaf(w, ld_cluster(po + 4 * (row * kHeadDim + 2 * lane + 1), k), o1);
+        }
+        reinterpret_cast<float2*>(out + ((static_cast<long long>(b) * T + i0 + row) * H + h) * kHeadDim)[lane] = make_float2(o0 / sum, o1 / sum);
+    }
+    cluster_sync();
 }
 
 // --------------------------------------------------------------------------- host
 
 int g_smem_done_e4[8][64];
+
+// Query tiles of Tp rows, and shares of the keys while the (stream, head, tile) triples leave half of the
+// SMs idle and every share keeps two stages of the keys a well-formed stream can have; the number of triples.
+long long e4_splits(E4Args& a, int B, int Tp, int k_max)
+{
+    a.q_tiles = (a.T + Tp - 1) / Tp;
+    const long long pairs = static_cast<long long>(B) * a.H * a.q_tiles;
+    const int stages = (k_max + kStageKeys - 1) / kStageKeys, sms = sm_count();
+    a.splits = 1;
+    while (a.splits < 8 && pairs * a.splits * 2 <= sms && stages >= 2 * a.splits) a.splits *= 2;
+    return pairs;
+}
+
+// Launch with programmatic stream serialization (host_common.h) and clusters of `splits` CTAs.
+template <typename... KArgs, typename... Args>
+oasr_status launch_e4_cluster(void (*kern)(KArgs...), long long ctas, int threads, int smem, int splits,
+                              cudaStream_t stream, Args&&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...) != cudaSuccess) return OASR_ERR_CUDA;
+    return launch_status();
+}
 
 template <int MT, int NS, int CTAS, bool FUSED>
 oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const void* rel, E4Args& a, int k_max, int B,
@@ -1076,32 +1240,13 @@ oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const
     auto kern = chunk_e4m3_kernel<MT, NS, CTAS, FUSED>;
     const int smem = SP::bytes + 2 * a.mbps * 4;
     if (!ensure_smem(kern, smem, g_smem_done_e4[slot])) return OASR_ERR_CUDA;
-    const int stages = (k_max + kStageKeys - 1) / kStageKeys;   // of a well-formed stream, at most
-    a.q_tiles = (a.T + SP::Tp - 1) / SP::Tp;
-    const long long pairs = static_cast<long long>(B) * a.H * a.q_tiles;
-    const int sms = sm_count();
-    a.splits = 1;
-    while (a.splits < 8 && pairs * a.splits * 2 <= sms && stages >= 2 * a.splits) a.splits *= 2;
+    const long long pairs = e4_splits(a, B, SP::Tp, k_max);
     if (pairs > 0x7fffffffLL / 2) return OASR_ERR_UNSUPPORTED;
     a.items = static_cast<int>(pairs);
-    const long long ctas = a.splits > 1 ? pairs * a.splits : pairs < static_cast<long long>(CTAS) * sms ? pairs : static_cast<long long>(CTAS) * sms;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, tm_r, tm_kn, tm_vn, static_cast<const E4Args>(a)) != cudaSuccess)
-        return OASR_ERR_CUDA;
-    return launch_status();
+    const long long most = static_cast<long long>(CTAS) * sm_count();
+    const long long ctas = a.splits > 1 ? pairs * a.splits : pairs < most ? pairs : most;
+    return launch_e4_cluster(kern, ctas, kThreads, smem, a.splits, stream, tm_q, tm_k, tm_v, tm_r, tm_kn, tm_vn,
+                             static_cast<const E4Args>(a));
 }
 
 template <bool FUSED>
@@ -1134,14 +1279,6 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
                                                       bt, mbps, cs, B, T, H, D, dt, stream);
         if (st != OASR_OK) return st;
     }
-    if (dt == OASR_F32) {
-        chunk_e4m3_f32_kernel<<<static_cast<unsigned>(B) * H, 128, 0, stream>>>(
-            static_cast<const float*>(q), static_cast<const uint8_t*>(k_pool), static_cast<const uint8_t*>(v_pool),
-            static_cast<const uint8_t*>(kv_scale), num_blocks, block_size, bt, mbps, cs,
-            static_cast<const float*>(u), static_cast<const float*>(vb), static_cast<const float*>(rel), R,
-            static_cast<float*>(out), T, H, scale, status);
-        return launch_status();
-    }
     E4Args a = {};
     a.k_pool = static_cast<uint8_t*>(k_pool);
     a.v_pool = static_cast<uint8_t*>(v_pool);
@@ -1159,11 +1296,22 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     a.T = T;
     a.H = H;
     a.R = R;
+    a.scale = scale;
     a.scale_log2 = scale * 1.4426950408889634f;
     // keys a well-formed stream of the call can have
     const long long pages = static_cast<long long>(mbps) * block_size, dist = static_cast<long long>(R) - T + 1;
     const long long k_max = pages < dist ? pages : dist;
     const int km = static_cast<int>(k_max < T ? T : k_max);
+    if (dt == OASR_F32) {
+        const long long pairs = e4_splits(a, B, kFRows, km);
+        if (pairs * a.splits > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
+        if (!ensure_smem(chunk_e4m3_f32_kernel, sizeof(F32Smem), g_smem_done_e4[3])) return OASR_ERR_CUDA;
+        return launch_e4_cluster(chunk_e4m3_f32_kernel, pairs * a.splits, kFThreads, static_cast<int>(sizeof(F32Smem)), a.splits,
+                                 stream, static_cast<const float*>(q), static_cast<const uint8_t*>(a.k_pool),
+                                 static_cast<const uint8_t*>(a.v_pool), static_cast<const uint8_t*>(a.kv_scale),
+                                 static_cast<const float*>(u), static_cast<const float*>(vb), static_cast<const float*>(rel),
+                                 static_cast<float*>(out), static_cast<const E4Args>(a));
+    }
     if (T <= 16) return launch_e4<1, E4NS, E4CTAS, FUSED>(q, k_new, v_new, rel, a, km, B, FUSED ? 1 : 0, stream);
     return launch_e4<2, E4NS2, E4CTAS2, false>(q, k_new, v_new, rel, a, km, B, 2, stream);
 }
