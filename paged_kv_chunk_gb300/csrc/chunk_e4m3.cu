@@ -1185,7 +1185,23 @@ __global__ void __launch_bounds__(kFThreads) chunk_e4m3_f32_kernel(
 
 // --------------------------------------------------------------------------- host
 
-int g_smem_done_e4[8][64];
+int g_smem_done_e4[4][64];
+bool g_clusters_e4[4][64];
+
+// Allow clusters of more than eight CTAs of `func`, once per device.
+template <typename F>
+bool ensure_clusters(F* func, bool (&done)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!done[dev] && cudaFuncSetAttribute(reinterpret_cast<const void*>(func), cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                           1) != cudaSuccess)
+        return false;
+    done[dev] = true;
+    return true;
+}
+
+constexpr int kMaxShares = 16;   // CTAs of a cluster (over the portable eight: enabled per kernel)
 
 // Query tiles of Tp rows, and shares of the keys while the (stream, head, tile) triples leave half of the
 // SMs idle and every share keeps two stages of the keys a well-formed stream can have; the number of triples.
@@ -1195,7 +1211,7 @@ long long e4_splits(E4Args& a, int B, int Tp, int k_max)
     const long long pairs = static_cast<long long>(B) * a.H * a.q_tiles;
     const int stages = (k_max + kStageKeys - 1) / kStageKeys, sms = sm_count();
     a.splits = 1;
-    while (a.splits < 8 && pairs * a.splits * 2 <= sms && stages >= 2 * a.splits) a.splits *= 2;
+    while (a.splits < kMaxShares && pairs * a.splits * 2 <= sms && stages >= 2 * a.splits) a.splits *= 2;
     return pairs;
 }
 
@@ -1239,7 +1255,7 @@ oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const
         return OASR_ERR_INVALID_ARG;
     auto kern = chunk_e4m3_kernel<MT, NS, CTAS, FUSED>;
     const int smem = SP::bytes + 2 * a.mbps * 4;
-    if (!ensure_smem(kern, smem, g_smem_done_e4[slot])) return OASR_ERR_CUDA;
+    if (!ensure_smem(kern, smem, g_smem_done_e4[slot]) || !ensure_clusters(kern, g_clusters_e4[slot])) return OASR_ERR_CUDA;
     const long long pairs = e4_splits(a, B, SP::Tp, k_max);
     if (pairs > 0x7fffffffLL / 2) return OASR_ERR_UNSUPPORTED;
     a.items = static_cast<int>(pairs);
@@ -1305,7 +1321,9 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     if (dt == OASR_F32) {
         const long long pairs = e4_splits(a, B, kFRows, km);
         if (pairs * a.splits > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
-        if (!ensure_smem(chunk_e4m3_f32_kernel, sizeof(F32Smem), g_smem_done_e4[3])) return OASR_ERR_CUDA;
+        if (!ensure_smem(chunk_e4m3_f32_kernel, sizeof(F32Smem), g_smem_done_e4[3]) ||
+            !ensure_clusters(chunk_e4m3_f32_kernel, g_clusters_e4[3]))
+            return OASR_ERR_CUDA;
         return launch_e4_cluster(chunk_e4m3_f32_kernel, pairs * a.splits, kFThreads, static_cast<int>(sizeof(F32Smem)), a.splits,
                                  stream, static_cast<const float*>(q), static_cast<const uint8_t*>(a.k_pool),
                                  static_cast<const uint8_t*>(a.v_pool), static_cast<const uint8_t*>(a.kv_scale),
