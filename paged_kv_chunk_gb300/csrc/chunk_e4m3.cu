@@ -35,9 +35,9 @@ namespace oasr {
 namespace {
 
 #ifndef E4NS
-#define E4NS 5
+#define E4NS 4
 #define E4CTAS 3
-#define E4NS2 6
+#define E4NS2 4
 #define E4CTAS2 2
 #endif
 constexpr int kE4MaxPages = 512;                    // block-table entries a CTA caches
@@ -264,11 +264,15 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, con
 {
     const int g4 = lane >> 2, t4 = lane & 3;
     uint4 bl[2], bh[2];
+    const uint32_t at = smem_addr(rows) + swz128(g4, 2 * t4) + warp * 1024;   // eight rows a kilobyte
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const int r = 8 * (warp + kConsumerWarps * u) + g4;
-        bl[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4));
-        bh[u] = *reinterpret_cast<const uint4*>(rows + swz128(r, 2 * t4 + 1));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(bl[u].x), "=r"(bl[u].y), "=r"(bl[u].z), "=r"(bl[u].w)
+                     : "r"(at + 4096 * u));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(bh[u].x), "=r"(bh[u].y), "=r"(bh[u].z), "=r"(bh[u].w)
+                     : "r"((at ^ 16u) + 4096 * u));
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -286,14 +290,29 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, con
         mma_bf16_16816(c[0], qa[3], bh[0].z, bh[0].w);
         mma_bf16_16816(c[1], qa[3], bh[1].z, bh[1].w);
         if (mt == 0) mbar_arrive_release(release_bar);   // the rel rows are in registers
+        // only the window's last slot can run over its end
+        const int x = (col0 & (kTableW - 1)) + 8 * warp + 2 * t4 + 16 * mt + g4 + 1;
+        const uint32_t w[4] = {pack_bf16(c[0][0], c[0][1]), pack_bf16(c[0][2], c[0][3]), pack_bf16(c[1][0], c[1][1]),
+                               pack_bf16(c[1][2], c[1][3])};
+        if ((col0 & (kTableW - 1)) != kTableW - kStageKeys) {
+            uint16_t* d = r0 + x;
+            d[0] = static_cast<uint16_t>(w[0]);
+            d[1] = static_cast<uint16_t>(w[0] >> 16);
+            d[8 * kTableStride + 8] = static_cast<uint16_t>(w[1]);
+            d[8 * kTableStride + 9] = static_cast<uint16_t>(w[1] >> 16);
+            d[32] = static_cast<uint16_t>(w[2]);
+            d[33] = static_cast<uint16_t>(w[2] >> 16);
+            d[8 * kTableStride + 40] = static_cast<uint16_t>(w[3]);
+            d[8 * kTableStride + 41] = static_cast<uint16_t>(w[3] >> 16);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int x = col0 + 8 * (warp + kConsumerWarps * u) + 2 * t4 + 16 * mt + g4 + 1;
-            const uint32_t w0 = pack_bf16(c[u][0], c[u][1]), w1 = pack_bf16(c[u][2], c[u][3]);
-            r0[x & (kTableW - 1)] = static_cast<uint16_t>(w0);
-            r0[(x + 1) & (kTableW - 1)] = static_cast<uint16_t>(w0 >> 16);
-            r1[(x + 8) & (kTableW - 1)] = static_cast<uint16_t>(w1);
-            r1[(x + 9) & (kTableW - 1)] = static_cast<uint16_t>(w1 >> 16);
+            for (int u = 0; u < 2; ++u) {
+                const int y = x + 8 * kConsumerWarps * u;
+                r0[y & (kTableW - 1)] = static_cast<uint16_t>(w[2 * u]);
+                r0[(y + 1) & (kTableW - 1)] = static_cast<uint16_t>(w[2 * u] >> 16);
+                r1[(y + 8) & (kTableW - 1)] = static_cast<uint16_t>(w[2 * u + 1]);
+                r1[(y + 9) & (kTableW - 1)] = static_cast<uint16_t>(w[2 * u + 1] >> 16);
+            }
         }
     }
 }
@@ -681,14 +700,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 __syncwarp();
                 if (q < nbox) {
                     const int in_page = j & (bs - 1);
-                    const long long page = static_cast<long long>(valid ? blk : 0) * H + h;
-                    // an invalid block's box lies outside the pool and reads zeros
-                    const int line = valid ? static_cast<int>((page * bs + in_page) >> 1) : -2 * box;
+                    // rows of the pools are below 2^31; an invalid block's box lies outside and reads zeros
+                    const int row = valid ? (((blk * H + h) << sh) + in_page) : -4 * box;
+                    const int line = row >> 1;
                     const uint32_t dst = sb + slot * kE4Stage + q * box * kE4Row;
                     if (lane < 16) {
                         tma_load_2d_hint(dst, &tm_k, bar, 0, line, pol);
                         if (valid) {
-                            const uint8_t* src = a.kv_scale + 2 * page * bs + in_page;
+                            const uint8_t* src = a.kv_scale + 2 * static_cast<long long>(row - in_page) + in_page;
                             if (bs <= kStageKeys) {
                                 bulk_load(sb + sc_dst, src, 2 * box, bar);   // K and V scales of the page are adjacent
                             } else {
