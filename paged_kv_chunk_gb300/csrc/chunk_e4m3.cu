@@ -47,6 +47,7 @@ constexpr int kChunkRows = 16;                      // rows of the chunk region 
 constexpr int kE4Consumers = 32 * kConsumerWarps;
 constexpr int kTableW = 256;                        // columns of the position table's window
 constexpr int kTableStride = kTableW + 16;          // 8 mod 32 words: 8-byte reads without conflicts
+constexpr int kOrderMax = 512;                      // streams of a cohort whose items are sorted by length
 constexpr int kMaxRowExp = 120;
 constexpr float kNoMax = -3.0e38f;                  // the running maximum before any key
 
@@ -62,6 +63,7 @@ struct E4Args {
     unsigned* status;
     int num_blocks, block_size, bs_shift, mbps, T, H, R;
     int items;        // (stream, head, query tile)
+    int B, sorted;    // sorted: items of unequal streams go to the CTAs longest first
     int q_tiles, splits;
     float scale, scale_log2;   // the latter times log2(e)
 };
@@ -86,7 +88,8 @@ struct E4Smem {
     static constexpr int off_re = off_csc + 2 * kChunkRows;           // 2^x of the query rows
     static constexpr int off_item = off_re + Tp * 4;                  // cache length of the item, two of them; failed
     static constexpr int off_bar = off_item + 16;                     // full[NS], empty[NS], q full, q free
-    static constexpr int off_bt = off_bar + (2 * NS + 2) * 8;         // block-table row, two of them
+    static constexpr int off_order = off_bar + (2 * NS + 2) * 8;      // streams by length (16 bits each)
+    static constexpr int off_bt = off_order + 2 * kOrderMax;          // block-table row, two of them
     static constexpr int bytes = off_bt;                              // + 2 * mbps * 4
     // clusters (one item each): the CTA's share, in the ring's memory
     static constexpr int part_o = 0;
@@ -570,7 +573,32 @@ __device__ __forceinline__ E4Item e4_item(const E4Args& a, int C, int split)
     return t;
 }
 
-// Persistent: CTA x takes items x, x + grid, ...  The producer warp runs ahead of the consumers by the
+// The items of CTA x in turn: x, grid + x, ... of the items in order, or, with the streams sorted by
+// length, alternately from both ends of each round of `grid` items (longest first: every CTA gets about the
+// same number of keys; streams of 0 to 1024 keys, seven items a CTA: 144 -> 124 us).
+struct E4Walk {
+    int items, grid, x, round;
+    const uint16_t* order;   // streams by length, or null
+
+    __device__ __forceinline__ int at(int r) const { return order && (r & 1) ? (r + 1) * grid - 1 - x : r * grid + x; }
+    // the round of the first item from round r on (a reversed last round may leave a CTA out), or -1
+    __device__ __forceinline__ int from(int r) const
+    {
+        for (; r * static_cast<long long>(grid) < items; ++r)
+            if (at(r) < items) return r;
+        return -1;
+    }
+    __device__ __forceinline__ void decode(int r, int H, int q_tiles, int& b, int& h, int& qt) const
+    {
+        const int i = at(r), bh = i / q_tiles;
+        qt = i - bh * q_tiles;
+        b = bh / H;
+        h = bh - b * H;
+        if (order) b = order[b];
+    }
+};
+
+// Persistent: CTA x takes the items of its E4Walk.  The producer warp runs ahead of the consumers by the
 // ring's slots, across items, so the next item's rows arrive while this one's are multiplied and joined.
 // Ring order of an item with stages s = 0, 1, ..: rel slots 0 and 1, stage 0, rel slot 2, stage 1, ...
 // (stage s needs the table's columns up to rel slot s + 1).
@@ -587,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     const uint32_t sb = smem_addr(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.splits, T = a.T, H = a.H, sh = a.bs_shift, bs = a.block_size;
-    const int split = blockIdx.x % S, first = blockIdx.x / S, step = gridDim.x / S;
+    const int split = blockIdx.x % S;
     const uint32_t bar_full = sb + SP::off_bar;
     const uint32_t bar_empty = bar_full + NS * 8;
     const uint32_t bar_q = bar_empty + NS * 8;    // an item's q, chunk rows, cache length and block-table row are in
@@ -616,6 +644,29 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     __syncthreads();
     grid_dep_wait();   // the previous grid on the stream has finished (programmatic launch)
 
+    E4Walk walk = {a.items, static_cast<int>(gridDim.x) / S, static_cast<int>(blockIdx.x) / S, 0, nullptr};
+    if (a.sorted) {
+        // streams by length, longest first: each counts the longer ones (and, of its own length, the earlier)
+        int* len = reinterpret_cast<int*>(sm + SP::off_gt);
+        uint16_t* order = reinterpret_cast<uint16_t*>(sm + SP::off_order);
+        const int len0 = __ldg(a.cache_seqlens);
+        int differ = 0;
+        for (int i = tid; i < a.B; i += kThreads) {
+            len[i] = __ldg(a.cache_seqlens + i);
+            differ |= len[i] != len0;
+        }
+        if (__syncthreads_or(differ)) {
+            for (int i = tid; i < a.B; i += kThreads) {
+                const int mine = len[i];
+                int rank = 0;
+                for (int j = 0; j < a.B; ++j) rank += len[j] > mine || (len[j] == mine && j < i);
+                order[rank] = static_cast<uint16_t>(i);
+            }
+            walk.order = order;
+        }
+        __syncthreads();
+    }
+
     if (warp == kConsumerWarps) {
         // ------------------------------------------------------------ producer
         const uint64_t pol = policy_evict_first();
@@ -629,17 +680,20 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         };
         constexpr int kRowRegs = 4;   // entries of a lane loaded ahead (128 pages); the rest of a longer row later
         int C = 0, row[kRowRegs];
-        auto request = [&](int item) {
-            const int b = item / (H * a.q_tiles);
+        auto request = [&](int r) {
+            int b, h, qt;
+            walk.decode(r, H, a.q_tiles, b, h, qt);
             C = __ldg(a.cache_seqlens + b);
 #pragma unroll
             for (int k = 0; k < kRowRegs; ++k)
                 if (lane + 32 * k < a.mbps) row[k] = __ldg(a.block_table + static_cast<long long>(b) * a.mbps + lane + 32 * k);
         };
-        if (first < a.items) request(first);
-        for (int item = first; item < a.items && ok; item += step, ++n_items) {
-            const int qt = item % a.q_tiles, bh = item / a.q_tiles;
-            const int b = bh / H, h = bh - b * H, i0 = qt * Tp;
+        int next = walk.from(0);
+        if (next >= 0) request(next);
+        for (int round = next; round >= 0 && ok; round = next, ++n_items) {
+            int b, h, qt;
+            walk.decode(round, H, a.q_tiles, b, h, qt);
+            const int i0 = qt * Tp;
             // the item's cache length and block-table row, into the buffers of the item before last
             if (n_items >= 1) {
                 ok = __all_sync(0xffffffffu, e4_wait(bar_qfree, (n_items - 1) & 1));
@@ -662,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                     tma_load_3d(sb + SP::off_cn + kChunkRows * kRowBytes, &tm_vn, bar_q, 0, h, b * T);
                 }
             }
-            if (item + step < a.items) request(item + step);
+            next = walk.from(round + 1);
+            if (next >= 0) request(next);
             auto issue_rel = [&](int r) {
                 if (!acquire()) return;
                 if (lane == 0) {
@@ -750,9 +805,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
     bool failed = false;
     int it = 0, n_items = 0;   // ring slots read, items begun
 #pragma unroll 1
-    for (int item = first; item < a.items; item += step, ++n_items) {
-        const int qt = item % a.q_tiles, bh = item / a.q_tiles;
-        const int b = bh / H, h = bh - b * H, i0 = qt * Tp;
+    for (int round = walk.from(0), next; round >= 0; round = next, ++n_items) {
+        next = walk.from(round + 1);
+        int b, h, qt;
+        walk.decode(round, H, a.q_tiles, b, h, qt);
+        const int i0 = qt * Tp;
         if (!failed && !e4_wait(bar_q, n_items & 1)) failed = true;
         const E4Item t = e4_item<MT, FUSED>(a, failed ? 0 : s_len[n_items & 1], split);
         err |= t.err;
@@ -896,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             __syncwarp();
             put(warp);
         }
-        if (item + step >= a.items) grid_dep_trigger();   // the next grid may schedule (it waits for this one)
+        if (next < 0) grid_dep_trigger();   // the next grid may schedule (it waits for this one)
         named_bar_sync(1, kE4Consumers);
         if (s_failed) {
             failed = true;
@@ -1278,8 +1335,10 @@ oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const
     const long long pairs = e4_splits(a, B, SP::Tp, k_max);
     if (pairs > 0x7fffffffLL / 2) return OASR_ERR_UNSUPPORTED;
     a.items = static_cast<int>(pairs);
+    a.B = B;
     const long long most = static_cast<long long>(CTAS) * sm_count();
     const long long ctas = a.splits > 1 ? pairs * a.splits : pairs < most ? pairs : most;
+    a.sorted = a.splits == 1 && pairs > ctas && B <= kOrderMax;
     return launch_e4_cluster(kern, ctas, kThreads, smem, a.splits, stream, tm_q, tm_k, tm_v, tm_r, tm_kn, tm_vn,
                              static_cast<const E4Args>(a));
 }

@@ -271,6 +271,27 @@ def test_attention_bf16(B, H, T, Cs, bs, fused):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("B,H,T,mode", [(300, 2, 3, "uneven"), (300, 2, 16, "even"), (110, 2, 40, "uneven"),
+                                        (90, 3, 64, "even"), (600, 1, 2, "uneven"), (250, 2, 1, "one long")])
+def test_many_items_per_cta(B, H, T, mode, fused):
+    """More (stream, head, query tile) items than the GPU holds at once, in streams of equal and of
+    unequal lengths (which are handed out longest first up to 512 streams)."""
+    g = torch.Generator().manual_seed(B + T)
+    Cs = [23] * B if mode == "even" else torch.randint(0, 90, (B,), generator=g).tolist()
+    if mode == "one long":
+        Cs = [3] * B
+        Cs[77] = 900
+    c, x, lens = make(B, H, T, Cs, 16, "bf16", B * T)
+    capi.oasr_device_status()
+    out, pools = step(c, x, lens, fused=fused)
+    assert capi.oasr_device_status() == 0
+    c.append(x["k_new"], x["v_new"], lens)
+    assert c.same(*pools[:3])
+    check(c, x, lens, out, "bf16", streams=range(B) if T < 16 else list(range(0, B, 7)) + [B - 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fused", [True, False])
 @pytest.mark.parametrize("B,H,T,Cs,bs", SHAPES[:12] + [(1, 1, 1, [700], 16)])
 def test_attention_f32(B, H, T, Cs, bs, fused):
     c, x, lens = make(B, H, T, Cs, bs, "f32", 200 + T)
