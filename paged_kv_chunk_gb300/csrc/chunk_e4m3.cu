@@ -533,12 +533,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
 // maximum of its own.  out = sum(o 2^(m - m*)) 2^(m* - lambda*) / sum(2^(lambda - lambda*)).
 __device__ __forceinline__ float part_weight(float x, float top) { return x <= kNoMax ? 0.f : ex2_approx(x - top); }
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
 // What a CTA does with one item: keys, ring slots and the position table, from the stream's cache length.
 struct E4Item {
     int C, K;          // cached frames; keys (frames and chunk, as far as the table reaches)
@@ -1291,29 +1285,6 @@ long long e4_splits(E4Args& a, int B, int Tp, int k_max)
     return pairs;
 }
 
-// Launch with programmatic stream serialization (host_common.h) and clusters of `splits` CTAs.
-template <typename... KArgs, typename... Args>
-oasr_status launch_e4_cluster(void (*kern)(KArgs...), long long ctas, int threads, int smem, int splits,
-                              cudaStream_t stream, Args&&... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...) != cudaSuccess) return OASR_ERR_CUDA;
-    return launch_status();
-}
-
 template <int MT, int NS, int CTAS, bool FUSED>
 oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const void* rel, E4Args& a, int k_max, int B,
                       int slot, cudaStream_t stream)
@@ -1339,8 +1310,8 @@ oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const
     const long long most = static_cast<long long>(CTAS) * sm_count();
     const long long ctas = a.splits > 1 ? pairs * a.splits : pairs < most ? pairs : most;
     a.sorted = a.splits == 1 && pairs > ctas && B <= kOrderMax;
-    return launch_e4_cluster(kern, ctas, kThreads, smem, a.splits, stream, tm_q, tm_k, tm_v, tm_r, tm_kn, tm_vn,
-                             static_cast<const E4Args>(a));
+    return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, a.splits, stream, tm_q, tm_k, tm_v,
+                              tm_r, tm_kn, tm_vn, static_cast<const E4Args>(a));
 }
 
 template <bool FUSED>
@@ -1402,8 +1373,8 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
         if (!ensure_smem(chunk_e4m3_f32_kernel, sizeof(F32Smem), g_smem_done_e4[3]) ||
             !ensure_clusters(chunk_e4m3_f32_kernel, g_clusters_e4[3]))
             return OASR_ERR_CUDA;
-        return launch_e4_cluster(chunk_e4m3_f32_kernel, pairs * a.splits, kFThreads, static_cast<int>(sizeof(F32Smem)), a.splits,
-                                 stream, static_cast<const float*>(q), static_cast<const uint8_t*>(a.k_pool),
+        return launch_pdl_cluster(chunk_e4m3_f32_kernel, dim3(static_cast<unsigned>(pairs * a.splits)), dim3(kFThreads),
+                                  static_cast<int>(sizeof(F32Smem)), a.splits, stream, static_cast<const float*>(q), static_cast<const uint8_t*>(a.k_pool),
                                  static_cast<const uint8_t*>(a.v_pool), static_cast<const uint8_t*>(a.kv_scale),
                                  static_cast<const float*>(u), static_cast<const float*>(vb), static_cast<const float*>(rel),
                                  static_cast<float*>(out), static_cast<const E4Args>(a));

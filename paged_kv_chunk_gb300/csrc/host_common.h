@@ -66,6 +66,30 @@ oasr_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, int smem
     return launch_status();
 }
 
+// The same with clusters of `ctas` CTAs (the grid's x a multiple of it).
+template <typename... KArgs, typename... Args>
+oasr_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int smem, int ctas,
+                               cudaStream_t stream, Args&&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...) != cudaSuccess)
+        return OASR_ERR_CUDA;
+    return launch_status();
+}
+
 // Raise the dynamic shared-memory limit of `func` once per device.
 template <typename F>
 bool ensure_smem(F* func, int bytes, int (&done)[64])

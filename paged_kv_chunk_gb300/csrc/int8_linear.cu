@@ -142,17 +142,17 @@ constexpr int kI8EpiWarps = 8, kI8Group = 256, kI8Groups = 2;
 constexpr int kI8Conv0 = 32 * kI8EpiWarps;                        // first converter thread
 constexpr int kI8Issuer = kI8EpiWarps + kI8Groups * kI8Group / 32;   // its warp; the producer's is the next
 constexpr int kI8Threads = 32 * (kI8Issuer + 2);
-constexpr int kI8OutStride = 20;   // floats of a row of an epilogue warp's staging tile (32 x 16)
 
-template <int BN>
+template <int BN, bool PAIR>
 struct I8Smem {
-    static constexpr int rows = 128 + BN;                              // x rows, then w rows
+    static constexpr int b_rows = PAIR ? BN / 2 : BN;                  // of a tile's w rows, the CTA's
+    static constexpr int rows = 128 + b_rows;                          // x rows, then w rows
     static constexpr int tile_a = 128 * 128, tile = rows * 128;        // fp16, 64 of K
     static constexpr int raw = rows * 64;                              // 8-bit, 64 of K
-    static constexpr int stages = BN == 256 ? 2 : 4, raws = 4;
+    static constexpr int stages = 4, raws = 4;
     static constexpr int off_raw = stages * tile;
-    static constexpr int off_out = off_raw + raws * raw;               // [8 warps][32][kI8OutStride] floats
-    static constexpr int off_ws = off_out + kI8EpiWarps * 32 * kI8OutStride * 4;   // [8 warps][2][BN / 2] floats
+    static constexpr int off_out = off_raw + raws * raw;               // [8 warps][32][16] floats
+    static constexpr int off_ws = off_out + kI8EpiWarps * 32 * 16 * 4;   // [8 warps][2][BN / 2] floats
     static constexpr int off_bar = off_ws + kI8EpiWarps * BN * 4;      // full, empty, raw full, raw empty, acc full[2], acc free[2], drain
     static constexpr int off_misc = off_bar + (2 * stages + 2 * raws + 5) * 8;
     static constexpr int bytes = off_misc + 16 + 1024;
@@ -167,12 +167,13 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-template <int BN, typename Elem>
+template <int BN, bool PAIR, typename Elem>
 __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
     const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_w0,
     const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_w1, const I8Args a)
 {
-    using SP = I8Smem<BN>;
+    using SP = I8Smem<BN, PAIR>;
+    constexpr int CTAS = PAIR ? 2 : 1;
     constexpr int S = SP::stages, R = SP::raws;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -185,18 +186,19 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
     const uint32_t bar_acc_full = bar_raw_free + 8 * R, bar_acc_free = bar_acc_full + 16;
     const uint32_t bar_drain = bar_acc_free + 16;
     const int ksteps = (a.K + 63) / 64;
+    const int rank = PAIR ? blockIdx.x & 1 : 0;   // in the pair; 0 issues the products of both
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(bar_full + 8 * i, kI8Group);
+            mbar_init(bar_full + 8 * i, kI8Group / 32 + (PAIR && rank == 0));
             mbar_init(bar_empty + 8 * i, 1);
         }
         for (int i = 0; i < R; ++i) {
             mbar_init(bar_raw + 8 * i, 1);
-            mbar_init(bar_raw_free + 8 * i, kI8Group);
+            mbar_init(bar_raw_free + 8 * i, kI8Group / 32);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_acc_full + 8 * i, 1);
-            mbar_init(bar_acc_free + 8 * i, kI8EpiWarps);
+            mbar_init(bar_acc_free + 8 * i, CTAS * kI8EpiWarps);
         }
         mbar_init(bar_drain, 1);
         fence_mbar_init();
@@ -209,12 +211,21 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         prefetch_tensormap(&tm_w1);
     }
     if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)),
-                     "r"(SP::cols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)),
+                         "r"(SP::cols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)),
+                         "r"(SP::cols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     grid_dep_wait();
@@ -226,7 +237,9 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         mt = t / n;
         nt = t - mt * n;
     };
-    const int my_tiles = static_cast<int>(blockIdx.x) < a.tiles ? (a.tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    // tiles first, first + stride, ... are the CTA's (the pair's)
+    const int first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
+    const int my_tiles = first < a.tiles ? (a.tiles - 1 - first) / stride + 1 : 0;
     const int iters = my_tiles * ksteps;
 
     if (warp == kI8Issuer + 1) {
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
             bool ok = true;
             for (int lt = 0; lt < my_tiles && ok; ++lt) {
                 int g, mt, nt;
-                decode(blockIdx.x + lt * gridDim.x, g, mt, nt);
+                decode(first + lt * stride, g, mt, nt);
                 for (int kb = 0; kb < ksteps; ++kb, ++i) {
                     const int slot = i % R;
                     if (i >= R && !wait_or_abort(bar_raw_free + 8 * slot, ((i / R) - 1) & 1, s_abort)) {
@@ -246,8 +259,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
                     // rows past M or N and bytes past K come as zeros
                     const uint32_t dst = sb + SP::off_raw + slot * SP::raw, bar = bar_raw + 8 * slot;
                     mbar_arrive_expect_tx(bar, SP::raw);
-                    tma_load_2d(dst, g ? &tm_x1 : &tm_x0, bar, 64 * kb, mt * 128);
-                    tma_load_2d(dst + 128 * 64, g ? &tm_w1 : &tm_w0, bar, 64 * kb, nt * BN);
+                    tma_load_2d(dst, g ? &tm_x1 : &tm_x0, bar, 64 * kb, (mt * CTAS + rank) * 128);
+                    tma_load_2d(dst + 128 * 64, g ? &tm_w1 : &tm_w0, bar, 64 * kb, nt * BN + rank * SP::b_rows);
                 }
             }
             // no copy may still be landing when the CTA exits
@@ -256,35 +269,56 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         }
     } else if (warp == kI8Issuer) {
         // ------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
+        if (lane == 0 && rank) {
+            // passes on to the other CTA that this one's rows of a slot are written
+            for (int i = 0; i < iters; ++i) {
+                if (!wait_or_abort(bar_full + 8 * (i % S), (i / S) & 1, s_abort)) break;
+                fence_release_smem_cluster();
+                mbar_arrive_cluster_relaxed(bar_full + 8 * (i % S), 0);
+            }
+            // the other's commits have landed before this CTA ends
+            for (int u = iters - S; u < iters; ++u)
+                if (u >= 0 && !wait_or_abort(bar_empty + 8 * (u % S), (u / S) & 1, s_abort)) break;
+            if (!mbar_wait(bar_drain, 0)) *s_abort = 1;
+        } else if (lane == 0) {
             // fp16 A and B, fp32 D
-            constexpr uint32_t id = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | ((128u >> 4) << 24);
+            constexpr uint32_t id = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | ((CTAS * 128u >> 4) << 24);
+            auto commit = [](uint32_t bar) {
+                if constexpr (PAIR)
+                    umma_commit_pair(bar);
+                else
+                    umma_commit(bar);
+            };
             int i = 0, nacc = 0, nfree = 0;
             bool ok = true;
             for (int lt = 0; lt < my_tiles && ok; ++lt) {
                 const int buf = lt & 1;
-                if (lt >= 2 && !wait_or_abort(bar_acc_free + 8 * buf, ((lt >> 1) - 1) & 1, s_abort)) break;
+                if (lt >= 2 && !wait_or_abort<PAIR>(bar_acc_free + 8 * buf, ((lt >> 1) - 1) & 1, s_abort)) break;
                 for (int kb = 0; kb < ksteps; ++kb, ++i) {
                     const int slot = i % S;
-                    if (!wait_or_abort(bar_full + 8 * slot, (i / S) & 1, s_abort)) {
+                    if (!wait_or_abort<PAIR>(bar_full + 8 * slot, (i / S) & 1, s_abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t base = sb + slot * SP::tile;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_ss(tmem + buf * BN, sdesc(base + 32 * k), sdesc(base + SP::tile_a + 32 * k), id,
-                                (kb > 0 || k > 0) ? 1 : 0);
-                    umma_commit(bar_empty + 8 * slot);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t da = sdesc(base + 32 * k), db = sdesc(base + SP::tile_a + 32 * k);
+                        if constexpr (PAIR)
+                            umma_ss_pair(tmem + buf * BN, da, db, id, kb > 0 || k > 0);
+                        else
+                            umma_ss(tmem + buf * BN, da, db, id, kb > 0 || k > 0);
+                    }
+                    commit(bar_empty + 8 * slot);
                     ++nfree;
                 }
                 if (!ok) break;
-                umma_commit(bar_acc_full + 8 * buf);
+                commit(bar_acc_full + 8 * buf);
                 ++nacc;
             }
             // drain: every MMA issued has finished and every arrival it owes has landed
-            umma_commit(bar_drain);
+            commit(bar_drain);
             bool drained = mbar_wait(bar_drain, 0);
             for (int u = nacc - 2; u < nacc; ++u)
                 if (u >= 0) drained = mbar_wait(bar_acc_full + 8 * (u & 1), (u >> 1) & 1) && drained;
@@ -299,13 +333,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         const int grp = (tid - kI8Conv0) / kI8Group, ct = (tid - kI8Conv0) % kI8Group, c = ct & 3, r0 = ct >> 2;
         for (int i = grp; i < iters; i += kI8Groups) {
             const int rs = i % R, slot = i % S;
-            if (!wait_or_abort(bar_raw + 8 * rs, (i / R) & 1, s_abort)) break;
+            if (!__all_sync(0xffffffffu, wait_or_abort(bar_raw + 8 * rs, (i / R) & 1, s_abort))) break;
             const uint8_t* src = sm + SP::off_raw + rs * SP::raw + 16 * ct;
             uint4 buf[NU];
 #pragma unroll
             for (int u = 0; u < NU; ++u)
                 if (r0 + 64 * u < SP::rows) buf[u] = *reinterpret_cast<const uint4*>(src + 4096 * u);
-            if (i >= S && !wait_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort)) break;
+            if (i >= S && !__all_sync(0xffffffffu, wait_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort))) break;
             uint8_t* lo = sm + slot * SP::tile + swz128(r0, 2 * c);
             uint8_t* hi = sm + slot * SP::tile + swz128(r0, 2 * c + 1);
 #pragma unroll
@@ -315,100 +349,130 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
                     *reinterpret_cast<uint4*>(hi + 8192 * u) = i8_to_f16(buf[u].z, buf[u].w);
                 }
             fence_proxy_async_smem();
-            mbar_arrive_release(bar_full + 8 * slot);
+            __syncwarp();
             // the raw slot is released only here, its words converted: an arrival right behind the loads can
             // overtake them (they wait in another unit's queue), and a copy then lands under them
-            mbar_arrive_release(bar_raw_free + 8 * rs);
+            if (lane == 0) {
+                mbar_arrive_release(bar_full + 8 * slot);
+                mbar_arrive_release(bar_raw_free + 8 * rs);
+            }
         }
     } else {
         // --------------------------------------------------------------- epilogue
-        // warp: 32 rows (its TMEM lanes, warp % 4) of one half of the tile's columns (warp / 4)
-        constexpr int HN = BN / 2;
+        // warp: 32 rows (its TMEM lanes, warp % 4) of one half of the tile's columns (warp / 4), 16 columns at a
+        // time, the next 16 on their way from TMEM meanwhile
+        constexpr int HN = BN / 2, NC = HN / 16;
         const int rq = warp & 3, half = warp >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * rq) << 16) + half * HN;
         float* s_ws = reinterpret_cast<float*>(sm + SP::off_ws) + warp * BN;   // w scales, then biases
-        float* s_out = reinterpret_cast<float*>(sm + SP::off_out) + warp * 32 * kI8OutStride;
+        float* s_out = reinterpret_cast<float*>(sm + SP::off_out) + warp * 32 * 16;
         for (int lt = 0; lt < my_tiles; ++lt) {
             int g, mt, nt;
-            decode(blockIdx.x + lt * gridDim.x, g, mt, nt);
+            decode(first + lt * stride, g, mt, nt);
             const I8Problem& p = a.p[g];
-            const int buf = lt & 1;
+            const int M = p.M, N = p.N, buf = lt & 1;
             const Elem* bias = static_cast<const Elem*>(p.bias);
-            const int row0 = mt * 128 + 32 * rq, col0 = nt * BN + half * HN;
+            const int row0 = (mt * CTAS + rank) * 128 + 32 * rq, col0 = nt * BN + half * HN;
             __syncwarp();
+#pragma unroll
             for (int j = lane; j < HN; j += 32) {
                 const int n = col0 + j;
-                s_ws[j] = n < p.N ? __ldg(p.ws + n) : 0.f;
-                s_ws[HN + j] = bias && n < p.N ? bias_at(bias, n) : 0.f;
+                s_ws[j] = n < N ? __ldg(p.ws + n) : 0.f;
+                s_ws[HN + j] = bias && n < N ? bias_at(bias, n) : 0.f;
             }
-            const float xs = row0 + lane < p.M ? __ldg(p.xs + row0 + lane) : 0.f;
+            const float x = row0 + lane < M ? __ldg(p.xs + row0 + lane) : 0.f;
             __syncwarp();
             if (!__all_sync(0xffffffffu, wait_or_abort(bar_acc_full + 8 * buf, (lt >> 1) & 1, s_abort))) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < HN / 16; ++c) {
-                const int col = col0 + 16 * c;
-                if (col >= p.N) break;
-                uint32_t r[16];
-                OASR_TMEM_LD16(tl + buf * BN + 16 * c, r);
-                tmem_wait_ld();
-                // thread = row: scaled, into the staging tile
+            // the output of the block's columns (a block of 16 lies within one: widths are multiples of 64, or
+            // there is one) and the block's first column there
+            const int width = g ? N : a.width;
+            int which = g ? 3 : col0 / width, at = g ? col0 : col0 - which * width;
+            uint32_t r[2][16];
+            OASR_TMEM_LD16(tl + buf * BN, r[0]);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 w4 = *reinterpret_cast<const float4*>(s_ws + 16 * c + j);
-                    const float4 b4 = *reinterpret_cast<const float4*>(s_ws + HN + 16 * c + j);
-                    float4 v;
-                    v.x = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j]), xs), w4.x), b4.x);
-                    v.y = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j + 1]), xs), w4.y), b4.y);
-                    v.z = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j + 2]), xs), w4.z), b4.z);
-                    v.w = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(r[j + 3]), xs), w4.w), b4.w);
-                    *reinterpret_cast<float4*>(s_out + lane * kI8OutStride + j) = v;
+            for (int c = 0; c < NC; ++c) {
+                const int col = col0 + 16 * c;
+                if (col >= N) break;
+                tmem_wait_ld();
+                if (c + 1 < NC) OASR_TMEM_LD16(tl + buf * BN + 16 * (c + 1), r[(c + 1) & 1]);
+                // thread = row: times the row's scale, into the staging tile (16-byte chunks exchanged by row, so
+                // that neither side has bank conflicts)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t* s4 = r[c & 1] + 4 * j;
+                    *reinterpret_cast<float4*>(s_out + 16 * lane + 4 * (j ^ ((lane >> 1) & 3))) =
+                        make_float4(__fmul_rn(__uint_as_float(s4[0]), x), __fmul_rn(__uint_as_float(s4[1]), x),
+                                    __fmul_rn(__uint_as_float(s4[2]), x), __fmul_rn(__uint_as_float(s4[3]), x));
                 }
                 __syncwarp();
-                // rows from there in whole 64- or 32-byte runs.  A block of 16 columns lies within one
-                // output (widths are multiples of 64, or there is one output).
-                const int which = g ? 3 : col / a.width;
-                const int width = g ? p.N : a.width;
                 void* ob = which == 0 ? a.out[0] : which == 1 ? a.out[1] : which == 2 ? a.out[2] : a.out[3];
-                Elem* dst = static_cast<Elem*>(ob) + (col - (g ? 0 : which * a.width));
-                if (col + 16 <= p.N && (width & 7) == 0) {
+                Elem* dst = static_cast<Elem*>(ob) + static_cast<long long>(row0) * width + at;
+                auto finish = [&](int row, int j4) {   // four columns' values
+                    const float4 v = *reinterpret_cast<const float4*>(s_out + 16 * row + 4 * (j4 ^ ((row >> 1) & 3)));
+                    const float4 w = *reinterpret_cast<const float4*>(s_ws + 16 * c + 4 * j4);
+                    const float4 b = *reinterpret_cast<const float4*>(s_ws + HN + 16 * c + 4 * j4);
+                    return make_float4(__fadd_rn(__fmul_rn(v.x, w.x), b.x), __fadd_rn(__fmul_rn(v.y, w.y), b.y),
+                                       __fadd_rn(__fmul_rn(v.z, w.z), b.z), __fadd_rn(__fmul_rn(v.w, w.w), b.w));
+                };
+                if (col + 16 <= N && (width & 7) == 0) {
+                    // rows in runs of 64 or 32 bytes, 16 bytes a lane
                     constexpr int V = 16 / sizeof(Elem), L = 16 / V;   // values of a store, lanes of a row
+                    const int j = lane % L;
 #pragma unroll
                     for (int i = 0; i < 32; i += 32 / L) {
-                        const int rr = i + lane / L, j = (lane % L) * V;
-                        if (row0 + rr < p.M) {
-                            const float* v = s_out + rr * kI8OutStride + j;
-                            Elem* to = dst + static_cast<long long>(row0 + rr) * width + j;
-                            const float4 v0 = *reinterpret_cast<const float4*>(v);
-                            if constexpr (sizeof(Elem) == 2) {
-                                const float4 v1 = *reinterpret_cast<const float4*>(v + 4);
+                        const int row = i + lane / L;
+                        const float4 v0 = finish(row, j * V / 4);
+                        Elem* to = dst + static_cast<long long>(row) * width + j * V;
+                        if constexpr (sizeof(Elem) == 2) {
+                            const float4 v1 = finish(row, j * V / 4 + 1);
+                            if (row0 + row < M)
                                 *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(v0.x, v0.y), pack_bf16(v0.z, v0.w),
                                                                            pack_bf16(v1.x, v1.y), pack_bf16(v1.z, v1.w));
-                            } else {
-                                *reinterpret_cast<float4*>(to) = v0;
-                            }
+                        } else if (row0 + row < M) {
+                            *reinterpret_cast<float4*>(to) = v0;
                         }
                     }
                 } else {
-                    for (int e = lane; e < 512; e += 32) {
-                        const int rr = e >> 4, j = e & 15;
-                        if (row0 + rr < p.M && col + j < p.N)
-                            put(dst + static_cast<long long>(row0 + rr) * width + j, s_out[rr * kI8OutStride + j]);
+                    const int j = lane & 3;
+                    for (int row = lane >> 2; row < 32; row += 8) {
+                        const float4 v = finish(row, j);
+                        const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (row0 + row < M && col + 4 * j + k < N)
+                                put(dst + static_cast<long long>(row) * width + 4 * j + k, e[k]);
                     }
+                }
+                if ((at += 16) == width && !g) {
+                    at = 0;
+                    ++which;
                 }
                 __syncwarp();
             }
+            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_acc_free + 8 * buf);
+            if (lane == 0) {
+                if constexpr (PAIR)
+                    mbar_arrive_cluster_relaxed(bar_acc_free + 8 * buf, 0);   // nothing but the accumulators passes on
+                else
+                    mbar_arrive(bar_acc_free + 8 * buf);
+            }
         }
     }
     grid_dep_trigger();
     tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SP::cols));
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SP::cols));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SP::cols));
     }
     if (tid == 0 && *s_abort) atomicOr(a.status, kErrTimeout);
 }
@@ -456,53 +520,65 @@ __global__ void __launch_bounds__(256) linear_i8_few_kernel(const I8Problem p, E
 
 int g_smem_done_i8[8][64];
 
-template <int BN, typename Elem>
+template <int BN, bool PAIR, typename Elem>
 oasr_status launch_i8(I8Args a, int slot, int sms, cudaStream_t stream)
 {
-    auto tiles_of = [](const I8Problem& p) { return static_cast<long long>((p.M + 127LL) / 128) * ((p.N + BN - 1) / BN); };
+    using SP = I8Smem<BN, PAIR>;
+    constexpr int MT = PAIR ? 256 : 128;
+    auto tiles_of = [](const I8Problem& p) { return static_cast<long long>((p.M + MT - 1LL) / MT) * ((p.N + BN - 1) / BN); };
     const long long t0 = tiles_of(a.p[0]), t1 = a.p[1].M ? tiles_of(a.p[1]) : 0;
     if (t0 + t1 > 0x7fffffffLL - sms) return OASR_ERR_UNSUPPORTED;
     a.nt0 = (a.p[0].N + BN - 1) / BN;
     a.nt1 = a.p[1].M ? (a.p[1].N + BN - 1) / BN : 1;
     a.tiles0 = static_cast<int>(t0);
     a.tiles = static_cast<int>(t0 + t1);
-    auto kern = linear_i8_kernel<BN, Elem>;
-    if (!ensure_smem(kern, I8Smem<BN>::bytes, g_smem_done_i8[slot])) return OASR_ERR_CUDA;
+    auto kern = linear_i8_kernel<BN, PAIR, Elem>;
+    if (!ensure_smem(kern, SP::bytes, g_smem_done_i8[slot])) return OASR_ERR_CUDA;
     CUtensorMap tm[4];
     for (int g = 0; g < 2; ++g) {
         const I8Problem& p = a.p[a.p[1].M ? g : 0];   // one problem: its maps stand in for the other's
-        if (!encode_bytes(&tm[2 * g], p.x, p.M, a.K, 128) || !encode_bytes(&tm[2 * g + 1], p.w, p.N, a.K, BN))
+        if (!encode_bytes(&tm[2 * g], p.x, p.M, a.K, 128) || !encode_bytes(&tm[2 * g + 1], p.w, p.N, a.K, SP::b_rows))
             return OASR_ERR_INVALID_ARG;
     }
-    return launch_pdl(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(kI8Threads), I8Smem<BN>::bytes, stream, tm[0], tm[1],
-                      tm[2], tm[3], static_cast<const I8Args>(a));
+    if constexpr (PAIR)
+        return launch_pdl_cluster(kern, dim3(2 * (a.tiles < sms / 2 ? a.tiles : sms / 2)), dim3(kI8Threads), SP::bytes, 2, stream,
+                                  tm[0], tm[1], tm[2], tm[3], static_cast<const I8Args>(a));
+    else
+        return launch_pdl(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(kI8Threads), SP::bytes, stream, tm[0], tm[1], tm[2],
+                          tm[3], static_cast<const I8Args>(a));
 }
 
-// Tile width: the one of the least estimated time, waves of tiles times a tile's cycles.  A K step of 64
-// costs the larger of converting its 128 + BN rows (I8COST cycles a row) and the matrix instructions.
+// Tile: the one of the least estimated time.  Measured per K step of 64 (ns, by the slope over K): 400 for a
+// pair's 256 x 256, 340 for 128 x 128, 310 and 305 for 128 x 64 and 128 x 32, where the steps' latency is the cost;
+// a tile's epilogue takes 3200, 1700, 800 and 400, half of which the next tile's products hide.  8191 x 4096 x 1024
+// in fp32: 65.5 us in pairs, 95.3 in 128 x 128; 1024 x 768 x 256: 8.2 in pairs, 6.0, 4.9 in 128 x 64 and 6.1 in
+// 128 x 32.  256 x 128 in pairs and 128 x 256 without were nowhere the fastest.
 template <typename Elem>
 oasr_status dispatch_i8(const I8Args& a, cudaStream_t stream)
 {
     const int sms = sm_count();
     if (!sms || !a.status) return OASR_ERR_CUDA;
-    int best = 256;
+    constexpr struct { int m, n, ctas, step, epilogue; } kinds[] = {
+        {256, 256, 2, 400, 3200}, {128, 128, 1, 340, 1700}, {128, 64, 1, 310, 800}, {128, 32, 1, 305, 400}};
+    int best = 0;
     long long least = 0x7fffffffffffffffLL;
-    for (int bn = 256; bn >= 32; bn /= 2) {
-        long long n = 0;
+    for (int k = 0; k < 4; ++k) {
+        const auto& t = kinds[k];
+        long long tiles = 0;
         for (const I8Problem& p : a.p)
-            if (p.M) n += ((p.M + 127LL) / 128) * ((p.N + bn - 1) / bn);
-        const long long step = 2 * (128 + bn), fill = 1500 + 8 * bn;
-        const long long t = ((n + sms - 1) / sms) * step * ((a.K + 63) / 64) + fill;
-        if (t < least) {
-            least = t;
-            best = bn;
+            if (p.M) tiles += ((p.M + t.m - 1LL) / t.m) * ((p.N + t.n - 1) / t.n);
+        const long long waves = (tiles * t.ctas + sms - 1) / sms, steps = static_cast<long long>((a.K + 63) / 64) * t.step;
+        const long long wave = steps > t.epilogue / 2 ? steps + t.epilogue / 2 : t.epilogue;
+        if (waves * wave + t.epilogue < least) {
+            least = waves * wave + t.epilogue;
+            best = k;
         }
     }
     constexpr int s = sizeof(Elem) == 4 ? 4 : 0;
-    if (best == 256) return launch_i8<256, Elem>(a, s, sms, stream);
-    if (best == 128) return launch_i8<128, Elem>(a, s + 1, sms, stream);
-    if (best == 64) return launch_i8<64, Elem>(a, s + 2, sms, stream);
-    return launch_i8<32, Elem>(a, s + 3, sms, stream);
+    if (best == 0) return launch_i8<256, true, Elem>(a, s, sms, stream);
+    if (best == 1) return launch_i8<128, false, Elem>(a, s + 1, sms, stream);
+    if (best == 2) return launch_i8<64, false, Elem>(a, s + 2, sms, stream);
+    return launch_i8<32, false, Elem>(a, s + 3, sms, stream);
 }
 
 template <typename Elem>

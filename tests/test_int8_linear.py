@@ -170,6 +170,21 @@ def test_sums_are_the_integers(M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(64, 4096, 1024), (1000, 513, 272), (3000, 700, 1008), (2600, 1100, 1024), (8191, 4096, 48),
+                                   (4100, 1000, 208), (257, 9000, 512)])
+def test_tiles_of_every_shape_bit_for_bit(M, N, K):
+    """Several tiles per CTA, last tiles of a row or column, a CTA pair whose second half has no row; the same
+    sums at every repetition."""
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    x8, w8 = (torch.randint(-128, 128, (n, K), generator=g, device="cuda", dtype=torch.int8) for n in (M, N))
+    want = (x8.double() @ w8.double().t()).float()   # integers below 2^24
+    one = torch.ones(M, device="cuda"), torch.ones(N, device="cuda")
+    for _ in range(20):
+        assert torch.equal(capi.oasr_linear_w8a8(x8, one[0], w8, one[1], out_dtype=torch.float32), want)
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_longest_rows():
     g = torch.Generator().manual_seed(2)
     for M in (3, 20):
