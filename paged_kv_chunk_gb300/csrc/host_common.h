@@ -33,8 +33,9 @@ bool encode_head_pairs_bf16(CUtensorMap* map, const void* base, long long rows, 
 bool encode_rows_e4m3(CUtensorMap* map, const void* base, long long rows, int box_rows);
 
 // Encode a 2-D map over rows of row_bytes bytes (a multiple of 16) with a box of 64 bytes of box_rows rows,
-// not swizzled.  Returns false if the driver rejects it.
-bool encode_bytes(CUtensorMap* map, const void* base, long long rows, int row_bytes, int box_rows);
+// not swizzled or (swizzle64) with the 16-byte chunks of rows 2i and 2i + 1 exchanged by i % 4.  Returns false if
+// the driver rejects it.
+bool encode_bytes(CUtensorMap* map, const void* base, long long rows, int row_bytes, int box_rows, bool swizzle64 = false);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

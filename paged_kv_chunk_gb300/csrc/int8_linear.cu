@@ -7,8 +7,14 @@
 // This GPU's tensor cores have next to no 8-bit integer rate, but an 8-bit integer is exact in fp16
 // and a product of two exact in fp32, so the sums run on tcgen05's fp16 rate: converter warps
 // read the 8-bit rows and write them as fp16 into the swizzled tiles the matrix instructions
-// read.  A sum stays below 2^24 for K <= 1024, where fp32 holds every integer: the accumulated
+// read.  A sum stays within 2^24 for K <= 1024, where fp32 holds every integer: the accumulated
 // sum is the integer sum.  For longer K it is that of an fp32 accumulation.
+//
+// What bounds a large product is shared memory: of a K step of 64, a tile's rows come in as bytes,
+// are read, written as fp16 and read by the matrix unit.  A pair of CTAs on one 256 x 256 tile
+// (cta_group::2) holds and converts each w row once for both, 96 KB of traffic per CTA and step
+// where a CTA alone on 128 x 256 has 144.  8191 x 4096 x 1024: 57 us in fp32, 51 in bf16
+// (1.2 and 1.35 PFLOP/s), 86 with 128 x 256 tiles.
 #include <type_traits>
 
 #include "attn_core.cuh"
@@ -110,6 +116,7 @@ struct I8Args {
     void* out[4];           // problem 0: column block n / width into out[n / width]; problem 1: out[3]
     int width;
     int K, nt0, nt1, tiles0, tiles;   // column tiles of each problem; tiles of problem 0, of both
+    int by_tma;             // the outputs' rows suit TMA: stored by it
     unsigned* status;
 };
 
@@ -117,6 +124,21 @@ __device__ __forceinline__ float bias_at(const float* b, int n) { return __ldg(b
 __device__ __forceinline__ float bias_at(const __nv_bfloat16* b, int n) { return __bfloat162float(b[n]); }
 __device__ __forceinline__ void put(float* o, float v) { *o = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
+
+// 32 bytes to global memory, aligned to 32.
+__device__ __forceinline__ void st_32bytes(void* to, const uint32_t* v)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Four sums times their row's scale x and columns' scales w, plus the bias b; each operation rounded.
+__device__ __forceinline__ float4 scaled(const uint32_t* s, float x, float4 w, float4 b)
+{
+    auto one = [&](uint32_t v, float wj, float bj) { return __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v), x), wj), bj); };
+    return make_float4(one(s[0], w.x, b.x), one(s[1], w.y, b.y), one(s[2], w.z, b.z), one(s[3], w.w, b.w));
+}
 
 // Eight 8-bit integers (natural order) to fp16: with its sign bit flipped a byte b is b + 128 as
 // an unsigned number, which under the exponent of 1024 reads 1152 + b.
@@ -134,11 +156,13 @@ __device__ __forceinline__ uint4 i8_to_f16(uint32_t w0, uint32_t w1)
                       i8_sub(__byte_perm(w1, 0x64646464u, 0x4140)), i8_sub(__byte_perm(w1, 0x64646464u, 0x4342)));
 }
 
-// Warps: eight for the epilogue, two groups of eight converters, the issuer, the TMA producer.  The producer
+// Warps: eight for the epilogue, four groups of four converters, the issuer, the TMA producer.  The producer
 // brings 8-bit tiles of 64 K into a ring; the converter groups take its slots in turn (one group's proxy
-// fence and waits pass while the other converts) and write the fp16 ring that the products read; two
-// accumulators let a tile's epilogue overlap the next tile's products.
-constexpr int kI8EpiWarps = 8, kI8Group = 256, kI8Groups = 2;
+// fence and waits pass while the others convert: 59.8 us where two groups of eight warps take 63.1) and write
+// the fp16 ring that the products read; two accumulators let a tile's epilogue overlap the next tile's products.
+// In a pair both CTAs do so with their own rows, and the even one issues the products of both: the odd one's
+// issuer passes on that a slot is written.
+constexpr int kI8EpiWarps = 8, kI8Group = 128, kI8Groups = 4;
 constexpr int kI8Conv0 = 32 * kI8EpiWarps;                        // first converter thread
 constexpr int kI8Issuer = kI8EpiWarps + kI8Groups * kI8Group / 32;   // its warp; the producer's is the next
 constexpr int kI8Threads = 32 * (kI8Issuer + 2);
@@ -151,12 +175,15 @@ struct I8Smem {
     static constexpr int raw = rows * 64;                              // 8-bit, 64 of K
     static constexpr int stages = 4, raws = 4;
     static constexpr int off_raw = stages * tile;
-    static constexpr int off_out = off_raw + raws * raw;               // [8 warps][32][16] floats
-    static constexpr int off_ws = off_out + kI8EpiWarps * 32 * 16 * 4;   // [8 warps][2][BN / 2] floats
+    static constexpr bool tma_out = BN >= 128;
+    static constexpr int off_out = off_raw + raws * raw;               // [8 warps][32 rows][64 bytes]
+    static constexpr int off_ws = off_out + kI8EpiWarps * 32 * 64;   // [8 warps][2][BN / 2] floats
     static constexpr int off_bar = off_ws + kI8EpiWarps * BN * 4;      // full, empty, raw full, raw empty, acc full[2], acc free[2], drain
     static constexpr int off_misc = off_bar + (2 * stages + 2 * raws + 5) * 8;
     static constexpr int bytes = off_misc + 16 + 1024;
     static constexpr int cols = 2 * BN < 32 ? 32 : 2 * BN;
+    // a group's last wait on a slot's barrier was for the phase before (it comes by every slot in turn)
+    static_assert(stages % kI8Groups == 0 && raws % kI8Groups == 0, "a wait is one phase behind at most");
 };
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
@@ -167,10 +194,25 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// 64 bytes of 32 rows from shared memory to (x, y); what lies outside the tensor is not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+struct I8Outs {
+    CUtensorMap m[4];   // of I8Args::out
+};
+
 template <int BN, bool PAIR, typename Elem>
 __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
     const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_w0,
-    const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_w1, const I8Args a)
+    const __grid_constant__ CUtensorMap tm_x1, const __grid_constant__ CUtensorMap tm_w1,
+    const __grid_constant__ I8Outs outs, const I8Args a)
 {
     using SP = I8Smem<BN, PAIR>;
     constexpr int CTAS = PAIR ? 2 : 1;
@@ -328,8 +370,8 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         }
     } else if (warp >= kI8EpiWarps) {
         // ------------------------------------------------------------ converters
-        // thread: 16 bytes (chunk c) of rows r0, r0 + 64, ...
-        constexpr int NU = (SP::rows + 63) / 64;
+        // thread: 16 bytes (chunk c) of rows r0, r0 + CR, ...
+        constexpr int CR = kI8Group / 4, NU = (SP::rows + CR - 1) / CR;   // rows of a pass, passes
         const int grp = (tid - kI8Conv0) / kI8Group, ct = (tid - kI8Conv0) % kI8Group, c = ct & 3, r0 = ct >> 2;
         for (int i = grp; i < iters; i += kI8Groups) {
             const int rs = i % R, slot = i % S;
@@ -338,15 +380,15 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
             uint4 buf[NU];
 #pragma unroll
             for (int u = 0; u < NU; ++u)
-                if (r0 + 64 * u < SP::rows) buf[u] = *reinterpret_cast<const uint4*>(src + 4096 * u);
+                if (r0 + CR * u < SP::rows) buf[u] = *reinterpret_cast<const uint4*>(src + 64 * CR * u);
             if (i >= S && !__all_sync(0xffffffffu, wait_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort))) break;
             uint8_t* lo = sm + slot * SP::tile + swz128(r0, 2 * c);
             uint8_t* hi = sm + slot * SP::tile + swz128(r0, 2 * c + 1);
 #pragma unroll
-            for (int u = 0; u < NU; ++u)   // 64 rows on, the same swizzle
-                if (r0 + 64 * u < SP::rows) {
-                    *reinterpret_cast<uint4*>(lo + 8192 * u) = i8_to_f16(buf[u].x, buf[u].y);
-                    *reinterpret_cast<uint4*>(hi + 8192 * u) = i8_to_f16(buf[u].z, buf[u].w);
+            for (int u = 0; u < NU; ++u)   // a multiple of 8 rows on, the same swizzle
+                if (r0 + CR * u < SP::rows) {
+                    *reinterpret_cast<uint4*>(lo + 128 * CR * u) = i8_to_f16(buf[u].x, buf[u].y);
+                    *reinterpret_cast<uint4*>(hi + 128 * CR * u) = i8_to_f16(buf[u].z, buf[u].w);
                 }
             fence_proxy_async_smem();
             __syncwarp();
@@ -359,13 +401,12 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         }
     } else {
         // --------------------------------------------------------------- epilogue
-        // warp: 32 rows (its TMEM lanes, warp % 4) of one half of the tile's columns (warp / 4), 16 columns at a
-        // time, the next 16 on their way from TMEM meanwhile
+        // warp: 32 rows (its TMEM lanes, warp % 4) of one half of the tile's columns (warp / 4)
         constexpr int HN = BN / 2, NC = HN / 16;
         const int rq = warp & 3, half = warp >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * rq) << 16) + half * HN;
         float* s_ws = reinterpret_cast<float*>(sm + SP::off_ws) + warp * BN;   // w scales, then biases
-        float* s_out = reinterpret_cast<float*>(sm + SP::off_out) + warp * 32 * 16;
+        uint8_t* s_out = sm + SP::off_out + warp * 32 * 64;
         for (int lt = 0; lt < my_tiles; ++lt) {
             int g, mt, nt;
             decode(first + lt * stride, g, mt, nt);
@@ -388,69 +429,114 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
             // there is one) and the block's first column there
             const int width = g ? N : a.width;
             int which = g ? 3 : col0 / width, at = g ? col0 : col0 - which * width;
-            uint32_t r[2][16];
-            OASR_TMEM_LD16(tl + buf * BN, r[0]);
+            if (SP::tma_out && a.by_tma) {
+                // 64 bytes of every row at a time, staged and stored by TMA
+                constexpr int CB = 64 / sizeof(Elem);
+#pragma unroll 1
+                for (int c = 0; c < HN / CB; ++c) {
+                    const int col = col0 + CB * c;
+                    if (col >= N) break;
+                    uint32_t r[CB];
+                    OASR_TMEM_LD16(tl + buf * BN + CB * c, r);
+                    if constexpr (CB == 32) {
+                        uint32_t* r1 = r + 16;
+                        OASR_TMEM_LD16(tl + buf * BN + CB * c + 16, r1);
+                    }
+                    tmem_wait_ld();
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the tile's last use
+                    __syncwarp();
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int col = col0 + 16 * c;
-                if (col >= N) break;
-                tmem_wait_ld();
-                if (c + 1 < NC) OASR_TMEM_LD16(tl + buf * BN + 16 * (c + 1), r[(c + 1) & 1]);
-                // thread = row: times the row's scale, into the staging tile (16-byte chunks exchanged by row, so
-                // that neither side has bank conflicts)
+                    for (int j = 0; j < 4; ++j) {   // 16 bytes
+                        uint32_t o[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t* s4 = r[c & 1] + 4 * j;
-                    *reinterpret_cast<float4*>(s_out + 16 * lane + 4 * (j ^ ((lane >> 1) & 3))) =
-                        make_float4(__fmul_rn(__uint_as_float(s4[0]), x), __fmul_rn(__uint_as_float(s4[1]), x),
-                                    __fmul_rn(__uint_as_float(s4[2]), x), __fmul_rn(__uint_as_float(s4[3]), x));
+                        for (int q = 0; q < CB / 16; ++q) {
+                            const int e = (CB / 4) * j + 4 * q;
+                            const float4 w = *reinterpret_cast<const float4*>(s_ws + CB * c + e);
+                            const float4 b = *reinterpret_cast<const float4*>(s_ws + HN + CB * c + e);
+                            const float4 v = scaled(r + e, x, w, b);
+                            if constexpr (sizeof(Elem) == 2) {
+                                o[2 * q] = pack_bf16(v.x, v.y);
+                                o[2 * q + 1] = pack_bf16(v.z, v.w);
+                            } else {
+                                o[0] = __float_as_uint(v.x), o[1] = __float_as_uint(v.y);
+                                o[2] = __float_as_uint(v.z), o[3] = __float_as_uint(v.w);
+                            }
+                        }
+                        *reinterpret_cast<uint4*>(s_out + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && row0 < M)
+                        tma_store_2d(&outs.m[which], smem_addr(s_out), at * static_cast<int>(sizeof(Elem)), row0);
+                    if ((at += CB) == width && !g) {
+                        at = 0;
+                        ++which;
+                    }
                 }
-                __syncwarp();
-                void* ob = which == 0 ? a.out[0] : which == 1 ? a.out[1] : which == 2 ? a.out[2] : a.out[3];
-                Elem* dst = static_cast<Elem*>(ob) + static_cast<long long>(row0) * width + at;
-                auto finish = [&](int row, int j4) {   // four columns' values
-                    const float4 v = *reinterpret_cast<const float4*>(s_out + 16 * row + 4 * (j4 ^ ((row >> 1) & 3)));
-                    const float4 w = *reinterpret_cast<const float4*>(s_ws + 16 * c + 4 * j4);
-                    const float4 b = *reinterpret_cast<const float4*>(s_ws + HN + 16 * c + 4 * j4);
-                    return make_float4(__fadd_rn(__fmul_rn(v.x, w.x), b.x), __fadd_rn(__fmul_rn(v.y, w.y), b.y),
-                                       __fadd_rn(__fmul_rn(v.z, w.z), b.z), __fadd_rn(__fmul_rn(v.w, w.w), b.w));
-                };
-                if (col + 16 <= N && (width & 7) == 0) {
-                    // rows in runs of 64 or 32 bytes, 16 bytes a lane
-                    constexpr int V = 16 / sizeof(Elem), L = 16 / V;   // values of a store, lanes of a row
-                    const int j = lane % L;
+            } else {
+                // a lane's row straight from its registers, in whole 32-byte sectors where they are aligned
+                const long long row = row0 + lane;
+#pragma unroll 1
+                for (int c = 0; c < NC; ++c) {
+                    const int col = col0 + 16 * c;
+                    if (col >= N) break;
+                    uint32_t r[16];
+                    OASR_TMEM_LD16(tl + buf * BN + 16 * c, r);
+                    tmem_wait_ld();
+                    constexpr int W = sizeof(Elem) * 16 / 4;   // words of the row
+                    uint32_t o[W];
+                    float v[16];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 32 / L) {
-                        const int row = i + lane / L;
-                        const float4 v0 = finish(row, j * V / 4);
-                        Elem* to = dst + static_cast<long long>(row) * width + j * V;
-                        if constexpr (sizeof(Elem) == 2) {
-                            const float4 v1 = finish(row, j * V / 4 + 1);
-                            if (row0 + row < M)
-                                *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(v0.x, v0.y), pack_bf16(v0.z, v0.w),
-                                                                           pack_bf16(v1.x, v1.y), pack_bf16(v1.z, v1.w));
-                        } else if (row0 + row < M) {
-                            *reinterpret_cast<float4*>(to) = v0;
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 w = *reinterpret_cast<const float4*>(s_ws + 16 * c + j);
+                        const float4 b = *reinterpret_cast<const float4*>(s_ws + HN + 16 * c + j);
+                        const float4 t = scaled(r + j, x, w, b);
+                        v[j] = t.x, v[j + 1] = t.y, v[j + 2] = t.z, v[j + 3] = t.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if constexpr (sizeof(Elem) == 2)
+                            o[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                        else
+                            o[j] = __float_as_uint(v[j]);
+                    void* ob = which == 0 ? a.out[0] : which == 1 ? a.out[1] : which == 2 ? a.out[2] : a.out[3];
+                    Elem* to = static_cast<Elem*>(ob) + row * width + at;
+                    const int row_bytes = width * static_cast<int>(sizeof(Elem));
+                    if (col + 16 <= N && !(row_bytes & 15)) {
+                        if (row >= M) {
+                        } else if (!((row_bytes | reinterpret_cast<uintptr_t>(ob)) & 31)) {
+#pragma unroll
+                            for (int j = 0; j < W; j += 8) st_32bytes(reinterpret_cast<uint32_t*>(to) + j, o + j);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < W; j += 4)
+                                *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(to) + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                    } else {
+                        // rows of any alignment, or the last columns: 16 lanes to a row
+                        float* s_f = reinterpret_cast<float*>(s_out);
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<float4*>(s_f + 16 * lane + 4 * (j ^ ((lane >> 1) & 3))) =
+                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        __syncwarp();
+                        const int j = lane & 15;
+                        Elem* base = to + (static_cast<long long>(lane >> 4) - lane) * width + j;
+#pragma unroll 4
+                        for (int i = 0; i < 16; ++i) {
+                            const int rr = 2 * i + (lane >> 4);
+                            if (row0 + rr < M && col + j < N)
+                                put(base + 2LL * i * width, s_f[16 * rr + 4 * ((j >> 2) ^ (i & 3)) + (j & 3)]);
                         }
                     }
-                } else {
-                    const int j = lane & 3;
-                    for (int row = lane >> 2; row < 32; row += 8) {
-                        const float4 v = finish(row, j);
-                        const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (row0 + row < M && col + 4 * j + k < N)
-                                put(dst + static_cast<long long>(row) * width + 4 * j + k, e[k]);
+                    if ((at += 16) == width && !g) {
+                        at = 0;
+                        ++which;
                     }
                 }
-                if ((at += 16) == width && !g) {
-                    at = 0;
-                    ++which;
-                }
-                __syncwarp();
             }
-            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -460,6 +546,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
                     mbar_arrive(bar_acc_free + 8 * buf);
             }
         }
+        if (SP::tma_out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // every store has been made
     }
     grid_dep_trigger();
     tc_fence_before();
@@ -540,18 +627,27 @@ oasr_status launch_i8(I8Args a, int slot, int sms, cudaStream_t stream)
         if (!encode_bytes(&tm[2 * g], p.x, p.M, a.K, 128) || !encode_bytes(&tm[2 * g + 1], p.w, p.N, a.K, SP::b_rows))
             return OASR_ERR_INVALID_ARG;
     }
+    I8Outs outs = {};
+    for (int o = 0; SP::tma_out && o < 4; ++o) {
+        if (!a.out[o]) continue;
+        const I8Problem& p = a.p[o == 3];
+        const long long bytes = (o == 3 ? p.N : a.width) * static_cast<long long>(sizeof(Elem));
+        a.by_tma = bytes % 16 == 0 && bytes <= 0x7fffffffLL;
+        if (!a.by_tma) break;
+        if (!encode_bytes(&outs.m[o], a.out[o], p.M, static_cast<int>(bytes), 32, true)) return OASR_ERR_INVALID_ARG;
+    }
     if constexpr (PAIR)
         return launch_pdl_cluster(kern, dim3(2 * (a.tiles < sms / 2 ? a.tiles : sms / 2)), dim3(kI8Threads), SP::bytes, 2, stream,
-                                  tm[0], tm[1], tm[2], tm[3], static_cast<const I8Args>(a));
+                                  tm[0], tm[1], tm[2], tm[3], outs, static_cast<const I8Args>(a));
     else
         return launch_pdl(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(kI8Threads), SP::bytes, stream, tm[0], tm[1], tm[2],
-                          tm[3], static_cast<const I8Args>(a));
+                          tm[3], outs, static_cast<const I8Args>(a));
 }
 
-// Tile: the one of the least estimated time.  Measured per K step of 64 (ns, by the slope over K): 400 for a
-// pair's 256 x 256, 340 for 128 x 128, 310 and 305 for 128 x 64 and 128 x 32, where the steps' latency is the cost;
-// a tile's epilogue takes 3200, 1700, 800 and 400, half of which the next tile's products hide.  8191 x 4096 x 1024
-// in fp32: 65.5 us in pairs, 95.3 in 128 x 128; 1024 x 768 x 256: 8.2 in pairs, 6.0, 4.9 in 128 x 64 and 6.1 in
+// Tile: the one of the least estimated time.  Measured per K step of 64 (ns, by the slope over K): 375 for a
+// pair's 256 x 256, 315 for 128 x 128, 285 and 275 for 128 x 64 and 128 x 32, where the steps' latency is the cost;
+// a tile's epilogue takes 2400, 1300, 600 and 400, half of which the next tile's products hide.  8191 x 4096 x 1024
+// in fp32: 57 us in pairs, 87 in 128 x 128; 1024 x 768 x 256 in bf16: 7.0 in pairs, 5.2, 4.5 in 128 x 64 and 5.5 in
 // 128 x 32.  256 x 128 in pairs and 128 x 256 without were nowhere the fastest.
 template <typename Elem>
 oasr_status dispatch_i8(const I8Args& a, cudaStream_t stream)
@@ -559,7 +655,7 @@ oasr_status dispatch_i8(const I8Args& a, cudaStream_t stream)
     const int sms = sm_count();
     if (!sms || !a.status) return OASR_ERR_CUDA;
     constexpr struct { int m, n, ctas, step, epilogue; } kinds[] = {
-        {256, 256, 2, 400, 3200}, {128, 128, 1, 340, 1700}, {128, 64, 1, 310, 800}, {128, 32, 1, 305, 400}};
+        {256, 256, 2, 375, 2400}, {128, 128, 1, 315, 1300}, {128, 64, 1, 285, 600}, {128, 32, 1, 275, 400}};
     int best = 0;
     long long least = 0x7fffffffffffffffLL;
     for (int k = 0; k < 4; ++k) {

@@ -171,11 +171,12 @@ __device__ __forceinline__ bool mbar_try_wait_sleep_cluster(uint32_t bar, uint32
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort)
 {
-    if (!CLUSTER && mbar_try_wait(bar, parity)) return true;
+    // suspended until the phase completes, for 20 us at most between the checks below
+    auto wait = [&] { return CLUSTER ? mbar_try_wait_sleep_cluster(bar, parity, 20000u) : mbar_try_wait_sleep(bar, parity, 20000u); };
+    if (wait()) return true;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
-        // suspended until the phase completes, for 20 us at most between the checks below
-        if (CLUSTER ? mbar_try_wait_sleep_cluster(bar, parity, 20000u) : mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+        if (wait()) return true;
         if (*abort) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;

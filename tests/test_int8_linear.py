@@ -171,7 +171,7 @@ def test_sums_are_the_integers(M):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(64, 4096, 1024), (1000, 513, 272), (3000, 700, 1008), (2600, 1100, 1024), (8191, 4096, 48),
-                                   (4100, 1000, 208), (257, 9000, 512)])
+                                   (4100, 1000, 208), (257, 9000, 512), (2600, 1101, 1024), (5000, 2302, 64), (1000, 503, 64)])
 def test_tiles_of_every_shape_bit_for_bit(M, N, K):
     """Several tiles per CTA, last tiles of a row or column, a CTA pair whose second half has no row; the same
     sums at every repetition."""
