@@ -263,8 +263,9 @@ oasr_status oasr_paged_read_e4m3(const void* k_pool, const void* v_pool, const v
  * num_blocks * H * block_size < 2^31.  A stream with C_b + T > max_blocks_per_seq * block_size has the
  * keys past the table dropped; distances the rel table lacks (R < C_b + 2T - 1) count as zero rows; an
  * invalid block id reads as zero rows; each raises OASR_ERR_BOUNDS.
- * bf16: the chunk, biases, rel and out are bf16; the position term is rounded to bf16, P (times its
- * key's V scale) likewise, everything else is fp32.  f32: fp32 throughout.
+ * bf16: the chunk, biases, rel and out are bf16; q + v and the position term are rounded to bf16, q + u
+ * and the weights to fp16 (a weight with its key's V scale, relative to the row's largest such), everything
+ * else is fp32.  f32: fp32 throughout.
  */
 oasr_status oasr_chunk_relattn_paged_e4m3(const void* q, const void* k_pool, const void* v_pool,
                                           const void* kv_scale, int num_blocks, int block_size,
@@ -276,7 +277,7 @@ oasr_status oasr_chunk_relattn_paged_e4m3(const void* q, const void* k_pool, con
 
 /*
  * One fused streaming step over the 8-bit cache: oasr_paged_append_e4m3 followed by
- * oasr_chunk_relattn_paged_e4m3 (in one launch for bf16, in two for f32).  The chunk's own keys are
+ * oasr_chunk_relattn_paged_e4m3 (in one launch for bf16 and T <= 16, else in two).  The chunk's own keys are
  * attended to as quantised, so the result is that of the two calls up to summation order, and the
  * pools afterwards are bit-identical.  The requirements of both apply.  Block ids of different streams
  * must not alias a block that this step writes.
@@ -307,7 +308,7 @@ oasr_status oasr_quantize_rows(const void* x, void* x8, float* scale, int M, int
  * x8 [M, K] and w8 [N, K] int8, x_scale [M] and w_scale [N] fp32, bias [N] (null: none) and out [M, N]
  * of `dt`.  The sum is exact for K <= 1024 and for M <= 8 and is accumulated in fp32 otherwise; the
  * scales and the bias are applied in that order in fp32, and the result is rounded once.  K a multiple
- * of 16, at most 65536; every pointer 16-byte aligned.
+ * of 16, at most 65536; M and N at most 2^31 - 256; every pointer 16-byte aligned.
  */
 oasr_status oasr_linear_w8a8(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
                              const void* bias, void* out, int M, int N, int K, oasr_dtype dt,
@@ -316,8 +317,9 @@ oasr_status oasr_linear_w8a8(const void* x8, const float* x_scale, const void* w
 /*
  * oasr_project_qkv_pos with 8-bit integer products (one launch): q | k | v from x8 [M, d_model] and
  * w_qkv8 [3 d_model, d_model] with bias b_qkv [3 d_model], each written as [M, H, 64], and rel
- * [R, H, 64] from pos8 [R, d_model] and w_pos8 [d_model, d_model], without bias.  Scales, rounding and
- * the sums are those of oasr_linear_w8a8.  d_model = 64 H, at most 16384; outputs and bias of `dt`.
+ * [R, H, 64] from pos8 [R, d_model] and w_pos8 [d_model, d_model], without bias.  Scales and rounding
+ * are those of oasr_linear_w8a8; the sums are exact for d_model <= 1024 and accumulated in fp32 otherwise.
+ * d_model = 64 H, at most 16384; M and R at most 2^31 - 256; outputs and bias of `dt`.
  */
 oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_scale, const void* w_qkv8,
                                       const float* w_qkv_scale, const void* b_qkv, const void* pos8,

@@ -8,23 +8,27 @@
 //
 // The scales stay out of the products: 2^ek multiplies the accumulated score of its key (one fused
 // multiply-add with the position term) and 2^ev adds ev to the exponent of its key's weight; both are
-// exact.  k8 and v8 go into fp16 matrix instructions: e4m3's exponent and fraction, shifted into an
-// fp16's, are the value times 2^-8, subnormals included, for three or four integer instructions per
-// two values.  fp16 holds q + u (each query row scaled by a power of two) and the weights with three
-// bits more than bf16 would: rms error against 64 bits 0.0021 of the output's on random data, 0.0031
-// with bf16 (0.0017 is the rounding of the output itself).
+// exact.  k8 and v8 go into fp16 matrix instructions (e4m3 is exact in fp16).  fp16 holds q + u (each
+// query row scaled by a power of two) and the weights with three bits more than bf16 would: rms error
+// against 64 bits 0.0021 of the output's on random data, 0.0031 with bf16 (0.0017 is the rounding of
+// the output itself).
 //
-// One CTA per (stream, head, block of up to 32 queries, share of the keys): four consumer warps and
-// a producer warp.  The producer brings stages of 64 keys by TMA (a box of K and one of V per page,
-// 64-byte rows, 64-byte swizzle, and one bulk copy of the page's scales) into a ring; consumer warp
-// w takes keys 16w .. 16w+15 of each stage for all the CTA's queries.  The position term is computed
-// per segment of the keys into a pre-skewed bf16 table (PosTable, attn_core.cuh), so its shared
-// memory does not grow with the history.  The chunk itself never comes through the pool: the
-// consumer warps quantise it from k_new / v_new into a region of its own, from which it is attended
-// to, and store the same bytes into the pool.
+// A CTA takes items (stream, head, tile of 16 or 32 queries) in turn: four consumer warps and a producer
+// warp.  The producer brings stages of 64 keys by TMA (boxes of K and V rows, two 64-byte rows to a
+// 128-byte swizzled line, and one bulk copy of each page's scales) and tiles of 64 rel rows into a ring;
+// consumer warp w takes keys 16w .. 16w+15 of each stage for all the item's queries.  The position term
+// is computed beside the stages into a skewed bf16 table that is a window of 256 of its columns, so its
+// shared memory does not grow with the history.  In the fused step (T <= 16) the chunk itself never comes
+// through the pool: the consumer warps quantise k_new's and v_new's rows into a region of their own, from
+// which they are attended to, and store the same bytes into the pool.
 //
-// When the (stream, head) pairs are too few to fill the GPU the keys of each are divided over a
-// cluster of up to eight CTAs, whose partial sums meet through distributed shared memory.
+// When the (stream, head) pairs are too few to fill the GPU the keys of each are divided over a cluster
+// of up to 16 CTAs, whose partial sums meet through distributed shared memory.
+//
+// What bounds it is issue: per 16 keys and 16 queries a warp converts 24 words, multiplies, adds the
+// position term, exponentiates and rounds; HBM is at a tenth to a third of its rate.  Device times: the
+// Conformer-large step (256 streams, 8 heads, 16 frames, window 512) 62 us, one stream and one frame over 8000
+// keys 14.6, 128 streams of 64 frames over 0 to 1024 keys 124.
 #include "attn_core.cuh"
 #include "e4m3.cuh"
 #include "host_common.h"
@@ -34,14 +38,9 @@ namespace oasr {
 
 namespace {
 
-#ifndef E4NS
-#define E4NS 4
-#define E4CTAS 3
-#define E4NS2 4
-#define E4CTAS2 2
-#endif
 constexpr int kE4MaxPages = 512;                    // block-table entries a CTA caches
 constexpr int kE4Stage = 2 * kStageKeys * kE4Row;   // a ring slot: K and V rows of a stage, or 64 rel rows
+constexpr int kSlots = 4;                           // of the ring: 3 and 6 were 1% slower over 1984 keys
 constexpr int kE4MaxT = 64;
 constexpr int kChunkRows = 16;                      // rows of the chunk region (fused: T <= 16)
 constexpr int kE4Consumers = 32 * kConsumerWarps;
@@ -1374,13 +1373,16 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
             !ensure_clusters(chunk_e4m3_f32_kernel, g_clusters_e4[3]))
             return OASR_ERR_CUDA;
         return launch_pdl_cluster(chunk_e4m3_f32_kernel, dim3(static_cast<unsigned>(pairs * a.splits)), dim3(kFThreads),
-                                  static_cast<int>(sizeof(F32Smem)), a.splits, stream, static_cast<const float*>(q), static_cast<const uint8_t*>(a.k_pool),
-                                 static_cast<const uint8_t*>(a.v_pool), static_cast<const uint8_t*>(a.kv_scale),
-                                 static_cast<const float*>(u), static_cast<const float*>(vb), static_cast<const float*>(rel),
-                                 static_cast<float*>(out), static_cast<const E4Args>(a));
+                                  static_cast<int>(sizeof(F32Smem)), a.splits, stream, static_cast<const float*>(q),
+                                  static_cast<const uint8_t*>(a.k_pool), static_cast<const uint8_t*>(a.v_pool),
+                                  static_cast<const uint8_t*>(a.kv_scale), static_cast<const float*>(u),
+                                  static_cast<const float*>(vb), static_cast<const float*>(rel), static_cast<float*>(out),
+                                  static_cast<const E4Args>(a));
     }
-    if (T <= 16) return launch_e4<1, E4NS, E4CTAS, FUSED>(q, k_new, v_new, rel, a, km, B, FUSED ? 1 : 0, stream);
-    return launch_e4<2, E4NS2, E4CTAS2, false>(q, k_new, v_new, rel, a, km, B, 2, stream);
+    // 32 queries a CTA convert each key once for both m-tiles, and two CTAs fit an SM's registers: 76 streams of 64
+    // queries over 960 keys take 102 us, 112 with tiles of 16 (three CTAs), 108 with three CTAs and spills
+    if (T <= 16) return launch_e4<1, kSlots, 3, FUSED>(q, k_new, v_new, rel, a, km, B, FUSED ? 1 : 0, stream);
+    return launch_e4<2, kSlots, 2, false>(q, k_new, v_new, rel, a, km, B, 2, stream);
 }
 
 }  // namespace

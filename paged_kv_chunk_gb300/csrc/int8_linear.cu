@@ -688,6 +688,7 @@ oasr_status few_rows(const I8Problem& p, void* out, int K, cudaStream_t stream)
 }
 
 constexpr int kI8MaxK = 65536;   // integer sums of K products of at most 2^14 stay below 2^31
+constexpr int kI8MaxRows = 0x7fffff00;   // the rows and columns of whole tiles are 32-bit numbers
 
 }  // namespace
 }  // namespace oasr
@@ -721,7 +722,8 @@ extern "C" oasr_status oasr_linear_w8a8(const void* x8, const float* x_scale, co
 {
     using namespace oasr;
     if (!x8 || !x_scale || !w8 || !w_scale || !out || M <= 0 || N <= 0 || K <= 0) return OASR_ERR_INVALID_ARG;
-    if ((dt != OASR_F32 && dt != OASR_BF16) || K % 16 || K > kI8MaxK) return OASR_ERR_UNSUPPORTED;
+    if ((dt != OASR_F32 && dt != OASR_BF16) || K % 16 || K > kI8MaxK || M > kI8MaxRows || N > kI8MaxRows)
+        return OASR_ERR_UNSUPPORTED;
     const void* ptrs[] = {x8, x_scale, w8, w_scale, bias ? bias : x8, out};
     for (const void* p : ptrs)
         if (!aligned16(p)) return OASR_ERR_INVALID_ARG;
@@ -748,7 +750,8 @@ extern "C" oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_
     for (const void* p : ptrs)
         if (!p || !aligned16(p)) return OASR_ERR_INVALID_ARG;
     if (M <= 0 || R <= 0 || d_model <= 0 || H <= 0) return OASR_ERR_INVALID_ARG;
-    if ((dt != OASR_F32 && dt != OASR_BF16) || d_model % kHeadDim || d_model / kHeadDim != H || d_model > kI8MaxK / 4)
+    if ((dt != OASR_F32 && dt != OASR_BF16) || d_model % kHeadDim || d_model / kHeadDim != H || d_model > kI8MaxK / 4 ||
+        M > kI8MaxRows || R > kI8MaxRows)
         return OASR_ERR_UNSUPPORTED;
     I8Args a = {};
     a.p[0] = {static_cast<const int8_t*>(x8), static_cast<const int8_t*>(w_qkv8), x_scale, w_qkv_scale, b_qkv, M,

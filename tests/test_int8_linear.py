@@ -73,7 +73,8 @@ def test_quantize_refusals(lib, kw, expect):
     (dict(w=None), capi.OASR_ERR_INVALID_ARG), (dict(N=0), capi.OASR_ERR_INVALID_ARG),
     (dict(K=72), capi.OASR_ERR_UNSUPPORTED), (dict(K=65552), capi.OASR_ERR_UNSUPPORTED),
     (dict(dt=2), capi.OASR_ERR_UNSUPPORTED), (dict(out=FAKE + 4), capi.OASR_ERR_INVALID_ARG),
-    (dict(bias=FAKE + 2), capi.OASR_ERR_INVALID_ARG),
+    (dict(bias=FAKE + 2), capi.OASR_ERR_INVALID_ARG), (dict(M=2 ** 31 - 255), capi.OASR_ERR_UNSUPPORTED),
+    (dict(N=2 ** 31 - 1), capi.OASR_ERR_UNSUPPORTED),
 ])
 def test_linear_refusals(lib, kw, expect):
     a = dict(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, bias=None, out=FAKE, M=4, N=64, K=64, dt=capi.OASR_F32)
@@ -86,6 +87,7 @@ def test_linear_refusals(lib, kw, expect):
     (dict(M=0), capi.OASR_ERR_INVALID_ARG), (dict(R=-1), capi.OASR_ERR_INVALID_ARG),
     (dict(d=96), capi.OASR_ERR_UNSUPPORTED), (dict(H=3), capi.OASR_ERR_UNSUPPORTED),
     (dict(dt=4), capi.OASR_ERR_UNSUPPORTED), (dict(d=16448, H=257), capi.OASR_ERR_UNSUPPORTED),
+    (dict(M=2 ** 31 - 1), capi.OASR_ERR_UNSUPPORTED), (dict(R=2 ** 31 - 1), capi.OASR_ERR_UNSUPPORTED),
 ])
 def test_project_refusals(lib, kw, expect):
     a = dict(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, b=FAKE, p=FAKE, ps=FAKE, wp=FAKE, wps=FAKE, q=FAKE, k=FAKE, v=FAKE,
