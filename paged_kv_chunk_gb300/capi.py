@@ -519,12 +519,15 @@ def oasr_project_qkv_pos_w8a8(x8, x_scale, w_qkv8, w_qkv_scale, b_qkv, pos8, pos
     D, dt = d // H, b_qkv.dtype
     code = _code(dt)
     rows = (M, H, D)
-    if q is None and k is None and v is None:
-        q, k, v = torch.empty((3, M, H, D), dtype=dt, device=x8.device).unbind(0)
-    else:
-        q, k, v = (torch.empty(rows, dtype=dt, device=x8.device) if t is None else t for t in (q, k, v))
+    device = x8.device
+    if q is None:
+        q = torch.empty(rows, dtype=dt, device=device)
+    if k is None:
+        k = torch.empty(rows, dtype=dt, device=device)
+    if v is None:
+        v = torch.empty(rows, dtype=dt, device=device)
     if rel is None:
-        rel = torch.empty((R, H, D), dtype=dt, device=x8.device)
+        rel = torch.empty((R, H, D), dtype=dt, device=device)
     if q.shape != rows or k.shape != rows or v.shape != rows or rel.shape != (R, H, D):
         raise ValueError("q, k, v must be [M, H, d/H] and rel [R, H, d/H]")
     i8, f32 = torch.int8, torch.float32

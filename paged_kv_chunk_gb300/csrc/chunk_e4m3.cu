@@ -30,9 +30,9 @@
 // Conformer-large step (256 streams, 8 heads, 16 frames, window 512) 62 us, one stream and one frame over 8000
 // keys 14.6, 128 streams of 64 frames over 0 to 1024 keys 124.
 #include "attn_core.cuh"
+#include "cluster.cuh"
 #include "e4m3.cuh"
 #include "host_common.h"
-#include "tcgen05.cuh"
 
 namespace oasr {
 

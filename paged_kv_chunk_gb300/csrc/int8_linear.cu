@@ -18,9 +18,9 @@
 #include <type_traits>
 
 #include "attn_core.cuh"
+#include "cluster.cuh"
 #include "e4m3.cuh"
 #include "host_common.h"
-#include "tcgen05.cuh"
 
 namespace oasr {
 namespace {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
                 decode(first + lt * stride, g, mt, nt);
                 for (int kb = 0; kb < ksteps; ++kb, ++i) {
                     const int slot = i % R;
-                    if (i >= R && !wait_or_abort(bar_raw_free + 8 * slot, ((i / R) - 1) & 1, s_abort)) {
+                    if (i >= R && !sleep_or_abort(bar_raw_free + 8 * slot, ((i / R) - 1) & 1, s_abort)) {
                         ok = false;
                         break;
                     }
@@ -314,13 +314,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         if (lane == 0 && rank) {
             // passes on to the other CTA that this one's rows of a slot are written
             for (int i = 0; i < iters; ++i) {
-                if (!wait_or_abort(bar_full + 8 * (i % S), (i / S) & 1, s_abort)) break;
+                if (!sleep_or_abort(bar_full + 8 * (i % S), (i / S) & 1, s_abort)) break;
                 fence_release_smem_cluster();
                 mbar_arrive_cluster_relaxed(bar_full + 8 * (i % S), 0);
             }
             // the other's commits have landed before this CTA ends
             for (int u = iters - S; u < iters; ++u)
-                if (u >= 0 && !wait_or_abort(bar_empty + 8 * (u % S), (u / S) & 1, s_abort)) break;
+                if (u >= 0 && !sleep_or_abort(bar_empty + 8 * (u % S), (u / S) & 1, s_abort)) break;
             if (!mbar_wait(bar_drain, 0)) *s_abort = 1;
         } else if (lane == 0) {
             // fp16 A and B, fp32 D
@@ -335,10 +335,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
             bool ok = true;
             for (int lt = 0; lt < my_tiles && ok; ++lt) {
                 const int buf = lt & 1;
-                if (lt >= 2 && !wait_or_abort<PAIR>(bar_acc_free + 8 * buf, ((lt >> 1) - 1) & 1, s_abort)) break;
+                if (lt >= 2 && !sleep_or_abort<PAIR>(bar_acc_free + 8 * buf, ((lt >> 1) - 1) & 1, s_abort)) break;
                 for (int kb = 0; kb < ksteps; ++kb, ++i) {
                     const int slot = i % S;
-                    if (!wait_or_abort<PAIR>(bar_full + 8 * slot, (i / S) & 1, s_abort)) {
+                    if (!sleep_or_abort<PAIR>(bar_full + 8 * slot, (i / S) & 1, s_abort)) {
                         ok = false;
                         break;
                     }
@@ -375,13 +375,13 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
         const int grp = (tid - kI8Conv0) / kI8Group, ct = (tid - kI8Conv0) % kI8Group, c = ct & 3, r0 = ct >> 2;
         for (int i = grp; i < iters; i += kI8Groups) {
             const int rs = i % R, slot = i % S;
-            if (!__all_sync(0xffffffffu, wait_or_abort(bar_raw + 8 * rs, (i / R) & 1, s_abort))) break;
+            if (!__all_sync(0xffffffffu, sleep_or_abort(bar_raw + 8 * rs, (i / R) & 1, s_abort))) break;
             const uint8_t* src = sm + SP::off_raw + rs * SP::raw + 16 * ct;
             uint4 buf[NU];
 #pragma unroll
             for (int u = 0; u < NU; ++u)
                 if (r0 + CR * u < SP::rows) buf[u] = *reinterpret_cast<const uint4*>(src + 64 * CR * u);
-            if (i >= S && !__all_sync(0xffffffffu, wait_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort))) break;
+            if (i >= S && !__all_sync(0xffffffffu, sleep_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort))) break;
             uint8_t* lo = sm + slot * SP::tile + swz128(r0, 2 * c);
             uint8_t* hi = sm + slot * SP::tile + swz128(r0, 2 * c + 1);
 #pragma unroll
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
             }
             const float x = row0 + lane < M ? __ldg(p.xs + row0 + lane) : 0.f;
             __syncwarp();
-            if (!__all_sync(0xffffffffu, wait_or_abort(bar_acc_full + 8 * buf, (lt >> 1) & 1, s_abort))) break;
+            if (!__all_sync(0xffffffffu, sleep_or_abort(bar_acc_full + 8 * buf, (lt >> 1) & 1, s_abort))) break;
             tc_fence_after();
             // the output of the block's columns (a block of 16 lies within one: widths are multiples of 64, or
             // there is one) and the block's first column there

@@ -119,31 +119,6 @@ __device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity,
     }
 }
 
-// --------------------------------------------------------------- clusters
-
-// All threads of the cluster; shared-memory accesses before it happen before those behind it.
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// Releases in the cluster what happened to this CTA's shared memory before it; a release of all memory at that
-// scope waits for global memory's writes as well (0.6 us measured).
-__device__ __forceinline__ void fence_release_smem_cluster()
-{
-    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-}
-
-// Arrive on CTA `rank`'s barrier at the address that `bar` has here; orders no memory access by itself.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar, uint32_t rank)
-{
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-                 "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar),
-                 "r"(rank)
-                 : "memory");
-}
-
 // --------------------------------------------------------------- proxies
 
 // Order this thread's earlier generic-proxy global writes before later async-proxy

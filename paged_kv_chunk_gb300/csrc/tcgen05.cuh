@@ -57,24 +57,6 @@ __device__ __forceinline__ void umma_commit(uint32_t bar)
         : "memory");
 }
 
-// A pair of CTAs (cta_group::2, issued by the even one): D has A's rows of each CTA in that CTA's TMEM, B's rows
-// are half in one's shared memory and half in the other's, at the same offsets.
-__device__ __forceinline__ void umma_ss_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, int acc)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a), "l"(b), "r"(id), "r"(acc));
-}
-
-// Arrives at `bar`'s offset in both CTAs of the pair.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
-        : "memory");
-}
-
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -94,14 +76,6 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"         \
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),          \
                    "=r"(r[6]), "=r"(r[7])                                                           \
-                 : "r"(taddr))
-
-#define OASR_TMEM_LD16(taddr, r)                                                                   \
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"  \
-                 "%12,%13,%14,%15}, [%16];"                                                        \
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),          \
-                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),        \
-                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])                               \
                  : "r"(taddr))
 
 #define OASR_TMEM_ST32(taddr, r)                                                                   \
@@ -153,30 +127,14 @@ __device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// The same with acquire semantics in the cluster: for a barrier that another CTA's threads arrive on.
-__device__ __forceinline__ bool mbar_try_wait_sleep_cluster(uint32_t bar, uint32_t parity, uint32_t hint_ns)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(hint_ns)
-        : "memory");
-    return done != 0;
-}
-
 // Bounded wait that also gives up as soon as another role has aborted the CTA.
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort)
 {
-    // suspended until the phase completes, for 20 us at most between the checks below
-    auto wait = [&] { return CLUSTER ? mbar_try_wait_sleep_cluster(bar, parity, 20000u) : mbar_try_wait_sleep(bar, parity, 20000u); };
-    if (wait()) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
-        if (wait()) return true;
+        // suspended until the phase completes, for 20 us at most between the checks below
+        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
         if (*abort) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
