@@ -19,6 +19,19 @@ CUDA device; the layer's pools, the shared block table and cache lengths persist
     # a trained window commit with eviction:
     capi.oasr_window_commit(block_table, cache_seqlens, T, block_size, window_frames)
 
+The same step with an 8-bit cache (``float8_e4m3fn`` pools ``[num_blocks, H, block_size, 64]`` and ``uint8``
+scales ``[num_blocks, H, 2, block_size]``) and int8 projections::
+
+    x8, x_scale = capi.oasr_quantize_rows(x)               # weights once, in the same way
+    q, k_new, v_new, rel = capi.oasr_project_qkv_pos_w8a8(x8, x_scale, w_qkv8, w_qkv_scale, b_qkv,
+                                                          pos8, pos_scale, w_pos8, w_pos_scale, H)
+    out = capi.oasr_chunk_step_paged_e4m3(q.view(B, T, H, 64), k_new.view(B, T, H, 64),
+                                          v_new.view(B, T, H, 64), k_pool8, v_pool8, kv_scale,
+                                          block_table, cache_seqlens, pos_bias_u, pos_bias_v, rel)
+
+``oasr_paged_append_e4m3``, ``oasr_chunk_relattn_paged_e4m3`` and ``oasr_paged_read_e4m3`` are its parts and
+the way back; ``oasr_linear_w8a8`` is the int8 linear layer by itself.
+
 The offline pass over packed utterances is ``oasr_packed_relattn_varlen`` (or
 ``oasr_packed_relattn_chunked`` under the Nemotron chunked-limited window).
 """
