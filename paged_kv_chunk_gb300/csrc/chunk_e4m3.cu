@@ -324,7 +324,8 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, con
 // sum of 2^(s - m + E), where E is within 7 of the largest V scale exponent so far.
 struct E4Acc {
     float o[8][4];   // o[d]: dims 8 d + 2 t4, 8 d + 2 t4 + 1 of row g4, then of row g4 + 8
-    float m[2], l[2];
+    float m[2];
+    float2 l[2];     // a share of the even keys, one of the odd; lambda (in .x) from the join on
 };
 
 // One warp, 16 MT query rows against one slice.  x0: the position table's column of the slice's first key
@@ -389,13 +390,15 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
             far = __any_sync(0xffffffffu, mine < E - 40);
         }
     }
-    float ks[4], ev[4], back[4];
+    float2 ks[2], ev[2], back[2];   // by pairs of keys: two operations an instruction
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        ks[e] = __uint_as_float(__byte_perm(x.ks, 0u, 0x0444 | (e << 12)) >> 1);
-        const uint32_t w = __byte_perm(x.vs, 0x4b000000u, 0x7440 | e);
-        ev[e] = __uint_as_float(w) - 8388735.f;                    // 2^23 + 127
-        back[e] = __uint_as_float(static_cast<uint32_t>(E + 254) * 0x00800000u - w * 0x00800000u);
+    for (int n = 0; n < 2; ++n) {
+        auto kscale = [&](int e) { return __uint_as_float(__byte_perm(x.ks, 0u, 0x0444 | (e << 12)) >> 1); };
+        const uint32_t w0 = __byte_perm(x.vs, 0x4b000000u, 0x7440 | (2 * n)), w1 = __byte_perm(x.vs, 0x4b000000u, 0x7441 | (2 * n));
+        auto to_E = [&](uint32_t w) { return __uint_as_float(static_cast<uint32_t>(E + 254) * 0x00800000u - w * 0x00800000u); };
+        ks[n] = make_float2(kscale(2 * n), kscale(2 * n + 1));
+        ev[n] = __fadd2_rn(make_float2(__uint_as_float(w0), __uint_as_float(w1)), make_float2(-8388735.f, -8388735.f));   // 2^23 + 127
+        back[n] = make_float2(to_E(w0), to_E(w1));
     }
     uint32_t pa[MT][4];
 #pragma unroll
@@ -420,13 +423,14 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            const float gb[4] = {bf16_lo(y0[n]), bf16_hi(y0[n]), bf16_lo(y1[n]), bf16_hi(y1[n])};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = 2 * n + (e & 1);
-                s[mt][n][e] = fmaf(fmaf(s[mt][n][e], ks[k], gb[e]), sc[mt][e >> 1], ev[k]);
-                if (tail && 4 * t4 + k >= kvalid) s[mt][n][e] = -INFINITY;
-            }
+            auto score = [&](int e, uint32_t g, float sc1) {
+                const float2 t = __ffma2_rn(__ffma2_rn(make_float2(s[mt][n][e], s[mt][n][e + 1]), ks[n], make_float2(bf16_lo(g), bf16_hi(g))),
+                                            make_float2(sc1, sc1), ev[n]);
+                s[mt][n][e] = tail && 4 * t4 + 2 * n >= kvalid ? -INFINITY : t.x;
+                s[mt][n][e + 1] = tail && 4 * t4 + 2 * n + 1 >= kvalid ? -INFINITY : t.y;
+            };
+            score(0, y0[n], sc[mt][0]);
+            score(2, y1[n], sc[mt][1]);
             mx0 = fmax3(mx0, s[mt][n][0], s[mt][n][1]);
             mx1 = fmax3(mx1, s[mt][n][2], s[mt][n][3]);
         }
@@ -438,8 +442,9 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
             const float d0 = a.m[0] - mx0, d1 = a.m[1] - mx1;
             const float alpha0 = ex2_approx(d0), alpha1 = ex2_approx(d1);
-            a.l[0] *= ex2_approx(fminf(d0 + dE, 126.f));
-            a.l[1] *= ex2_approx(fminf(d1 + dE, 126.f));
+            const float beta0 = ex2_approx(fminf(d0 + dE, 126.f)), beta1 = ex2_approx(fminf(d1 + dE, 126.f));
+            a.l[0] = make_float2(a.l[0].x * beta0, a.l[0].y * beta0);
+            a.l[1] = make_float2(a.l[1].x * beta1, a.l[1].y * beta1);
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
                 a.o[d][0] *= alpha0;
@@ -457,22 +462,22 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int k = 2 * n + e;
-                    a.l[0] += ex2_approx(s[mt][n][e] - ev[k] - base0 + off);
-                    a.l[1] += ex2_approx(s[mt][n][2 + e] - ev[k] - base1 + off);
-                    back[k] = 0.f;
+                    const float v = e ? ev[n].y : ev[n].x;
+                    a.l[0].x += ex2_approx(s[mt][n][e] - v - base0 + off);
+                    a.l[1].x += ex2_approx(s[mt][n][2 + e] - v - base1 + off);
                 }
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            s[mt][n][0] = ex2_approx(s[mt][n][0] - base0);
-            s[mt][n][1] = ex2_approx(s[mt][n][1] - base0);
-            s[mt][n][2] = ex2_approx(s[mt][n][2] - base1);
-            s[mt][n][3] = ex2_approx(s[mt][n][3] - base1);
-            a.l[0] = fmaf(s[mt][n][0], back[2 * n], fmaf(s[mt][n][1], back[2 * n + 1], a.l[0]));
-            a.l[1] = fmaf(s[mt][n][2], back[2 * n], fmaf(s[mt][n][3], back[2 * n + 1], a.l[1]));
-            pa[mt][2 * n] = pack_f16(s[mt][n][0], s[mt][n][1]);
-            pa[mt][2 * n + 1] = pack_f16(s[mt][n][2], s[mt][n][3]);
+            const float2 t0 = __fadd2_rn(make_float2(s[mt][n][0], s[mt][n][1]), make_float2(-base0, -base0));
+            const float2 t1 = __fadd2_rn(make_float2(s[mt][n][2], s[mt][n][3]), make_float2(-base1, -base1));
+            const float2 p0 = make_float2(ex2_approx(t0.x), ex2_approx(t0.y)), p1 = make_float2(ex2_approx(t1.x), ex2_approx(t1.y));
+            if (!far) {
+                a.l[0] = __ffma2_rn(p0, back[n], a.l[0]);
+                a.l[1] = __ffma2_rn(p1, back[n], a.l[1]);
+            }
+            pa[mt][2 * n] = pack_f16(p0.x, p0.y);
+            pa[mt][2 * n + 1] = pack_f16(p1.x, p1.y);
         }
     }
 #pragma unroll
@@ -852,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
 #pragma unroll
             for (int d = 0; d < 8; ++d) acc[mt].o[d][0] = acc[mt].o[d][1] = acc[mt].o[d][2] = acc[mt].o[d][3] = 0.f;
             acc[mt].m[0] = acc[mt].m[1] = kNoMax;
-            acc[mt].l[0] = acc[mt].l[1] = 0.f;
+            acc[mt].l[0] = acc[mt].l[1] = make_float2(0.f, 0.f);
         }
         int E = -127;   // the smallest a scale byte says; the first keys raise it
         const int n = t.st1 - t.st0;
@@ -908,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                             make_float2(acc[mt].o[d][2 * half], acc[mt].o[d][2 * half + 1]);
                     if (t4 == 0) {
                         comb_m[row] = acc[mt].m[half];
-                        comb_l[row] = acc[mt].l[half];
+                        comb_l[row] = acc[mt].l[half].x;
                     }
                 }
         };
@@ -916,10 +921,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float l = acc[mt].l[half];
+                float l = acc[mt].l[half].x + acc[mt].l[half].y;
                 l += __shfl_xor_sync(0xffffffffu, l, 1);
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
-                acc[mt].l[half] = acc[mt].m[half] - static_cast<float>(E) + log2f(l);   // lambda from here on
+                acc[mt].l[half].x = acc[mt].m[half] - static_cast<float>(E) + log2f(l);   // lambda from here on
             }
         named_bar_sync(1, kE4Consumers);   // every warp is done with the table
         if (warp >= 2) put(warp - 2);
@@ -932,9 +937,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 for (int half = 0; half < 2; ++half) {
                     const int row = warp * Tp + 16 * mt + g4 + 8 * half;
                     const float m2 = comb_m[row], l2 = comb_l[row];
-                    const float m = fmaxf(acc[mt].m[half], m2), l = fmaxf(acc[mt].l[half], l2);
+                    const float m = fmaxf(acc[mt].m[half], m2), l = fmaxf(acc[mt].l[half].x, l2);
                     const float w1 = part_weight(acc[mt].m[half], m), w2 = part_weight(m2, m);
-                    acc[mt].l[half] = l + log2f(part_weight(acc[mt].l[half], l) + part_weight(l2, l));
+                    acc[mt].l[half].x = l + log2f(part_weight(acc[mt].l[half].x, l) + part_weight(l2, l));
                     acc[mt].m[half] = m;
 #pragma unroll
                     for (int d = 0; d < 8; ++d) {
