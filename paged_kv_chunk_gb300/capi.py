@@ -419,7 +419,7 @@ def _attention_e4m3(dev, q, pos_bias_u, pos_bias_v, rel, out, k_new=None, v_new=
     if len(r) != 3 or r[1] != H or r[2] != D:
         raise ValueError("rel must be [R, H, D]")
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=q.device)
+        out = torch.empty_like(q)
     elif out.shape != shape or out.dtype != dt:
         raise ValueError("out must be [B, T, H, D] of q's dtype")
     if k_new is not None and (k_new.shape != shape or v_new.shape != shape):
@@ -523,9 +523,9 @@ def oasr_project_qkv_pos_w8a8(x8, x_scale, w_qkv8, w_qkv_scale, b_qkv, pos8, pos
     if q is None:
         q = torch.empty(rows, dtype=dt, device=device)
     if k is None:
-        k = torch.empty(rows, dtype=dt, device=device)
+        k = torch.empty_like(q)
     if v is None:
-        v = torch.empty(rows, dtype=dt, device=device)
+        v = torch.empty_like(q)
     if rel is None:
         rel = torch.empty((R, H, D), dtype=dt, device=device)
     if q.shape != rows or k.shape != rows or v.shape != rows or rel.shape != (R, H, D):

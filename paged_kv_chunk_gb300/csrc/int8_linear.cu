@@ -231,12 +231,12 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
     const int rank = PAIR ? blockIdx.x & 1 : 0;   // in the pair; 0 issues the products of both
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(bar_full + 8 * i, kI8Group / 32 + (PAIR && rank == 0));
+            mbar_init(bar_full + 8 * i, kI8Group + (PAIR && rank == 0));
             mbar_init(bar_empty + 8 * i, 1);
         }
         for (int i = 0; i < R; ++i) {
             mbar_init(bar_raw + 8 * i, 1);
-            mbar_init(bar_raw_free + 8 * i, kI8Group / 32);
+            mbar_init(bar_raw_free + 8 * i, kI8Group);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_acc_full + 8 * i, 1);
@@ -391,13 +391,10 @@ __global__ void __launch_bounds__(kI8Threads, 1) linear_i8_kernel(
                     *reinterpret_cast<uint4*>(hi + 128 * CR * u) = i8_to_f16(buf[u].z, buf[u].w);
                 }
             fence_proxy_async_smem();
-            __syncwarp();
+            mbar_arrive_release(bar_full + 8 * slot);
             // the raw slot is released only here, its words converted: an arrival right behind the loads can
             // overtake them (they wait in another unit's queue), and a copy then lands under them
-            if (lane == 0) {
-                mbar_arrive_release(bar_full + 8 * slot);
-                mbar_arrive_release(bar_raw_free + 8 * rs);
-            }
+            mbar_arrive_release(bar_raw_free + 8 * rs);
         }
     } else {
         // --------------------------------------------------------------- epilogue
