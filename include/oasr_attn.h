@@ -306,7 +306,7 @@ oasr_status oasr_quantize_rows(const void* x, void* x8, float* scale, int M, int
  *   out[i][n] = (sum_k x8[i][k] * w8[n][k]) * x_scale[i] * w_scale[n] + bias[n]
  *
  * x8 [M, K] and w8 [N, K] int8, x_scale [M] and w_scale [N] fp32, bias [N] (null: none) and out [M, N]
- * of `dt`.  The sum is exact for K <= 1024 and for M <= 8 and is accumulated in fp32 otherwise; the
+ * of `dt`.  The sum is exact for K <= 1024 and for M <= 8 and may be accumulated in fp32 otherwise; the
  * scales and the bias are applied in that order in fp32, and the result is rounded once.  K a multiple
  * of 16, at most 65536; M and N at most 2^31 - 256; every pointer 16-byte aligned.
  */

@@ -600,6 +600,76 @@ __global__ void __launch_bounds__(256) linear_i8_few_kernel(const I8Problem p, E
     grid_dep_trigger();
 }
 
+// Some rows (nine to some dozens): a warp takes 16 rows and four output channels, its lanes every 32nd 16 bytes
+// of K, integer dot products; KS warps share the K of the same outputs.  A K step of the tensor-core kernel costs
+// 0.28 us whatever its tile holds, which is what these shapes would wait for: 16 x 512 x 4096 takes 8.1 us here and
+// 20.9 there, 9 x 512 x 2048 3.6 and 11.9, 64 x 512 x 2048 5.7 and 12.0 (K over 512 with KS = 1: 26.8, 9.2, 14.4).
+constexpr int kI8SomeRows = 16, kI8SomeCols = 4;
+
+template <int KS, typename Elem>
+__global__ void __launch_bounds__(128) linear_i8_some_kernel(const I8Problem p, Elem* __restrict__ out, int K)
+{
+    grid_dep_wait();
+    constexpr int MR = kI8SomeRows, NC = kI8SomeCols, G = 4 / KS;   // groups of KS warps in the block
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = (blockIdx.x * G + warp / KS) * NC, m0 = blockIdx.y * MR;
+    int acc[MR * NC];
+#pragma unroll
+    for (int i = 0; i < MR * NC; ++i) acc[i] = 0;
+    const int8_t* w[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) w[c] = p.w + static_cast<long long>(min(n0 + c, p.N - 1)) * K;   // surplus: not stored
+    for (int k = 16 * (lane + 32 * (warp % KS)); k < K; k += 512 * KS) {
+        int4 b[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) b[c] = __ldg(reinterpret_cast<const int4*>(w[c] + k));
+        const int8_t* x = p.x + static_cast<long long>(m0) * K + k;
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+            if (m0 + m < p.M) {
+                const int4 a = __ldg(reinterpret_cast<const int4*>(x + static_cast<long long>(m) * K));
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    acc[m * NC + c] = __dp4a(b[c].x, a.x, __dp4a(b[c].y, a.y, __dp4a(b[c].z, a.z, __dp4a(b[c].w, a.w, acc[m * NC + c]))));
+            }
+        }
+    }
+    // sums over the lanes, half of the values handed on at each step: lane L ends with values 2 L and 2 L + 1
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < 2 * o; ++i) {
+            const int give = up ? acc[i] : acc[i + 2 * o], keep = up ? acc[i + 2 * o] : acc[i];
+            acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    if constexpr (KS > 1) {
+        __shared__ int s_sum[4][MR * NC];
+        s_sum[warp][2 * lane] = acc[0];
+        s_sum[warp][2 * lane + 1] = acc[1];
+        __syncthreads();
+        if (warp % KS == 0)
+#pragma unroll
+            for (int j = 1; j < KS; ++j) {
+                acc[0] += s_sum[warp + j][2 * lane];
+                acc[1] += s_sum[warp + j][2 * lane + 1];
+            }
+    }
+    if (warp % KS == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = m0 + (2 * lane + e) / NC, n = n0 + (2 * lane + e) % NC;
+            if (m < p.M && n < p.N) {
+                const float bias = p.bias ? bias_at(static_cast<const Elem*>(p.bias), n) : 0.f;
+                put(out + static_cast<long long>(m) * p.N + n,
+                    __fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(acc[e]), __ldg(p.xs + m)), __ldg(p.ws + n)), bias));
+            }
+        }
+    }
+    grid_dep_trigger();
+}
+
 // --------------------------------------------------------------------------- host
 
 int g_smem_done_i8[8][64];
@@ -647,6 +717,16 @@ oasr_status launch_i8(I8Args a, int slot, int sms, cudaStream_t stream)
 // in fp32: 57 us in pairs, 87 in 128 x 128; 1024 x 768 x 256 in bf16: 7.0 in pairs, 5.2, 4.5 in 128 x 64 and 5.5 in
 // 128 x 32.  256 x 128 in pairs and 128 x 256 without were nowhere the fastest.
 template <typename Elem>
+oasr_status some_rows(const I8Problem& p, void* out, int K, cudaStream_t stream)
+{
+    const unsigned groups = (p.N + kI8SomeCols - 1) / kI8SomeCols, rows = (p.M + kI8SomeRows - 1) / kI8SomeRows;
+    if (K > 512)
+        return launch_pdl(linear_i8_some_kernel<4, Elem>, dim3(groups, rows), dim3(128), 0, stream, p, static_cast<Elem*>(out), K);
+    return launch_pdl(linear_i8_some_kernel<1, Elem>, dim3((groups + 3) / 4, rows), dim3(128), 0, stream, p,
+                      static_cast<Elem*>(out), K);
+}
+
+template <typename Elem>
 oasr_status dispatch_i8(const I8Args& a, cudaStream_t stream)
 {
     const int sms = sm_count();
@@ -666,6 +746,14 @@ oasr_status dispatch_i8(const I8Args& a, cudaStream_t stream)
             least = waves * wave + t.epilogue;
             best = k;
         }
+    }
+    // the integer kernel: blocks of 16 x 4 outputs (16 x 16 up to K = 512), four of them on an SM at a time, each
+    // 0.5 us and 2.0 for every round of its K.  Over 128 rows its reads of x pass the caches: 256 x 512 x 2048 takes
+    // 17.9 us there, 12.0 here
+    if (!a.p[1].M && a.p[0].M <= 128) {
+        const long long split = a.K > 512 ? 4 : 1, blocks = ((a.p[0].M + 15) / 16) * ((a.p[0].N + 16 / split - 1) / (16 / split));
+        const long long round = 500 + 2000 * ((a.K + 512 * split - 1) / (512 * split)), full = 4LL * sms;
+        if ((blocks > full ? round * blocks / full : round) < least) return some_rows<Elem>(a.p[0], a.out[0], a.K, stream);
     }
     constexpr int s = sizeof(Elem) == 4 ? 4 : 0;
     if (best == 0) return launch_i8<256, true, Elem>(a, s, sms, stream);

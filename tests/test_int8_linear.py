@@ -155,6 +155,24 @@ def test_linear(M, N, K, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(9, 37, 528), (16, 3, 2064), (33, 130, 4112), (128, 70, 1040), (100, 513, 80), (17, 4096, 1024),
+                                   (127, 501, 2048), (31, 512, 512)])
+def test_some_rows(M, N, K, dtype):
+    """Batches of a few dozen tokens: rows and columns that end inside a block, K that ends inside a round."""
+    g = torch.Generator().manual_seed(M * 5 + N + K)
+    x8, w8 = integers(g, M, K), integers(g, N, K)
+    xs, ws = torch.rand(M, generator=g) + 0.1, torch.rand(N, generator=g) * 1e-3
+    bias = torch.randn(N, generator=g).to(DT[dtype])
+    # a guard behind the last row stays as it was
+    out = torch.full((M + 1, N), 7.0, dtype=DT[dtype], device="cuda")
+    for b in (bias, None):
+        capi.oasr_linear_w8a8(x8.cuda(), xs.cuda(), w8.cuda(), ws.cuda(), None if b is None else b.cuda(), out=out[:M])
+        close(out[:M], product(x8, xs, w8, ws, b, DT[dtype]))
+        assert bool((out[M] == 7.0).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 8, 9, 140])
 def test_sums_are_the_integers(M):
     """The largest sums K = 1024 can have, and alternating ones, bit for bit."""
