@@ -28,7 +28,7 @@
 // What bounds it is issue: per 16 keys and 16 queries a warp converts 24 words, multiplies, adds the
 // position term, exponentiates and rounds; HBM is at a tenth to a third of its rate.  Device times: the
 // Conformer-large step (256 streams, 8 heads, 16 frames, window 512) 62 us, one stream and one frame over 8000
-// keys 14.6, 128 streams of 64 frames over 0 to 1024 keys 124.
+// keys 14.4, 128 streams of 64 frames over 0 to 1024 keys 122.
 #include "attn_core.cuh"
 #include "cluster.cuh"
 #include "e4m3.cuh"
