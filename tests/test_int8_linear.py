@@ -205,6 +205,35 @@ def test_tiles_of_every_shape_bit_for_bit(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(2600, 1100, 512), (300, 700, 512), (40, 500, 2048)])
+def test_captured_products_side_by_side(M, N, K):
+    """Two graphs of the same products on two streams at once, replayed over and over with new rows."""
+    w8 = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda")
+    ws = torch.rand(N, device="cuda")
+    jobs = []
+    for _ in range(2):
+        x8, xs = torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.rand(M, device="cuda")
+        out = capi.oasr_linear_w8a8(x8, xs, w8, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                capi.oasr_linear_w8a8(x8, xs, w8, ws, out=out)
+        jobs.append((x8, xs, out, graph, torch.cuda.Stream()))
+    for _ in range(5):
+        for x8, xs, _, _, _ in jobs:
+            x8.copy_(torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda"))
+        torch.cuda.synchronize()
+        for _, _, _, graph, stream in jobs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x8, xs, out, _, _ in jobs:
+            assert torch.equal(out, capi.oasr_linear_w8a8(x8, xs, w8, ws))
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_longest_rows():
     g = torch.Generator().manual_seed(2)
     for M in (3, 20):
