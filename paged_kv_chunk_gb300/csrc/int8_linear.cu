@@ -14,7 +14,7 @@
 // are read, written as fp16 and read by the matrix unit.  A pair of CTAs on one 256 x 256 tile
 // (cta_group::2) holds and converts each w row once for both, 96 KB of traffic per CTA and step
 // where a CTA alone on 128 x 256 has 144.  8191 x 4096 x 1024: 57 us in fp32, 51 in bf16
-// (1.2 and 1.35 PFLOP/s), 86 with 128 x 256 tiles.
+// (1.2 and 1.35 PFLOP/s); with 128 x 128 tiles 87 and 79.
 #include <type_traits>
 
 #include "attn_core.cuh"
