@@ -65,6 +65,7 @@ struct E4Args {
     int B, sorted;    // sorted: items of unequal streams go to the CTAs longest first
     int q_tiles, splits;
     float scale, scale_log2;   // the latter times log2(e)
+    uint32_t zero;             // 0, which the compiler does not know (mbar_arrive_after)
 };
 
 // Shared memory (byte offsets from a 1024-aligned base).
@@ -155,6 +156,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// Arrives on `bar` once the loads that `words` came from have returned: the arrival's address depends on them
+// (zero is 0).  A slot may only be released then: loads wait in another unit's queue than the arrival, which can
+// overtake them, and a copy then lands under them.  One word of a load is enough, its words come together.
+__device__ __forceinline__ void mbar_arrive_after(uint32_t bar, uint32_t words, uint32_t zero)
+{
+    mbar_arrive_release(bar + words * zero);
+}
+
 // A slice of 16 keys in registers: raw K and V words and scale bytes.  A lane's four keys are
 // neighbours, 4 t4 .. 4 t4 + 3: as columns of the scores they are columns 2 t4, 2 t4 + 1 of two 8-key tiles
 // (tile n holds keys 4 i + 2 n and 4 i + 2 n + 1), as rows of V the bytes of a transposed word.
@@ -167,8 +176,6 @@ struct E4Slice {
 // k_s, v_s: shared addresses of the slice's first rows; sc: its first K scale, v_off bytes before its first
 // V scale; far_off: bytes from the scales of keys 0 .. 7 to those of keys 8 .. 15 (pages of eight keys
 // hold 16 scales each).
-// K comes last: once a product has taken K's registers, all of the slice has been read (the loads complete
-// in order), and only then may the slot be released; an arrival right behind the loads can overtake them.
 // The lane's part of the addresses is computed once (E4Lane); the other rows and chunks it reads differ from
 // it in single bits of the swizzled offset.
 struct E4Lane {
@@ -259,10 +266,10 @@ __device__ __forceinline__ void load_a(uint32_t (&f)[4][4], const uint8_t* tile,
 // table G[i][c], c counting rel rows from the one of the last query's first key.  G[i][c] goes to
 // gs[i * kTableStride + (c + i + 1) % kTableW] rounded to bf16 (a relative 2^-8 of the position term, the
 // size of the rounding of q + v), so that query i and key j read column (j + Tp) % kTableW of row i.
-// Every lane arrives on release_bar once it has read its rows.
+// Every lane arrives on release_bar once it has read its rows (zero: see mbar_arrive_after).
 template <int MT>
 __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, const uint8_t* rows, int col0, int warp,
-                                            int lane, uint32_t release_bar)
+                                            int lane, uint32_t release_bar, uint32_t zero)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
     uint4 bl[2], bh[2];
@@ -291,7 +298,7 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, con
         mma_bf16_16816(c[1], qa[2], bh[1].x, bh[1].y);
         mma_bf16_16816(c[0], qa[3], bh[0].z, bh[0].w);
         mma_bf16_16816(c[1], qa[3], bh[1].z, bh[1].w);
-        if (mt == 0) mbar_arrive_release(release_bar);   // the rel rows are in registers
+        if (mt == 0) mbar_arrive_after(release_bar, __float_as_uint(c[0][0]) ^ __float_as_uint(c[1][0]), zero);
         // only the window's last slot can run over its end
         const int x = (col0 & (kTableW - 1)) + 8 * warp + 2 * t4 + 16 * mt + g4 + 1;
         const uint32_t w[4] = {pack_bf16(c[0][0], c[0][1]), pack_bf16(c[0][2], c[0][3]), pack_bf16(c[1][0], c[1][1]),
@@ -331,7 +338,7 @@ struct E4Acc {
 // One warp, 16 MT query rows against one slice.  x0: the position table's column of the slice's first key
 // (aligned: a multiple of 16, so that a lane's four keys are eight bytes of one row); keys [0, kvalid) of
 // the slice exist; sc: scale * log2(e) * 2^x of rows g4 and g4 + 8 of each m-tile.  Every lane arrives on
-// release_bar (unless 0) when the slice has been read.
+// release_bar (unless 0) when the slice has been read (zero: see mbar_arrive_after).
 //
 // P is 2^(t - m), at most one, and goes into the product as fp16: its rounding is 2^-11 of each
 // weight and never more than 2^-25 of the row's largest contribution, whatever the scales.  The
@@ -340,7 +347,8 @@ struct E4Acc {
 template <int MT>
 __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_tile, E4Slice& x,
                                            const uint16_t* gs, int x0, bool aligned, int kvalid,
-                                           const float (&sc)[MT][2], int& E, int lane, uint32_t release_bar)
+                                           const float (&sc)[MT][2], int& E, int lane, uint32_t release_bar,
+                                           uint32_t zero)
 {
     const int g4 = lane >> 2, t4 = lane & 3;
     float s[MT][2][4];
@@ -366,7 +374,6 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
             }
         }
     }
-    if (release_bar) mbar_arrive_release(release_bar);
     const bool tail = kvalid < 16;
     if (tail) {   // rows past the last key may hold anything: V bytes and scales (their scores are replaced below)
         const int have = max(0, min(4, kvalid - 4 * t4));
@@ -434,6 +441,8 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
             mx0 = fmax3(mx0, s[mt][n][0], s[mt][n][1]);
             mx1 = fmax3(mx1, s[mt][n][2], s[mt][n][3]);
         }
+        // the maximum has come of both K loads and both scale loads
+        if (mt == 0 && release_bar) mbar_arrive_after(release_bar, __float_as_uint(mx0) ^ x.v[0] ^ x.v[4], zero);
         // the reference only moves when a weight would pass 2^8 (fp16 holds 2^15)
         if (__any_sync(0xffffffffu, mx0 > a.m[0] + 8.f || mx1 > a.m[1] + 8.f) || dE != 0.f) {
             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
@@ -867,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
             if (!failed && !e4_wait(bar_full + 8 * (it % NS), (it / NS) & 1)) failed = true;
             if (!failed)
                 table_tiles<MT>(gs, sm + SP::off_qv, sm + (it % NS) * kE4Stage, kStageKeys * r, warp, lane,
-                                bar_empty + 8 * (it % NS));
+                                bar_empty + 8 * (it % NS), a.zero);
             ++it;
             ++r;
         };
@@ -886,7 +895,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 load_slice(x, ll, sb + slot * kE4Stage + jl * kE4Row, sb + slot * kE4Stage + (kStageKeys + jl) * kE4Row,
                            sb + sc_off + slot * 2 * kStageKeys, box);
             if (kv > 0)
-                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, s * kStageKeys + jl + Tp, true, kv, sc, E, lane, bar_empty + 8 * slot);
+                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, s * kStageKeys + jl + Tp, true, kv, sc, E, lane, bar_empty + 8 * slot,
+                               a.zero);
             else
                 mbar_arrive_release(bar_empty + 8 * slot);
         }
@@ -896,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 E4Slice x;
                 load_slice(x, e4_lane(lane, 8), sb + SP::off_ck, sb + SP::off_ck + kChunkRows * kE4Row, sb + SP::off_csc, kChunkRows);
                 const int x0 = t.C - t.st0 * kStageKeys + Tp;
-                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, x0, (x0 & 15) == 0, t.nc, sc, E, lane, 0u);
+                slice_e4m3<MT>(acc, sm + SP::off_qu, x, gs, x0, (x0 & 15) == 0, t.nc, sc, E, lane, 0u, 0u);
             }
         }
 

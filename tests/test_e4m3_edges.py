@@ -1,0 +1,25 @@
+"""The 8-bit attention where its pieces meet: ring slots used over and over, values at the ends of the formats."""
+import pytest
+import torch
+
+from paged_kv_chunk_gb300 import capi
+
+from test_e4m3_cache import check, make, step
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,C", [(40, 16, 700), (12, 40, 900), (3, 1, 4000)])
+def test_slots_are_refilled_only_once_read(B, T, C):
+    """Long histories, every ring slot refilled many times beside other CTAs: the same bits each time, and
+    those of the definition (a copy that lands under a slot's readers changes some of them)."""
+    c, x, lens = make(B, 4, T, [C - 5 * (b % 7) for b in range(B)], 16, "bf16", 70 + T)
+    pools = c.cuda()
+    outs = []
+    for fused in (True, False):
+        outs.append(step(c, x, lens, pools=pools, fused=fused)[0])
+        assert all(torch.equal(step(c, x, lens, pools=pools, fused=fused)[0], outs[-1]) for _ in range(15))
+    c.append(x["k_new"], x["v_new"], lens)
+    assert c.same(*pools[:3])
+    for out in outs:
+        check(c, x, lens, out, "bf16", streams=[0, B - 1])
+    assert capi.oasr_device_status() == 0
