@@ -757,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                     }
                 }
                 const int nvalid = __popc(__ballot_sync(0xffffffffu, valid) & 0xffffu);
+                __syncwarp();   // the zeros are written before the arrival (a ballot orders no memory)
                 if (lane == 0)
                     mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nbox * box * 2 * kE4Row + nvalid * 2 * box));
                 __syncwarp();

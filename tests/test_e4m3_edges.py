@@ -23,3 +23,21 @@ def test_slots_are_refilled_only_once_read(B, T, C):
     for out in outs:
         check(c, x, lens, out, "bf16", streams=[0, B - 1])
     assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 20])
+def test_bad_blocks_beside_nan_rows(T):
+    """Streams whose pages name no block take their turns in ring slots that held NaN scales: zero rows."""
+    B, C = 300, 90
+    c, x, lens = make(B, 2, T, [C] * B, 16, "bf16", 80 + T)
+    for b in range(0, B, 2):
+        c.scale[c.table[b].long()] = 255
+        c.table[b + 1, torch.arange(0, c.mbps - 2, 2)] = -1 - b
+    for fused in (True, False):
+        for _ in range(3):
+            out, _ = step(c, x, lens, fused=fused)
+            assert out[1::2].isfinite().all()
+    assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+    c.append(x["k_new"], x["v_new"], lens)
+    check(c, x, lens, out, "bf16", streams=range(1, B, 30))
