@@ -48,6 +48,7 @@ constexpr int kTableW = 256;                        // columns of the position t
 constexpr int kTableStride = kTableW + 16;          // 8 mod 32 words: 8-byte reads without conflicts
 constexpr int kOrderMax = 512;                      // streams of a cohort whose items are sorted by length
 constexpr int kMaxRowExp = 120;
+constexpr uint32_t kRowRoom = 30;                   // octaves a row's |q + v| may lie above its |q + u|, scaled as one
 constexpr float kNoMax = -3.0e38f;                  // the running maximum before any key
 
 struct E4Args {
@@ -209,31 +210,38 @@ __device__ __forceinline__ void load_slice(E4Slice& x, const E4Lane& l, uint32_t
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // Eight dims (chunk l8) of one query row, by eight neighbouring lanes: bf16(q + v) into the swizzled
-// tile qv and fp16(q + u) into qu, both times the power of two that brings the row's largest |q + u|
-// into [1, 2), and its inverse into row_pow.  u, v: the head's biases.
+// tile qv and fp16(q + u) into qu, both times a power of two 2^-x, and 2^x into row_pow.  u, v: the head's
+// biases.  x brings the row's largest |q + u| into [1, 2), but the largest |q + v| no further up than 2^31: where
+// q + u vanishes beside it (a padded frame, q = -u), 2^-x alone would take the position term past fp32's range.  Where
+// that holds x back, fp16 loses bits of q + u only if it is below 2^-44 of q + v.
 __device__ __forceinline__ void prepare_row(const uint8_t* q_tile, uint8_t* qv, uint8_t* qu, float* row_pow,
                                             const uint16_t* u, const uint16_t* v, int row, int l8)
 {
     const uint4 qw = *reinterpret_cast<const uint4*>(q_tile + swz128(row, l8));
     const uint4 uw = __ldg(reinterpret_cast<const uint4*>(u) + l8), vw = __ldg(reinterpret_cast<const uint4*>(v) + l8);
     const uint32_t q[4] = {qw.x, qw.y, qw.z, qw.w}, un[4] = {uw.x, uw.y, uw.z, uw.w}, vn[4] = {vw.x, vw.y, vw.z, vw.w};
-    float a[8];
-    float m = 0.f;
+    float a[8], p[8];
+    float m = 0.f, mp = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         a[2 * i] = bf16_lo(q[i]) + bf16_lo(un[i]);
         a[2 * i + 1] = bf16_hi(q[i]) + bf16_hi(un[i]);
+        p[2 * i] = bf16_lo(q[i]) + bf16_lo(vn[i]);
+        p[2 * i + 1] = bf16_hi(q[i]) + bf16_hi(vn[i]);
         m = fmax3(m, fabsf(a[2 * i]), fabsf(a[2 * i + 1]));
+        mp = fmax3(mp, fabsf(p[2 * i]), fabsf(p[2 * i + 1]));
     }
+    // the exponents' maximum is that of m and 2^-30 mp (signs are clear, so bits order as the values do)
+    uint32_t e = max(__float_as_uint(m), max(__float_as_uint(mp), kRowRoom << 23) - (kRowRoom << 23));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int x = max(-kMaxRowExp, min(kMaxRowExp, static_cast<int>(__float_as_uint(m) >> 23) - 127));
+    for (int o = 1; o < 8; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+    const int x = max(-kMaxRowExp, min(kMaxRowExp, static_cast<int>(e >> 23) - 127));
     const float f = pow2(-x);
     uint32_t pu[4], pv[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         pu[i] = pack_f16(a[2 * i] * f, a[2 * i + 1] * f);
-        pv[i] = pack_bf16((bf16_lo(q[i]) + bf16_lo(vn[i])) * f, (bf16_hi(q[i]) + bf16_hi(vn[i])) * f);
+        pv[i] = pack_bf16(p[2 * i] * f, p[2 * i + 1] * f);
     }
     *reinterpret_cast<uint4*>(qu + swz128(row, l8)) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
     *reinterpret_cast<uint4*>(qv + swz128(row, l8)) = make_uint4(pv[0], pv[1], pv[2], pv[3]);

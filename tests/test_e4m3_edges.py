@@ -41,3 +41,29 @@ def test_bad_blocks_beside_nan_rows(T):
     assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
     c.append(x["k_new"], x["v_new"], lens)
     check(c, x, lens, out, "bf16", streams=range(1, B, 30))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("T", [5, 20])
+@pytest.mark.parametrize("kind", ["q = u = 0", "q = -u", "tiny"])
+def test_rows_without_a_content_term(kind, T, sign):
+    """Query rows whose q + u is zero (a padded frame where u is zero) or next to it, with a position term far
+    above: 64 products of +-1 and 4, some of them turned, a logit of up to 32."""
+    c, x, lens = make(2, 2, T, [70, 0], 16, "bf16", 90 + T)
+    x["vb"] = torch.full((2, 64), float(sign), dtype=torch.bfloat16)
+    x["rel"] = torch.full_like(x["rel"], 4.0)
+    turned = torch.arange(x["rel"].shape[0]) % 5
+    for i in range(x["rel"].shape[0]):
+        x["rel"][i, :, :6 * int(turned[i])] *= -1
+    if kind == "q = u = 0":
+        x["q"][:, ::2], x["u"] = 0, torch.zeros_like(x["u"])
+    elif kind == "q = -u":
+        x["q"][:, ::2] = -x["u"]
+        x["vb"] = x["vb"] * 2.0 ** 4
+        x["rel"] = x["rel"] * 0.25
+    else:
+        x["q"][:, ::2], x["u"] = x["q"][:, ::2] * 2.0 ** -120, x["u"] * 2.0 ** -120
+    out, _ = step(c, x, lens)
+    c.append(x["k_new"], x["v_new"], lens)
+    check(c, x, lens, out, "bf16")
