@@ -262,7 +262,8 @@ oasr_status oasr_paged_read_e4m3(const void* k_pool, const void* v_pool, const v
  * stand for.  D = 64; 1 <= T <= 64; block_size a power of two in [8, 256]; max_blocks_per_seq <= 512;
  * num_blocks * H * block_size < 2^31.  A stream with C_b + T > max_blocks_per_seq * block_size has the
  * keys past the table dropped; distances the rel table lacks (R < C_b + 2T - 1) count as zero rows; an
- * invalid block id reads as zero rows; each raises OASR_ERR_BOUNDS.
+ * invalid block id reads as zero rows; a stream of negative C_b has output rows that are unspecified; each
+ * raises OASR_ERR_BOUNDS.
  * bf16: the chunk, biases, rel and out are bf16; q + v and the position term are rounded to bf16, q + u
  * and the weights to fp16 (a weight with its key's V scale, relative to the row's largest such), everything
  * else is fp32.  f32: fp32 throughout.
@@ -279,7 +280,8 @@ oasr_status oasr_chunk_relattn_paged_e4m3(const void* q, const void* k_pool, con
  * One fused streaming step over the 8-bit cache: oasr_paged_append_e4m3 followed by
  * oasr_chunk_relattn_paged_e4m3 (in one launch for bf16 and T <= 16, else in two).  The chunk's own keys are
  * attended to as quantised, so the result is that of the two calls up to summation order, and the
- * pools afterwards are bit-identical.  The requirements of both apply.  Block ids of different streams
+ * pools afterwards are bit-identical (rows that the append drops, at negative positions too, are dropped here).
+ * The requirements of both apply.  Block ids of different streams
  * must not alias a block that this step writes.
  */
 oasr_status oasr_chunk_step_paged_e4m3(const void* q, const void* k_new, const void* v_new,

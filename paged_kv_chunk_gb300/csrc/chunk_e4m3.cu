@@ -557,6 +557,7 @@ __device__ __forceinline__ float part_weight(float x, float top) { return x <= k
 // What a CTA does with one item: keys, ring slots and the position table, from the stream's cache length.
 struct E4Item {
     int C, K;          // cached frames; keys (frames and chunk, as far as the table reaches)
+    int p0;            // position of the chunk's first row: C, or below zero where the length is (no row there)
     int kc, nc;        // keys from the pool, from the chunk region
     int st0, st1;      // stages of this CTA's share
     int nrel;          // rel slots: the table has a column for each distance of the share's keys
@@ -570,6 +571,7 @@ __device__ __forceinline__ E4Item e4_item(const E4Args& a, int C, int split)
     E4Item t;
     t.err = 0;
     const int cap = a.mbps << a.bs_shift;                 // keys the block table holds (at most 2^17)
+    t.p0 = max(C, -kE4MaxT);
     if (C < 0) { C = 0; t.err = kErrBounds; }
     if (C > cap) { C = cap; t.err = kErrBounds; }
     t.C = C;
@@ -832,8 +834,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
         if (FUSED && t.nc > 0 && !failed) {
             // the chunk's rows, eight lanes each: quantised into the chunk region (rows past T zero) and the pool
             const int r = tid >> 3, l8 = lane & 7;
-            const int p = t.C + r;
-            const int blk = r < t.nc ? s_bt[(n_items & 1) * a.mbps + (p >> sh)] : -1;
+            const int p = t.p0 + r;
+            const int blk = r < t.nc && p >= 0 ? s_bt[(n_items & 1) * a.mbps + (p >> sh)] : -1;
             const bool valid = blk >= 0 && blk < a.num_blocks;
             if (r < t.nc && !valid) err |= kErrBounds;   // dropped by the append: reads as zeros
             const long long page = static_cast<long long>(valid ? blk : 0) * H + h;

@@ -67,3 +67,21 @@ def test_rows_without_a_content_term(kind, T, sign):
     out, _ = step(c, x, lens)
     c.append(x["k_new"], x["v_new"], lens)
     check(c, x, lens, out, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bs", [8, 32])
+@pytest.mark.parametrize("T,dtype", [(1, "bf16"), (6, "bf16"), (16, "bf16"), (20, "bf16"), (6, "f32")])
+def test_negative_lengths(T, dtype, bs):
+    """Rows at negative positions are dropped on every path: the fused step writes what the append does, the
+    other streams are attended to as ever."""
+    c, x, lens = make(4, 2, T, [20, 21, 22, 23], bs, dtype, 100 + T)
+    lens = torch.tensor([-2, 21, -1000, -2 ** 31], dtype=torch.int32)
+    for fused in (True, False):
+        capi.oasr_device_status()
+        out, pools = step(c, x, lens, fused=fused)
+        assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+        d, _, _ = make(4, 2, T, [20, 21, 22, 23], bs, dtype, 100 + T)
+        d.append(x["k_new"], x["v_new"], lens)
+        assert d.same(*pools[:3])
+        check(d, x, lens, out, dtype, streams=[1])
