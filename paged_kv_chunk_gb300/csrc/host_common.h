@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "oasr_attn.h"
 
 namespace oasr {
@@ -91,17 +93,23 @@ oasr_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
     return launch_status();
 }
 
-// Raise the dynamic shared-memory limit of `func` once per device.
+// Held while a kernel's attributes are changed: calls from several threads may want different ones.
+inline std::mutex g_attribute_mutex;
+
+// Raise the dynamic shared-memory limit of `func` on the current device to at least `bytes`; done: the limits
+// set so far, by device.  They only ever rise, whatever the threads that call it at once want.
 template <typename F>
 bool ensure_smem(F* func, int bytes, int (&done)[64])
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (__atomic_load_n(&done[dev], __ATOMIC_ACQUIRE) >= bytes) return true;
+    std::lock_guard<std::mutex> lock(g_attribute_mutex);
     if (done[dev] >= bytes) return true;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(func),
                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return false;
-    done[dev] = bytes;
+    __atomic_store_n(&done[dev], bytes, __ATOMIC_RELEASE);
     return true;
 }
 

@@ -1,4 +1,6 @@
 """The 8-bit attention where its pieces meet: ring slots used over and over, values at the ends of the formats."""
+import threading
+
 import pytest
 import torch
 
@@ -85,3 +87,36 @@ def test_negative_lengths(T, dtype, bs):
         d.append(x["k_new"], x["v_new"], lens)
         assert d.same(*pools[:3])
         check(d, x, lens, out, dtype, streams=[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [4, 24])
+def test_threads_with_tables_of_many_widths(T):
+    """The shared memory of a launch grows with the block table: threads that want different amounts at once."""
+    jobs = []
+    for i, mbps in enumerate((512, 30, 400, 35)):
+        c, x, lens = make(2, 1, T, [150 + i, 7], 8, "bf16", 110 + i, mbps=mbps)
+        jobs.append((c, x, lens, c.cuda()))
+    torch.cuda.synchronize()
+    outs, wrong = [None] * len(jobs), []
+
+    def work(i):
+        c, x, lens, pools = jobs[i]
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    outs[i], _ = step(c, x, lens, pools=pools)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    for (c, x, lens, pools), out in zip(jobs, outs):
+        c.append(x["k_new"], x["v_new"], lens)
+        assert c.same(*pools[:3])
+        check(c, x, lens, out, "bf16")
