@@ -1310,9 +1310,10 @@ long long e4_splits(E4Args& a, int B, int Tp, int k_max)
     return pairs;
 }
 
-template <int MT, int NS, int CTAS, bool FUSED>
+// first: enqueues what goes before the kernel, once nothing but the launch itself can fail.
+template <int MT, int NS, int CTAS, bool FUSED, typename First>
 oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const void* rel, E4Args& a, int k_max, int B,
-                      int slot, cudaStream_t stream)
+                      int slot, cudaStream_t stream, First first)
 {
     using SP = E4Smem<MT, NS, FUSED>;
     CUtensorMap tm_q, tm_k, tm_v, tm_r, tm_kn, tm_vn;
@@ -1329,12 +1330,12 @@ oasr_status launch_e4(const void* q, const void* k_new, const void* v_new, const
     const int smem = SP::bytes + 2 * a.mbps * 4;
     if (!ensure_smem(kern, smem, g_smem_done_e4[slot]) || !ensure_clusters(kern, g_clusters_e4[slot])) return OASR_ERR_CUDA;
     const long long pairs = e4_splits(a, B, SP::Tp, k_max);
-    if (pairs > 0x7fffffffLL / 2) return OASR_ERR_UNSUPPORTED;
     a.items = static_cast<int>(pairs);
     a.B = B;
     const long long most = static_cast<long long>(CTAS) * sm_count();
     const long long ctas = a.splits > 1 ? pairs * a.splits : pairs < most ? pairs : most;
     a.sorted = a.splits == 1 && pairs > ctas && B <= kOrderMax;
+    if (const oasr_status st = first(); st != OASR_OK) return st;
     return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, a.splits, stream, tm_q, tm_k, tm_v,
                               tm_r, tm_kn, tm_vn, static_cast<const E4Args>(a));
 }
@@ -1361,14 +1362,18 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     const void* ptrs[] = {q, k_pool, v_pool, kv_scale, u, vb, rel, out, FUSED ? k_new : q, FUSED ? v_new : q};
     for (const void* p : ptrs)
         if (!aligned16(p)) return OASR_ERR_INVALID_ARG;
+    // (stream, head, query tile) items are 32-bit numbers; fp32 has a CTA for each
+    const int Tp = dt == OASR_F32 || T <= 16 ? 16 : 32;
+    if (static_cast<long long>(B) * H * ((T + Tp - 1) / Tp) > (dt == OASR_F32 ? 0x7fffffffLL : 0x7fffffffLL / 2))
+        return OASR_ERR_UNSUPPORTED;
     unsigned* status = status_word();
     if (!status || !sm_count()) return OASR_ERR_CUDA;
     // more than one m-tile of queries (and fp32): the append first, then the attention over the pool
-    if (FUSED && (dt == OASR_F32 || T > 16)) {
-        const oasr_status st = oasr_paged_append_e4m3(k_new, v_new, k_pool, v_pool, kv_scale, num_blocks, block_size,
-                                                      bt, mbps, cs, B, T, H, D, dt, stream);
-        if (st != OASR_OK) return st;
-    }
+    auto append = [&] {
+        if (!FUSED || (dt == OASR_BF16 && T <= 16)) return OASR_OK;
+        return oasr_paged_append_e4m3(k_new, v_new, k_pool, v_pool, kv_scale, num_blocks, block_size, bt, mbps, cs, B, T,
+                                      H, D, dt, stream);
+    };
     E4Args a = {};
     a.k_pool = static_cast<uint8_t*>(k_pool);
     a.v_pool = static_cast<uint8_t*>(v_pool);
@@ -1394,10 +1399,10 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     const int km = static_cast<int>(k_max < T ? T : k_max);
     if (dt == OASR_F32) {
         const long long pairs = e4_splits(a, B, kFRows, km);
-        if (pairs * a.splits > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
         if (!ensure_smem(chunk_e4m3_f32_kernel, sizeof(F32Smem), g_smem_done_e4[3]) ||
             !ensure_clusters(chunk_e4m3_f32_kernel, g_clusters_e4[3]))
             return OASR_ERR_CUDA;
+        if (const oasr_status st = append(); st != OASR_OK) return st;
         return launch_pdl_cluster(chunk_e4m3_f32_kernel, dim3(static_cast<unsigned>(pairs * a.splits)), dim3(kFThreads),
                                   static_cast<int>(sizeof(F32Smem)), a.splits, stream, static_cast<const float*>(q),
                                   static_cast<const uint8_t*>(a.k_pool), static_cast<const uint8_t*>(a.v_pool),
@@ -1407,8 +1412,8 @@ oasr_status dispatch_e4(const void* q, const void* k_new, const void* v_new, voi
     }
     // 32 queries a CTA convert each key once for both m-tiles, and two CTAs fit an SM's registers: 76 streams of 64
     // queries over 960 keys take 102 us, 112 with tiles of 16 (three CTAs), 108 with three CTAs and spills
-    if (T <= 16) return launch_e4<1, kSlots, 3, FUSED>(q, k_new, v_new, rel, a, km, B, FUSED ? 1 : 0, stream);
-    return launch_e4<2, kSlots, 2, false>(q, k_new, v_new, rel, a, km, B, 2, stream);
+    if (T <= 16) return launch_e4<1, kSlots, 3, FUSED>(q, k_new, v_new, rel, a, km, B, FUSED ? 1 : 0, stream, append);
+    return launch_e4<2, kSlots, 2, false>(q, k_new, v_new, rel, a, km, B, 2, stream, append);
 }
 
 }  // namespace

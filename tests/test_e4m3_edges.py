@@ -4,10 +4,33 @@ import threading
 import pytest
 import torch
 
-from paged_kv_chunk_gb300 import capi
+from paged_kv_chunk_gb300 import build, capi
 
 from test_e4m3_cache import check, make, step
 
+# ------------------------------------------------------------------- CPU
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return capi.load()
+
+
+FAKE = 1 << 20
+
+
+@pytest.mark.parametrize("dt,H", [(capi.OASR_BF16, 33), (capi.OASR_F32, 43)])
+def test_too_many_items_are_refused_before_the_append(lib, dt, H):
+    """2^24 streams of 33 frames are rows that the append takes, but more query tiles than the attention can count:
+    the step says so before it looks for a device, and so before it enqueues the append."""
+    a = dict(q=FAKE, k=FAKE, v=FAKE, kp=FAKE, vp=FAKE, sc=FAKE, nb=16, bs=16, bt=FAKE, mbps=8, cs=FAKE, u=FAKE,
+             vb=FAKE, rel=FAKE, R=95, out=FAKE, B=1 << 24, T=33, H=H, D=64, scale=0.125, dt=dt)
+    assert lib.oasr_chunk_step_paged_e4m3(*a.values(), None) == capi.OASR_ERR_UNSUPPORTED
+    del a["k"], a["v"]
+    assert lib.oasr_chunk_relattn_paged_e4m3(*a.values(), None) == capi.OASR_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------- GPU
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,T,C", [(40, 16, 700), (12, 40, 900), (3, 1, 4000)])
