@@ -336,7 +336,8 @@ __device__ __forceinline__ void table_tiles(uint16_t* gs, const uint8_t* qv, con
 
 // Running state of 16 query rows of one warp.  With t_ij = s_ij + ev_j (log2 units: the size of key j's
 // contribution to the output), m is the running maximum of t, o the sum of 2^(t - m) v8 and l the
-// sum of 2^(s - m + E), where E is within 7 of the largest V scale exponent so far.
+// sum of 2^(s - m + E - kSumRoom), where E is within 7 of the largest V scale exponent so far.
+constexpr int kSumRoom = 70;
 struct E4Acc {
     float o[8][4];   // o[d]: dims 8 d + 2 t4, 8 d + 2 t4 + 1 of row g4, then of row g4 + 8
     float m[2];
@@ -350,8 +351,10 @@ struct E4Acc {
 //
 // P is 2^(t - m), at most one, and goes into the product as fp16: its rounding is 2^-11 of each
 // weight and never more than 2^-25 of the row's largest contribution, whatever the scales.  The
-// row sum takes p back out of it, l += P 2^(E - ev); a slice with a scale below 2^(E - 40) (a row of
-// zeros has 2^-100), where that could underflow, sums 2^(s - m + E) of its own.
+// row sum takes p back out of it, l += P 2^(E - ev - kSumRoom); a slice with a scale below 2^(E - 40) (a row of
+// zeros has 2^-100), where that could underflow, sums 2^(s - m + E - kSumRoom) of its own.  A key of far smaller
+// scale can have a score far above m - E; its term and the sum then stop at 2^90 and 2^100, of which the terms
+// of the largest contributions, 2^-kSumRoom, are less than 2^-150: no more than fp32 weights can tell from nothing.
 template <int MT>
 __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_tile, E4Slice& x,
                                            const uint16_t* gs, int x0, bool aligned, int kvalid,
@@ -390,7 +393,7 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
         for (int i = 0; i < 8; ++i) x.v[i] &= mask;
         x.vs = (x.vs & mask) | (static_cast<uint32_t>(E + 127) * 0x01010101u & ~mask);
     }
-    // keys 4 t4 ..: 2^ek, ev and 2^(E - ev), from the scale bytes in place
+    // keys 4 t4 ..: 2^ek, ev and 2^(E - ev - kSumRoom), from the scale bytes in place
     // (0x4b000000 | byte is 2^23 + byte)
     bool far = false;
     float dE = 0.f;
@@ -410,7 +413,7 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
     for (int n = 0; n < 2; ++n) {
         auto kscale = [&](int e) { return __uint_as_float(__byte_perm(x.ks, 0u, 0x0444 | (e << 12)) >> 1); };
         const uint32_t w0 = __byte_perm(x.vs, 0x4b000000u, 0x7440 | (2 * n)), w1 = __byte_perm(x.vs, 0x4b000000u, 0x7441 | (2 * n));
-        auto to_E = [&](uint32_t w) { return __uint_as_float(static_cast<uint32_t>(E + 254) * 0x00800000u - w * 0x00800000u); };
+        auto to_E = [&](uint32_t w) { return __uint_as_float(static_cast<uint32_t>(E + 254 - kSumRoom) * 0x00800000u - w * 0x00800000u); };
         ks[n] = make_float2(kscale(2 * n), kscale(2 * n + 1));
         ev[n] = __fadd2_rn(make_float2(__uint_as_float(w0), __uint_as_float(w1)), make_float2(-8388735.f, -8388735.f));   // 2^23 + 127
         back[n] = make_float2(to_E(w0), to_E(w1));
@@ -459,9 +462,10 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
             const float d0 = a.m[0] - mx0, d1 = a.m[1] - mx1;
             const float alpha0 = ex2_approx(d0), alpha1 = ex2_approx(d1);
-            const float beta0 = ex2_approx(fminf(d0 + dE, 126.f)), beta1 = ex2_approx(fminf(d1 + dE, 126.f));
-            a.l[0] = make_float2(a.l[0].x * beta0, a.l[0].y * beta0);
-            a.l[1] = make_float2(a.l[1].x * beta1, a.l[1].y * beta1);
+            // l by halves: the factor may pass fp32's range where l is small
+            const float h0 = ex2_approx(0.5f * (d0 + dE)), h1 = ex2_approx(0.5f * (d1 + dE));
+            a.l[0] = make_float2(fminf(a.l[0].x * h0 * h0, 0x1p100f), fminf(a.l[0].y * h0 * h0, 0x1p100f));
+            a.l[1] = make_float2(fminf(a.l[1].x * h1 * h1, 0x1p100f), fminf(a.l[1].y * h1 * h1, 0x1p100f));
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
                 a.o[d][0] *= alpha0;
@@ -474,14 +478,14 @@ __device__ __forceinline__ void slice_e4m3(E4Acc (&acc)[MT], const uint8_t* qu_t
         }
         const float base0 = a.m[0], base1 = a.m[1];
         if (far) {
-            const float off = static_cast<float>(E);
+            const float off = static_cast<float>(E - kSumRoom);
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float v = e ? ev[n].y : ev[n].x;
-                    a.l[0].x += ex2_approx(s[mt][n][e] - v - base0 + off);
-                    a.l[1].x += ex2_approx(s[mt][n][2 + e] - v - base1 + off);
+                    a.l[0].x += ex2_approx(fminf(s[mt][n][e] - v - base0 + off, 90.f));
+                    a.l[1].x += ex2_approx(fminf(s[mt][n][2 + e] - v - base1 + off, 90.f));
                 }
         }
 #pragma unroll
@@ -549,7 +553,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank)
 // Weight of a share whose maximum (log2) is `x` against the largest, `top`; a share without keys has
 // kNoMax (or -inf) and weight 0.
 //
-// Shares of a row are joined from o, m and lambda = log2(sum of 2^s) = m - E + log2(l): the V scales
+// Shares of a row are joined from o, m and lambda = log2(sum of 2^s) = m - E + kSumRoom + log2(l): the V scales
 // move m away from the scores (a share of zero rows has an m of s - 100), so the row sum has a
 // maximum of its own.  out = sum(o 2^(m - m*)) 2^(m* - lambda*) / sum(2^(lambda - lambda*)).
 __device__ __forceinline__ float part_weight(float x, float top) { return x <= kNoMax ? 0.f : ex2_approx(x - top); }
@@ -945,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
                 float l = acc[mt].l[half].x + acc[mt].l[half].y;
                 l += __shfl_xor_sync(0xffffffffu, l, 1);
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
-                acc[mt].l[half].x = acc[mt].m[half] - static_cast<float>(E) + log2f(l);   // lambda from here on
+                acc[mt].l[half].x = acc[mt].m[half] - static_cast<float>(E - kSumRoom) + log2f(l);   // lambda from here on
             }
         named_bar_sync(1, kE4Consumers);   // every warp is done with the table
         if (warp >= 2) put(warp - 2);

@@ -6,6 +6,7 @@ import torch
 
 from paged_kv_chunk_gb300 import build, capi
 
+import e4m3_ref as ref
 from test_e4m3_cache import check, make, step
 
 # ------------------------------------------------------------------- CPU
@@ -143,3 +144,37 @@ def test_threads_with_tables_of_many_widths(T):
         c.append(x["k_new"], x["v_new"], lens)
         assert c.same(*pools[:3])
         check(c, x, lens, out, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 20])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("loud", [2.0 ** 40, 2.0 ** 100])
+@pytest.mark.parametrize("gap", [100, 140, 200])
+@pytest.mark.parametrize("order", ["early", "late", "apart", "rising"])
+def test_zero_value_rows_with_all_the_weight(order, gap, loud, dtype, T):
+    """Keys whose value rows are zero take the whole weight, `gap` octaves above keys of large values: in the same
+    slices of keys, in stages before them, before stages of rising values.  The row sum spans the scales' range and
+    the output is that of the definition, next to nothing.
+
+    The bound takes in what fp32 weights cannot hold: one below 2^-126 may count as zero, at most C + T of them
+    with values up to max|v|."""
+    C = 220
+    c, x, lens = make(1, 2, T, [C], 16, dtype, 120, fill=False)
+    k, v = torch.zeros(1, C, 2, 64), torch.randn(1, C, 2, 64, generator=torch.Generator().manual_seed(gap)) * loud
+    at = dict(early=[1, 70], late=[14, 218], apart=list(range(64)), rising=list(range(64)))[order]
+    k[:, at], v[:, at] = 1.0, 0.0
+    if order == "rising":
+        v[:, 64:128] *= 2.0 ** -20 / loud
+        v[:, 128:192] *= loud ** -0.5
+    c.append(k.to(x["q"].dtype), v.to(x["q"].dtype), [0])
+    x["q"], x["u"] = torch.full_like(x["q"], gap * 0.6931 / 8), torch.zeros_like(x["u"])     # 64 products times 1/8
+    x["rel"], x["k_new"], x["v_new"] = (torch.zeros_like(x[n]) for n in ("rel", "k_new", "v_new"))
+    out, pools = step(c, x, lens)
+    c.append(x["k_new"], x["v_new"], lens)
+    assert c.same(*pools[:3])
+    history = c.history(0, C + T)
+    want, tol = ref.attention(x["q"][0], x["u"], x["vb"], x["rel"], history, C, 0.125, x["q"].dtype)
+    tol = tol + (C + T) * 2.0 ** -126 * float(history[1].abs().max())
+    err = (out[0].double().cpu() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
