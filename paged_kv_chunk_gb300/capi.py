@@ -326,6 +326,12 @@ def _code(dtype) -> int:
     return code
 
 
+def _fits(*sizes):
+    """Sizes reach the library as C ints, which ctypes would cut off without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError("sizes must be below 2^31")
+
+
 def _lib_device():
     """The library and the current device (-2 without one: no tensor is on it)."""
     try:
@@ -350,6 +356,7 @@ def _cache_e4m3(dev, k_pool, v_pool, kv_scale, block_table, cache_seqlens, B, H,
     table = block_table.shape
     if len(table) != 2 or table[0] != B or cache_seqlens.shape != (B,):
         raise ValueError("block_table must be [B, mbps] and cache_seqlens [B]")
+    _fits(nb, bs, table[1])
     if not (_good(dev, torch.float8_e4m3fn, k_pool, v_pool) and _good(dev, torch.uint8, kv_scale)
             and _good(dev, torch.int32, block_table, cache_seqlens)):
         _refuse(k_pool=(k_pool, torch.float8_e4m3fn), v_pool=(v_pool, torch.float8_e4m3fn),
@@ -386,6 +393,7 @@ def oasr_paged_read_e4m3(k_pool, v_pool, kv_scale, block_table, cache_seqlens, l
     _, H, _, D = k_pool.shape
     if n < 1:
         raise ValueError("length must be at least 1")
+    _fits(n)
     if start is not None and start.shape != (B,):
         raise ValueError("start must be [B]")
     nb, bs, mbps = _cache_e4m3(dev, k_pool, v_pool, kv_scale, block_table, cache_seqlens, B, H, D)
@@ -466,6 +474,7 @@ def oasr_quantize_rows(x, x8=None, scale=None, stream=None):
     dt = x.dtype
     code = _code(dt)
     M, K = x.shape
+    _fits(M, K)
     if x8 is None:
         x8 = torch.empty((M, K), dtype=torch.int8, device=x.device)
     if scale is None:
@@ -486,6 +495,7 @@ def oasr_linear_w8a8(x8, x_scale, w8, w_scale, bias=None, out=None, out_dtype=to
     L, dev = _lib_device()
     M, K = x8.shape
     N, Kw = w8.shape
+    _fits(M, N, K)
     if Kw != K or x_scale.shape != (M,) or w_scale.shape != (N,):
         raise ValueError("shapes: x8 [M,K], x_scale [M], w8 [N,K], w_scale [N]")
     if out is None:
@@ -511,6 +521,7 @@ def oasr_project_qkv_pos_w8a8(x8, x_scale, w_qkv8, w_qkv_scale, b_qkv, pos8, pos
     L, dev = _lib_device()
     M, d = x8.shape
     R = pos8.shape[0]
+    _fits(M, R, d)
     if w_qkv8.shape != (3 * d, d) or w_qkv_scale.shape != (3 * d,) or b_qkv.shape != (3 * d,) or \
             pos8.shape != (R, d) or w_pos8.shape != (d, d) or w_pos_scale.shape != (d,) or \
             x_scale.shape != (M,) or pos_scale.shape != (R,) or d % H:
