@@ -266,7 +266,8 @@ oasr_status oasr_paged_read_e4m3(const void* k_pool, const void* v_pool, const v
  * raises OASR_ERR_BOUNDS.
  * bf16: the chunk, biases, rel and out are bf16; q + v and the position term are rounded to bf16, q + u
  * and the weights to fp16 (a weight with its key's V scale, relative to the row's largest such), everything
- * else is fp32.  f32: fp32 throughout.
+ * else is fp32.  The products are taken with q + u and q + v brought near one by a power of two for each row, so
+ * K rows above 2^110 and rel rows above 2^90 may overflow whatever the query.  f32: fp32 throughout.
  */
 oasr_status oasr_chunk_relattn_paged_e4m3(const void* q, const void* k_pool, const void* v_pool,
                                           const void* kv_scale, int num_blocks, int block_size,
@@ -308,9 +309,11 @@ oasr_status oasr_quantize_rows(const void* x, void* x8, float* scale, int M, int
  *   out[i][n] = (sum_k x8[i][k] * w8[n][k]) * x_scale[i] * w_scale[n] + bias[n]
  *
  * x8 [M, K] and w8 [N, K] int8, x_scale [M] and w_scale [N] fp32, bias [N] (null: none) and out [M, N]
- * of `dt`.  The sum is exact for K <= 1024 and for M <= 8 and may be accumulated in fp32 otherwise; the
- * scales and the bias are applied in that order in fp32, and the result is rounded once.  K a multiple
- * of 16, at most 65536; M and N at most 2^31 - 256; every pointer 16-byte aligned.
+ * of `dt`.  The sum is exact for K <= 1024.  For longer K it is the integer sum rounded once to fp32 for M <= 8,
+ * and for M <= 128 where the library finds integer dot products faster than matrix tiles (its choice depends on
+ * M, N, K and the GPU alone), else an fp32 accumulation: the same row can then differ in its last bits with the
+ * batch that it is in.  The scales and the bias are applied in that order in fp32, and the result is rounded once.
+ * K a multiple of 16, at most 65536; M and N at most 2^31 - 256; every pointer 16-byte aligned.
  */
 oasr_status oasr_linear_w8a8(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
                              const void* bias, void* out, int M, int N, int K, oasr_dtype dt,

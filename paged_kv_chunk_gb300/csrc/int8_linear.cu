@@ -8,7 +8,8 @@
 // and a product of two exact in fp32, so the sums run on tcgen05's fp16 rate: converter warps
 // read the 8-bit rows and write them as fp16 into the swizzled tiles the matrix instructions
 // read.  A sum stays within 2^24 for K <= 1024, where fp32 holds every integer: the accumulated
-// sum is the integer sum.  For longer K it is that of an fp32 accumulation.
+// sum is the integer sum.  For longer K it is that of an fp32 accumulation.  Few rows (dispatch_i8) go through
+// integer dot products, whose sum is the integer whatever K is, rounded once to fp32.
 //
 // What bounds a large product is shared memory: of a K step of 64, a tile's rows come in as bytes,
 // are read, written as fp16 and read by the matrix unit.  A pair of CTAs on one 256 x 256 tile
@@ -711,11 +712,6 @@ oasr_status launch_i8(I8Args a, int slot, int sms, cudaStream_t stream)
                           tm[3], outs, static_cast<const I8Args>(a));
 }
 
-// Tile: the one of the least estimated time.  Measured per K step of 64 (ns, by the slope over K): 375 for a
-// pair's 256 x 256, 315 for 128 x 128, 285 and 275 for 128 x 64 and 128 x 32, where the steps' latency is the cost;
-// a tile's epilogue takes 2400, 1300, 600 and 400, half of which the next tile's products hide.  8191 x 4096 x 1024
-// in fp32: 57 us in pairs, 87 in 128 x 128; 1024 x 768 x 256 in bf16: 7.0 in pairs, 5.2, 4.5 in 128 x 64 and 5.5 in
-// 128 x 32.  256 x 128 in pairs and 128 x 256 without were nowhere the fastest.
 template <typename Elem>
 oasr_status some_rows(const I8Problem& p, void* out, int K, cudaStream_t stream)
 {
@@ -726,6 +722,11 @@ oasr_status some_rows(const I8Problem& p, void* out, int K, cudaStream_t stream)
                       static_cast<Elem*>(out), K);
 }
 
+// Tile: the one of the least estimated time.  Measured per K step of 64 (ns, by the slope over K): 375 for a
+// pair's 256 x 256, 315 for 128 x 128, 285 and 275 for 128 x 64 and 128 x 32, where the steps' latency is the cost;
+// a tile's epilogue takes 2400, 1300, 600 and 400, half of which the next tile's products hide.  8191 x 4096 x 1024
+// in fp32: 57 us in pairs, 87 in 128 x 128; 1024 x 768 x 256 in bf16: 7.0 in pairs, 5.2, 4.5 in 128 x 64 and 5.5 in
+// 128 x 32.  256 x 128 in pairs and 128 x 256 without were nowhere the fastest.
 template <typename Elem>
 oasr_status dispatch_i8(const I8Args& a, cudaStream_t stream)
 {
