@@ -25,10 +25,11 @@
 // When the (stream, head) pairs are too few to fill the GPU the keys of each are divided over a cluster
 // of up to 16 CTAs, whose partial sums meet through distributed shared memory.
 //
-// What bounds it is issue: per 16 keys and 16 queries a warp converts 24 words, multiplies, adds the
-// position term, exponentiates and rounds; HBM is at a tenth to a third of its rate.  Device times: the
-// Conformer-large step (256 streams, 8 heads, 16 frames, window 512) 62 us, one stream and one frame over 8000
-// keys 14.4, 128 streams of 64 frames over 0 to 1024 keys 122.
+// What bounds it: per 16 keys and 16 queries a warp converts 24 words, multiplies, adds the position term,
+// exponentiates and rounds, 405 warp instructions in all, at half of the issue rate because registers leave too
+// few warps to cover the chains' latencies; HBM is at a tenth to a third of its rate.  Device times: the
+// Conformer-large step (256 streams, 8 heads, 16 frames, window 512) 63.5 us, one stream and one frame over 8000
+// keys 14.4, 128 streams of 64 frames over 0 to 1024 keys 125.
 #include "attn_core.cuh"
 #include "cluster.cuh"
 #include "e4m3.cuh"
@@ -1049,8 +1050,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) chunk_e4m3_kernel(
 // of the keys); tiles of 64 keys, K and V decoded to fp32 on their way into shared memory (exact), the
 // rel rows the tile's distances need (79 of them) copied beside them a tile ahead.  Content and position
 // products are register tiles of 2 rows by 4 keys or 5 distances, summed apart (their sum is rounded
-// once); the position term is skewed through shared memory.  Bound by the fp32 FMA rate: 16 * 64 * (64 +
-// 80 + 64) of them a tile.
+// once); the position term is skewed through shared memory.  The operands of a tile's 16 * 64 *
+// (64 + 80 + 64) FMAs come through shared memory: its wavefronts are at 65% of their peak, the FMA pipe at 31% (64
+// streams of 16 frames over 512 keys, 8 heads: 112 us; the Conformer-large step 380).
 constexpr int kFRows = 16, kFKeys = 64, kFRel = 80;
 constexpr int kFStride = 68;      // floats of a 64-value row: rows apart by four banks
 constexpr int kFThreads = 128;
