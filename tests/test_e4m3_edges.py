@@ -178,3 +178,40 @@ def test_zero_value_rows_with_all_the_weight(order, gap, loud, dtype, T):
     tol = tol + (C + T) * 2.0 ** -126 * float(history[1].abs().max())
     err = (out[0].double().cpu() - want).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 16, 20, 40])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_query_rows_that_are_not_finite(T, dtype):
+    """A query row with a NaN or an infinity is NaN itself; its neighbours in the tile and the next stream are not."""
+    c, x, lens = make(3, 2, T, [90, 0, 33], 16, dtype, 130 + T)
+    x["q"][0, 1, 0, 3], x["q"][1, T - 1, 1, 63], x["q"][2, 0, 0, 0] = float("nan"), float("inf"), float("-inf")
+    for fused in (True, False):
+        out, pools = step(c, x, lens, fused=fused)
+        for b, t, h in ((0, 1, 0), (1, T - 1, 1), (2, 0, 0)):
+            assert out[b, t, h].isnan().all()
+        d, y, _ = make(3, 2, T, [90, 0, 33], 16, dtype, 130 + T)
+        d.append(y["k_new"], y["v_new"], lens)
+        assert d.same(*pools[:3])
+        for b, t, h in ((0, 1, 0), (1, T - 1, 1), (2, 0, 0)):
+            y["q"][b, t, h] = 0
+            out[b, t, h] = step(c, y, lens, fused=fused)[0][b, t, h]
+        check(d, y, lens, out, dtype)
+
+
+@pytest.mark.gpu
+def test_calls_on_a_stream_that_is_named():
+    """Every call of a step enqueued on a stream given by name, none of it on the current one."""
+    c, x, lens = make(2, 2, 9, [70, 12], 16, "bf16", 140)
+    pools, d, ln = c.cuda(), {n: t.cuda() for n, t in x.items()}, lens.cuda()
+    out = torch.empty_like(d["q"])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        capi.oasr_paged_append_e4m3(d["k_new"], d["v_new"], *pools, ln, stream=handle)
+        capi.oasr_chunk_relattn_paged_e4m3(d["q"], *pools, ln, d["u"], d["vb"], d["rel"], out=out, stream=handle)
+        side.synchronize()
+        c.append(x["k_new"], x["v_new"], lens)
+        assert c.same(*pools[:3])
+        check(c, x, lens, out, "bf16")
