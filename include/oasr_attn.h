@@ -333,6 +333,100 @@ oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_scale, cons
                                       int M, int R, int d_model, int H, oasr_dtype dt,
                                       cudaStream_t stream);
 
+/*
+ * Pages for requests of any lengths, taken and given back on the device (ASR Engine page, section 4.3: each
+ * step allocates its streams' blocks from the pool and stacks the block table; here one call does both for
+ * streams that grow, shrink and end, and gives the pool slot of every new row).
+ *
+ * Stream b changes from C = cache_seqlens[b] to N = new_seqlens[b] frames and so from P0 = ceil(C / block_size) to
+ * P1 = ceil(N / block_size) pages.  free_blocks [num_blocks] is a ring of free block ids and free_state int32 [4]
+ * its state: {place of its first id, number of ids, pages that the last call lacked, 0}; the first two are the
+ * caller's to set up, the last two start as 0.  In the order of streams and pages:
+ *   growing:   block_table[b][P0 .. P1) become the ring's first ids, which leave it;
+ *   shrinking: block_table[b][P1 .. P0) go behind the ring's last id and become -1.
+ * Pages given back in a call are not handed out in the same call.  Where the ring holds fewer ids than the
+ * growing streams need, none of them gets any: their entries stay as they were, free_state[2] is the number of
+ * pages short (else 0), and every slot is -1; shrinking streams give theirs back all the same.
+ *   cu_seqlens [B + 1]: offsets of the streams' new rows, cu[b + 1] - cu[b] = max(N - C, 0);
+ *   slot_map [total]:   slot_map[cu[b] + t] = block_table[b][(C + t) / block_size] * block_size +
+ *                       (C + t) % block_size, the row of the pools ([num_blocks * block_size, H, D]) that
+ *                       position C + t of stream b has; -1 behind cu[B].
+ * cache_seqlens is not changed: the caller commits new_seqlens once the rows are written.  A stream has at most
+ * max_blocks_per_seq pages; lengths below 0 or past them are clamped, a slot whose page names no block is -1, rows
+ * past `total` get no slot, a ring state out of range hands out nothing: each raises OASR_ERR_BOUNDS.
+ * Requirements: B at most 4096; num_blocks * block_size, B * max_blocks_per_seq and (max_blocks_per_seq + 1) *
+ * block_size below 2^31 (else OASR_ERR_UNSUPPORTED).  One call at a time may work on a ring and its state.
+ */
+oasr_status oasr_block_table_update(int32_t* block_table, const int32_t* cache_seqlens,
+                                    const int32_t* new_seqlens, int B, int max_blocks_per_seq, int block_size,
+                                    int32_t* free_blocks, int num_blocks, int32_t* free_state,
+                                    int32_t* slot_map, int total, int32_t* cu_seqlens, cudaStream_t stream);
+
+/*
+ * Rows of requests of different lengths into the pools ([num_blocks, block_size, H, D], `dt`) by their slots: row i of
+ * k_new and v_new (rows of H * D values, k_stride and v_stride values apart: views of one product's output will do)
+ * becomes row slot_map[i] of k_pool and v_pool, a pure copy.  Slots of -1 are skipped; slots below that or past the
+ * pools are skipped and raise OASR_ERR_BOUNDS.  A slot named twice holds one of its rows, unspecified which.
+ * Requirements: D * sizeof(dtype) and both strides multiples of 16 bytes; num_blocks * block_size < 2^31.
+ */
+oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                    void* k_pool, void* v_pool, int num_blocks, int block_size,
+                                    const int32_t* slot_map, int total, int H, int D, oasr_dtype dt,
+                                    cudaStream_t stream);
+
+/*
+ * Cross attention: a decoder's tokens over the encoder's states of their utterance (Model Layer page, the
+ * TransformerDecoder and the AR decoder contracts: their layers attend to the encoder's output, of another length).
+ * Sequence s has the queries [cu_q[s], cu_q[s + 1]) of q, those of all its hypotheses one after the other, and
+ *   packed: the keys [cu_k[s], cu_k[s + 1]) of k and v;
+ *   paged:  the first cache_seqlens[s] positions of block_table[s], in pools [num_blocks, block_size, Hkv, 64].
+ *     out[i][h] = sum_j softmax_j(scale q[i][h] . k[j][h / G]) v[j][h / G],   G = H / Hkv
+ * No position term and no mask but the lengths.  A sequence without keys has zeros; rows of out that no sequence
+ * owns keep what they held.  Rows of q, k and v are q_stride, k_stride, v_stride values apart (heads are
+ * contiguous: k and v may be the halves of one product's rows); out is [total_q, H, 64].
+ * max_q and max_k are the lengths that the launch is laid out for: a longer sequence is right, and slower.
+ * Requirements: D = 64; H a multiple of Hkv and at most 1024; num_seqs at most 65536; scale > 0 and finite; pointers
+ * and strides multiples of 16 bytes; total_q * G below 2^31 - 256; num_blocks * block_size < 2^31.
+ * Offsets that decrease or pass total_q or total_k, and lengths past the table, are clamped; an invalid block id
+ * reads as zero rows; each raises OASR_ERR_BOUNDS.  Keys past a sequence's end are never part of a result, whatever
+ * they hold.  bf16: fp32 scores, softmax and sums, the weights rounded to bf16 for their product with v, one
+ * rounding of out.  f32: fp32 throughout (no TF32).
+ */
+oasr_status oasr_cross_attn_packed(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,
+                                   int num_seqs, int max_q, int max_k, int total_q, int total_k, void* out, int H,
+                                   int Hkv, int D, float scale, oasr_dtype dt, cudaStream_t stream);
+
+oasr_status oasr_cross_attn_paged(const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+                                  int num_blocks, int block_size, const int32_t* block_table,
+                                  int max_blocks_per_seq, const int32_t* cache_seqlens, const int32_t* cu_q,
+                                  int num_seqs, int max_q, int max_k, int total_q, void* out, int H, int Hkv, int D,
+                                  float scale, oasr_dtype dt, cudaStream_t stream);
+
+/*
+ * Quantise the rows of x ([M, K], `dt`) to e4m3 with one power-of-two scale for each 128 neighbouring values (the
+ * last block of a row may be shorter): x8 [M, K] e4m3 bytes, scale [M, ceil(K / 128)] bytes.  A block is quantised as
+ * a row of the 8-bit cache is: e = max(-100, the least e for which max|x_block| <= 448 * 2^e), the scale byte
+ * e + 127, x8 = x * 2^-e rounded to e4m3 (nearest, ties to even); a block with a NaN or an infinity has the byte 255
+ * and stands for NaN in every element.  K must be a multiple of 16.
+ */
+oasr_status oasr_quantize_blocks(const void* x, void* x8, void* scale, int M, int K, oasr_dtype dt,
+                                 cudaStream_t stream);
+
+/*
+ * Product of e4m3 rows with a scale for each block of 128, activations x and weights w in the same format:
+ *
+ *   out[i][n] = sum_b 2^(ex[i][b] + ew[n][b]) (sum_{k in block b} x8[i][k] * w8[n][k]) + bias[n]
+ *
+ * x8 [M, K] and w8 [N, K] e4m3, their scale bytes e + 127 [M, ceil(K / 128)] and [N, ceil(K / 128)] (1 to 254, 255:
+ * NaN), bias [N] (null: none) and out [M, N] of `dt`.  Products are exact, their sums fp32; out is rounded once.
+ * A product of two blocks' scales outside fp32's range may overflow or vanish.
+ * K a multiple of 16, at most 65536; M and N at most 2^31 - 256; x8, w8, bias and out 16-byte aligned.
+ */
+oasr_status oasr_linear_e4m3(const void* x8, const void* x_scale, const void* w8, const void* w_scale,
+                             const void* bias, void* out, int M, int N, int K, oasr_dtype dt,
+                             cudaStream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* oasr_status_string(oasr_status status);
 

@@ -32,19 +32,35 @@ scales ``[num_blocks, H, 2, block_size]``) and int8 projections::
 ``oasr_paged_append_e4m3``, ``oasr_chunk_relattn_paged_e4m3`` and ``oasr_paged_read_e4m3`` are its parts and
 the way back; ``oasr_linear_w8a8`` is the int8 linear layer by itself.
 
+A batch of requests of different lengths, from its pages to a decoder's tokens over its encoder states::
+
+    slot_map, cu = capi.oasr_block_table_update(block_table, cache_seqlens, new_seqlens, free_blocks,
+                                                free_state, block_size, total)
+    x8, x_scale = capi.oasr_quantize_blocks(states)        # [total, d]; weights once, in the same way
+    kv = capi.oasr_linear_e4m3(x8, x_scale, w_kv8, w_kv_scale, b_kv).view(total, 2, Hkv, 64)
+    capi.oasr_paged_append_slots(kv[:, 0], kv[:, 1], k_pool, v_pool, slot_map)
+    cache_seqlens.copy_(new_seqlens)
+    out = capi.oasr_cross_attn_paged(q, k_pool, v_pool, block_table, cache_seqlens, cu_q, max_q)
+
+(``oasr_cross_attn_packed`` over states that are only packed.)
+
 The offline pass over packed utterances is ``oasr_packed_relattn_varlen`` (or
 ``oasr_packed_relattn_chunked`` under the Nemotron chunked-limited window).
 """
-from .capi import (OasrError, oasr_chunk_relattn_paged, oasr_chunk_relattn_paged_e4m3,  # noqa: F401
-                   oasr_chunk_step_paged, oasr_chunk_step_paged_e4m3, oasr_device_status,
-                   oasr_linear_w8a8, oasr_packed_relattn_chunked, oasr_packed_relattn_varlen,
-                   oasr_paged_append, oasr_paged_append_e4m3, oasr_paged_read_e4m3,
-                   oasr_project_qkv_pos, oasr_project_qkv_pos_w8a8, oasr_quantize_rows,
+from .capi import (OasrError, oasr_block_table_update, oasr_chunk_relattn_paged,  # noqa: F401
+                   oasr_chunk_relattn_paged_e4m3, oasr_chunk_step_paged, oasr_chunk_step_paged_e4m3,
+                   oasr_cross_attn_packed, oasr_cross_attn_paged, oasr_device_status,
+                   oasr_linear_e4m3, oasr_linear_w8a8, oasr_packed_relattn_chunked,
+                   oasr_packed_relattn_varlen, oasr_paged_append, oasr_paged_append_e4m3,
+                   oasr_paged_append_slots, oasr_paged_read_e4m3, oasr_project_qkv_pos,
+                   oasr_project_qkv_pos_w8a8, oasr_quantize_blocks, oasr_quantize_rows,
                    oasr_selftest_wait, oasr_version, oasr_window_commit)
 
 __all__ = ["OasrError", "oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
            "oasr_packed_relattn_varlen", "oasr_packed_relattn_chunked", "oasr_window_commit",
            "oasr_project_qkv_pos", "oasr_paged_append_e4m3", "oasr_paged_read_e4m3",
            "oasr_chunk_relattn_paged_e4m3", "oasr_chunk_step_paged_e4m3", "oasr_quantize_rows",
-           "oasr_linear_w8a8", "oasr_project_qkv_pos_w8a8", "oasr_device_status",
+           "oasr_linear_w8a8", "oasr_project_qkv_pos_w8a8", "oasr_block_table_update",
+           "oasr_paged_append_slots", "oasr_cross_attn_packed", "oasr_cross_attn_paged",
+           "oasr_quantize_blocks", "oasr_linear_e4m3", "oasr_device_status",
            "oasr_selftest_wait", "oasr_version"]

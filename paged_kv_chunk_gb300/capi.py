@@ -65,7 +65,16 @@ def load() -> ctypes.CDLL:
         L.oasr_quantize_rows.argtypes = [P, P, P, I, I, I, S]
         L.oasr_linear_w8a8.argtypes = [P, P, P, P, P, P, I, I, I, I, S]
         L.oasr_project_qkv_pos_w8a8.argtypes = [P] * 13 + [I, I, I, I, I, S]
-        for fn in ("oasr_quantize_rows", "oasr_linear_w8a8", "oasr_project_qkv_pos_w8a8",
+        Q = ctypes.c_int64
+        L.oasr_block_table_update.argtypes = [P, P, P, I, I, I, P, I, P, P, I, P, S]
+        L.oasr_paged_append_slots.argtypes = [P, P, Q, Q, P, P, I, I, P, I, I, I, I, S]
+        L.oasr_cross_attn_packed.argtypes = [P, Q, P, Q, P, Q, P, P, I, I, I, I, I, P, I, I, I, F, I, S]
+        L.oasr_cross_attn_paged.argtypes = [P, Q, P, P, I, I, P, I, P, P, I, I, I, I, P, I, I, I, F, I, S]
+        L.oasr_quantize_blocks.argtypes = [P, P, P, I, I, I, S]
+        L.oasr_linear_e4m3.argtypes = [P, P, P, P, P, P, I, I, I, I, S]
+        for fn in ("oasr_block_table_update", "oasr_paged_append_slots", "oasr_cross_attn_packed",
+                   "oasr_cross_attn_paged", "oasr_quantize_blocks", "oasr_linear_e4m3",
+                   "oasr_quantize_rows", "oasr_linear_w8a8", "oasr_project_qkv_pos_w8a8",
                    "oasr_paged_append_e4m3", "oasr_paged_read_e4m3",
                    "oasr_chunk_relattn_paged_e4m3", "oasr_chunk_step_paged_e4m3",
                    "oasr_paged_append", "oasr_chunk_relattn_paged", "oasr_chunk_step_paged",
@@ -554,6 +563,205 @@ def oasr_project_qkv_pos_w8a8(x8, x_scale, w_qkv8, w_qkv_scale, b_qkv, pos8, pos
     return q, k, v, rel
 
 
+def _rows_apart(t, name, dtype, dev) -> int:
+    """Values from row to row of t [rows, H, D], whose rows are contiguous each but may lie apart (half of a
+    product's columns); 16-byte steps."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0 or t.dtype is not dtype:
+        _dev(t, name, dtype)
+    n, H, D = t.shape
+    apart, head, one = t.stride()
+    if (one != 1 and D > 1) or (head != D and H > 1):
+        raise ValueError(f"{name} must have contiguous rows")
+    if n <= 1:
+        return H * D
+    if apart < H * D or apart * t.element_size() % 16:
+        raise ValueError(f"{name}'s rows must lie a multiple of 16 bytes apart and not overlap")
+    return apart
+
+
+def oasr_block_table_update(block_table, cache_seqlens, new_seqlens, free_blocks, free_state, block_size, total,
+                            slot_map=None, cu_seqlens=None, stream=None):
+    """Pages for streams that change from cache_seqlens to new_seqlens frames (int32 [B] each), taken
+    from and given back to the ring of free block ids (free_blocks int32 [num_blocks], free_state int32
+    [4]: first place, count, pages short, 0), in place.  Returns (slot_map int32 [total], the pool row
+    of every new frame, stream after stream, -1 behind the last and where the ring was short; cu_seqlens
+    int32 [B + 1], the streams' offsets in it)."""
+    L, dev = _lib_device()
+    table = block_table.shape
+    total, block_size = int(total), int(block_size)
+    if len(table) != 2 or cache_seqlens.shape != (table[0],) or new_seqlens.shape != (table[0],):
+        raise ValueError("block_table must be [B, mbps], cache_seqlens and new_seqlens [B]")
+    if free_blocks.dim() != 1 or free_state.shape != (4,):
+        raise ValueError("free_blocks must be [num_blocks] and free_state [4]")
+    _fits(table[0], table[1], total, block_size, free_blocks.shape[0])
+    if total < 0:
+        raise ValueError("total must not be negative")
+    if slot_map is None:
+        slot_map = torch.empty((total,), dtype=torch.int32, device=block_table.device)
+    if cu_seqlens is None:
+        cu_seqlens = torch.empty((table[0] + 1,), dtype=torch.int32, device=block_table.device)
+    if slot_map.shape != (total,) or cu_seqlens.shape != (table[0] + 1,):
+        raise ValueError("slot_map must be [total] and cu_seqlens [B + 1]")
+    i32 = torch.int32
+    if not _good(dev, i32, block_table, cache_seqlens, new_seqlens, free_blocks, free_state, slot_map, cu_seqlens):
+        _refuse(block_table=(block_table, i32), cache_seqlens=(cache_seqlens, i32), new_seqlens=(new_seqlens, i32),
+                free_blocks=(free_blocks, i32), free_state=(free_state, i32), slot_map=(slot_map, i32),
+                cu_seqlens=(cu_seqlens, i32))
+    _check("oasr_block_table_update", L.oasr_block_table_update(
+        block_table.data_ptr(), cache_seqlens.data_ptr(), new_seqlens.data_ptr(), table[0], table[1], block_size,
+        free_blocks.data_ptr(), free_blocks.shape[0], free_state.data_ptr(), slot_map.data_ptr(), total,
+        cu_seqlens.data_ptr(), _stream(stream)))
+    return slot_map, cu_seqlens
+
+
+def oasr_paged_append_slots(k_new, v_new, k_pool, v_pool, slot_map, stream=None):
+    """Write row i of k_new and v_new ([total,H,D], rows may lie apart) into row slot_map[i] of the pools
+    ([nb,bs,H,D] as rows), in place; slots of -1 are skipped."""
+    L, dev = _lib_device()
+    dt = k_new.dtype
+    code = _code(dt)
+    n, H, D = k_new.shape
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must share their shape [total, H, D]")
+    shape = k_pool.shape
+    if len(shape) != 4 or shape[2] != H or shape[3] != D or v_pool.shape != shape:
+        raise ValueError("k_pool and v_pool must be [num_blocks, block_size, H, D]")
+    if slot_map.shape != (n,):
+        raise ValueError("slot_map must be [total]")
+    _fits(n, H, D, shape[0], shape[1])
+    k_apart, v_apart = _rows_apart(k_new, "k_new", dt, dev), _rows_apart(v_new, "v_new", dt, dev)
+    if not (_good(dev, dt, k_pool, v_pool) and _good(dev, torch.int32, slot_map)):
+        _refuse(k_pool=(k_pool, dt), v_pool=(v_pool, dt), slot_map=(slot_map, torch.int32))
+    _check("oasr_paged_append_slots", L.oasr_paged_append_slots(
+        k_new.data_ptr(), v_new.data_ptr(), k_apart, v_apart, k_pool.data_ptr(), v_pool.data_ptr(), shape[0], shape[1],
+        slot_map.data_ptr(), n, H, D, code, _stream(stream)))
+
+
+def _cross(dev, q, cu_q, max_q, Hkv, out):
+    """Checks what both forms of the cross attention take; returns the output, total_q, N, H, D, q's
+    row stride and the dtype's code."""
+    dt = q.dtype
+    code = _code(dt)
+    n, H, D = q.shape
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("q's heads must be a multiple of k's")
+    if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("cu_q must be [num_seqs + 1]")
+    _fits(n, H, D, cu_q.shape[0], max_q)
+    if out is None:
+        out = torch.empty((n, H, D), dtype=dt, device=q.device)
+    elif out.shape != (n, H, D):
+        raise ValueError("out must be [total_q, H, D]")
+    apart = _rows_apart(q, "q", dt, dev)
+    if not (_good(dev, dt, out) and _good(dev, torch.int32, cu_q)):
+        _refuse(out=(out, dt), cu_q=(cu_q, torch.int32))
+    return out, n, cu_q.shape[0] - 1, H, D, apart, code
+
+
+def oasr_cross_attn_packed(q, k, v, cu_q, cu_k, max_q, max_k, out=None, scale=None, stream=None):
+    """Cross attention of packed queries [total_q,H,64] (sequence s: rows cu_q[s] to cu_q[s+1]) over packed
+    keys and values [total_k,Hkv,64] (cu_k), Hkv dividing H; rows of q, k and v may lie apart.  max_q and
+    max_k: the longest sequences' lengths.  Returns out [total_q,H,64]; without keys zeros."""
+    L, dev = _lib_device()
+    nk, Hkv, Dk = k.shape
+    max_q, max_k = int(max_q), int(max_k)
+    if v.shape != k.shape or Dk != q.shape[2]:
+        raise ValueError("k and v must be [total_k, Hkv, D]")
+    out, n, N, H, D, q_apart, code = _cross(dev, q, cu_q, max_q, Hkv, out)
+    if cu_k.shape != cu_q.shape:
+        raise ValueError("cu_k must have cu_q's length")
+    _fits(nk, max_k)
+    k_apart, v_apart = _rows_apart(k, "k", q.dtype, dev), _rows_apart(v, "v", q.dtype, dev)
+    if not _good(dev, torch.int32, cu_k):
+        _refuse(cu_k=(cu_k, torch.int32))
+    _check("oasr_cross_attn_packed", L.oasr_cross_attn_packed(
+        q.data_ptr(), q_apart, k.data_ptr(), k_apart, v.data_ptr(), v_apart, cu_q.data_ptr(), cu_k.data_ptr(), N, max_q,
+        max_k, n, nk, out.data_ptr(), H, Hkv, D, D ** -0.5 if scale is None else scale, code, _stream(stream)))
+    return out
+
+
+def oasr_cross_attn_paged(q, k_pool, v_pool, block_table, cache_seqlens, cu_q, max_q, max_k=None, out=None, scale=None,
+                          stream=None):
+    """The same over keys and values in pages: the first cache_seqlens[s] positions of block_table[s] in the
+    pools [nb,bs,Hkv,64].  max_k: the longest sequence's keys (None: the table's width)."""
+    L, dev = _lib_device()
+    shape, table = k_pool.shape, block_table.shape
+    if len(shape) != 4 or shape[3] != q.shape[2]:
+        raise ValueError("k_pool must be [num_blocks, block_size, Hkv, D]")
+    if v_pool.shape != shape:
+        raise ValueError("v_pool must have k_pool's shape")
+    if len(table) != 2 or cu_q.shape != (table[0] + 1,) or cache_seqlens.shape != table[:1]:
+        raise ValueError("block_table must be [num_seqs, mbps], cache_seqlens [num_seqs] and cu_q [num_seqs + 1]")
+    max_q = int(max_q)
+    out, n, N, H, D, q_apart, code = _cross(dev, q, cu_q, max_q, shape[2], out)
+    max_k = table[1] * shape[1] if max_k is None else int(max_k)
+    _fits(shape[0], shape[1], table[1], max_k)
+    if not (_good(dev, q.dtype, k_pool, v_pool) and _good(dev, torch.int32, block_table, cache_seqlens)):
+        _refuse(k_pool=(k_pool, q.dtype), v_pool=(v_pool, q.dtype), block_table=(block_table, torch.int32),
+                cache_seqlens=(cache_seqlens, torch.int32))
+    _check("oasr_cross_attn_paged", L.oasr_cross_attn_paged(
+        q.data_ptr(), q_apart, k_pool.data_ptr(), v_pool.data_ptr(), shape[0], shape[1], block_table.data_ptr(), table[1],
+        cache_seqlens.data_ptr(), cu_q.data_ptr(), N, max_q, max_k, n, out.data_ptr(), H, shape[2], D,
+        D ** -0.5 if scale is None else scale, code, _stream(stream)))
+    return out
+
+
+def _blocks(x8, scale, name):
+    """Rows, row length and blocks of a matrix held in blocks of 128."""
+    M, K = x8.shape
+    if scale.shape != (M, -(-K // 128)):
+        raise ValueError(f"{name}'s scale must be [rows, ceil(K / 128)]")
+    return M, K
+
+
+def oasr_quantize_blocks(x, x8=None, scale=None, stream=None):
+    """Rows of x [M,K] in e4m3 with one power-of-two scale for each 128 values; returns (x8 float8_e4m3fn
+    [M,K], scale uint8 [M, ceil(K/128)], the byte e + 127 standing for 2^e)."""
+    L, dev = _lib_device()
+    dt = x.dtype
+    code = _code(dt)
+    M, K = x.shape
+    _fits(M, K)
+    if x8 is None:
+        x8 = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+    if scale is None:
+        scale = torch.empty((M, -(-K // 128)), dtype=torch.uint8, device=x.device)
+    if x8.shape != (M, K):
+        raise ValueError("x8 must be [M, K]")
+    _blocks(x8, scale, "x8")
+    if not (_good(dev, dt, x) and _good(dev, torch.float8_e4m3fn, x8) and _good(dev, torch.uint8, scale)):
+        _refuse(x=(x, dt), x8=(x8, torch.float8_e4m3fn), scale=(scale, torch.uint8))
+    _check("oasr_quantize_blocks", L.oasr_quantize_blocks(
+        x.data_ptr(), x8.data_ptr(), scale.data_ptr(), M, K, code, _stream(stream)))
+    return x8, scale
+
+
+def oasr_linear_e4m3(x8, x_scale, w8, w_scale, bias=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """x . w^T + bias of rows held as `oasr_quantize_blocks` leaves them (x8 [M,K], w8 [N,K]); returns out
+    [M,N] of ``out_dtype`` (or of the out given)."""
+    L, dev = _lib_device()
+    M, K = _blocks(x8, x_scale, "x8")
+    N, Kw = _blocks(w8, w_scale, "w8")
+    _fits(M, N, K)
+    if Kw != K:
+        raise ValueError("shapes: x8 [M,K], w8 [N,K]")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x8.device)
+    if out.shape != (M, N) or (bias is not None and bias.shape != (N,)):
+        raise ValueError("out must be [M, N] and bias [N]")
+    dt = out.dtype
+    code = _code(dt)
+    e4 = torch.float8_e4m3fn
+    if not (_good(dev, e4, x8, w8) and _good(dev, torch.uint8, x_scale, w_scale) and _good(dev, dt, out)
+            and (bias is None or _good(dev, dt, bias))):
+        _refuse(x8=(x8, e4), x_scale=(x_scale, torch.uint8), w8=(w8, e4), w_scale=(w_scale, torch.uint8), out=(out, dt),
+                **({} if bias is None else {"bias": (bias, dt)}))
+    _check("oasr_linear_e4m3", L.oasr_linear_e4m3(
+        x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(), None if bias is None else bias.data_ptr(),
+        out.data_ptr(), M, N, K, code, _stream(stream)))
+    return out
+
+
 def oasr_device_status(clear: bool = True) -> int:
     """Raw device status bits (1 = an index was out of range, 2 = a wait timed out)."""
     L = load()
@@ -595,5 +803,7 @@ if NVTX:
                   "oasr_project_qkv_pos", "oasr_selftest_wait", "oasr_paged_append_e4m3",
                   "oasr_paged_read_e4m3", "oasr_chunk_relattn_paged_e4m3",
                   "oasr_chunk_step_paged_e4m3", "oasr_quantize_rows", "oasr_linear_w8a8",
-                  "oasr_project_qkv_pos_w8a8"):
+                  "oasr_project_qkv_pos_w8a8", "oasr_block_table_update", "oasr_paged_append_slots",
+                  "oasr_cross_attn_packed", "oasr_cross_attn_paged", "oasr_quantize_blocks",
+                  "oasr_linear_e4m3"):
         globals()[_name] = _traced(globals()[_name])

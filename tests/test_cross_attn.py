@@ -1,0 +1,405 @@
+"""Cross attention, packed and paged, against its definition in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from paged_kv_chunk_gb300 import build, capi
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+FAKE = 1 << 20
+
+
+def reference(q, k, v, scale, bf16):
+    """Rows q [n, H, 64] over keys k, v [m, H, 64]: the output in 64 bits and its elementwise bound.
+
+    An fp32 score is off by at most (64 + 4) 2^-24 scale sum|q k| (64 products summed, the scaling and the maximum's
+    subtraction), an exponential by that and 2^-21 (the hardware's exp2, its argument's last bit); bf16 weights by
+    another 2^-8 relative to each.  Sums of n weights are off by n 2^-24, and the result is rounded once more."""
+    if not k.shape[0]:
+        return torch.zeros_like(q, dtype=torch.float64), torch.zeros_like(q, dtype=torch.float64)
+    q, k, v = (x.double().transpose(0, 1) for x in (q, k, v))
+    s = q @ k.transpose(1, 2) * scale
+    p = torch.softmax(s, -1)
+    out = p @ v
+    ds = 68 * 2.0 ** -24 * scale * (q.abs() @ k.abs().transpose(1, 2)).amax(-1, keepdim=True) + 2.0 ** -21
+    rel = 2 * ds * 1.01 + 2 * k.shape[1] * 2.0 ** -24 + (2.0 ** -8 if bf16 else 0)
+    tol = rel * (p @ v.abs()) + out.abs() * (2.0 ** -8 if bf16 else 2.0 ** -22) * 1.01 + 1e-37
+    return out.transpose(0, 1), tol.transpose(0, 1)
+
+
+class Case:
+    """Sequences of nq[s] queries and nk[s] keys; `spare` rows of queries behind the last sequence, NaN wherever no
+    sequence has a key."""
+
+    def __init__(self, nq, nk, H, Hkv, dtype, seed, bs=16, std=1.0, spare=0, split=True):
+        g = torch.Generator().manual_seed(seed)
+        self.nq, self.nk, self.H, self.Hkv, self.dt, self.bs = nq, nk, H, Hkv, DT[dtype], bs
+        N, tq, tk = len(nq), sum(nq), sum(nk)
+        self.cu_q = torch.tensor([sum(nq[:i]) for i in range(N + 1)], dtype=torch.int32)
+        self.cu_k = torch.tensor([sum(nk[:i]) for i in range(N + 1)], dtype=torch.int32)
+        self.q = (torch.randn(tq + spare, H, 64, generator=g) * std).to(self.dt)
+        kv = (torch.randn(tk + 3, 2, Hkv, 64, generator=g) * std).to(self.dt)
+        kv[tk:] = float("nan")
+        self.k, self.v = (kv[:, 0], kv[:, 1]) if split else (kv[:, 0].contiguous(), kv[:, 1].contiguous())
+        pages = [-(-n // bs) for n in nk]
+        self.mbps = max(1, max(pages))
+        nb = sum(pages) + 4
+        ids = torch.randperm(nb, generator=g).tolist()
+        self.table = torch.full((N, self.mbps), -1, dtype=torch.int32)
+        self.kp, self.vp = (torch.full((nb, bs, Hkv, 64), float("nan"), dtype=self.dt) for _ in range(2))
+        for s, n in enumerate(nk):
+            for p in range(pages[s]):
+                b = self.table[s, p] = ids.pop()
+                rows = slice(int(self.cu_k[s]) + p * bs, int(self.cu_k[s]) + min(n, (p + 1) * bs))
+                m = rows.stop - rows.start
+                self.kp[b, :m], self.vp[b, :m] = self.k[rows], self.v[rows]
+        self.lens = torch.tensor(nk, dtype=torch.int32)
+
+    def cuda(self):
+        kv = torch.stack([self.k, self.v], 1).cuda()       # rows of k and v side by side, as a product leaves them
+        x = dict(q=self.q.cuda(), k=kv[:, 0], v=kv[:, 1], kp=self.kp.cuda(), vp=self.vp.cuda(), table=self.table.cuda(),
+                 lens=self.lens.cuda(), cu_q=self.cu_q.cuda(), cu_k=self.cu_k.cuda())
+        return x
+
+    def packed(self, x, **kw):
+        return capi.oasr_cross_attn_packed(x["q"], x["k"], x["v"], x["cu_q"], x["cu_k"], kw.pop("max_q", max(self.nq)),
+                                           kw.pop("max_k", max(1, max(self.nk))), **kw)
+
+    def paged(self, x, **kw):
+        return capi.oasr_cross_attn_paged(x["q"], x["kp"], x["vp"], x["table"], x["lens"], x["cu_q"],
+                                          kw.pop("max_q", max(self.nq)), **kw)
+
+    def check(self, out, scale=0.125):
+        out, G = out.double().cpu(), self.H // self.Hkv
+        for s in range(len(self.nq)):
+            rows, keys = (slice(int(c[s]), int(c[s + 1])) for c in (self.cu_q, self.cu_k))
+            want, tol = reference(self.q[rows], self.k[keys].repeat_interleave(G, 1), self.v[keys].repeat_interleave(G, 1),
+                                  scale, self.dt == torch.bfloat16)
+            err = (out[rows] - want).abs()
+            assert bool((err <= tol).all()), (s, float((err / tol.clamp(min=1e-30)).nan_to_num(9e9).max()))
+
+
+# ------------------------------------------------------------------- CPU
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return capi.load()
+
+
+COMMON = [
+    (dict(q=None), capi.OASR_ERR_INVALID_ARG), (dict(cuq=None), capi.OASR_ERR_INVALID_ARG),
+    (dict(out=None), capi.OASR_ERR_INVALID_ARG), (dict(N=0), capi.OASR_ERR_INVALID_ARG),
+    (dict(mq=0), capi.OASR_ERR_INVALID_ARG), (dict(mk=-1), capi.OASR_ERR_INVALID_ARG),
+    (dict(H=6, Hkv=4), capi.OASR_ERR_INVALID_ARG), (dict(Hkv=0), capi.OASR_ERR_INVALID_ARG),
+    (dict(scale=0.0), capi.OASR_ERR_INVALID_ARG), (dict(scale=-1.0), capi.OASR_ERR_INVALID_ARG),
+    (dict(scale=math.inf), capi.OASR_ERR_INVALID_ARG), (dict(scale=math.nan), capi.OASR_ERR_INVALID_ARG),
+    (dict(qs=508), capi.OASR_ERR_INVALID_ARG), (dict(qs=448), capi.OASR_ERR_INVALID_ARG),
+    (dict(q=FAKE + 8), capi.OASR_ERR_INVALID_ARG), (dict(out=FAKE + 4), capi.OASR_ERR_INVALID_ARG),
+    (dict(D=32), capi.OASR_ERR_UNSUPPORTED), (dict(dt=2), capi.OASR_ERR_UNSUPPORTED),
+    (dict(N=65537), capi.OASR_ERR_UNSUPPORTED), (dict(H=2048, qs=131072), capi.OASR_ERR_UNSUPPORTED),
+    (dict(tq=2 ** 31 - 1), capi.OASR_ERR_UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,expect", COMMON + [
+    (dict(cuk=None), capi.OASR_ERR_INVALID_ARG), (dict(tk=0), capi.OASR_ERR_INVALID_ARG),
+    (dict(ks=248), capi.OASR_ERR_INVALID_ARG), (dict(vs=257), capi.OASR_ERR_INVALID_ARG),
+])
+def test_packed_refusals(lib, kw, expect):
+    a = dict(q=FAKE, qs=512, k=FAKE, ks=256, v=FAKE, vs=256, cuq=FAKE, cuk=FAKE, N=2, mq=4, mk=9, tq=8, tk=18, out=FAKE,
+             H=8, Hkv=4, D=64, scale=0.125, dt=capi.OASR_BF16)
+    a.update(kw)
+    assert lib.oasr_cross_attn_packed(*a.values(), None) == expect
+
+
+@pytest.mark.parametrize("kw,expect", COMMON + [
+    (dict(bt=None), capi.OASR_ERR_INVALID_ARG), (dict(cs=None), capi.OASR_ERR_INVALID_ARG),
+    (dict(bs=0), capi.OASR_ERR_INVALID_ARG), (dict(nb=1 << 27), capi.OASR_ERR_UNSUPPORTED),
+    (dict(mbps=1 << 27), capi.OASR_ERR_UNSUPPORTED),
+])
+def test_paged_refusals(lib, kw, expect):
+    a = dict(q=FAKE, qs=512, k=FAKE, v=FAKE, nb=64, bs=16, bt=FAKE, mbps=4, cs=FAKE, cuq=FAKE, N=2, mq=4, mk=9, tq=8, out=FAKE,
+             H=8, Hkv=4, D=64, scale=0.125, dt=capi.OASR_BF16)
+    a.update(kw)
+    assert lib.oasr_cross_attn_paged(*a.values(), None) == expect
+
+
+def test_binding_refusals():
+    q, k, cu = torch.zeros(4, 8, 64), torch.zeros(9, 4, 64), torch.zeros(3, dtype=torch.int32)
+    pool, table = torch.zeros(6, 8, 4, 64), torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        capi.oasr_cross_attn_packed(q, k, k, cu, cu, 2, 9)
+    with pytest.raises(ValueError, match="multiple"):
+        capi.oasr_cross_attn_packed(q[:, :6], k, k, cu, cu, 2, 9)
+    with pytest.raises(ValueError, match="k and v"):
+        capi.oasr_cross_attn_packed(q, k, k[:8], cu, cu, 2, 9)
+    with pytest.raises(TypeError):
+        capi.oasr_cross_attn_packed(q.half(), k.half(), k.half(), cu, cu, 2, 9)
+    with pytest.raises(ValueError, match="block_table"):
+        capi.oasr_cross_attn_paged(q, pool, pool, table[:1], cu[:2], cu, 2)
+    with pytest.raises(ValueError, match="v_pool"):
+        capi.oasr_cross_attn_paged(q, pool, pool[:5], table, cu[:2], cu, 2)
+
+
+# ------------------------------------------------------------------- GPU
+
+SHAPES = [  # queries, keys, H, Hkv
+    ([1], [1], 1, 1),
+    ([1], [1500], 4, 4),                          # a single token: the keys are shared by a cluster
+    ([1, 1, 1], [16, 17, 15], 2, 2),
+    ([8] * 5, [50, 333, 128, 1, 700], 8, 8),      # beams
+    ([3, 0, 5, 1], [40, 90, 0, 33], 4, 2),        # no queries, no keys
+    ([5, 2], [100, 64], 6, 2),                    # three query heads to a key head
+    ([2, 1], [70, 9], 7, 1),                      # seven
+    ([16], [31], 2, 1),
+    ([17, 40], [130, 257], 4, 4),
+    ([128], [128], 2, 2),
+    ([129, 1, 64], [127, 300, 129], 2, 2),
+    ([300, 20, 150], [1500, 0, 640], 2, 2),
+    ([100, 43], [200, 385], 6, 2),                # tiles of 126 rows
+    ([33], [1], 8, 1),
+    ([450], [2000], 1, 1),
+    ([37, 91, 130], [5, 1000, 256], 20, 4),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq,nk,H,Hkv", SHAPES)
+def test_cross(nq, nk, H, Hkv, dtype):
+    c = Case(nq, nk, H, Hkv, dtype, sum(nq) + H)
+    x = c.cuda()
+    c.check(c.packed(x))
+    c.check(c.paged(x))
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bs", [1, 3, 8, 24, 32, 64, 128, 256, 512])
+def test_page_sizes(bs, dtype):
+    for nq, nk in (([2, 1], [70, 333]), ([140, 60], [300, 129])):
+        c = Case(nq, nk, 4, 2, dtype, bs, bs=bs)
+        c.check(c.paged(c.cuda()))
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq,std,scale", [([4, 9], 6.0, 0.125), ([200, 70], 6.0, 0.125), ([200, 70], 0.05, 3.0),
+                                          ([4, 9], 0.05, 3.0), ([150], 1.0, 1e-6)])
+def test_peaked_and_flat(nq, std, scale, dtype):
+    """Scores of up to some hundreds, where a few keys have all the weight and the maximum moves far, and flat ones."""
+    nk = [700, 129][:len(nq)]
+    c = Case(nq, nk, 2, 2, dtype, 5, std=std)
+    x = c.cuda()
+    c.check(c.packed(x, scale=scale), scale)
+    c.check(c.paged(x, scale=scale), scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 180])
+def test_rising_scores(n, dtype):
+    """Keys in order of their scores, each tile's maximum above the last one's by far."""
+    c = Case([n], [900], 1, 1, dtype, 9)
+    q = torch.zeros(n, 1, 64)
+    q[:, 0, 0] = torch.linspace(1, 20, n)
+    c.q = q.to(c.dt)
+    k = torch.zeros(903, 1, 64)
+    k[:, 0, 0] = torch.arange(903) / 4.0
+    c.k = k.to(c.dt)
+    x = c.cuda()
+    c.check(c.packed(x))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 150])
+def test_values_that_are_not_finite(n):
+    """An infinite or NaN key, value or query shows where the formula has it: in its sequence and head, and for a query
+    in its row; its neighbours are not touched."""
+    c = Case([n, n, n], [140, 200, 30], 2, 2, "bf16", 11)
+    for which in "kvq":
+        c2 = Case([n, n, n], [140, 200, 30], 2, 2, "bf16", 11)
+        t = getattr(c2, which)
+        row = n + 1 if which == "q" else 140 + 133
+        t[row, 1, 5] = float("nan")
+        out = c2.packed(c2.cuda()).cpu()
+        bad = torch.zeros_like(out, dtype=torch.bool)
+        if which == "q":
+            bad[n + 1, 1] = True
+        elif which == "k":
+            bad[n:2 * n, 1] = True
+        else:
+            bad[n:2 * n, 1, 5] = True
+        assert torch.equal(out.isnan(), bad), which
+        base = c.packed(c.cuda()).cpu()
+        assert torch.equal(out[~bad], base[~bad])
+    c2 = Case([n, n, n], [140, 200, 30], 2, 2, "bf16", 11)
+    c2.v[140 + 3, 0, 7] = float("inf")
+    out = c2.packed(c2.cuda()).cpu()
+    assert torch.equal(out[n:2 * n, 0, 7], torch.full((n,), float("inf"), dtype=torch.bfloat16))
+    assert out[:n].isfinite().all() and out[2 * n:].isfinite().all() and out[n:2 * n, 1].isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [3, 140])
+def test_rows_behind_the_last_sequence(n, dtype):
+    c = Case([n, n], [200, 60], 2, 1, dtype, 3, spare=150)
+    x = c.cuda()
+    for call in (c.packed, c.paged):
+        out = torch.full_like(x["q"], 7.0)
+        assert call(x, out=out) is out
+        c.check(out)
+        assert bool((out[2 * n:] == 7.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [5, 200])
+def test_longer_than_announced(n, dtype):
+    """max_q and max_k below the sequences' lengths, or far above them."""
+    c = Case([n, 2], [1000, 300], 4, 2, dtype, 4)
+    x = c.cuda()
+    for max_q, max_k in ((1, 1), (n, 1), (1, 1000), (5000, 100000)):
+        c.check(c.packed(x, max_q=max_q, max_k=max_k))
+        c.check(c.paged(x, max_q=max_q, max_k=max_k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [2, 150])
+def test_bad_blocks_and_offsets(n, dtype):
+    c = Case([n, n], [100, 90], 2, 2, dtype, 6)
+    x = c.cuda()
+    x["table"][0, 2], x["table"][1, 1] = -5, 10 ** 9
+    out = c.paged(x)
+    assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+    c.k[32:48], c.v[32:48] = 0, 0           # the pages' rows count as zeros
+    c.k[116:132], c.v[116:132] = 0, 0
+    c.check(out)
+    c = Case([n, n], [100, 90], 2, 2, dtype, 6)
+    x = c.cuda()
+    x["lens"][0], x["lens"][1] = 10 ** 6, -4
+    out = c.paged(x)
+    assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+    assert not out[n:].any() and out.shape[0] == 2 * n
+    x = c.cuda()
+    x["cu_q"][2], x["cu_k"][1] = 10 ** 6, -7
+    keep = torch.full_like(x["q"], 3.0)
+    c.packed(x, out=keep)
+    assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 200])
+def test_pools_past_4_gb(n):
+    nb, bs, H = 140000, 64, 4
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kp, vp = (torch.full((nb, bs, H, 64), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ids = [nb - 1, 3, nb // 2, nb - 7]
+    c = Case([n], [250], H, H, "bf16", 8)
+    for p, b in enumerate(ids):
+        m = min(64, 250 - 64 * p)
+        kp[b, :m], vp[b, :m] = c.k[64 * p:64 * p + m].cuda(), c.v[64 * p:64 * p + m].cuda()
+    out = capi.oasr_cross_attn_paged(c.q.cuda(), kp, vp, torch.tensor([ids], dtype=torch.int32, device="cuda"),
+                                     torch.tensor([250], dtype=torch.int32, device="cuda"), c.cu_q.cuda(), n)
+    c.check(out)
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [4, 300])
+def test_captured_streams_and_side_by_side(n, dtype):
+    """Two captured calls replayed at once on their own streams beside an eager one on a third: each its own bits."""
+    c = [Case([n, n // 2], [800, 333], 4, 2, dtype, 20 + i) for i in range(3)]
+    x = [y.cuda() for y in c]
+    want = [y.packed(z) for y, z in zip(c, x)]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            c[i].packed(x[i], out=outs[i])
+    for _ in range(20):
+        for i in range(2):
+            outs[i].zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        c[2].packed(x[2], out=outs[2], stream=streams[2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    for y, w in zip(c, want):
+        y.check(w)
+
+
+@pytest.mark.gpu
+def test_decoder_step_together():
+    """The operators as a server uses them: pages for two utterances, their states' keys and values by an e4m3 product
+    into the pages by their slots, a beam's tokens over them, and the output projection; eager and replayed, a third
+    utterance in the second round while one has ended."""
+    d, H, Hkv, bs, nb, mbps = 256, 4, 2, 16, 64, 8
+    g = torch.Generator().manual_seed(2)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()
+    w_kv, b_kv, w_o = rnd(2 * Hkv * 64, d) / 16, rnd(2 * Hkv * 64), rnd(d, H * 64) / 16
+    w_kv8, w_kv_scale = capi.oasr_quantize_blocks(w_kv)
+    w_o8, w_o_scale = capi.oasr_quantize_blocks(w_o)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    total, beam, N = 240, 4, 3
+    table, lens, new = torch.full((N, mbps), -1, **i32), torch.zeros(N, **i32), torch.zeros(N, **i32)
+    ring, state = torch.randperm(nb, generator=g).to(torch.int32).cuda(), torch.tensor([0, nb, 0, 0], **i32)
+    kp, vp = (torch.full((nb, bs, Hkv, 64), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    states, q = torch.zeros(total, d, dtype=torch.bfloat16, device="cuda"), rnd(N * beam, H, 64)
+    cu_q = torch.arange(N + 1, **i32) * beam
+
+    def step():
+        slots, _ = capi.oasr_block_table_update(table, lens, new, ring, state, bs, total)
+        x8, xs = capi.oasr_quantize_blocks(states)
+        kv = capi.oasr_linear_e4m3(x8, xs, w_kv8, w_kv_scale, b_kv).view(total, 2, Hkv, 64)
+        capi.oasr_paged_append_slots(kv[:, 0], kv[:, 1], kp, vp, slots)
+        lens.copy_(new)
+        out = capi.oasr_cross_attn_paged(q, kp, vp, table, lens, cu_q, beam)
+        o8, os_ = capi.oasr_quantize_blocks(out.view(N * beam, H * 64))
+        return kv, out, capi.oasr_linear_e4m3(o8, os_, w_o8, w_o_scale, out_dtype=torch.float32)
+
+    graph, held = None, [[] for _ in range(N)]
+    for lengths in ([100, 37, 0], [110, 0, 128], [0, 20, 128]):
+        old = lens.tolist()
+        new.copy_(torch.tensor(lengths, dtype=torch.int32))
+        states.copy_(rnd(total, d))
+        torch.cuda.synchronize()
+        if graph is None:
+            kv, out, y = step()
+            eager = [t.clone() for t in (kv, out, y)]
+            # once more from the same start, captured: the same bits, blocks aside
+            for t in (table, lens):
+                t.fill_(-1 if t is table else 0)
+            ring.copy_(torch.randperm(nb, generator=g).to(torch.int32))
+            state.copy_(torch.tensor([0, nb, 0, 0], dtype=torch.int32))
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                kv, out, y = step()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(eager, (kv, out, y)))
+        else:
+            graph.replay()
+            torch.cuda.synchronize()
+        at = 0
+        for s in range(N):
+            grown = max(0, lengths[s] - old[s])
+            held[s] = held[s][:lengths[s]] + list(kv[at:at + grown].cpu())
+            at += grown
+            rows = slice(s * beam, (s + 1) * beam)
+            k, v = (torch.stack(held[s])[:, i] if held[s] else torch.zeros(0, Hkv, 64) for i in range(2))
+            want, tol = reference(q[rows].cpu(), k.repeat_interleave(2, 1), v.repeat_interleave(2, 1), 0.125, True)
+            assert bool(((out[rows].double().cpu() - want).abs() <= tol).all())
+    assert capi.oasr_device_status() == 0
