@@ -122,6 +122,35 @@ bool encode_bytes(CUtensorMap* map, const void* base, long long rows, int row_by
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_bytes128(CUtensorMap* map, const void* base, long long rows, int row_bytes, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rows < 1 || row_bytes < 16 || row_bytes % 16 || box_rows < 1 || box_rows > 256 || !aligned16(base)) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_head_rows_bf16(CUtensorMap* map, const void* base, long long rows, int H, long long row_stride, int box_heads,
+                           int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rows < 1 || H < 1 || row_stride < 64LL * H || row_stride % 8 || box_heads < 1 || box_heads > 256 ||
+        box_rows < 1 || box_rows > 256 || !aligned16(base))
+        return false;
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {64 * 2, static_cast<cuuint64_t>(row_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 // A wait on a barrier that no thread or copy ever signals: it runs out after limit_ns and
 // takes the path every pipeline wait of the library takes when it runs out.

@@ -7,8 +7,10 @@
 // shorter.  The format is the 8-bit cache's (e4m3.cuh) with 128 values to a scale.
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "e4m3.cuh"
 #include "host_common.h"
+#include "linear.cuh"
 
 namespace oasr {
 namespace {
@@ -58,11 +60,6 @@ struct E4Problem {
     const void* bias;         // null: none
     int M, N, K, kb;
 };
-
-__device__ __forceinline__ float bias_at(const float* b, int n) { return __ldg(b + n); }
-__device__ __forceinline__ float bias_at(const __nv_bfloat16* b, int n) { return __bfloat162float(b[n]); }
-__device__ __forceinline__ void put(float* o, float v) { *o = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
 
 __device__ __forceinline__ void unpack16(const uint4& w, float (&v)[16])
 {
@@ -116,18 +113,360 @@ __global__ void __launch_bounds__(256) linear_e4m3_few_kernel(const E4Problem p,
     grid_dep_trigger();
 }
 
+// Warps of the tensor-core kernel: eight for the epilogue, four for the scales, the issuer, the TMA producer.  The
+// producer brings 128 bytes of K of the tile's rows into a ring; the scale warps write the scales of four
+// blocks (a word a row) into tensor memory, where every quadrant of lanes has them once; the issuer's products take
+// them from there, a block's scale for each of its four steps of 32.  Two accumulators let a tile's
+// epilogue overlap the next tile's products.
+constexpr int kE4EpiWarps = 8, kE4ScaleWarps = 4, kE4Issuer = kE4EpiWarps + kE4ScaleWarps;
+constexpr int kE4Threads = 32 * (kE4Issuer + 2);
+
+template <int BN>
+struct E4Smem {
+    static constexpr int tile_a = 128 * 128, tile = (128 + BN) * 128;   // x rows, then w rows
+    static constexpr int stages = BN > 128 ? 5 : 6;
+    static constexpr int off_out = stages * tile;                       // [8 warps][32 rows][64 bytes]
+    static constexpr int off_bias = off_out + kE4EpiWarps * 32 * 64;    // [8 warps][BN / 2] floats
+    static constexpr int off_bar = off_bias + kE4EpiWarps * BN / 2 * 4;   // full, empty, scales full[2], free[2], acc full[2], free[2], drain
+    static constexpr int off_misc = off_bar + (2 * stages + 9) * 8;
+    static constexpr int bytes = off_misc + 16 + 1024;
+    static constexpr int sb_cols = (BN + 127) / 128 * 4;                // columns of w's scales
+    static constexpr int sf_cols = 4 + sb_cols, off_sf = 2 * BN;        // x's, then w's; two buffers
+    static constexpr int used = off_sf + 2 * sf_cols;
+    static constexpr int cols = used <= 128 ? 128 : used <= 256 ? 256 : 512;
+};
+
+struct E4Args {
+    E4Problem p;
+    void* out;
+    int nt, tiles, ksteps;
+    int by_tma;   // the output's rows suit TMA: stored by it
+    unsigned* status;
+};
+
+// D [+]= (A . B) with the scales at sa (A's rows) and sb (B's), one for each 32 of K.
+__device__ __forceinline__ void umma_e4m3_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sa, uint32_t sb,
+                                                 int acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(sa), "r"(sb), "r"(acc));
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* w)
+{
+    static_assert(N == 2 || N == 4 || N == 8, "columns of a store");
+    if constexpr (N == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(at), "r"(w[0]), "r"(w[1]) : "memory");
+    else if constexpr (N == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3])
+                     : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+}
+
+// The scale bytes of blocks 4 g .. 4 g + 3 of a row; 2^0 for rows past the matrix and blocks past the row, whose
+// values come as zeros.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int row, int rows, int kb, int g)
+{
+    uint32_t w = 0x7f7f7f7fu;
+    if (row >= rows) return w;
+    const uint8_t* p = s + static_cast<long long>(row) * kb + 4 * g;
+    if (!((kb | static_cast<int>(reinterpret_cast<uintptr_t>(s))) & 3)) return __ldg(reinterpret_cast<const uint32_t*>(p));
+    const int n = min(4, kb - 4 * g);
+    for (int i = 0; i < n; ++i) w = (w & ~(255u << (8 * i))) | (static_cast<uint32_t>(__ldg(p + i)) << (8 * i));
+    return w;
+}
+
+template <int BN, typename Elem>
+__global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid_constant__ CUtensorMap tm_x,
+                                                                    const __grid_constant__ CUtensorMap tm_w,
+                                                                    const __grid_constant__ CUtensorMap tm_out, const E4Args a)
+{
+    using SP = E4Smem<BN>;
+    constexpr int S = SP::stages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_addr(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SP::off_misc);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SP::off_misc + 4);
+    const uint32_t bar_full = sb + SP::off_bar, bar_empty = bar_full + 8 * S;
+    const uint32_t bar_sf = bar_empty + 8 * S, bar_sf_free = bar_sf + 16;
+    const uint32_t bar_acc_full = bar_sf_free + 16, bar_acc_free = bar_acc_full + 16, bar_drain = bar_acc_free + 16;
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_sf + 8 * i, kE4ScaleWarps);
+            mbar_init(bar_sf_free + 8 * i, 1);
+            mbar_init(bar_acc_full + 8 * i, 1);
+            mbar_init(bar_acc_free + 8 * i, kE4EpiWarps);
+        }
+        mbar_init(bar_drain, 1);
+        fence_mbar_init();
+        *s_abort = 0;
+    }
+    if (warp == kE4Issuer + 1 && lane == 0) {
+        prefetch_tensormap(&tm_x);
+        prefetch_tensormap(&tm_w);
+        if (a.by_tma) prefetch_tensormap(&tm_out);
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)), "r"(SP::cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    grid_dep_wait();
+
+    // tiles blockIdx.x, + gridDim.x, ... are the CTA's, a row of tiles after the other
+    const int first = blockIdx.x, stride = gridDim.x;
+    const int my_tiles = first < a.tiles ? (a.tiles - 1 - first) / stride + 1 : 0;
+    const int groups = (a.ksteps + 3) / 4;   // of four blocks
+
+    if (warp == kE4Issuer + 1) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int i = 0;
+            bool ok = true;
+            for (int lt = 0; lt < my_tiles && ok; ++lt) {
+                const int t = first + lt * stride, mt = t / a.nt, nt = t - mt * a.nt;
+                for (int kb = 0; kb < a.ksteps; ++kb, ++i) {
+                    const int slot = i % S;
+                    if (i >= S && !sleep_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    // rows past M or N and bytes past K come as zeros
+                    const uint32_t dst = sb + slot * SP::tile, bar = bar_full + 8 * slot;
+                    mbar_arrive_expect_tx(bar, SP::tile);
+                    tma_load_2d(dst, &tm_x, bar, 128 * kb, mt * 128);
+                    tma_load_2d(dst + SP::tile_a, &tm_w, bar, 128 * kb, nt * BN);
+                }
+            }
+            // no copy may still be landing when the CTA exits
+            for (int u = i - S; u < i; ++u)
+                if (u >= 0 && !mbar_wait(bar_full + 8 * (u % S), (u / S) & 1)) *s_abort = 1;
+        }
+    } else if (warp == kE4Issuer) {
+        // ------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            // e4m3 A and B, fp32 D, UE8M0 scales, M = 128
+            constexpr uint32_t id = (static_cast<uint32_t>(BN >> 3) << 17) | (1u << 23) | (1u << 27);
+            int i = 0, gi = 0, nacc = 0, nfree = 0;
+            bool ok = true;
+            for (int lt = 0; lt < my_tiles && ok; ++lt) {
+                const int buf = lt & 1;
+                if (lt >= 2 && !sleep_or_abort(bar_acc_free + 8 * buf, ((lt >> 1) - 1) & 1, s_abort)) break;
+                for (int kb = 0; kb < a.ksteps; ++kb, ++i) {
+                    const int slot = i % S, sf = gi & 1;
+                    if ((!(kb & 3) && !sleep_or_abort(bar_sf + 8 * sf, (gi >> 1) & 1, s_abort)) ||
+                        !sleep_or_abort(bar_full + 8 * slot, (i / S) & 1, s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t base = sb + slot * SP::tile, sa = tmem + SP::off_sf + sf * SP::sf_cols;
+                    const uint32_t idk = id | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_e4m3_scaled(tmem + buf * BN, sdesc(base + 32 * k), sdesc(base + SP::tile_a + 32 * k), idk, sa, sa + 4,
+                                         kb > 0 || k > 0);
+                    umma_commit(bar_empty + 8 * slot);
+                    ++nfree;
+                    if ((kb & 3) == 3 || kb == a.ksteps - 1) {
+                        umma_commit(bar_sf_free + 8 * sf);
+                        ++gi;
+                    }
+                }
+                if (!ok) break;
+                umma_commit(bar_acc_full + 8 * buf);
+                ++nacc;
+            }
+            // drain: every MMA issued has finished and every arrival it owes has landed
+            umma_commit(bar_drain);
+            bool drained = mbar_wait(bar_drain, 0);
+            for (int u = nacc - 2; u < nacc; ++u)
+                if (u >= 0) drained = mbar_wait(bar_acc_full + 8 * (u & 1), (u >> 1) & 1) && drained;
+            for (int u = gi - 2; u < gi; ++u)
+                if (u >= 0) drained = mbar_wait(bar_sf_free + 8 * (u & 1), (u >> 1) & 1) && drained;
+            for (int u = nfree - S; u < nfree; ++u)
+                if (u >= 0) drained = mbar_wait(bar_empty + 8 * (u % S), (u / S) & 1) && drained;
+            if (!drained) *s_abort = 1;
+        }
+    } else if (warp >= kE4EpiWarps) {
+        // --------------------------------------------------------------- scales
+        // lane l of each quadrant: the words of rows l, l + 32, ... in neighbouring columns
+        constexpr int NB = BN / 32, NBS = NB <= 2 ? 2 : NB <= 4 ? 4 : 8;
+        const uint32_t quad = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + SP::off_sf;
+        int gi = 0;
+        bool ok = true;
+        for (int lt = 0; lt < my_tiles && ok; ++lt) {
+            const int t = first + lt * stride, mt = t / a.nt, nt = t - mt * a.nt;
+            for (int g = 0; g < groups; ++g, ++gi) {
+                uint32_t wa[4], wb[NBS];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) wa[j] = scale_word(a.p.xs, mt * 128 + 32 * j + lane, a.p.M, a.p.kb, g);
+#pragma unroll
+                for (int j = 0; j < NBS; ++j)
+                    wb[j] = j < NB ? scale_word(a.p.ws, nt * BN + 32 * j + lane, a.p.N, a.p.kb, g) : 0u;
+                const int sf = gi & 1;
+                if (gi >= 2 && !__all_sync(0xffffffffu, sleep_or_abort(bar_sf_free + 8 * sf, ((gi >> 1) - 1) & 1, s_abort))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                tmem_st<4>(quad + sf * SP::sf_cols, wa);
+                tmem_st<NBS>(quad + sf * SP::sf_cols + 4, wb);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_release(bar_sf + 8 * sf);
+            }
+        }
+    } else {
+        // --------------------------------------------------------------- epilogue
+        // warp: 32 rows (its TMEM lanes, warp % 4) of one half of the tile's columns (warp / 4)
+        constexpr int HN = BN / 2;
+        const int rq = warp & 3, half = warp >> 2, M = a.p.M, N = a.p.N;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * rq) << 16) + half * HN;
+        float* s_bias = reinterpret_cast<float*>(sm + SP::off_bias) + warp * HN;
+        uint8_t* s_out = sm + SP::off_out + warp * 32 * 64;
+        const Elem* bias = static_cast<const Elem*>(a.p.bias);
+        for (int lt = 0; lt < my_tiles; ++lt) {
+            const int t = first + lt * stride, mt = t / a.nt, nt = t - mt * a.nt, buf = lt & 1;
+            const int row0 = mt * 128 + 32 * rq, col0 = nt * BN + half * HN;
+            __syncwarp();
+            for (int j = lane; j < HN; j += 32) s_bias[j] = bias && col0 + j < N ? bias_at(bias, col0 + j) : 0.f;
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, sleep_or_abort(bar_acc_full + 8 * buf, (lt >> 1) & 1, s_abort))) break;
+            tc_fence_after();
+            // 16 sums of the lane's row at a time
+            auto sums = [&](int c, float* v) {
+                uint32_t r[16];
+                OASR_TMEM_LD16(tl + buf * BN + c, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 b = *reinterpret_cast<const float4*>(s_bias + c + j);
+                    v[j] = __uint_as_float(r[j]) + b.x, v[j + 1] = __uint_as_float(r[j + 1]) + b.y;
+                    v[j + 2] = __uint_as_float(r[j + 2]) + b.z, v[j + 3] = __uint_as_float(r[j + 3]) + b.w;
+                }
+            };
+            if (a.by_tma) {
+                // 64 bytes of every row at a time, staged and stored by TMA
+                constexpr int CB = 64 / sizeof(Elem);
+#pragma unroll 1
+                for (int c = 0; c < HN; c += CB) {
+                    if (col0 + c >= N) break;
+                    float v[CB];
+#pragma unroll
+                    for (int j = 0; j < CB; j += 16) sums(c + j, v + j);
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the tile's last use
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {   // 16 bytes
+                        uint4 o;
+                        if constexpr (sizeof(Elem) == 2)
+                            o = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                           pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+                        else
+                            o = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                           __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+                        *reinterpret_cast<uint4*>(s_out + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) = o;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && row0 < M)
+                        tma_store_2d(&tm_out, smem_addr(s_out), (col0 + c) * static_cast<int>(sizeof(Elem)), row0);
+                }
+            } else {
+                // rows of any alignment: 16 columns at a time, staged, 16 lanes to a row
+                float* s_f = reinterpret_cast<float*>(s_out);
+#pragma unroll 1
+                for (int c = 0; c < HN; c += 16) {
+                    if (col0 + c >= N) break;
+                    float v[16];
+                    sums(c, v);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4*>(s_f + 16 * lane + 4 * (j ^ ((lane >> 1) & 3))) =
+                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    __syncwarp();
+                    const int j = lane & 15;
+                    Elem* to = static_cast<Elem*>(a.out) + static_cast<long long>(row0 + (lane >> 4)) * N + col0 + c + j;
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) {
+                        const int rr = 2 * i + (lane >> 4);
+                        if (row0 + rr < M && col0 + c + j < N)
+                            put(to + 2LL * i * N, s_f[16 * rr + 4 * ((j >> 2) ^ (i & 3)) + (j & 3)]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_release(bar_acc_free + 8 * buf);
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // every store has been made
+    }
+    grid_dep_trigger();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(SP::cols));
+    }
+    if (tid == 0 && *s_abort) atomicOr(a.status, kErrTimeout);
+}
+
 // --------------------------------------------------------------------------- host
 
 constexpr int kE4MaxRows = 0x7fffff00, kE4MaxK = 65536;
 
+int g_smem_done_e4l[4][64];
+
+template <int BN, typename Elem>
+oasr_status launch_e4(const E4Problem& p, void* out, int slot, int sms, cudaStream_t stream)
+{
+    using SP = E4Smem<BN>;
+    const long long mt = (p.M + 127LL) / 128, nt = (p.N + BN - 1LL) / BN, row = p.N * static_cast<long long>(sizeof(Elem));
+    if (mt * nt > 0x7fffffffLL - sms) return OASR_ERR_UNSUPPORTED;
+    auto kern = linear_e4m3_kernel<BN, Elem>;
+    if (!ensure_smem(kern, SP::bytes, g_smem_done_e4l[slot])) return OASR_ERR_CUDA;
+    CUtensorMap tm_x, tm_w, tm_out = {};
+    const bool by_tma = row % 16 == 0 && row <= 0x7fffffffLL;
+    if (!encode_bytes128(&tm_x, p.x, p.M, p.K, 128) || !encode_bytes128(&tm_w, p.w, p.N, p.K, BN) ||
+        (by_tma && !encode_bytes(&tm_out, out, p.M, static_cast<int>(row), 32, true)))
+        return OASR_ERR_INVALID_ARG;
+    const E4Args a = {p, out, static_cast<int>(nt), static_cast<int>(mt * nt), p.kb, by_tma, status_word()};
+    if (!a.status) return OASR_ERR_CUDA;
+    return launch_pdl(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(kE4Threads), SP::bytes, stream, tm_x, tm_w, tm_out, a);
+}
+
 template <typename Elem>
 oasr_status dispatch_e4(const E4Problem& p, void* out, cudaStream_t stream)
 {
-    const long long groups = (p.M + kE4FewRows - 1LL) / kE4FewRows;
-    if (groups > 65535) return OASR_ERR_UNSUPPORTED;
-    const dim3 grid((p.N + 7) / 8, static_cast<unsigned>(groups));
-    if (p.M == 1) return launch_pdl(linear_e4m3_few_kernel<1, Elem>, grid, dim3(256), 0, stream, p, static_cast<Elem*>(out));
-    return launch_pdl(linear_e4m3_few_kernel<kE4FewRows, Elem>, grid, dim3(256), 0, stream, p, static_cast<Elem*>(out));
+    if (p.M <= kE4FewRows) {
+        const dim3 grid((p.N + 7) / 8);
+        if (p.M == 1) return launch_pdl(linear_e4m3_few_kernel<1, Elem>, grid, dim3(256), 0, stream, p, static_cast<Elem*>(out));
+        return launch_pdl(linear_e4m3_few_kernel<kE4FewRows, Elem>, grid, dim3(256), 0, stream, p, static_cast<Elem*>(out));
+    }
+    const int sms = sm_count();
+    if (!sms) return OASR_ERR_CUDA;
+    constexpr int s = sizeof(Elem) == 4 ? 2 : 0;
+    const long long wide = ((p.M + 127LL) / 128) * ((p.N + 191LL) / 192);
+    if (wide >= sms) return launch_e4<192, Elem>(p, out, s, sms, stream);
+    return launch_e4<64, Elem>(p, out, s + 1, sms, stream);
 }
 
 }  // namespace

@@ -39,6 +39,16 @@ bool encode_rows_e4m3(CUtensorMap* map, const void* base, long long rows, int bo
 // the driver rejects it.
 bool encode_bytes(CUtensorMap* map, const void* base, long long rows, int row_bytes, int box_rows, bool swizzle64 = false);
 
+// Encode a 2-D map over rows of row_bytes bytes (a multiple of 16) with a box of 128 bytes of box_rows rows, 128-byte
+// swizzled.  Returns false if the driver rejects it.
+bool encode_bytes128(CUtensorMap* map, const void* base, long long rows, int row_bytes, int box_rows);
+
+// Encode a 3-D bf16 map over rows of [rows, H, 64] that lie row_stride elements apart (a multiple of 8) with a box
+// of box_heads heads of box_rows rows, 128-byte swizzled: in shared memory [row][head][64].  Returns false if the
+// driver rejects it.
+bool encode_head_rows_bf16(CUtensorMap* map, const void* base, long long rows, int H, long long row_stride, int box_heads,
+                           int box_rows);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline oasr_status launch_status()

@@ -22,6 +22,7 @@
 #include "cluster.cuh"
 #include "e4m3.cuh"
 #include "host_common.h"
+#include "linear.cuh"
 
 namespace oasr {
 namespace {
@@ -121,19 +122,6 @@ struct I8Args {
     unsigned* status;
 };
 
-__device__ __forceinline__ float bias_at(const float* b, int n) { return __ldg(b + n); }
-__device__ __forceinline__ float bias_at(const __nv_bfloat16* b, int n) { return __bfloat162float(b[n]); }
-__device__ __forceinline__ void put(float* o, float v) { *o = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
-
-// 32 bytes to global memory, aligned to 32.
-__device__ __forceinline__ void st_32bytes(void* to, const uint32_t* v)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 // Four sums times their row's scale x and columns' scales w, plus the bias b; each operation rounded.
 __device__ __forceinline__ float4 scaled(const uint32_t* s, float x, float4 w, float4 b)
 {
@@ -186,24 +174,6 @@ struct I8Smem {
     // a group's last wait on a slot's barrier was for the phase before (it comes by every slot in turn)
     static_assert(stages % kI8Groups == 0 && raws % kI8Groups == 0, "a wait is one phase behind at most");
 };
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-
-// 64 bytes of 32 rows from shared memory to (x, y); what lies outside the tensor is not written.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(src), "r"(x), "r"(y)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
 
 struct I8Outs {
     CUtensorMap m[4];   // of I8Args::out
