@@ -74,7 +74,8 @@ __device__ __forceinline__ int cross_row(const CrossArgs& a, const CrossSeq& t, 
     return id * a.bs + (j - page * a.bs);
 }
 
-// The tensor-core form (csrc/cross_tc.cu).
-oasr_status cross_tc(const CrossArgs& a, int max_q, int max_k, cudaStream_t stream);
+// The tensor-core form (cross_tc.cu), and whether it takes the call's heads and pages.
+bool cross_tc_takes(const CrossArgs& a);
+oasr_status cross_tc(CrossArgs a, int max_q, cudaStream_t stream);
 
 }  // namespace oasr

@@ -380,6 +380,7 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     const int sms = sm_count();
     if (!sms || !a.status) return OASR_ERR_CUDA;
     const bool f32 = dt == OASR_F32, paged = a.table != nullptr;
+    if (!f32 && static_cast<long long>(max_q) * a.G > kXRows && cross_tc_takes(a)) return cross_tc(a, max_q, stream);
     // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
     const long long want = (static_cast<long long>(max_q) * a.G + kXRows - 1) / kXRows, items = static_cast<long long>(a.N) * a.Hkv;
     long long tiles = want;

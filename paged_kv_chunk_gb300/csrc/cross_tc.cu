@@ -1,0 +1,387 @@
+// Cross attention for many rows a sequence (whole transcripts, rescored hypotheses), bf16, on tcgen05.
+//
+// A CTA takes tiles of up to 128 rows (queries times the heads of a group, cross.cuh) against all keys of their
+// sequence, 128 at a time:
+//
+//   S = Q . K^T    tcgen05, 128 x 128 in tensor memory
+//   P = 2^(c S - m), m the row's running maximum, its sum in fp32      a softmax thread per row
+//   O += P . V     tcgen05, P bf16 in tensor memory, O 128 x 64
+//
+// S, P and O have columns of their own (128 + 64 + 64 of 256), so the next stage's S is computed while this one's
+// exponentials are, and two CTAs share an SM: one's softmax runs beside the other's products.  O is rescaled
+// only when a row's maximum has grown by more than 2^8 (P then stays below 2^8, the same relative
+// rounding).  P . V stops at the 16 keys that hold the last one; V rows behind it within those are zeroed.
+#include "cluster.cuh"
+#include "cross.cuh"
+
+namespace oasr {
+namespace {
+
+constexpr int kCRows = 128, kCKeys = 128, kCRowBytes = 128;
+constexpr int kCSoftWarps = 4, kCProducer = kCSoftWarps, kCIssuer = kCSoftWarps + 1, kCThreads = 32 * (kCIssuer + 1);
+constexpr int kCColS = 0, kCColP = 128, kCColO = 192, kCCols = 256;
+
+struct CSmem {
+    static constexpr int tile = kCKeys * kCRowBytes, ks = 3, vs = 2;
+    static constexpr int off_q = 0, off_k = tile, off_v = off_k + ks * tile;
+    static constexpr int off_bar = off_v + vs * tile;   // k full[3], empty[3], v full[2], empty[2], q full, q free, s full, s free, p full, pv done, drain
+    static constexpr int off_misc = off_bar + (2 * ks + 2 * vs + 7) * 8;
+    static constexpr int bytes = off_misc + 24 + 1024;
+};
+
+// Which rows an item has.
+struct CItem {
+    int s, h, tile;
+    __device__ __forceinline__ CItem(const CrossArgs& a, unsigned x)
+    {
+        tile = x % a.tiles;
+        x /= a.tiles;
+        h = x % a.Hkv;
+        s = x / a.Hkv;
+    }
+};
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
+                                                                const __grid_constant__ CUtensorMap tm_k,
+                                                                const __grid_constant__ CUtensorMap tm_v, const CrossArgs a)
+{
+    using SP = CSmem;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_addr(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SP::off_misc);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(sm + SP::off_misc + 4);
+    const uint32_t bar_k = sb + SP::off_bar, bar_k_free = bar_k + 8 * SP::ks;
+    const uint32_t bar_v = bar_k_free + 8 * SP::ks, bar_v_free = bar_v + 8 * SP::vs;
+    const uint32_t bar_q = bar_v_free + 8 * SP::vs, bar_q_free = bar_q + 8, bar_s = bar_q_free + 8, bar_s_free = bar_s + 8;
+    const uint32_t bar_p = bar_s_free + 8, bar_pv = bar_p + 8, bar_drain = bar_pv + 8;
+    unsigned err = 0;
+    if (tid == 0) {
+        for (int i = 0; i < SP::ks; ++i) {
+            mbar_init(bar_k + 8 * i, 1);
+            mbar_init(bar_k_free + 8 * i, 1);
+        }
+        for (int i = 0; i < SP::vs; ++i) {
+            mbar_init(bar_v + 8 * i, 1);
+            mbar_init(bar_v_free + 8 * i, 1);
+        }
+        mbar_init(bar_q, 1);
+        mbar_init(bar_q_free, 1);
+        mbar_init(bar_s, 1);
+        mbar_init(bar_s_free, kCSoftWarps);
+        mbar_init(bar_p, kCSoftWarps);
+        mbar_init(bar_pv, 1);
+        mbar_init(bar_drain, 1);
+        fence_mbar_init();
+        *s_abort = 0;
+    }
+    if (warp == kCProducer && lane == 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    if (warp == kCIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(s_tmem)), "r"(kCCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    grid_dep_wait();
+
+    const CItem it(a, blockIdx.x);
+    const CrossSeq t(a, it.s, err);
+    const int qpt = kCRows / a.G, rpt = qpt * a.G;   // queries and rows of a tile
+    const int rows = t.nq * a.G, stages = (t.nk + kCKeys - 1) / kCKeys;
+    const int my_tiles = it.tile * rpt < rows ? ((rows - 1) / rpt - it.tile) / a.tiles + 1 : 0;
+
+    if (stages == 0) {
+        // no keys: zeros
+        for (int lt = 0; lt < my_tiles; ++lt) {
+            const int r0 = (it.tile + lt * a.tiles) * rpt;
+            for (int i = tid; i < min(rpt, rows - r0) * 8; i += kCThreads) {
+                const int R = r0 + (i >> 3), qi = R / a.G;
+                reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                                         (static_cast<long long>(t.q0 + qi) * a.H + it.h * a.G + R - qi * a.G) * 64)[i & 7] =
+                    make_uint4(0, 0, 0, 0);
+            }
+        }
+    } else if (warp == kCProducer) {
+        // ------------------------------------------------------------ TMA producer
+        // paged: lane i brings the i-th page of a stage (its part of one, for pages over 128), so block ids are
+        // read one stage ahead by the lanes that need them
+        const int bs = min(a.bs, kCKeys), boxes = PAGED ? kCKeys / bs : 1;
+        auto page_of = [&](int j0) {   // row of the lane's box; -1: past the last key
+            const int j = j0 + lane * bs;
+            if (!PAGED) return lane == 0 ? t.k0 + j0 : -1;
+            if (lane >= boxes || j >= t.nk) return -1;
+            const int r = cross_row<true>(a, t, it.s, j, err);
+            return r < 0 ? a.num_blocks * a.bs : r;   // outside the pools: comes as zeros
+        };
+        int g = 0, nv = 0, nq = 0;   // K stages, V stages and Q tiles requested
+        bool ok = true;
+        for (int lt = 0; lt < my_tiles && ok; ++lt) {
+            if (lt > 0 && !__all_sync(0xffffffffu, sleep_or_abort(bar_q_free, (lt - 1) & 1, s_abort))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar_q, rpt * kCRowBytes);
+                tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, it.h * a.G, t.q0 + (it.tile + lt * a.tiles) * qpt);
+            }
+            ++nq;
+            int row = page_of(0);
+            for (int st = 0; st < stages; ++st) {
+                const int next = st + 1 < stages ? page_of((st + 1) * kCKeys) : -1;
+                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                const int bytes = PAGED ? n * bs * kCRowBytes : SP::tile;
+                auto bring = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar) {
+                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (row >= 0) tma_load_3d(dst + lane * bs * kCRowBytes, tm, bar, 0, it.h, row);
+                };
+                const int ks = g % SP::ks, vs = nv % SP::vs;
+                if (g >= SP::ks && !__all_sync(0xffffffffu, sleep_or_abort(bar_k_free + 8 * ks, ((g / SP::ks) - 1) & 1, s_abort))) {
+                    ok = false;
+                    break;
+                }
+                bring(&tm_k, sb + SP::off_k + ks * SP::tile, bar_k + 8 * ks);
+                ++g;
+                if (nv >= SP::vs && !__all_sync(0xffffffffu, sleep_or_abort(bar_v_free + 8 * vs, ((nv / SP::vs) - 1) & 1, s_abort))) {
+                    ok = false;
+                    break;
+                }
+                bring(&tm_v, sb + SP::off_v + vs * SP::tile, bar_v + 8 * vs);
+                ++nv;
+                row = next;
+            }
+        }
+        // no copy may still be landing when the CTA exits
+        if (lane == 0) {
+            for (int u = g - SP::ks; u < g; ++u)
+                if (u >= 0 && !mbar_wait(bar_k + 8 * (u % SP::ks), (u / SP::ks) & 1)) *s_abort = 1;
+            for (int u = nv - SP::vs; u < nv; ++u)
+                if (u >= 0 && !mbar_wait(bar_v + 8 * (u % SP::vs), (u / SP::vs) & 1)) *s_abort = 1;
+            if (nq && !mbar_wait(bar_q, (nq - 1) & 1)) *s_abort = 1;
+        }
+    } else if (warp == kCIssuer) {
+        // ------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc(kCRows, kCKeys, 0), id_o = idesc(kCRows, 64, 1);
+            int gs = 0, g = 0;   // S issued, P . V issued
+            bool ok = true;
+            for (int lt = 0; lt < my_tiles && ok; ++lt) {
+                if (!sleep_or_abort(bar_q, lt & 1, s_abort)) break;
+                auto issue_s = [&](bool last) {
+                    const int ks = gs % SP::ks;
+                    if (!sleep_or_abort(bar_k + 8 * ks, (gs / SP::ks) & 1, s_abort) ||
+                        (gs > 0 && !sleep_or_abort(bar_s_free, (gs - 1) & 1, s_abort)))
+                        return false;
+                    tc_fence_after();
+                    const uint32_t kb = sb + SP::off_k + ks * SP::tile;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_ss(tmem + kCColS, sdesc(sb + SP::off_q + 32 * k), sdesc(kb + 32 * k), id_s, k > 0);
+                    umma_commit(bar_s);
+                    umma_commit(bar_k_free + 8 * ks);
+                    if (last) umma_commit(bar_q_free);
+                    ++gs;
+                    return true;
+                };
+                ok = issue_s(stages == 1);
+                for (int st = 0; st < stages && ok; ++st, ++g) {
+                    if (st + 1 < stages && !(ok = issue_s(st + 2 == stages))) break;
+                    const int vs = g % SP::vs;
+                    if (!sleep_or_abort(bar_p, g & 1, s_abort) || !sleep_or_abort(bar_v + 8 * vs, (g / SP::vs) & 1, s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t vb = sb + SP::off_v + vs * SP::tile;
+                    const int steps = min((t.nk - st * kCKeys + 15) >> 4, kCKeys / 16);
+#pragma unroll
+                    for (int k = 0; k < kCKeys / 16; ++k)
+                        if (k < steps) umma_ts(tmem + kCColO, tmem + kCColP + 8 * k, sdesc(vb + 2048 * k), id_o, st > 0 || k > 0);
+                    umma_commit(bar_pv);
+                    umma_commit(bar_v_free + 8 * vs);
+                }
+            }
+            // drain: every product issued has finished and its arrivals have landed
+            umma_commit(bar_drain);
+            if (!mbar_wait(bar_drain, 0)) *s_abort = 1;
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+        const int r = tid;   // the thread's row of the tile
+        int g = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, sleep_or_abort(bar, parity, s_abort)); };
+        for (int lt = 0; lt < my_tiles && ok; ++lt) {
+            const int R = (it.tile + lt * a.tiles) * rpt + r;
+            const int live = min(rpt, rows - (it.tile + lt * a.tiles) * rpt);   // rows of the tile
+            float m = -INFINITY, l = 0.f;
+            for (int st = 0; st < stages; ++st, ++g) {
+                if (!(ok = wait(bar_s, g & 1))) break;
+                tc_fence_after();
+                const int left = t.nk - st * kCKeys;   // keys of this stage and later ones
+                if (32 * warp < live) {
+                    float s[kCKeys];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t* w = reinterpret_cast<uint32_t*>(s) + 32 * q;
+                        OASR_TMEM_LD32(tl + kCColS + 32 * q, w);
+                    }
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_release(bar_s_free);
+                    if (left < kCKeys) {
+#pragma unroll
+                        for (int j = 0; j < kCKeys; ++j)
+                            if (j >= left) s[j] = -INFINITY;
+                    }
+                    float x[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        x[q] = s[q];
+#pragma unroll
+                        for (int j = 4; j < kCKeys - 4; j += 8) x[q] = fmax3(x[q], s[j + q], s[j + 4 + q]);
+                        x[q] = fmaxf(x[q], s[kCKeys - 4 + q]);
+                    }
+                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.c;
+                    if (st == 0) {
+                        m = top;
+                    } else {
+                        const bool grown = top > m + 8.f;
+                        if (__any_sync(0xffffffffu, grown)) {
+                            if (!(ok = wait(bar_pv, (g - 1) & 1))) break;
+                            tc_fence_after();
+                            const float f = grown ? ex2_approx(m - top) : 1.f;
+                            if (grown) m = top;
+                            l *= f;
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t w[32];
+                                OASR_TMEM_LD32(tl + kCColO + 32 * q, w);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
+                                OASR_TMEM_ST32(tl + kCColO + 32 * q, w);
+                            }
+                        }
+                    }
+                    float2 sum = make_float2(0.f, 0.f);
+                    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-m, -m);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 e = __ffma2_rn(make_float2(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]), c2, m2);
+                            const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+                            sum = __fadd2_rn(sum, p);
+                            pk[j] = pack_bf16(p.x, p.y);
+                        }
+                        if (q == 0 && g > 0) {   // the last P . V has read P
+                            if (!(ok = wait(bar_pv, (g - 1) & 1))) break;
+                            tc_fence_after();
+                        }
+                        OASR_TMEM_ST16(tl + kCColP + 16 * q, pk);
+                    }
+                    if (!ok) break;
+                    l += sum.x + sum.y;
+                    tmem_wait_st();
+                    tc_fence_before();
+                } else {
+                    // no rows of this warp's lanes: what their P holds reaches no other row
+                    if (lane == 0) mbar_arrive_release(bar_s_free);
+                    if (g > 0 && !(ok = wait(bar_pv, (g - 1) & 1))) break;
+                }
+                // V rows past the last key: P is 0 there, and must not meet what they hold
+                const int end = (left + 15) & ~15;
+                if (left < end && end <= kCKeys && 32 * warp < end && 32 * warp + 32 > left) {
+                    if (!(ok = wait(bar_v + 8 * (g % SP::vs), (g / SP::vs) & 1))) break;
+                    if (r >= left && r < end) {
+                        uint4* row = reinterpret_cast<uint4*>(sm + SP::off_v + (g % SP::vs) * SP::tile + r * kCRowBytes);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_release(bar_p);
+            }
+            if (!ok || !(ok = wait(bar_pv, (g - 1) & 1))) break;
+            tc_fence_after();
+            if (32 * warp < live) {
+                const float f = 1.f / l;
+                const int qi = R / a.G;
+                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) +
+                                    (static_cast<long long>(t.q0 + qi) * a.H + it.h * a.G + R - qi * a.G) * 64;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[32];
+                    OASR_TMEM_LD32(tl + kCColO + 32 * q, w);
+                    tmem_wait_ld();
+                    if (r < live) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[e] = pack_bf16(__uint_as_float(w[8 * j + 2 * e]) * f, __uint_as_float(w[8 * j + 2 * e + 1]) * f);
+                            reinterpret_cast<uint4*>(to)[4 * q + j] = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    grid_dep_trigger();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kCIssuer) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCCols));
+    }
+    if (tid == 0 && *s_abort) err |= kErrTimeout;
+    if (err) atomicOr(a.status, err);
+}
+
+int g_smem_done_xtc[2][64];
+
+}  // namespace
+
+bool cross_tc_takes(const CrossArgs& a)
+{
+    // pages that tile a stage of 128 keys
+    return a.G <= kCRows && (!a.table || (a.bs >= 8 && a.bs <= 32768 && !(a.bs & (a.bs - 1))));
+}
+
+oasr_status cross_tc(CrossArgs a, int max_q, cudaStream_t stream)
+{
+    const bool paged = a.table != nullptr;
+    const int qpt = kCRows / a.G;
+    CUtensorMap tm_q, tm_k, tm_v;
+    const long long keys = paged ? static_cast<long long>(a.num_blocks) * a.bs : a.total_k;
+    const int box = paged && a.bs < kCKeys ? a.bs : kCKeys;
+    if (!encode_head_rows_bf16(&tm_q, a.q, a.total_q, a.H, a.q_stride, a.G, qpt) ||
+        !encode_head_rows_bf16(&tm_k, a.k, keys, a.Hkv, a.k_stride, 1, box) ||
+        !encode_head_rows_bf16(&tm_v, a.v, keys, a.Hkv, a.v_stride, 1, box))
+        return OASR_ERR_INVALID_ARG;
+    auto kern = paged ? cross_tc_kernel<true> : cross_tc_kernel<false>;
+    if (!ensure_smem(kern, CSmem::bytes, g_smem_done_xtc[paged])) return OASR_ERR_CUDA;
+    // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
+    const long long items = static_cast<long long>(a.N) * a.Hkv;
+    long long tiles = (static_cast<long long>(max_q) + qpt - 1) / qpt;
+    while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
+    if (items * tiles > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
+    a.tiles = static_cast<int>(tiles);
+    a.splits = 1;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(items * tiles)), dim3(kCThreads), CSmem::bytes, stream, tm_q, tm_k, tm_v,
+                      static_cast<const CrossArgs>(a));
+}
+
+}  // namespace oasr
