@@ -29,15 +29,27 @@ struct CSmem {
     static constexpr int bytes = off_misc + 24 + 1024;
 };
 
-// Which rows an item has.
+// Out of line: the kernel's roles run different code at once, and instruction fetch stalls them otherwise.
+__device__ __noinline__ bool c_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    return sleep_or_abort(bar, parity, abort);
+}
+__device__ __forceinline__ bool c_wait(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    return mbar_try_wait(bar, parity) || c_wait_slow(bar, parity, abort);
+}
+
+// The work of a CTA: row tiles tile, tile + tiles, ... of one sequence, for key heads h0 .. h0 + heads - 1.
 struct CItem {
-    int s, h, tile;
+    int s, h0, tile, heads;
     __device__ __forceinline__ CItem(const CrossArgs& a, unsigned x)
     {
+        const int groups = (a.Hkv + a.group - 1) / a.group;
         tile = x % a.tiles;
         x /= a.tiles;
-        h = x % a.Hkv;
-        s = x / a.Hkv;
+        h0 = x % groups * a.group;
+        s = x / groups;
+        heads = min(a.group, a.Hkv - h0);
     }
 };
 
@@ -96,16 +108,24 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
     const CrossSeq t(a, it.s, err);
     const int qpt = kCRows / a.G, rpt = qpt * a.G;   // queries and rows of a tile
     const int rows = t.nq * a.G, stages = (t.nk + kCKeys - 1) / kCKeys;
-    const int my_tiles = it.tile * rpt < rows ? ((rows - 1) / rpt - it.tile) / a.tiles + 1 : 0;
+    const int seq_tiles = it.tile * rpt < rows ? ((rows - 1) / rpt - it.tile) / a.tiles + 1 : 0;
+    const int my_tiles = seq_tiles * it.heads;   // head after head for each row tile
+    auto tile_of = [&](int lt, int& tile, int& h) {
+        const int k = lt / it.heads;
+        tile = it.tile + k * a.tiles;
+        h = it.h0 + lt - k * it.heads;
+    };
 
     if (stages == 0) {
         // no keys: zeros
         for (int lt = 0; lt < my_tiles; ++lt) {
-            const int r0 = (it.tile + lt * a.tiles) * rpt;
+            int tile, h;
+            tile_of(lt, tile, h);
+            const int r0 = tile * rpt;
             for (int i = tid; i < min(rpt, rows - r0) * 8; i += kCThreads) {
                 const int R = r0 + (i >> 3), qi = R / a.G;
                 reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                         (static_cast<long long>(t.q0 + qi) * a.H + it.h * a.G + R - qi * a.G) * 64)[i & 7] =
+                                         (static_cast<long long>(t.q0 + qi) * a.H + h * a.G + R - qi * a.G) * 64)[i & 7] =
                     make_uint4(0, 0, 0, 0);
             }
         }
@@ -121,40 +141,47 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
             const int r = cross_row<true>(a, t, it.s, j, err);
             return r < 0 ? a.num_blocks * a.bs : r;   // outside the pools: comes as zeros
         };
+        // K runs two stages ahead of V, whose slots are free only once their weights are through
         int g = 0, nv = 0, nq = 0;   // K stages, V stages and Q tiles requested
         bool ok = true;
-        for (int lt = 0; lt < my_tiles && ok; ++lt) {
-            if (lt > 0 && !__all_sync(0xffffffffu, sleep_or_abort(bar_q_free, (lt - 1) & 1, s_abort))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar_q, rpt * kCRowBytes);
-                tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, it.h * a.G, t.q0 + (it.tile + lt * a.tiles) * qpt);
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, c_wait(bar, parity, s_abort)); };
+        auto bring = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar, int h, int row) {
+            const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(bar, PAGED ? n * bs * kCRowBytes : SP::tile);
+            __syncwarp();
+            if (row >= 0) tma_load_3d(dst + lane * bs * kCRowBytes, tm, bar, 0, h, row);
+        };
+        const int total = my_tiles * stages;
+        int k_tile = 0, k_st = 0, v_tile = 0, v_st = 0, krow = page_of(0), vrow = krow;
+        for (int i = 0; i <= total && ok; ++i) {
+            // a new Q tile waits for the last one's scores, which may wait for any V before them: all are requested by then
+            const int due = i == total || k_st == 0 ? i : i - 2;
+            for (; nv < due && ok; ++nv) {
+                int tile, h;
+                tile_of(v_tile, tile, h);
+                const int vs = nv % SP::vs;
+                if (nv >= SP::vs && !(ok = wait(bar_v_free + 8 * vs, ((nv / SP::vs) - 1) & 1))) break;
+                bring(&tm_v, sb + SP::off_v + vs * SP::tile, bar_v + 8 * vs, h, vrow);
+                if (++v_st == stages) v_st = 0, ++v_tile;
+                vrow = page_of(v_st * kCKeys);
             }
-            ++nq;
-            int row = page_of(0);
-            for (int st = 0; st < stages; ++st) {
-                const int next = st + 1 < stages ? page_of((st + 1) * kCKeys) : -1;
-                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                const int bytes = PAGED ? n * bs * kCRowBytes : SP::tile;
-                auto bring = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar) {
-                    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-                    __syncwarp();
-                    if (row >= 0) tma_load_3d(dst + lane * bs * kCRowBytes, tm, bar, 0, it.h, row);
-                };
-                const int ks = g % SP::ks, vs = nv % SP::vs;
-                if (g >= SP::ks && !__all_sync(0xffffffffu, sleep_or_abort(bar_k_free + 8 * ks, ((g / SP::ks) - 1) & 1, s_abort))) {
-                    ok = false;
-                    break;
+            if (i == total || !ok) break;
+            int tile, h;
+            tile_of(k_tile, tile, h);
+            if (k_st == 0) {
+                if (k_tile > 0 && !(ok = wait(bar_q_free, (k_tile - 1) & 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar_q, rpt * kCRowBytes);
+                    tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, h * a.G, t.q0 + tile * qpt);
                 }
-                bring(&tm_k, sb + SP::off_k + ks * SP::tile, bar_k + 8 * ks);
-                ++g;
-                if (nv >= SP::vs && !__all_sync(0xffffffffu, sleep_or_abort(bar_v_free + 8 * vs, ((nv / SP::vs) - 1) & 1, s_abort))) {
-                    ok = false;
-                    break;
-                }
-                bring(&tm_v, sb + SP::off_v + vs * SP::tile, bar_v + 8 * vs);
-                ++nv;
-                row = next;
+                ++nq;
             }
+            const int ks = g % SP::ks;
+            if (g >= SP::ks && !(ok = wait(bar_k_free + 8 * ks, ((g / SP::ks) - 1) & 1))) break;
+            bring(&tm_k, sb + SP::off_k + ks * SP::tile, bar_k + 8 * ks, h, krow);
+            ++g;
+            if (++k_st == stages) k_st = 0, ++k_tile;
+            krow = page_of(k_st * kCKeys);
         }
         // no copy may still be landing when the CTA exits
         if (lane == 0) {
@@ -171,11 +198,11 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
             int gs = 0, g = 0;   // S issued, P . V issued
             bool ok = true;
             for (int lt = 0; lt < my_tiles && ok; ++lt) {
-                if (!sleep_or_abort(bar_q, lt & 1, s_abort)) break;
+                if (!c_wait(bar_q, lt & 1, s_abort)) break;
                 auto issue_s = [&](bool last) {
                     const int ks = gs % SP::ks;
-                    if (!sleep_or_abort(bar_k + 8 * ks, (gs / SP::ks) & 1, s_abort) ||
-                        (gs > 0 && !sleep_or_abort(bar_s_free, (gs - 1) & 1, s_abort)))
+                    if (!c_wait(bar_k + 8 * ks, (gs / SP::ks) & 1, s_abort) ||
+                        (gs > 0 && !c_wait(bar_s_free, (gs - 1) & 1, s_abort)))
                         return false;
                     tc_fence_after();
                     const uint32_t kb = sb + SP::off_k + ks * SP::tile;
@@ -192,7 +219,7 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                 for (int st = 0; st < stages && ok; ++st, ++g) {
                     if (st + 1 < stages && !(ok = issue_s(st + 2 == stages))) break;
                     const int vs = g % SP::vs;
-                    if (!sleep_or_abort(bar_p, g & 1, s_abort) || !sleep_or_abort(bar_v + 8 * vs, (g / SP::vs) & 1, s_abort)) {
+                    if (!c_wait(bar_p, g & 1, s_abort) || !c_wait(bar_v + 8 * vs, (g / SP::vs) & 1, s_abort)) {
                         ok = false;
                         break;
                     }
@@ -216,40 +243,47 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
         const int r = tid;   // the thread's row of the tile
         int g = 0;
         bool ok = true;
-        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, sleep_or_abort(bar, parity, s_abort)); };
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, c_wait(bar, parity, s_abort)); };
         for (int lt = 0; lt < my_tiles && ok; ++lt) {
-            const int R = (it.tile + lt * a.tiles) * rpt + r;
-            const int live = min(rpt, rows - (it.tile + lt * a.tiles) * rpt);   // rows of the tile
+            int tile, h;
+            tile_of(lt, tile, h);
+            const int R = tile * rpt + r, live = min(rpt, rows - tile * rpt);   // the thread's row, rows of the tile
             float m = -INFINITY, l = 0.f;
             for (int st = 0; st < stages; ++st, ++g) {
                 if (!(ok = wait(bar_s, g & 1))) break;
                 tc_fence_after();
                 const int left = t.nk - st * kCKeys;   // keys of this stage and later ones
                 if (32 * warp < live) {
-                    float s[kCKeys];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t* w = reinterpret_cast<uint32_t*>(s) + 32 * q;
-                        OASR_TMEM_LD32(tl + kCColS + 32 * q, w);
-                    }
+                    uint32_t s0[32], s1[32], s2[32], s3[32];
+                    OASR_TMEM_LD32(tl + kCColS, s0);
+                    OASR_TMEM_LD32(tl + kCColS + 32, s1);
+                    OASR_TMEM_LD32(tl + kCColS + 64, s2);
+                    OASR_TMEM_LD32(tl + kCColS + 96, s3);
                     tmem_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_release(bar_s_free);
-                    if (left < kCKeys) {
+                    float top = -INFINITY;
+                    auto largest = [&](uint32_t (&w)[32], int j0) {   // of keys j0 .. j0 + 31, those past the last aside
+                        if (left < j0 + 32) {
 #pragma unroll
-                        for (int j = 0; j < kCKeys; ++j)
-                            if (j >= left) s[j] = -INFINITY;
-                    }
-                    float x[4];
+                            for (int j = 0; j < 32; ++j)
+                                if (j0 + j >= left) w[j] = 0xff800000u;
+                        }
+                        float y[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        x[q] = s[q];
+                        for (int q = 0; q < 4; ++q) {
+                            y[q] = fmaxf(__uint_as_float(w[q]), __uint_as_float(w[q + 4]));
 #pragma unroll
-                        for (int j = 4; j < kCKeys - 4; j += 8) x[q] = fmax3(x[q], s[j + q], s[j + 4 + q]);
-                        x[q] = fmaxf(x[q], s[kCKeys - 4 + q]);
-                    }
-                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.c;
+                            for (int j = 8; j < 32; j += 8) y[q] = fmax3(y[q], __uint_as_float(w[j + q]), __uint_as_float(w[j + 4 + q]));
+                        }
+                        top = fmax3(top, fmax3(y[0], y[1], y[2]), y[3]);
+                    };
+                    largest(s0, 0);
+                    largest(s1, 32);
+                    largest(s2, 64);
+                    largest(s3, 96);
+                    top *= a.c;
                     if (st == 0) {
                         m = top;
                     } else {
@@ -260,36 +294,41 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                             const float f = grown ? ex2_approx(m - top) : 1.f;
                             if (grown) m = top;
                             l *= f;
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                uint32_t w[32];
-                                OASR_TMEM_LD32(tl + kCColO + 32 * q, w);
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {
+                                uint32_t w[8];
+                                OASR_TMEM_LD8(tl + kCColO + 8 * q, w);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
-                                OASR_TMEM_ST32(tl + kCColO + 32 * q, w);
+                                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
+                                OASR_TMEM_ST8(tl + kCColO + 8 * q, w);
                             }
                         }
                     }
                     float2 sum = make_float2(0.f, 0.f);
                     const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-m, -m);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[16];
+                    auto weights = [&](const uint32_t (&w)[32], uint32_t (&pk)[16]) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            const float2 e = __ffma2_rn(make_float2(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]), c2, m2);
+                            const float2 e = __ffma2_rn(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])), c2, m2);
                             const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
                             sum = __fadd2_rn(sum, p);
                             pk[j] = pack_bf16(p.x, p.y);
                         }
-                        if (q == 0 && g > 0) {   // the last P . V has read P
-                            if (!(ok = wait(bar_pv, (g - 1) & 1))) break;
-                            tc_fence_after();
-                        }
-                        OASR_TMEM_ST16(tl + kCColP + 16 * q, pk);
+                    };
+                    uint32_t pk[16];
+                    weights(s0, pk);
+                    if (g > 0) {   // the last P . V has read P
+                        if (!(ok = wait(bar_pv, (g - 1) & 1))) break;
+                        tc_fence_after();
                     }
-                    if (!ok) break;
+                    OASR_TMEM_ST16(tl + kCColP, pk);
+                    weights(s1, pk);
+                    OASR_TMEM_ST16(tl + kCColP + 16, pk);
+                    weights(s2, pk);
+                    OASR_TMEM_ST16(tl + kCColP + 32, pk);
+                    weights(s3, pk);
+                    OASR_TMEM_ST16(tl + kCColP + 48, pk);
                     l += sum.x + sum.y;
                     tmem_wait_st();
                     tc_fence_before();
@@ -318,7 +357,7 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                 const float f = 1.f / l;
                 const int qi = R / a.G;
                 __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) +
-                                    (static_cast<long long>(t.q0 + qi) * a.H + it.h * a.G + R - qi * a.G) * 64;
+                                    (static_cast<long long>(t.q0 + qi) * a.H + h * a.G + R - qi * a.G) * 64;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t w[32];
@@ -374,8 +413,12 @@ oasr_status cross_tc(CrossArgs a, int max_q, cudaStream_t stream)
     auto kern = paged ? cross_tc_kernel<true> : cross_tc_kernel<false>;
     if (!ensure_smem(kern, CSmem::bytes, g_smem_done_xtc[paged])) return OASR_ERR_CUDA;
     // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
-    const long long items = static_cast<long long>(a.N) * a.Hkv;
+    // and as many heads a CTA as leave every SM some CTAs
+    const int sms = sm_count();
     long long tiles = (static_cast<long long>(max_q) + qpt - 1) / qpt;
+    a.group = 1;
+    while (a.group < a.Hkv && a.N * tiles * (a.Hkv / (2 * a.group)) >= 12LL * sms) a.group *= 2;
+    const long long items = static_cast<long long>(a.N) * ((a.Hkv + a.group - 1) / a.group);
     while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
     if (items * tiles > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);
