@@ -24,7 +24,7 @@ struct CrossArgs {
     int N, H, Hkv, G, total_q, total_k;
     void* out;                                // [total_q][H][64]
     float c;                                  // scale * log2(e)
-    int splits, tiles, group;                 // CTAs that share the keys of a row tile; row tiles at a time; heads a CTA
+    int splits, tiles;                        // CTAs that share the keys of a row tile; row tiles at a time
     unsigned* status;
 };
 

@@ -21,13 +21,6 @@ constexpr int kCRows = 128, kCKeys = 128, kCRowBytes = 128;
 constexpr int kCSoftWarps = 4, kCProducer = kCSoftWarps, kCIssuer = kCSoftWarps + 1, kCThreads = 32 * (kCIssuer + 1);
 constexpr int kCColS = 0, kCColP = 128, kCColO = 192, kCCols = 256;
 
-struct CSmem {
-    static constexpr int tile = kCKeys * kCRowBytes, ks = 3, vs = 2;
-    static constexpr int off_q = 0, off_k = tile, off_v = off_k + ks * tile;
-    static constexpr int off_bar = off_v + vs * tile;   // k full[3], empty[3], v full[2], empty[2], q full, q free, s full, s free, p full, pv done, drain
-    static constexpr int off_misc = off_bar + (2 * ks + 2 * vs + 7) * 8;
-    static constexpr int bytes = off_misc + 24 + 1024;
-};
 
 // Out of line: the kernel's roles run different code at once, and instruction fetch stalls them otherwise.
 __device__ __noinline__ bool c_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort)
@@ -39,18 +32,46 @@ __device__ __forceinline__ bool c_wait(uint32_t bar, uint32_t parity, volatile i
     return mbar_try_wait(bar, parity) || c_wait_slow(bar, parity, abort);
 }
 
-// The work of a CTA: row tiles tile, tile + tiles, ... of one sequence, for key heads h0 .. h0 + heads - 1.
+// A row tile of one sequence and key head, as the producer hands it to the other roles.
 struct CItem {
-    int s, h0, tile, heads;
-    __device__ __forceinline__ CItem(const CrossArgs& a, unsigned x)
-    {
-        const int groups = (a.Hkv + a.group - 1) / a.group;
-        tile = x % a.tiles;
-        x /= a.tiles;
-        h0 = x % groups * a.group;
-        s = x / groups;
-        heads = min(a.group, a.Hkv - h0);
-    }
+    int q0, r0, live;   // the sequence's first query; the tile's first row and its rows (0: no more items)
+    int h, nk;          // key head, keys
+};
+constexpr int kCItems = 4;   // handed over and not yet finished
+
+// Ask the hardware for the next CTA of the grid that has not started, to do its work here: the answer (16 bytes)
+// goes to `to`, counted on `bar`.
+__device__ __forceinline__ void ask_next(uint32_t to, uint32_t bar)
+{
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to), "r"(bar)
+                 : "memory");
+}
+// Its index; -1 when every CTA has started (no more is asked then).
+__device__ __forceinline__ int next_cta(uint32_t from)
+{
+    uint32_t x, got;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tmov.u32 %0, 0;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}"
+        : "=&r"(x), "=&r"(got)
+        : "r"(from)
+        : "memory");
+    return got ? static_cast<int>(x) : -1;
+}
+
+struct CSmem {
+    static constexpr int tile = kCKeys * kCRowBytes, ks = 3, vs = 2;
+    static constexpr int off_q = 0, off_k = tile, off_v = off_k + ks * tile;
+    static constexpr int off_bar = off_v + vs * tile;   // k full[3], empty[3], v full[2], empty[2], q full, q free, s full, s free, p full, pv done, drain
+    static constexpr int off_item_bar = off_bar + (2 * ks + 2 * vs + 7) * 8;   // item full[4], free[4], the answer's
+    static constexpr int off_next = (off_item_bar + (2 * kCItems + 1) * 8 + 15) / 16 * 16;
+    static constexpr int off_item = off_next + 16;
+    static constexpr int off_misc = off_item + kCItems * static_cast<int>(sizeof(CItem));
+    static constexpr int bytes = off_misc + 16 + 1024;
 };
 
 template <bool PAGED>
@@ -69,6 +90,8 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
     const uint32_t bar_v = bar_k_free + 8 * SP::ks, bar_v_free = bar_v + 8 * SP::vs;
     const uint32_t bar_q = bar_v_free + 8 * SP::vs, bar_q_free = bar_q + 8, bar_s = bar_q_free + 8, bar_s_free = bar_s + 8;
     const uint32_t bar_p = bar_s_free + 8, bar_pv = bar_p + 8, bar_drain = bar_pv + 8;
+    const uint32_t bar_item = sb + SP::off_item_bar, bar_item_free = bar_item + 8 * kCItems, bar_next = bar_item_free + 8 * kCItems;
+    volatile CItem* items = reinterpret_cast<volatile CItem*>(sm + SP::off_item);
     unsigned err = 0;
     if (tid == 0) {
         for (int i = 0; i < SP::ks; ++i) {
@@ -86,6 +109,11 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
         mbar_init(bar_p, kCSoftWarps);
         mbar_init(bar_pv, 1);
         mbar_init(bar_drain, 1);
+        for (int i = 0; i < kCItems; ++i) {
+            mbar_init(bar_item + 8 * i, 1);
+            mbar_init(bar_item_free + 8 * i, kCSoftWarps + 1);
+        }
+        mbar_init(bar_next, 1);
         fence_mbar_init();
         *s_abort = 0;
     }
@@ -104,85 +132,83 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
     const uint32_t tmem = *s_tmem;
     grid_dep_wait();
 
-    const CItem it(a, blockIdx.x);
-    const CrossSeq t(a, it.s, err);
     const int qpt = kCRows / a.G, rpt = qpt * a.G;   // queries and rows of a tile
-    const int rows = t.nq * a.G, stages = (t.nk + kCKeys - 1) / kCKeys;
-    const int seq_tiles = it.tile * rpt < rows ? ((rows - 1) / rpt - it.tile) / a.tiles + 1 : 0;
-    const int my_tiles = seq_tiles * it.heads;   // head after head for each row tile
-    auto tile_of = [&](int lt, int& tile, int& h) {
-        const int k = lt / it.heads;
-        tile = it.tile + k * a.tiles;
-        h = it.h0 + lt - k * it.heads;
-    };
 
-    if (stages == 0) {
-        // no keys: zeros
-        for (int lt = 0; lt < my_tiles; ++lt) {
-            int tile, h;
-            tile_of(lt, tile, h);
-            const int r0 = tile * rpt;
-            for (int i = tid; i < min(rpt, rows - r0) * 8; i += kCThreads) {
-                const int R = r0 + (i >> 3), qi = R / a.G;
-                reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                         (static_cast<long long>(t.q0 + qi) * a.H + h * a.G + R - qi * a.G) * 64)[i & 7] =
-                    make_uint4(0, 0, 0, 0);
-            }
-        }
-    } else if (warp == kCProducer) {
+    if (warp == kCProducer) {
         // ------------------------------------------------------------ TMA producer
-        // paged: lane i brings the i-th page of a stage (its part of one, for pages over 128), so block ids are
-        // read one stage ahead by the lanes that need them
+        // It takes the grid's work items one after the other, hands each to the other roles and requests its tiles: K two
+        // stages ahead of V, whose slots are free only once their weights are through.
+        // paged: lane i brings the i-th page of a stage (its part of one, for pages over 128)
         const int bs = min(a.bs, kCKeys), boxes = PAGED ? kCKeys / bs : 1;
-        auto page_of = [&](int j0) {   // row of the lane's box; -1: past the last key
-            const int j = j0 + lane * bs;
-            if (!PAGED) return lane == 0 ? t.k0 + j0 : -1;
-            if (lane >= boxes || j >= t.nk) return -1;
-            const int r = cross_row<true>(a, t, it.s, j, err);
-            return r < 0 ? a.num_blocks * a.bs : r;   // outside the pools: comes as zeros
-        };
-        // K runs two stages ahead of V, whose slots are free only once their weights are through
-        int g = 0, nv = 0, nq = 0;   // K stages, V stages and Q tiles requested
+        int g = 0, nv = 0, nq = 0, ni = 0;   // K stages, V stages, Q tiles requested; items handed over
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, c_wait(bar, parity, s_abort)); };
+        auto hand_over = [&](const CItem& it) {
+            const int slot = ni % kCItems;
+            if (ni >= kCItems && !wait(bar_item_free + 8 * slot, ((ni / kCItems) - 1) & 1)) return false;
+            if (lane == 0) {
+                items[slot].q0 = it.q0, items[slot].r0 = it.r0, items[slot].live = it.live, items[slot].h = it.h, items[slot].nk = it.nk;
+                mbar_arrive_release(bar_item + 8 * slot);
+            }
+            ++ni;
+            return true;
+        };
         auto bring = [&](const CUtensorMap* tm, uint32_t dst, uint32_t bar, int h, int row) {
             const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
             if (lane == 0) mbar_arrive_expect_tx(bar, PAGED ? n * bs * kCRowBytes : SP::tile);
             __syncwarp();
             if (row >= 0) tma_load_3d(dst + lane * bs * kCRowBytes, tm, bar, 0, h, row);
         };
-        const int total = my_tiles * stages;
-        int k_tile = 0, k_st = 0, v_tile = 0, v_st = 0, krow = page_of(0), vrow = krow;
-        for (int i = 0; i <= total && ok; ++i) {
-            // a new Q tile waits for the last one's scores, which may wait for any V before them: all are requested by then
-            const int due = i == total || k_st == 0 ? i : i - 2;
-            for (; nv < due && ok; ++nv) {
-                int tile, h;
-                tile_of(v_tile, tile, h);
-                const int vs = nv % SP::vs;
-                if (nv >= SP::vs && !(ok = wait(bar_v_free + 8 * vs, ((nv / SP::vs) - 1) & 1))) break;
-                bring(&tm_v, sb + SP::off_v + vs * SP::tile, bar_v + 8 * vs, h, vrow);
-                if (++v_st == stages) v_st = 0, ++v_tile;
-                vrow = page_of(v_st * kCKeys);
-            }
-            if (i == total || !ok) break;
-            int tile, h;
-            tile_of(k_tile, tile, h);
-            if (k_st == 0) {
-                if (k_tile > 0 && !(ok = wait(bar_q_free, (k_tile - 1) & 1))) break;
+        if (lane == 0) ask_next(sb + SP::off_next, bar_next);
+        int asked = 1;
+        for (int x = blockIdx.x; ok;) {
+            const int tile0 = x % a.tiles, sh = x / a.tiles, h = sh % a.Hkv, s = sh / a.Hkv;
+            const CrossSeq t(a, s, err);
+            const int rows = t.nq * a.G, stages = (t.nk + kCKeys - 1) / kCKeys;
+            auto page_of = [&](int j0) {   // row of the lane's box; -1: past the last key
+                const int j = j0 + lane * bs;
+                if (!PAGED) return lane == 0 ? t.k0 + j0 : -1;
+                if (lane >= boxes || j >= t.nk) return -1;
+                const int r = cross_row<true>(a, t, s, j, err);
+                return r < 0 ? a.num_blocks * a.bs : r;   // outside the pools: comes as zeros
+            };
+            const int row0 = page_of(0);
+            for (int tile = tile0; tile * rpt < rows && ok; tile += a.tiles) {
+                if (!(ok = hand_over({t.q0, tile * rpt, min(rpt, rows - tile * rpt), h, t.nk}))) break;
+                if (!stages) continue;
+                // the Q tile is free once the last item's scores are, which wait for no V of it but the ones requested
+                if (nq > 0 && !(ok = wait(bar_q_free, (nq - 1) & 1))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar_q, rpt * kCRowBytes);
                     tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, h * a.G, t.q0 + tile * qpt);
                 }
                 ++nq;
+                int krow = row0, vrow = row0;
+                for (int i = 0, v = 0; i <= stages && ok; ++i) {
+                    for (; v < (i == stages ? i : i - 2); ++v) {
+                        const int vs = nv % SP::vs;
+                        if (nv >= SP::vs && !(ok = wait(bar_v_free + 8 * vs, ((nv / SP::vs) - 1) & 1))) break;
+                        bring(&tm_v, sb + SP::off_v + vs * SP::tile, bar_v + 8 * vs, h, vrow);
+                        ++nv;
+                        vrow = page_of((v + 1) * kCKeys);
+                    }
+                    if (i == stages || !ok) break;
+                    const int ks = g % SP::ks;
+                    if (g >= SP::ks && !(ok = wait(bar_k_free + 8 * ks, ((g / SP::ks) - 1) & 1))) break;
+                    bring(&tm_k, sb + SP::off_k + ks * SP::tile, bar_k + 8 * ks, h, krow);
+                    ++g;
+                    krow = page_of((i + 1) * kCKeys);
+                }
             }
-            const int ks = g % SP::ks;
-            if (g >= SP::ks && !(ok = wait(bar_k_free + 8 * ks, ((g / SP::ks) - 1) & 1))) break;
-            bring(&tm_k, sb + SP::off_k + ks * SP::tile, bar_k + 8 * ks, h, krow);
-            ++g;
-            if (++k_st == stages) k_st = 0, ++k_tile;
-            krow = page_of(k_st * kCKeys);
+            if (!ok || !(ok = wait(bar_next, (asked - 1) & 1))) break;
+            x = next_cta(sb + SP::off_next);
+            if (x < 0) break;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ask_next(sb + SP::off_next, bar_next);
+            ++asked;
         }
+        if (ok) hand_over({0, 0, 0, 0, 0});
         // no copy may still be landing when the CTA exits
         if (lane == 0) {
             for (int u = g - SP::ks; u < g; ++u)
@@ -190,15 +216,23 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
             for (int u = nv - SP::vs; u < nv; ++u)
                 if (u >= 0 && !mbar_wait(bar_v + 8 * (u % SP::vs), (u / SP::vs) & 1)) *s_abort = 1;
             if (nq && !mbar_wait(bar_q, (nq - 1) & 1)) *s_abort = 1;
+            if (!mbar_wait(bar_next, (asked - 1) & 1)) *s_abort = 1;
         }
     } else if (warp == kCIssuer) {
         // ------------------------------------------------------------- MMA issuer
         if (lane == 0) {
             constexpr uint32_t id_s = idesc(kCRows, kCKeys, 0), id_o = idesc(kCRows, 64, 1);
-            int gs = 0, g = 0;   // S issued, P . V issued
+            int gs = 0, g = 0, nq = 0;   // S issued, P . V issued, Q tiles
             bool ok = true;
-            for (int lt = 0; lt < my_tiles && ok; ++lt) {
-                if (!c_wait(bar_q, lt & 1, s_abort)) break;
+            for (int ni = 0; ok; ++ni) {
+                const int slot = ni % kCItems;
+                if (!c_wait(bar_item + 8 * slot, (ni / kCItems) & 1, s_abort)) break;
+                const int live = items[slot].live, nk = items[slot].nk, stages = (nk + kCKeys - 1) / kCKeys;
+                mbar_arrive_release(bar_item_free + 8 * slot);
+                if (!live) break;
+                if (!stages) continue;
+                if (!c_wait(bar_q, nq & 1, s_abort)) break;
+                ++nq;
                 auto issue_s = [&](bool last) {
                     const int ks = gs % SP::ks;
                     if (!c_wait(bar_k + 8 * ks, (gs / SP::ks) & 1, s_abort) ||
@@ -225,7 +259,7 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                     }
                     tc_fence_after();
                     const uint32_t vb = sb + SP::off_v + vs * SP::tile;
-                    const int steps = min((t.nk - st * kCKeys + 15) >> 4, kCKeys / 16);
+                    const int steps = min((nk - st * kCKeys + 15) >> 4, kCKeys / 16);
 #pragma unroll
                     for (int k = 0; k < kCKeys / 16; ++k)
                         if (k < steps) umma_ts(tmem + kCColO, tmem + kCColP + 8 * k, sdesc(vb + 2048 * k), id_o, st > 0 || k > 0);
@@ -244,15 +278,27 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
         int g = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, c_wait(bar, parity, s_abort)); };
-        for (int lt = 0; lt < my_tiles && ok; ++lt) {
-            int tile, h;
-            tile_of(lt, tile, h);
-            const int R = tile * rpt + r, live = min(rpt, rows - tile * rpt);   // the thread's row, rows of the tile
+        for (int ni = 0; ok; ++ni) {
+            const int slot = ni % kCItems;
+            if (!wait(bar_item + 8 * slot, (ni / kCItems) & 1)) break;
+            const int q0 = items[slot].q0, R = items[slot].r0 + r, live = items[slot].live, h = items[slot].h, nk = items[slot].nk;
+            const int stages = (nk + kCKeys - 1) / kCKeys;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_release(bar_item_free + 8 * slot);
+            if (!live) break;
+            const int qi = R / a.G;
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) +
+                                (static_cast<long long>(q0 + qi) * a.H + h * a.G + R - qi * a.G) * 64;
+            if (!stages) {   // no keys: zeros
+                if (r < live)
+                    for (int j = 0; j < 8; ++j) reinterpret_cast<uint4*>(to)[j] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
             float m = -INFINITY, l = 0.f;
             for (int st = 0; st < stages; ++st, ++g) {
                 if (!(ok = wait(bar_s, g & 1))) break;
                 tc_fence_after();
-                const int left = t.nk - st * kCKeys;   // keys of this stage and later ones
+                const int left = nk - st * kCKeys;   // keys of this stage and later ones
                 if (32 * warp < live) {
                     uint32_t s0[32], s1[32], s2[32], s3[32];
                     OASR_TMEM_LD32(tl + kCColS, s0);
@@ -355,9 +401,6 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
             tc_fence_after();
             if (32 * warp < live) {
                 const float f = 1.f / l;
-                const int qi = R / a.G;
-                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) +
-                                    (static_cast<long long>(t.q0 + qi) * a.H + h * a.G + R - qi * a.G) * 64;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t w[32];
@@ -413,12 +456,8 @@ oasr_status cross_tc(CrossArgs a, int max_q, cudaStream_t stream)
     auto kern = paged ? cross_tc_kernel<true> : cross_tc_kernel<false>;
     if (!ensure_smem(kern, CSmem::bytes, g_smem_done_xtc[paged])) return OASR_ERR_CUDA;
     // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
-    // and as many heads a CTA as leave every SM some CTAs
-    const int sms = sm_count();
     long long tiles = (static_cast<long long>(max_q) + qpt - 1) / qpt;
-    a.group = 1;
-    while (a.group < a.Hkv && a.N * tiles * (a.Hkv / (2 * a.group)) >= 12LL * sms) a.group *= 2;
-    const long long items = static_cast<long long>(a.N) * ((a.Hkv + a.group - 1) / a.group);
+    const long long items = static_cast<long long>(a.N) * a.Hkv;
     while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
     if (items * tiles > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);

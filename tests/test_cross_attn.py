@@ -177,6 +177,21 @@ def test_cross(nq, nk, H, Hkv, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("top_q,top_k,H", [(200, 300, 4), (40, 130, 8), (300, 20, 2)])
+def test_many_sequences(top_q, top_k, H):
+    """More row tiles than the GPU holds at a time, of any length, empty ones among them: CTAs go from one to the next."""
+    g = torch.Generator().manual_seed(top_q)
+    nq, nk = (torch.randint(0, top + 1, (400,), generator=g).tolist() for top in (top_q, top_k))
+    c = Case(nq, nk, H, H // 2, "bf16", top_k)
+    x = c.cuda()
+    out = c.packed(x)
+    c.check(out)
+    assert all(torch.equal(c.packed(x), out) for _ in range(5))
+    assert torch.equal(c.paged(x), out)
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bs", [1, 3, 8, 24, 32, 64, 128, 256, 512])
 def test_page_sizes(bs, dtype):
