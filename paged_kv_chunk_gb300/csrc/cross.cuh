@@ -32,6 +32,7 @@ struct CrossArgs {
 // outside their tensors are clamped and flagged.
 struct CrossSeq {
     int q0, nq, k0, nk;
+    CrossSeq() = default;
     __device__ __forceinline__ CrossSeq(const CrossArgs& a, int s, unsigned& err)
     {
         int q1 = __ldg(a.cu_q + s + 1);
@@ -76,6 +77,6 @@ __device__ __forceinline__ int cross_row(const CrossArgs& a, const CrossSeq& t, 
 
 // The tensor-core form (cross_tc.cu), and whether it takes the call's heads and pages.
 bool cross_tc_takes(const CrossArgs& a);
-oasr_status cross_tc(CrossArgs a, int max_q, cudaStream_t stream);
+oasr_status cross_tc(const CrossArgs& a, int max_q, cudaStream_t stream);
 
 }  // namespace oasr

@@ -39,6 +39,10 @@ struct CItem {
 };
 constexpr int kCItems = 4;   // handed over and not yet finished
 
+// The grid counts row tiles of all sequences, one after the other, with their key heads: the producer finds a tile's
+// sequence from the tiles before every kCIndex-th part of them.
+constexpr int kCIndex = 1024;
+
 // Ask the hardware for the next CTA of the grid that has not started, to do its work here: the answer (16 bytes)
 // goes to `to`, counted on `bar`.
 __device__ __forceinline__ void ask_next(uint32_t to, uint32_t bar)
@@ -71,7 +75,8 @@ struct CSmem {
     static constexpr int off_next = (off_item_bar + (2 * kCItems + 1) * 8 + 15) / 16 * 16;
     static constexpr int off_item = off_next + 16;
     static constexpr int off_misc = off_item + kCItems * static_cast<int>(sizeof(CItem));
-    static constexpr int bytes = off_misc + 16 + 1024;
+    static constexpr int off_index = off_misc + 16;
+    static constexpr int bytes = off_index + kCIndex * 4 + 1024;
 };
 
 template <bool PAGED>
@@ -161,30 +166,75 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
         };
         if (lane == 0) ask_next(sb + SP::off_next, bar_next);
         int asked = 1;
-        for (int x = blockIdx.x; ok;) {
-            const int tile0 = x % a.tiles, sh = x / a.tiles, h = sh % a.Hkv, s = sh / a.Hkv;
-            const CrossSeq t(a, s, err);
-            const int rows = t.nq * a.G, stages = (t.nk + kCKeys - 1) / kCKeys;
-            auto page_of = [&](int j0) {   // row of the lane's box; -1: past the last key
-                const int j = j0 + lane * bs;
-                if (!PAGED) return lane == 0 ? t.k0 + j0 : -1;
-                if (lane >= boxes || j >= t.nk) return -1;
-                const int r = cross_row<true>(a, t, s, j, err);
-                return r < 0 ? a.num_blocks * a.bs : r;   // outside the pools: comes as zeros
-            };
-            const int row0 = page_of(0);
-            for (int tile = tile0; tile * rpt < rows && ok; tile += a.tiles) {
+        // tiles before sequence i * per
+        int* index = reinterpret_cast<int*>(sm + SP::off_index);
+        const int per = (a.N + kCIndex - 1) / kCIndex;
+        auto tiles_of = [&](int s) {
+            int q0 = __ldg(a.cu_q + s), q1 = __ldg(a.cu_q + s + 1);
+            CrossSeq::clamp(q0, q1, a.total_q, err);
+            return ((q1 - q0) * a.G + rpt - 1) / rpt;
+        };
+        int all = 0;
+        for (int i0 = 0; i0 * per < a.N; i0 += 32) {
+            int n = 0;
+            for (int s = (i0 + lane) * per; s < min((i0 + lane + 1) * per, a.N); ++s) n += tiles_of(s);
+            int sum = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            index[i0 + lane] = all + sum - n;
+            all += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        __syncwarp();
+        struct Work {
+            int s, h, tile;   // s < 0: past the last tile
+            CrossSeq t;
+        };
+        auto look_up = [&](int x) {
+            Work w = {-1, x % a.Hkv, x / a.Hkv, {}};
+            if (w.tile >= all) return w;
+            const int parts = (a.N + per - 1) / per;
+            // the last part that begins at or before the tile
+            int lo = 0;
+            for (int step = kCIndex / 32; step; step >>= 5) {
+                const int i = lo + step * lane;
+                lo += step * (__popc(__ballot_sync(0xffffffffu, i < parts && index[min(i, parts - 1)] <= w.tile)) - 1);
+            }
+            w.tile -= index[lo];
+            w.s = lo * per;
+            if (per > 1)
+                for (int n; w.tile >= (n = tiles_of(w.s)); ++w.s) w.tile -= n;
+            w.t = CrossSeq(a, w.s, err);
+            return w;
+        };
+        int x = blockIdx.x;
+        Work w = look_up(x);
+        while (ok) {
+            const CrossSeq t = w.t;
+            const int h = w.h, s = w.s, tile = w.tile;
+            if (s >= 0) {
+                const int rows = t.nq * a.G, stages = (t.nk + kCKeys - 1) / kCKeys;
+                auto page_of = [&](int j0) {   // row of the lane's box; -1: past the last key
+                    const int j = j0 + lane * bs;
+                    if (!PAGED) return lane == 0 ? t.k0 + j0 : -1;
+                    if (lane >= boxes || j >= t.nk) return -1;
+                    const int r = cross_row<true>(a, t, s, j, err);
+                    return r < 0 ? a.num_blocks * a.bs : r;   // outside the pools: comes as zeros
+                };
+                int krow = page_of(0), vrow = krow;
                 if (!(ok = hand_over({t.q0, tile * rpt, min(rpt, rows - tile * rpt), h, t.nk}))) break;
-                if (!stages) continue;
-                // the Q tile is free once the last item's scores are, which wait for no V of it but the ones requested
-                if (nq > 0 && !(ok = wait(bar_q_free, (nq - 1) & 1))) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar_q, rpt * kCRowBytes);
-                    tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, h * a.G, t.q0 + tile * qpt);
+                if (stages) {
+                    // the Q tile is free once the last item's scores are, which wait for no V but the ones requested
+                    if (nq > 0 && !(ok = wait(bar_q_free, (nq - 1) & 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar_q, rpt * kCRowBytes);
+                        tma_load_3d(sb + SP::off_q, &tm_q, bar_q, 0, h * a.G, t.q0 + tile * qpt);
+                    }
+                    ++nq;
                 }
-                ++nq;
-                int krow = row0, vrow = row0;
-                for (int i = 0, v = 0; i <= stages && ok; ++i) {
+                for (int i = 0, v = 0; stages && i <= stages && ok; ++i) {
                     for (; v < (i == stages ? i : i - 2); ++v) {
                         const int vs = nv % SP::vs;
                         if (nv >= SP::vs && !(ok = wait(bar_v_free + 8 * vs, ((nv / SP::vs) - 1) & 1))) break;
@@ -200,13 +250,21 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                     krow = page_of((i + 1) * kCKeys);
                 }
             }
-            if (!ok || !(ok = wait(bar_next, (asked - 1) & 1))) break;
+            if (!ok) break;
+            // sequences longer than announced have tiles past the grid
+            if (x + static_cast<long long>(gridDim.x) < static_cast<long long>(all) * a.Hkv) {
+                x += gridDim.x;
+                w = look_up(x);
+                continue;
+            }
+            if (!(ok = wait(bar_next, (asked - 1) & 1))) break;
             x = next_cta(sb + SP::off_next);
             if (x < 0) break;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ask_next(sb + SP::off_next, bar_next);
             ++asked;
+            w = look_up(x);
         }
         if (ok) hand_over({0, 0, 0, 0, 0});
         // no copy may still be landing when the CTA exits
@@ -305,31 +363,33 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                     OASR_TMEM_LD32(tl + kCColS + 32, s1);
                     OASR_TMEM_LD32(tl + kCColS + 64, s2);
                     OASR_TMEM_LD32(tl + kCColS + 96, s3);
-                    tmem_wait_ld();
+                    tmem_wait_ld();   // of the whole warp
                     tc_fence_before();
-                    __syncwarp();
                     if (lane == 0) mbar_arrive_release(bar_s_free);
-                    float top = -INFINITY;
-                    auto largest = [&](uint32_t (&w)[32], int j0) {   // of keys j0 .. j0 + 31, those past the last aside
-                        if (left < j0 + 32) {
+                    if (left < kCKeys) {   // keys past the last one
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j0 + j >= left) w[j] = 0xff800000u;
+                        for (int j = 0; j < 32; ++j) {
+                            if (j >= left) s0[j] = 0xff800000u;
+                            if (32 + j >= left) s1[j] = 0xff800000u;
+                            if (64 + j >= left) s2[j] = 0xff800000u;
+                            if (96 + j >= left) s3[j] = 0xff800000u;
                         }
-                        float y[4];
+                    }
+                    // eight maxima side by side
+                    float y[8];
+                    auto f32 = [](uint32_t w) { return __uint_as_float(w); };
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            y[q] = fmaxf(__uint_as_float(w[q]), __uint_as_float(w[q + 4]));
-#pragma unroll
-                            for (int j = 8; j < 32; j += 8) y[q] = fmax3(y[q], __uint_as_float(w[j + q]), __uint_as_float(w[j + 4 + q]));
-                        }
-                        top = fmax3(top, fmax3(y[0], y[1], y[2]), y[3]);
-                    };
-                    largest(s0, 0);
-                    largest(s1, 32);
-                    largest(s2, 64);
-                    largest(s3, 96);
-                    top *= a.c;
+                    for (int q = 0; q < 8; ++q) {
+                        y[q] = fmax3(f32(s0[q]), f32(s0[q + 8]), f32(s0[q + 16]));
+                        y[q] = fmax3(y[q], f32(s0[q + 24]), f32(s1[q]));
+                        y[q] = fmax3(y[q], f32(s1[q + 8]), f32(s1[q + 16]));
+                        y[q] = fmax3(y[q], f32(s1[q + 24]), f32(s2[q]));
+                        y[q] = fmax3(y[q], f32(s2[q + 8]), f32(s2[q + 16]));
+                        y[q] = fmax3(y[q], f32(s2[q + 24]), f32(s3[q]));
+                        y[q] = fmax3(y[q], f32(s3[q + 8]), f32(s3[q + 16]));
+                        y[q] = fmaxf(y[q], f32(s3[q + 24]));
+                    }
+                    const float top = fmax3(fmax3(y[0], y[1], y[2]), fmax3(y[3], y[4], y[5]), fmaxf(y[6], y[7])) * a.c;
                     if (st == 0) {
                         m = top;
                     } else {
@@ -351,14 +411,14 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                             }
                         }
                     }
-                    float2 sum = make_float2(0.f, 0.f);
+                    float2 sum[4] = {};
                     const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-m, -m);
                     auto weights = [&](const uint32_t (&w)[32], uint32_t (&pk)[16]) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float2 e = __ffma2_rn(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])), c2, m2);
                             const float2 p = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-                            sum = __fadd2_rn(sum, p);
+                            sum[j & 3] = __fadd2_rn(sum[j & 3], p);
                             pk[j] = pack_bf16(p.x, p.y);
                         }
                     };
@@ -375,7 +435,8 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                     OASR_TMEM_ST16(tl + kCColP + 32, pk);
                     weights(s3, pk);
                     OASR_TMEM_ST16(tl + kCColP + 48, pk);
-                    l += sum.x + sum.y;
+                    sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                    l += sum[0].x + sum[0].y;
                     tmem_wait_st();
                     tc_fence_before();
                 } else {
@@ -393,8 +454,8 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                         for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
+                    __syncwarp();
                 }
-                __syncwarp();
                 if (lane == 0) mbar_arrive_release(bar_p);
             }
             if (!ok || !(ok = wait(bar_pv, (g - 1) & 1))) break;
@@ -442,7 +503,7 @@ bool cross_tc_takes(const CrossArgs& a)
     return a.G <= kCRows && (!a.table || (a.bs >= 8 && a.bs <= 32768 && !(a.bs & (a.bs - 1))));
 }
 
-oasr_status cross_tc(CrossArgs a, int max_q, cudaStream_t stream)
+oasr_status cross_tc(const CrossArgs& a, int max_q, cudaStream_t stream)
 {
     const bool paged = a.table != nullptr;
     const int qpt = kCRows / a.G;
@@ -455,15 +516,12 @@ oasr_status cross_tc(CrossArgs a, int max_q, cudaStream_t stream)
         return OASR_ERR_INVALID_ARG;
     auto kern = paged ? cross_tc_kernel<true> : cross_tc_kernel<false>;
     if (!ensure_smem(kern, CSmem::bytes, g_smem_done_xtc[paged])) return OASR_ERR_CUDA;
-    // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
-    long long tiles = (static_cast<long long>(max_q) + qpt - 1) / qpt;
-    const long long items = static_cast<long long>(a.N) * a.Hkv;
-    while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
-    if (items * tiles > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
-    a.tiles = static_cast<int>(tiles);
-    a.splits = 1;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(items * tiles)), dim3(kCThreads), CSmem::bytes, stream, tm_q, tm_k, tm_v,
-                      static_cast<const CrossArgs>(a));
+    // a CTA for each tile there can be: no more than the longest sequence has for all, or than all queries and a
+    // partly filled tile of each sequence make (CTAs without one would only crowd those that have)
+    const long long most = static_cast<long long>(a.total_q) / qpt + a.N, each = (static_cast<long long>(max_q) + qpt - 1) / qpt * a.N;
+    const long long tiles = most < each ? most : each;
+    if (most * a.Hkv > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles * a.Hkv)), dim3(kCThreads), CSmem::bytes, stream, tm_q, tm_k, tm_v, a);
 }
 
 }  // namespace oasr

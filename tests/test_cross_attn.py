@@ -192,6 +192,19 @@ def test_many_sequences(top_q, top_k, H):
 
 
 @pytest.mark.gpu
+def test_thousands_of_sequences():
+    """More sequences than the row tiles' index has entries, the rows all over them."""
+    g = torch.Generator().manual_seed(7)
+    nq, nk = torch.randint(0, 4, (5003,), generator=g), torch.randint(0, 9, (5003,), generator=g)
+    nq[[0, 2100, 5002]], nk[2100] = torch.tensor([300, 200, 17]), 400
+    c = Case(nq.tolist(), nk.tolist(), 2, 1, "bf16", 1, bs=8)
+    x = c.cuda()
+    out = c.packed(x)
+    c.check(out)
+    assert torch.equal(c.paged(x), out) and capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bs", [1, 3, 8, 24, 32, 64, 128, 256, 512])
 def test_page_sizes(bs, dtype):
