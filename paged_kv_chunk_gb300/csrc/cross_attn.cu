@@ -5,11 +5,11 @@
 // Few rows: every key row is read once for at most 16 rows, so the bytes of k and v are the cost and what counts is
 // how many of them are on the way.  A warp takes 16 keys at a time straight into the registers that the
 // matrix instructions read, without shared memory, and requests the next 16 before it works on these.
-// The contraction of q . k may run over the 64 dimensions in any order, and the columns of P . V stand for
-// any dimensions, so the order is taken in which a lane's share of a row is contiguous: lane 4 g + c
-// holds dimensions 16 c .. 16 c + 15 of keys g and 8 + g (K) and 8 g .. 8 g + 7 of keys 2 c, 2 c + 1, 8 + 2 c and
-// 9 + 2 c (V, whose pairs of keys are interleaved by byte permutes).  The keys of a sequence are shared by the
-// warps of a CTA and, where that leaves SMs idle, by a cluster of CTAs.
+// The contraction of q . k may run over the 64 dimensions in any order, and the rows of O^T stand for any
+// dimensions, so the order is taken in which a lane loads 16 bytes at a time and its neighbours the next ones:
+// lane 4 g + c holds dimensions 8 c .. 8 c + 7 and 32 + 8 c .. 32 + 8 c + 7 of keys g and 8 + g (K) and 8 g .. 8 g + 7
+// of keys 2 c, 2 c + 1, 8 + 2 c and 9 + 2 c (V, whose pairs of keys are interleaved by byte permutes).  The keys of a
+// sequence are shared by the warps of a CTA and, where that leaves SMs idle, by a cluster of CTAs.
 #include "cluster.cuh"
 #include "cross.cuh"
 #include "e4m3.cuh"
@@ -102,12 +102,19 @@ __device__ __forceinline__ void join_shares(Shares& s, int shares, int splits, i
     }
 }
 
+// An 8 x 8 matrix of 16-bit elements, a row's two neighbours in each lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 // The work of a CTA: one sequence, key head, share of the keys and every tiles-th row tile from `tile`.
 struct CrossItem {
     int s, h, tile, split;
-    __device__ __forceinline__ explicit CrossItem(const CrossArgs& a)
+    __device__ __forceinline__ CrossItem(const CrossArgs& a, unsigned x)
     {
-        unsigned x = blockIdx.x;
         split = x % a.splits;
         x /= a.splits;
         h = x % a.Hkv;
@@ -117,14 +124,17 @@ struct CrossItem {
     }
 };
 
-template <bool PAGED>
-__global__ void __launch_bounds__(kXThreads, 4) cross_few_kernel(const CrossArgs a)
+// NT: eights of rows.  Scores are computed with the keys as the matrix instruction's rows (S^T = K . Q^T, O^T = V^T . P^T),
+// so that eight rows fill its columns; P^T comes from S^T by two 8 x 8 transpositions.
+template <bool PAGED, int NT>
+__global__ void __launch_bounds__(kXThreads, 3) cross_few_kernel(const CrossArgs a)
 {
     using Elem = __nv_bfloat16;
+    constexpr int RT = 8 * NT;
     __shared__ Shares s_sh;
     grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const CrossItem it(a);
+    const CrossItem it(a, blockIdx.x);
     unsigned err = 0;
     const CrossSeq t(a, it.s, err);
     const int rows = t.nq * a.G;
@@ -133,119 +143,132 @@ __global__ void __launch_bounds__(kXThreads, 4) cross_few_kernel(const CrossArgs
     const int first = it.split * share, last = min(first + share, chunks);
     const Elem* kb = static_cast<const Elem*>(a.k) + it.h * kHd;
     const Elem* vb = static_cast<const Elem*>(a.v) + it.h * kHd;
-
-    for (int tile = it.tile; tile * kXRows < rows; tile += a.tiles) {
-        const int r0 = tile * kXRows, n = min(rows - r0, kXRows);
-        // a lane's part of query rows g and g + 8: dimensions 16 c .. 16 c + 15
-        uint32_t qa[8], qb[8];
-        auto load_q = [&](int r, uint32_t (&w)[8]) {
+    // K of keys g, 8 + g (two words of 16 bytes each), V of keys 2c, 2c + 1, 8 + 2c, 9 + 2c
+    using Chunk = uint4[8];
+    auto row_of = [&](int chunk) {   // lanes 0 .. 15: the row of the chunk's key
+        const int j = chunk * kXKeys + (lane & 15);
+        return chunk < last && j < t.nk ? cross_row<PAGED>(a, t, it.s, j, err) : -1;
+    };
+    auto request = [&](int row, Chunk& kv) {
+        const bool whole = __all_sync(0xffffffffu, row >= 0);
+        auto at = [&](const Elem* base, long long stride, int j, int d) {
+            return reinterpret_cast<const uint4*>(base + __shfl_sync(0xffffffffu, row, j) * stride + d);
+        };
+        const uint4 *k0 = at(kb, a.k_stride, g, 8 * c), *k1 = at(kb, a.k_stride, 8 + g, 8 * c);
+        const uint4 *v0 = at(vb, a.v_stride, 2 * c, 8 * g), *v1 = at(vb, a.v_stride, 2 * c + 1, 8 * g);
+        const uint4 *v2 = at(vb, a.v_stride, 8 + 2 * c, 8 * g), *v3 = at(vb, a.v_stride, 9 + 2 * c, 8 * g);
+        if (whole) {
+            kv[0] = __ldg(k0), kv[1] = __ldg(k0 + 4), kv[2] = __ldg(k1), kv[3] = __ldg(k1 + 4);
+            kv[4] = __ldg(v0), kv[5] = __ldg(v1), kv[6] = __ldg(v2), kv[7] = __ldg(v3);
+        } else {   // keys past the end, or in no block: zeros
+            const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
+            auto get = [&](const uint4* p, int j) { return there >> j & 1 ? __ldg(p) : make_uint4(0, 0, 0, 0); };
+            kv[0] = get(k0, g), kv[1] = get(k0 + 4, g), kv[2] = get(k1, 8 + g), kv[3] = get(k1 + 4, 8 + g);
+            kv[4] = get(v0, 2 * c), kv[5] = get(v1, 2 * c + 1), kv[6] = get(v2, 8 + 2 * c), kv[7] = get(v3, 9 + 2 * c);
+        }
+    };
+    for (int tile = it.tile; tile * RT < rows; tile += a.tiles) {
+        const int r0 = tile * RT, n = min(rows - r0, RT);
+        // a lane's part of query row g of each eight: the dimensions that it has of a key
+        uint32_t q[NT][8];
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
             uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            if (r < n) {
-                const int R = r0 + r, i = R / a.G, hd = it.h * a.G + R - i * a.G;
+            if (8 * e + g < n) {
+                const int R = r0 + 8 * e + g, i = R / a.G, hd = it.h * a.G + R - i * a.G;
                 const uint4* p = reinterpret_cast<const uint4*>(static_cast<const Elem*>(a.q) + (t.q0 + i) * a.q_stride +
-                                                                hd * kHd + 16 * c);
+                                                                hd * kHd + 8 * c);
                 x = __ldg(p);
-                y = __ldg(p + 1);
+                y = __ldg(p + 4);
             }
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-        };
-        load_q(g, qa);
-        load_q(g + 8, qb);
-
-        float o[8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            q[e][0] = x.x, q[e][1] = x.y, q[e][2] = x.z, q[e][3] = x.w, q[e][4] = y.x, q[e][5] = y.y, q[e][6] = y.z, q[e][7] = y.w;
+        }
+        // a lane has rows 2 c and 2 c + 1 of each eight: their maxima, its keys' sums, and dimensions 8 g + 2 d (+ 1) of O
+        float o[NT][4][4], m[NT][2], l[NT][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-        uint4 kv[8];   // K of keys g, 8 + g (two words of 16 bytes each), V of keys 2c, 2c + 1, 8 + 2c, 9 + 2c
-        auto row_of = [&](int chunk) {   // lanes 0 .. 15: the row of the chunk's key
-            const int j = chunk * kXKeys + (lane & 15);
-            return chunk < last && j < t.nk ? cross_row<PAGED>(a, t, it.s, j, err) : -1;
-        };
-        auto request = [&](int row) {
-            auto get = [&](const Elem* base, long long stride, int j, int at) {
-                const int r = __shfl_sync(0xffffffffu, row, j);
-                return r < 0 ? static_cast<const uint4*>(nullptr) : reinterpret_cast<const uint4*>(base + r * stride + at);
-            };
-            const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < NT; ++e) {
+            m[e][0] = m[e][1] = -INFINITY, l[e][0] = l[e][1] = 0.f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint4* p = get(kb, a.k_stride, 8 * u + g, 16 * c);
-                kv[2 * u] = p ? __ldg(p) : zero;
-                kv[2 * u + 1] = p ? __ldg(p + 1) : zero;
-            }
+            for (int d = 0; d < 4; ++d) o[e][d][0] = o[e][d][1] = o[e][d][2] = o[e][d][3] = 0.f;
+        }
+        auto work = [&](int chunk, const Chunk& kv) {
+            uint32_t p[NT][2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint4* p = get(vb, a.v_stride, 8 * (u >> 1) + 2 * c + (u & 1), 8 * g);
-                kv[4 + u] = p ? __ldg(p) : zero;
-            }
-        };
-        request(row_of(first + warp));
-        int next_row = row_of(first + warp + kXWarps);
-        for (int chunk = first + warp; chunk < last; chunk += kXWarps) {
-            uint4 now[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) now[i] = kv[i];
-            request(next_row);
-            next_row = row_of(chunk + 2 * kXWarps);
-            float s[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
-                const uint32_t w[8] = {now[2 * u].x,     now[2 * u].y,     now[2 * u].z,     now[2 * u].w,
-                                       now[2 * u + 1].x, now[2 * u + 1].y, now[2 * u + 1].z, now[2 * u + 1].w};
+            for (int e = 0; e < NT; ++e) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};   // keys g (0, 1) and 8 + g (2, 3) of rows 2c, 2c + 1
+                const uint32_t kg[8] = {kv[0].x, kv[0].y, kv[0].z, kv[0].w, kv[1].x, kv[1].y, kv[1].z, kv[1].w};
+                const uint32_t k8[8] = {kv[2].x, kv[2].y, kv[2].z, kv[2].w, kv[3].x, kv[3].y, kv[3].z, kv[3].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t qf[4] = {qa[2 * k], qb[2 * k], qa[2 * k + 1], qb[2 * k + 1]};
-                    mma_bf16_16816(s[u], qf, w[2 * k], w[2 * k + 1]);
+                    const uint32_t kf[4] = {kg[2 * k], k8[2 * k], kg[2 * k + 1], k8[2 * k + 1]};
+                    mma_bf16_16816(s, kf, q[e][2 * k], q[e][2 * k + 1]);
                 }
-            }
-            // keys past the sequence's end do not count
-            const int left = t.nk - chunk * kXKeys - 2 * c;
-            if (left < 16) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (8 * u + (i & 1) >= left) s[u][i] = -INFINITY;
-            }
-            uint32_t p[4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {   // rows g, g + 8
-                float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)) * a.c;
-                if (x > m[r]) {
-                    const float f = ex2_approx(m[r] - x);
-                    m[r] = x;
-                    l[r] *= f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i][2 * r] *= f, o[i][2 * r + 1] *= f;
+                // keys past the sequence's end do not count
+                const int left = t.nk - chunk * kXKeys;
+                if (left < kXKeys) {
+                    if (g >= left) s[0] = s[1] = -INFINITY;
+                    if (8 + g >= left) s[2] = s[3] = -INFINITY;
                 }
-                float e[4];
+                float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = ex2_approx(fmaf(s[i >> 1][2 * r + (i & 1)], a.c, -m[r]));
-                l[r] += (e[0] + e[1]) + (e[2] + e[3]);
-                p[r] = pack_bf16(e[0], e[1]);
-                p[2 + r] = pack_bf16(e[2], e[3]);
-            }
-            const uint32_t v[4][4] = {{now[4].x, now[4].y, now[4].z, now[4].w}, {now[5].x, now[5].y, now[5].z, now[5].w},
-                                      {now[6].x, now[6].y, now[6].z, now[6].w}, {now[7].x, now[7].y, now[7].z, now[7].w}};
+                for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
-            for (int d = 0; d < 8; ++d) {   // dimension 8 g + d
-                const uint32_t sel = d & 1 ? 0x7632 : 0x5410;
-                mma_bf16_16816(o[d], p, __byte_perm(v[0][d >> 1], v[1][d >> 1], sel),
-                               __byte_perm(v[2][d >> 1], v[3][d >> 1], sel));
+                    for (int r = 0; r < 2; ++r) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], x));
+                top[0] *= a.c, top[1] *= a.c;
+                // the reference moves only when a row's maximum has grown by more than 2^8: weights stay below 2^8
+                const bool grown0 = top[0] > m[e][0] + 8.f, grown1 = top[1] > m[e][1] + 8.f;
+                if (__any_sync(0xffffffffu, grown0 || grown1)) {
+                    const float f0 = grown0 ? ex2_approx(m[e][0] - top[0]) : 1.f, f1 = grown1 ? ex2_approx(m[e][1] - top[1]) : 1.f;
+                    if (grown0) m[e][0] = top[0];
+                    if (grown1) m[e][1] = top[1];
+                    l[e][0] *= f0, l[e][1] *= f1;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) o[e][d][0] *= f0, o[e][d][1] *= f1, o[e][d][2] *= f0, o[e][d][3] *= f1;
+                }
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = ex2_approx(fmaf(s[i], a.c, -m[e][i & 1]));
+                l[e][0] += w[0] + w[2], l[e][1] += w[1] + w[3];
+                p[e][0] = transposed(pack_bf16(w[0], w[1]));
+                p[e][1] = transposed(pack_bf16(w[2], w[3]));
             }
+            const uint32_t v[4][4] = {{kv[4].x, kv[4].y, kv[4].z, kv[4].w}, {kv[5].x, kv[5].y, kv[5].z, kv[5].w},
+                                      {kv[6].x, kv[6].y, kv[6].z, kv[6].w}, {kv[7].x, kv[7].y, kv[7].z, kv[7].w}};
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const uint32_t vf[4] = {__byte_perm(v[0][d], v[1][d], 0x5410), __byte_perm(v[0][d], v[1][d], 0x7632),
+                                        __byte_perm(v[2][d], v[3][d], 0x5410), __byte_perm(v[2][d], v[3][d], 0x7632)};
+#pragma unroll
+                for (int e = 0; e < NT; ++e) mma_bf16_16816(o[e][d], vf, p[e][0], p[e][1]);
+            }
+        };
+        // two chunks' registers in turn: one is requested while the other is worked on
+        int chunk = first + warp;
+        Chunk even, odd;
+        request(row_of(chunk), even);
+        int row = row_of(chunk + kXWarps);
+        while (chunk < last) {
+            request(row, odd);
+            row = row_of(chunk + 2 * kXWarps);
+            work(chunk, even);
+            if ((chunk += kXWarps) >= last) break;
+            request(row, even);
+            row = row_of(chunk + 2 * kXWarps);
+            work(chunk, odd);
+            chunk += kXWarps;
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if (c == 0) s_sh.m[warp][g + 8 * r] = m[r], s_sh.l[warp][g + 8 * r] = l[r];
-            float* to = &s_sh.o[warp][g + 8 * r][16 * c];   // column 2c + e of product d: dimension 16 c + 8 e + d
+        for (int e = 0; e < NT; ++e)
 #pragma unroll
-            for (int d = 0; d < 8; ++d) to[d] = o[d][2 * r], to[8 + d] = o[d][2 * r + 1];
-        }
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[e][r] += __shfl_xor_sync(0xffffffffu, l[e][r], x);
+                const int R = 8 * e + 2 * c + r;
+                if (g == 0) s_sh.m[warp][R] = m[e][r], s_sh.l[warp][R] = l[e][r];
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    *reinterpret_cast<float2*>(&s_sh.o[warp][R][8 * g + 2 * d]) = make_float2(o[e][d][r], o[e][d][2 + r]);
+            }
         join_shares<Elem>(s_sh, kXWarps, a.splits, n, [&](int r) {
             const int R = r0 + r, i = R / a.G;
             return static_cast<Elem*>(a.out) + (static_cast<long long>(t.q0 + i) * a.H + it.h * a.G + R - i * a.G) * kHd;
@@ -274,7 +297,7 @@ __global__ void __launch_bounds__(kXThreads) cross_f32_kernel(const CrossArgs a)
     CrossF32Smem& sm = *reinterpret_cast<CrossF32Smem*>(smem_raw);
     grid_dep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const CrossItem it(a);
+    const CrossItem it(a, blockIdx.x);
     unsigned err = 0;
     const CrossSeq t(a, it.s, err);
     const int rows = t.nq * a.G;
@@ -382,8 +405,9 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     const bool f32 = dt == OASR_F32, paged = a.table != nullptr;
     if (!f32 && static_cast<long long>(max_q) * a.G > kXRows && cross_tc_takes(a)) return cross_tc(a, max_q, stream);
     // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
-    const long long want = (static_cast<long long>(max_q) * a.G + kXRows - 1) / kXRows, items = static_cast<long long>(a.N) * a.Hkv;
-    long long tiles = want;
+    const long long max_rows = static_cast<long long>(max_q) * a.G, items = static_cast<long long>(a.N) * a.Hkv;
+    const int tile_rows = !f32 && max_rows <= 8 ? 8 : kXRows;
+    long long tiles = (max_rows + tile_rows - 1) / tile_rows;
     while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
     if (items * tiles > 0x7fffffffLL / 8) return OASR_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);
@@ -398,8 +422,9 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
         if (!ensure_smem(kern, smem, g_smem_done_x32[paged])) return OASR_ERR_CUDA;
         return launch_pdl_cluster(kern, grid, block, smem, a.splits, stream, static_cast<const CrossArgs>(a));
     }
-    return launch_pdl_cluster(paged ? cross_few_kernel<true> : cross_few_kernel<false>, grid, block, smem, a.splits, stream,
-                              static_cast<const CrossArgs>(a));
+    auto few = [&](auto kern) { return launch_pdl_cluster(kern, grid, block, 0, a.splits, stream, static_cast<const CrossArgs>(a)); };
+    if (tile_rows == 8) return few(paged ? cross_few_kernel<true, 1> : cross_few_kernel<false, 1>);
+    return few(paged ? cross_few_kernel<true, 2> : cross_few_kernel<false, 2>);
 }
 
 // Arguments that both entry points have.

@@ -43,30 +43,6 @@ constexpr int kCItems = 4;   // handed over and not yet finished
 // sequence from the tiles before every kCIndex-th part of them.
 constexpr int kCIndex = 1024;
 
-// Ask the hardware for the next CTA of the grid that has not started, to do its work here: the answer (16 bytes)
-// goes to `to`, counted on `bar`.
-__device__ __forceinline__ void ask_next(uint32_t to, uint32_t bar)
-{
-    mbar_arrive_expect_tx(bar, 16);
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to), "r"(bar)
-                 : "memory");
-}
-// Its index; -1 when every CTA has started (no more is asked then).
-__device__ __forceinline__ int next_cta(uint32_t from)
-{
-    uint32_t x, got;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tmov.u32 %0, 0;\n\t"
-        "ld.shared.b128 r, [%2];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-        "selp.u32 %1, 1, 0, p;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}"
-        : "=&r"(x), "=&r"(got)
-        : "r"(from)
-        : "memory");
-    return got ? static_cast<int>(x) : -1;
-}
-
 struct CSmem {
     static constexpr int tile = kCKeys * kCRowBytes, ks = 3, vs = 2;
     static constexpr int off_q = 0, off_k = tile, off_v = off_k + ks * tile;

@@ -177,7 +177,7 @@ def test_cross(nq, nk, H, Hkv, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("top_q,top_k,H", [(200, 300, 4), (40, 130, 8), (300, 20, 2)])
+@pytest.mark.parametrize("top_q,top_k,H", [(200, 300, 4), (40, 130, 8), (300, 20, 2), (8, 300, 4), (1, 70, 8), (4, 12, 2)])
 def test_many_sequences(top_q, top_k, H):
     """More row tiles than the GPU holds at a time, of any length, empty ones among them: CTAs go from one to the next."""
     g = torch.Generator().manual_seed(top_q)
