@@ -19,23 +19,54 @@ constexpr int kBlk = 128;   // values that share a scale
 
 // ------------------------------------------------------------------ rows to 8 bits
 
-// Sixteen lanes to a block, eight values each.
-template <typename Elem>
+__device__ __forceinline__ void load8_once(const __nv_bfloat16* p, float (&x)[8])
+{
+    unpack8(__ldcs(reinterpret_cast<const uint4*>(p)), x);
+}
+__device__ __forceinline__ void load8_once(const float* p, float (&x)[8])
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// Sixteen lanes to a block, eight values each; four blocks at a time, every load ahead of the first use.  Bound by HBM: 2
+// or 4 bytes in, one out per value.  EVEN: rows are whole blocks, and block i begins at value 128 i (the division of a
+// block's number by the blocks of a row took half of the time).
+constexpr int kQBlocks = 4;
+
+template <bool EVEN, typename Elem>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const Elem* __restrict__ x, uint8_t* __restrict__ x8,
                                                               uint8_t* __restrict__ scale, int M, int K, int kb)
 {
     grid_dep_wait();
     const int l = threadIdx.x & 15;
-    const long long blocks = static_cast<long long>(M) * kb, stride = static_cast<long long>(gridDim.x) * 16;
-    for (long long i = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 4); i < blocks; i += stride) {
-        const long long row = i / kb;
-        const int b = static_cast<int>(i - row * kb), k = b * kBlk + 8 * l;
-        float v[8] = {};
-        if (k < K) load8(x + row * K + k, v);
+    const unsigned mask = 0xffffu << (threadIdx.x & 16);
+    const long long blocks = static_cast<long long>(M) * kb;
+    const long long i0 = static_cast<long long>(blockIdx.x) * (16 * kQBlocks) + (threadIdx.x >> 4);
+    float v[kQBlocks][8];
+    long long at[kQBlocks];   // the lane's first value; -1: none
+#pragma unroll
+    for (int u = 0; u < kQBlocks; ++u) {
+        const long long i = i0 + 16 * u;
+        at[u] = -1;
+        if (i < blocks) {
+            if (EVEN) {
+                at[u] = i * kBlk + 8 * l;
+            } else {
+                const long long row = i / kb;
+                const int k = static_cast<int>(i - row * kb) * kBlk + 8 * l;
+                if (k < K) at[u] = row * K + k;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+        if (at[u] >= 0) load8_once(x + at[u], v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kQBlocks; ++u) {
         uint32_t most = 0;   // the bits of magnitudes order as the values do, NaN above infinity
 #pragma unroll
-        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
-        const unsigned mask = 0xffffu << (threadIdx.x & 16);
+        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[u][e]) & 0x7fffffffu);
 #pragma unroll
         for (int o = 8; o; o >>= 1) most = max(most, __shfl_xor_sync(mask, most, o));
         uint32_t byte = kE4NanScale;
@@ -43,11 +74,11 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const Elem* __rest
         if (most < 0x7f800000u) {
             byte = e4m3_scale_byte(__uint_as_float(most));
             const float f = e4m3_scale_inverse(byte);
-            q.x = e4m3_pack2(v[0] * f, v[1] * f) | (e4m3_pack2(v[2] * f, v[3] * f) << 16);
-            q.y = e4m3_pack2(v[4] * f, v[5] * f) | (e4m3_pack2(v[6] * f, v[7] * f) << 16);
+            q.x = e4m3_pack2(v[u][0] * f, v[u][1] * f) | (e4m3_pack2(v[u][2] * f, v[u][3] * f) << 16);
+            q.y = e4m3_pack2(v[u][4] * f, v[u][5] * f) | (e4m3_pack2(v[u][6] * f, v[u][7] * f) << 16);
         }
-        if (k < K) *reinterpret_cast<uint2*>(x8 + row * K + k) = q;
-        if (l == 0) scale[i] = static_cast<uint8_t>(byte);
+        if (at[u] >= 0) *reinterpret_cast<uint2*>(x8 + at[u]) = q;
+        if (l == 0 && i0 + 16 * u < blocks) scale[i0 + 16 * u] = static_cast<uint8_t>(byte);
     }
     grid_dep_trigger();
 }
@@ -124,9 +155,9 @@ constexpr int kE4Threads = 32 * (kE4Issuer + 2);
 template <int BN>
 struct E4Smem {
     static constexpr int tile_a = 128 * 128, tile = (128 + BN) * 128;   // x rows, then w rows
-    static constexpr int stages = BN > 128 ? 5 : 6;
-    static constexpr int off_out = stages * tile;                       // [8 warps][32 rows][64 bytes]
-    static constexpr int off_bias = off_out + kE4EpiWarps * 32 * 64;    // [8 warps][BN / 2] floats
+    static constexpr int stages = BN > 128 ? 4 : BN > 64 ? 5 : 6;
+    static constexpr int off_out = stages * tile;                       // [8 warps][2][32 rows][64 bytes]
+    static constexpr int off_bias = off_out + kE4EpiWarps * 2 * 32 * 64;    // [8 warps][BN / 2] floats
     static constexpr int off_bar = off_bias + kE4EpiWarps * BN / 2 * 4;   // full, empty, scales full[2], free[2], acc full[2], free[2], drain
     static constexpr int off_misc = off_bar + (2 * stages + 9) * 8;
     static constexpr int bytes = off_misc + 16 + 1024;
@@ -340,8 +371,9 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
         const int rq = warp & 3, half = warp >> 2, M = a.p.M, N = a.p.N;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * rq) << 16) + half * HN;
         float* s_bias = reinterpret_cast<float*>(sm + SP::off_bias) + warp * HN;
-        uint8_t* s_out = sm + SP::off_out + warp * 32 * 64;
+        uint8_t* s_out = sm + SP::off_out + warp * 2 * 32 * 64;
         const Elem* bias = static_cast<const Elem*>(a.p.bias);
+        int staged = 0;   // tiles handed to TMA
         for (int lt = 0; lt < my_tiles; ++lt) {
             const int t = first + lt * stride, mt = t / a.nt, nt = t - mt * a.nt, buf = lt & 1;
             const int row0 = mt * 128 + 32 * rq, col0 = nt * BN + half * HN;
@@ -350,72 +382,68 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
             __syncwarp();
             if (!__all_sync(0xffffffffu, sleep_or_abort(bar_acc_full + 8 * buf, (lt >> 1) & 1, s_abort))) break;
             tc_fence_after();
-            // 16 sums of the lane's row at a time
-            auto sums = [&](int c, float* v) {
-                uint32_t r[16];
-                OASR_TMEM_LD16(tl + buf * BN + c, r);
-                tmem_wait_ld();
+            // the lane's row of the half tile into registers, so that the accumulator is free for the tile after next
+            uint32_t acc[HN];
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 b = *reinterpret_cast<const float4*>(s_bias + c + j);
-                    v[j] = __uint_as_float(r[j]) + b.x, v[j + 1] = __uint_as_float(r[j + 1]) + b.y;
-                    v[j + 2] = __uint_as_float(r[j + 2]) + b.z, v[j + 3] = __uint_as_float(r[j + 3]) + b.w;
-                }
-            };
+            for (int c = 0; c < HN; c += 32) {
+                uint32_t* r = acc + c;
+                OASR_TMEM_LD32(tl + buf * BN + c, r);
+            }
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_release(bar_acc_free + 8 * buf);
+            auto sum = [&](int j) { return __uint_as_float(acc[j]) + s_bias[j]; };
             if (a.by_tma) {
-                // 64 bytes of every row at a time, staged and stored by TMA
+                // 64 bytes of every row at a time, staged in turn in two tiles and stored by TMA
                 constexpr int CB = 64 / sizeof(Elem);
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < HN; c += CB) {
-                    if (col0 + c >= N) break;
-                    float v[CB];
+                    if (col0 + c < N) {
+                        uint8_t* to = s_out + (staged++ & 1) * 32 * 64;
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the tile's last use
+                        __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < CB; j += 16) sums(c + j, v + j);
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the tile's last use
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {   // 16 bytes
-                        uint4 o;
-                        if constexpr (sizeof(Elem) == 2)
-                            o = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                                           pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-                        else
-                            o = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                           __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-                        *reinterpret_cast<uint4*>(s_out + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) = o;
+                        for (int j = 0; j < 4; ++j) {   // 16 bytes
+                            uint4 o;
+                            if constexpr (sizeof(Elem) == 2)
+                                o = make_uint4(pack_bf16(sum(c + 8 * j), sum(c + 8 * j + 1)), pack_bf16(sum(c + 8 * j + 2), sum(c + 8 * j + 3)),
+                                               pack_bf16(sum(c + 8 * j + 4), sum(c + 8 * j + 5)),
+                                               pack_bf16(sum(c + 8 * j + 6), sum(c + 8 * j + 7)));
+                            else
+                                o = make_uint4(__float_as_uint(sum(c + 4 * j)), __float_as_uint(sum(c + 4 * j + 1)),
+                                               __float_as_uint(sum(c + 4 * j + 2)), __float_as_uint(sum(c + 4 * j + 3)));
+                            *reinterpret_cast<uint4*>(to + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) = o;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && row0 < M)
+                            tma_store_2d(&tm_out, smem_addr(to), (col0 + c) * static_cast<int>(sizeof(Elem)), row0);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && row0 < M)
-                        tma_store_2d(&tm_out, smem_addr(s_out), (col0 + c) * static_cast<int>(sizeof(Elem)), row0);
                 }
             } else {
                 // rows of any alignment: 16 columns at a time, staged, 16 lanes to a row
                 float* s_f = reinterpret_cast<float*>(s_out);
-#pragma unroll 1
-                for (int c = 0; c < HN; c += 16) {
-                    if (col0 + c >= N) break;
-                    float v[16];
-                    sums(c, v);
-                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4*>(s_f + 16 * lane + 4 * (j ^ ((lane >> 1) & 3))) =
-                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    __syncwarp();
-                    const int j = lane & 15;
-                    Elem* to = static_cast<Elem*>(a.out) + static_cast<long long>(row0 + (lane >> 4)) * N + col0 + c + j;
+                for (int c = 0; c < HN; c += 16) {
+                    if (col0 + c < N) {
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<float4*>(s_f + 16 * lane + 4 * (j ^ ((lane >> 1) & 3))) =
+                                make_float4(sum(c + 4 * j), sum(c + 4 * j + 1), sum(c + 4 * j + 2), sum(c + 4 * j + 3));
+                        __syncwarp();
+                        const int j = lane & 15;
+                        Elem* to = static_cast<Elem*>(a.out) + static_cast<long long>(row0 + (lane >> 4)) * N + col0 + c + j;
 #pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const int rr = 2 * i + (lane >> 4);
-                        if (row0 + rr < M && col0 + c + j < N)
-                            put(to + 2LL * i * N, s_f[16 * rr + 4 * ((j >> 2) ^ (i & 3)) + (j & 3)]);
+                        for (int i = 0; i < 16; ++i) {
+                            const int rr = 2 * i + (lane >> 4);
+                            if (row0 + rr < M && col0 + c + j < N)
+                                put(to + 2LL * i * N, s_f[16 * rr + 4 * ((j >> 2) ^ (i & 3)) + (j & 3)]);
+                        }
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_release(bar_acc_free + 8 * buf);
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // every store has been made
     }
@@ -433,7 +461,7 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
 
 constexpr int kE4MaxRows = 0x7fffff00, kE4MaxK = 65536;
 
-int g_smem_done_e4l[4][64];
+int g_smem_done_e4l[6][64];
 
 template <int BN, typename Elem>
 oasr_status launch_e4(const E4Problem& p, void* out, int slot, int sms, cudaStream_t stream)
@@ -463,10 +491,14 @@ oasr_status dispatch_e4(const E4Problem& p, void* out, cudaStream_t stream)
     }
     const int sms = sm_count();
     if (!sms) return OASR_ERR_CUDA;
-    constexpr int s = sizeof(Elem) == 4 ? 2 : 0;
+#ifndef E4BN
+#define E4BN 0
+#endif
+    constexpr int s = sizeof(Elem) == 4 ? 3 : 0;
     const long long wide = ((p.M + 127LL) / 128) * ((p.N + 191LL) / 192);
-    if (wide >= sms) return launch_e4<192, Elem>(p, out, s, sms, stream);
-    return launch_e4<64, Elem>(p, out, s + 1, sms, stream);
+    if (E4BN == 192 || (!E4BN && wide >= sms)) return launch_e4<192, Elem>(p, out, s, sms, stream);
+    if (E4BN == 128) return launch_e4<128, Elem>(p, out, s + 1, sms, stream);
+    return launch_e4<64, Elem>(p, out, s + 2, sms, stream);
 }
 
 }  // namespace
@@ -479,13 +511,13 @@ extern "C" oasr_status oasr_quantize_blocks(const void* x, void* x8, void* scale
     if (!x || !x8 || !scale || M <= 0 || K <= 0) return OASR_ERR_INVALID_ARG;
     if ((dt != OASR_F32 && dt != OASR_BF16) || K % 16) return OASR_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(x8)) return OASR_ERR_INVALID_ARG;
-    const int sms = sm_count(), kb = (K + kBlk - 1) / kBlk;
-    if (!sms) return OASR_ERR_CUDA;
-    const long long ctas = (static_cast<long long>(M) * kb + 15) / 16, most = 8LL * sms;
-    const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
+    const int kb = (K + kBlk - 1) / kBlk;
+    const long long ctas = (static_cast<long long>(M) * kb + 16 * kQBlocks - 1) / (16 * kQBlocks);
+    if (ctas > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
     auto go = [&](auto* src) {
         using E = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
-        return launch_pdl(quantize_blocks_kernel<E>, grid, dim3(256), 0, stream, src, static_cast<uint8_t*>(x8),
+        return launch_pdl(K % kBlk ? quantize_blocks_kernel<false, E> : quantize_blocks_kernel<true, E>,
+                          dim3(static_cast<unsigned>(ctas)), dim3(256), 0, stream, src, static_cast<uint8_t*>(x8),
                           static_cast<uint8_t*>(scale), M, K, kb);
     };
     return dt == OASR_F32 ? go(static_cast<const float*>(x)) : go(static_cast<const __nv_bfloat16*>(x));
