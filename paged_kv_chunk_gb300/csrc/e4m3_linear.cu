@@ -5,6 +5,14 @@
 //
 // A block is 128 neighbouring values of a row, of activations and weights alike; the last of a row may be
 // shorter.  The format is the 8-bit cache's (e4m3.cuh) with 128 values to a scale.
+//
+// A scale is a power of two, its byte the one that tcgen05's block-scaled products take (kind::mxf8f6f4, one for each 32 of
+// K): a block's byte serves four steps, and the sums come out of the tensor core scaled, without a pass over the
+// accumulators per block.  Products of two e4m3 values are exact in fp32.
+//
+// What bounds a large product is what it copies into shared memory: 40 KB a step of 128 of K and 128 x 192 outputs, 12 TB/s
+// over the GPU at 65537 x 1024 x 512 (43 us, 1.6 PFLOP/s, 168 MB of HBM traffic); 8191 x 4096 x 1024 takes 37 us (1.86 PFLOP/s;
+// the int8 product 51).  Pairs of CTAs on 256 x 192 (cta_group::2), half of w each, were right and slower: 69 us.
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -208,8 +216,9 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int row, int ro
     if (row >= rows) return w;
     const uint8_t* p = s + static_cast<long long>(row) * kb + 4 * g;
     if (!((kb | static_cast<int>(reinterpret_cast<uintptr_t>(s))) & 3)) return __ldg(reinterpret_cast<const uint32_t*>(p));
-    const int n = min(4, kb - 4 * g);
-    for (int i = 0; i < n; ++i) w = (w & ~(255u << (8 * i))) | (static_cast<uint32_t>(__ldg(p + i)) << (8 * i));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (4 * g + i < kb) w = (w & ~(255u << (8 * i))) | (static_cast<uint32_t>(__ldg(p + i)) << (8 * i));
     return w;
 }
 
@@ -491,13 +500,21 @@ oasr_status dispatch_e4(const E4Problem& p, void* out, cudaStream_t stream)
     }
     const int sms = sm_count();
     if (!sms) return OASR_ERR_CUDA;
-#ifndef E4BN
-#define E4BN 0
-#endif
     constexpr int s = sizeof(Elem) == 4 ? 3 : 0;
-    const long long wide = ((p.M + 127LL) / 128) * ((p.N + 191LL) / 192);
-    if (E4BN == 192 || (!E4BN && wide >= sms)) return launch_e4<192, Elem>(p, out, s, sms, stream);
-    if (E4BN == 128) return launch_e4<128, Elem>(p, out, s + 1, sms, stream);
+    // Tile: the one of the least estimated time.  A step of 128 of K costs 470 ns in 128 x 192, 430 in 128 x 128 and 380 in
+    // 128 x 64 (the copies into shared memory are the cost), a tile's hand-over 250, 100 and 50, the last epilogue 1000, 700
+    // and 400.  Bf16 results, in this order: 8191 x 4096 x 1024 37.0, 44.5 and 75.5 us; 4096 x 512 x 2048 9.5, 9.2 and 13.6;
+    // 1024 x 768 x 256 5.8, 5.3 and 4.4.
+    constexpr struct { int n, step, tile, end; } kinds[] = {{192, 470, 250, 1000}, {128, 430, 100, 700}, {64, 380, 50, 400}};
+    int best = 0;
+    long long least = 0x7fffffffffffffffLL;
+    for (int k = 0; k < 3; ++k) {
+        const long long tiles = ((p.M + 127LL) / 128) * ((p.N + kinds[k].n - 1LL) / kinds[k].n);
+        const long long ns = (tiles + sms - 1) / sms * (static_cast<long long>(p.kb) * kinds[k].step + kinds[k].tile) + kinds[k].end;
+        if (ns < least) least = ns, best = k;
+    }
+    if (best == 0) return launch_e4<192, Elem>(p, out, s, sms, stream);
+    if (best == 1) return launch_e4<128, Elem>(p, out, s + 1, sms, stream);
     return launch_e4<64, Elem>(p, out, s + 2, sms, stream);
 }
 
