@@ -10,15 +10,17 @@
 // lane 4 g + c holds dimensions 8 c .. 8 c + 7 and 32 + 8 c .. 32 + 8 c + 7 of keys g and 8 + g (K) and 8 g .. 8 g + 7
 // of keys 2 c, 2 c + 1, 8 + 2 c and 9 + 2 c (V, whose pairs of keys are interleaved by byte permutes).  The keys of a
 // sequence are shared by the warps of a CTA and, where that leaves SMs idle, by a cluster of CTAs.
+#include <type_traits>
+
 #include "cluster.cuh"
 #include "cross.cuh"
-#include "e4m3.cuh"
 
 namespace oasr {
 namespace {
 
 constexpr int kHd = 64;
 constexpr int kXWarps = 4, kXThreads = 32 * kXWarps, kXRows = 16, kXKeys = 16;
+constexpr int kXSplits = 8;   // CTAs of a cluster at most (the portable size)
 
 __device__ __forceinline__ float ld_shared_cluster(uint32_t addr, uint32_t rank)
 {
@@ -26,6 +28,15 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr, uint32_t rank)
     uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr, uint32_t rank)
+{
+    float4 v;
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
 
@@ -39,9 +50,9 @@ struct Shares {
     float m[kXWarps][kXRows], l[kXWarps][kXRows];
 };
 
-// Join the warps' shares into share 0, then the cluster's, and write the rows.  n: rows of the tile; row r
+// Join the warps' shares (into share 0, and those of a cluster's CTAs then) and write the rows.  n: rows of the tile; row r
 // is written to dst(r).
-template <typename Elem, typename Dst>
+template <typename Elem, bool CLUSTER, typename Dst>
 __device__ __forceinline__ void join_shares(Shares& s, int shares, int splits, int n, Dst dst)
 {
     const int tid = threadIdx.x, r = tid >> 3, d0 = (tid & 7) * 8;   // a thread: a row, eight dimensions
@@ -57,7 +68,7 @@ __device__ __forceinline__ void join_shares(Shares& s, int shares, int splits, i
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] += s.o[w][r][d0 + i] * f;
     }
-    if (splits > 1) {
+    if constexpr (CLUSTER) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) s.o[0][r][d0 + i] = o[i];
@@ -65,23 +76,33 @@ __device__ __forceinline__ void join_shares(Shares& s, int shares, int splits, i
         cluster_sync();
         uint32_t rank;
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        // CTA `rank` finishes rows rank, rank + splits, ...
-        for (int i = tid; i < kXRows * kHd; i += kXThreads) {
-            const int row = i / kHd, d = i % kHd;
-            if (row >= n || row % splits != static_cast<int>(rank)) continue;
-            float top = -INFINITY;
-            for (int p = 0; p < splits; ++p)
-                if (ld_shared_cluster(smem_addr(&s.l[0][row]), p) != 0.f)
-                    top = fmaxf(top, ld_shared_cluster(smem_addr(&s.m[0][row]), p));
-            float sum = 0.f, v = 0.f;
-            for (int p = 0; p < splits; ++p) {
-                const float lp = ld_shared_cluster(smem_addr(&s.l[0][row]), p);
-                if (lp == 0.f) continue;
-                const float f = exp2f(ld_shared_cluster(smem_addr(&s.m[0][row]), p) - top);
-                sum += lp * f;
-                v += ld_shared_cluster(smem_addr(&s.o[0][row][d]), p) * f;
+        // four dimensions of a row at a time, dealt out over the cluster's threads; every remote load of a step on the
+        // way at once
+        for (int i = tid * splits + rank; i < n * (kHd / 4); i += kXThreads * splits) {
+            const int row = i / (kHd / 4), d = i % (kHd / 4) * 4;
+            float lp[kXSplits], mp[kXSplits], top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int p = 0; p < kXSplits; ++p) {
+                lp[p] = p < splits ? ld_shared_cluster(smem_addr(&s.l[0][row]), p) : 0.f;
+                mp[p] = p < splits ? ld_shared_cluster(smem_addr(&s.m[0][row]), p) : 0.f;
             }
-            store_out(static_cast<Elem*>(dst(row)) + d, sum == 0.f ? 0.f : v / sum);
+            float4 op[kXSplits], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < kXSplits; ++p)
+                if (p < splits) op[p] = ld_shared_cluster4(smem_addr(&s.o[0][row][d]), p);
+#pragma unroll
+            for (int p = 0; p < kXSplits; ++p)
+                if (lp[p] != 0.f) top = fmaxf(top, mp[p]);
+#pragma unroll
+            for (int p = 0; p < kXSplits; ++p) {
+                if (lp[p] == 0.f) continue;   // no keys
+                const float f = exp2f(mp[p] - top);
+                sum += lp[p] * f;
+                v.x += op[p].x * f, v.y += op[p].y * f, v.z += op[p].z * f, v.w += op[p].w * f;
+            }
+            const float f = sum == 0.f ? 0.f : 1.f / sum;
+            Elem* to = static_cast<Elem*>(dst(row)) + d;
+            store_out(to, v.x * f), store_out(to + 1, v.y * f), store_out(to + 2, v.z * f), store_out(to + 3, v.w * f);
         }
         cluster_sync();   // no CTA leaves or starts its next tile while another one reads its shares
     } else {
@@ -126,7 +147,7 @@ struct CrossItem {
 
 // NT: eights of rows.  Scores are computed with the keys as the matrix instruction's rows (S^T = K . Q^T, O^T = V^T . P^T),
 // so that eight rows fill its columns; P^T comes from S^T by two 8 x 8 transpositions.
-template <bool PAGED, int NT>
+template <bool PAGED, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kXThreads, 3) cross_few_kernel(const CrossArgs a)
 {
     using Elem = __nv_bfloat16;
@@ -269,7 +290,7 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_few_kernel(const CrossArgs
                 for (int d = 0; d < 4; ++d)
                     *reinterpret_cast<float2*>(&s_sh.o[warp][R][8 * g + 2 * d]) = make_float2(o[e][d][r], o[e][d][2 + r]);
             }
-        join_shares<Elem>(s_sh, kXWarps, a.splits, n, [&](int r) {
+        join_shares<Elem, CLUSTER>(s_sh, kXWarps, a.splits, n, [&](int r) {
             const int R = r0 + r, i = R / a.G;
             return static_cast<Elem*>(a.out) + (static_cast<long long>(t.q0 + i) * a.H + it.h * a.G + R - i * a.G) * kHd;
         });
@@ -320,20 +341,31 @@ __global__ void __launch_bounds__(kXThreads) cross_f32_kernel(const CrossArgs a)
         float m[4], l[4], o[8] = {};   // of rows 4 warp .. 4 warp + 3, the same in every lane
 #pragma unroll
         for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.f;
+        // the next 64 keys are on the way in registers while these are worked on: a thread has 16 bytes of eight of them
+        float4 kn[8], vn[8];
+        auto request = [&](int chunk) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = chunk * kFKeys + 8 * u + (tid >> 4);
+                const int row = chunk < last && j < t.nk ? cross_row<PAGED>(a, t, it.s, j, err) : -1;
+                kn[u] = vn[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row >= 0) {
+                    kn[u] = __ldg(reinterpret_cast<const float4*>(kb + row * a.k_stride) + (tid & 15));
+                    vn[u] = __ldg(reinterpret_cast<const float4*>(vb + row * a.v_stride) + (tid & 15));
+                }
+            }
+        };
+        request(first);
         for (int chunk = first; chunk < last; ++chunk) {
             const int j0 = chunk * kFKeys;
             __syncthreads();
-            for (int i = tid; i < kFKeys * 16; i += kXThreads) {   // 16 threads to a row, so each row is looked up by 16
-                const int j = i >> 4, row = j0 + j < t.nk ? cross_row<PAGED>(a, t, it.s, j0 + j, err) : -1;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-                if (row >= 0) {
-                    x = __ldg(reinterpret_cast<const float4*>(kb + row * a.k_stride) + (i & 15));
-                    y = __ldg(reinterpret_cast<const float4*>(vb + row * a.v_stride) + (i & 15));
-                }
-                *reinterpret_cast<float4*>(&sm.k[j][4 * (i & 15)]) = x;
-                *reinterpret_cast<float4*>(&sm.v[j][4 * (i & 15)]) = y;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                *reinterpret_cast<float4*>(&sm.k[8 * u + (tid >> 4)][4 * (tid & 15)]) = kn[u];
+                *reinterpret_cast<float4*>(&sm.v[8 * u + (tid >> 4)][4 * (tid & 15)]) = vn[u];
             }
             __syncthreads();
+            request(chunk + 1);
             float s[8] = {};
 #pragma unroll 4
             for (int d = 0; d < kHd; d += 4) {
@@ -383,7 +415,7 @@ __global__ void __launch_bounds__(kXThreads) cross_f32_kernel(const CrossArgs a)
         if (lane == 0)
 #pragma unroll
             for (int r = 0; r < 4; ++r) sm.sh.m[0][4 * warp + r] = m[r], sm.sh.l[0][4 * warp + r] = l[r];
-        join_shares<float>(sm.sh, 1, a.splits, n, [&](int r) {
+        join_shares<float, true>(sm.sh, 1, a.splits, n, [&](int r) {
             const int R = r0 + r, i = R / a.G;
             return static_cast<float*>(a.out) + (static_cast<long long>(t.q0 + i) * a.H + it.h * a.G + R - i * a.G) * kHd;
         });
@@ -411,10 +443,12 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
     if (items * tiles > 0x7fffffffLL / 8) return OASR_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);
-    // shares of the keys while SMs would stay idle and every share has keys for its four warps
+    // as many shares of the keys as three CTAs an SM leave room for (a second wave of CTAs costs more than it gains), while
+    // each has keys for its four warps
     const int least = f32 ? kFKeys : 2 * kXWarps * kXKeys;
-    a.splits = 1;
-    while (a.splits < 8 && items * tiles * a.splits < 2LL * sms && max_k >= 2 * a.splits * least) a.splits *= 2;
+    const long long room = 3LL * sms / (items * tiles), wanted = max_k / least;
+    a.splits = static_cast<int>(room < 1 || wanted < 1 ? 1 : room < wanted ? room : wanted);
+    if (a.splits > kXSplits) a.splits = kXSplits;
     const dim3 grid(static_cast<unsigned>(items * tiles * a.splits)), block(kXThreads);
     const int smem = f32 ? static_cast<int>(sizeof(CrossF32Smem)) : 0;
     if (f32) {
@@ -423,8 +457,16 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
         return launch_pdl_cluster(kern, grid, block, smem, a.splits, stream, static_cast<const CrossArgs>(a));
     }
     auto few = [&](auto kern) { return launch_pdl_cluster(kern, grid, block, 0, a.splits, stream, static_cast<const CrossArgs>(a)); };
-    if (tile_rows == 8) return few(paged ? cross_few_kernel<true, 1> : cross_few_kernel<false, 1>);
-    return few(paged ? cross_few_kernel<true, 2> : cross_few_kernel<false, 2>);
+    auto by_pages = [&](auto nt, auto cluster) {
+        return few(paged ? cross_few_kernel<true, nt.value, cluster.value> : cross_few_kernel<false, nt.value, cluster.value>);
+    };
+    using std::false_type, std::true_type;
+    if (tile_rows == 8) {
+        constexpr std::integral_constant<int, 1> nt;
+        return a.splits > 1 ? by_pages(nt, true_type()) : by_pages(nt, false_type());
+    }
+    constexpr std::integral_constant<int, 2> nt;
+    return a.splits > 1 ? by_pages(nt, true_type()) : by_pages(nt, false_type());
 }
 
 // Arguments that both entry points have.

@@ -13,8 +13,7 @@
 namespace oasr {
 namespace {
 
-constexpr int kTabThreads = 256, kTabStreams = 4, kTabGroup = kTabThreads / kTabStreams;   // threads of a stream
-constexpr int kTabMaxStreams = 4096;
+constexpr int kTabThreads = 256, kTabMaxStreams = 4096;
 
 // What a stream's change of length asks for.
 struct Change {
@@ -46,12 +45,16 @@ struct TableArgs {
     unsigned* status;
 };
 
+// STREAMS to a CTA: one, so that a stream's slots have 256 threads, while the CTAs' sums over all streams cost less
+// than that gains (256 streams of up to 1500 new rows: 4.9 us against 7.7 with four), else four.
+template <int STREAMS>
 __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArgs a)
 {
+    constexpr int kTabGroup = kTabThreads / STREAMS;   // threads of a stream
     grid_dep_wait();     // the previous grid on the stream has finished (programmatic launch)
     grid_dep_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b0 = blockIdx.x * kTabStreams, cap = a.mbps * a.bs;
+    const int b0 = blockIdx.x * STREAMS, cap = a.mbps * a.bs;
     unsigned err = 0;
 
     // pages and rows of all streams, and of those before this CTA's
@@ -236,7 +239,8 @@ extern "C" oasr_status oasr_block_table_update(int32_t* block_table, const int32
     const TableArgs a = {block_table, cache_seqlens, new_seqlens, B,     max_blocks_per_seq, block_size,   free_blocks,
                          num_blocks,  free_state,    slot_map,    total, cu_seqlens,         status_word()};
     if (!a.status) return OASR_ERR_CUDA;
-    return launch_pdl(block_table_kernel, dim3((B + kTabStreams - 1) / kTabStreams), dim3(kTabThreads), 0, stream, a);
+    if (B <= 512) return launch_pdl(block_table_kernel<1>, dim3(B), dim3(kTabThreads), 0, stream, a);
+    return launch_pdl(block_table_kernel<4>, dim3((B + 3) / 4), dim3(kTabThreads), 0, stream, a);
 }
 
 extern "C" oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
