@@ -569,11 +569,13 @@ def _rows_apart(t, name, dtype, dev) -> int:
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0 or t.dtype is not dtype:
         _dev(t, name, dtype)
     n, H, D = t.shape
+    if n <= 1 or t.is_contiguous():
+        if n == 1 and not t[0].is_contiguous():
+            raise ValueError(f"{name} must have contiguous rows")
+        return H * D
     apart, head, one = t.stride()
     if (one != 1 and D > 1) or (head != D and H > 1):
         raise ValueError(f"{name} must have contiguous rows")
-    if n <= 1:
-        return H * D
     if apart < H * D or apart * t.element_size() % 16:
         raise ValueError(f"{name}'s rows must lie a multiple of 16 bytes apart and not overlap")
     return apart
@@ -597,9 +599,9 @@ def oasr_block_table_update(block_table, cache_seqlens, new_seqlens, free_blocks
     if total < 0:
         raise ValueError("total must not be negative")
     if slot_map is None:
-        slot_map = torch.empty((total,), dtype=torch.int32, device=block_table.device)
+        slot_map = block_table.new_empty((total,))
     if cu_seqlens is None:
-        cu_seqlens = torch.empty((table[0] + 1,), dtype=torch.int32, device=block_table.device)
+        cu_seqlens = block_table.new_empty((table[0] + 1,))
     if slot_map.shape != (total,) or cu_seqlens.shape != (table[0] + 1,):
         raise ValueError("slot_map must be [total] and cu_seqlens [B + 1]")
     i32 = torch.int32
@@ -649,7 +651,7 @@ def _cross(dev, q, cu_q, max_q, Hkv, out):
         raise ValueError("cu_q must be [num_seqs + 1]")
     _fits(n, H, D, cu_q.shape[0], max_q)
     if out is None:
-        out = torch.empty((n, H, D), dtype=dt, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((n, H, D))
     elif out.shape != (n, H, D):
         raise ValueError("out must be [total_q, H, D]")
     apart = _rows_apart(q, "q", dt, dev)
@@ -723,9 +725,9 @@ def oasr_quantize_blocks(x, x8=None, scale=None, stream=None):
     M, K = x.shape
     _fits(M, K)
     if x8 is None:
-        x8 = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=x.device)
+        x8 = torch.empty_like(x, dtype=torch.float8_e4m3fn)   # x is contiguous, or refused below
     if scale is None:
-        scale = torch.empty((M, -(-K // 128)), dtype=torch.uint8, device=x.device)
+        scale = x.new_empty((M, -(-K // 128)), dtype=torch.uint8)
     if x8.shape != (M, K):
         raise ValueError("x8 must be [M, K]")
     _blocks(x8, scale, "x8")
@@ -746,7 +748,7 @@ def oasr_linear_e4m3(x8, x_scale, w8, w_scale, bias=None, out=None, out_dtype=to
     if Kw != K:
         raise ValueError("shapes: x8 [M,K], w8 [N,K]")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x8.device)
+        out = x8.new_empty((M, N), dtype=out_dtype)
     if out.shape != (M, N) or (bias is not None and bias.shape != (N,)):
         raise ValueError("out must be [M, N] and bias [N]")
     dt = out.dtype

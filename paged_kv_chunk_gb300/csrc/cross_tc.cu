@@ -11,6 +11,17 @@
 // exponentials are, and two CTAs share an SM: one's softmax runs beside the other's products.  O is rescaled
 // only when a row's maximum has grown by more than 2^8 (P then stays below 2^8, the same relative
 // rounding).  P . V stops at the 16 keys that hold the last one; V rows behind it within those are zeroed.
+//
+// The grid has a CTA for every tile; those that run take over the ones that have not started (cluster launch control), so
+// that a tile's start-up (2.7 us of a CTA) passes while the one before it is worked on: 256 transcripts of 20 to
+// 448 rows over up to 1500 states 225 -> 149 us.
+//
+// What bounds it: the chain of a stage (128 keys), about 1830 cycles of a CTA alone: S read 240, maxima 200, exponentials
+// 820 (the exponential unit would need 512), the hand-overs between roles 110 to 400 each; 1250 a stage with two CTAs an SM.
+// 304 sequences of 512 rows over 1280 keys, 8 heads: 428 us, 0.95 PFLOP/s, the tensor pipe 31 % active in the rescoring
+// of 64 utterances (51.6 us).  Right and slower there: eight softmax warps (rows in halves, joined through shared memory, or
+// four lanes to a row), 96 keys a stage with two P, issuers of their own for S and P . V (the registers then leave 128 a
+// thread), rows written during the next tile's first stage, polling instead of suspended waits.
 #include "cluster.cuh"
 #include "cross.cuh"
 
@@ -20,7 +31,6 @@ namespace {
 constexpr int kCRows = 128, kCKeys = 128, kCRowBytes = 128;
 constexpr int kCSoftWarps = 4, kCProducer = kCSoftWarps, kCIssuer = kCSoftWarps + 1, kCThreads = 32 * (kCIssuer + 1);
 constexpr int kCColS = 0, kCColP = 128, kCColO = 192, kCCols = 256;
-
 
 // Out of line: the kernel's roles run different code at once, and instruction fetch stalls them otherwise.
 __device__ __noinline__ bool c_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort)
@@ -150,18 +160,19 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
             CrossSeq::clamp(q0, q1, a.total_q, err);
             return ((q1 - q0) * a.G + rpt - 1) / rpt;
         };
-        int all = 0;
+        constexpr long long kMost = 0x3fffffff;   // offsets that run wild may add up to more; they are flagged already
+        long long all = 0;
         for (int i0 = 0; i0 * per < a.N; i0 += 32) {
-            int n = 0;
+            long long n = 0;
             for (int s = (i0 + lane) * per; s < min((i0 + lane + 1) * per, a.N); ++s) n += tiles_of(s);
-            int sum = n;
+            long long sum = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                const long long v = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += v;
             }
-            index[i0 + lane] = all + sum - n;
-            all += __shfl_sync(0xffffffffu, sum, 31);
+            index[i0 + lane] = static_cast<int>(min(all + sum - n, kMost));
+            all = min(all + __shfl_sync(0xffffffffu, sum, 31), kMost);
         }
         __syncwarp();
         struct Work {
@@ -228,7 +239,7 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
             }
             if (!ok) break;
             // sequences longer than announced have tiles past the grid
-            if (x + static_cast<long long>(gridDim.x) < static_cast<long long>(all) * a.Hkv) {
+            if (x + static_cast<long long>(gridDim.x) < all * a.Hkv && x + static_cast<long long>(gridDim.x) <= 0x7fffffff) {
                 x += gridDim.x;
                 w = look_up(x);
                 continue;
