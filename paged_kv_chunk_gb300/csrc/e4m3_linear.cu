@@ -164,7 +164,7 @@ template <int BN>
 struct E4Smem {
     static constexpr int tile_a = 128 * 128, tile = (128 + BN) * 128;   // x rows, then w rows
     static constexpr int stages = BN > 128 ? 4 : BN > 64 ? 5 : 6;
-    static constexpr int off_out = stages * tile;                       // [8 warps][2][32 rows][64 bytes]
+    static constexpr int off_out = stages * tile;                       // [8 warps][2][32 rows][64 bytes] or [8 warps][32 rows][128 bytes]
     static constexpr int off_bias = off_out + kE4EpiWarps * 2 * 32 * 64;    // [8 warps][BN / 2] floats
     static constexpr int off_bar = off_bias + kE4EpiWarps * BN / 2 * 4;   // full, empty, scales full[2], free[2], acc full[2], free[2], drain
     static constexpr int off_misc = off_bar + (2 * stages + 9) * 8;
@@ -431,24 +431,38 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
                     }
                 }
             } else {
-                // rows of any alignment: 16 columns at a time, staged, 16 lanes to a row
-                float* s_f = reinterpret_cast<float*>(s_out);
+                // rows of any alignment: 32 columns at a time, staged as the lanes' rows and written row by row, a lane
+                // a column
+                constexpr int RB = 32 * sizeof(Elem), PV = 16 / sizeof(Elem);   // bytes of a staged row, values of 16 bytes
+                auto place = [](int r, int v) { return RB * r + 16 * (v ^ (RB == 64 ? r >> 1 & 3 : r & 7)); };
 #pragma unroll
-                for (int c = 0; c < HN; c += 16) {
+                for (int c = 0; c < HN; c += 32) {
                     if (col0 + c < N) {
                         __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<float4*>(s_f + 16 * lane + 4 * (j ^ ((lane >> 1) & 3))) =
-                                make_float4(sum(c + 4 * j), sum(c + 4 * j + 1), sum(c + 4 * j + 2), sum(c + 4 * j + 3));
+                        for (int v = 0; v < RB / 16; ++v) {
+                            uint4 o;
+                            const int j = c + PV * v;
+                            if constexpr (sizeof(Elem) == 2)
+                                o = make_uint4(pack_bf16(sum(j), sum(j + 1)), pack_bf16(sum(j + 2), sum(j + 3)),
+                                               pack_bf16(sum(j + 4), sum(j + 5)), pack_bf16(sum(j + 6), sum(j + 7)));
+                            else
+                                o = make_uint4(__float_as_uint(sum(j)), __float_as_uint(sum(j + 1)), __float_as_uint(sum(j + 2)),
+                                               __float_as_uint(sum(j + 3)));
+                            *reinterpret_cast<uint4*>(s_out + place(lane, v)) = o;
+                        }
                         __syncwarp();
-                        const int j = lane & 15;
-                        Elem* to = static_cast<Elem*>(a.out) + static_cast<long long>(row0 + (lane >> 4)) * N + col0 + c + j;
-#pragma unroll 4
-                        for (int i = 0; i < 16; ++i) {
-                            const int rr = 2 * i + (lane >> 4);
-                            if (row0 + rr < M && col0 + c + j < N)
-                                put(to + 2LL * i * N, s_f[16 * rr + 4 * ((j >> 2) ^ (i & 3)) + (j & 3)]);
+                        if (col0 + c + lane < N) {
+                            Elem* to = static_cast<Elem*>(a.out) + static_cast<long long>(row0) * N + col0 + c + lane;
+                            auto at = [&](int r) {
+                                return reinterpret_cast<const Elem*>(s_out + place(r, lane / PV))[lane % PV];
+                            };
+                            if (row0 + 32 <= M) {
+#pragma unroll 16
+                                for (int r = 0; r < 32; ++r) to[static_cast<long long>(r) * N] = at(r);
+                            } else {
+                                for (int r = 0; r < M - row0; ++r) to[static_cast<long long>(r) * N] = at(r);
+                            }
                         }
                     }
                 }
