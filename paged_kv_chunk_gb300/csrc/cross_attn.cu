@@ -312,7 +312,7 @@ struct CrossF32Smem {
 };
 
 template <bool PAGED>
-__global__ void __launch_bounds__(kXThreads) cross_f32_kernel(const CrossArgs a)
+__global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs a)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     CrossF32Smem& sm = *reinterpret_cast<CrossF32Smem*>(smem_raw);
@@ -344,15 +344,19 @@ __global__ void __launch_bounds__(kXThreads) cross_f32_kernel(const CrossArgs a)
         // the next 64 keys are on the way in registers while these are worked on: a thread has 16 bytes of eight of them
         float4 kn[8], vn[8];
         auto request = [&](int chunk) {
+            if (chunk >= last) return;
+            int row[8];   // every page looked up before the first key is asked for
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const int j = chunk * kFKeys + 8 * u + (tid >> 4);
-                const int row = chunk < last && j < t.nk ? cross_row<PAGED>(a, t, it.s, j, err) : -1;
-                kn[u] = vn[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (row >= 0) {
-                    kn[u] = __ldg(reinterpret_cast<const float4*>(kb + row * a.k_stride) + (tid & 15));
-                    vn[u] = __ldg(reinterpret_cast<const float4*>(vb + row * a.v_stride) + (tid & 15));
-                }
+                const int j = chunk * kFKeys + 8 * u + (tid >> 4), r = cross_row<PAGED>(a, t, it.s, min(j, t.nk - 1), err);
+                row[u] = j < t.nk ? r : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const long long r = max(row[u], 0);   // a row without a key is read and not used
+                kn[u] = __ldg(reinterpret_cast<const float4*>(kb + r * a.k_stride) + (tid & 15));
+                vn[u] = __ldg(reinterpret_cast<const float4*>(vb + r * a.v_stride) + (tid & 15));
+                if (row[u] < 0) kn[u] = vn[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         };
         request(first);
