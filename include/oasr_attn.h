@@ -385,7 +385,7 @@ oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_
  * owns keep what they held.  Rows of q, k and v are q_stride, k_stride, v_stride values apart (heads are
  * contiguous: k and v may be the halves of one product's rows); out is [total_q, H, 64].
  * max_q and max_k are the lengths that the launch is laid out for: a longer sequence is right, and slower.
- * Requirements: D = 64; H a multiple of Hkv and at most 1024; num_seqs at most 65536; scale > 0 and finite; pointers
+ * Requirements: D = 64; H a multiple of Hkv and at most 1024; num_seqs at most 65536; 0 < scale <= 2e38; pointers
  * and strides multiples of 16 bytes; total_q, total_k, max_q and max_k at least 1; total_q * G below 2^31 - 256;
  * num_blocks * block_size < 2^31.
  * Offsets that decrease or pass total_q or total_k, and lengths past the table, are clamped; an invalid block id

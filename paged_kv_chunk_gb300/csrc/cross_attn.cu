@@ -479,7 +479,7 @@ oasr_status cross_check(const CrossArgs& a, int max_q, int max_k, int D, float s
     if (!a.q || !a.k || !a.v || !a.cu_q || !a.out) return OASR_ERR_INVALID_ARG;
     if (a.N <= 0 || a.H <= 0 || a.Hkv <= 0 || a.H % a.Hkv || max_q <= 0 || max_k <= 0 || a.total_q <= 0 || D <= 0)
         return OASR_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || scale > 3e38f) return OASR_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale > 2e38f) return OASR_ERR_INVALID_ARG;
     if ((dt != OASR_F32 && dt != OASR_BF16) || D != kHd || a.N > kXMaxSeqs || a.H > kXMaxHeads) return OASR_ERR_UNSUPPORTED;
     const long long es = dt == OASR_F32 ? 4 : 2;
     if (a.q_stride < a.H * kHd || a.k_stride < a.Hkv * kHd || a.v_stride < a.Hkv * kHd || (a.q_stride * es) % 16 ||

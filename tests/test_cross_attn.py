@@ -94,7 +94,7 @@ COMMON = [
     (dict(mq=0), capi.OASR_ERR_INVALID_ARG), (dict(mk=-1), capi.OASR_ERR_INVALID_ARG),
     (dict(H=6, Hkv=4), capi.OASR_ERR_INVALID_ARG), (dict(Hkv=0), capi.OASR_ERR_INVALID_ARG),
     (dict(scale=0.0), capi.OASR_ERR_INVALID_ARG), (dict(scale=-1.0), capi.OASR_ERR_INVALID_ARG),
-    (dict(scale=math.inf), capi.OASR_ERR_INVALID_ARG), (dict(scale=math.nan), capi.OASR_ERR_INVALID_ARG),
+    (dict(scale=math.inf), capi.OASR_ERR_INVALID_ARG), (dict(scale=2.5e38), capi.OASR_ERR_INVALID_ARG), (dict(scale=math.nan), capi.OASR_ERR_INVALID_ARG),
     (dict(qs=508), capi.OASR_ERR_INVALID_ARG), (dict(qs=448), capi.OASR_ERR_INVALID_ARG),
     (dict(q=FAKE + 8), capi.OASR_ERR_INVALID_ARG), (dict(out=FAKE + 4), capi.OASR_ERR_INVALID_ARG),
     (dict(D=32), capi.OASR_ERR_UNSUPPORTED), (dict(dt=2), capi.OASR_ERR_UNSUPPORTED),
@@ -162,6 +162,8 @@ SHAPES = [  # queries, keys, H, Hkv
     ([33], [1], 8, 1),
     ([450], [2000], 1, 1),
     ([37, 91, 130], [5, 1000, 256], 20, 4),
+    ([3, 1], [40, 200], 300, 2),                  # 150 query heads to a key head: more than a tile's rows
+    ([2] * 8, [1500, 700, 3, 0, 129, 1000, 64, 900], 8, 8),   # keys shared by seven CTAs
 ]
 
 
