@@ -3,13 +3,18 @@
 // (single tokens, beams) in bf16, and the fp32 kernel.  Many rows go to the tensor-core kernel of cross_tc.cu.
 //
 // Few rows: every key row is read once for at most 16 rows, so the bytes of k and v are the cost and what counts is
-// how many of them are on the way.  A warp takes 16 keys at a time straight into the registers that the
-// matrix instructions read, without shared memory, and requests the next 16 before it works on these.
-// The contraction of q . k may run over the 64 dimensions in any order, and the rows of O^T stand for any
-// dimensions, so the order is taken in which a lane loads 16 bytes at a time and its neighbours the next ones:
-// lane 4 g + c holds dimensions 8 c .. 8 c + 7 and 32 + 8 c .. 32 + 8 c + 7 of keys g and 8 + g (K) and 8 g .. 8 g + 7
-// of keys 2 c, 2 c + 1, 8 + 2 c and 9 + 2 c (V, whose pairs of keys are interleaved by byte permutes).  The keys of a
-// sequence are shared by the warps of a CTA and, where that leaves SMs idle, by a cluster of CTAs.
+// how many of them are on the way.  A warp takes 16 keys at a time from a ring of its own in shared memory, three
+// chunks (12 KB) ahead, by asynchronous copies of whole 128-byte lines; no other warp waits for it until the shares are
+// joined.  Scores are computed with the keys as the matrix instruction's rows (S^T = K . Q^T, O^T = V^T . P^T), so that eight
+// query rows fill its columns.  The contraction of q . k may run over the 64 dimensions in any order, and the rows of O^T
+// stand for any dimensions, so the order is taken in which a lane's part of a row is 16 bytes: lane 4 g + c has dimensions
+// 8 c .. 8 c + 7 and 32 + 8 c .. 32 + 8 c + 7 of keys g and 8 + g (K) and 8 g .. 8 g + 7 of keys 2 c, 2 c + 1, 8 + 2 c and
+// 9 + 2 c (V, whose pairs of keys are interleaved by byte permutes).  The keys of a sequence are shared by the warps of a
+// CTA and, where that leaves SMs idle, by a cluster of CTAs.
+//
+// A beam of 8 over 256 utterances of 50 to 1500 keys, 8 heads, in pages (410 MB): 73 us, 0.83 of the copy rate; 456 heads of
+// 3480 keys, one wave: 0.99 of it.  With keys in registers, a lane loading what it uses, 86.5: half a row of K at a time, its
+// lines came twice from L2, and so did copies by lane (88).
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -20,6 +25,7 @@ namespace {
 
 constexpr int kHd = 64;
 constexpr int kXWarps = 4, kXThreads = 32 * kXWarps, kXRows = 16, kXKeys = 16;
+constexpr int kXRing = 4, kXChunk = 4096, kXCtas = 3;   // chunks of a warp's ring, bytes of one; CTAs an SM
 constexpr int kXSplits = 8;   // CTAs of a cluster at most (the portable size)
 
 __device__ __forceinline__ float ld_shared_cluster(uint32_t addr, uint32_t rank)
@@ -145,14 +151,20 @@ struct CrossItem {
     }
 };
 
-// NT: eights of rows.  Scores are computed with the keys as the matrix instruction's rows (S^T = K . Q^T, O^T = V^T . P^T),
-// so that eight rows fill its columns; P^T comes from S^T by two 8 x 8 transpositions.
+// 16 bytes of a key, copied without passing registers; zeros where there is none.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+
+// NT: eights of rows; P^T comes from S^T by two 8 x 8 transpositions.
 template <bool PAGED, int NT, bool CLUSTER>
-__global__ void __launch_bounds__(kXThreads, 3) cross_few_kernel(const CrossArgs a)
+__global__ void __launch_bounds__(kXThreads, kXCtas) cross_few_kernel(const CrossArgs a)
 {
     using Elem = __nv_bfloat16;
     constexpr int RT = 8 * NT;
-    __shared__ Shares s_sh;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Shares& s_sh = *reinterpret_cast<Shares*>(smem_raw);   // once the rings are done with
     grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const CrossItem it(a, blockIdx.x);
@@ -166,27 +178,26 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_few_kernel(const CrossArgs
     const Elem* vb = static_cast<const Elem*>(a.v) + it.h * kHd;
     // K of keys g, 8 + g (two words of 16 bytes each), V of keys 2c, 2c + 1, 8 + 2c, 9 + 2c
     using Chunk = uint4[8];
+    const uint8_t* ring = smem_raw + warp * (kXRing * kXChunk);
     auto row_of = [&](int chunk) {   // lanes 0 .. 15: the row of the chunk's key
         const int j = chunk * kXKeys + (lane & 15);
         return chunk < last && j < t.nk ? cross_row<PAGED>(a, t, it.s, j, err) : -1;
     };
-    auto request = [&](int row, Chunk& kv) {
-        const bool whole = __all_sync(0xffffffffu, row >= 0);
-        auto at = [&](const Elem* base, long long stride, int j, int d) {
-            return reinterpret_cast<const uint4*>(base + __shfl_sync(0xffffffffu, row, j) * stride + d);
-        };
-        const uint4 *k0 = at(kb, a.k_stride, g, 8 * c), *k1 = at(kb, a.k_stride, 8 + g, 8 * c);
-        const uint4 *v0 = at(vb, a.v_stride, 2 * c, 8 * g), *v1 = at(vb, a.v_stride, 2 * c + 1, 8 * g);
-        const uint4 *v2 = at(vb, a.v_stride, 8 + 2 * c, 8 * g), *v3 = at(vb, a.v_stride, 9 + 2 * c, 8 * g);
-        if (whole) {
-            kv[0] = __ldg(k0), kv[1] = __ldg(k0 + 4), kv[2] = __ldg(k1), kv[3] = __ldg(k1 + 4);
-            kv[4] = __ldg(v0), kv[5] = __ldg(v1), kv[6] = __ldg(v2), kv[7] = __ldg(v3);
-        } else {   // keys past the end, or in no block: zeros
-            const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
-            auto get = [&](const uint4* p, int j) { return there >> j & 1 ? __ldg(p) : make_uint4(0, 0, 0, 0); };
-            kv[0] = get(k0, g), kv[1] = get(k0 + 4, g), kv[2] = get(k1, 8 + g), kv[3] = get(k1 + 4, 8 + g);
-            kv[4] = get(v0, 2 * c), kv[5] = get(v1, 2 * c + 1), kv[6] = get(v2, 8 + 2 * c), kv[7] = get(v3, 9 + 2 * c);
+    // A chunk in the warp's ring: 16 rows of K, then of V, of 128 bytes each.  The 16 bytes of a row change places so that
+    // the lanes' reads below meet no bank twice.  Eight lanes copy a row: whole lines (with a lane copying what it will
+    // read, half a row of K at a time, the lines of K came twice from L2).
+    auto k_at = [](int r, int piece) { return 128 * r + 16 * (piece ^ (r & 1) << 2); };
+    auto v_at = [](int r, int piece) { return 2048 + 128 * r + 16 * (piece ^ (r & 7)); };
+    auto request = [&](int row, int slot) {
+        const uint32_t to = smem_addr(ring + slot * kXChunk);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = 4 * u + (lane >> 3), piece = lane & 7, at = __shfl_sync(0xffffffffu, row, r);
+            const long long from = max(at, 0);
+            copy16(to + k_at(r, piece), kb + from * a.k_stride + 8 * piece, at >= 0);
+            copy16(to + v_at(r, piece), vb + from * a.v_stride + 8 * piece, at >= 0);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int tile = it.tile; tile * RT < rows; tile += a.tiles) {
         const int r0 = tile * RT, n = min(rows - r0, RT);
@@ -263,21 +274,27 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_few_kernel(const CrossArgs
                 for (int e = 0; e < NT; ++e) mma_bf16_16816(o[e][d], vf, p[e][0], p[e][1]);
             }
         };
-        // two chunks' registers in turn: one is requested while the other is worked on
-        int chunk = first + warp;
-        Chunk even, odd;
-        request(row_of(chunk), even);
-        int row = row_of(chunk + kXWarps);
-        while (chunk < last) {
-            request(row, odd);
-            row = row_of(chunk + 2 * kXWarps);
-            work(chunk, even);
-            if ((chunk += kXWarps) >= last) break;
-            request(row, even);
-            row = row_of(chunk + 2 * kXWarps);
-            work(chunk, odd);
-            chunk += kXWarps;
+        // kXRing - 1 chunks on the way, and the row of the next one looked up
+        int row[kXRing];
+#pragma unroll
+        for (int i = 0; i < kXRing; ++i) row[i] = row_of(first + warp + i * kXWarps);
+#pragma unroll
+        for (int i = 0; i < kXRing - 1; ++i) request(row[i], i);
+        int next = row[kXRing - 1], slot = 0;
+        for (int chunk = first + warp; chunk < last; chunk += kXWarps) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kXRing - 2) : "memory");
+            __syncwarp();   // every lane's copies
+            const uint8_t* from = ring + slot * kXChunk;
+            auto get = [&](int at) { return *reinterpret_cast<const uint4*>(from + at); };
+            const Chunk kv = {get(k_at(g, c)),         get(k_at(g, 4 + c)),         get(k_at(8 + g, c)),     get(k_at(8 + g, 4 + c)),
+                              get(v_at(2 * c, g)),     get(v_at(2 * c + 1, g)),     get(v_at(8 + 2 * c, g)), get(v_at(9 + 2 * c, g))};
+            request(next, slot == 0 ? kXRing - 1 : slot - 1);   // where the last chunk was
+            next = row_of(chunk + kXRing * kXWarps);
+            work(chunk, kv);
+            if (++slot == kXRing) slot = 0;
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();   // the rings become the shares' place
 #pragma unroll
         for (int e = 0; e < NT; ++e)
 #pragma unroll
@@ -430,7 +447,7 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs
 
 // --------------------------------------------------------------------------- host
 
-int g_smem_done_x32[2][64];
+int g_smem_done_x32[2][64], g_smem_done_few[8][64];
 
 constexpr int kXMaxSeqs = 65536, kXMaxHeads = 1024;
 
@@ -447,10 +464,10 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
     if (items * tiles > 0x7fffffffLL / 8) return OASR_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);
-    // as many shares of the keys as three CTAs an SM leave room for (a second wave of CTAs costs more than it gains), while
-    // each has keys for its four warps
+    // as many shares of the keys as two CTAs an SM leave room for, while each has keys for its four warps (64 rows of a key head
+    // over 1500 keys: 8.8 us with four shares, 13.4 with seven, which a wave of clusters does not take)
     const int least = f32 ? kFKeys : 2 * kXWarps * kXKeys;
-    const long long room = 3LL * sms / (items * tiles), wanted = max_k / least;
+    const long long room = 2LL * sms / (items * tiles), wanted = max_k / least;
     a.splits = static_cast<int>(room < 1 || wanted < 1 ? 1 : room < wanted ? room : wanted);
     if (a.splits > kXSplits) a.splits = kXSplits;
     const dim3 grid(static_cast<unsigned>(items * tiles * a.splits)), block(kXThreads);
@@ -460,9 +477,11 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
         if (!ensure_smem(kern, smem, g_smem_done_x32[paged])) return OASR_ERR_CUDA;
         return launch_pdl_cluster(kern, grid, block, smem, a.splits, stream, static_cast<const CrossArgs>(a));
     }
-    auto few = [&](auto kern) { return launch_pdl_cluster(kern, grid, block, 0, a.splits, stream, static_cast<const CrossArgs>(a)); };
     auto by_pages = [&](auto nt, auto cluster) {
-        return few(paged ? cross_few_kernel<true, nt.value, cluster.value> : cross_few_kernel<false, nt.value, cluster.value>);
+        constexpr int ring = kXWarps * kXRing * kXChunk;
+        auto kern = paged ? cross_few_kernel<true, nt.value, cluster.value> : cross_few_kernel<false, nt.value, cluster.value>;
+        if (!ensure_smem(kern, ring, g_smem_done_few[4 * (nt.value - 1) + 2 * cluster.value + paged])) return OASR_ERR_CUDA;
+        return launch_pdl_cluster(kern, grid, block, ring, a.splits, stream, static_cast<const CrossArgs>(a));
     };
     using std::false_type, std::true_type;
     if (tile_rows == 8) {
