@@ -208,18 +208,35 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* w)
                      : "memory");
 }
 
-// The scale bytes of blocks 4 g .. 4 g + 3 of a row; 2^0 for rows past the matrix and blocks past the row, whose
-// values come as zeros.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* s, int row, int rows, int kb, int g)
+// The scale bytes of blocks 4 g .. 4 g + 3 of rows first + 32 j + the lane, j < N; 2^0 for rows past the matrix and blocks past
+// the row, whose values come as zeros.  Every load goes out before the first is used (a branch for each row had the
+// loads of one wait for the other's: 3 us a tile at K = 240).
+template <int N>
+__device__ __forceinline__ void scale_words(const uint8_t* s, int first, int rows, int kb, int g, uint32_t* w)
 {
-    uint32_t w = 0x7f7f7f7fu;
-    if (row >= rows) return w;
-    const uint8_t* p = s + static_cast<long long>(row) * kb + 4 * g;
-    if (!((kb | static_cast<int>(reinterpret_cast<uintptr_t>(s))) & 3)) return __ldg(reinterpret_cast<const uint32_t*>(p));
+    const int lane = threadIdx.x & 31;
+    const uint8_t* p[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (4 * g + i < kb) w = (w & ~(255u << (8 * i))) | (static_cast<uint32_t>(__ldg(p + i)) << (8 * i));
-    return w;
+    for (int j = 0; j < N; ++j) p[j] = s + static_cast<long long>(min(first + 32 * j + lane, rows - 1)) * kb;
+    if (!((kb | static_cast<int>(reinterpret_cast<uintptr_t>(s))) & 3)) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p[j] + 4 * g));
+    } else {
+        uint32_t byte[N][4];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) byte[j][i] = __ldg(p[j] + min(4 * g + i, kb - 1));
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            w[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[j] |= (4 * g + i < kb ? byte[j][i] : 0x7fu) << (8 * i);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (first + 32 * j + lane >= rows) w[j] = 0x7f7f7f7fu;
 }
 
 template <int BN, typename Elem>
@@ -354,11 +371,10 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
             const int t = first + lt * stride, mt = t / a.nt, nt = t - mt * a.nt;
             for (int g = 0; g < groups; ++g, ++gi) {
                 uint32_t wa[4], wb[NBS];
+                scale_words<4>(a.p.xs, mt * 128, a.p.M, a.p.kb, g, wa);
+                scale_words<NB>(a.p.ws, nt * BN, a.p.N, a.p.kb, g, wb);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) wa[j] = scale_word(a.p.xs, mt * 128 + 32 * j + lane, a.p.M, a.p.kb, g);
-#pragma unroll
-                for (int j = 0; j < NBS; ++j)
-                    wb[j] = j < NB ? scale_word(a.p.ws, nt * BN + 32 * j + lane, a.p.N, a.p.kb, g) : 0u;
+                for (int j = NB; j < NBS; ++j) wb[j] = 0u;
                 const int sf = gi & 1;
                 if (gi >= 2 && !__all_sync(0xffffffffu, sleep_or_abort(bar_sf_free + 8 * sf, ((gi >> 1) - 1) & 1, s_abort))) {
                     ok = false;
