@@ -27,15 +27,46 @@ constexpr int kBlk = 128;   // values that share a scale
 
 // ------------------------------------------------------------------ rows to 8 bits
 
-__device__ __forceinline__ void load8_once(const __nv_bfloat16* p, float (&x)[8])
-{
-    unpack8(__ldcs(reinterpret_cast<const uint4*>(p)), x);
-}
-__device__ __forceinline__ void load8_once(const float* p, float (&x)[8])
-{
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
+// Eight values as they come, the fp32 bits of the largest magnitude among them and the block's other lanes' (the bits order
+// as the values do, NaN above infinity), and the values in fp32.
+struct Raw8Bf16 {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void clear() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ uint32_t largest(unsigned mask) const
+    {
+        constexpr uint32_t A = 0x7fff7fffu;
+        uint32_t m = __vmaxu2(__vimax3_u16x2(w.x & A, w.y & A, w.z & A), w.w & A);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(mask, m, o));
+        return max(m << 16, m & 0xffff0000u);
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const { unpack8(w, x); }
+};
+struct Raw8F32 {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ uint32_t largest(unsigned mask) const
+    {
+        float x[8];
+        values(x);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
+        return m;
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const
+    {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
 
 // Sixteen lanes to a block, eight values each; four blocks at a time, every load ahead of the first use.  Bound by HBM: 2
 // or 4 bytes in, one out per value.  EVEN: rows are whole blocks, and block i begins at value 128 i (the division of a
@@ -44,14 +75,14 @@ constexpr int kQBlocks = 4;
 
 template <bool EVEN, typename Elem>
 __global__ void __launch_bounds__(256) quantize_blocks_kernel(const Elem* __restrict__ x, uint8_t* __restrict__ x8,
-                                                              uint8_t* __restrict__ scale, int M, int K, int kb)
+                                                              uint8_t* __restrict__ scale, int M, int K, int kb, unsigned recip)
 {
     grid_dep_wait();
     const int l = threadIdx.x & 15;
     const unsigned mask = 0xffffu << (threadIdx.x & 16);
     const long long blocks = static_cast<long long>(M) * kb;
     const long long i0 = static_cast<long long>(blockIdx.x) * (16 * kQBlocks) + (threadIdx.x >> 4);
-    float v[kQBlocks][8];
+    std::conditional_t<sizeof(Elem) == 2, Raw8Bf16, Raw8F32> raw[kQBlocks];
     long long at[kQBlocks];   // the lane's first value; -1: none
 #pragma unroll
     for (int u = 0; u < kQBlocks; ++u) {
@@ -61,29 +92,28 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(const Elem* __rest
             if (EVEN) {
                 at[u] = i * kBlk + 8 * l;
             } else {
-                const long long row = i / kb;
+                // i / kb by the reciprocal 2^32 / kb, rounded up: at most one too many below 2^31; 64-bit divisions beyond
+                long long row = kb == 1 ? i : blocks >> 31 ? i / kb : __umulhi(static_cast<unsigned>(i), recip);
+                if (row * kb > i) --row;
                 const int k = static_cast<int>(i - row * kb) * kBlk + 8 * l;
                 if (k < K) at[u] = row * K + k;
             }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
-        if (at[u] >= 0) load8_once(x + at[u], v[u]);
+        raw[u].clear();
+        if (at[u] >= 0) raw[u].load(x + at[u]);
     }
 #pragma unroll
     for (int u = 0; u < kQBlocks; ++u) {
-        uint32_t most = 0;   // the bits of magnitudes order as the values do, NaN above infinity
-#pragma unroll
-        for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[u][e]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) most = max(most, __shfl_xor_sync(mask, most, o));
+        const uint32_t most = raw[u].largest(mask);
+        float v[8];
+        raw[u].values(v);
         uint32_t byte = kE4NanScale;
         uint2 q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
         if (most < 0x7f800000u) {
             byte = e4m3_scale_byte(__uint_as_float(most));
             const float f = e4m3_scale_inverse(byte);
-            q.x = e4m3_pack2(v[u][0] * f, v[u][1] * f) | (e4m3_pack2(v[u][2] * f, v[u][3] * f) << 16);
-            q.y = e4m3_pack2(v[u][4] * f, v[u][5] * f) | (e4m3_pack2(v[u][6] * f, v[u][7] * f) << 16);
+            q.x = e4m3_pack2(v[0] * f, v[1] * f) | (e4m3_pack2(v[2] * f, v[3] * f) << 16);
+            q.y = e4m3_pack2(v[4] * f, v[5] * f) | (e4m3_pack2(v[6] * f, v[7] * f) << 16);
         }
         if (at[u] >= 0) *reinterpret_cast<uint2*>(x8 + at[u]) = q;
         if (l == 0 && i0 + 16 * u < blocks) scale[i0 + 16 * u] = static_cast<uint8_t>(byte);
@@ -523,10 +553,17 @@ oasr_status launch_e4(const E4Problem& p, void* out, int slot, int sms, cudaStre
 template <typename Elem>
 oasr_status dispatch_e4(const E4Problem& p, void* out, cudaStream_t stream)
 {
-    if (p.M <= kE4FewRows) {
+    // A few rows without tiles, where that is the shorter of the two: about 1300 ns and 90 for each row and 128 of K (512 at a
+    // time, and up to 2048 columns), against 2600 and 300 for each 128 of K.  2 x 512 x 2048: 4.0 and 7.3 us, 4 x 2048 x
+    // 512 2.6 and 3.8, 6 x 4096 x 1024 8.7 and 5.7, 8 x 512 x 2048 9.7 and 7.3.
+    const long long steps = (p.K + 511LL) / 512 * 4, few = 1300 + 90 * p.M * steps * (p.N > 2048 ? p.N : 2048) / 2048;
+    if (p.M == 1 || (p.M <= kE4FewRows && few < 2600 + 300LL * p.kb)) {
         const dim3 grid((p.N + 7) / 8);
-        if (p.M == 1) return launch_pdl(linear_e4m3_few_kernel<1, Elem>, grid, dim3(256), 0, stream, p, static_cast<Elem*>(out));
-        return launch_pdl(linear_e4m3_few_kernel<kE4FewRows, Elem>, grid, dim3(256), 0, stream, p, static_cast<Elem*>(out));
+        auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(256), 0, stream, p, static_cast<Elem*>(out)); };
+        if (p.M == 1) return go(linear_e4m3_few_kernel<1, Elem>);
+        if (p.M == 2) return go(linear_e4m3_few_kernel<2, Elem>);
+        if (p.M <= 4) return go(linear_e4m3_few_kernel<4, Elem>);
+        return go(linear_e4m3_few_kernel<kE4FewRows, Elem>);
     }
     const int sms = sm_count();
     if (!sms) return OASR_ERR_CUDA;
@@ -565,7 +602,8 @@ extern "C" oasr_status oasr_quantize_blocks(const void* x, void* x8, void* scale
         using E = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
         return launch_pdl(K % kBlk ? quantize_blocks_kernel<false, E> : quantize_blocks_kernel<true, E>,
                           dim3(static_cast<unsigned>(ctas)), dim3(256), 0, stream, src, static_cast<uint8_t*>(x8),
-                          static_cast<uint8_t*>(scale), M, K, kb);
+                          static_cast<uint8_t*>(scale), M, K, kb,
+                          kb > 1 ? static_cast<unsigned>(0xffffffffu / kb + 1) : 0u);
     };
     return dt == OASR_F32 ? go(static_cast<const float*>(x)) : go(static_cast<const __nv_bfloat16*>(x));
 }
