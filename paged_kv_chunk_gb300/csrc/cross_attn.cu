@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs
                                                           (it.h * a.G + R - qi * a.G) * kHd) + (i & 15));
             *reinterpret_cast<float4*>(&sm.q[r][4 * (i & 15)]) = x;
         }
-        float m[4], l[4], o[8] = {};   // of rows 4 warp .. 4 warp + 3, the same in every lane
+        float2 o[8] = {};   // sums over even and odd keys
+        float m[4], l[4];   // of rows 4 warp .. 4 warp + 3, the same in every lane
 #pragma unroll
         for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.f;
         // the next 64 keys are on the way in registers while these are worked on: a thread has 16 bytes of eight of them
@@ -387,16 +388,21 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs
             }
             __syncthreads();
             request(chunk + 1);
-            float s[8] = {};
+            // sums of even and odd terms side by side: two products an instruction
+            float2 s2[8] = {};
 #pragma unroll 4
             for (int d = 0; d < kHd; d += 4) {
                 const float4 k = *reinterpret_cast<const float4*>(&sm.k[col][d]);
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     const float4 q = *reinterpret_cast<const float4*>(&sm.q[8 * half + r][d]);
-                    s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+                    s2[r] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k.x, k.y), s2[r]);
+                    s2[r] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k.z, k.w), s2[r]);
                 }
             }
+            float s[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s[r] = s2[r].x + s2[r].y;
 #pragma unroll
             for (int r = 0; r < 8; ++r) sm.p[8 * half + r][col] = j0 + col < t.nk ? s[r] * a.c : -INFINITY;
             __syncthreads();
@@ -420,19 +426,20 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs
             }
             __syncthreads();
 #pragma unroll
-            for (int r = 0; r < 8; ++r) o[r] *= sm.f[8 * half + r];
+            for (int r = 0; r < 8; ++r) o[r].x *= sm.f[8 * half + r], o[r].y *= sm.f[8 * half + r];
 #pragma unroll 4
             for (int j = 0; j < kFKeys; j += 4) {
-                const float v0 = sm.v[j][col], v1 = sm.v[j + 1][col], v2 = sm.v[j + 2][col], v3 = sm.v[j + 3][col];
+                const float2 v0 = make_float2(sm.v[j][col], sm.v[j + 1][col]), v1 = make_float2(sm.v[j + 2][col], sm.v[j + 3][col]);
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     const float4 p = *reinterpret_cast<const float4*>(&sm.p[8 * half + r][j]);
-                    o[r] = fmaf(p.x, v0, fmaf(p.y, v1, fmaf(p.z, v2, fmaf(p.w, v3, o[r]))));
+                    o[r] = __ffma2_rn(make_float2(p.x, p.y), v0, o[r]);
+                    o[r] = __ffma2_rn(make_float2(p.z, p.w), v1, o[r]);
                 }
             }
         }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) sm.sh.o[0][8 * half + r][col] = o[r];
+        for (int r = 0; r < 8; ++r) sm.sh.o[0][8 * half + r][col] = o[r].x + o[r].y;
         if (lane == 0)
 #pragma unroll
             for (int r = 0; r < 4; ++r) sm.sh.m[0][4 * warp + r] = m[r], sm.sh.l[0][4 * warp + r] = l[r];
