@@ -49,42 +49,45 @@ __device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr, uint32_t ran
 __device__ __forceinline__ void store_out(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_out(float* o, float v) { *o = v; }
 
-// Shares of 16 rows: each with its maximum (in log2 units), its sum of exponentials and its unnormalised
+// Shares of a tile's rows: each with its maximum (in log2 units), its sum of exponentials and its unnormalised
 // output.  A share without keys has the maximum -inf and is left out.
+template <int SHARES, int ROWS, int THREADS>
 struct Shares {
-    float o[kXWarps][kXRows][kHd + 4];
-    float m[kXWarps][kXRows], l[kXWarps][kXRows];
+    static constexpr int kThreads = THREADS, kDims = ROWS * kHd / THREADS;   // a thread joins kDims dimensions of a row
+    float o[SHARES][ROWS][kHd + 4];
+    float m[SHARES][ROWS], l[SHARES][ROWS];
 };
 
 // Join the warps' shares (into share 0, and those of a cluster's CTAs then) and write the rows.  n: rows of the tile; row r
 // is written to dst(r).
-template <typename Elem, bool CLUSTER, typename Dst>
-__device__ __forceinline__ void join_shares(Shares& s, int shares, int splits, int n, Dst dst)
+template <typename Elem, bool CLUSTER, typename AllShares, typename Dst>
+__device__ __forceinline__ void join_shares(AllShares& s, int shares, int splits, int n, Dst dst)
 {
-    const int tid = threadIdx.x, r = tid >> 3, d0 = (tid & 7) * 8;   // a thread: a row, eight dimensions
+    constexpr int W = AllShares::kDims;
+    const int tid = threadIdx.x, r = tid / (kHd / W), d0 = tid % (kHd / W) * W;
     __syncthreads();
     float m = -INFINITY;
     for (int w = 0; w < shares; ++w)
         if (s.l[w][r] != 0.f) m = fmaxf(m, s.m[w][r]);
-    float l = 0.f, o[8] = {};
+    float l = 0.f, o[W] = {};
     for (int w = 0; w < shares; ++w) {
         if (s.l[w][r] == 0.f) continue;   // no keys
         const float f = exp2f(s.m[w][r] - m);
         l += s.l[w][r] * f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += s.o[w][r][d0 + i] * f;
+        for (int i = 0; i < W; ++i) o[i] += s.o[w][r][d0 + i] * f;
     }
     if constexpr (CLUSTER) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s.o[0][r][d0 + i] = o[i];
-        if ((tid & 7) == 0) s.m[0][r] = m, s.l[0][r] = l;
+        for (int i = 0; i < W; ++i) s.o[0][r][d0 + i] = o[i];
+        if (d0 == 0) s.m[0][r] = m, s.l[0][r] = l;
         cluster_sync();
         uint32_t rank;
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
         // four dimensions of a row at a time, dealt out over the cluster's threads; every remote load of a step on the
         // way at once
-        for (int i = tid * splits + rank; i < n * (kHd / 4); i += kXThreads * splits) {
+        for (int i = tid * splits + rank; i < n * (kHd / 4); i += AllShares::kThreads * splits) {
             const int row = i / (kHd / 4), d = i % (kHd / 4) * 4;
             float lp[kXSplits], mp[kXSplits], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -116,13 +119,14 @@ __device__ __forceinline__ void join_shares(Shares& s, int shares, int splits, i
             const float f = l == 0.f ? 0.f : 1.f / l;
             Elem* to = static_cast<Elem*>(dst(r)) + d0;
             if constexpr (sizeof(Elem) == 2) {
+                static_assert(W == 8);
                 uint4 w;
                 w.x = pack_bf16(o[0] * f, o[1] * f), w.y = pack_bf16(o[2] * f, o[3] * f);
                 w.z = pack_bf16(o[4] * f, o[5] * f), w.w = pack_bf16(o[6] * f, o[7] * f);
                 *reinterpret_cast<uint4*>(to) = w;
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) to[i] = o[i] * f;
+                for (int i = 0; i < W; ++i) to[i] = o[i] * f;
             }
         }
         __syncthreads();
@@ -156,6 +160,13 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until all but the last LEFT groups of the thread's copies have arrived.
+template <int LEFT>
+__device__ __forceinline__ void copies_there()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
 
 // NT: eights of rows; P^T comes from S^T by two 8 x 8 transpositions.
 template <bool PAGED, int NT, bool CLUSTER>
@@ -164,7 +175,8 @@ __global__ void __launch_bounds__(kXThreads, kXCtas) cross_few_kernel(const Cros
     using Elem = __nv_bfloat16;
     constexpr int RT = 8 * NT;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Shares& s_sh = *reinterpret_cast<Shares*>(smem_raw);   // once the rings are done with
+    using WarpShares = Shares<kXWarps, kXRows, kXThreads>;
+    WarpShares& s_sh = *reinterpret_cast<WarpShares*>(smem_raw);   // once the rings are done with
     grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const CrossItem it(a, blockIdx.x);
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(kXThreads, kXCtas) cross_few_kernel(const Cros
             copy16(to + k_at(r, piece), kb + from * a.k_stride + 8 * piece, at >= 0);
             copy16(to + v_at(r, piece), vb + from * a.v_stride + 8 * piece, at >= 0);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        copies_sent();
     };
     for (int tile = it.tile; tile * RT < rows; tile += a.tiles) {
         const int r0 = tile * RT, n = min(rows - r0, RT);
@@ -282,7 +294,7 @@ __global__ void __launch_bounds__(kXThreads, kXCtas) cross_few_kernel(const Cros
         for (int i = 0; i < kXRing - 1; ++i) request(row[i], i);
         int next = row[kXRing - 1], slot = 0;
         for (int chunk = first + warp; chunk < last; chunk += kXWarps) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kXRing - 2) : "memory");
+            copies_there<kXRing - 2>();
             __syncwarp();   // every lane's copies
             const uint8_t* from = ring + slot * kXChunk;
             auto get = [&](int at) { return *reinterpret_cast<const uint4*>(from + at); };
@@ -293,7 +305,7 @@ __global__ void __launch_bounds__(kXThreads, kXCtas) cross_few_kernel(const Cros
             work(chunk, kv);
             if (++slot == kXRing) slot = 0;
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        copies_there<0>();
         __syncthreads();   // the rings become the shares' place
 #pragma unroll
         for (int e = 0; e < NT; ++e)
@@ -316,38 +328,64 @@ __global__ void __launch_bounds__(kXThreads, kXCtas) cross_few_kernel(const Cros
     if (err) atomicOr(a.status, err);
 }
 
-// fp32: tiles of 16 rows and 64 keys in shared memory, fp32 products (no TF32).  A thread has one key of eight rows
-// of q . k, then one dimension of eight rows of P . V.
-constexpr int kFKeys = 64;
-
-struct CrossF32Smem {
-    float q[kXRows][kHd];
-    float k[kFKeys][kHd + 4], v[kFKeys][kHd + 4];
-    float p[kXRows][kFKeys];
-    float f[kXRows];
-    Shares sh;
+// fp32: a tile's rows and some keys in shared memory, fp32 products (no TF32).  RG warps have eight rows each, and the 4 / RG
+// groups of them each their own 32 KL of the keys, joined at the end.  A lane has KL keys of the eight rows of q . k, then two
+// dimensions of the eight rows of P . V: of 16 bytes that all lanes load alike (q, P) a warp takes 16 from shared memory, of
+// others 512, and with two keys to a lane these are as long as the products.  The next keys are on the way while the weights
+// are worked on, the next values during the scores.
+template <int RG, int KL>
+struct CrossF32 {
+    static constexpr int kRows = 8 * RG, kGroups = kXWarps / RG, kWarpKeys = 32 * KL, kKeys = kGroups * kWarpKeys;
+    static constexpr int kLoad = kKeys / kXWarps;   // keys that a warp loads: its own, where RG is 1
+    static_assert(kLoad <= 32);
+    struct Smem {
+        float q[kRows][kHd];
+        float k[kKeys][kHd + 4], v[kKeys][kHd];   // the padding puts eight keys' 16 bytes side by side into different banks
+        float p[kXWarps][8][kWarpKeys];
+        Shares<kGroups, kRows, kXThreads> sh;
+    };
 };
 
-template <bool PAGED>
+template <bool PAGED, int RG, int KL>
 __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs a)
 {
+    using F = CrossF32<RG, KL>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    CrossF32Smem& sm = *reinterpret_cast<CrossF32Smem*>(smem_raw);
+    typename F::Smem& sm = *reinterpret_cast<typename F::Smem*>(smem_raw);
     grid_dep_wait();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rg = warp % RG, kg = warp / RG;
     const CrossItem it(a, blockIdx.x);
     unsigned err = 0;
     const CrossSeq t(a, it.s, err);
     const int rows = t.nq * a.G;
-    const int chunks = (t.nk + kFKeys - 1) / kFKeys, share = (chunks + a.splits - 1) / a.splits;
+    const int chunks = (t.nk + F::kKeys - 1) / F::kKeys, share = (chunks + a.splits - 1) / a.splits;
     const int first = it.split * share, last = min(first + share, chunks);
     const float* kb = static_cast<const float*>(a.k) + it.h * kHd;
     const float* vb = static_cast<const float*>(a.v) + it.h * kHd;
-    const int col = tid & 63, half = tid >> 6;   // key, then dimension; rows 8 half .. 8 half + 7
+    const int key0 = kg * F::kWarpKeys;   // of a chunk
+    auto sync = [&] { RG == 1 ? __syncwarp() : __syncthreads(); };   // the warps that share keys
 
-    for (int tile = it.tile; tile * kXRows < rows; tile += a.tiles) {
-        const int r0 = tile * kXRows, n = min(rows - r0, kXRows);
-        for (int i = tid; i < kXRows * kHd / 4; i += kXThreads) {
+    for (int tile = it.tile; tile * F::kRows < rows; tile += a.tiles) {
+        const int r0 = tile * F::kRows, n = min(rows - r0, F::kRows);
+        const bool has_rows = 8 * rg < n;
+        auto row_of = [&](int chunk) {   // of key `lane` of those that the warp loads; -1: none
+            const int j = chunk * F::kKeys + warp * F::kLoad + (lane & (F::kLoad - 1));
+            return chunk < last && j < t.nk ? cross_row<PAGED>(a, t, it.s, j, err) : -1;
+        };
+        auto request = [&](auto& to, const float* from, long long stride, int row, bool any) {
+            if (any)
+#pragma unroll
+                for (int u = 0; u < F::kLoad / 2; ++u) {
+                    const int i = 2 * u + (lane >> 4), part = 4 * (lane & 15), r = __shfl_sync(0xffffffffu, row, i);
+                    copy16(smem_addr(&to[warp * F::kLoad + i][part]), from + max(r, 0) * stride + part, r >= 0);
+                }
+            copies_sent();
+        };
+        int row = row_of(first);
+        request(sm.k, kb, a.k_stride, row, first < last);
+        request(sm.v, vb, a.v_stride, row, first < last);
+        row = row_of(first + 1);
+        for (int i = tid; i < F::kRows * kHd / 4; i += kXThreads) {
             const int r = i >> 4, R = r0 + r, qi = R / a.G;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < n)
@@ -355,106 +393,111 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs
                                                           (it.h * a.G + R - qi * a.G) * kHd) + (i & 15));
             *reinterpret_cast<float4*>(&sm.q[r][4 * (i & 15)]) = x;
         }
-        float2 o[8] = {};   // sums over even and odd keys
-        float m[4], l[4];   // of rows 4 warp .. 4 warp + 3, the same in every lane
+        __syncthreads();
+        float2 o[8][2] = {};   // dimensions 2 lane and 2 lane + 1, sums over even and odd keys
+        float m[8], l[8];      // the maximum, the same in every lane; the lane's part of the sum
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.f;
-        // the next 64 keys are on the way in registers while these are worked on: a thread has 16 bytes of eight of them
-        float4 kn[8], vn[8];
-        auto request = [&](int chunk) {
-            if (chunk >= last) return;
-            int row[8];   // every page looked up before the first key is asked for
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int j = chunk * kFKeys + 8 * u + (tid >> 4), r = cross_row<PAGED>(a, t, it.s, min(j, t.nk - 1), err);
-                row[u] = j < t.nk ? r : -1;
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const long long r = max(row[u], 0);   // a row without a key is read and not used
-                kn[u] = __ldg(reinterpret_cast<const float4*>(kb + r * a.k_stride) + (tid & 15));
-                vn[u] = __ldg(reinterpret_cast<const float4*>(vb + r * a.v_stride) + (tid & 15));
-                if (row[u] < 0) kn[u] = vn[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-        };
-        request(first);
+        for (int r = 0; r < 8; ++r) m[r] = -INFINITY, l[r] = 0.f;
         for (int chunk = first; chunk < last; ++chunk) {
-            const int j0 = chunk * kFKeys;
-            __syncthreads();
+            const int left = t.nk - chunk * F::kKeys - key0;   // keys from the warp's first on
+            const bool works = has_rows && left > 0;
+            copies_there<1>();
+            sync();   // the keys are there
+            float s[8][KL];
+            if (works) {
+                float2 s2[8][KL] = {};   // sums of even and odd terms: two products an instruction
+#pragma unroll 2
+                for (int d = 0; d < kHd; d += 4) {
+                    float4 k[KL];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                *reinterpret_cast<float4*>(&sm.k[8 * u + (tid >> 4)][4 * (tid & 15)]) = kn[u];
-                *reinterpret_cast<float4*>(&sm.v[8 * u + (tid >> 4)][4 * (tid & 15)]) = vn[u];
+                    for (int i = 0; i < KL; ++i) k[i] = *reinterpret_cast<const float4*>(&sm.k[key0 + lane + 32 * i][d]);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float4 q = *reinterpret_cast<const float4*>(&sm.q[8 * rg + r][d]);
+#pragma unroll
+                        for (int i = 0; i < KL; ++i) {
+                            s2[r][i] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k[i].x, k[i].y), s2[r][i]);
+                            s2[r][i] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k[i].z, k[i].w), s2[r][i]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int i = 0; i < KL; ++i) s[r][i] = lane + 32 * i < left ? (s2[r][i].x + s2[r][i].y) * a.c : -INFINITY;
             }
-            __syncthreads();
-            request(chunk + 1);
-            // sums of even and odd terms side by side: two products an instruction
-            float2 s2[8] = {};
-#pragma unroll 4
-            for (int d = 0; d < kHd; d += 4) {
-                const float4 k = *reinterpret_cast<const float4*>(&sm.k[col][d]);
+            sync();   // the keys are done with
+            request(sm.k, kb, a.k_stride, row, chunk + 1 < last);
+            if (works) {
+                float x[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const float4 q = *reinterpret_cast<const float4*>(&sm.q[8 * half + r][d]);
-                    s2[r] = __ffma2_rn(make_float2(q.x, q.y), make_float2(k.x, k.y), s2[r]);
-                    s2[r] = __ffma2_rn(make_float2(q.z, q.w), make_float2(k.z, k.w), s2[r]);
+                    x[r] = s[r][0];
+#pragma unroll
+                    for (int i = 1; i < KL; ++i) x[r] = fmaxf(x[r], s[r][i]);
                 }
-            }
-            float s[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) s[r] = s2[r].x + s2[r].y;
+                for (int e = 16; e; e >>= 1)
 #pragma unroll
-            for (int r = 0; r < 8; ++r) sm.p[8 * half + r][col] = j0 + col < t.nk ? s[r] * a.c : -INFINITY;
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float* p = sm.p[4 * warp + r];
-                const float x0 = p[lane], x1 = p[lane + 32];
-                float x = fmaxf(x0, x1);
-#pragma unroll
-                for (int e = 16; e; e >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, e));
-                x = fmaxf(x, m[r]);
-                const float f = exp2f(m[r] - x), e0 = exp2f(x0 - x), e1 = exp2f(x1 - x);
-                float sum = e0 + e1;
-#pragma unroll
-                for (int e = 16; e; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
-                m[r] = x;
-                l[r] = l[r] * f + sum;
-                p[lane] = e0;
-                p[lane + 32] = e1;
-                if (lane == 0) sm.f[4 * warp + r] = f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < 8; ++r) o[r].x *= sm.f[8 * half + r], o[r].y *= sm.f[8 * half + r];
-#pragma unroll 4
-            for (int j = 0; j < kFKeys; j += 4) {
-                const float2 v0 = make_float2(sm.v[j][col], sm.v[j + 1][col]), v1 = make_float2(sm.v[j + 2][col], sm.v[j + 3][col]);
+                    for (int r = 0; r < 8; ++r) x[r] = fmaxf(x[r], __shfl_xor_sync(0xffffffffu, x[r], e));
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    const float4 p = *reinterpret_cast<const float4*>(&sm.p[8 * half + r][j]);
-                    o[r] = __ffma2_rn(make_float2(p.x, p.y), v0, o[r]);
-                    o[r] = __ffma2_rn(make_float2(p.z, p.w), v1, o[r]);
+                    x[r] = fmaxf(x[r], m[r]);
+                    const float f = exp2f(m[r] - x[r]);
+                    m[r] = x[r];
+                    l[r] *= f;
+#pragma unroll
+                    for (int i = 0; i < KL; ++i) {
+                        const float p = exp2f(s[r][i] - x[r]);
+                        l[r] += p;
+                        sm.p[warp][r][lane + 32 * i] = p;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) o[r][e].x *= f, o[r][e].y *= f;
                 }
             }
+            copies_there<1>();
+            sync();   // the weights and the values are there
+            if (works) {
+#pragma unroll 2
+                for (int j = 0; j < min(F::kWarpKeys, left); j += 4) {
+                    float2 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float2*>(&sm.v[key0 + j + i][2 * lane]);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float4 p = *reinterpret_cast<const float4*>(&sm.p[warp][r][j]);
+                        o[r][0] = __ffma2_rn(make_float2(p.x, p.y), make_float2(v[0].x, v[1].x), o[r][0]);
+                        o[r][1] = __ffma2_rn(make_float2(p.x, p.y), make_float2(v[0].y, v[1].y), o[r][1]);
+                        o[r][0] = __ffma2_rn(make_float2(p.z, p.w), make_float2(v[2].x, v[3].x), o[r][0]);
+                        o[r][1] = __ffma2_rn(make_float2(p.z, p.w), make_float2(v[2].y, v[3].y), o[r][1]);
+                    }
+                }
+            }
+            sync();   // the values are done with
+            request(sm.v, vb, a.v_stride, row, chunk + 1 < last);
+            row = row_of(chunk + 2);
         }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) sm.sh.o[0][8 * half + r][col] = o[r].x + o[r].y;
-        if (lane == 0)
+        for (int r = 0; r < 8; ++r) {
+            *reinterpret_cast<float2*>(&sm.sh.o[kg][8 * rg + r][2 * lane]) = make_float2(o[r][0].x + o[r][0].y, o[r][1].x + o[r][1].y);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sm.sh.m[0][4 * warp + r] = m[r], sm.sh.l[0][4 * warp + r] = l[r];
-        join_shares<float, true>(sm.sh, 1, a.splits, n, [&](int r) {
+            for (int e = 16; e; e >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], e);
+            if (lane == 0) sm.sh.m[kg][8 * rg + r] = m[r], sm.sh.l[kg][8 * rg + r] = l[r];
+        }
+        join_shares<float, true>(sm.sh, F::kGroups, a.splits, n, [&](int r) {
             const int R = r0 + r, i = R / a.G;
             return static_cast<float*>(a.out) + (static_cast<long long>(t.q0 + i) * a.H + it.h * a.G + R - i * a.G) * kHd;
         });
     }
+    copies_there<0>();
     grid_dep_trigger();
     if (err) atomicOr(a.status, err);
 }
 
 // --------------------------------------------------------------------------- host
 
-int g_smem_done_x32[2][64], g_smem_done_few[8][64];
+int g_smem_done_x32[6][64], g_smem_done_few[8][64];
 
 constexpr int kXMaxSeqs = 65536, kXMaxHeads = 1024;
 
@@ -466,23 +509,33 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     if (!f32 && static_cast<long long>(max_q) * a.G > kXRows && cross_tc_takes(a)) return cross_tc(a, max_q, stream);
     // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
     const long long max_rows = static_cast<long long>(max_q) * a.G, items = static_cast<long long>(a.N) * a.Hkv;
-    const int tile_rows = !f32 && max_rows <= 8 ? 8 : kXRows;
+    // fp32: 32 rows to a tile where those fill the SMs (64 utterances, 200 rows over 775 states: 764 us, 922 with 16), 16 where
+    // they do not (5 utterances, 20 rows of 4 heads over 170 states: 8.5 us, 12.9 with 32)
+    const int tile_rows = max_rows <= 8 ? 8 : f32 && max_rows > kXRows && items * ((max_rows + 31) / 32) >= sms ? 32 : kXRows;
     long long tiles = (max_rows + tile_rows - 1) / tile_rows;
     while (tiles > 1 && items * tiles > (1 << 24)) tiles = (tiles + 1) / 2;
     if (items * tiles > 0x7fffffffLL / 8) return OASR_ERR_UNSUPPORTED;
     a.tiles = static_cast<int>(tiles);
     // as many shares of the keys as two CTAs an SM leave room for, while each has keys for its four warps (64 rows of a key head
     // over 1500 keys: 8.8 us with four shares, 13.4 with seven, which a wave of clusters does not take)
-    const int least = f32 ? kFKeys : 2 * kXWarps * kXKeys;
-    const long long room = 2LL * sms / (items * tiles), wanted = max_k / least;
+    // (fp32, as many as there are tiles of keys: 192 keys 6.9 us, 9.3 where a share had two)
+    const int least = !f32 ? 2 * kXWarps * kXKeys : tile_rows == 32 ? CrossF32<4, 2>::kKeys : CrossF32<2, 2>::kKeys;
+    static_assert(CrossF32<1, 1>::kKeys == CrossF32<2, 2>::kKeys);
+    const long long room = 2LL * sms / (items * tiles), wanted = (static_cast<long long>(max_k) + (f32 ? least - 1 : 0)) / least;
     a.splits = static_cast<int>(room < 1 || wanted < 1 ? 1 : room < wanted ? room : wanted);
     if (a.splits > kXSplits) a.splits = kXSplits;
     const dim3 grid(static_cast<unsigned>(items * tiles * a.splits)), block(kXThreads);
-    const int smem = f32 ? static_cast<int>(sizeof(CrossF32Smem)) : 0;
     if (f32) {
-        auto kern = paged ? cross_f32_kernel<true> : cross_f32_kernel<false>;
-        if (!ensure_smem(kern, smem, g_smem_done_x32[paged])) return OASR_ERR_CUDA;
-        return launch_pdl_cluster(kern, grid, block, smem, a.splits, stream, static_cast<const CrossArgs>(a));
+        auto by_rows = [&](auto rg, auto kl) {
+            constexpr int smem = sizeof(typename CrossF32<rg.value, kl.value>::Smem);
+            auto kern = paged ? cross_f32_kernel<true, rg.value, kl.value> : cross_f32_kernel<false, rg.value, kl.value>;
+            if (!ensure_smem(kern, smem, g_smem_done_x32[2 * (rg.value / 2) + paged])) return OASR_ERR_CUDA;
+            return launch_pdl_cluster(kern, grid, block, smem, a.splits, stream, static_cast<const CrossArgs>(a));
+        };
+        constexpr std::integral_constant<int, 1> one;
+        constexpr std::integral_constant<int, 2> two;
+        constexpr std::integral_constant<int, 4> four;
+        return tile_rows == 8 ? by_rows(one, one) : tile_rows == kXRows ? by_rows(two, two) : by_rows(four, two);
     }
     auto by_pages = [&](auto nt, auto cluster) {
         constexpr int ring = kXWarps * kXRing * kXChunk;
