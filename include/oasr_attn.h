@@ -381,8 +381,9 @@ oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_
  *   packed: the keys [cu_k[s], cu_k[s + 1]) of k and v;
  *   paged:  the first cache_seqlens[s] positions of block_table[s], in pools [num_blocks, block_size, Hkv, 64].
  *     out[i][h] = sum_j softmax_j(scale q[i][h] . k[j][h / G]) v[j][h / G],   G = H / Hkv
- * No position term and no mask but the lengths.  A sequence without keys has zeros; rows of out that no sequence
- * owns keep what they held.  Rows of q, k and v are q_stride, k_stride, v_stride values apart (heads are
+ * No position term and no mask but the lengths.  A sequence without keys has zeros, a key whose score is -inf the
+ * weight zero, and a row of such scores alone zeros; rows of out that no sequence owns keep what they held.  Rows
+ * of q, k and v are q_stride, k_stride, v_stride values apart (heads are
  * contiguous: k and v may be the halves of one product's rows); out is [total_q, H, 64].
  * max_q and max_k are the lengths that the launch is laid out for: a longer sequence is right, and slower.
  * Requirements: D = 64; H a multiple of Hkv and at most 1024; num_seqs at most 65536; 0 < scale <= 2e38; pointers

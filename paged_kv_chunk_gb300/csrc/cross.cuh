@@ -5,13 +5,16 @@
 //
 // G = H / Hkv query heads share a key head.  Row R of a sequence's (key head) problem is query R / G,
 // head R % G of the group: the queries of all hypotheses and of all heads of a group are rows of one
-// tile against the same keys.  A sequence without keys gets zeros.
+// tile against the same keys.  A sequence without keys gets zeros, and so does a row whose every score is -inf.
 #pragma once
 
 #include "host_common.h"
 #include "ptx.cuh"
 
 namespace oasr {
+
+// A row's maximum before its first key: lowest of the finite values, so that scores of -inf have the weight zero.
+constexpr float kLowest = -3.402823466e38f;
 
 struct CrossArgs {
     const void *q, *k, *v;

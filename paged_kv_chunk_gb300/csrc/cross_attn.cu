@@ -50,7 +50,7 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* o, float v) { *o = __fl
 __device__ __forceinline__ void store_out(float* o, float v) { *o = v; }
 
 // Shares of a tile's rows: each with its maximum (in log2 units), its sum of exponentials and its unnormalised
-// output.  A share without keys has the maximum -inf and is left out.
+// output.  A share without keys, or with scores of -inf alone, has the sum zero and is left out.
 template <int SHARES, int ROWS, int THREADS>
 struct Shares {
     static constexpr int kThreads = THREADS, kDims = ROWS * kHd / THREADS;   // a thread joins kDims dimensions of a row
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kXThreads, kXCtas) cross_few_kernel(const Cros
         float o[NT][4][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
-            m[e][0] = m[e][1] = -INFINITY, l[e][0] = l[e][1] = 0.f;
+            m[e][0] = m[e][1] = kLowest, l[e][0] = l[e][1] = 0.f;
 #pragma unroll
             for (int d = 0; d < 4; ++d) o[e][d][0] = o[e][d][1] = o[e][d][2] = o[e][d][3] = 0.f;
         }
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs
         float2 o[8][2] = {};   // dimensions 2 lane and 2 lane + 1, sums over even and odd keys
         float m[8], l[8];      // the maximum, the same in every lane; the lane's part of the sum
 #pragma unroll
-        for (int r = 0; r < 8; ++r) m[r] = -INFINITY, l[r] = 0.f;
+        for (int r = 0; r < 8; ++r) m[r] = kLowest, l[r] = 0.f;
         for (int chunk = first; chunk < last; ++chunk) {
             const int left = t.nk - chunk * F::kKeys - key0;   // keys from the warp's first on
             const bool works = has_rows && left > 0;

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
                     }
                     const float top = fmax3(fmax3(y[0], y[1], y[2]), fmax3(y[3], y[4], y[5]), fmaxf(y[6], y[7])) * a.c;
                     if (st == 0) {
-                        m = top;
+                        m = fmaxf(top, kLowest);
                     } else {
                         const bool grown = top > m + 8.f;
                         if (__any_sync(0xffffffffu, grown)) {
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kCThreads, 2) cross_tc_kernel(const __grid_con
             if (!ok || !(ok = wait(bar_pv, (g - 1) & 1))) break;
             tc_fence_after();
             if (32 * warp < live) {
-                const float f = 1.f / l;
+                const float f = l == 0.f ? 0.f : 1.f / l;   // scores of -inf alone
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t w[32];

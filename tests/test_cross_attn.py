@@ -276,6 +276,31 @@ def test_values_that_are_not_finite(n):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 2, 8, 20, 150])
+def test_scores_of_minus_infinity(n, dtype):
+    """Keys whose scores are -inf have no weight, wherever in a tile they lie and if they fill it; a row of them alone
+    has zeros."""
+    lens = [140, 129, 321, 5, 65, 400]
+    gone = [[0, 139], [128], list(range(260)), list(range(5)), [64], list(range(17, 399))]
+    c = Case([n] * 6, lens, 2, 1, dtype, 12)
+    c.q[..., 5] = c.q[..., 5].abs() + 0.25
+    c.k = c.k.clone()
+    for s, js in enumerate(gone):
+        for j in js:
+            c.k[int(c.cu_k[s]) + j, :, 5] = -math.inf
+            c.kp[int(c.table[s, j // c.bs]), j % c.bs, :, 5] = -math.inf
+    x = c.cuda()
+    for out in (c.packed(x), c.paged(x)):
+        for s, js in enumerate(gone):
+            rows = slice(n * s, n * s + n)
+            keys = [int(c.cu_k[s]) + j for j in range(lens[s]) if j not in js]
+            want, tol = reference(c.q[rows], c.k[keys].repeat_interleave(2, 1), c.v[keys].repeat_interleave(2, 1), 0.125,
+                                  dtype == "bf16")
+            assert bool(((out[rows].double().cpu() - want).abs() <= tol).all()), s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [3, 140])
 def test_rows_behind_the_last_sequence(n, dtype):
     c = Case([n, n], [200, 60], 2, 1, dtype, 3, spare=150)
