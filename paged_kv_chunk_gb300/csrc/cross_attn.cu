@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(kXThreads, 3) cross_f32_kernel(const CrossArgs
         }
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            *reinterpret_cast<float2*>(&sm.sh.o[kg][8 * rg + r][2 * lane]) = make_float2(o[r][0].x + o[r][0].y, o[r][1].x + o[r][1].y);
+            *reinterpret_cast<float2*>(&sm.sh.o[kg][8 * rg + r][2 * lane]) =
+                make_float2(o[r][0].x + o[r][0].y, o[r][1].x + o[r][1].y);
 #pragma unroll
             for (int e = 16; e; e >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], e);
             if (lane == 0) sm.sh.m[kg][8 * rg + r] = m[r], sm.sh.l[kg][8 * rg + r] = l[r];
@@ -506,9 +507,13 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     const int sms = sm_count();
     if (!sms || !a.status) return OASR_ERR_CUDA;
     const bool f32 = dt == OASR_F32, paged = a.table != nullptr;
-    if (!f32 && static_cast<long long>(max_q) * a.G > kXRows && cross_tc_takes(a)) return cross_tc(a, max_q, stream);
-    // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
     const long long max_rows = static_cast<long long>(max_q) * a.G, items = static_cast<long long>(a.N) * a.Hkv;
+    // Tiles of 128 rows where the tiles of 16 are more than two an SM: few tiles leave SMs idle, and their keys can be shared by
+    // a cluster (8 heads over 1500 keys: 32 rows 8.4 us, 15.0 in tiles of 128; 128 rows 9.4 and 16.5; 448 rows, 224 tiles, 16.5
+    // and 16.6; 256 tiles 18.0 and 17.3).
+    if (!f32 && max_rows > kXRows && items * ((max_rows + kXRows - 1) / kXRows) > 2LL * sms && cross_tc_takes(a))
+        return cross_tc(a, max_q, stream);
+    // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
     // fp32: 32 rows to a tile where those fill the SMs (64 utterances, 200 rows over 775 states: 764 us, 922 with 16), 16 where
     // they do not (5 utterances, 20 rows of 4 heads over 170 states: 8.5 us, 12.9 with 32)
     const int tile_rows = max_rows <= 8 ? 8 : f32 && max_rows > kXRows && items * ((max_rows + 31) / 32) >= sms ? 32 : kXRows;

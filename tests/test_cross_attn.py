@@ -396,6 +396,53 @@ def test_captured_streams_and_side_by_side(n, dtype):
         y.check(w)
 
 
+@pytest.fixture
+def wide(monkeypatch):
+    """Calls laid out for 10000 queries a sequence: tiles of 128 rows, also where the sequences are short and few."""
+    packed, paged = capi.oasr_cross_attn_packed, capi.oasr_cross_attn_paged
+    monkeypatch.setattr(capi, "oasr_cross_attn_packed", lambda q, k, v, cu_q, cu_k, max_q, *a, **kw:
+                        packed(q, k, v, cu_q, cu_k, 10000, *a, **kw))
+    monkeypatch.setattr(capi, "oasr_cross_attn_paged", lambda q, kp, vp, table, lens, cu_q, max_q, *a, **kw:
+                        paged(q, kp, vp, table, lens, cu_q, 10000, *a, **kw))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nq,nk,H,Hkv", SHAPES)
+def test_wide(wide, nq, nk, H, Hkv):
+    test_cross(nq, nk, H, Hkv, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bs", [1, 3, 8, 24, 32, 64, 128, 256, 512])
+def test_wide_page_sizes(wide, bs):
+    test_page_sizes(bs, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("test", [
+    lambda: test_peaked_and_flat([200, 70], 6.0, 0.125, "bf16"), lambda: test_peaked_and_flat([200, 70], 0.05, 3.0, "bf16"),
+    lambda: test_peaked_and_flat([150], 1.0, 1e-6, "bf16"), lambda: test_rising_scores(180, "bf16"),
+    lambda: test_values_that_are_not_finite(150), lambda: test_scores_of_minus_infinity(20, "bf16"),
+    lambda: test_scores_of_minus_infinity(150, "bf16"), lambda: test_rows_behind_the_last_sequence(140, "bf16"),
+    lambda: test_bad_blocks_and_offsets(150, "bf16"), lambda: test_pools_past_4_gb(200),
+    lambda: test_captured_streams_and_side_by_side(300, "bf16")],
+    ids=["peaked", "flat", "tiny", "rising", "nan", "inf20", "inf150", "behind", "bad", "past4gb", "captured"])
+def test_wide_edges(wide, test):
+    test()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,keys", [(17, 1500), (32, 333), (128, 1500), (448, 700)])
+def test_few_tiles_of_many_rows(rows, keys):
+    """Many rows of one utterance: tiles of 16 rows, their keys shared by a cluster, and the wide form agree."""
+    for H, Hkv in ((8, 8), (4, 2)):
+        c = Case([rows], [keys], H, Hkv, "bf16", rows)
+        x = c.cuda()
+        for kw in (dict(), dict(max_q=10000)):
+            c.check(c.packed(x, **kw))
+            c.check(c.paged(x, **kw))
+
+
 @pytest.mark.gpu
 def test_decoder_step_together():
     """The operators as a server uses them: pages for two utterances, their states' keys and values by an e4m3 product
