@@ -11,7 +11,7 @@
 // accumulators per block.  Products of two e4m3 values are exact in fp32.
 //
 // What bounds a large product is what it copies into shared memory: 40 KB a step of 128 of K and 128 x 192 outputs, 12 TB/s
-// over the GPU at 65537 x 1024 x 512 (43 us, 1.6 PFLOP/s, 168 MB of HBM traffic); 8191 x 4096 x 1024 takes 37 us (1.86 PFLOP/s;
+// over the GPU at 65537 x 1024 x 512 (43 us, 1.6 PFLOP/s, 168 MB of HBM traffic); 8191 x 4096 x 1024 takes 36 us (1.89 PFLOP/s;
 // the int8 product 51).  Pairs of CTAs on 256 x 192 (cta_group::2), half of w each, were right and slower: 69 us.
 #include <type_traits>
 
@@ -570,8 +570,8 @@ oasr_status dispatch_e4(const E4Problem& p, void* out, cudaStream_t stream)
     constexpr int s = sizeof(Elem) == 4 ? 3 : 0;
     // Tile: the one of the least estimated time.  A step of 128 of K costs 470 ns in 128 x 192, 430 in 128 x 128 and 380 in
     // 128 x 64 (the copies into shared memory are the cost), a tile's hand-over 250, 100 and 50, the last epilogue 1000, 700
-    // and 400.  Bf16 results, in this order: 8191 x 4096 x 1024 37.0, 44.5 and 75.5 us; 4096 x 512 x 2048 9.5, 9.2 and 13.6;
-    // 1024 x 768 x 256 5.8, 5.3 and 4.4.
+    // and 400.  Bf16 results, in this order: 8191 x 4096 x 1024 36.4, 43.4 and 74.9 us; 4096 x 512 x 2048 9.2, 8.8 and 13.4;
+    // 1024 x 768 x 256 4.3, 3.9 and 3.8.
     constexpr struct { int n, step, tile, end; } kinds[] = {{192, 470, 250, 1000}, {128, 430, 100, 700}, {64, 380, 50, 400}};
     int best = 0;
     long long least = 0x7fffffffffffffffLL;
