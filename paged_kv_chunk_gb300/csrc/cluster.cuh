@@ -13,6 +13,25 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// What CTA `rank` of the cluster has in shared memory where `addr` is here.
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr, uint32_t rank)
+{
+    float v;
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr, uint32_t rank)
+{
+    float4 v;
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 // Releases in the cluster what happened to this CTA's shared memory before it; a release of all memory at that
 // scope waits for global memory's writes as well (0.6 us measured).
 __device__ __forceinline__ void fence_release_smem_cluster()

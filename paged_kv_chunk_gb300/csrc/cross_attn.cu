@@ -28,24 +28,6 @@ constexpr int kXWarps = 4, kXThreads = 32 * kXWarps, kXRows = 16, kXKeys = 16;
 constexpr int kXRing = 4, kXChunk = 4096, kXCtas = 3;   // chunks of a warp's ring, bytes of one; CTAs an SM
 constexpr int kXSplits = 8;   // CTAs of a cluster at most (the portable size)
 
-__device__ __forceinline__ float ld_shared_cluster(uint32_t addr, uint32_t rank)
-{
-    float v;
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float4 ld_shared_cluster4(uint32_t addr, uint32_t rank)
-{
-    float4 v;
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void store_out(__nv_bfloat16* o, float v) { *o = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_out(float* o, float v) { *o = v; }
 
@@ -85,9 +67,9 @@ __device__ __forceinline__ void join_shares(AllShares& s, int shares, int splits
         cluster_sync();
         uint32_t rank;
         asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-        // four dimensions of a row at a time, dealt out over the cluster's threads; every remote load of a step on the
-        // way at once
-        for (int i = tid * splits + rank; i < n * (kHd / 4); i += AllShares::kThreads * splits) {
+        // four dimensions of a row at a time, a run of them to each CTA; every remote load of a step on the way at once
+        const int run = (n * (kHd / 4) + splits - 1) / splits, end = min(n * (kHd / 4), static_cast<int>(rank + 1) * run);
+        for (int i = rank * run + tid; i < end; i += AllShares::kThreads) {
             const int row = i / (kHd / 4), d = i % (kHd / 4) * 4;
             float lp[kXSplits], mp[kXSplits], top = -INFINITY, sum = 0.f;
 #pragma unroll
