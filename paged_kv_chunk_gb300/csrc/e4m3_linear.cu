@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(256) linear_e4m3_few_kernel(const E4Problem p,
 // epilogue overlap the next tile's products.
 constexpr int kE4EpiWarps = 8, kE4ScaleWarps = 4, kE4Issuer = kE4EpiWarps + kE4ScaleWarps;
 constexpr int kE4Threads = 32 * (kE4Issuer + 2);
+constexpr int kE4Splits = 8;   // CTAs of a cluster at most (the portable size)
 
 template <int BN>
 struct E4Smem {
@@ -199,6 +200,8 @@ struct E4Smem {
     static constexpr int off_bar = off_bias + kE4EpiWarps * BN / 2 * 4;   // full, empty, scales full[2], free[2], acc full[2], free[2], drain
     static constexpr int off_misc = off_bar + (2 * stages + 9) * 8;
     static constexpr int bytes = off_misc + 16 + 1024;
+    static constexpr int part_row = BN + 4;                             // floats of a row of a split tile's sums, in the ring
+    static_assert(128 * part_row * 4 <= stages * tile);
     static constexpr int sb_cols = (BN + 127) / 128 * 4;                // columns of w's scales
     static constexpr int sf_cols = 4 + sb_cols, off_sf = 2 * BN;        // x's, then w's; two buffers
     static constexpr int used = off_sf + 2 * sf_cols;
@@ -208,8 +211,9 @@ struct E4Smem {
 struct E4Args {
     E4Problem p;
     void* out;
-    int nt, tiles, ksteps;
+    int nt, tiles;
     int by_tma;   // the output's rows suit TMA: stored by it
+    int splits, share;   // CTAs that share a tile's blocks of K, blocks of each
     unsigned* status;
 };
 
@@ -238,30 +242,30 @@ __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t* w)
                      : "memory");
 }
 
-// The scale bytes of blocks 4 g .. 4 g + 3 of rows first + 32 j + the lane, j < N; 2^0 for rows past the matrix and blocks past
+// The scale bytes of blocks b .. b + 3 of rows first + 32 j + the lane, j < N; 2^0 for rows past the matrix and blocks past
 // the row, whose values come as zeros.  Every load goes out before the first is used (a branch for each row had the
 // loads of one wait for the other's: 3 us a tile at K = 240).
 template <int N>
-__device__ __forceinline__ void scale_words(const uint8_t* s, int first, int rows, int kb, int g, uint32_t* w)
+__device__ __forceinline__ void scale_words(const uint8_t* s, int first, int rows, int kb, int b, uint32_t* w)
 {
     const int lane = threadIdx.x & 31;
     const uint8_t* p[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] = s + static_cast<long long>(min(first + 32 * j + lane, rows - 1)) * kb;
-    if (!((kb | static_cast<int>(reinterpret_cast<uintptr_t>(s))) & 3)) {
+    if (!((kb | b | static_cast<int>(reinterpret_cast<uintptr_t>(s))) & 3)) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p[j] + 4 * g));
+        for (int j = 0; j < N; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p[j] + b));
     } else {
         uint32_t byte[N][4];
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) byte[j][i] = __ldg(p[j] + min(4 * g + i, kb - 1));
+            for (int i = 0; i < 4; ++i) byte[j][i] = __ldg(p[j] + min(b + i, kb - 1));
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             w[j] = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[j] |= (4 * g + i < kb ? byte[j][i] : 0x7fu) << (8 * i);
+            for (int i = 0; i < 4; ++i) w[j] |= (b + i < kb ? byte[j][i] : 0x7fu) << (8 * i);
         }
     }
 #pragma unroll
@@ -269,7 +273,9 @@ __device__ __forceinline__ void scale_words(const uint8_t* s, int first, int row
         if (first + 32 * j + lane >= rows) w[j] = 0x7f7f7f7fu;
 }
 
-template <int BN, typename Elem>
+// SPLIT: the blocks of K of a CTA's one tile are shared by a cluster, whose sums meet in shared memory: each CTA adds up
+// its part of the tile from all of them, in their order.
+template <int BN, typename Elem, bool SPLIT>
 __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid_constant__ CUtensorMap tm_x,
                                                                     const __grid_constant__ CUtensorMap tm_w,
                                                                     const __grid_constant__ CUtensorMap tm_out, const E4Args a)
@@ -316,9 +322,11 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
     grid_dep_wait();
 
     // tiles blockIdx.x, + gridDim.x, ... are the CTA's, a row of tiles after the other
-    const int first = blockIdx.x, stride = gridDim.x;
+    const int rank = SPLIT ? blockIdx.x % a.splits : 0;
+    const int first = SPLIT ? blockIdx.x / a.splits : blockIdx.x, stride = SPLIT ? a.tiles : gridDim.x;
     const int my_tiles = first < a.tiles ? (a.tiles - 1 - first) / stride + 1 : 0;
-    const int groups = (a.ksteps + 3) / 4;   // of four blocks
+    const int k0 = rank * a.share, ksteps = SPLIT ? min(a.share, a.p.kb - k0) : a.p.kb;   // blocks
+    const int groups = (ksteps + 3) / 4;   // of four blocks
 
     if (warp == kE4Issuer + 1) {
         // ------------------------------------------------------------ TMA producer
@@ -327,7 +335,7 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
             bool ok = true;
             for (int lt = 0; lt < my_tiles && ok; ++lt) {
                 const int t = first + lt * stride, mt = t / a.nt, nt = t - mt * a.nt;
-                for (int kb = 0; kb < a.ksteps; ++kb, ++i) {
+                for (int kb = 0; kb < ksteps; ++kb, ++i) {
                     const int slot = i % S;
                     if (i >= S && !sleep_or_abort(bar_empty + 8 * slot, ((i / S) - 1) & 1, s_abort)) {
                         ok = false;
@@ -336,8 +344,8 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
                     // rows past M or N and bytes past K come as zeros
                     const uint32_t dst = sb + slot * SP::tile, bar = bar_full + 8 * slot;
                     mbar_arrive_expect_tx(bar, SP::tile);
-                    tma_load_2d(dst, &tm_x, bar, 128 * kb, mt * 128);
-                    tma_load_2d(dst + SP::tile_a, &tm_w, bar, 128 * kb, nt * BN);
+                    tma_load_2d(dst, &tm_x, bar, 128 * (k0 + kb), mt * 128);
+                    tma_load_2d(dst + SP::tile_a, &tm_w, bar, 128 * (k0 + kb), nt * BN);
                 }
             }
             // no copy may still be landing when the CTA exits
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
             for (int lt = 0; lt < my_tiles && ok; ++lt) {
                 const int buf = lt & 1;
                 if (lt >= 2 && !sleep_or_abort(bar_acc_free + 8 * buf, ((lt >> 1) - 1) & 1, s_abort)) break;
-                for (int kb = 0; kb < a.ksteps; ++kb, ++i) {
+                for (int kb = 0; kb < ksteps; ++kb, ++i) {
                     const int slot = i % S, sf = gi & 1;
                     if ((!(kb & 3) && !sleep_or_abort(bar_sf + 8 * sf, (gi >> 1) & 1, s_abort)) ||
                         !sleep_or_abort(bar_full + 8 * slot, (i / S) & 1, s_abort)) {
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
                                          kb > 0 || k > 0);
                     umma_commit(bar_empty + 8 * slot);
                     ++nfree;
-                    if ((kb & 3) == 3 || kb == a.ksteps - 1) {
+                    if ((kb & 3) == 3 || kb == ksteps - 1) {
                         umma_commit(bar_sf_free + 8 * sf);
                         ++gi;
                     }
@@ -401,8 +409,8 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
             const int t = first + lt * stride, mt = t / a.nt, nt = t - mt * a.nt;
             for (int g = 0; g < groups; ++g, ++gi) {
                 uint32_t wa[4], wb[NBS];
-                scale_words<4>(a.p.xs, mt * 128, a.p.M, a.p.kb, g, wa);
-                scale_words<NB>(a.p.ws, nt * BN, a.p.N, a.p.kb, g, wb);
+                scale_words<4>(a.p.xs, mt * 128, a.p.M, a.p.kb, k0 + 4 * g, wa);
+                scale_words<NB>(a.p.ws, nt * BN, a.p.N, a.p.kb, k0 + 4 * g, wb);
 #pragma unroll
                 for (int j = NB; j < NBS; ++j) wb[j] = 0u;
                 const int sf = gi & 1;
@@ -448,6 +456,13 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_release(bar_acc_free + 8 * buf);
+            if constexpr (SPLIT) {   // every product has read the ring: the sums' place
+                float* to = reinterpret_cast<float*>(sm) + (32 * rq + lane) * SP::part_row + half * HN;
+#pragma unroll
+                for (int c = 0; c < HN; c += 4)
+                    *reinterpret_cast<uint4*>(to + c) = make_uint4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+                continue;
+            }
             auto sum = [&](int j) { return __uint_as_float(acc[j]) + s_bias[j]; };
             if (a.by_tma) {
                 // 64 bytes of every row at a time, staged in turn in two tiles and stored by TMA
@@ -516,6 +531,32 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // every store has been made
     }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_sync();
+        const int mt = first / a.nt, nt = first - mt * a.nt;
+        const Elem* bias = static_cast<const Elem*>(a.p.bias);
+        // four columns of a row at a time, a run of them to each CTA
+        const int all = min(128, a.p.M - mt * 128) * (BN / 4), run = (all + a.splits - 1) / a.splits;
+        for (int i = rank * run + tid; i < min(all, (rank + 1) * run); i += kE4Threads) {
+            const int r = i / (BN / 4), c = i % (BN / 4) * 4, row = mt * 128 + r, col = nt * BN + c;
+            if (col >= a.p.N) continue;
+            const uint32_t at = sb + (r * SP::part_row + c) * 4;
+            float4 part[kE4Splits];
+#pragma unroll
+            for (int p = 0; p < kE4Splits; ++p)
+                if (p < a.splits) part[p] = ld_shared_cluster4(at, p);
+            float v[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
+#pragma unroll
+            for (int p = 1; p < kE4Splits; ++p)
+                if (p < a.splits) v[0] += part[p].x, v[1] += part[p].y, v[2] += part[p].z, v[3] += part[p].w;
+            Elem* to = static_cast<Elem*>(a.out) + static_cast<long long>(row) * a.p.N + col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < a.p.N) put(to + e, v[e] + (bias ? bias_at(bias, col + e) : 0.f));
+        }
+        cluster_sync();   // no CTA leaves while another one reads its sums
+    }
     grid_dep_trigger();
     tc_fence_before();
     __syncthreads();
@@ -530,23 +571,27 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
 
 constexpr int kE4MaxRows = 0x7fffff00, kE4MaxK = 65536;
 
-int g_smem_done_e4l[6][64];
+int g_smem_done_e4l[8][64];
 
-template <int BN, typename Elem>
-oasr_status launch_e4(const E4Problem& p, void* out, int slot, int sms, cudaStream_t stream)
+// splits > 1 (SPLIT): CTAs that share a tile's K, at most one tile a CTA
+template <int BN, typename Elem, bool SPLIT = false>
+oasr_status launch_e4(const E4Problem& p, void* out, int slot, int sms, cudaStream_t stream, int splits = 1, int share = 0)
 {
     using SP = E4Smem<BN>;
     const long long mt = (p.M + 127LL) / 128, nt = (p.N + BN - 1LL) / BN, row = p.N * static_cast<long long>(sizeof(Elem));
     if (mt * nt > 0x7fffffffLL - sms) return OASR_ERR_UNSUPPORTED;
-    auto kern = linear_e4m3_kernel<BN, Elem>;
+    auto kern = linear_e4m3_kernel<BN, Elem, SPLIT>;
     if (!ensure_smem(kern, SP::bytes, g_smem_done_e4l[slot])) return OASR_ERR_CUDA;
     CUtensorMap tm_x, tm_w, tm_out = {};
-    const bool by_tma = row % 16 == 0 && row <= 0x7fffffffLL;
+    const bool by_tma = !SPLIT && row % 16 == 0 && row <= 0x7fffffffLL;
     if (!encode_bytes128(&tm_x, p.x, p.M, p.K, 128) || !encode_bytes128(&tm_w, p.w, p.N, p.K, BN) ||
         (by_tma && !encode_bytes(&tm_out, out, p.M, static_cast<int>(row), 32, true)))
         return OASR_ERR_INVALID_ARG;
-    const E4Args a = {p, out, static_cast<int>(nt), static_cast<int>(mt * nt), p.kb, by_tma, status_word()};
+    const E4Args a = {p, out, static_cast<int>(nt), static_cast<int>(mt * nt), by_tma, splits, share, status_word()};
     if (!a.status) return OASR_ERR_CUDA;
+    if (SPLIT)
+        return launch_pdl_cluster(kern, dim3(a.tiles * splits), dim3(kE4Threads), SP::bytes, splits, stream, tm_x, tm_w,
+                                  tm_out, a);
     return launch_pdl(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(kE4Threads), SP::bytes, stream, tm_x, tm_w, tm_out, a);
 }
 
@@ -580,6 +625,18 @@ oasr_status dispatch_e4(const E4Problem& p, void* out, cudaStream_t stream)
         const long long ns = (tiles + sms - 1) / sms * (static_cast<long long>(p.kb) * kinds[k].step + kinds[k].tile) + kinds[k].end;
         if (ns < least) least = ns, best = k;
     }
+    // Few tiles of 128 x 64: K shared by a cluster, 2700 ns for its start and the sums' way (64 x 512 x 2048 5.9 us, 7.3
+    // without; 64 x 512 x 4096 6.5 and 12.0; 64 x 1024 x 8192 10.5 and 22.0; 16 x 512 x 1024 5.2 and 5.0, so not shared).  On more
+    // than half of the SMs the clusters wait for one another (300 x 512 x 2048 on 144 SMs 11.6 us, 7.5 without).
+    const long long tiles = ((p.M + 127LL) / 128) * ((p.N + 63LL) / 64);
+    int share = p.kb;
+    for (int n = 2; n <= kE4Splits && 2 * tiles * n <= sms; ++n) {
+        const int each = (p.kb + n - 1) / n;
+        const long long ns = each * 380LL + 50 + 400 + 2700;
+        if (ns < least) least = ns, share = each, best = 3;
+    }
+    if (best == 3)
+        return launch_e4<64, Elem, true>(p, out, s ? 7 : 6, sms, stream, (p.kb + share - 1) / share, share);
     if (best == 0) return launch_e4<192, Elem>(p, out, s, sms, stream);
     if (best == 1) return launch_e4<128, Elem>(p, out, s + 1, sms, stream);
     return launch_e4<64, Elem>(p, out, s + 2, sms, stream);

@@ -187,6 +187,41 @@ def test_linear(M, N, K, dtype, bias):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(9, 512, 2048), (64, 100, 1552), (200, 70, 4096), (128, 64, 2064), (129, 65, 1424),
+                                   (10, 41, 16384), (300, 520, 2560), (17, 64, 65536)])
+def test_blocks_shared_by_a_cluster(M, N, K, dtype, bias):
+    test_linear(M, N, K, dtype, bias)
+
+
+@pytest.mark.gpu
+def test_each_block_of_a_cluster_counts_once():
+    """Rows that are zero but for one block, in every share of K, the last shorter block among them; captured, twice the
+    same bits."""
+    g = torch.Generator().manual_seed(4)
+    M, N, K = 70, 100, 2064
+    x, w = matrix(g, M, K), matrix(g, N, K).cuda()
+    w8, ws = capi.oasr_quantize_blocks(w)
+    for b in range(17):
+        y = torch.zeros_like(x)
+        y[:, 128 * b:128 * b + 128] = x[:, 128 * b:128 * b + 128]
+        x8, xs = capi.oasr_quantize_blocks(y.cuda())
+        out = capi.oasr_linear_e4m3(x8, xs, w8, ws, out_dtype=torch.float32)
+        close(out, product(x8.cpu(), xs.cpu(), w8.cpu(), ws.cpu(), None, torch.float32))
+    again = torch.zeros_like(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        capi.oasr_linear_e4m3(x8, xs, w8, ws, out=again)
+    for _ in range(5):
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, again)
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [3, 300])
 def test_each_scale_reaches_its_block(M):
     """One block of one row at a time stands out, in x and in w."""
