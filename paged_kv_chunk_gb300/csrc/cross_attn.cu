@@ -492,7 +492,7 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     const bool f32 = dt == OASR_F32, paged = a.table != nullptr;
     const long long max_rows = static_cast<long long>(max_q) * a.G, items = static_cast<long long>(a.N) * a.Hkv;
     // Tiles of 128 rows where the tiles of 16 are more than two an SM: few tiles leave SMs idle, and their keys can be shared by
-    // a cluster (8 heads over 1500 keys: 32 rows 8.4 us, 15.0 in tiles of 128; 128 rows 9.4 and 16.5; 448 rows, 224 tiles, 16.5
+    // a cluster (8 heads over 1500 keys: 32 rows 7.4 us, 15.0 in tiles of 128; 128 rows 9.3 and 16.5; 448 rows, 224 tiles, 16.5
     // and 16.6; 256 tiles 18.0 and 17.3).
     if (!f32 && max_rows > kXRows && items * ((max_rows + kXRows - 1) / kXRows) > 2LL * sms && cross_tc_takes(a))
         return cross_tc(a, max_q, stream);
