@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(256) linear_e4m3_few_kernel(const E4Problem p,
                     unpack16(__ldg(reinterpret_cast<const uint4*>(p.x + row * p.K + k)), xv);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s = fmaf(xv[i], wv[i], s);
-                    acc[m] += s * e4m3_scale(__ldg(p.xs + row * p.kb + b)) * ws;
+                    // the scales' product first: a power of two and exact, where s times one of them may leave fp32's range
+                    acc[m] += s * (e4m3_scale(__ldg(p.xs + row * p.kb + b)) * ws);
                 }
             }
         }

@@ -238,6 +238,31 @@ def test_each_scale_reaches_its_block(M):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 2, 3, 9, 200])
+def test_scales_whose_product_alone_is_in_range(M, dtype):
+    """A block's sum times one of its two scales is past fp32's range, or below it, where the product of all three is
+    not: large activations by small weights, and scales of 2^-126 by 2^127."""
+    g = torch.Generator().manual_seed(M)
+    N, K = 40, 400
+    x, w = torch.randn(M, K, generator=g), torch.randn(N, K, generator=g)
+    x[:, 200], w[:, 128:256] = 3.0e38, w[:, 128:256].clamp(-3, 3)
+    x[:, 128:200], x[:, 201:256], w[:, 200] = 0, 0, 0.5
+    w[0, 201] = 3
+    x8, xs = (t.cpu() for t in capi.oasr_quantize_blocks(x.cuda()))
+    w8, ws = (t.cpu() for t in capi.oasr_quantize_blocks(w.cuda()))
+    assert int(xs[0, 1]) - 127 == 120 and 1.0e38 < float(values(x8, xs)[0] @ values(w8, ws)[0]) < 2.0e38
+    out = capi.oasr_linear_e4m3(x8.cuda(), xs.cuda(), w8.cuda(), ws.cuda(), out_dtype=DT[dtype])
+    close(out, product(x8, xs, w8, ws, None, DT[dtype]))
+    xs[:], ws[:] = 1, 254
+    out = capi.oasr_linear_e4m3(x8.cuda(), xs.cuda(), w8.cuda(), ws.cuda(), out_dtype=DT[dtype])
+    close(out, product(x8, xs, w8, ws, None, DT[dtype]))
+    xs[:], ws[:] = 254, 1
+    out = capi.oasr_linear_e4m3(x8.cuda(), xs.cuda(), w8.cuda(), ws.cuda(), out_dtype=DT[dtype])
+    close(out, product(x8, xs, w8, ws, None, DT[dtype]))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(300, 500, 512), (2, 700, 256)])
 def test_same_bits_captured_and_beside_others(M, N, K):
     g = torch.Generator().manual_seed(3)
