@@ -464,6 +464,8 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
                     *reinterpret_cast<uint4*>(to + c) = make_uint4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
                 continue;
             }
+            // no rows of this warp's: nothing staged, as a staging tile is free again only by a store made after its last use
+            if (row0 >= M) continue;
             auto sum = [&](int j) { return __uint_as_float(acc[j]) + s_bias[j]; };
             if (a.by_tma) {
                 // 64 bytes of every row at a time, staged in turn in two tiles and stored by TMA
@@ -488,8 +490,7 @@ __global__ void __launch_bounds__(kE4Threads, 1) linear_e4m3_kernel(const __grid
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && row0 < M)
-                            tma_store_2d(&tm_out, smem_addr(to), (col0 + c) * static_cast<int>(sizeof(Elem)), row0);
+                        if (lane == 0) tma_store_2d(&tm_out, smem_addr(to), (col0 + c) * static_cast<int>(sizeof(Elem)), row0);
                     }
                 }
             } else {

@@ -263,6 +263,23 @@ def test_scales_whose_product_alone_is_in_range(M, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(20001, 1024, 16), (19969, 1032, 128), (40033, 512, 16)])
+def test_full_tiles_before_one_of_few_rows(M, N, K, dtype):
+    """CTAs that take a last row tile of 1, 33 or 97 rows after full ones: warps without rows there leave the tile that
+    is still on its way to memory alone.  Short K, so that little time lies between; the same bits every time."""
+    g = torch.Generator().manual_seed(K)
+    x8, xs = capi.oasr_quantize_blocks(matrix(g, M, K).cuda())
+    w8, ws = capi.oasr_quantize_blocks(matrix(g, N, K).cuda())
+    want = product(x8, xs, w8, ws, None, DT[dtype])
+    first = capi.oasr_linear_e4m3(x8, xs, w8, ws, out_dtype=DT[dtype])
+    assert bool(((first.double() - want[0]).abs() <= want[1]).all())
+    for _ in range(30):
+        assert torch.equal(capi.oasr_linear_e4m3(x8, xs, w8, ws, out_dtype=DT[dtype]), first)
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(300, 500, 512), (2, 700, 256)])
 def test_same_bits_captured_and_beside_others(M, N, K):
     g = torch.Generator().manual_seed(3)
