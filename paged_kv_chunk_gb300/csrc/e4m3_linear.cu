@@ -140,9 +140,9 @@ __device__ __forceinline__ void unpack16(const uint4& w, float (&v)[16])
     }
 }
 
-// A few rows (one to eight tokens): every weight byte is used once per row.  One warp per output channel, 16
-// values per lane and step (within one block), products in fp32 (exact) and their sums too.
-constexpr int kE4FewRows = 8;
+// A few rows (one to six tokens, which of them goes by K: dispatch_e4): every weight byte is used once per row.  One warp
+// per output channel, 16 values per lane and step (within one block), products in fp32 (exact) and their sums too.
+constexpr int kE4FewRows = 6;   // the most that dispatch_e4's estimate ever prefers: 7 rows of 512 cost 3820 ns against 3800
 
 template <int MR, typename Elem>
 __global__ void __launch_bounds__(256) linear_e4m3_few_kernel(const E4Problem p, Elem* __restrict__ out)

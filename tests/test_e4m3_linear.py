@@ -280,6 +280,38 @@ def test_full_tiles_before_one_of_few_rows(M, N, K, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(3, 77, 512), (4, 2050, 1024), (5, 512, 512), (5, 100, 1024), (6, 33, 512), (6, 1000, 144),
+                                   (7, 512, 512), (8, 100, 16)])
+def test_rows_around_the_border_of_the_forms(M, N, K, dtype, bias):
+    """Every instance of the form without tiles (1, 2, 3 to 4, 5 to 6 rows) and the first sizes that tiles take."""
+    test_linear(M, N, K, dtype, bias)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 6, 40])
+def test_blocks_that_stand_for_nan(M, dtype):
+    """A scale of 255, of x or of w, makes its row's or its column's results NaN and no other."""
+    g = torch.Generator().manual_seed(M)
+    N, K = 24, 272
+    x, w = torch.randn(M, K, generator=g), torch.randn(N, K, generator=g)
+    x[M // 2, 260], w[5, 3], w[9, 200] = float("inf"), float("nan"), float("-inf")
+    x8, xs = capi.oasr_quantize_blocks(x.cuda())
+    w8, ws = capi.oasr_quantize_blocks(w.cuda())
+    assert xs[M // 2].tolist()[2] == 255 and ws[5].tolist()[0] == 255 and ws[9].tolist()[1] == 255
+    out = capi.oasr_linear_e4m3(x8, xs, w8, ws, out_dtype=DT[dtype]).cpu()
+    bad = torch.zeros(M, N, dtype=torch.bool)
+    bad[M // 2], bad[:, 5], bad[:, 9] = True, True, True
+    assert torch.equal(out.isnan(), bad)
+    rows, cols = [i for i in range(M) if i != M // 2], [j for j in range(N) if j not in (5, 9)]
+    x8, xs, w8, ws = x8.cpu().float()[rows], xs.cpu()[rows], w8.cpu().float()[cols], ws.cpu()[cols]
+    if rows:
+        close(out[rows][:, cols], product(x8, xs, w8, ws, None, DT[dtype]))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(300, 500, 512), (2, 700, 256)])
 def test_same_bits_captured_and_beside_others(M, N, K):
     g = torch.Generator().manual_seed(3)
