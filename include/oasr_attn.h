@@ -353,7 +353,8 @@ oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_scale, cons
  *                       position C + t of stream b has; -1 behind cu[B].
  * cache_seqlens is not changed: the caller commits new_seqlens once the rows are written.  A stream has at most
  * max_blocks_per_seq pages; lengths below 0 or past them are clamped, a slot whose page names no block is -1, rows
- * past `total` get no slot, a ring state out of range hands out nothing: each raises OASR_ERR_BOUNDS.
+ * past `total` get no slot, a ring state out of range stays as it is while nothing is handed out or taken back: each
+ * raises OASR_ERR_BOUNDS.
  * Requirements: B at most 4096; num_blocks * block_size, B * max_blocks_per_seq and (max_blocks_per_seq + 1) *
  * block_size below 2^31 (else OASR_ERR_UNSUPPORTED).  One call at a time may work on a ring and its state.
  */

@@ -95,9 +95,10 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
         rows += s_rows[0][w], rows0 += s_rows[1][w];
     }
 
-    // a state that no call of the library has left: nothing is handed out, nothing is taken back
+    // a state that no call of the library has left: nothing is handed out or taken back, and it stays as it is
     int head = a.state[0], count = a.state[1];
-    if (head < 0 || head >= a.nb || count < 0 || count > a.nb) {
+    const bool sane = head >= 0 && head < a.nb && count >= 0 && count <= a.nb;
+    if (!sane) {
         err = kErrBounds;
         head = count = 0;
         give = 0;
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
         };
         if (granted)
             for (int i = t0; i < c.need(); i += kTabGroup) row[c.P0 + i] = fresh(i);
-        for (int i = t0; i < c.give(); i += kTabGroup) {
+        for (int i = t0; sane && i < c.give(); i += kTabGroup) {
             if (give0 + i < give) a.ring[place(static_cast<unsigned>(head + count) + (give0 + i))] = row[c.P1 + i];
             row[c.P1 + i] = -1;
         }
@@ -162,8 +163,10 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
         __threadfence();
         if (atomicInc(reinterpret_cast<unsigned*>(a.state) + 3, gridDim.x - 1) == gridDim.x - 1) {
             const int taken = granted ? need : 0;
-            a.state[0] = static_cast<int32_t>(place(static_cast<unsigned>(head) + taken));
-            a.state[1] = count - taken + give;
+            if (sane) {
+                a.state[0] = static_cast<int32_t>(place(static_cast<unsigned>(head) + taken));
+                a.state[1] = count - taken + give;
+            }
             a.state[2] = granted ? 0 : need - count;
         }
     }

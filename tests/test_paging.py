@@ -195,6 +195,24 @@ def test_update_clamps_what_is_out_of_range():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("head,count", [(12, 3), (-1, 3), (2, 13), (2, -1), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_update_with_a_state_out_of_range(head, count):
+    """Nothing is handed out, no page is lost: table, ring and the state's first two stay; rows within a page that a
+    stream has get their slots where no stream needs a new page."""
+    bs, mbps, nb = 4, 3, 12
+    for lens, new in (([0, 9, 2], [5, 0, 9]), ([0, 9, 2], [0, 1, 4])):
+        table, ring, _ = batch(4, lens, bs, mbps, nb)
+        t, r, s, c, n = cuda(table, ring, [head, count, 0, 0], lens, new)
+        slots, cu = capi.oasr_block_table_update(t, c, n, r, s, bs, 16)
+        assert t.tolist() == table and r.tolist() == ring and s.tolist()[:2] == [head, count] and s.tolist()[3] == 0
+        if new[2] == 4:
+            assert slots.tolist() == [table[2][0] * bs + 2, table[2][0] * bs + 3] + [-1] * 14 and cu.tolist() == [0, 0, 0, 2]
+        else:
+            assert set(slots.tolist()) == {-1} and cu.tolist() == [0, 5, 5, 12] and s.tolist()[2] > 0
+        assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+
+
+@pytest.mark.gpu
 def test_update_captured():
     """A captured update replayed: each replay goes on from the state that the last one left."""
     bs, mbps, nb = 16, 8, 40
