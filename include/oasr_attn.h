@@ -346,14 +346,19 @@ oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_scale, cons
  *   shrinking: block_table[b][P1 .. P0) go behind the ring's last id and become -1.
  * Pages given back in a call are not handed out in the same call.  Where the ring holds fewer ids than the
  * growing streams need, none of them gets any: their entries stay as they were, free_state[2] is the number of
- * pages short (else 0), and every slot is -1; shrinking streams give theirs back all the same.
+ * pages short (else 0), and every slot is -1; shrinking streams give theirs back all the same.  After such a call the
+ * growing streams still have C frames: new_seqlens is committed for the others alone (the lesser of the two lengths
+ * for each), or not at all, and the call repeated once pages are back; the same call again is safe.
+ * An entry given back that is -1 (the page was given back before, or never handed out) is passed over, and so is one
+ * that names no block otherwise, which raises OASR_ERR_BOUNDS: the ring holds ids of blocks alone.  The entries of
+ * pages that a stream does not have are the caller's to set to -1 at the start.
  *   cu_seqlens [B + 1]: offsets of the streams' new rows, cu[b + 1] - cu[b] = max(N - C, 0);
  *   slot_map [total]:   slot_map[cu[b] + t] = block_table[b][(C + t) / block_size] * block_size +
  *                       (C + t) % block_size, the row of the pools ([num_blocks * block_size, H, D]) that
  *                       position C + t of stream b has; -1 behind cu[B].
- * cache_seqlens is not changed: the caller commits new_seqlens once the rows are written.  A stream has at most
+ * cache_seqlens is not changed: the caller commits the new lengths once the rows are written.  A stream has at most
  * max_blocks_per_seq pages; lengths below 0 or past them are clamped, a slot whose page names no block is -1, rows
- * past `total` get no slot, a ring state out of range stays as it is while nothing is handed out or taken back: each
+ * past `total` get no slot, pages that come back beyond num_blocks ids are lost, a ring state out of range stays as it is while nothing is handed out or taken back: each
  * raises OASR_ERR_BOUNDS.
  * Requirements: B at most 4096; num_blocks * block_size, B * max_blocks_per_seq and (max_blocks_per_seq + 1) *
  * block_size below 2^31 (else OASR_ERR_UNSUPPORTED).  One call at a time may work on a ring and its state.

@@ -39,7 +39,7 @@ A batch of requests of different lengths, from its pages to a decoder's tokens o
     x8, x_scale = capi.oasr_quantize_blocks(states)        # [total, d]; weights once, in the same way
     kv = capi.oasr_linear_e4m3(x8, x_scale, w_kv8, w_kv_scale, b_kv).view(total, 2, Hkv, 64)
     capi.oasr_paged_append_slots(kv[:, 0], kv[:, 1], k_pool, v_pool, slot_map)
-    cache_seqlens.copy_(new_seqlens)
+    cache_seqlens.copy_(torch.where(free_state[2] == 0, new_seqlens, torch.minimum(cache_seqlens, new_seqlens)))
     out = capi.oasr_cross_attn_paged(q, k_pool, v_pool, block_table, cache_seqlens, cu_q, max_q)
 
 (``oasr_cross_attn_packed`` over states that are only packed.)

@@ -587,7 +587,8 @@ def oasr_block_table_update(block_table, cache_seqlens, new_seqlens, free_blocks
     from and given back to the ring of free block ids (free_blocks int32 [num_blocks], free_state int32
     [4]: first place, count, pages short, 0), in place.  Returns (slot_map int32 [total], the pool row
     of every new frame, stream after stream, -1 behind the last and where the ring was short; cu_seqlens
-    int32 [B + 1], the streams' offsets in it)."""
+    int32 [B + 1], the streams' offsets in it).  Where it was short (free_state[2] > 0) no stream has grown, and
+    only the shorter lengths are committed.  Entries of the table without a page are -1."""
     L, dev = _lib_device()
     table = block_table.shape
     total, block_size = int(total), int(block_size)

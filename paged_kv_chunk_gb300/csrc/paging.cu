@@ -7,6 +7,11 @@
 // prefix and the totals: one launch and no wait between CTAs, where a scan of its own would be another
 // launch.  The ring is what keeps the CTAs apart: pages are taken at its head and given back behind its
 // tail, so no CTA writes what another one still reads, and the last CTA to finish moves both ends.
+//
+// An entry given back may name no block: -1 where an earlier call was short and left the stream without the page, or took
+// it back already.  Such entries must not enter the ring, and which places the ones behind them get is then known only once
+// every entry has been read.  The places above count every entry; where one turns out to name none, the last CTA to finish
+// closes the gaps, and where there are more entries than places (so some must name none), it alone does the taking back.
 #include "host_common.h"
 #include "ptx.cuh"
 
@@ -14,6 +19,8 @@ namespace oasr {
 namespace {
 
 constexpr int kTabThreads = 256, kTabMaxStreams = 4096;
+constexpr int kTabItems = 8;              // entries a thread sorts out at a time
+constexpr unsigned kTabGap = 1u << 16;    // in the count of finished CTAs (at most 1024): one that found such an entry
 
 // What a stream's change of length asks for.
 struct Change {
@@ -38,7 +45,7 @@ struct TableArgs {
     int B, mbps, bs;
     int32_t* ring;
     int nb;
-    int32_t* state;   // head, count, short, CTAs that have finished
+    int32_t* state;   // head, count, short, CTAs that have finished (and kTabGap for each that found gaps)
     int32_t* slots;
     int total;
     int32_t* cu;
@@ -103,13 +110,13 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
         head = count = 0;
         give = 0;
     }
-    if (give > a.nb - count) {   // more pages come back than were ever out
-        err = kErrBounds;
-        give = a.nb - count;
-    }
+    const int room = a.nb - count;
+    const unsigned tail = static_cast<unsigned>(head) + count;
     const bool granted = need <= count;
     auto place = [&](unsigned i) { return i >= static_cast<unsigned>(a.nb) ? i - a.nb : i; };   // i < 2 nb
 
+    auto names_block = [&](int id) { return id >= 0 && id < a.nb; };
+    int gaps = 0;
     const int b = b0 + tid / kTabGroup, t0 = tid % kTabGroup;
     if (b < a.B) {
         for (int i = b0; i < b; ++i) {
@@ -124,13 +131,18 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
         const unsigned from = head + need0;
         auto fresh = [&](int i) {   // the i-th page handed to this stream
             const int id = a.ring[place(from + i)];
-            return id >= 0 && id < a.nb ? id : -1;
+            return names_block(id) ? id : -1;
         };
         if (granted)
             for (int i = t0; i < c.need(); i += kTabGroup) row[c.P0 + i] = fresh(i);
-        for (int i = t0; sane && i < c.give(); i += kTabGroup) {
-            if (give0 + i < give) a.ring[place(static_cast<unsigned>(head + count) + (give0 + i))] = row[c.P1 + i];
+        for (int i = t0; sane && give <= room && i < c.give(); i += kTabGroup) {
+            const int id = row[c.P1 + i];
             row[c.P1 + i] = -1;
+            a.ring[place(tail + (give0 + i))] = names_block(id) ? id : -1;
+            if (!names_block(id)) {
+                gaps = 1;
+                if (id != -1) err = kErrBounds;
+            }
         }
         for (int t = t0; t < c.rows(); t += kTabGroup) {
             if (rows0 + t >= static_cast<unsigned long long>(a.total)) {
@@ -141,7 +153,7 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
             if (granted) {
                 const int p = c.C + t, page = static_cast<unsigned>(p) / static_cast<unsigned>(a.bs);
                 const int id = page < c.P0 ? row[page] : fresh(page - c.P0);
-                if (id >= 0 && id < a.nb)
+                if (names_block(id))
                     slot = id * a.bs + (p - page * a.bs);
                 else
                     err = kErrBounds;
@@ -157,19 +169,83 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
     for (unsigned long long i = rows + blockIdx.x * kTabThreads + tid; i < static_cast<unsigned long long>(a.total);
          i += static_cast<unsigned long long>(gridDim.x) * kTabThreads)
         a.slots[i] = -1;
-    if (err) atomicOr(a.status, err);
-    __syncthreads();   // head and count have been read
+    auto finish = [&](int back) {
+        if (sane) {
+            a.state[0] = static_cast<int32_t>(place(static_cast<unsigned>(head) + (granted ? need : 0)));
+            a.state[1] = count - (granted ? need : 0) + back;
+        }
+        a.state[2] = granted ? 0 : need - count;
+        a.state[3] = 0;
+    };
+    gaps = __syncthreads_or(gaps);   // and head and count have been read
+    __shared__ bool s_sort;          // the last CTA to finish, and there are gaps
     if (tid == 0) {
         __threadfence();
-        if (atomicInc(reinterpret_cast<unsigned*>(a.state) + 3, gridDim.x - 1) == gridDim.x - 1) {
-            const int taken = granted ? need : 0;
-            if (sane) {
-                a.state[0] = static_cast<int32_t>(place(static_cast<unsigned>(head) + taken));
-                a.state[1] = count - taken + give;
-            }
-            a.state[2] = granted ? 0 : need - count;
-        }
+        const unsigned seen = atomicAdd(reinterpret_cast<unsigned*>(a.state) + 3, gaps ? kTabGap + 1 : 1u) + (gaps ? kTabGap : 0u);
+        const bool last = seen % kTabGap == gridDim.x - 1;
+        s_sort = last && (seen >= kTabGap || give > room);
+        if (s_sort)
+            __threadfence();
+        else if (last)
+            finish(give);
     }
+    __syncthreads();
+    if (s_sort) {
+        int back = 0;
+        __shared__ int s_warp[kTabThreads / 32];
+        // those of n entries that name a block go behind the ones before them, in their order
+        auto take_back = [&](int n, auto&& entry) {
+            for (unsigned i0 = 0; i0 < static_cast<unsigned>(n); i0 += kTabThreads * kTabItems) {
+                const unsigned i = i0 + tid * kTabItems;
+                int id[kTabItems], own = 0;
+#pragma unroll
+                for (int u = 0; u < kTabItems; ++u) {
+                    id[u] = i + u < static_cast<unsigned>(n) ? entry(i + u) : -1;
+                    own += names_block(id[u]);
+                }
+                int upto = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                if (lane == 31) s_warp[warp] = upto;
+                __syncthreads();   // every entry of this step has been read
+                int at = back + upto - own;
+#pragma unroll
+                for (int w = 0; w < kTabThreads / 32; ++w) {
+                    if (w < warp) at += s_warp[w];
+                    back += s_warp[w];
+                }
+#pragma unroll
+                for (int u = 0; u < kTabItems; ++u)
+                    if (names_block(id[u])) {
+                        if (at < room)
+                            a.ring[place(tail + at)] = id[u];
+                        else
+                            err = kErrBounds;   // more pages come back than were ever out
+                        ++at;
+                    }
+                __syncthreads();
+            }
+        };
+        if (give <= room) {
+            take_back(give, [&](unsigned i) { return __ldcg(a.ring + place(tail + i)); });
+        } else {
+            for (int i = 0; i < a.B; ++i) {
+                const Change c(__ldg(a.lens + i), __ldg(a.news + i), cap, a.bs);
+                int32_t* row = a.table + static_cast<long long>(i) * a.mbps + c.P1;
+                take_back(c.give(), [&](unsigned p) {
+                    const int id = row[p];
+                    row[p] = -1;
+                    if (id < -1 || id >= a.nb) err = kErrBounds;
+                    return id;
+                });
+            }
+        }
+        if (tid == 0) finish(min(back, room));
+    }
+    if (err) atomicOr(a.status, err);
 }
 
 // A warp moves two rows of K and of V, every load of them ahead of the first store.

@@ -212,6 +212,123 @@ def test_update_with_a_state_out_of_range(head, count):
         assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
 
 
+def walk_any(table, lens, new, ring, state, bs, total):
+    """`walk` where entries given back may name no block: (table, the ring's ids in their order, count, short, slots,
+    cu)."""
+    nb, (head, count) = len(ring), state[:2]
+    free = [ring[(head + i) % nb] for i in range(count)]
+    back = []
+    for b, (c, n) in enumerate(zip(lens, new)):
+        back += [x for x in table[b][-(-n // bs):-(-c // bs)] if 0 <= x < nb]
+    table, _, (_, _, short, _), slots, cu = walk(table, lens, new, ring, state, bs, total)
+    got = sum(max(0, -(-n // bs) - -(-c // bs)) for c, n in zip(lens, new))
+    free = (free if short else free[got:]) + back
+    return table, free[:nb], len(free[:nb]), short, slots, cu
+
+
+def live(ring, state):
+    ring, (head, count, _, zero) = ring.tolist(), state.tolist()
+    assert zero == 0
+    return [ring[(head + i) % len(ring)] for i in range(count)], count
+
+
+@pytest.mark.gpu
+def test_update_short_and_repeated():
+    """A short call, then the same call again: what the shrinking streams gave back counts once."""
+    lens, new, bs, mbps, nb = [40, 3], [0, 50], 8, 7, 16
+    table, ring, state = batch(1, lens, bs, mbps, nb, 3, 2)
+    t, r, s, c, n = cuda(table, ring, state, lens, new)
+    slots, _ = capi.oasr_block_table_update(t, c, n, r, s, bs, 50)
+    assert s.tolist()[1:3] == [7, 4] and set(slots.tolist()) == {-1}
+    assert live(r, s)[0] == [ring[3], ring[4]] + table[0][:5]
+    slots, cu = capi.oasr_block_table_update(t, c, n, r, s, bs, 50)
+    assert t.tolist()[0] == [-1] * 7 and t.tolist()[1] == [table[1][0], ring[3], ring[4]] + table[0][:4]
+    assert live(r, s) == ([table[0][4]], 1) and s.tolist()[2] == 0
+    row = t.tolist()[1]
+    assert slots.tolist() == [row[i // bs] * bs + i % bs for i in range(3, 50)] + [-1] * 3 and cu.tolist() == [0, 0, 47]
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("commit", ["the shorter", "all"])
+@pytest.mark.parametrize("B,bs,longest", [(3, 4, 60), (40, 8, 300), (700, 2, 40), (30, 1, 3000)])
+def test_update_of_a_pool_that_is_too_small(B, bs, longest, commit):
+    """A pool of half of what the streams want, through thirty batches: free and held ids stay apart and whole, where
+    the lengths committed after a short call are the shorter ones and also where they are all committed."""
+    rng = random.Random(B)
+    mbps = -(-longest // bs)
+    nb = B * mbps // 4 + 2
+    lens = [0] * B
+    table, ring, state = batch(B, lens, bs, mbps, nb)
+    t, r, s = cuda(table, ring, state)
+    cut = lambda: [row[:] for row in t.tolist()]
+    shorts = 0
+    for step in range(30):
+        new = [rng.choice([0, n, n // 2, min(longest, n + rng.randint(1, longest))]) for n in lens]
+        if step % 10 == 9:
+            new = [0] * B
+        total = sum(max(0, n - c) for c, n in zip(lens, new))
+        want = walk_any(cut(), lens, new, r.tolist(), s.tolist(), bs, total)
+        slots, cu = capi.oasr_block_table_update(t, *cuda(lens, new), r, s, bs, total)
+        short = s.tolist()[2]
+        shorts += short > 0
+        ids, count = live(r, s)
+        assert (t.tolist(), ids, count, short, cu.tolist()) == want[:4] + want[5:]
+        if commit != "all":
+            assert slots.tolist() == want[4]
+        held = [x for row in t.tolist() for x in row if x != -1]
+        assert sorted(held + ids) == list(range(nb))       # no block lost, none in two places
+        lens = new if commit == "all" or not short else [min(c, n) for c, n in zip(lens, new)]
+        # a stream that was refused and committed all the same has pages missing: its next slots are flagged
+        assert capi.oasr_device_status() == 0 or commit == "all"
+    assert shorts > 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("room", ["enough", "too little"])
+@pytest.mark.parametrize("B", [2, 9, 600])
+def test_update_entries_that_name_no_block(B, room):
+    """Entries of -1, of other negative values and of large ones among those given back, more of them than a step of the
+    sorting takes; and more entries than the ring has places."""
+    rng = random.Random(B)
+    bs, mbps = 1, 5000 if B < 10 else 40
+    nb = 4 * B * mbps if room == "enough" else B * mbps // 20
+    ids = rng.sample(range(nb), nb * 9 // 10)
+    held, spare = (ids[:B * mbps // 2], ids[-nb // 2:]) if room == "enough" else (ids[:nb // 2], ids[nb // 2:])
+    places = set(rng.sample(range(B * mbps), len(held)))
+    fill = iter(held)
+    table = [[next(fill) if b * mbps + p in places else -1 for p in range(mbps)] for b in range(B)]
+    for flagged in (False, True):
+        ring = [-7] * nb
+        head = nb - 5
+        for i, x in enumerate(spare):
+            ring[(head + i) % nb] = x
+        if flagged:
+            b, p = next((b, p) for b in range(B) for p in range(mbps) if table[b][p] == -1)
+            table[b][p] = nb
+            b, p = next((b, p) for b in reversed(range(B)) for p in reversed(range(mbps)) if table[b][p] == -1)
+            table[b][p] = -2 ** 31
+        lens, new = [mbps] * B, [0] * B
+        new[B // 2] = 3
+        state = [head, len(spare), 0, 0]
+        want = walk_any(table, lens, new, ring, state, bs, 5)
+        t, r, s, c, n = cuda(table, ring, state, lens, new)
+        slots, cu = capi.oasr_block_table_update(t, c, n, r, s, bs, 5)
+        got, count = live(r, s)
+        assert (t.tolist(), got, count) == want[:3] and slots.tolist() == [-1] * 5 and not any(cu.tolist())
+        assert capi.oasr_device_status() == (capi.STATUS_BOUNDS_BIT if flagged else 0)
+
+
+@pytest.mark.gpu
+def test_update_more_pages_than_were_ever_out():
+    """A block in two streams' tables: the ring is full before all are back, the rest is dropped and flagged."""
+    bs, mbps, nb = 2, 4, 6
+    t, r, s, c, n = cuda([[0, 1, 2, 3], [3, 2, 1, 0]], [4, 5, -7, -7, -7, -7], [0, 2, 0, 0], [8, 8], [0, 0])
+    capi.oasr_block_table_update(t, c, n, r, s, bs, 0)
+    assert live(r, s) == ([4, 5, 0, 1, 2, 3], 6) and set(t.flatten().tolist()) == {-1}
+    assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+
+
 @pytest.mark.gpu
 def test_update_captured():
     """A captured update replayed: each replay goes on from the state that the last one left."""
