@@ -360,8 +360,8 @@ oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_scale, cons
  * max_blocks_per_seq pages; lengths below 0 or past them are clamped, a slot whose page names no block is -1, rows
  * past `total` get no slot, pages that come back beyond num_blocks ids are lost, a ring state out of range stays as it is while nothing is handed out or taken back: each
  * raises OASR_ERR_BOUNDS.
- * Requirements: B at most 4096; num_blocks * block_size, B * max_blocks_per_seq and (max_blocks_per_seq + 1) *
- * block_size below 2^31 (else OASR_ERR_UNSUPPORTED).  One call at a time may work on a ring and its state.
+ * Requirements: B at most 4096; num_blocks * block_size and B * max_blocks_per_seq below 2^31 and
+ * (max_blocks_per_seq + 1) * block_size below 2^31 - 256 (else OASR_ERR_UNSUPPORTED).  One call at a time may work on a ring and its state.
  */
 oasr_status oasr_block_table_update(int32_t* block_table, const int32_t* cache_seqlens,
                                     const int32_t* new_seqlens, int B, int max_blocks_per_seq, int block_size,

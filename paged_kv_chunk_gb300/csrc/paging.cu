@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const TableArg
         const Change c(__ldg(a.lens + b), __ldg(a.news + b), cap, a.bs);
         if (c.bad) err = kErrBounds;
         int32_t* row = a.table + static_cast<long long>(b) * a.mbps;
-        const unsigned from = head + need0;
+        const unsigned from = static_cast<unsigned>(head) + need0;
         auto fresh = [&](int i) {   // the i-th page handed to this stream
             const int id = a.ring[place(from + i)];
             return names_block(id) ? id : -1;
@@ -312,7 +312,7 @@ extern "C" oasr_status oasr_block_table_update(int32_t* block_table, const int32
     if (B <= 0 || max_blocks_per_seq <= 0 || block_size <= 0 || num_blocks <= 0 || total < 0) return OASR_ERR_INVALID_ARG;
     constexpr long long kInt = 0x7fffffff;
     if (B > kTabMaxStreams || static_cast<long long>(B) * max_blocks_per_seq > kInt ||
-        static_cast<long long>(max_blocks_per_seq) * block_size > kInt - block_size ||
+        static_cast<long long>(max_blocks_per_seq) * block_size > kInt - kTabThreads - block_size ||   // loops step past it
         static_cast<long long>(num_blocks) * block_size > kInt)
         return OASR_ERR_UNSUPPORTED;
     const TableArgs a = {block_table, cache_seqlens, new_seqlens, B,     max_blocks_per_seq, block_size,   free_blocks,

@@ -82,6 +82,13 @@ def test_update_refusals(lib, kw, expect):
     assert lib.oasr_block_table_update(*a.values(), None) == expect
 
 
+@pytest.mark.parametrize("mbps,bs", [(2 ** 31 - 2, 1), (2 ** 31 - 257, 1), (2 ** 30 - 129, 2), (1, 2 ** 30 - 128)])
+def test_update_refuses_lengths_within_a_step_of_2_31(lib, mbps, bs):
+    """A stream's rows and pages are walked 256 at a time in 32 bits."""
+    a = dict(bt=FAKE, cs=FAKE, new=FAKE, B=1, mbps=mbps, bs=bs, free=FAKE, nb=1, state=FAKE, slots=FAKE, total=64, cu=FAKE)
+    assert lib.oasr_block_table_update(*a.values(), None) == capi.OASR_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("kw,expect", [
     (dict(k=None), capi.OASR_ERR_INVALID_ARG), (dict(slots=None), capi.OASR_ERR_INVALID_ARG),
     (dict(total=0), capi.OASR_ERR_INVALID_ARG), (dict(ks=255), capi.OASR_ERR_INVALID_ARG),
