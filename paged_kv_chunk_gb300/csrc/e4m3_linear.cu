@@ -654,7 +654,7 @@ extern "C" oasr_status oasr_quantize_blocks(const void* x, void* x8, void* scale
     if (!x || !x8 || !scale || M <= 0 || K <= 0) return OASR_ERR_INVALID_ARG;
     if ((dt != OASR_F32 && dt != OASR_BF16) || K % 16) return OASR_ERR_UNSUPPORTED;
     if (!aligned16(x) || !aligned16(x8)) return OASR_ERR_INVALID_ARG;
-    const int kb = (K + kBlk - 1) / kBlk;
+    const int kb = (K - 1) / kBlk + 1;
     const long long ctas = (static_cast<long long>(M) * kb + 16 * kQBlocks - 1) / (16 * kQBlocks);
     if (ctas > 0x7fffffffLL) return OASR_ERR_UNSUPPORTED;
     auto go = [&](auto* src) {

@@ -132,6 +132,21 @@ def test_quantize_blocks(M, K, dtype):
 
 
 @pytest.mark.gpu
+def test_quantize_the_longest_row():
+    """A row of 2^31 - 16 values, its last block of 112: the same bytes as its blocks by themselves."""
+    K = 2 ** 31 - 16
+    x = torch.randn(1, 1 << 20, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda().repeat(1, 2048)[:, 16:].contiguous()
+    x8, scale = capi.oasr_quantize_blocks(x)
+    whole = K // 128 * 128
+    for part, rows in ((slice(0, whole), -1), (slice(whole, K), 1)):
+        y = x[0, part].contiguous().view(rows, 128 if rows < 0 else 112)
+        y8, s = capi.oasr_quantize_blocks(y)
+        assert torch.equal(x8.view(torch.uint8)[0, part], y8.view(torch.uint8).view(-1))
+        assert torch.equal(scale[0, part.start // 128:-(-part.stop // 128)], s.view(-1))
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_quantize_blocks_edges():
     """Ties to even, magnitudes at 448's border, below the least scale, the largest, and values that are not finite."""
     x = torch.zeros(7, 272)
