@@ -393,7 +393,8 @@ oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_
  * contiguous: k and v may be the halves of one product's rows); out is [total_q, H, 64].
  * max_q and max_k are the lengths that the launch is laid out for: a longer sequence is right, and slower.
  * Requirements: D = 64; H a multiple of Hkv and at most 1024; num_seqs at most 65536; 0 < scale <= 2e38; pointers
- * and strides multiples of 16 bytes; total_q, total_k, max_q and max_k at least 1; total_q * G below 2^31 - 256;
+ * and strides multiples of 16 bytes; total_q, total_k, max_q and max_k at least 1; total_q * G, max_q * G, total_k
+ * and max_blocks_per_seq * block_size below 2^31 - 256;
  * num_blocks * block_size < 2^31.
  * Offsets that decrease or pass total_q or total_k, and lengths past the table, are clamped; an invalid block id
  * reads as zero rows; each raises OASR_ERR_BOUNDS.  Keys past a sequence's end are never part of a result, whatever

@@ -577,6 +577,7 @@ extern "C" oasr_status oasr_cross_attn_packed(const void* q, int64_t q_stride, c
     const oasr_status bad = cross_check(a, max_q, max_k, D, scale, dt);
     if (bad != OASR_OK) return bad;
     if (!cu_k || total_k <= 0) return OASR_ERR_INVALID_ARG;
+    if (total_k > 0x7fffffff - 256) return OASR_ERR_UNSUPPORTED;   // keys are counted in 32 bits, a tile at a time
     a.c = scale * 1.4426950408889634f;
     a.status = status_word();
     return cross_dispatch(a, max_q, max_k, dt, stream);

@@ -126,6 +126,13 @@ def test_paged_refusals(lib, kw, expect):
     assert lib.oasr_cross_attn_paged(*a.values(), None) == expect
 
 
+@pytest.mark.parametrize("tk", [2 ** 31 - 1, 2 ** 31 - 256])
+def test_packed_refuses_keys_within_a_tile_of_2_31(lib, tk):
+    a = dict(q=FAKE, qs=512, k=FAKE, ks=256, v=FAKE, vs=256, cuq=FAKE, cuk=FAKE, N=2, mq=4, mk=9, tq=8, tk=tk, out=FAKE,
+             H=8, Hkv=4, D=64, scale=0.125, dt=capi.OASR_BF16)
+    assert lib.oasr_cross_attn_packed(*a.values(), None) == capi.OASR_ERR_UNSUPPORTED
+
+
 def test_binding_refusals():
     q, k, cu = torch.zeros(4, 8, 64), torch.zeros(9, 4, 64), torch.zeros(3, dtype=torch.int32)
     pool, table = torch.zeros(6, 8, 4, 64), torch.zeros(2, 3, dtype=torch.int32)
