@@ -373,7 +373,8 @@ oasr_status oasr_block_table_update(int32_t* block_table, const int32_t* cache_s
  * k_new and v_new (rows of H * D values, k_stride and v_stride values apart: views of one product's output will do)
  * becomes row slot_map[i] of k_pool and v_pool, a pure copy.  Slots of -1 are skipped; slots below that or past the
  * pools are skipped and raise OASR_ERR_BOUNDS.  A slot named twice holds one of its rows, unspecified which.
- * Requirements: D * sizeof(dtype) and both strides multiples of 16 bytes; num_blocks * block_size < 2^31.
+ * Requirements: total at least 1 (a step in which streams only end has no rows and no call); D * sizeof(dtype) and both
+ * strides multiples of 16 bytes; num_blocks * block_size < 2^31.
  */
 oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
                                     void* k_pool, void* v_pool, int num_blocks, int block_size,

@@ -619,7 +619,8 @@ def oasr_block_table_update(block_table, cache_seqlens, new_seqlens, free_blocks
 
 def oasr_paged_append_slots(k_new, v_new, k_pool, v_pool, slot_map, stream=None):
     """Write row i of k_new and v_new ([total,H,D], rows may lie apart) into row slot_map[i] of the pools
-    ([nb,bs,H,D] as rows), in place; slots of -1 are skipped."""
+    ([nb,bs,H,D] as rows), in place; slots of -1 are skipped.  No rows (a step in which streams only end):
+    nothing to do, here and in the calls below."""
     L, dev = _lib_device()
     dt = k_new.dtype
     code = _code(dt)
@@ -635,6 +636,8 @@ def oasr_paged_append_slots(k_new, v_new, k_pool, v_pool, slot_map, stream=None)
     k_apart, v_apart = _rows_apart(k_new, "k_new", dt, dev), _rows_apart(v_new, "v_new", dt, dev)
     if not (_good(dev, dt, k_pool, v_pool) and _good(dev, torch.int32, slot_map)):
         _refuse(k_pool=(k_pool, dt), v_pool=(v_pool, dt), slot_map=(slot_map, torch.int32))
+    if n == 0:
+        return
     _check("oasr_paged_append_slots", L.oasr_paged_append_slots(
         k_new.data_ptr(), v_new.data_ptr(), k_apart, v_apart, k_pool.data_ptr(), v_pool.data_ptr(), shape[0], shape[1],
         slot_map.data_ptr(), n, H, D, code, _stream(stream)))
@@ -664,7 +667,8 @@ def _cross(dev, q, cu_q, max_q, Hkv, out):
 def oasr_cross_attn_packed(q, k, v, cu_q, cu_k, max_q, max_k, out=None, scale=None, stream=None):
     """Cross attention of packed queries [total_q,H,64] (sequence s: rows cu_q[s] to cu_q[s+1]) over packed
     keys and values [total_k,Hkv,64] (cu_k), Hkv dividing H; rows of q, k and v may lie apart.  max_q and
-    max_k: the longest sequences' lengths.  Returns out [total_q,H,64]; without keys zeros."""
+    max_k: the longest sequences' lengths.  Returns out [total_q,H,64]; without keys zeros (k and v have a
+    row all the same)."""
     L, dev = _lib_device()
     nk, Hkv, Dk = k.shape
     max_q, max_k = int(max_q), int(max_k)
@@ -677,6 +681,8 @@ def oasr_cross_attn_packed(q, k, v, cu_q, cu_k, max_q, max_k, out=None, scale=No
     k_apart, v_apart = _rows_apart(k, "k", q.dtype, dev), _rows_apart(v, "v", q.dtype, dev)
     if not _good(dev, torch.int32, cu_k):
         _refuse(cu_k=(cu_k, torch.int32))
+    if n == 0:
+        return out
     _check("oasr_cross_attn_packed", L.oasr_cross_attn_packed(
         q.data_ptr(), q_apart, k.data_ptr(), k_apart, v.data_ptr(), v_apart, cu_q.data_ptr(), cu_k.data_ptr(), N, max_q,
         max_k, n, nk, out.data_ptr(), H, Hkv, D, D ** -0.5 if scale is None else scale, code, _stream(stream)))
@@ -702,6 +708,8 @@ def oasr_cross_attn_paged(q, k_pool, v_pool, block_table, cache_seqlens, cu_q, m
     if not (_good(dev, q.dtype, k_pool, v_pool) and _good(dev, torch.int32, block_table, cache_seqlens)):
         _refuse(k_pool=(k_pool, q.dtype), v_pool=(v_pool, q.dtype), block_table=(block_table, torch.int32),
                 cache_seqlens=(cache_seqlens, torch.int32))
+    if n == 0:
+        return out
     _check("oasr_cross_attn_paged", L.oasr_cross_attn_paged(
         q.data_ptr(), q_apart, k_pool.data_ptr(), v_pool.data_ptr(), shape[0], shape[1], block_table.data_ptr(), table[1],
         cache_seqlens.data_ptr(), cu_q.data_ptr(), N, max_q, max_k, n, out.data_ptr(), H, shape[2], D,
@@ -734,6 +742,8 @@ def oasr_quantize_blocks(x, x8=None, scale=None, stream=None):
     _blocks(x8, scale, "x8")
     if not (_good(dev, dt, x) and _good(dev, torch.float8_e4m3fn, x8) and _good(dev, torch.uint8, scale)):
         _refuse(x=(x, dt), x8=(x8, torch.float8_e4m3fn), scale=(scale, torch.uint8))
+    if M == 0:
+        return x8, scale
     _check("oasr_quantize_blocks", L.oasr_quantize_blocks(
         x.data_ptr(), x8.data_ptr(), scale.data_ptr(), M, K, code, _stream(stream)))
     return x8, scale
@@ -759,6 +769,8 @@ def oasr_linear_e4m3(x8, x_scale, w8, w_scale, bias=None, out=None, out_dtype=to
             and (bias is None or _good(dev, dt, bias))):
         _refuse(x8=(x8, e4), x_scale=(x_scale, torch.uint8), w8=(w8, e4), w_scale=(w_scale, torch.uint8), out=(out, dt),
                 **({} if bias is None else {"bias": (bias, dt)}))
+    if M == 0:
+        return out
     _check("oasr_linear_e4m3", L.oasr_linear_e4m3(
         x8.data_ptr(), x_scale.data_ptr(), w8.data_ptr(), w_scale.data_ptr(), None if bias is None else bias.data_ptr(),
         out.data_ptr(), M, N, K, code, _stream(stream)))

@@ -451,6 +451,34 @@ def test_few_tiles_of_many_rows(rows, keys):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_step_in_which_streams_only_end(dtype):
+    """No new rows and no queries: every call of the step goes through, and the pages are back."""
+    d, H, Hkv, bs = 256, 4, 2, 16
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(2)
+    w8, ws = capi.oasr_quantize_blocks(torch.randn(2 * Hkv * 64, d, generator=g).cuda())
+    table, lens, new = torch.tensor([[3, 1], [0, -1]], **i32), torch.tensor([20, 16], **i32), torch.zeros(2, **i32)
+    ring, state = torch.tensor([2, -7, -7, -7], **i32), torch.tensor([0, 1, 0, 0], **i32)
+    kp, vp = (torch.zeros(4, bs, Hkv, 64, dtype=DT[dtype], device="cuda") for _ in range(2))
+    slots, cu = capi.oasr_block_table_update(table, lens, new, ring, state, bs, 0)
+    x8, xs = capi.oasr_quantize_blocks(torch.empty(0, d, dtype=DT[dtype], device="cuda"))
+    kv = capi.oasr_linear_e4m3(x8, xs, w8, ws, out_dtype=DT[dtype]).view(0, 2, Hkv, 64)
+    capi.oasr_paged_append_slots(kv[:, 0], kv[:, 1], kp, vp, slots)
+    lens.copy_(torch.where(state[2] == 0, new, torch.minimum(lens, new)))
+    q, cu_q = torch.empty(0, H, 64, dtype=DT[dtype], device="cuda"), torch.zeros(3, **i32)
+    assert capi.oasr_cross_attn_paged(q, kp, vp, table, lens, cu_q, 1).shape == (0, H, 64)
+    k = torch.zeros(1, Hkv, 64, dtype=DT[dtype], device="cuda")
+    assert capi.oasr_cross_attn_packed(q, k, k, cu_q, cu_q, 1, 1).shape == (0, H, 64)
+    assert ring.tolist() == [2, 3, 1, 0] and state.tolist() == [0, 4, 0, 0] and cu.tolist() == [0, 0, 0]
+    assert set(table.flatten().tolist()) == {-1} and not lens.any() and capi.oasr_device_status() == 0
+    with pytest.raises(ValueError, match="slot_map"):     # the checks are made all the same
+        capi.oasr_paged_append_slots(kv[:, 0], kv[:, 1], kp, vp, ring)
+    with pytest.raises(ValueError, match="shapes"):
+        capi.oasr_linear_e4m3(x8, xs, w8[:, :128].contiguous(), ws[:, :1].contiguous())
+
+
+@pytest.mark.gpu
 def test_decoder_step_together():
     """The operators as a server uses them: pages for two utterances, their states' keys and values by an e4m3 product
     into the pages by their slots, a beam's tokens over them, and the output projection; eager and replayed, a third
