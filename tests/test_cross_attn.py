@@ -357,6 +357,60 @@ def test_bad_blocks_and_offsets(n, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad_q,bad_k", [({2: 10 ** 6}, {1: -7}), ({}, {2: 10 ** 6}), ({1: 10 ** 6}, {}), ({0: -5}, {0: -2 ** 31}),
+                                         ({2: -1}, {}), ({}, {1: 2 ** 31 - 1}), ({1: -3}, {2: 40})])
+@pytest.mark.parametrize("dtype,n,max_q", [("bf16", 2, 2), ("bf16", 150, 150), ("bf16", 150, 10000), ("f32", 2, 2), ("f32", 150, 150)])
+def test_offsets_out_of_range_are_clamped(dtype, n, max_q, bad_q, bad_k):
+    """Each sequence has the rows that its two offsets leave within the tensors, a first one that is out of range or
+    after the second moved first; rows that then belong to none keep what they held."""
+    c = Case([n, n], [100, 90], 4, 2, dtype, 6)
+    c.k, c.v = (torch.where(t.isnan(), 0.5, t) for t in (c.k, c.v))      # rows behind the last sequence are read
+    x = c.cuda()
+    for cu, name, bad in ((c.cu_q, "cu_q", bad_q), (c.cu_k, "cu_k", bad_k)):
+        for i, to in bad.items():
+            x[name][i] = to
+
+    def spans(cu, total):
+        for a, b in zip(cu[:-1], cu[1:]):
+            if a < 0 or b < a or b > total:
+                a = min(max(a, 0), total)
+                b = min(max(a, b), total)
+            yield slice(a, b)
+
+    out = torch.full_like(x["q"], 3.0)
+    c.packed(x, out=out, max_q=max_q)
+    assert capi.oasr_device_status() == capi.STATUS_BOUNDS_BIT
+    owned = torch.zeros(2 * n, dtype=torch.bool)
+    for rows, keys in zip(spans(x["cu_q"].tolist(), 2 * n), spans(x["cu_k"].tolist(), c.k.shape[0])):
+        assert not owned[rows].any()
+        owned[rows] = True
+        want, tol = reference(c.q[rows], *(t[keys].repeat_interleave(2, 1) for t in (c.k, c.v)), 0.125, dtype == "bf16")
+        assert bool(((out[rows].double().cpu() - want).abs() <= tol).all())
+    assert bool((out[~owned.cuda()] == 3.0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,max_q", [(4, 4, 20), (6, 2, 9), (8, 4, 17)])
+def test_many_sequences_longer_than_announced(H, Hkv, max_q):
+    """Tiles of 128 rows, more of them than the launch was laid out for: CTAs go on past the grid's end."""
+    g = torch.Generator().manual_seed(H)
+    N, G = 130, H // Hkv
+    nq, nk = torch.randint(0, 500, (N,), generator=g).tolist(), torch.randint(0, 200, (N,), generator=g).tolist()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    qpt = 128 // G
+    assert max_q * G > 16 and N * Hkv * -(-max_q * G // 16) > 2 * sms                          # the kernel of 128-row tiles
+    assert sum(-(-n // qpt) for n in nq) > min(sum(nq) // qpt + N, -(-max_q // qpt) * N)      # fewer CTAs than tiles
+    c = Case(nq, nk, H, Hkv, "bf16", 31)
+    x = c.cuda()
+    want = c.packed(x)
+    c.check(want)
+    for _ in range(3):
+        assert torch.equal(c.packed(x, max_q=max_q), want)
+        assert torch.equal(c.paged(x, max_q=max_q), want)
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [1, 200])
 def test_pools_past_4_gb(n):
     nb, bs, H = 140000, 64, 4

@@ -362,6 +362,31 @@ def test_update_captured():
 
 
 @pytest.mark.gpu
+def test_update_captured_flags_only_what_is_out_of_range():
+    """Replays whose rows fit `total` raise nothing; those with more rows do, and the next ones nothing again."""
+    bs, mbps, nb, total = 16, 8, 40, 40
+    lens = [20, 0, 64]
+    table, ring, state = batch(3, lens, bs, mbps, nb)
+    t, r, s, c, n = cuda(table, ring, state, lens, lens)
+    slots = torch.empty(total, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    capi.oasr_device_status()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        capi.oasr_block_table_update(t, c, n, r, s, bs, total, slot_map=slots)
+        c.copy_(n)
+    for step in ([40, 16, 0], [56, 32, 8], [0, 0, 0], [3, 70, 100], [0, 70, 110], [128, 128, 128], [0, 0, 0]):
+        n.copy_(torch.tensor(step, dtype=torch.int32))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        fits = sum(max(0, b - a) for a, b in zip(lens, step)) <= total
+        table, ring, state, want, _ = walk(table, lens, step, ring, state, bs, total)
+        assert [x.tolist() for x in (t, r, s, slots)] == [table, ring, state, want]
+        assert capi.oasr_device_status() == (0 if fits else capi.STATUS_BOUNDS_BIT)
+        lens = step
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows,H,D,bs", [(1, 1, 64, 16), (7, 4, 64, 8), (333, 8, 64, 32), (40, 3, 64, 5), (65, 5, 8, 16),
                                          (12, 20, 128, 7)])
