@@ -400,7 +400,8 @@ oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_
  * Offsets that decrease or pass total_q or total_k, and lengths past the table, are clamped; an invalid block id
  * reads as zero rows; each raises OASR_ERR_BOUNDS.  Keys past a sequence's end are never part of a result, whatever
  * they hold.  bf16: fp32 scores, softmax and sums, the weights rounded to bf16 for their product with v, one
- * rounding of out.  f32: fp32 throughout (no TF32).
+ * rounding of out.  f32: fp32 throughout (no TF32).  The weights are normalised last: values above 3e38 / (256 * keys)
+ * in magnitude (f32: 3e38 / keys) may overflow.
  */
 oasr_status oasr_cross_attn_packed(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                    const void* v, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,

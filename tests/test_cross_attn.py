@@ -237,6 +237,27 @@ def test_peaked_and_flat(nq, std, scale, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("max_q", [None, 10000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 12, 180])
+def test_the_largest_values(n, dtype, max_q):
+    """Values at the header's limit, the scores after the first 128 keys a factor just below 2^8 above theirs, for which
+    the maximum does not move: sums close to fp32's range."""
+    c = Case([n], [900], 1, 1, dtype, 9, split=False)
+    c.q.zero_()
+    c.q[:, 0, 0] = 1
+    c.k.zero_()
+    c.k[128:, 0, 0] = 43.75      # 7.89 in log2 units
+    top = 3e38 / (900 * (256 if dtype == "bf16" else 1))
+    c.v[:, 0] = torch.linspace(top / 2, top, 903)[:, None].to(c.dt) * (1 - 2.0 ** -7)
+    c.v[:, 0, 1::2] *= -1
+    x = c.cuda()
+    out = c.packed(x, max_q=max_q or n)
+    c.check(out)
+    assert float(out.abs().max()) > 0.7 * top
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [1, 180])
 def test_rising_scores(n, dtype):
