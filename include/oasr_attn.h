@@ -372,7 +372,8 @@ oasr_status oasr_block_table_update(int32_t* block_table, const int32_t* cache_s
  * Rows of requests of different lengths into the pools ([num_blocks, block_size, H, D], `dt`) by their slots: row i of
  * k_new and v_new (rows of H * D values, k_stride and v_stride values apart: views of one product's output will do)
  * becomes row slot_map[i] of k_pool and v_pool, a pure copy.  Slots of -1 are skipped; slots below that or past the
- * pools are skipped and raise OASR_ERR_BOUNDS.  A slot named twice holds one of its rows, unspecified which.
+ * pools are skipped and raise OASR_ERR_BOUNDS.  What a slot named twice holds is unspecified (each 16 bytes of it are
+ * one of its rows').
  * Requirements: total at least 1 (a step in which streams only end has no rows and no call); D * sizeof(dtype) and both
  * strides multiples of 16 bytes; num_blocks * block_size < 2^31.
  */

@@ -409,6 +409,20 @@ def test_append_slots(rows, H, D, bs, dtype):
 
 
 @pytest.mark.gpu
+def test_append_slots_named_twice():
+    """Each 16 bytes of such a slot are one of its rows', the slots beside it are not touched."""
+    k = torch.arange(1, 65, device="cuda").view(64, 1, 1).expand(64, 16, 64).to(torch.bfloat16).contiguous()
+    pools = [torch.zeros(3, 1, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    slots = torch.full((64,), 1, dtype=torch.int32, device="cuda")
+    capi.oasr_paged_append_slots(k, -k, *pools, slots)
+    for p, sign in zip(pools, (1, -1)):
+        got = sign * p[1].view(-1, 8).float()
+        assert bool((got == got[:, :1]).all()) and bool(((got >= 1) & (got <= 64)).all())
+        assert not p[0].any() and not p[2].any()
+    assert capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_append_slots_out_of_range():
     k = torch.randn(6, 2, 64, device="cuda")
     pools = [torch.zeros(2, 4, 2, 64, device="cuda") for _ in range(2)]
