@@ -491,9 +491,10 @@ oasr_status cross_dispatch(CrossArgs a, int max_q, int max_k, oasr_dtype dt, cud
     if (!sms || !a.status) return OASR_ERR_CUDA;
     const bool f32 = dt == OASR_F32, paged = a.table != nullptr;
     const long long max_rows = static_cast<long long>(max_q) * a.G, items = static_cast<long long>(a.N) * a.Hkv;
-    // Tiles of 128 rows where the tiles of 16 are more than two an SM: few tiles leave SMs idle, and their keys can be shared by
-    // a cluster (8 heads over 1500 keys: 32 rows 7.4 us, 15.0 in tiles of 128; 128 rows 9.3 and 16.5; 448 rows, 224 tiles, 16.5
-    // and 16.6; 256 tiles 18.0 and 17.3).
+    // Tiles of 128 rows where the tiles of 16 are more than two an SM: few tiles leave SMs idle, and up to one an SM the keys
+    // are shared by a cluster (8 heads over 1500 keys: 32 rows 7.4 us, 15.0 in tiles of 128; 128 rows 9.3 and 16.5).  With 153
+    // to 304 tiles of 16 rows they take 0.8 of the other's time over 100 or 300 keys, 0.9 over 700, 1.01 over 1500 and 1.04
+    // over 3000; with 320, a second round of CTAs, 0.93, 1.1, 1.25 and 1.33.
     if (!f32 && max_rows > kXRows && items * ((max_rows + kXRows - 1) / kXRows) > 2LL * sms && cross_tc_takes(a))
         return cross_tc(a, max_q, stream);
     // row tiles side by side, as many as the longest sequence has (a longer one is walked through)
