@@ -486,7 +486,9 @@ int g_smem_done_xtc[2][64];
 
 bool cross_tc_takes(const CrossArgs& a)
 {
-    // pages that tile a stage of 128 keys
+    // Pages that tile a stage of 128 keys, as a stage's boxes lie one behind the other.  Others (of 24 frames, say), and groups of
+    // more than 128 heads, stay with tiles of 16 rows: 256 transcripts 760 us in pages of 24, 150 in pages of 32 and 205 in
+    // pages of 8, whose boxes are the smallest.
     return a.G <= kCRows && (!a.table || (a.bs >= 8 && a.bs <= 32768 && !(a.bs & (a.bs - 1))));
 }
 
