@@ -394,8 +394,8 @@ oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_
  * of q, k and v are q_stride, k_stride, v_stride values apart (heads are
  * contiguous: k and v may be the halves of one product's rows); out is [total_q, H, 64].
  * max_q and max_k are the lengths that the launch is laid out for: a longer sequence is right, and slower.  Many bf16
- * rows a sequence take four to five times as long in pages whose block_size is not a power of two from 8 on, and where
- * more than 128 query heads share a key head.
+ * rows a sequence take four to five times as long in pages whose block_size is not a power of two from 8 on; tiles of
+ * 16 rows, as those, are also what more than 128 query heads to a key head get.
  * Requirements: D = 64; H a multiple of Hkv and at most 1024; num_seqs at most 65536; 0 < scale <= 2e38; pointers
  * and strides multiples of 16 bytes; total_q, total_k, max_q and max_k at least 1; total_q * G, max_q * G, total_k
  * and max_blocks_per_seq * block_size below 2^31 - 256;
