@@ -303,6 +303,40 @@ def test_values_that_are_not_finite(n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [2, 20, 150])
+def test_values_that_are_not_finite_f32(n):
+    base = Case([n, n, n], [140, 200, 30], 2, 2, "f32", 11)
+    want = base.packed(base.cuda())
+    for which in "kvq":
+        c = Case([n, n, n], [140, 200, 30], 2, 2, "f32", 11)
+        getattr(c, which)[n + 1 if which == "q" else 140 + 133, 1, 5] = float("nan")
+        out = c.packed(c.cuda())
+        bad = torch.zeros_like(out, dtype=torch.bool)
+        bad[(n + 1, 1) if which == "q" else (slice(n, 2 * n), 1) if which == "k" else (slice(n, 2 * n), 1, 5)] = True
+        assert torch.equal(out.isnan(), bad), which
+        assert torch.equal(out[~bad], want[~bad])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,max_q", [("bf16", None), ("bf16", 10000), ("f32", None)])
+@pytest.mark.parametrize("H,Hkv,nq", [(4, 2, [70, 3]), (3, 3, [1, 1]), (65, 1, [5, 2]), (256, 2, [3, 1]), (100, 1, [1, 4])])
+def test_queries_of_one_product_with_their_keys(H, Hkv, nq, dtype, max_q):
+    """q, k and v are columns of one product's rows, the rows of q behind the last sequence among them; groups of 65, 100
+    and 128 heads to a key head."""
+    c = Case(nq, nq, H, Hkv, dtype, H)
+    n = sum(nq)
+    g = torch.Generator().manual_seed(7)
+    rows = torch.randn(n + 2, H + 2 * Hkv, 64, generator=g).to(c.dt)
+    c.q, c.k, c.v = rows[:, :H], rows[:, H:H + Hkv], rows[:, H + Hkv:]
+    d = rows.cuda()
+    cu = c.cu_q.cuda()
+    out = torch.full((n + 2, H, 64), 5.0, dtype=c.dt, device="cuda")
+    capi.oasr_cross_attn_packed(d[:, :H], d[:, H:H + Hkv], d[:, H + Hkv:], cu, cu, max_q or max(nq), max(nq), out=out)
+    c.check(out)
+    assert bool((out[n:] == 5.0).all()) and capi.oasr_device_status() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [1, 2, 8, 20, 150])
 def test_scores_of_minus_infinity(n, dtype):
