@@ -9,7 +9,9 @@
 // query rows fill its columns.  The contraction of q . k may run over the 64 dimensions in any order, and the rows of O^T
 // stand for any dimensions, so the order is taken in which a lane's part of a row is 16 bytes: lane 4 g + c has dimensions
 // 8 c .. 8 c + 7 and 32 + 8 c .. 32 + 8 c + 7 of keys g and 8 + g (K) and 8 g .. 8 g + 7 of keys 2 c, 2 c + 1, 8 + 2 c and
-// 9 + 2 c (V, whose pairs of keys are interleaved by byte permutes).  The keys of a sequence are shared by the warps of a
+// 9 + 2 c (V, whose pairs of keys are interleaved by byte permutes).  The weights are rounded to bf16, as the instruction takes
+// them and v in one type; their sum is of the unrounded ones.  Against 64 bits a result is off by 0.0022 of its size in rms,
+// of which its own rounding alone makes 0.0017.  The keys of a sequence are shared by the warps of a
 // CTA and, where that leaves SMs idle, by a cluster of CTAs.
 //
 // A beam of 8 over 256 utterances of 50 to 1500 keys, 8 heads, in pages (410 MB): 73 us, 0.83 of the copy rate; 456 heads of

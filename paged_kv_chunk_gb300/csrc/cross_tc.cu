@@ -10,14 +10,16 @@
 // S, P and O have columns of their own (128 + 64 + 64 of 256), so the next stage's S is computed while this one's
 // exponentials are, and two CTAs share an SM: one's softmax runs beside the other's products.  O is rescaled
 // only when a row's maximum has grown by more than 2^8 (P then stays below 2^8, the same relative
-// rounding).  P . V stops at the 16 keys that hold the last one; V rows behind it within those are zeroed.
+// rounding).  P is rounded to bf16, as the product takes both operands in one type: 0.0022 of the result in rms against 64 bits,
+// 0.0017 by the result's own rounding; its other half in bf16 would need 64 more columns, or a stage of 96 keys.  P . V stops at the 16 keys that hold the last one; V rows behind it within those are zeroed.
 //
 // The grid has a CTA for every tile; those that run take over the ones that have not started (cluster launch control), so
 // that a tile's start-up (2.7 us of a CTA) passes while the one before it is worked on: 256 transcripts of 20 to
 // 448 rows over up to 1500 states 225 -> 149 us.
 //
 // What bounds it: the chain of a stage (128 keys), about 1830 cycles of a CTA alone: S read 240, maxima 200, exponentials
-// 820 (the exponential unit would need 512), the hand-overs between roles 110 to 400 each; 1250 a stage with two CTAs an SM.
+// 820 (the exponential unit would need 512), the hand-overs between roles 110 to 400 each.  Two CTAs an SM take some 2500
+// cycles each for one of theirs, so an SM finishes a stage every 1270.
 // 304 sequences of 512 rows over 1280 keys, 8 heads: 428 us, 0.95 PFLOP/s, the tensor pipe 31 % active in the rescoring
 // of 64 utterances (51.6 us).  Right and slower there: eight softmax warps (rows in halves, joined through shared memory, or
 // four lanes to a row), 96 keys a stage with two P, issuers of their own for S and P . V (the registers then leave 128 a

@@ -601,8 +601,9 @@ template <typename Elem>
 oasr_status dispatch_e4(const E4Problem& p, void* out, cudaStream_t stream)
 {
     // A few rows without tiles, where that is the shorter of the two: about 1300 ns and 90 for each row and 128 of K (512 at a
-    // time, and up to 2048 columns), against 2600 and 300 for each 128 of K.  2 x 512 x 2048: 4.0 and 7.3 us, 4 x 2048 x
-    // 512 2.6 and 3.8, 6 x 4096 x 1024 8.7 and 5.7, 8 x 512 x 2048 9.7 and 7.3.
+    // time, and up to 2048 columns), against 2600 and 300 for each 128 of K.  2 x 512 x 2048: 3.8 and 5.0 us, 4 x 2048 x
+    // 512 2.5 and 3.7, 6 x 512 x 512 2.9 and 3.6, 6 x 4096 x 1024 11.1 and 6.2, 6 x 512 x 2048 7.4 and 5.5.  That K may be shared
+    // by a cluster below is not weighed here: 4 x 512 x 2560 takes 8.0 us and would 5.9, 3 x 512 x 4096 14.4 and 6.8.
     const long long steps = (p.K + 511LL) / 512 * 4, few = 1300 + 90LL * p.M * steps * (p.N > 2048 ? p.N : 2048) / 2048;
     if (p.M == 1 || (p.M <= kE4FewRows && few < 2600 + 300LL * p.kb)) {
         const dim3 grid((p.N + 7) / 8);
