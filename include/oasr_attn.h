@@ -358,10 +358,11 @@ oasr_status oasr_project_qkv_pos_w8a8(const void* x8, const float* x_scale, cons
  *                       position C + t of stream b has; -1 behind cu[B].
  * cache_seqlens is not changed: the caller commits the new lengths once the rows are written.  A stream has at most
  * max_blocks_per_seq pages; lengths below 0 or past them are clamped, a slot whose page names no block is -1, rows
- * past `total` get no slot, pages that come back beyond num_blocks ids are lost, a ring state out of range stays as it is while nothing is handed out or taken back: each
- * raises OASR_ERR_BOUNDS.
+ * past `total` get no slot, pages that come back beyond num_blocks ids are lost, a ring state out of range stays as it
+ * is while nothing is handed out or taken back: each raises OASR_ERR_BOUNDS.
  * Requirements: B at most 4096; num_blocks * block_size and B * max_blocks_per_seq below 2^31 and
- * (max_blocks_per_seq + 1) * block_size below 2^31 - 256 (else OASR_ERR_UNSUPPORTED).  One call at a time may work on a ring and its state.
+ * (max_blocks_per_seq + 1) * block_size below 2^31 - 256 (else OASR_ERR_UNSUPPORTED).  One call at a time may work on
+ * a ring and its state.
  */
 oasr_status oasr_block_table_update(int32_t* block_table, const int32_t* cache_seqlens,
                                     const int32_t* new_seqlens, int B, int max_blocks_per_seq, int block_size,
@@ -398,8 +399,7 @@ oasr_status oasr_paged_append_slots(const void* k_new, const void* v_new, int64_
  * 16 rows, as those, are also what more than 128 query heads to a key head get.
  * Requirements: D = 64; H a multiple of Hkv and at most 1024; num_seqs at most 65536; 0 < scale <= 2e38; pointers
  * and strides multiples of 16 bytes; total_q, total_k, max_q and max_k at least 1; total_q * G, max_q * G, total_k
- * and max_blocks_per_seq * block_size below 2^31 - 256;
- * num_blocks * block_size < 2^31.
+ * and max_blocks_per_seq * block_size below 2^31 - 256; num_blocks * block_size < 2^31.
  * Offsets that decrease or pass total_q or total_k, and lengths past the table, are clamped; an invalid block id
  * reads as zero rows; each raises OASR_ERR_BOUNDS.  Keys past a sequence's end are never part of a result, whatever
  * they hold.  bf16: fp32 scores, softmax and sums, the weights rounded to bf16 for their product with v, one
@@ -422,7 +422,7 @@ oasr_status oasr_cross_attn_paged(const void* q, int64_t q_stride, const void* k
  * last block of a row may be shorter): x8 [M, K] e4m3 bytes, scale [M, ceil(K / 128)] bytes.  A block is quantised as
  * a row of the 8-bit cache is: e = max(-100, the least e for which max|x_block| <= 448 * 2^e), the scale byte
  * e + 127, x8 = x * 2^-e rounded to e4m3 (nearest, ties to even); a block with a NaN or an infinity has the byte 255
- * and stands for NaN in every element.  K must be a multiple of 16.
+ * and stands for NaN in every element.  M at least 1, K a multiple of 16.
  */
 oasr_status oasr_quantize_blocks(const void* x, void* x8, void* scale, int M, int K, oasr_dtype dt,
                                  cudaStream_t stream);
